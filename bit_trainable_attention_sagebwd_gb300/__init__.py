@@ -19,6 +19,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsage_attn.so")
 
 SAGE_OK, SAGE_ERR_INVALID_ARG, SAGE_ERR_UNSUPPORTED, SAGE_ERR_CUDA, SAGE_ERR_TIMEOUT = 0, 1, 2, 3, 4
+SAGE_ERR_NO_PAGES = 5
+SAGE_KV_INT8, SAGE_KV_E4M3 = 0, 1
 
 # names declared in include/sage_attn.h
 ABI_FUNCTIONS = ("sage_attn_ws_bytes", "sage_attn_bwd_ws_bytes", "sage_attn_quantize", "sage_attn_fwd",
@@ -31,7 +33,10 @@ ABI_FUNCTIONS = ("sage_attn_ws_bytes", "sage_attn_bwd_ws_bytes", "sage_attn_quan
                  "sage_attn_qs_bwd", "sage_attn_qs_ws_views", "sage_attn_thrift_ws_bytes",
                  "sage_attn_thrift_quantize", "sage_attn_thrift_fwd", "sage_attn_thrift_sel",
                  "sage_attn_fp4_ws_bytes", "sage_attn_fp4_quantize", "sage_attn_fp4_fwd",
-                 "sage_attn_fp4_ws_views", "sage_attn_fp4_bwd_ws_bytes", "sage_attn_fp4_bwd")
+                 "sage_attn_fp4_ws_views", "sage_attn_fp4_bwd_ws_bytes", "sage_attn_fp4_bwd",
+                 "sage_attn_kv_append", "sage_attn_kv_ws_bytes", "sage_attn_kv_attention", "sage_attn_kv_fork",
+                 "sage_attn_kv_extend", "sage_attn_kv_truncate", "sage_attn_kv_compact_ws_bytes",
+                 "sage_attn_kv_compact")
 
 
 class SageError(RuntimeError):
@@ -47,6 +52,11 @@ class sage_ws_views(ctypes.Structure):
                 ("status", ctypes.c_void_p), ("n_pad", ctypes.c_int), ("qmean", ctypes.c_void_p),
                 ("dsb", ctypes.c_void_p), ("vg", ctypes.c_void_p), ("v4", ctypes.c_void_p),
                 ("v4sf", ctypes.c_void_p)]
+
+
+class sage_kv_cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "table", "lengths", "refs", "status")] + \
+        [(n, ctypes.c_int) for n in ("n_pages", "Hkv", "page", "D", "n_slots", "max_pages", "kind")]
 
 
 _lib = None
@@ -98,6 +108,17 @@ def lib():
             L.sage_attn_thrift_fwd.argtypes = [vp] * 5 + [i] * 5 + [fp, vp]
             L.sage_attn_thrift_sel.restype = vp
             L.sage_attn_thrift_sel.argtypes = [vp] + [i] * 4
+            cp = ctypes.POINTER(sage_kv_cache)
+            L.sage_attn_kv_append.argtypes = [cp] + [vp] * 6 + [i, i, vp]
+            L.sage_attn_kv_ws_bytes.restype = sz
+            L.sage_attn_kv_ws_bytes.argtypes = [i] * 5
+            L.sage_attn_kv_attention.argtypes = [cp] + [vp] * 6 + [sz, i, i, i, i, fp, vp]
+            L.sage_attn_kv_fork.argtypes = [cp, vp, vp]
+            L.sage_attn_kv_extend.argtypes = [cp, vp, vp, vp, vp]
+            L.sage_attn_kv_truncate.argtypes = [cp, vp, vp]
+            L.sage_attn_kv_compact_ws_bytes.restype = sz
+            L.sage_attn_kv_compact_ws_bytes.argtypes = [i]
+            L.sage_attn_kv_compact.argtypes = [cp, cp, vp, sz, vp]
             L.sage_attn_ws_views.argtypes = [vp, i, i, i, i, ctypes.POINTER(sage_ws_views)]
             L.sage_attn_get_status.argtypes = [vp, vp]
             L.sage_attn_selftest_wait.argtypes = [vp, u64, vp]
@@ -191,6 +212,39 @@ def sage_attn_thrift_fwd(ws, tws, O, LSE, O32, B, H, N, D, causal, sm_scale, str
 
 def sage_attn_thrift_sel(tws, B, H, N, D):
     return lib().sage_attn_thrift_sel(tws, B, H, N, D)
+
+
+def sage_attn_kv_append(cache, K, V, k_shift, slots, pos, n_new, B, Nn, stream):
+    return lib().sage_attn_kv_append(cache, K, V, k_shift, slots, pos, n_new, B, Nn, stream)
+
+
+def sage_attn_kv_ws_bytes(B, H, Hkv, D, Nq):
+    return lib().sage_attn_kv_ws_bytes(B, H, Hkv, D, Nq)
+
+
+def sage_attn_kv_attention(cache, Q, slots, q_len, O, LSE, ws, ws_bytes, B, H, Nq, causal, sm_scale, stream):
+    return lib().sage_attn_kv_attention(cache, Q, slots, q_len, O, LSE, ws, ws_bytes, B, H, Nq, int(causal),
+                                        float(sm_scale), stream)
+
+
+def sage_attn_kv_fork(cache, src, stream):
+    return lib().sage_attn_kv_fork(cache, src, stream)
+
+
+def sage_attn_kv_extend(cache, n_new, pos, cow, stream):
+    return lib().sage_attn_kv_extend(cache, n_new, pos, cow, stream)
+
+
+def sage_attn_kv_truncate(cache, keep, stream):
+    return lib().sage_attn_kv_truncate(cache, keep, stream)
+
+
+def sage_attn_kv_compact_ws_bytes(n_pages):
+    return lib().sage_attn_kv_compact_ws_bytes(n_pages)
+
+
+def sage_attn_kv_compact(cache, to, ws, ws_bytes, stream):
+    return lib().sage_attn_kv_compact(cache, to, ws, ws_bytes, stream)
 
 
 def sage_attn_bwd_noalloc(Q, K, V, O, LSE, dO, dQ, dK, dV, ws, B, H, N, D, causal, qk_norm, k_smooth, sm_scale,
@@ -603,3 +657,7 @@ def ws_tensors(ws, B, H, N, D, hkv=None, q_smooth=False, fp4=False) -> dict:
         "kr": view(v.kr, bk * np_ * 4, torch.float32, (B, hk, np_)),
         "n_pad": np_,
     }
+
+
+from .kvcache import (KVCache, alloc_kv_compact_ws, alloc_kv_ws, kv_append, kv_attention, kv_cache,  # noqa: E402,F401
+                      kv_compact, kv_extend, kv_fork, kv_truncate)

@@ -7,6 +7,7 @@
 #include "../../include/sage_attn.h"
 #include "args.h"
 #include "kernels.h"
+#include "kv.h"
 #include "layout.h"
 #include "ptx.cuh"
 #include "timer.h"
@@ -337,7 +338,13 @@ int sage_attn_get_status(void* ws, void* stream) {
     if (cudaMemcpyAsync(dev, &zero, sizeof(int), cudaMemcpyHostToDevice, st) != cudaSuccess) return SAGE_ERR_CUDA;
     if (cudaStreamSynchronize(st) != cudaSuccess) return SAGE_ERR_CUDA;
   }
-  return h == 0 ? SAGE_OK : (h == sage::kDevTimeout ? SAGE_ERR_TIMEOUT : SAGE_ERR_CUDA);
+  switch (h) {
+    case 0: return SAGE_OK;
+    case sage::kDevTimeout: return SAGE_ERR_TIMEOUT;
+    case sage::kDevPages: return SAGE_ERR_NO_PAGES;
+    case sage::kDevIndex: return SAGE_ERR_INVALID_ARG;
+    default: return SAGE_ERR_CUDA;
+  }
 }
 
 int sage_attn_selftest_wait(void* ws, unsigned long long budget_ns, void* stream) {
@@ -368,6 +375,7 @@ const char* sage_attn_status_str(int s) {
     case SAGE_ERR_UNSUPPORTED: return "unsupported shape";
     case SAGE_ERR_CUDA: return "CUDA runtime error";
     case SAGE_ERR_TIMEOUT: return "device wait timed out";
+    case SAGE_ERR_NO_PAGES: return "too few free pages";
     default: return "unknown status";
   }
 }

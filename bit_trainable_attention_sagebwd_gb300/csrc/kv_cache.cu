@@ -1,0 +1,538 @@
+// The 8-bit paged key/value cache: the quantizing write and the bookkeeping of its pages
+// (sage_attn_kv_append, _fork, _extend, _truncate, _compact in include/sage_attn.h).
+//
+// Every decision that numbers depend on (which page is taken, who copies a shared page, where a
+// live page goes) follows the order of slots and pages, never the order in which threads arrive:
+// the same state and arguments give the same tables.  The only atomics are integer additions
+// into `refs` and the maximum of the status word, whose results do not depend on their order.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "codes.cuh"
+#include "kv.h"
+#include "launch.h"
+#include "ptx.cuh"
+#include "timer.h"
+
+namespace sage {
+
+namespace {
+
+__device__ __forceinline__ void kv_error(int* status, int code) { atomicMax(status, code); }
+
+// ------------------------------------------------------------------------------ append
+
+constexpr int kAppendThreads = 128;
+
+// e4m3 codes of eight values under the scale s, and what a code stands for under it
+__device__ __forceinline__ uint2 e4m3_codes8(const float (&x)[8], float s) {
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; i += 2)
+    w[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[i], s), __fdiv_rn(x[i + 1], s)),
+                                                    __NV_SATFINITE, __NV_E4M3)
+                 << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ uint2 int8_codes8(const float (&x)[8], float s) {
+  float c[8];
+  const float inv = __frcp_rn(s);
+  if (inv < INFINITY) {
+    int_codes8(x, s, inv, c);
+  } else {  // a subnormal scale whose reciprocal overflows
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -127.f), 127.f);
+  }
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i >> 2] |= ((uint32_t)(int)c[i] & 0xffu) << (8 * (i & 3));
+  return make_uint2(w[0], w[1]);
+}
+template <int KIND>
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
+  if (!(s > 0.f)) return make_uint2(0u, 0u);
+  return KIND == SAGE_KV_INT8 ? int8_codes8(x, s) : e4m3_codes8(x, s);
+}
+template <int KIND>
+__device__ __forceinline__ void values8(uint2 c, float s, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = ((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xffu;
+    const float v = KIND == SAGE_KV_INT8 ? (float)(int)(int8_t)b
+                                         : __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3)));
+    x[i] = __fmul_rn(v, s);
+  }
+}
+
+struct AppendParams {
+  sage_kv_cache c;
+  const __nv_bfloat16 *K, *V;
+  const float* shift;
+  const int *slots, *pos, *n_new;
+  int B, Nn;
+};
+
+// One CTA per (page that the new tokens of a batch row can touch, key/value head, K or V).  A
+// thread holds its eight channels of P D / 1024 tokens in registers between the maximum and the
+// codes, so the new tokens are read once.
+template <int D, int P, int KIND>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
+  constexpr int TPR = D / 8, RPP = kAppendThreads / TPR, NP = P / RPP;  // threads a token, tokens a pass, passes
+  static_assert(P % RPP == 0, "a page is a whole number of passes");
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.z, hk = blockIdx.y >> 1, tid = threadIdx.x;
+  const bool is_v = blockIdx.y & 1;
+  const int slot = p.slots ? p.slots[b] : b;
+  if ((unsigned)slot >= (unsigned)p.c.n_slots) {
+    if (tid == 0) kv_error(p.c.status, kDevIndex);
+    return;
+  }
+  const int pos = p.pos[slot], n = p.n_new[slot];
+  if (pos < 0 || n <= 0) return;  // nothing new, or refused by sage_attn_kv_extend
+  const int j = pos / P + blockIdx.x, t0 = j * P;
+  if ((long long)t0 >= (long long)pos + n) return;
+  // a batch row that names a slot again is left out
+  if (p.slots) {
+    bool again = false;
+    for (int i = tid; i < b; i += kAppendThreads) again |= p.slots[i] == slot;
+    if (__syncthreads_or(again)) {
+      if (tid == 0) kv_error(p.c.status, kDevIndex);
+      return;
+    }
+  }
+  const int page = n <= p.Nn && j < p.c.max_pages ? p.c.table[(size_t)slot * p.c.max_pages + j] : -1;
+  // a page that is not reserved, or that another slot lists too, is not written
+  if ((unsigned)page >= (unsigned)p.c.n_pages || p.c.refs[page] != 1) {
+    if (tid == 0) kv_error(p.c.status, kDevIndex);
+    return;
+  }
+  const int off = max(0, pos - t0);              // tokens of the page that are there already
+  const int end = min((long long)P, (long long)pos + n - t0);
+  const size_t block = (size_t)page * p.c.Hkv + hk;
+  float* scale = (is_v ? p.c.v_scale : p.c.k_scale) + block;
+  uint8_t* codes = static_cast<uint8_t*>(is_v ? p.c.v : p.c.k) + block * P * D;
+  // token 0 of the page is token t0 - pos of the new ones
+  const __nv_bfloat16* src =
+      (is_v ? p.V : p.K) + (((size_t)b * p.c.Hkv + hk) * p.Nn) * D + (ptrdiff_t)(t0 - pos) * D;
+  const int g = tid % TPR, r0 = tid / TPR;
+  const float was = off > 0 ? *scale : 0.f;
+  float sh[8] = {};
+  if (!is_v && p.shift) {
+    const float4* s4 = reinterpret_cast<const float4*>(p.shift + hk * D + g * 8);
+    const float4 a = s4[0], c = s4[1];
+    sh[0] = a.x, sh[1] = a.y, sh[2] = a.z, sh[3] = a.w, sh[4] = c.x, sh[5] = c.y, sh[6] = c.z, sh[7] = c.w;
+  }
+  uint4 u[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int r = r0 + i * RPP;
+    if (r >= off && r < end) u[i] = reinterpret_cast<const uint4*>(src + (size_t)r * D)[g];
+  }
+  auto value = [&](const uint4& w, float (&x)[8]) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __fsub_rn(__uint_as_float(v[e] << 16), sh[2 * e]);
+      x[2 * e + 1] = __fsub_rn(__uint_as_float(v[e] & 0xffff0000u), sh[2 * e + 1]);
+    }
+  };
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int r = r0 + i * RPP;
+    if (r >= off && r < end) {
+      float x[8];
+      value(u[i], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  __shared__ float wtop[kAppendThreads / 32];
+  if ((tid & 31) == 0) wtop[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kAppendThreads / 32; ++i) top = fmaxf(top, wtop[i]);
+  const float fresh = __fmul_rn(top, KIND == SAGE_KV_INT8 ? 1.f / 127.f : 1.f / 448.f);
+  const float now = fmaxf(was, fresh);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int r = r0 + i * RPP;
+    uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)r * D) + g;
+    if (r >= off && r < end) {
+      float x[8];
+      value(u[i], x);
+      *dst = codes8<KIND>(x, now);
+    } else if (r < off && now != was) {  // the page's scale grew: what the old codes stand for, under the new one
+      float x[8];
+      values8<KIND>(*dst, was, x);
+      *dst = codes8<KIND>(x, now);
+    }
+  }
+  if (tid == 0) *scale = now;
+}
+
+template <int D, int P>
+auto append_kernel_for(int kind) {
+  return kind == SAGE_KV_INT8 ? kv_append_kernel<D, P, SAGE_KV_INT8> : kv_append_kernel<D, P, SAGE_KV_E4M3>;
+}
+template <int D>
+auto append_kernel_for(int page, int kind) {
+  return page == 16 ? append_kernel_for<D, 16>(kind)
+                    : page == 32 ? append_kernel_for<D, 32>(kind)
+                                 : page == 64 ? append_kernel_for<D, 64>(kind) : append_kernel_for<D, 128>(kind);
+}
+
+// ------------------------------------------------------------------------------ pages
+
+constexpr int kScanThreads = 1024;
+
+// sum of v over the threads before this one, and over all (whole CTA of kScanThreads)
+__device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += t;
+  }
+  __syncthreads();  // the last call's sums have been read
+  if (lane == 31) warp_sums[w] = s;
+  __syncthreads();
+  if (w == 0) {
+    int x = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += t;
+    }
+    warp_sums[lane] = x;
+  }
+  __syncthreads();
+  *total = warp_sums[31];
+  return s - v + (w ? warp_sums[w - 1] : 0);
+}
+
+// One CTA per slot that takes over another slot's pages.
+__global__ void __launch_bounds__(256) kv_fork_kernel(const sage_kv_cache c, const int* __restrict__ src) {
+  pdl_wait();
+  pdl_trigger();
+  const int s = blockIdx.x, from = src[s];
+  if (from < 0) return;
+  // only an empty slot takes over, and from a slot that does not take over itself
+  const int n = from < c.n_slots ? c.lengths[from] : -1;
+  const bool ok = from < c.n_slots && src[from] < 0 && c.lengths[s] == 0 && n >= 0 &&
+                  (long long)n <= (long long)c.max_pages * c.page;
+  if (!ok) {
+    if (threadIdx.x == 0) kv_error(c.status, kDevIndex);
+    return;
+  }
+  const int np = (n + c.page - 1) / c.page;
+  const int* row = c.table + (size_t)from * c.max_pages;
+  int* to = c.table + (size_t)s * c.max_pages;
+  for (int j = threadIdx.x; j < np; j += blockDim.x) {
+    const int page = row[j];
+    to[j] = page;
+    if ((unsigned)page < (unsigned)c.n_pages)
+      atomicAdd(c.refs + page, 1);
+    else
+      kv_error(c.status, kDevIndex);
+  }
+  __syncthreads();  // every thread has read this slot's length
+  if (threadIdx.x == 0) c.lengths[s] = n;
+}
+
+__global__ void __launch_bounds__(128) kv_truncate_kernel(const sage_kv_cache c, const int* __restrict__ keep) {
+  pdl_wait();
+  pdl_trigger();
+  const int s = blockIdx.x, want = keep[s];
+  if (want < 0) return;
+  const int len = c.lengths[s];
+  const long long cap = (long long)c.max_pages * c.page;
+  if (len < 0 || len > cap) {
+    if (threadIdx.x == 0) kv_error(c.status, kDevIndex);
+    return;
+  }
+  const int now = min(want, len);
+  const int* row = c.table + (size_t)s * c.max_pages;
+  for (int j = (int)(((long long)now + c.page - 1) / c.page) + threadIdx.x; (long long)j * c.page < len; j += blockDim.x) {
+    const int page = row[j];
+    if ((unsigned)page < (unsigned)c.n_pages)
+      atomicSub(c.refs + page, 1);
+    else
+      kv_error(c.status, kDevIndex);
+  }
+  __syncthreads();  // every thread has read the length
+  if (threadIdx.x == 0) c.lengths[s] = now;
+}
+
+// What a slot needs: `have` pages now, `want` after, one more if its last page is shared and
+// partly filled (it is copied first; `last` is that page, else -1).
+struct Need {
+  int len, n, have, want, last;
+  bool bad;
+  __device__ int count() const { return want - have + (last >= 0); }
+};
+__device__ __forceinline__ Need slot_need(const sage_kv_cache& c, const int* n_new, int s) {
+  Need q;
+  q.len = c.lengths[s];
+  q.n = n_new[s];
+  q.last = -1;
+  const long long cap = (long long)c.max_pages * c.page, end = (long long)q.len + q.n;
+  q.bad = q.len < 0 || q.n < 0 || end > cap;
+  q.have = q.bad ? 0 : (q.len + c.page - 1) / c.page;
+  q.want = q.bad ? 0 : (int)((end + c.page - 1) / c.page);
+  if (!q.bad && q.n > 0 && q.len % c.page) {
+    const int page = c.table[(size_t)s * c.max_pages + q.have - 1];
+    if ((unsigned)page >= (unsigned)c.n_pages)
+      q.bad = true, q.have = q.want = 0;
+    else if (c.refs[page] > 1)
+      q.last = page;
+  }
+  return q;
+}
+
+// One CTA: the slots' needs are summed in slot order, then refs is scanned for free pages and
+// the r-th free page goes to the slot whose range of needs holds r.  `excl` (shared) keeps the
+// sums, so finding the slot is a binary search.
+__global__ void __launch_bounds__(kScanThreads) kv_extend_kernel(const sage_kv_cache c, const int* __restrict__ n_new,
+                                                                 int* __restrict__ pos, int* __restrict__ cow) {
+  extern __shared__ int excl[];  // [n_slots + 1]
+  __shared__ int warp_sums[32];
+  constexpr int kPer = 16;  // pages a thread looks at in one step
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x;
+  int carry = 0;
+  for (int s0 = 0; s0 < c.n_slots; s0 += kScanThreads) {
+    const int s = s0 + tid;
+    int need = 0;
+    if (s < c.n_slots) {
+      const Need q = slot_need(c, n_new, s);
+      need = q.count();
+      cow[s] = q.last;
+      if (q.bad) kv_error(c.status, kDevIndex);
+    }
+    int total;
+    const int e = block_exclusive(need, warp_sums, &total);
+    // needs are at most max_pages + 1 each; past 2^30 in all nothing can be served any more
+    const int at = (int)min((long long)carry + e, 1ll << 30);
+    if (s < c.n_slots) excl[s] = at;
+    carry = (int)min((long long)carry + total, 1ll << 30);
+  }
+  if (tid == 0) excl[c.n_slots] = carry;
+  __syncthreads();
+  int found = 0;
+  for (int p0 = 0; p0 < c.n_pages && found < carry; p0 += kScanThreads * kPer) {
+    const int first = p0 + tid * kPer;
+    unsigned free = 0;
+    if (first + kPer <= c.n_pages) {
+#pragma unroll
+      for (int i = 0; i < kPer / 4; ++i) {
+        const int4 r = reinterpret_cast<const int4*>(c.refs + first)[i];
+        free |= (unsigned)(r.x == 0) << (4 * i) | (unsigned)(r.y == 0) << (4 * i + 1) |
+                (unsigned)(r.z == 0) << (4 * i + 2) | (unsigned)(r.w == 0) << (4 * i + 3);
+      }
+    } else {
+      for (int i = 0; i < kPer; ++i)
+        if (first + i < c.n_pages && c.refs[first + i] == 0) free |= 1u << i;
+    }
+    int total;
+    int r = found + block_exclusive(__popc(free), warp_sums, &total);
+    for (; free && r < carry; free &= free - 1, ++r) {
+      const int page = first + __ffs(free) - 1;
+      int lo = 0, hi = c.n_slots;  // the slot with excl[lo] <= r < excl[lo + 1]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (excl[mid] <= r) lo = mid;
+        else hi = mid;
+      }
+      const int have = (c.lengths[lo] + c.page - 1) / c.page;
+      const int begin = have - (cow[lo] >= 0);
+      c.table[(size_t)lo * c.max_pages + begin + r - excl[lo]] = page;
+      c.refs[page] = 1;
+    }
+    found += total;
+  }
+  __syncthreads();
+  for (int s = tid; s < c.n_slots; s += kScanThreads) {
+    const int n = n_new[s], len = c.lengths[s], from = cow[s];
+    const int need = excl[s + 1] - excl[s];
+    const long long cap = (long long)c.max_pages * c.page;
+    const bool bad = len < 0 || n < 0 || (long long)len + n > cap;
+    if (!bad && (need == 0 || excl[s + 1] <= found)) {
+      pos[s] = len;
+      if (n > 0) c.lengths[s] = len + n;
+      if (from >= 0) atomicSub(c.refs + from, 1);
+    } else {
+      pos[s] = -1;
+      cow[s] = -1;
+      if (!bad) {
+        // too few pages: what this slot has been given goes back
+        int* row = c.table + (size_t)s * c.max_pages;
+        const int begin = (len + c.page - 1) / c.page - (from >= 0);
+        for (int i = 0; i < need && excl[s] + i < found; ++i) c.refs[row[begin + i]] = 0;
+        if (from >= 0) row[begin] = from;
+        kv_error(c.status, kDevPages);
+      }
+    }
+  }
+}
+
+// copy of `bytes` (a multiple of 16) with `n` threads, the t-th of them
+__device__ __forceinline__ void copy16(void* dst, const void* src, size_t bytes, size_t t, size_t n) {
+  const uint4* s = static_cast<const uint4*>(src);
+  uint4* d = static_cast<uint4*>(dst);
+  const size_t m = bytes / 16;
+  size_t i = t;
+  for (; i + 3 * n < m; i += 4 * n) {
+    const uint4 a = s[i], b = s[i + n], e = s[i + 2 * n], f = s[i + 3 * n];
+    d[i] = a, d[i + n] = b, d[i + 2 * n] = e, d[i + 3 * n] = f;
+  }
+  for (; i < m; i += n) d[i] = s[i];
+}
+
+// The pages that kv_extend_kernel moved from a shared page to one of the slot's own.
+constexpr int kCowParts = 8;
+__global__ void __launch_bounds__(256) kv_cow_kernel(const sage_kv_cache c, const int* __restrict__ pos,
+                                                     const int* __restrict__ cow) {
+  pdl_wait();
+  pdl_trigger();
+  const int s = blockIdx.x, from = cow[s];
+  if (from < 0) return;
+  const int to = c.table[(size_t)s * c.max_pages + pos[s] / c.page];
+  const size_t bytes = (size_t)c.Hkv * c.page * c.D;
+  const size_t t = blockIdx.y * 256 + threadIdx.x, n = kCowParts * 256;
+  copy16(static_cast<uint8_t*>(c.k) + to * bytes, static_cast<const uint8_t*>(c.k) + from * bytes, bytes, t, n);
+  copy16(static_cast<uint8_t*>(c.v) + to * bytes, static_cast<const uint8_t*>(c.v) + from * bytes, bytes, t, n);
+  for (size_t h = t; h < (size_t)c.Hkv; h += n) {
+    c.k_scale[(size_t)to * c.Hkv + h] = c.k_scale[(size_t)from * c.Hkv + h];
+    c.v_scale[(size_t)to * c.Hkv + h] = c.v_scale[(size_t)from * c.Hkv + h];
+  }
+}
+
+// ------------------------------------------------------------------------------ compact
+
+// ws: int count, then (256-byte aligned) int number[n_pages] (the new number of a live page, -1
+// of a free one) and int live[n_pages] (the live pages in order)
+__global__ void __launch_bounds__(kScanThreads) kv_rank_kernel(const sage_kv_cache c, int to_pages,
+                                                               int* __restrict__ count, int* __restrict__ number,
+                                                               int* __restrict__ live) {
+  __shared__ int warp_sums[32];
+  constexpr int kPer = 16;
+  pdl_wait();
+  pdl_trigger();
+  int done = 0;
+  for (int p0 = 0; p0 < c.n_pages; p0 += kScanThreads * kPer) {
+    const int first = p0 + threadIdx.x * kPer;
+    unsigned used = 0;
+    for (int i = 0; i < kPer; ++i)
+      if (first + i < c.n_pages && c.refs[first + i] > 0) used |= 1u << i;
+    int total;
+    int r = done + block_exclusive(__popc(used), warp_sums, &total);
+    for (int i = 0; i < kPer && first + i < c.n_pages; ++i) {
+      const bool u = used >> i & 1;
+      number[first + i] = u ? r : -1;
+      if (u) live[r++] = first + i;
+    }
+    done += total;
+  }
+  if (threadIdx.x == 0) {
+    const bool fits = done <= to_pages;
+    *count = fits ? done : -1;
+    if (!fits) kv_error(c.status, kDevPages);
+  }
+}
+
+// Persistent CTAs: first the tables, lengths and refs, then the live pages, a piece at a time.
+__global__ void __launch_bounds__(256) kv_move_kernel(const sage_kv_cache c, const sage_kv_cache to,
+                                                      const int* __restrict__ count, const int* __restrict__ number,
+                                                      const int* __restrict__ live) {
+  pdl_wait();
+  pdl_trigger();
+  const int n = *count;
+  if (n < 0) return;
+  const size_t t = (size_t)blockIdx.x * 256 + threadIdx.x, nt = (size_t)gridDim.x * 256;
+  for (size_t i = t; i < (size_t)to.n_pages; i += nt) to.refs[i] = i < (size_t)n ? c.refs[live[i]] : 0;
+  for (size_t i = t; i < (size_t)n * c.Hkv; i += nt) {
+    const size_t from = (size_t)live[i / c.Hkv] * c.Hkv + i % c.Hkv;
+    to.k_scale[i] = c.k_scale[from];
+    to.v_scale[i] = c.v_scale[from];
+  }
+  for (size_t i = t; i < (size_t)c.n_slots * c.max_pages; i += nt) {
+    const size_t s = i / c.max_pages, j = i % c.max_pages;
+    if ((long long)j * c.page < c.lengths[s]) {
+      const int page = c.table[i];
+      const bool ok = (unsigned)page < (unsigned)c.n_pages;
+      to.table[i] = ok ? number[page] : -1;
+      if (!ok) kv_error(c.status, kDevIndex);
+    }
+  }
+  for (size_t i = t; i < (size_t)c.n_slots; i += nt) to.lengths[i] = c.lengths[i];
+  const size_t bytes = (size_t)c.Hkv * c.page * c.D;
+  for (size_t i = blockIdx.x; i < 2 * (size_t)n; i += gridDim.x) {
+    const bool v = i & 1;
+    const size_t k = i >> 1;
+    copy16(static_cast<uint8_t*>(v ? to.v : to.k) + k * bytes,
+           static_cast<const uint8_t*>(v ? c.v : c.k) + (size_t)live[k] * bytes, bytes, threadIdx.x, 256);
+  }
+}
+
+}  // namespace
+
+size_t kv_compact_ws_bytes(int n_pages) { return 256 + 2 * (((size_t)n_pages * 4 + 255) & ~(size_t)255); }
+
+int launch_kv_append(const sage_kv_cache& c, const void* K, const void* V, const float* k_shift, const int* slots,
+                     const int* pos, const int* n_new, int B, int Nn, cudaStream_t st) {
+  AppendParams p{c, static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), k_shift, slots, pos,
+                 n_new, B, Nn};
+  auto kern = c.D == 128 ? append_kernel_for<128>(c.page, c.kind) : append_kernel_for<64>(c.page, c.kind);
+  const unsigned pages = (unsigned)(((long long)Nn + c.page - 2) / c.page + 1);  // that Nn tokens can touch
+  ScopedTimer timer("kv_append", st);
+  if (launch_pdl(kern, dim3(pages, 2 * c.Hkv, B), dim3(kAppendThreads), 0, st, p) != cudaSuccess) return 3;
+  return cudaGetLastError() == cudaSuccess ? 0 : 3;
+}
+
+int launch_kv_fork(const sage_kv_cache& c, const int* src, cudaStream_t st) {
+  ScopedTimer timer("kv_pages", st);
+  if (launch_pdl(kv_fork_kernel, dim3(c.n_slots), dim3(256), 0, st, c, src) != cudaSuccess) return 3;
+  return cudaGetLastError() == cudaSuccess ? 0 : 3;
+}
+
+int launch_kv_truncate(const sage_kv_cache& c, const int* keep, cudaStream_t st) {
+  ScopedTimer timer("kv_pages", st);
+  if (launch_pdl(kv_truncate_kernel, dim3(c.n_slots), dim3(128), 0, st, c, keep) != cudaSuccess) return 3;
+  return cudaGetLastError() == cudaSuccess ? 0 : 3;
+}
+
+int launch_kv_extend(const sage_kv_cache& c, const int* n_new, int* pos, int* cow, cudaStream_t st) {
+  ScopedTimer timer("kv_pages", st);
+  const size_t smem = ((size_t)c.n_slots + 1) * 4;  // at most 32 KB (kKvMaxSlots)
+  if (launch_pdl(kv_extend_kernel, dim3(1), dim3(kScanThreads), smem, st, c, n_new, pos, cow) != cudaSuccess ||
+      launch_pdl(kv_cow_kernel, dim3(c.n_slots, kCowParts), dim3(256), 0, st, c, (const int*)pos, (const int*)cow) !=
+          cudaSuccess)
+    return 3;
+  return cudaGetLastError() == cudaSuccess ? 0 : 3;
+}
+
+int launch_kv_compact(const sage_kv_cache& c, const sage_kv_cache& to, void* ws, cudaStream_t st) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  int* count = reinterpret_cast<int*>(w);
+  int* number = reinterpret_cast<int*>(w + 256);
+  int* live = reinterpret_cast<int*>(w + 256 + (((size_t)c.n_pages * 4 + 255) & ~(size_t)255));
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 3;
+  ScopedTimer timer("kv_compact", st);
+  if (launch_pdl(kv_rank_kernel, dim3(1), dim3(kScanThreads), 0, st, c, to.n_pages, count, number, live) !=
+          cudaSuccess ||
+      launch_pdl(kv_move_kernel, dim3(sms * 8), dim3(256), 0, st, c, to, (const int*)count, (const int*)number,
+                 (const int*)live) != cudaSuccess)
+    return 3;
+  return cudaGetLastError() == cudaSuccess ? 0 : 3;
+}
+
+}  // namespace sage

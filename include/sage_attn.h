@@ -61,7 +61,8 @@ typedef enum {
   SAGE_ERR_INVALID_ARG = 1, /* null or misaligned pointer, bad size, workspace too small */
   SAGE_ERR_UNSUPPORTED = 2, /* shape outside the supported set */
   SAGE_ERR_CUDA = 3,        /* a CUDA runtime call failed (launch, attribute, tensor map) */
-  SAGE_ERR_TIMEOUT = 4      /* a device-side wait ran out of its time budget */
+  SAGE_ERR_TIMEOUT = 4,     /* a device-side wait ran out of its time budget */
+  SAGE_ERR_NO_PAGES = 5     /* a cache pool has too few free pages (device status) */
 } sage_status;
 
 /* Pointers into a quantize workspace (for inspection and parity tests).
@@ -283,11 +284,114 @@ int sage_attn_fp4_bwd(const void *Q, const void *K, const void *V, const void *O
                       void *dQ, void *dK, void *dV, const void *ws, void *bwd_ws, size_t bwd_ws_bytes, int B, int H,
                       int N, int D, int causal, int qk_norm, int k_smooth, float sm_scale, void *stream);
 
+/*
+ * The 8-bit paged key/value cache: what a model trained with the calls above is served from.
+ * The training scheme quantizes K to INT8 in 64-token blocks and V to e4m3 ("SageBwd: A Trainable
+ * Low-bit Attention" (euno.news summary), Methodology 1); the cache holds K and V in either of the
+ * two formats with one fp32 scale per block and head, a block being a page.
+ *
+ * State, all of it device memory of the caller (one cache per layer):
+ *  - k, v: codes [n_pages, Hkv, page, D], one byte each, 16-byte aligned; k_scale, v_scale: fp32
+ *    [n_pages, Hkv].  A key is k = code * k_scale.  A page is `page` tokens of every head.
+ *  - table: int32 [n_slots, max_pages]; slot s (one sequence) holds lengths[s] tokens (int32) in the
+ *    pages table[s][0 .. ceil(lengths[s] / page)), in order.  What a row holds behind them is not
+ *    read and may be anything.
+ *  - refs: int32 [n_pages], 16-byte aligned: how many slots list the page; 0: the page is free.
+ *  - status: one int32, zero at the start: the device status word (sage_attn_get_status(status,
+ *    stream)).  SAGE_ERR_NO_PAGES: a slot could not be served; SAGE_ERR_INVALID_ARG: a number on the
+ *    device was out of its range (a slot, a length, a page), and what it asked for was left out.  Of
+ *    both the word keeps SAGE_ERR_INVALID_ARG.
+ *  An empty cache is lengths, refs and status zero.
+ * page is 16, 32, 64 or 128; D 64 or 128; n_slots at most 8192; max_pages * page below 2^31.
+ *
+ * The order of a serving step: sage_attn_kv_extend (room for the new tokens), sage_attn_kv_append
+ * (their keys and values), sage_attn_kv_attention (their queries).  All sizes that change from step to
+ * step are read on the device, so a captured CUDA graph of the step can be replayed.  Calls that
+ * change one cache, or use one workspace, must not overlap on the GPU.
+ */
+typedef enum { SAGE_KV_INT8 = 0, SAGE_KV_E4M3 = 1 } sage_kv_kind;
+
+typedef struct sage_kv_cache {
+  void *k, *v;              /* [n_pages, Hkv, page, D] codes */
+  float *k_scale, *v_scale; /* [n_pages, Hkv] */
+  int *table;               /* [n_slots, max_pages] */
+  int *lengths;             /* [n_slots] */
+  int *refs;                /* [n_pages] */
+  int *status;              /* [1] */
+  int n_pages, Hkv, page, D, n_slots, max_pages;
+  int kind;                 /* sage_kv_kind */
+} sage_kv_cache;
+
+/*
+ * Quantize new tokens into their pages.  K, V: bf16 [B, Hkv, Nn, D]; batch row b belongs to slot
+ * s = slots[b] (slots NULL: s = b); its first n_new[s] tokens become tokens pos[s] .. of the slot
+ * (n_new, pos: int32 [n_slots], n_new[s] <= Nn; what K and V hold behind them is not read).  A slot
+ * with n_new[s] <= 0 or pos[s] < 0 (as sage_attn_kv_extend leaves a slot that it refused) is left alone.
+ * k_shift (NULL: none): fp32 [Hkv, D], 16-byte aligned, subtracted from every key (in fp32): K-smoothing
+ * with a fixed mean (SageBwd summary, Results).  A shift that is the same for every token of a head
+ * leaves the softmax as it is and moves LSE by -sm_scale q . k_shift.
+ * Per (page, head), with a = max|x| over the call's tokens in the page and r = RN32(1/127) (INT8) or
+ * RN32(1/448) (e4m3): s = RN32(a r) if the page holds no earlier token, else max(its scale, RN32(a r));
+ * code = rint(RN32(x / s)) or e4m3(RN32(x / s)), saturating.  Where s has grown, an earlier code c becomes
+ * the code of RN32(c s_old) under s.  A block whose s is 0 has codes 0.  Values must be finite.
+ * Not written, with SAGE_ERR_INVALID_ARG in the status word: a page that is not reserved or that another
+ * slot lists too (refs != 1); a batch row that names the slot of an earlier row again.
+ */
+int sage_attn_kv_append(const sage_kv_cache *cache, const void *K, const void *V, const float *k_shift,
+                        const int *slots, const int *pos, const int *n_new, int B, int Nn, void *stream);
+
+/*
+ * Attention of queries over the cache.  Q: bf16 [B, H, Nq, D], query head h reads key/value head
+ * h / (H / Hkv); O as Q, LSE fp32 [B, H, Nq].  Batch row b reads slot slots[b] (NULL: slot b; a slot may
+ * be named by several rows); its first q_len[b] queries count (q_len int32 [B]; NULL: Nq), rows behind
+ * them are neither read nor written.  With len = lengths[slot]: causal (causal != 0) lets query i see
+ * keys j <= len - q_len + i, as for the newest q_len tokens of the sequence; otherwise every query sees
+ * all len keys (an encoder's states of another length).
+ * S = sm_scale q . k, O = softmax(S) V, LSE = log sum e^S; a row that sees no key has O = 0 and
+ * LSE = -infinity.  Codes enter the products exactly; P is rounded to fp16 relative to the running
+ * maximum; everything else is fp32.  sm_scale <= 0 selects 1/sqrt(D).
+ * ws: sage_attn_kv_ws_bytes(B, H, Hkv, D, Nq) bytes, 16-byte aligned, contents free before and after.
+ * Deterministic.  B is at most 4096.
+ */
+size_t sage_attn_kv_ws_bytes(int B, int H, int Hkv, int D, int Nq);
+int sage_attn_kv_attention(const sage_kv_cache *cache, const void *Q, const int *slots, const int *q_len, void *O,
+                           float *LSE, void *ws, size_t ws_bytes, int B, int H, int Nq, int causal, float sm_scale,
+                           void *stream);
+
+/*
+ * Pages.  Arrays are int32 [n_slots], one entry per slot; results do not depend on the order in which
+ * the GPU works.
+ *  - fork: slot s with src[s] >= 0 takes over slot src[s]: its pages (shared, refs + 1) and length.  Slot
+ *    s must be empty and src[s] must not take over itself (else SAGE_ERR_INVALID_ARG in the status word,
+ *    and slot s is left alone).  src[s] < 0: nothing.
+ *  - extend: room for n_new[s] >= 0 more tokens: pos[s] = lengths[s], lengths[s] += n_new[s].  The pages
+ *    it takes are the free pages with the lowest numbers, in slot order.  A last page that is partly
+ *    filled and listed by another slot too is first copied to a page of the slot's own; cow[s] = the page
+ *    it was copied from (else -1).  Slots are served while the needs of the slots up to them fit in the
+ *    free pages; one that is not served has pos[s] = -1 and is otherwise left alone
+ *    (SAGE_ERR_NO_PAGES; past max_pages pages: SAGE_ERR_INVALID_ARG).
+ *  - truncate: slot s with keep[s] >= 0 keeps its first min(keep[s], lengths[s]) tokens and gives the
+ *    pages behind them back (refs - 1); keep[s] = 0 frees the slot.
+ *  - compact: the live pages of `cache` (refs > 0), in order, become pages 0, 1, ... of the pool `to`;
+ *    tables, lengths and refs of `to` follow (its refs behind them 0).  The caches have equal page, Hkv,
+ *    D, kind, n_slots and max_pages, may differ in n_pages, and share no memory but, if the caller
+ *    likes, the status word; errors go to the one of `cache`.  More live pages than `to` has:
+ *    SAGE_ERR_NO_PAGES, and `to` is left alone.
+ *    ws: sage_attn_kv_compact_ws_bytes(cache->n_pages) bytes, 16-byte aligned.
+ */
+int sage_attn_kv_fork(const sage_kv_cache *cache, const int *src, void *stream);
+int sage_attn_kv_extend(const sage_kv_cache *cache, const int *n_new, int *pos, int *cow, void *stream);
+int sage_attn_kv_truncate(const sage_kv_cache *cache, const int *keep, void *stream);
+size_t sage_attn_kv_compact_ws_bytes(int n_pages);
+int sage_attn_kv_compact(const sage_kv_cache *cache, const sage_kv_cache *to, void *ws, size_t ws_bytes,
+                         void *stream);
+
 /* Fill `views` with the device pointers inside a quantize workspace (qmean, dsb: NULL). */
 int sage_attn_ws_views(void *ws, int B, int H, int N, int D, sage_ws_views *views);
 
 /* Synchronise `stream`, read and clear the workspace status word.  Returns SAGE_OK
- * or SAGE_ERR_TIMEOUT (or SAGE_ERR_CUDA if the read itself failed). */
+ * or SAGE_ERR_TIMEOUT (or SAGE_ERR_CUDA if the read itself failed); for the status word of
+ * a cache also SAGE_ERR_NO_PAGES and SAGE_ERR_INVALID_ARG. */
 int sage_attn_get_status(void *ws, void *stream);
 
 /* Self-test of the bounded wait: launches one CTA that waits on a barrier nothing

@@ -1,0 +1,495 @@
+"""The 8-bit paged cache on the GPU (sage_attn_kv_*) against its plain numpy form (kv_ref.py):
+codes, scales, tables, lengths and refs bit for bit, attention within the roundings that its
+definition names (kv_ref.attention_tolerances)."""
+import numpy as np
+import pytest
+import torch
+
+import bit_trainable_attention_sagebwd_gb300 as sa
+import kv_ref
+
+pytestmark = pytest.mark.gpu
+
+
+def dev(x, dtype=torch.int32):
+    return torch.as_tensor(np.asarray(x)).to(dtype).cuda()
+
+
+def bf16(rng, shape, scale=1.0):
+    """Values on the GPU in bf16, and the same as fp32 on the host."""
+    t = torch.from_numpy((rng.standard_normal(shape) * scale).astype(np.float32)).to(torch.bfloat16)
+    return t.cuda(), t.float().numpy()
+
+
+def pair(n_pages, hkv, d, n_slots, max_pages, page, kind, poison=True):
+    """An empty cache on the GPU and its reference.  Free memory holds what earlier use may leave
+    there: the largest codes, NaN in e4m3 among them, NaN scales and page numbers out of range."""
+    c = sa.kv_cache(n_pages, hkv, d, n_slots, max_pages, page=page, kind=kind)
+    r = kv_ref.Cache(n_pages, hkv, d, n_slots, max_pages, page, kind)
+    if poison:
+        for a, b in ((c.k, r.k), (c.v, r.v)):
+            a.view(torch.int8).fill_(127)
+            b[:] = 127
+        for a, b in ((c.k_scale, r.k_scale), (c.v_scale, r.v_scale)):
+            a.fill_(float("nan"))
+            b[:] = np.nan
+        c.table.fill_(-2 ** 31)
+        r.table[:] = -2 ** 31
+    return c, r
+
+
+def same_state(c, r):
+    torch.cuda.synchronize()
+    assert np.array_equal(c.lengths.cpu().numpy(), r.lengths)
+    assert np.array_equal(c.refs.cpu().numpy(), r.refs)
+    for s, n in enumerate(r.lengths):
+        m = r.pages(int(n))
+        assert np.array_equal(c.table[s, :m].cpu().numpy(), r.table[s, :m]), f"table of slot {s}"
+    for name in ("k", "v"):
+        got, want = getattr(c, name).view(torch.uint8).cpu().numpy(), getattr(r, name)
+        assert np.array_equal(got, want), f"{name}: {np.sum(got != want)} codes differ"
+        assert np.array_equal(getattr(c, name + "_scale").cpu().numpy(), getattr(r, name + "_scale"), equal_nan=True)
+
+
+def fill(c, r, rng, lengths, shift=None, step=None):
+    """Append `lengths` tokens to the slots, at most `step` at a time."""
+    left = np.asarray(lengths)
+    step = step or max(1, int(left.max(initial=1)))
+    while left.any():
+        n = np.minimum(left, step)
+        pos = sa.kv_extend(c, dev(n))
+        rpos, _ = r.extend(n)
+        assert np.array_equal(pos.cpu().numpy(), rpos)
+        shape = (len(left), r.k.shape[1], int(n.max()), r.k.shape[3])
+        k, kf = bf16(rng, shape, 1.5)
+        v, vf = bf16(rng, shape)
+        sa.kv_append(c, k, v, pos, dev(n), k_shift=None if shift is None else dev(shift, torch.float32))
+        r.append(kf, vf, rpos, n, shift=shift)
+        left = left - n
+
+
+def check_attention(c, r, rng, H, Nq, causal=True, slots=None, q_len=None, sm_scale=None, q_scale=1.0, **kw):
+    B = c.n_slots if slots is None else len(slots)
+    q, qf = bf16(rng, (B, H, Nq, c.d), q_scale)
+    o = torch.full((B, H, Nq, c.d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, H, Nq), 7.0, device="cuda")
+    sa.kv_attention(q, c, causal=causal, slots=None if slots is None else dev(slots), q_len=None if q_len is None else dev(q_len),
+                    sm_scale=sm_scale, o=o, lse=lse, **kw)
+    torch.cuda.synchronize()
+    assert sa.get_status(c.status) == sa.SAGE_OK
+    compare(o, lse, r.attention(qf.astype(np.float64), causal, slots, q_len, sm_scale), int(r.lengths.max(initial=0)), c.d)
+    return q, o, lse
+
+
+def compare(o, lse, want, n, d):
+    wo, wl, pv, av, mag, rows = want
+    tol_o, tol_l = kv_ref.attention_tolerances(wo, wl, pv, av, mag, n, d)
+    go, gl = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.all(go[~rows] == 7.0) and np.all(gl[~rows] == 7.0), "rows behind q_len were written"
+    empty = rows & (wl == -np.inf)
+    assert np.all(go[empty] == 0.0) and np.all(gl[empty] == -np.inf)
+    full = rows & ~empty
+    eo, el = np.abs(go[full] - wo[full]), np.abs(gl[full] - wl[full])
+    assert np.all(eo <= tol_o[full]), f"O off by up to {np.max(eo / tol_o[full]):.3g} of its tolerance"
+    assert np.all(el <= tol_l[full]), f"LSE off by up to {np.max(el / tol_l[full]):.3g} of its tolerance"
+
+
+# ------------------------------------------------------------------------------ append
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("page,d", [(16, 64), (16, 128), (32, 128), (64, 64), (64, 128), (128, 64), (128, 128)])
+def test_append_codes(kind, page, d):
+    """Prompts of odd lengths, then tokens one and a few at a time (pages begun before, whose scale
+    grows or stays), with and without a shift of the keys: bit for bit."""
+    rng = np.random.default_rng(page + d)
+    c, r = pair(40, 3, d, 4, 20, page, kind)
+    shift = rng.standard_normal((3, d)).astype(np.float32)
+    fill(c, r, rng, [0, 1, page - 1, page + 1], shift)
+    same_state(c, r)
+    fill(c, r, rng, [5, 0, 2, 3], shift, step=1)
+    same_state(c, r)
+    fill(c, r, rng, [2 * page + 3, 1, page, 0])
+    same_state(c, r)
+    assert sa.get_status(c.status) == sa.SAGE_OK
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_append_extreme_values(kind):
+    """Blocks of zeros (scale 0), the largest and the smallest bf16 (subnormal scales), a page whose
+    scale grows by 2^60, and quotients that fall on rounding borders."""
+    c, r = pair(8, 1, 64, 1, 8, 16, kind, poison=False)
+    rng = np.random.default_rng(5)
+    big = float(torch.finfo(torch.bfloat16).max)
+    steps = [np.zeros((3, 64)), np.full((2, 64), 2.0 ** -133), np.full((1, 64), 2.0 ** -70), rng.standard_normal((4, 64)),
+             np.where(rng.random((16, 64)) < 0.5, big, -big), np.arange(-32, 32)[None].repeat(3, 0) * 0.5,
+             np.full((3, 64), 2.0 ** -130), rng.standard_normal((9, 64)) * 2.0 ** -126]
+    for x in steps:
+        k = torch.from_numpy(x.astype(np.float32)).to(torch.bfloat16)[None, None]
+        n = dev([x.shape[0]])
+        pos = sa.kv_extend(c, n)
+        rpos, _ = r.extend([x.shape[0]])
+        sa.kv_append(c, k.cuda(), (-k).cuda().contiguous(), pos, n)
+        r.append(k.float().numpy(), -k.float().numpy(), rpos, [x.shape[0]])
+        same_state(c, r)
+
+
+def test_append_slots_and_padding():
+    """Rows that belong to other slots, rows without tokens, NaN behind the tokens that count."""
+    rng = np.random.default_rng(11)
+    c, r = pair(30, 2, 64, 5, 8, 16, "int8")
+    n = np.array([3, 0, 17, 1, 9])
+    pos, (rpos, _) = sa.kv_extend(c, dev(n)), r.extend(n)
+    slots = [4, 2, 0]
+    k, kf = bf16(rng, (3, 2, 20, 64))
+    v, vf = bf16(rng, (3, 2, 20, 64))
+    for b, s in enumerate(slots):
+        k[b, :, n[s]:] = float("nan")
+        v[b, :, n[s]:] = float("inf")
+    sa.kv_append(c, k, v, pos, dev(n), slots=dev(slots))
+    r.append(kf, vf, rpos, n, slots=slots)
+    same_state(c, r)
+    assert sa.get_status(c.status) == sa.SAGE_OK
+
+
+def test_append_leaves_out_what_it_must_not_write():
+    rng = np.random.default_rng(12)
+    c, r = pair(30, 2, 64, 4, 4, 16, "int8")
+    fill(c, r, rng, [10, 20, 0, 0])
+    k, kf = bf16(rng, (4, 2, 4, 64))
+
+    def refused(pos, n, slots=None):
+        sa.kv_append(c, k, k, dev(pos), dev(n), slots=None if slots is None else dev(slots))
+        same_state(c, r)
+        assert sa.get_status(c.status) == sa.SAGE_ERR_INVALID_ARG
+        assert sa.get_status(c.status) == sa.SAGE_OK  # read and cleared
+
+    refused([0, 0, 0, 0], [0, 0, 2, 0])                      # slot 2 has no pages (its table is out of range)
+    refused([0, 63, 0, 0], [0, 4, 0, 0])                     # past the reserved pages and the table
+    refused([0, 0, 0, 0], [5, 0, 0, 0])                      # more tokens than K and V hold
+    refused([2 ** 31 - 8, 0, 0, 0], [4, 0, 0, 0])
+    refused([8, 0, 0, 0], [0, 0, 0, 0], [4, -1, 1, 0])       # slots that are not there
+    sa.kv_fork(c, dev([-1, -1, 0, -1]))                      # slots 0 and 2 share a page
+    r.fork([-1, -1, 0, -1])
+    refused([8, 0, 0, 0], [2, 0, 0, 0])
+    # a slot named twice: the first row counts
+    sa.kv_append(c, k, k, dev([0, 18, 0, 0]), dev([0, 2, 0, 0]), slots=dev([0, 1, 1, 2]))
+    r.append(kf[1:2], kf[1:2], [0, 18, 0, 0], [0, 2, 0, 0], slots=[1])
+    same_state(c, r)
+    assert sa.get_status(c.status) == sa.SAGE_ERR_INVALID_ARG
+
+
+# ------------------------------------------------------------------------------ attention
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+def test_attention_one_token(kind, d, page):
+    """Lengths of nothing, one, around a chunk of 16 and a page, and of several parts."""
+    rng = np.random.default_rng(page * d)
+    lengths = [0, 1, 15, 16, 17, page - 1, page, page + 1, 333, 700]
+    c, r = pair(200, 2, d, len(lengths), 60, page, kind)
+    fill(c, r, rng, lengths)
+    check_attention(c, r, rng, 8, 1)
+
+
+GROUPS = [(1, 1, 1), (1, 7, 1), (2, 8, 1), (3, 5, 2), (1, 16, 1), (1, 32, 1), (2, 3, 7), (2, 1, 16), (1, 4, 33), (2, 2, 70),
+          (1, 8, 130)]
+
+
+@pytest.mark.parametrize("hkv,g,nq", GROUPS)
+@pytest.mark.parametrize("d,kind", [(64, "e4m3"), (128, "int8"), (128, "e4m3")])
+def test_attention_groups_and_queries(hkv, g, nq, d, kind):
+    """Shared heads and several queries; slots in another order and twice, ragged q_len, more queries
+    than keys (rows that see nothing), causal and not."""
+    rng = np.random.default_rng(hkv + 10 * g + 100 * nq)
+    c, r = pair(60, hkv, d, 5, 10, 64, kind)
+    fill(c, r, rng, [130, 5, 0, 77, 200])
+    slots, q_len = [3, 0, 4, 1, 2, 0], [nq, max(1, nq - 1), (nq + 1) // 2, nq, nq, 0]
+    check_attention(c, r, rng, hkv * g, nq, True, slots, q_len)
+    check_attention(c, r, rng, hkv * g, nq, False, slots[:4], None, sm_scale=0.3)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+def test_attention_long(kind):
+    """One sequence of 20,011 tokens among short ones: cut over the whole GPU."""
+    rng = np.random.default_rng(3)
+    c, r = pair(700, 1, 128, 3, 400, 64, kind)
+    fill(c, r, rng, [20011, 1, 260])
+    check_attention(c, r, rng, 4, 1)
+    check_attention(c, r, rng, 4, 3, slots=[0, 2])
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_sharp_and_wide_values(nq):
+    """Logits of hundreds (one key takes all), tiny and huge queries (their products stay in range
+    after the row's power of two), pages whose V scales differ by 2^40."""
+    rng = np.random.default_rng(8)
+    c, r = pair(20, 1, 128, 2, 10, 16, "int8")
+    fill(c, r, rng, [100, 37], step=16)
+    for p in range(20):
+        f = np.float32(2.0 ** ((p % 5) * 10 - 20))
+        c.v_scale[p] *= float(f)
+        r.v_scale[p] *= f
+    for q_scale, sm_scale in ((60.0, None), (2.0 ** -100, 2.0 ** 98), (2.0 ** 100, 2.0 ** -102), (0.0, None)):
+        check_attention(c, r, rng, 4, nq, sm_scale=sm_scale, q_scale=q_scale)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_bad_numbers_are_reported(nq):
+    """A length past the table, a slot and a page out of range: reported, nothing read out of range,
+    the other rows as ever."""
+    rng = np.random.default_rng(9)
+    c, r = pair(40, 1, 64, 4, 4, 16, "int8")
+    fill(c, r, rng, [40, 20, 33, 10])
+    q, qf = bf16(rng, (4, 2, nq, 64))
+    want = r.attention(qf.astype(np.float64))
+
+    def same(o, lse, rows):
+        compare(o[rows], lse[rows], [x[rows] for x in want], 40, 64)
+
+    same(*sa.kv_attention(q, c), [0, 1, 2, 3])
+    assert sa.get_status(c.status) == sa.SAGE_OK
+    c.lengths[0] = 65
+    c.table[2, 1] = 40
+    o, lse = sa.kv_attention(q, c)
+    assert sa.get_status(c.status) == sa.SAGE_ERR_INVALID_ARG
+    same(o, lse, [1, 3])
+    assert not o[0].any() and (lse[0] == -np.inf).all()
+    c.lengths[0] = -1
+    sa.kv_attention(q, c)
+    assert sa.get_status(c.status) == sa.SAGE_ERR_INVALID_ARG
+    c.lengths[0] = 40
+    o, lse = sa.kv_attention(q, c, slots=dev([1, 4, -1, 3]))
+    assert sa.get_status(c.status) == sa.SAGE_ERR_INVALID_ARG
+    same(o, lse, [3])
+    assert not o[1].any() and not o[2].any()
+
+
+def test_attention_offsets_past_32_bits():
+    """A pool of more than 2^32 codes, the sequence in its last pages."""
+    rng = np.random.default_rng(10)
+    n_pages, hkv, d, page = 33000, 8, 128, 128
+    kind = "e4m3"
+    c = sa.KVCache(*[torch.empty((n_pages, hkv, page, d), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2)],
+                   *[torch.empty((n_pages, hkv), device="cuda") for _ in range(2)],
+                   torch.zeros((1, 8), dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                   torch.ones(n_pages, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"))
+    assert n_pages * hkv * page * d > 2 ** 32
+    c.refs[-8:] = 0
+    r = kv_ref.Cache(8, hkv, d, 1, 8, page, kind)
+    n = 700
+    pos = sa.kv_extend(c, dev([n]))
+    rpos, _ = r.extend([n])
+    assert np.array_equal(c.table[0, :6].cpu().numpy() - (n_pages - 8), r.table[0, :6])
+    k, kf = bf16(rng, (1, hkv, n, d))
+    v, vf = bf16(rng, (1, hkv, n, d))
+    sa.kv_append(c, k, v, pos, dev([n]))
+    r.append(kf, vf, rpos, [n])
+    torch.cuda.synchronize()
+    assert np.array_equal(c.k[-8:-2].view(torch.uint8).cpu().numpy(), r.k[:6])
+    check_attention(c, r, rng, 16, 1)
+    check_attention(c, r, rng, 16, 20)
+
+
+# ------------------------------------------------------------------------------ pages
+
+@pytest.mark.parametrize("seed", range(4))
+def test_pages_random_walk(seed):
+    """Forks, extensions (shared last pages copied, pools that run out), truncations and compactions in a
+    random order, the state compared bit for bit after each."""
+    rng = np.random.default_rng(seed)
+    S, M, page = 9, 6, 16
+    c, r = pair(24, 2, 64, S, M, page, "int8", poison=False)
+    for step in range(30):
+        what = rng.integers(0, 4)
+        expect = {sa.SAGE_OK}
+        if what == 0:
+            src = np.where(rng.random(S) < 0.4, rng.integers(-1, S, S), -1)
+            if any(f >= 0 and (src[f] >= 0 or r.lengths[s]) for s, f in enumerate(src)):
+                expect = {sa.SAGE_ERR_INVALID_ARG}
+            sa.kv_fork(c, dev(src))
+            r.fork(src)
+        elif what == 1:
+            n = np.where(rng.random(S) < 0.6, rng.integers(0, 2 * page, S), 0)
+            pos, cow = torch.empty(S, dtype=torch.int32, device="cuda"), torch.empty(S, dtype=torch.int32, device="cuda")
+            sa.kv_extend(c, dev(n), pos=pos, cow=cow)
+            rpos, rcow = r.extend(n)
+            assert np.array_equal(pos.cpu().numpy(), rpos) and np.array_equal(cow.cpu().numpy(), rcow)
+            if (rpos < 0).any():
+                expect = {sa.SAGE_ERR_NO_PAGES, sa.SAGE_ERR_INVALID_ARG}
+            k, kf = bf16(rng, (S, 2, max(1, n.max()), 64))
+            sa.kv_append(c, k, k, pos, dev(n))
+            r.append(kf, kf, rpos, n)
+        elif what == 2:
+            keep = np.where(rng.random(S) < 0.5, rng.integers(0, M * page, S), -1)
+            sa.kv_truncate(c, dev(keep))
+            r.truncate(keep)
+        else:
+            c2, r2 = pair(24 + step % 3, 2, 64, S, M, page, "int8", poison=False)
+            sa.kv_compact(c, c2)
+            if r.compact(r2):
+                assert sa.get_status(c.status) == sa.SAGE_OK
+                c, r = c2, r2
+            else:
+                same_state(c2, r2)
+                expect = {sa.SAGE_ERR_NO_PAGES}
+        same_state(c, r)
+        assert sa.get_status(c.status) in expect
+        live = np.zeros(len(r.refs), np.int32)
+        for s in range(S):
+            live += np.bincount(r.table[s, :r.pages(int(r.lengths[s]))], minlength=len(live)).astype(np.int32)
+        assert np.array_equal(live, r.refs)
+
+
+def test_extend_many_slots_and_pages():
+    """More slots than the kernel has threads, more pages than one step of its scan looks at; an
+    exact fit, then a pool without a page left."""
+    rng = np.random.default_rng(2)
+    S, N = 2500, 40000
+    c = sa.kv_cache(N, 1, 64, S, 30, page=16)
+    r = kv_ref.Cache(N, 1, 64, S, 30, 16, "int8")
+    taken = rng.random(N) < 0.3
+    c.refs.copy_(dev(taken))
+    r.refs[:] = taken
+    n = rng.integers(0, 150, S)
+    assert np.array_equal(sa.kv_extend(c, dev(n)).cpu().numpy(), r.extend(n)[0])
+    same_state(c, r)
+    left = int((r.refs == 0).sum())
+    room = 30 * 16 - r.lengths
+    n = np.zeros(S, np.int64)
+    for s in range(S):  # whole pages until exactly none is left
+        give = min(left, room[s] // 16)
+        n[s] = give * 16
+        left -= give
+    assert left == 0
+    pos = sa.kv_extend(c, dev(n))
+    assert np.array_equal(pos.cpu().numpy(), r.extend(n)[0]) and (pos >= 0).all() and sa.get_status(c.status) == sa.SAGE_OK
+    same_state(c, r)
+    assert (r.refs > 0).all()
+    n = np.ones(S, np.int64)
+    assert np.array_equal(sa.kv_extend(c, dev(n)).cpu().numpy(), r.extend(n)[0])
+    same_state(c, r)
+    # some slots ask for more than their table holds: of two errors the word keeps that one
+    assert (r.lengths == 480).any() and sa.get_status(c.status) == sa.SAGE_ERR_INVALID_ARG
+    n = (r.lengths < 480).astype(np.int64)
+    assert np.array_equal(sa.kv_extend(c, dev(n)).cpu().numpy(), r.extend(n)[0])
+    same_state(c, r)
+    assert sa.get_status(c.status) == sa.SAGE_ERR_NO_PAGES
+
+
+def test_compact_too_small_and_refusals():
+    rng = np.random.default_rng(4)
+    c, r = pair(12, 1, 64, 3, 6, 16, "e4m3", poison=False)
+    fill(c, r, rng, [40, 33, 7])
+    to, rt = pair(6, 1, 64, 3, 6, 16, "e4m3", poison=False)
+    sa.kv_compact(c, to)
+    same_state(to, rt)  # seven live pages do not fit in six: left alone
+    assert sa.get_status(c.status) == sa.SAGE_ERR_NO_PAGES
+    to, rt = pair(7, 1, 64, 3, 6, 16, "e4m3", poison=False)
+    to.refs.fill_(3)
+    sa.kv_compact(c, to)
+    r.compact(rt)
+    same_state(to, rt)
+    with pytest.raises(sa.SageError):
+        sa.kv_compact(c, c)
+    with pytest.raises(ValueError):
+        sa.kv_extend(c, dev([1, 2]))
+    with pytest.raises(ValueError):
+        sa.kv_attention(torch.zeros((1, 1, 1, 64), device="cuda"), c)  # fp32 queries
+    with pytest.raises(ValueError):
+        sa.kv_attention(torch.zeros((4, 1, 1, 64), dtype=torch.bfloat16, device="cuda"), c)  # rows without slots
+    with pytest.raises(ValueError):
+        q = torch.zeros((1, 2, 3, 64), dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+        sa.kv_attention(q, c, slots=dev([0]))
+
+
+# ------------------------------------------------------------------------------ together
+
+def test_serving_run_in_graphs_and_streams():
+    """As a server uses them: prompts, a fork into samples, a decoding step captured once and replayed
+    while lengths, pages and inputs change, on a stream of its own; a second captured graph (another
+    batch) shares the workspace.  Every step against the reference."""
+    rng = np.random.default_rng(6)
+    S, H, hkv, d = 6, 8, 2, 128
+    c, r = pair(64, hkv, d, S, 12, 16, "int8", poison=False)
+    fill(c, r, rng, [50, 33, 0, 0, 0, 0])
+    src = [-1, -1, 0, 0, 1, 1]
+    sa.kv_fork(c, dev(src))
+    r.fork(src)
+    n = dev(np.ones(S))
+    k, v = (torch.zeros((S, hkv, 1, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros((S, H, 1, d), dtype=torch.bfloat16, device="cuda")
+    pos, cow = torch.empty_like(n), torch.empty_like(n)
+    o, lse = torch.empty_like(q), torch.empty((S, H, 1), device="cuda")
+    ws = sa.alloc_kv_ws(c, S, H, 1)
+    q2 = torch.zeros((2, H, 1, d), dtype=torch.bfloat16, device="cuda")
+    o2, lse2 = torch.empty_like(q2), torch.empty((2, H, 1), device="cuda")
+    slots2 = dev([5, 0])
+    assert sa.alloc_kv_ws(c, 2, H, 1).numel() <= ws.numel()
+
+    def step():
+        sa.kv_extend(c, n, pos=pos, cow=cow)
+        sa.kv_append(c, k, v, pos, n)
+        sa.kv_attention(q, c, o=o, lse=lse, ws=ws)
+
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    saved = [t.clone() for t in (c.lengths, c.refs, c.table, c.k.view(torch.int8), c.v.view(torch.int8), c.k_scale, c.v_scale)]
+    with torch.cuda.stream(stream):
+        step()  # (and back)
+        for t, x in zip((c.lengths, c.refs, c.table, c.k.view(torch.int8), c.v.view(torch.int8), c.k_scale, c.v_scale), saved):
+            t.copy_(x)
+        stream.synchronize()
+        graph, graph2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step()
+        with torch.cuda.graph(graph2, stream=stream):
+            sa.kv_attention(q2, c, slots=slots2, o=o2, lse=lse2, ws=ws)
+    for i in range(20):
+        kb, kf = bf16(rng, (S, hkv, 1, d))
+        vb, vf = bf16(rng, (S, hkv, 1, d))
+        qb, qf = bf16(rng, (S, H, 1, d))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(stream):
+            k.copy_(kb), v.copy_(vb), q.copy_(qb), q2.copy_(qb[[5, 0]])
+            graph.replay()
+            graph2.replay()
+        torch.cuda.synchronize()
+        one = np.ones(S, np.int64)
+        rpos, _ = r.extend(one)
+        r.append(kf, vf, rpos, one)
+        same_state(c, r)
+        want = r.attention(qf.astype(np.float64))
+        compare(o, lse, want, 80, d)
+        compare(o2, lse2, [x[[5, 0]] for x in want], 80, d)
+    assert sa.get_status(c.status) == sa.SAGE_OK
+    # the same call twice gives the same bits
+    a, b = (sa.kv_attention(q, c) for _ in range(2))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    keep = [0, -1, 10, 0, 0, 60]
+    sa.kv_truncate(c, dev(keep))
+    r.truncate(keep)
+    c2, r2 = pair(20, hkv, d, S, 12, 16, "int8", poison=False)
+    sa.kv_compact(c, c2)
+    r.compact(r2)
+    same_state(c2, r2)
+    check_attention(c2, r2, rng, H, 5, q_len=[5, 3, 1, 5, 5, 5])
+
+
+def test_prompt_in_chunks_equals_prompt_at_once():
+    """A prompt attended over in chunks against the same prompt in one call (the same cache)."""
+    rng = np.random.default_rng(7)
+    c, r = pair(20, 2, 128, 1, 20, 64, "e4m3")
+    fill(c, r, rng, [300])
+    q, o, lse = check_attention(c, r, rng, 4, 300)
+    c.lengths.fill_(0)
+    at = 0
+    for n in (64, 1, 100, 135):
+        c.lengths.add_(n)
+        r.lengths[0] = at + n
+        part = q[:, :, at:at + n].contiguous()
+        po, pl = torch.full_like(part, 7.0), torch.full((1, 4, n), 7.0, device="cuda")
+        sa.kv_attention(part, c, o=po, lse=pl)
+        torch.cuda.synchronize()
+        compare(po, pl, r.attention(part.double().cpu().numpy()), 300, 128)
+        at += n
