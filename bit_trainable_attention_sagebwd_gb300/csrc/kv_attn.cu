@@ -21,12 +21,8 @@
 //    exact in fp16 for every element within 2^-25 of the row's largest.  P is rounded to fp16
 //    (2^-12 relative, p <= 1): bf16, the output's type, would lose more than the output's own
 //    rounding.  Statistics, scales and sums are fp32.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "kv.h"
+#include "kv_attn.cuh"
 #include "launch.h"
-#include "ptx.cuh"
 #include "timer.h"
 
 namespace sage {
@@ -37,25 +33,7 @@ constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kChunk = 16;        // tokens of one step of a warp; a page is a whole number of them
 constexpr int kStages = 4;        // chunks of a warp in flight
 constexpr int kCtasPerSm = 3;     // the ring (4 warps x 4 chunks x 2 x 16 D bytes) of D = 128 is 64 KB
-constexpr int kMaxWorkers = 1024;
 
-struct AttnParams {
-  sage_kv_cache c;
-  const __nv_bfloat16* Q;
-  const int *slots, *q_len;
-  __nv_bfloat16* O;
-  float* LSE;
-  int2* info;      // first and last worker of each unit
-  float* part;     // two partial results of each worker: [R][D] sums, then [R] maxima and [R] row sums
-  int B, H, G, Nq, tiles, causal;
-  float alpha;     // sm_scale log2 e
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -81,33 +59,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ uint32_t h2bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-
-// Two codes as fp16.  int8, with the sign bit flipped (byte c + 128): 0x6400 + byte is the fp16
-// 1024 + c + 128.  e4m3: sign, exponent and fraction moved to fp16's places give the value times
-// 2^-8 (subnormal codes too), which kCodeUnit takes back in the scales; every byte is finite.
-template <int KIND>
-constexpr float kCodeUnit = KIND == SAGE_KV_INT8 ? 1.f : 256.f;
-
-// bytes (0, 1) and (2, 3) of a word
-template <int KIND>
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if (KIND == SAGE_KV_INT8) {
-    w ^= 0x80808080u;
-    lo = hsub2(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u);
-    hi = hsub2(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u);
-  } else {
-    const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
-    lo = (a & 0x80008000u) | ((a >> 1) & 0x3f803f80u);
-    hi = (b & 0x80008000u) | ((b >> 1) & 0x3f803f80u);
-  }
-}
-
 template <int D>
 struct Ring {
   static constexpr int kPieces = D / 32;                  // 16-byte K pieces of a lane and chunk
@@ -142,44 +93,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
   pdl_wait();
   pdl_trigger();
 
-  auto length_of = [&](int b, int& slot) {
-    slot = p.slots ? p.slots[b] : b;
-    int len = 0;
-    bool bad = (unsigned)slot >= (unsigned)c.n_slots;
-    if (!bad) {
-      len = c.lengths[slot];
-      bad = len < 0 || (long long)len > (long long)c.max_pages * c.page;
-    }
-    if (bad) {
-      atomicMax(c.status, kDevIndex);
-      slot = 0, len = 0;
-    }
-    return len;
-  };
   // a unit without keys still has one (empty) chunk: its rows are written like any other's
   const int per_b = c.Hkv * p.tiles;
-  {
-    const int n = (p.B + kThreads - 1) / kThreads, b0 = tid * n, b1 = min(p.B, b0 + n);
-    long long sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      int slot;
-      const int len = length_of(b, slot);
-      pre[b] = sum;
-      sum += (long long)max(1, (len + kChunk - 1) / kChunk) * per_b;
-    }
-    long long s = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += x;
-    }
-    if (lane == 31) wsum[warp] = s;
-    __syncthreads();
-    long long base = s - sum;
-    for (int w = 0; w < warp; ++w) base += wsum[w];
-    for (int b = b0; b < b1; ++b) pre[b] += base;
-    if (tid == kThreads - 1) pre[p.B] = base + sum;
-  }
+  prefix_of<kThreads>(p.B, pre, wsum, [&](int b) {
+    int slot;
+    return (long long)max(1, (row_length(p, b, slot) + kChunk - 1) / kChunk) * per_b;
+  });
   __syncthreads();
   const long long total = pre[p.B];
   // a worker takes at least one chunk for each of its warps
@@ -189,16 +108,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
   auto start_of = [&](int w) { return total * w / workers; };
   long long at = start_of(w0);
   const long long stop = start_of(w0 + 1);
-  int b = 0;
-  {
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] <= at) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-  }
+  int b = row_at(pre, p.B, at);
 
   const uint32_t my_ring = smem_u32(ring) + warp * Ring<D>::kWarpBytes;
   const uint8_t* my_ring_p = ring + warp * Ring<D>::kWarpBytes;
@@ -210,13 +120,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
     while (pre[b + 1] <= at) ++b;
     Unit u;
     u.b = b;
-    u.len = length_of(b, u.slot);
+    u.len = row_length(p, b, u.slot);
     u.chunks = max(1, (u.len + kChunk - 1) / kChunk);
     const int in_b = (int)((at - pre[b]) / u.chunks);
     const long long unit_at = pre[b] + (long long)in_b * u.chunks;
-    u.hk = in_b / p.tiles;
-    u.tile = in_b % p.tiles;
-    u.q_len = p.q_len ? max(0, min(p.Nq, p.q_len[b])) : p.Nq;
+    u.tile = in_b / c.Hkv;
+    u.hk = in_b % c.Hkv;
+    u.q_len = row_queries(p, b);
     const int c0 = (int)(at - unit_at);
     const int c1 = (int)min((long long)u.chunks, stop - unit_at);
     const long long unit_id = (long long)b * per_b + in_b;
@@ -252,9 +162,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      // the row's largest element comes to [2^8, 2^9)
-      const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -110), 126);
-      const float up = __uint_as_float((uint32_t)(127 + 8 - ex) << 23), down = __uint_as_float((uint32_t)(127 - 8 + ex) << 23);
+      float up, down;
+      row_power(top, up, down);
 #pragma unroll
       for (int s = 0; s < NK; ++s) {
         qf[t][s][0] = h2bits(__floats2half2_rn(x[s][0] * up, x[s][1] * up));
@@ -262,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
       }
       const float a = p.alpha * down * kCodeUnit<KIND>;
       // (a row that is not there holds q = 0 and masks nothing; it is not stored)
-      const int end = live && p.causal ? max(0, min(u.len, u.len - u.q_len + i + 1)) : u.len;
+      const int end = live ? row_end(p, u.len, u.q_len, i) : u.len;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         ar[t][e] = __shfl_sync(0xffffffffu, a, (2 * tig + e) * 4);
@@ -505,31 +414,31 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
   }
 }
 
-// One CTA per (unit that was cut, row): the parts in order, a quarter of them to each warp.
-template <int D>
+// Joins the parts of the units that were cut, in their order.  WARPS = 4: one CTA per (unit, row),
+// a quarter of the parts to each warp (few units, many parts).  WARPS = 1: four rows to a CTA, one
+// to each warp.
+template <int D, int WARPS>
 __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R) {
   constexpr int E = D / 32;  // channels of a lane
   pdl_wait();
   pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long unit = blockIdx.x;
-  const int r = blockIdx.y;
+  const int r = WARPS == 4 ? blockIdx.y : blockIdx.y * 4 + warp;
+  const int per_b = p.c.Hkv * p.tiles, b = (int)(unit / per_b), in_b = (int)(unit % per_b);
+  const int hk = in_b % p.c.Hkv, row = in_b / p.c.Hkv * R + r, i = row / p.G;
+  if (i >= row_queries(p, b)) return;
   const int2 w = p.info[unit];
   if (w.x == w.y) return;
-  const int per_b = p.c.Hkv * p.tiles, b = (int)(unit / per_b), in_b = (int)(unit % per_b);
-  const int hk = in_b / p.tiles, row = in_b % p.tiles * R + r, i = row / p.G;
-  const int q_len = p.q_len ? max(0, min(p.Nq, p.q_len[b])) : p.Nq;
-  if (i >= q_len) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __shared__ float sm[4], sl[4], so[4][D];
   const size_t stride = (size_t)R * (D + 2);
   auto part_of = [&](int k) { return p.part + (size_t)(k == w.x ? 2 * k + 1 : 2 * k) * stride; };
   float m = -INFINITY, l = 0.f, o[E] = {};
-  for (int k0 = w.x + warp; k0 <= w.y; k0 += 16) {
+  for (int k0 = w.x + (WARPS == 4 ? warp : 0); k0 <= w.y; k0 += 4 * WARPS) {
     // four parts at a time, their loads in flight together
     float mm[4], ll[4], oo[4][E];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int k = k0 + 4 * q;
+      const int k = k0 + WARPS * q;
       mm[q] = -INFINITY, ll[q] = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) oo[q][e] = 0.f;
@@ -557,6 +466,15 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R)
     }
     m = mn;
   }
+  const size_t orow = ((size_t)b * p.H + (size_t)hk * p.G + row % p.G) * p.Nq + i;
+  if (WARPS == 1) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) p.O[orow * D + e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
+    if (lane == 0) p.LSE[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    return;
+  }
+  __shared__ float sm[4], sl[4], so[4][D];
   if (lane == 0) sm[warp] = m, sl[warp] = l;
 #pragma unroll
   for (int e = 0; e < E; ++e) so[warp][e * 32 + lane] = o[e];
@@ -572,42 +490,46 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R)
     ls = fmaf(f, sl[k], ls);
     x = fmaf(f, so[k][d], x);
   }
-  const size_t orow = ((size_t)b * p.H + (size_t)hk * p.G + row % p.G) * p.Nq + i;
   p.O[orow * D + d] = __float2bfloat16_rn(ls > 0.f ? x / ls : 0.f);
   if (d == 0) p.LSE[orow] = ls > 0.f ? (mt + log2f(ls)) * 0.69314718055994531f : -INFINITY;
 }
 
-// row tiles of 8 where all rows of a shared head fit in one, of 16 where they do not
-int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
-
 template <int D, int KIND, int RT>
-int launch_attn(const AttnParams& p, int sms, cudaStream_t st) {
+int launch_few(const AttnParams& p, int sms, cudaStream_t st) {
   auto kern = kv_attn_kernel<D, KIND, RT>;
   const size_t smem = (size_t)kWarps * Ring<D>::kWarpBytes + ((size_t)p.B + 1) * 8;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 3;
   const int grid = sms * kCtasPerSm < kMaxWorkers ? sms * kCtasPerSm : kMaxWorkers;
-  ScopedTimer timer("kv_attention", st);
-  const long long units = (long long)p.B * p.c.Hkv * p.tiles;
-  if (launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p) != cudaSuccess ||
-      launch_pdl(kv_join_kernel<D>, dim3((unsigned)units, 8 * RT), dim3(128), 0, st, p, 8 * RT) != cudaSuccess)
-    return 3;
-  return cudaGetLastError() == cudaSuccess ? 0 : 3;
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p) == cudaSuccess ? 0 : 3;
 }
 template <int D, int KIND>
-int launch_attn_rt(const AttnParams& p, int rt, int sms, cudaStream_t st) {
-  return rt == 1 ? launch_attn<D, KIND, 1>(p, sms, st) : launch_attn<D, KIND, 2>(p, sms, st);
+int launch_few(const AttnParams& p, int rows, int sms, cudaStream_t st) {
+  return rows == 8 ? launch_few<D, KIND, 1>(p, sms, st) : launch_few<D, KIND, 2>(p, sms, st);
 }
 
+// Query rows of a unit: 8 where all rows of a shared head fit in one, 16 up to kFewRows rows, then
+// the tensor-core kernel's 256.
+constexpr long long kFewRows = 32;
+
 }  // namespace
+
+int launch_kv_few(const AttnParams& p, int kind, int rows, int sms, cudaStream_t st) {
+  if (p.c.D == 128)
+    return kind == SAGE_KV_INT8 ? launch_few<128, SAGE_KV_INT8>(p, rows, sms, st)
+                                : launch_few<128, SAGE_KV_E4M3>(p, rows, sms, st);
+  return kind == SAGE_KV_INT8 ? launch_few<64, SAGE_KV_INT8>(p, rows, sms, st)
+                              : launch_few<64, SAGE_KV_E4M3>(p, rows, sms, st);
+}
 
 KvAttnWs kv_attn_ws_layout(int B, int H, int Hkv, int D, int Nq) {
   KvAttnWs L{};
   const long long rows = (long long)(H / Hkv) * Nq;
-  L.rows = 8 * row_tiles((int)(rows < 16 ? rows : 16));
+  L.rows = rows <= 8 ? 8 : rows <= kFewRows ? 16 : kChunkRows;
   L.tiles = (int)((rows + L.rows - 1) / L.rows);
   L.info = 0;
   L.part = ((size_t)B * Hkv * L.tiles * 8 + 255) & ~(size_t)255;
-  L.total = L.part + (size_t)kMaxWorkers * 2 * L.rows * (D + 2) * 4;
+  const size_t workers = L.rows == kChunkRows ? kMaxChunkWorkers : kMaxWorkers;
+  L.total = L.part + workers * 2 * L.rows * (D + 2) * 4;
   return L;
 }
 
@@ -635,12 +557,14 @@ int launch_kv_attention(const sage_kv_cache& c, const void* Q, const int* slots,
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 3;
-  const int rt = L.rows / 8;
-  if (c.D == 128)
-    return c.kind == SAGE_KV_INT8 ? launch_attn_rt<128, SAGE_KV_INT8>(p, rt, sms, st)
-                                  : launch_attn_rt<128, SAGE_KV_E4M3>(p, rt, sms, st);
-  return c.kind == SAGE_KV_INT8 ? launch_attn_rt<64, SAGE_KV_INT8>(p, rt, sms, st)
-                                : launch_attn_rt<64, SAGE_KV_E4M3>(p, rt, sms, st);
+  ScopedTimer timer("kv_attention", st);
+  const bool many = L.rows == kChunkRows;
+  if (int rc = many ? launch_kv_chunk(p, c.kind, sms, st) : launch_kv_few(p, c.kind, L.rows, sms, st)) return rc;
+  const unsigned units = (unsigned)((long long)B * c.Hkv * L.tiles);
+  auto join = many ? (c.D == 128 ? kv_join_kernel<128, 1> : kv_join_kernel<64, 1>)
+                   : (c.D == 128 ? kv_join_kernel<128, 4> : kv_join_kernel<64, 4>);
+  if (launch_pdl(join, dim3(units, many ? L.rows / 4 : L.rows), dim3(128), 0, st, p, L.rows) != cudaSuccess) return 3;
+  return cudaGetLastError() == cudaSuccess ? 0 : 3;
 }
 
 }  // namespace sage

@@ -1,0 +1,136 @@
+// What the two attention kernels over the paged cache share: parameters, the line of work that
+// is cut over the grid, and the codes' way into fp16.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv.h"
+#include "ptx.cuh"
+
+namespace sage {
+
+struct AttnParams {
+  sage_kv_cache c;
+  const __nv_bfloat16* Q;
+  const int *slots, *q_len;
+  __nv_bfloat16* O;
+  float* LSE;
+  int2* info;      // first and last worker of each unit
+  float* part;     // two partial results of each worker: [R][D] sums, then [R] maxima and [R] row sums
+  int B, H, G, Nq, tiles, causal;
+  float alpha;     // sm_scale log2 e
+};
+
+namespace {  // internal linkage: each translation unit keeps its own copy
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Two codes as fp16.  int8, with the sign bit flipped (byte c + 128): 0x6400 + byte is the fp16
+// 1024 + c + 128.  e4m3: sign, exponent and fraction moved to fp16's places give the value times
+// 2^-8 (subnormal codes too), which kCodeUnit takes back in the scales; every byte is finite.
+template <int KIND>
+constexpr float kCodeUnit = KIND == SAGE_KV_INT8 ? 1.f : 256.f;
+
+// bytes (0, 1) and (2, 3) of a word
+template <int KIND>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (KIND == SAGE_KV_INT8) {
+    w ^= 0x80808080u;
+    lo = hsub2(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u);
+    hi = hsub2(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u);
+  } else {
+    const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
+    lo = (a & 0x80008000u) | ((a >> 1) & 0x3f803f80u);
+    hi = (b & 0x80008000u) | ((b >> 1) & 0x3f803f80u);
+  }
+}
+
+// The power of two that brings a query row's largest element `top` to [2^8, 2^9), where fp16 holds
+// every bf16 down to 2^-25 of it exactly, and its inverse.
+__device__ __forceinline__ void row_power(float top, float& up, float& down) {
+  const int ex = min(max((int)(__float_as_uint(top) >> 23) - 127, -110), 126);
+  up = __uint_as_float((uint32_t)(127 + 8 - ex) << 23);
+  down = __uint_as_float((uint32_t)(127 - 8 + ex) << 23);
+}
+
+// The slot of batch row b and its length; what is out of range is reported and counts as empty.
+__device__ __forceinline__ int row_length(const AttnParams& p, int b, int& slot) {
+  slot = p.slots ? p.slots[b] : b;
+  int len = 0;
+  bool bad = (unsigned)slot >= (unsigned)p.c.n_slots;
+  if (!bad) {
+    len = p.c.lengths[slot];
+    bad = len < 0 || (long long)len > (long long)p.c.max_pages * p.c.page;
+  }
+  if (bad) {
+    atomicMax(p.c.status, kDevIndex);
+    slot = 0, len = 0;
+  }
+  return len;
+}
+__device__ __forceinline__ int row_queries(const AttnParams& p, int b) {
+  return p.q_len ? max(0, min(p.Nq, p.q_len[b])) : p.Nq;
+}
+// keys that query i of q_len sees
+__device__ __forceinline__ int row_end(const AttnParams& p, int len, int q_len, int i) {
+  return p.causal ? max(0, min(len, len - q_len + i + 1)) : len;
+}
+
+// pre[b] = sum of cost(b') over b' < b, pre[B] = the total (all threads of the CTA, which must
+// synchronise before they read it); wsum: one word for each warp
+template <int NT, class Cost>
+__device__ __forceinline__ void prefix_of(int B, long long* pre, long long* wsum, Cost&& cost) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n = (B + NT - 1) / NT, b0 = min(B, tid * n), b1 = min(B, b0 + n);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    pre[b] = sum;
+    sum += cost(b);
+  }
+  long long s = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += x;
+  }
+  if (lane == 31) wsum[warp] = s;
+  __syncthreads();
+  long long base = s - sum;
+  for (int w = 0; w < warp; ++w) base += wsum[w];
+  for (int b = b0; b < b1; ++b) pre[b] += base;
+  if (tid == NT - 1) pre[B] = base + sum;
+}
+// the batch row that holds place `at` of the line
+__device__ __forceinline__ int row_at(const long long* pre, int B, long long at) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= at) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// the most CTAs that share the line
+constexpr int kMaxWorkers = 1024;      // few query rows
+constexpr int kMaxChunkWorkers = 160;  // many (one CTA an SM)
+constexpr int kChunkRows = 256;        // query rows of a unit, many
+
+}  // namespace
+
+// the kernel of a few (up to 16) query rows a unit, and the one of kChunkRows
+int launch_kv_few(const AttnParams& p, int kind, int rows, int sms, cudaStream_t st);
+int launch_kv_chunk(const AttnParams& p, int kind, int sms, cudaStream_t st);
+
+}  // namespace sage

@@ -1,0 +1,532 @@
+// Attention of many query rows over the 8-bit paged cache: a chunk of a prompt behind what the cache
+// holds of it (sage_attn_kv_attention, more than 32 query rows of a shared head).
+//
+// The products are what counts here: 4 D operations for every (query row, key) pair against
+// 2 D bytes for every key that 256 rows share.  One CTA an SM takes units of 256 rows (two tiles of
+// 128: the queries of the G heads of a key/value head, token by token) and walks the unit's
+// 128-key tiles:
+//  - warps 8-11 read the codes with plain 16-byte loads one tile ahead, turn them into fp16 (exact)
+//    and store them where tcgen05.mma reads them (128-byte swizzle), two K and two V tiles deep;
+//  - one thread issues S = Q K^T and O += P V (kind::f16, fp32 accumulators in TMEM) for the two row
+//    tiles in turn, so the tensor core works on one tile while the softmax works on the other;
+//  - warps 0-3 and 4-7 own a row tile each, a thread a row: S from TMEM, P back into TMEM over S's
+//    columns, from where the second product takes it.
+// Units are cut over the grid like those of the few-row kernel (kv_attn.cu), in 128-key tiles.
+//
+// Scales.  S gets the page's s_k before the exponent.  s_v goes into it: with t_j = S_j and
+// u_j = t_j + log2 s_v(j), P_j = 2^(u_j - m), m a running reference of the u that keeps the largest
+// P of a row between 2^7 and 2^15, so fp16 holds P whatever the pages' scales are (11 bits down to
+// 2^-21 of the largest, 2^-32 of it absolute below); the row sum takes P_j / s_v(j).  m moves only when a
+// row's maximum passes 2^15, so the accumulator is seldom rescaled.  A page of zeros (s_v = 0) takes
+// the largest scale met so far instead; scales below kLeast = 2^-80 (values below 2^-71) are read as
+// kLeast, so that the row sums stay in fp32's range.
+#include "kv_attn.cuh"
+#include "launch.h"
+
+namespace sage {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kTile = 128;                   // keys of a tile, rows of a row tile
+constexpr int kRegsSoftmax = 192, kRegsLoad = 88, kRegsIssue = 40;
+static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 4 * 128, "the launch's registers");
+constexpr uint32_t kCols = 512, kColO = 256; // TMEM: S of row tile t at 128 t, O at 256 + 128 t
+
+template <int D>
+struct ChunkSmem {
+  uint8_t q[2][kTile * D * 2];
+  uint8_t k[2][kTile * D * 2];
+  uint8_t v[2][kTile * D * 2];
+  uint64_t bar_q[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_s[2], bar_p[2], bar_o[2];
+  long long wsum[kThreads / 32];
+  uint32_t tmem_base;
+  int abort;
+};
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// D[tmem] (+)= A[tmem] * B[smem]: A's rows are the lanes, two fp16 along K in a column
+__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// A part of a unit: key tiles [c0, c1) of row tile pair rt of (batch row b, key/value head hk).
+struct Seg {
+  int b, slot, hk, rt, len, q_len, c0, c1, chunks;
+  bool two;  // the second row tile has rows
+  long long unit_at;
+};
+
+__device__ __forceinline__ int pair_chunks(const AttnParams& p, int len, int q_len, int rt) {
+  const int i0 = rt * kChunkRows / p.G;
+  if (i0 >= q_len) return 0;
+  const int last = min(q_len - 1, (int)(((long long)rt * kChunkRows + kChunkRows - 1) / p.G));
+  return max(1, (row_end(p, len, q_len, last) + kTile - 1) / kTile);
+}
+
+// The part that begins at `at`; b is the batch row of the part before.
+__device__ __forceinline__ Seg seg_at(const AttnParams& p, const long long* pre, long long at, long long stop, int b) {
+  Seg s;
+  while (pre[b + 1] <= at) ++b;
+  s.b = b;
+  s.len = row_length(p, b, s.slot);
+  s.q_len = row_queries(p, b);
+  long long base = pre[b];
+  int n = 0, rt = 0;
+  for (;; ++rt) {
+    n = pair_chunks(p, s.len, s.q_len, rt);
+    if (at < base + (long long)n * p.c.Hkv) break;
+    base += (long long)n * p.c.Hkv;
+  }
+  s.rt = rt;
+  s.hk = (int)((at - base) / n);
+  s.chunks = n;
+  s.unit_at = base + (long long)s.hk * n;
+  s.c0 = (int)(at - s.unit_at);
+  s.c1 = (int)min((long long)n, stop - s.unit_at);
+  s.two = (long long)rt * kChunkRows + kTile < (long long)s.q_len * p.G;
+  return s;
+}
+
+template <int D, int KIND>
+__global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams p) {
+  constexpr int kAtoms = D / 64;       // 128-byte columns of a tile row
+  constexpr int kAtom = kTile * 128;   // bytes of one
+  extern __shared__ uint8_t smem_raw[];
+  ChunkSmem<D>& sm = *reinterpret_cast<ChunkSmem<D>*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  long long* pre = reinterpret_cast<long long*>(&sm + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.bar_q[s], 128);
+      mbar_init(&sm.bar_k_full[s], 128);
+      mbar_init(&sm.bar_k_empty[s], 1);
+      mbar_init(&sm.bar_v_full[s], 128);
+      mbar_init(&sm.bar_v_empty[s], 1);
+      mbar_init(&sm.bar_s[s], 1);
+      mbar_init(&sm.bar_p[s], 128);
+      mbar_init(&sm.bar_o[s], 1);
+    }
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  if (warp == 12) {
+    tmem_alloc(&sm.tmem_base, kCols);
+    tmem_relinquish();
+  }
+  prefix_of<kThreads>(p.B, pre, sm.wsum, [&](int b) {
+    int slot;
+    const int len = row_length(p, b, slot), q_len = row_queries(p, b);
+    long long n = 0;
+    for (int rt = 0; rt < p.tiles; ++rt) n += pair_chunks(p, len, q_len, rt);
+    return n * p.c.Hkv;
+  });
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // dependents may come once this CTA holds its TMEM: a later kernel that allocates all columns
+  // must not reach this SM before
+  pdl_trigger();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+  const long long total = pre[p.B];
+  const int workers = (int)min((long long)gridDim.x, total), w0 = blockIdx.x;
+  auto start_of = [&](int w) { return total * w / workers; };
+  const long long begin = w0 < workers ? start_of(w0) : 0, stop = w0 < workers ? start_of(w0 + 1) : 0;
+  const int per_page = p.c.page >> 4;  // 16-key groups of a page
+  const int page_shift = 31 - __clz(per_page);
+  // the page of the 16-key group `grp` of a slot; -1: no key there
+  auto page_of = [&](int slot, int len, int grp) {
+    if (grp * 16 >= len) return -1;
+    const int page = p.c.table[(size_t)slot * p.c.max_pages + (grp >> page_shift)];
+    if ((unsigned)page < (unsigned)p.c.n_pages) return page;
+    atomicMax(p.c.status, kDevIndex);
+    return -1;
+  };
+
+  if (warp >= 12) {
+    regs_decrease<kRegsIssue>();
+    if (warp == 12 && lane == 0 && begin < stop) {
+      // ---------------- MMA issuer
+      constexpr uint32_t id_s = idesc_f16(kTile, kTile, false), id_o = idesc_f16(kTile, D, true);
+      uint32_t kc = 0, ns[2] = {0, 0}, np[2] = {0, 0};  // key tiles, segments and P tiles so far
+      auto issue_s = [&](int t, uint32_t kv) {
+        const uint32_t a = smem_u32(sm.q[t]), b = smem_u32(sm.k[kv & 1]);
+#pragma unroll
+        for (int h = 0; h < kAtoms; ++h)
+          umma_bf16_x4<2, 2>(tmem + t * 128, sdesc_sw128(a + h * kAtom, 16, 1024), sdesc_sw128(b + h * kAtom, 16, 1024),
+                             id_s, h > 0);
+        umma_commit(&sm.bar_s[t]);
+      };
+      auto issue_pv = [&](int t, uint32_t kv, uint32_t acc) {
+        const uint32_t b = smem_u32(sm.v[kv & 1]);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_f16_ts(tmem + kColO + t * 128, tmem + t * 128 + kk * 8, sdesc_sw128(b + kk * 2048, kAtom, 1024), id_o,
+                      acc | (kk > 0));
+      };
+      bool ok = true;
+      int b = row_at(pre, p.B, begin);
+      for (long long at = begin; ok && at < stop;) {
+        const Seg s = seg_at(p, pre, at, stop, b);
+        b = s.b;
+        at = s.unit_at + s.c1;
+        const int n = s.c1 - s.c0;
+        ok = mbar_wait(&sm.bar_q[0], ns[0] & 1, abort) && (!s.two || mbar_wait(&sm.bar_q[1], ns[1] & 1, abort)) &&
+             mbar_wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1, abort);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(0, kc);
+        if (s.two) issue_s(1, kc);
+        umma_commit(&sm.bar_k_empty[kc & 1]);
+        for (int j = 0; j < n; ++j, ++kc) {
+          const bool more = j + 1 < n;
+          ok = mbar_wait(&sm.bar_v_full[kc & 1], (kc >> 1) & 1, abort) && mbar_wait(&sm.bar_p[0], np[0] & 1, abort);
+          if (!ok) break;
+          ++np[0];
+          tc_fence_after();
+          issue_pv(0, kc, j > 0);
+          if (!more) umma_commit(&sm.bar_o[0]);
+          if (more) {
+            ok = mbar_wait(&sm.bar_k_full[(kc + 1) & 1], ((kc + 1) >> 1) & 1, abort);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(0, kc + 1);
+          }
+          if (s.two) {
+            ok = mbar_wait(&sm.bar_p[1], np[1] & 1, abort);
+            if (!ok) break;
+            ++np[1];
+            tc_fence_after();
+            issue_pv(1, kc, j > 0);
+            if (!more) umma_commit(&sm.bar_o[1]);
+          }
+          umma_commit(&sm.bar_v_empty[kc & 1]);
+          if (more) {
+            if (s.two) issue_s(1, kc + 1);
+            umma_commit(&sm.bar_k_empty[(kc + 1) & 1]);
+          }
+        }
+        ++ns[0];
+        if (s.two) ++ns[1];
+      }
+    }
+  } else if (warp >= 8) {
+    regs_decrease<kRegsLoad>();
+    // ---------------- loaders: thread `lt` takes 16 bytes of kRows rows of a tile
+    constexpr int kPerRow = D / 16, kRowStep = 128 / kPerRow, kRows = kTile / kRowStep;
+    const int lt = tid - 256, r0 = lt / kPerRow, piece = lt % kPerRow;
+    const size_t page_bytes = (size_t)p.c.page * D;
+    int b = begin < stop ? row_at(pre, p.B, begin) : 0;
+    long long at = begin;
+    Seg s{};
+    int c = 0;  // the tile whose codes are in flight
+    // the lane's 16-key group of a tile: its page (lanes 0-7)
+    auto ids_of = [&](int tile) { return lane < 8 ? page_of(s.slot, s.len, tile * 8 + lane) : -1; };
+    auto fetch = [&](const void* pool, int ids, int tile, uint4 (&raw)[kRows]) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = r0 + i * kRowStep, grp = r >> 4;
+        const int id = __shfl_sync(0xffffffffu, ids, grp);
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (id >= 0) {
+          const int in_page = ((tile * 8 + grp) & (per_page - 1)) * 16 + (r & 15);
+          raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) +
+                                                        ((size_t)id * p.c.Hkv + s.hk) * page_bytes + (size_t)in_page * D) +
+                         piece);
+        }
+      }
+    };
+    // 16 codes of a row -> two 16-byte chunks of the swizzled tile; lanes whose chunks would meet
+    // in the same banks store them in the other order
+    auto store = [&](uint8_t* tile, const uint4 (&raw)[kRows]) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = r0 + i * kRowStep, u = (piece * 2) & 7;
+        uint4 lo, hi;
+        codes_to_half<KIND>(raw[i].x, lo.x, lo.y);
+        codes_to_half<KIND>(raw[i].y, lo.z, lo.w);
+        codes_to_half<KIND>(raw[i].z, hi.x, hi.y);
+        codes_to_half<KIND>(raw[i].w, hi.z, hi.w);
+        uint8_t* row = tile + (piece >> 2) * kAtom + (r >> 3) * 1024 + (r & 7) * 128;
+        const bool swap = D == 128 && ((piece >> 2) & 1);
+        *reinterpret_cast<uint4*>(row + (((u + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
+        *reinterpret_cast<uint4*>(row + (((u + !swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+      }
+    };
+    uint4 raw_k[kRows], raw_v[kRows];
+    bool have = begin < stop;
+    int ids = -1;
+    if (have) {
+      s = seg_at(p, pre, at, stop, b);
+      b = s.b, at = s.unit_at + s.c1, c = s.c0;
+      ids = ids_of(c);
+      fetch(p.c.k, ids, c, raw_k);
+      fetch(p.c.v, ids, c, raw_v);
+    }
+    uint32_t kc = 0;
+    while (have) {
+      // where the tile after this one is
+      bool next = true;
+      if (++c == s.c1) {
+        next = at < stop;
+        if (next) {
+          s = seg_at(p, pre, at, stop, b);
+          b = s.b, at = s.unit_at + s.c1, c = s.c0;
+        }
+      }
+      if (next) ids = ids_of(c);
+      const uint32_t st = kc & 1, ph = ((kc >> 1) - 1) & 1;
+      if (kc >= 2 && !mbar_wait(&sm.bar_k_empty[st], ph, abort)) break;
+      store(sm.k[st], raw_k);
+      fence_proxy_async_smem();
+      mbar_arrive(&sm.bar_k_full[st]);
+      if (next) fetch(p.c.k, ids, c, raw_k);
+      if (kc >= 2 && !mbar_wait(&sm.bar_v_empty[st], ph, abort)) break;
+      store(sm.v[st], raw_v);
+      fence_proxy_async_smem();
+      mbar_arrive(&sm.bar_v_full[st]);
+      if (next) fetch(p.c.v, ids, c, raw_v);
+      ++kc;
+      have = next;
+    }
+  } else {
+    regs_increase<kRegsSoftmax>();
+    // ---------------- softmax: thread r of the group owns row r of row tile t
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + kColO + t * 128;
+    uint32_t n_s = 0, n_o = 0;
+    bool ok = true;
+    int b = begin < stop ? row_at(pre, p.B, begin) : 0;
+    for (long long at = begin; ok && at < stop;) {
+      const Seg s = seg_at(p, pre, at, stop, b);
+      b = s.b;
+      at = s.unit_at + s.c1;
+      const long long unit_id = ((long long)s.b * p.tiles + s.rt) * p.c.Hkv + s.hk;
+      if (s.c0 == 0 && tid == 0) {
+        int last = w0;
+        while (start_of(last + 1) < s.unit_at + s.chunks) ++last;
+        p.info[unit_id] = make_int2(w0, last);
+      }
+      if (t == 1 && !s.two) continue;
+      const long long row = (long long)s.rt * kChunkRows + t * kTile + r;
+      const int i = (int)(row / p.G);
+      const bool live = i < s.q_len;
+      const size_t orow =
+          ((size_t)s.b * p.H + (size_t)s.hk * p.G + (size_t)(row % p.G)) * p.Nq + (live ? i : 0);
+      // Q: the row times its power of two, as fp16 (the last part's S have been read: free)
+      float a_row;
+      {
+        const uint4* q = reinterpret_cast<const uint4*>(p.Q + orow * D);
+        uint4 w[D / 8];
+        float top = 0.f;
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) {
+          w[u] = live ? q[u] : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top = max3(top, fabsf(__uint_as_float(x[e] << 16)), fabsf(__uint_as_float(x[e] & 0xffff0000u)));
+        }
+        float up, down;
+        row_power(top, up, down);
+        a_row = p.alpha * down * kCodeUnit<KIND>;
+#pragma unroll
+        for (int u = 0; u < D / 8; ++u) {
+          const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            h[e] = h2bits(__floats2half2_rn(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xffff0000u) * up));
+          *reinterpret_cast<uint4*>(sm.q[t] + (u >> 3) * kAtom + (r >> 3) * 1024 + (r & 7) * 128 +
+                                    (((u & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sm.bar_q[t]);
+      const int lim = live ? row_end(p, s.len, s.q_len, i) : s.len;
+      float m = -INFINITY, l = 0.f, ref = 0.f;
+      // lanes 0-7: the tile's eight 16-key groups; scales one tile ahead, pages two
+      auto scales = [&](int id, float& ks, float& vs) {
+        ks = 0.f, vs = 0.f;
+        if (id >= 0) {
+          ks = p.c.k_scale[(size_t)id * p.c.Hkv + s.hk];
+          vs = p.c.v_scale[(size_t)id * p.c.Hkv + s.hk];
+        }
+      };
+      auto id_at = [&](int c) { return lane < 8 && c < s.c1 ? page_of(s.slot, s.len, c * 8 + lane) : -1; };
+      float ks, vs, ks_n, vs_n;
+      int id = id_at(s.c0);
+      scales(id, ks, vs);
+      id = id_at(s.c0 + 1);
+#pragma unroll 1
+      for (int c = s.c0; c < s.c1; ++c) {
+        scales(id, ks_n, vs_n);
+        id = id_at(c + 2);
+        // the groups' factors of S, log2 of V's scale and its inverse
+        float big = vs;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+        ref = fmaxf(ref, __shfl_sync(0xffffffffu, big, 0));
+        constexpr float kLeast = 0x1p-80f;
+        const float ve = vs > 0.f ? fmaxf(vs, kLeast) : ref > 0.f ? fmaxf(ref, kLeast) : 1.f;
+        const float lg = log2f(ve), iv = 1.f / ve;
+        ok = ok && mbar_wait(&sm.bar_s[t], n_s & 1, abort);
+        ++n_s;
+        tc_fence_after();
+        uint32_t sv[4][32];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_ld32(s_col + 32 * x, sv[x]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) reg_fence32(sv[x]);
+        const bool edge = __any_sync(0xffffffffu, lim < (c + 1) * kTile);
+        const int left = lim - c * kTile;
+        float mx = -INFINITY;
+        if (edge) {
+          // u of every key, -inf behind the row's last one; the factors below are then 1 and 0
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float f = __shfl_sync(0xffffffffu, ks, x) * a_row, g = __shfl_sync(0xffffffffu, lg, x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float u = fmaf(__uint_as_float(sv[x >> 1][(x & 1) * 16 + e]), f, g);
+              const float y = x * 16 + e < left ? u : -INFINITY;
+              sv[x >> 1][(x & 1) * 16 + e] = __float_as_uint(y);
+              mx = fmaxf(mx, y);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            float y = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2)
+              y = max3(y, __uint_as_float(sv[x >> 1][(x & 1) * 16 + e]), __uint_as_float(sv[x >> 1][(x & 1) * 16 + e + 1]));
+            const float f = __shfl_sync(0xffffffffu, ks, x) * a_row;
+            mx = fmaxf(mx, fmaf(y, f, __shfl_sync(0xffffffffu, lg, x)));
+          }
+        }
+        const bool raise = mx > m + 15.f;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float to = raise ? mx - 7.f : m, corr = raise ? ex2(m - to) : 1.f;
+          m = to;
+          l *= corr;
+          if (c > s.c0) {  // (the part's first product overwrites O; PV of the tile before is done: S came after it)
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_col + d, o);
+              tmem_wait32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              tmem_st32(o_col + d, o);
+            }
+          }
+        }
+        const float sub = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int grp = h * 4 + x;
+            const float f = edge ? 1.f : __shfl_sync(0xffffffffu, ks, grp) * a_row;
+            const float g = (edge ? 0.f : __shfl_sync(0xffffffffu, lg, grp)) - sub;
+            const uint64_t f2v = f2(f, f), g2v = f2(g, g);
+            uint64_t sum = f2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              float u0, u1;
+              f2split(ffma2(f2(__uint_as_float(sv[grp >> 1][(grp & 1) * 16 + e]),
+                               __uint_as_float(sv[grp >> 1][(grp & 1) * 16 + e + 1])),
+                            f2v, g2v),
+                      u0, u1);
+              u0 = ex2(u0), u1 = ex2(u1);
+              sum = fadd2(sum, f2(u0, u1));
+              w[x * 8 + (e >> 1)] = h2bits(__floats2half2_rn(u0, u1));
+            }
+            float y0, y1;
+            f2split(sum, y0, y1);
+            l = fmaf(y0 + y1, __shfl_sync(0xffffffffu, iv, grp), l);
+          }
+          tmem_st32(s_col + h * 32, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&sm.bar_p[t]);
+        ks = ks_n, vs = vs_n;
+      }
+      // ---- the part's result
+      ok = ok && mbar_wait(&sm.bar_o[t], n_o & 1, abort);
+      ++n_o;
+      tc_fence_after();
+      const bool whole = s.c0 == 0 && s.c1 == s.chunks;
+      float* part = p.part + (size_t)(2 * w0 + (s.c0 == 0 ? 1 : 0)) * kChunkRows * (D + 2);
+      const float f = whole ? (l > 0.f ? kCodeUnit<KIND> / l : 0.f) : kCodeUnit<KIND>;
+      const int pr = t * kTile + r;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_col + d, o);
+        tmem_wait32(o);
+        if (!(ok && live)) continue;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4 y;
+            __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&y);
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              h[z] = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * z]), __uint_as_float(o[8 * e + 2 * z + 1]));
+            *reinterpret_cast<uint4*>(p.O + orow * D + d + 8 * e) = y;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<uint4*>(part + (size_t)pr * D + d + 4 * e) =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        }
+      }
+      if (ok && live) {
+        if (whole)
+          p.LSE[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        else
+          part[(size_t)kChunkRows * D + pr] = m, part[(size_t)kChunkRows * D + kChunkRows + pr] = l;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) tmem_dealloc(tmem, kCols);
+  if (tid == 0 && sm.abort) atomicMax(p.c.status, (int)kDevTimeout);
+}
+
+template <int D, int KIND>
+int launch(const AttnParams& p, int sms, cudaStream_t st) {
+  auto kern = kv_chunk_kernel<D, KIND>;
+  const size_t smem = sizeof(ChunkSmem<D>) + 1024 + ((size_t)p.B + 1) * 8;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 3;
+  const int grid = sms < kMaxChunkWorkers ? sms : kMaxChunkWorkers;
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p) == cudaSuccess ? 0 : 3;
+}
+
+}  // namespace
+
+int launch_kv_chunk(const AttnParams& p, int kind, int sms, cudaStream_t st) {
+  if (p.c.D == 128)
+    return kind == SAGE_KV_INT8 ? launch<128, SAGE_KV_INT8>(p, sms, st) : launch<128, SAGE_KV_E4M3>(p, sms, st);
+  return kind == SAGE_KV_INT8 ? launch<64, SAGE_KV_INT8>(p, sms, st) : launch<64, SAGE_KV_E4M3>(p, sms, st);
+}
+
+}  // namespace sage
