@@ -34,17 +34,6 @@ constexpr int kChunk = 16;        // tokens of one step of a warp; a page is a w
 constexpr int kStages = 4;        // chunks of a warp in flight
 constexpr int kCtasPerSm = 3;     // the ring (4 warps x 4 chunks x 2 x 16 D bytes) of D = 128 is 64 KB
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {

@@ -5,8 +5,9 @@
 // 2 D bytes for every key that 256 rows share.  One CTA an SM takes units of 256 rows (two tiles of
 // 128: the queries of the G heads of a key/value head, token by token) and walks the unit's
 // 128-key tiles:
-//  - warps 8-11 read the codes with plain 16-byte loads one tile ahead, turn them into fp16 (exact)
-//    and store them where tcgen05.mma reads them (128-byte swizzle), two K and two V tiles deep;
+//  - warps 8-11 fetch the codes one tile ahead (cp.async, 16 bytes a thread into a place that only
+//    that thread reads), turn them into fp16 (exact) and store them where tcgen05.mma reads them
+//    (128-byte swizzle), two K and two V tiles deep;
 //  - one thread issues S = Q K^T and O += P V (kind::f16, fp32 accumulators in TMEM) for the two row
 //    tiles in turn, so the tensor core works on one tile while the softmax works on the other;
 //  - warps 0-3 and 4-7 own a row tile each, a thread a row: S from TMEM, P back into TMEM over S's
@@ -29,7 +30,8 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kTile = 128;                   // keys of a tile, rows of a row tile
-constexpr int kRegsSoftmax = 192, kRegsLoad = 88, kRegsIssue = 40;
+constexpr int kGroups = 128;                 // the batch rows in at most so many groups
+constexpr int kRegsSoftmax = 192, kRegsLoad = 72, kRegsIssue = 56;
 static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 4 * 128, "the launch's registers");
 constexpr uint32_t kCols = 512, kColO = 256; // TMEM: S of row tile t at 128 t, O at 256 + 128 t
 
@@ -38,8 +40,10 @@ struct ChunkSmem {
   uint8_t q[2][kTile * D * 2];
   uint8_t k[2][kTile * D * 2];
   uint8_t v[2][kTile * D * 2];
+  uint8_t raw[2][kTile * D];  // codes of a K and a V tile on their way; a loader reads what it copied
   uint64_t bar_q[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_s[2], bar_p[2], bar_o[2];
   long long wsum[kThreads / 32];
+  long long pre[kGroups + 1];  // tiles before each group of batch rows
   uint32_t tmem_base;
   int abort;
 };
@@ -70,29 +74,50 @@ __device__ __forceinline__ int pair_chunks(const AttnParams& p, int len, int q_l
   return max(1, (row_end(p, len, q_len, last) + kTile - 1) / kTile);
 }
 
-// The part that begins at `at`; b is the batch row of the part before.
-__device__ __forceinline__ Seg seg_at(const AttnParams& p, const long long* pre, long long at, long long stop, int b) {
-  Seg s;
-  while (pre[b + 1] <= at) ++b;
-  s.b = b;
-  s.len = row_length(p, b, s.slot);
-  s.q_len = row_queries(p, b);
-  long long base = pre[b];
-  int n = 0, rt = 0;
-  for (;; ++rt) {
-    n = pair_chunks(p, s.len, s.q_len, rt);
-    if (at < base + (long long)n * p.c.Hkv) break;
-    base += (long long)n * p.c.Hkv;
-  }
-  s.rt = rt;
-  s.hk = (int)((at - base) / n);
-  s.chunks = n;
-  s.unit_at = base + (long long)s.hk * n;
-  s.c0 = (int)(at - s.unit_at);
-  s.c1 = (int)min((long long)n, stop - s.unit_at);
-  s.two = (long long)rt * kChunkRows + kTile < (long long)s.q_len * p.G;
-  return s;
+// tiles of all units of batch row b
+__device__ __forceinline__ long long row_chunks(const AttnParams& p, int b) {
+  int slot;
+  const int len = row_length(p, b, slot), q_len = row_queries(p, b);
+  long long n = 0;
+  for (int rt = 0; rt < p.tiles; ++rt) n += pair_chunks(p, len, q_len, rt);
+  return n * p.c.Hkv;
 }
+
+// A worker's way along the line: the parts from `at` to `stop`, in order.
+struct Walk {
+  long long at, stop, base;  // base: tiles before batch row b
+  int b;
+  __device__ Walk(const long long* pre, int group, long long begin, long long end) : at(begin), stop(end), base(0), b(0) {
+    if (begin >= end) return;
+    const int g = row_at(pre, kGroups, begin);
+    b = g * group;
+    base = pre[g];
+  }
+  __device__ bool more() const { return at < stop; }
+  __device__ Seg next(const AttnParams& p) {
+    for (long long n; at >= base + (n = row_chunks(p, b)); ++b) base += n;
+    Seg s;
+    s.b = b;
+    s.len = row_length(p, b, s.slot);
+    s.q_len = row_queries(p, b);
+    long long unit = base;
+    int n = 0, rt = 0;
+    for (;; ++rt) {
+      n = pair_chunks(p, s.len, s.q_len, rt);
+      if (at < unit + (long long)n * p.c.Hkv) break;
+      unit += (long long)n * p.c.Hkv;
+    }
+    s.rt = rt;
+    s.hk = (int)((at - unit) / n);
+    s.chunks = n;
+    s.unit_at = unit + (long long)s.hk * n;
+    s.c0 = (int)(at - s.unit_at);
+    s.c1 = (int)min((long long)n, stop - s.unit_at);
+    s.two = (long long)rt * kChunkRows + kTile < (long long)s.q_len * p.G;
+    at = s.unit_at + s.c1;
+    return s;
+  }
+};
 
 template <int D, int KIND>
 __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams p) {
@@ -100,7 +125,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
   constexpr int kAtom = kTile * 128;   // bytes of one
   extern __shared__ uint8_t smem_raw[];
   ChunkSmem<D>& sm = *reinterpret_cast<ChunkSmem<D>*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  long long* pre = reinterpret_cast<long long*>(&sm + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -121,12 +145,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
     tmem_alloc(&sm.tmem_base, kCols);
     tmem_relinquish();
   }
-  prefix_of<kThreads>(p.B, pre, sm.wsum, [&](int b) {
-    int slot;
-    const int len = row_length(p, b, slot), q_len = row_queries(p, b);
+  const int group = (p.B + kGroups - 1) / kGroups;
+  prefix_of<kThreads>(kGroups, sm.pre, sm.wsum, [&](int g) {
     long long n = 0;
-    for (int rt = 0; rt < p.tiles; ++rt) n += pair_chunks(p, len, q_len, rt);
-    return n * p.c.Hkv;
+    for (int b = g * group; b < min(p.B, (g + 1) * group); ++b) n += row_chunks(p, b);
+    return n;
   });
   tc_fence_before();
   __syncthreads();
@@ -136,7 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
   pdl_trigger();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
-  const long long total = pre[p.B];
+  const long long total = sm.pre[kGroups];
   const int workers = (int)min((long long)gridDim.x, total), w0 = blockIdx.x;
   auto start_of = [&](int w) { return total * w / workers; };
   const long long begin = w0 < workers ? start_of(w0) : 0, stop = w0 < workers ? start_of(w0 + 1) : 0;
@@ -173,11 +196,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
                       acc | (kk > 0));
       };
       bool ok = true;
-      int b = row_at(pre, p.B, begin);
-      for (long long at = begin; ok && at < stop;) {
-        const Seg s = seg_at(p, pre, at, stop, b);
-        b = s.b;
-        at = s.unit_at + s.c1;
+      Walk walk(sm.pre, group, begin, stop);
+      while (ok && walk.more()) {
+        const Seg s = walk.next(p);
         const int n = s.c1 - s.c0;
         ok = mbar_wait(&sm.bar_q[0], ns[0] & 1, abort) && (!s.two || mbar_wait(&sm.bar_q[1], ns[1] & 1, abort)) &&
              mbar_wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1, abort);
@@ -224,79 +245,86 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
     constexpr int kPerRow = D / 16, kRowStep = 128 / kPerRow, kRows = kTile / kRowStep;
     const int lt = tid - 256, r0 = lt / kPerRow, piece = lt % kPerRow;
     const size_t page_bytes = (size_t)p.c.page * D;
-    int b = begin < stop ? row_at(pre, p.B, begin) : 0;
-    long long at = begin;
+    Walk walk(sm.pre, group, begin, stop);
     Seg s{};
-    int c = 0;  // the tile whose codes are in flight
-    // the lane's 16-key group of a tile: its page (lanes 0-7)
+    int c = 0;  // the tile that is fetched next; its eight 16-key groups' pages are in lanes 0-7
+    int ids = -1, ids_n = -1;
+    bool more = walk.more();
     auto ids_of = [&](int tile) { return lane < 8 ? page_of(s.slot, s.len, tile * 8 + lane) : -1; };
-    auto fetch = [&](const void* pool, int ids, int tile, uint4 (&raw)[kRows]) {
+    // the codes of tile c (zeros where there is no key), 16 bytes at a time
+    auto fetch = [&](int v) {
+      if (more) {
+        const uint8_t* pool = static_cast<const uint8_t*>(v ? p.c.v : p.c.k);
+        const uint32_t dst = smem_u32(sm.raw[v]) + lt * 16;
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const int r = r0 + i * kRowStep, grp = r >> 4;
-        const int id = __shfl_sync(0xffffffffu, ids, grp);
-        raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (id >= 0) {
-          const int in_page = ((tile * 8 + grp) & (per_page - 1)) * 16 + (r & 15);
-          raw[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) +
-                                                        ((size_t)id * p.c.Hkv + s.hk) * page_bytes + (size_t)in_page * D) +
-                         piece);
+        for (int i = 0; i < kRows; ++i) {
+          const int r = r0 + i * kRowStep, grp = r >> 4;
+          const int id = __shfl_sync(0xffffffffu, ids, grp);
+          const int in_page = ((c * 8 + grp) & (per_page - 1)) * 16 + (r & 15);
+          const uint8_t* src = pool + ((size_t)max(id, 0) * p.c.Hkv + s.hk) * page_bytes + (size_t)in_page * D + piece * 16;
+          cp_async16_or_zero(dst + i * 128 * 16, src, id >= 0);
         }
       }
+      cp_commit();
+    };
+    // the tile after tile c
+    auto advance = [&]() {
+      if (++c < s.c1) {
+        ids = ids_n;
+      } else {
+        more = walk.more();
+        if (!more) return;
+        s = walk.next(p);
+        c = s.c0;
+        ids = ids_of(c);
+      }
+      ids_n = c + 1 < s.c1 ? ids_of(c + 1) : -1;
     };
     // 16 codes of a row -> two 16-byte chunks of the swizzled tile; lanes whose chunks would meet
     // in the same banks store them in the other order
-    auto store = [&](uint8_t* tile, const uint4 (&raw)[kRows]) {
+    auto store = [&](uint8_t* tile, const uint8_t* raw) {
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(raw + (i * 128 + lt) * 16);
         const int r = r0 + i * kRowStep, u = (piece * 2) & 7;
         uint4 lo, hi;
-        codes_to_half<KIND>(raw[i].x, lo.x, lo.y);
-        codes_to_half<KIND>(raw[i].y, lo.z, lo.w);
-        codes_to_half<KIND>(raw[i].z, hi.x, hi.y);
-        codes_to_half<KIND>(raw[i].w, hi.z, hi.w);
+        codes_to_half<KIND>(x.x, lo.x, lo.y);
+        codes_to_half<KIND>(x.y, lo.z, lo.w);
+        codes_to_half<KIND>(x.z, hi.x, hi.y);
+        codes_to_half<KIND>(x.w, hi.z, hi.w);
         uint8_t* row = tile + (piece >> 2) * kAtom + (r >> 3) * 1024 + (r & 7) * 128;
         const bool swap = D == 128 && ((piece >> 2) & 1);
         *reinterpret_cast<uint4*>(row + (((u + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
         *reinterpret_cast<uint4*>(row + (((u + !swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
       }
     };
-    uint4 raw_k[kRows], raw_v[kRows];
-    bool have = begin < stop;
-    int ids = -1;
-    if (have) {
-      s = seg_at(p, pre, at, stop, b);
-      b = s.b, at = s.unit_at + s.c1, c = s.c0;
+    long long n = stop - begin;
+    if (more) {
+      s = walk.next(p);
+      c = s.c0;
       ids = ids_of(c);
-      fetch(p.c.k, ids, c, raw_k);
-      fetch(p.c.v, ids, c, raw_v);
+      ids_n = c + 1 < s.c1 ? ids_of(c + 1) : -1;
+      fetch(0);
+      fetch(1);
+      advance();
     }
-    uint32_t kc = 0;
-    while (have) {
-      // where the tile after this one is
-      bool next = true;
-      if (++c == s.c1) {
-        next = at < stop;
-        if (next) {
-          s = seg_at(p, pre, at, stop, b);
-          b = s.b, at = s.unit_at + s.c1, c = s.c0;
-        }
-      }
-      if (next) ids = ids_of(c);
+    for (uint32_t kc = 0; kc < n; ++kc) {
       const uint32_t st = kc & 1, ph = ((kc >> 1) - 1) & 1;
-      if (kc >= 2 && !mbar_wait(&sm.bar_k_empty[st], ph, abort)) break;
-      store(sm.k[st], raw_k);
-      fence_proxy_async_smem();
-      mbar_arrive(&sm.bar_k_full[st]);
-      if (next) fetch(p.c.k, ids, c, raw_k);
-      if (kc >= 2 && !mbar_wait(&sm.bar_v_empty[st], ph, abort)) break;
-      store(sm.v[st], raw_v);
-      fence_proxy_async_smem();
-      mbar_arrive(&sm.bar_v_full[st]);
-      if (next) fetch(p.c.v, ids, c, raw_v);
-      ++kc;
-      have = next;
+      bool ok = true;
+#pragma unroll 1
+      for (int v = 0; ok && v < 2; ++v) {  // K, then V
+        cp_wait<1>();
+        ok = kc < 2 || mbar_wait(v ? &sm.bar_v_empty[st] : &sm.bar_k_empty[st], ph, abort);
+        if (!ok) break;
+        store(v ? sm.v[st] : sm.k[st], sm.raw[v]);
+        fence_proxy_async_smem();
+        mbar_arrive(v ? &sm.bar_v_full[st] : &sm.bar_k_full[st]);
+        fetch(v);
+      }
+      if (!ok) break;
+      advance();
     }
+    cp_wait<0>();
   } else {
     regs_increase<kRegsSoftmax>();
     // ---------------- softmax: thread r of the group owns row r of row tile t
@@ -305,11 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
     const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + kColO + t * 128;
     uint32_t n_s = 0, n_o = 0;
     bool ok = true;
-    int b = begin < stop ? row_at(pre, p.B, begin) : 0;
-    for (long long at = begin; ok && at < stop;) {
-      const Seg s = seg_at(p, pre, at, stop, b);
-      b = s.b;
-      at = s.unit_at + s.c1;
+    Walk walk(sm.pre, group, begin, stop);
+    while (ok && walk.more()) {
+      const Seg s = walk.next(p);
       const long long unit_id = ((long long)s.b * p.tiles + s.rt) * p.c.Hkv + s.hk;
       if (s.c0 == 0 && tid == 0) {
         int last = w0;
@@ -515,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
 template <int D, int KIND>
 int launch(const AttnParams& p, int sms, cudaStream_t st) {
   auto kern = kv_chunk_kernel<D, KIND>;
-  const size_t smem = sizeof(ChunkSmem<D>) + 1024 + ((size_t)p.B + 1) * 8;
+  const size_t smem = sizeof(ChunkSmem<D>) + 1024;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 3;
   const int grid = sms < kMaxChunkWorkers ? sms : kMaxChunkWorkers;
   return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p) == cudaSuccess ? 0 : 3;
