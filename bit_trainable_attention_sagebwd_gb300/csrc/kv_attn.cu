@@ -6,33 +6,37 @@
 // A token is answered at the rate at which the codes come from HBM: 2 Hkv D bytes per cached token
 // against 4 H D operations, far below what the tensor cores could do.  So the kernel is built
 // around the loads:
-//  - The keys of all (batch row, key/value head) units form one line of 16-token chunks, cut into
+//  - The keys of all (batch row, key/value head) units form one line of 32-token chunks, cut into
 //    equal parts for a grid that fills the GPU once; a unit that is cut leaves partial results,
 //    joined by kv_join_kernel in the order of the parts.  Ragged batches and single long
 //    sequences load every SM alike.
-//  - A warp walks its own chunks and keeps kStages of them in flight with cp.async into a ring
-//    that only the same lane reads: no barrier and no bank conflict, registers left for the
-//    arithmetic.
+//  - A warp walks its own chunks and keeps kStages - 1 of them in flight with TMA, across the ends of
+//    units, in a ring of its own: a chunk of K or V is one box of a page's [head, token] rows (two with
+//    pages of 16 tokens).  (Copies of 16 bytes a thread, cp.async, read the same bytes at 5.6 TB/s against 6.7.)
 //  - S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16, fp16): the codes are the 16-row operand, the
 //    (at most 8 RT) query rows of the shared head the 8-column one, so a group of 8 query heads
 //    wastes nothing.  A lane's registers are read from whole 16-byte pieces of a token's row; the
 //    order of the contracted channels (K) and of the output channels (V) is permuted to fit.
 //  - int8 and e4m3 codes are exact in fp16.  q is bf16: scaled by a power of two per row it is
 //    exact in fp16 for every element within 2^-25 of the row's largest.  P is rounded to fp16
-//    (2^-12 relative, p <= 1): bf16, the output's type, would lose more than the output's own
+//    (2^-11 relative at most): bf16, the output's type, would lose as much as the output's own
 //    rounding.  Statistics, scales and sums are fp32.
 #include "kv_attn.cuh"
 #include "launch.h"
 #include "timer.h"
+#include "tmap.h"
 
 namespace sage {
 
 namespace {
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kChunk = 16;        // tokens of one step of a warp; a page is a whole number of them
-constexpr int kStages = 4;        // chunks of a warp in flight
-constexpr int kCtasPerSm = 3;     // the ring (4 warps x 4 chunks x 2 x 16 D bytes) of D = 128 is 64 KB
+constexpr int kSub = 2;           // 16-token MMA row tiles of a chunk
+constexpr int kChunk = 16 * kSub; // tokens of one step of a warp
+constexpr int kStages = 2;        // chunks of a warp in flight or at work
+constexpr int kTiers = 1;         // of the line's cut (see Line)
+constexpr int kTierChunks = 64;   // chunks for each CTA that a line needs to be cut in tiers
+constexpr int kCtasPerSm = 3;     // registers (168 a thread) and the rings (64 KB) allow as many
 
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -50,35 +54,37 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
 }
 template <int D>
 struct Ring {
-  static constexpr int kPieces = D / 32;                  // 16-byte K pieces of a lane and chunk
-  static constexpr int kBytes = 2 * kChunk * D;           // K and V of a chunk
+  static constexpr int kBytes = 2 * kChunk * D;  // K and V of a chunk; also 16 rows of D fp32
   static constexpr int kWarpBytes = kStages * kBytes;
 };
 
-// Cross-warp exchange at the end of a unit's part, in the ring's place: [warp][row][D + 4] sums,
-// then maxima, row sums
-template <int D, int RT>
-struct Exchange {
-  static constexpr int R = 8 * RT, kRow = D + 4;
-  static constexpr int kFloats = kWarps * R * (kRow + 2);
-  static_assert(kFloats * 4 <= kWarps * Ring<D>::kWarpBytes, "the exchange fits in the ring");
-};
-
-struct Unit {
-  int b, slot, hk, tile, len, q_len, chunks;
+// A part of a unit: chunks [c0, c1) of a row tile of (batch row b, key/value head hk).
+struct FewSeg {
+  int b, slot, len, hk, tile, chunks, c0, c1;
+  long long unit_at;
 };
 
 template <int D, int KIND, int RT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    kv_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v) {
   constexpr int R = 8 * RT, NK = D / 16, NJ = D / 16;     // k-steps of S^T, 16-channel tiles of O^T
   constexpr int VB = D / 8;                               // bytes of a V piece (8 lanes cover a row)
-  extern __shared__ __align__(16) uint8_t smem[];
-  uint8_t* ring = smem;
-  float* xch = reinterpret_cast<float*>(smem);
-  long long* pre = reinterpret_cast<long long*>(smem + kWarps * Ring<D>::kWarpBytes);  // [B + 1] chunks before a batch row
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  long long* pre = reinterpret_cast<long long*>(ring + kWarps * Ring<D>::kWarpBytes);  // [B + 1] chunks before a batch row
+  int2* rows = reinterpret_cast<int2*>(pre + p.B + 1);                                // [B] slot, length
   __shared__ long long wsum[kWarps];
+  __shared__ uint64_t bars[kWarps][kStages];  // a ring place's copies have landed
+  __shared__ float4 meta[kWarps][kStages][kSub];  // K scale, log2 of V's scale (-inf: no keys there) and its inverse
+  __shared__ int abort;
+  __shared__ float xm[kWarps][R], xl[kWarps][R];
+  __shared__ int left_place[kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
   const sage_kv_cache& c = p.c;
+  if (tid < kWarps * kStages) mbar_init(&bars[0][0] + tid, 1);
+  if (tid == 0) abort = 0;
+  fence_mbar_init();
   pdl_wait();
   pdl_trigger();
 
@@ -86,46 +92,155 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
   const int per_b = c.Hkv * p.tiles;
   prefix_of<kThreads>(p.B, pre, wsum, [&](int b) {
     int slot;
-    return (long long)max(1, (row_length(p, b, slot) + kChunk - 1) / kChunk) * per_b;
+    const int len = row_length(p, b, slot);
+    rows[b] = make_int2(slot, len);
+    return (long long)max(1, (len + kChunk - 1) / kChunk) * per_b;
   });
   __syncthreads();
   const long long total = pre[p.B];
-  // a worker takes at least one chunk for each of its warps
-  const int workers = (int)min((long long)gridDim.x, (total + kWarps - 1) / kWarps);
+  // a part has at least one chunk for each warp; a long line is cut in tiers
+  const int wide = (int)min((long long)p.wide, (total + kWarps - 1) / kWarps);
+  const Line line(total, wide, total >= (long long)wide * kTierChunks ? p.tiers : 1);
   const int w0 = blockIdx.x;
-  if (w0 >= workers) return;
-  auto start_of = [&](int w) { return total * w / workers; };
-  long long at = start_of(w0);
-  const long long stop = start_of(w0 + 1);
-  int b = row_at(pre, p.B, at);
-
-  const uint32_t my_ring = smem_u32(ring) + warp * Ring<D>::kWarpBytes;
-  const uint8_t* my_ring_p = ring + warp * Ring<D>::kWarpBytes;
-  const int per_page = c.page / kChunk;
-  const int page_shift = 31 - __clz(per_page);
-  const size_t page_bytes = (size_t)c.page * D;
-
-  while (at < stop) {
+  if (w0 >= line.parts()) return;
+  const long long begin = line.start(w0), stop = line.start(w0 + 1);
+  if (begin >= stop) return;
+  // the part of a unit that begins at `at`, in batch row b or behind it
+  auto seg_at = [&](long long at, int b) {
+    FewSeg s;
     while (pre[b + 1] <= at) ++b;
-    Unit u;
-    u.b = b;
-    u.len = row_length(p, b, u.slot);
-    u.chunks = max(1, (u.len + kChunk - 1) / kChunk);
-    const int in_b = (int)((at - pre[b]) / u.chunks);
-    const long long unit_at = pre[b] + (long long)in_b * u.chunks;
-    u.tile = in_b / c.Hkv;
-    u.hk = in_b % c.Hkv;
-    u.q_len = row_queries(p, b);
-    const int c0 = (int)(at - unit_at);
-    const int c1 = (int)min((long long)u.chunks, stop - unit_at);
-    const long long unit_id = (long long)b * per_b + in_b;
-    if (c0 == 0 && tid == 0) {
-      // the workers that hold the unit's first and last chunk
-      int last = w0;
-      while (start_of(last + 1) < unit_at + u.chunks) ++last;
-      p.info[unit_id] = make_int2(w0, last);
+    s.b = b;
+    s.slot = rows[b].x, s.len = rows[b].y;
+    s.chunks = max(1, (s.len + kChunk - 1) / kChunk);
+    const long long in = at - pre[b];
+    const int in_b = in <= 0xffffffffll ? (int)((uint32_t)in / (uint32_t)s.chunks) : (int)(in / s.chunks);
+    s.tile = in_b / c.Hkv;
+    s.hk = in_b % c.Hkv;
+    s.unit_at = pre[b] + (long long)in_b * s.chunks;
+    s.c0 = (int)(at - s.unit_at);
+    s.c1 = (int)min((long long)s.chunks, stop - s.unit_at);
+    return s;
+  };
+  // chunk k of this warp in a part is c0 + warp + kWarps k
+  auto chunks_of = [&](const FewSeg& s) { return max(0, (s.c1 - s.c0 - warp + kWarps - 1) / kWarps); };
+
+  // ---- copies.  They run ahead of the products, across parts, in windows of up to 32 chunks: a
+  // lane looks after one chunk, its page a window ahead.
+  uint8_t* my_ring = ring + warp * Ring<D>::kWarpBytes;
+  const int page_shift = 31 - __clz(c.page);
+  const bool halves = c.page < kChunk;  // a chunk is two pages of 16 tokens
+  int b = row_at(pre, p.B, begin);
+  FewSeg ns = seg_at(begin, b);    // the next window: window nw of part ns, nn chunks of this warp in it
+  int nw = 0, nn = chunks_of(ns), next_page = -1, next_half = -1;
+  bool have_next = true;
+  int left = 0, at_i = 0;          // chunks of the window that are still to be copied, and the next one's lane
+  int w_page = -1, w_half = -1, w_row = 0;  // the lane's chunk: page (-1: no keys), that of its second half, row
+  float ref = 0.f;
+  float4 w_meta[kSub] = {};
+  auto load_window = [&]() {
+    const int k = nw * 32 + lane, token = (ns.c0 + warp + kWarps * k) * kChunk;
+    const int* row = c.table + (size_t)ns.slot * c.max_pages + (token >> page_shift);
+    next_page = k < nn && token < ns.len ? row[0] : -1;
+    next_half = halves && k < nn && token + 16 < ns.len ? row[1] : -1;
+  };
+  auto next_window = [&]() {
+    if (++nw * 32 >= nn) {
+      nw = 0;
+      do {
+        const long long at = ns.unit_at + ns.c1;
+        if (at >= stop) {
+          have_next = false;
+          return;
+        }
+        ns = seg_at(at, ns.b);
+        nn = chunks_of(ns);
+      } while (nn == 0);
     }
-    at = unit_at + c1;
+    load_window();
+  };
+  int place = 0, flight = 0;       // ring place of the next copy; chunks copied or on their way, not yet used
+  auto issue = [&]() {
+    float ks[kSub] = {}, vs[kSub] = {};
+    const bool enter = left == 0 && have_next;
+    if (enter) {
+      w_page = (unsigned)next_page < (unsigned)c.n_pages ? next_page : -1;
+      w_half = (unsigned)next_half < (unsigned)c.n_pages ? next_half : -1;
+      if (w_page != next_page || w_half != next_half) atomicMax(c.status, kDevIndex);
+      w_row = ns.hk * c.page + (((ns.c0 + warp + kWarps * (nw * 32 + lane)) * kChunk) & (c.page - 1));
+      const int second = halves ? w_half : w_page;
+      if (w_page >= 0) {
+        ks[0] = c.k_scale[(size_t)w_page * c.Hkv + ns.hk];
+        vs[0] = c.v_scale[(size_t)w_page * c.Hkv + ns.hk];
+      }
+      if (second >= 0) {
+        ks[1] = c.k_scale[(size_t)second * c.Hkv + ns.hk];
+        vs[1] = c.v_scale[(size_t)second * c.Hkv + ns.hk];
+      }
+      left = min(32, nn - nw * 32);
+      at_i = 0;
+      next_window();
+    }
+    if (left == 0) return;
+    const int page = __shfl_sync(0xffffffffu, w_page, at_i), row = __shfl_sync(0xffffffffu, w_row, at_i);
+    const int half = halves ? __shfl_sync(0xffffffffu, w_half, at_i) : -1;
+    uint64_t* bar = &bars[warp][place];
+    if (lane == 0) {
+      uint8_t* dst = my_ring + place * Ring<D>::kBytes;
+      const uint32_t box = Ring<D>::kBytes >> (halves ? 1 : 0);
+      const uint32_t bytes = (page >= 0 ? box : 0) + (half >= 0 ? box : 0);
+      if (bytes)
+        mbar_arrive_expect_tx(bar, bytes);
+      else
+        mbar_arrive(bar);
+      if (page >= 0) {
+        tma_load_3d(dst, &tm_k, 0, row, page, bar);
+        tma_load_3d(dst + kChunk * D, &tm_v, 0, row, page, bar);
+      }
+      if (half >= 0) {
+        tma_load_3d(dst + 16 * D, &tm_k, 0, row, half, bar);
+        tma_load_3d(dst + (kChunk + 16) * D, &tm_v, 0, row, half, bar);
+      }
+    }
+    if (enter) {  // (the scales have been on their way)
+      float big = fmaxf(vs[0], vs[1]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+      ref = fmaxf(ref, big);
+#pragma unroll
+      for (int h = 0; h < kSub; ++h) {
+        const float ve = value_scale(vs[h], ref);
+        const bool none = (h && halves ? w_half : w_page) < 0;
+        w_meta[h] = make_float4(ks[h], none ? -INFINITY : lg2(ve), __frcp_rn(ve), 0.f);
+      }
+    }
+    if (lane == at_i) {
+#pragma unroll
+      for (int h = 0; h < kSub; ++h) meta[warp][place][h] = w_meta[h];
+    }
+    ++at_i, --left, ++flight;
+    place = place + 1 == kStages ? 0 : place + 1;
+  };
+  // where a lane reads in a 128-byte (D = 64: 64-byte) swizzled box.  MMA row g stands for token
+  // tk = g, odd g for g ^ 4: the eight lanes of a load then meet in no bank.  K token tk, unit tig (and
+  // tig + 4); V tokens 2 tig, (2 tig + 1) ^ 4 (and + 8), channels g VB ..
+  const int tk = g ^ (g & 1) << 2, tv = (2 * tig + 1) ^ 4;
+  const uint32_t at_k = D == 128 ? tk * 128 + ((tig ^ tk) << 4) : tk * 64 + ((tig ^ (tk >> 1)) << 4);
+  const uint32_t at_v0 = D == 128 ? tig * 256 + ((g ^ 2 * tig) << 4) : tig * 128 + (((g >> 1) ^ tig) << 4) + (g & 1) * 8;
+  const uint32_t at_v1 = D == 128 ? tv * 128 + ((g ^ tv) << 4) : tv * 64 + (((g >> 1) ^ (tv >> 1)) << 4) + (g & 1) * 8;
+  if (nn) load_window();
+  else next_window();
+#pragma unroll 1
+  for (int k = 0; k < kStages - 1; ++k) issue();
+
+  uint32_t phase = 0;
+  int here = 0;                    // ring place of the next products
+  for (long long at = begin; at < stop;) {
+    const FewSeg u = seg_at(at, b);
+    b = u.b;
+    at = u.unit_at + u.c1;
+    const int q_len = row_queries(p, b);
+    if (u.c0 == 0 && tid == 0)  // the parts that hold the unit's first and last chunk
+      p.info[(long long)b * per_b + u.tile * c.Hkv + u.hk] = make_int2(w0, line.holder(u.unit_at + u.chunks - 1));
 
     // rows of this lane as B columns (row g of each 8-row tile) and as accumulator columns
     uint32_t qf[RT][NK][2];
@@ -134,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const int row = u.tile * R + t * 8 + g, i = row / p.G;
-      const bool live = i < u.q_len;
+      const bool live = i < q_len;
       const __nv_bfloat16* q =
           p.Q + (((size_t)b * p.H + (size_t)u.hk * p.G + row % p.G) * p.Nq + (live ? i : 0)) * D;
       float x[NK][4];
@@ -155,12 +270,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
       row_power(top, up, down);
 #pragma unroll
       for (int s = 0; s < NK; ++s) {
-        qf[t][s][0] = h2bits(__floats2half2_rn(x[s][0] * up, x[s][1] * up));
-        qf[t][s][1] = h2bits(__floats2half2_rn(x[s][2] * up, x[s][3] * up));
+        qf[t][s][0] = h2bits(__floats2half2_rn(x[s][0] * up, x[s][2] * up));
+        qf[t][s][1] = h2bits(__floats2half2_rn(x[s][1] * up, x[s][3] * up));
       }
       const float a = p.alpha * down * kCodeUnit<KIND>;
       // (a row that is not there holds q = 0 and masks nothing; it is not stored)
-      const int end = live ? row_end(p, u.len, u.q_len, i) : u.len;
+      const int end = live ? row_end(p, u.len, q_len, i) : u.len;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         ar[t][e] = __shfl_sync(0xffffffffu, a, (2 * tig + e) * 4);
@@ -183,174 +298,147 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
       l[t][0] = l[t][1] = 0.f;
     }
 
-    // chunk k of this warp is c0 + warp + kWarps k; a lane looks up one of 32 pages at a time
-    const int mine = c1 > c0 + warp ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0;
-    const int* row = c.table + (size_t)u.slot * c.max_pages;
-    int id_next = -1, id_now = -1;
-    float ks_now = 0.f, vs_now = 0.f, ks_next = 0.f, vs_next = 0.f;
-    auto look_up = [&](int k, int& id, float& ks, float& vs) {
-      id = -1, ks = vs = 0.f;
-      const int ch = c0 + warp + kWarps * k;
-      if (k < mine && ch * kChunk < u.len) {
-        const int page = row[ch >> page_shift];
-        if ((unsigned)page < (unsigned)c.n_pages) {
-          id = page;
-          ks = c.k_scale[(size_t)page * c.Hkv + u.hk];
-          vs = c.v_scale[(size_t)page * c.Hkv + u.hk] * kCodeUnit<KIND>;
-        } else {
-          atomicMax(c.status, kDevIndex);
-        }
-      }
-    };
-    auto issue = [&](int k) {
-      if (k < mine) {
-        const int id = __shfl_sync(0xffffffffu, (k >> 5) & 1 ? id_next : id_now, k & 31);
-        if (id >= 0) {
-          const int ch = c0 + warp + kWarps * k;
-          const size_t off = ((size_t)id * c.Hkv + u.hk) * page_bytes + (size_t)((ch & (per_page - 1)) * kChunk) * D;
-          const uint8_t* kp = static_cast<const uint8_t*>(c.k) + off;
-          const uint8_t* vp = static_cast<const uint8_t*>(c.v) + off;
-          const uint32_t dst = my_ring + (k % kStages) * Ring<D>::kBytes;
-#pragma unroll
-          for (int i = 0; i < Ring<D>::kPieces; ++i) {
-            // D = 128: pieces 0, 1 of token g, 2, 3 of token g + 8; D = 64: one piece of each
-            const int tok = g + (D == 128 ? 8 * (i >> 1) : 8 * i), byte = tig * 16 + (D == 128 ? 64 * (i & 1) : 0);
-            cp_async16(dst + (i * 32 + lane) * 16, kp + tok * D + byte);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int tok = 2 * tig + (i & 1) + 8 * (i >> 1);
-            if (D == 128)
-              cp_async16(dst + kChunk * D + (i * 32 + lane) * 16, vp + tok * D + g * VB);
-            else
-              cp_async8(dst + kChunk * D + (i * 32 + lane) * 8, vp + tok * D + g * VB);
-          }
-        }
-      }
-      cp_commit();
-    };
-    look_up(lane, id_now, ks_now, vs_now);
-    look_up(lane + 32, id_next, ks_next, vs_next);
 #pragma unroll 1
-    for (int k = 0; k < kStages - 1; ++k) issue(k);
-
-#pragma unroll 1
-    for (int k = 0; k < mine; ++k) {
-      cp_wait<kStages - 2>();
-      issue(k + kStages - 1);
-      const bool odd = (k >> 5) & 1;
-      const int id = __shfl_sync(0xffffffffu, odd ? id_next : id_now, k & 31);
-      const float ks = __shfl_sync(0xffffffffu, odd ? ks_next : ks_now, k & 31);
-      const float vs = __shfl_sync(0xffffffffu, odd ? vs_next : vs_now, k & 31);
-      if ((k & 31) == 31) {
-        // the 32 pages just finished make room for those 64 ahead
-        if (odd) look_up(k + 33 + lane, id_next, ks_next, vs_next);
-        else look_up(k + 33 + lane, id_now, ks_now, vs_now);
-      }
-      if (id < 0) continue;
-      const uint8_t* src = my_ring_p + (k % kStages) * Ring<D>::kBytes;
+    for (int k = chunks_of(u), ch = u.c0 + warp; k > 0; --k, ch += kWarps) {
+      issue();
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars[warp][here], phase, &abort))) break;
+      __syncwarp();  // (meta)
+      --flight;
+      const uint8_t* src = my_ring + here * Ring<D>::kBytes;
+      float4 sc[kSub];
+#pragma unroll
+      for (int h = 0; h < kSub; ++h) sc[h] = meta[warp][here][h];
+      if (++here == kStages) here = 0, phase ^= 1;
       // S^T
-      float s[RT][4];
+      float s[kSub][RT][4];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-      constexpr int HP = Ring<D>::kPieces / 2;  // pieces of one token
+      for (int h = 0; h < kSub; ++h)
 #pragma unroll
-      for (int h = 0; h < HP; ++h) {
-        const uint4 ka = reinterpret_cast<const uint4*>(src)[h * 32 + lane];
-        const uint4 kb = reinterpret_cast<const uint4*>(src)[(HP + h) * 32 + lane];
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        for (int t = 0; t < RT; ++t) s[h][t][0] = s[h][t][1] = s[h][t][2] = s[h][t][3] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t a0, a1, a2, a3;
-          codes_to_half<KIND>(wa[w], a0, a2);
-          codes_to_half<KIND>(wb[w], a1, a3);
+      for (int x = 0; x < D / 64; ++x) {
 #pragma unroll
-          for (int t = 0; t < RT; ++t) mma16816(s[t], a0, a1, a2, a3, qf[t][h * 4 + w][0], qf[t][h * 4 + w][1]);
+        for (int h = 0; h < kSub; ++h) {
+          const uint4 ka = *reinterpret_cast<const uint4*>(src + h * 16 * D + (at_k ^ x * 64));
+          const uint4 kb = *reinterpret_cast<const uint4*>(src + h * 16 * D + (at_k ^ x * 64) + 8 * D);
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a0, a1, a2, a3;
+            codes_to_half<KIND>(wa[w], a0, a2);
+            codes_to_half<KIND>(wb[w], a1, a3);
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+              mma16816(s[h][t], a0, a1, a2, a3, qf[t][x * 4 + w][0], qf[t][x * 4 + w][1]);
+          }
         }
       }
-      // softmax of the lane's tokens g, g + 8 in rows 2 tig, 2 tig + 1
-      const int j0 = (c0 + warp + kWarps * k) * kChunk + g;
-      const bool edge = (c0 + warp + kWarps * k) * kChunk + kChunk > lim_min;
-      uint32_t pb[RT][2];
-      float corr[RT][2];
-      bool moved = false;
+      // softmax of the lane's tokens tk, tk + 8 of each row tile in rows 2 tig, 2 tig + 1
+      const bool edge = (ch + 1) * kChunk > lim_min;
+      bool raise = false;
+      float mx[RT][2];
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[t][e] = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < kSub; ++h) {
+            const float f = ar[t][e] * sc[h].x;
+            s[h][t][e] = fmaf(s[h][t][e], f, sc[h].y);
+            s[h][t][2 + e] = fmaf(s[h][t][2 + e], f, sc[h].y);
+            if (edge) {
+              const int j = ch * kChunk + h * 16 + tk;
+              if (j >= lim[t][e]) s[h][t][e] = -INFINITY;
+              if (j + 8 >= lim[t][e]) s[h][t][2 + e] = -INFINITY;
+            }
+            mx[t][e] = max3(mx[t][e], s[h][t][e], s[h][t][2 + e]);
+          }
+          raise |= mx[t][e] > m[t][e] + kRaise;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          float corr[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float x = mx[t][e];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float to = x > m[t][e] + kRaise ? x - kBelow : m[t][e];
+            corr[e] = to == m[t][e] ? 1.f : ex2(m[t][e] - to);
+            m[t][e] = to;
+            l[t][e] *= corr[e];
+          }
+#pragma unroll
+          for (int j = 0; j < NJ; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[t][j][e] *= corr[e & 1];
+        }
+      }
+      uint32_t pb[kSub][RT][2];
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float f = ar[t][e] * ks;
-          s[t][e] *= f;
-          s[t][2 + e] *= f;
-          if (edge) {
-            if (j0 >= lim[t][e]) s[t][e] = -INFINITY;
-            if (j0 + 8 >= lim[t][e]) s[t][2 + e] = -INFINITY;
+          const float sub = m[t][e] == -INFINITY ? 0.f : m[t][e];
+#pragma unroll
+          for (int h = 0; h < kSub; ++h) {
+            s[h][t][e] = ex2(s[h][t][e] - sub);
+            s[h][t][2 + e] = ex2(s[h][t][2 + e] - sub);
+            l[t][e] = fmaf(s[h][t][e] + s[h][t][2 + e], sc[h].z, l[t][e]);
           }
-          float mx = fmaxf(s[t][e], s[t][2 + e]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float mn = fmaxf(m[t][e], mx);
-          const float sub = mn == -INFINITY ? 0.f : mn;
-          corr[t][e] = ex2(m[t][e] - sub);
-          moved |= mn != m[t][e];
-          m[t][e] = mn;
-          s[t][e] = ex2(s[t][e] - sub);
-          s[t][2 + e] = ex2(s[t][2 + e] - sub);
-          l[t][e] = l[t][e] * corr[t][e] + (s[t][e] + s[t][2 + e]);
         }
-        pb[t][0] = movmatrix(h2bits(__floats2half2_rn(s[t][0], s[t][1])));
-        pb[t][1] = movmatrix(h2bits(__floats2half2_rn(s[t][2], s[t][3])));
-      }
-      if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int j = 0; j < NJ; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[t][j][e] *= corr[t][e & 1];
-      }
-      // O^T: tokens 2 tig, 2 tig + 1 (pair 0) and + 8 (pair 1), channels g VB + 2 j, + 1 of tile j
-      const uint8_t* vsrc = src + kChunk * D;
-      uint32_t v[4][VB / 4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (D == 128) {
-          const uint4 x = reinterpret_cast<const uint4*>(vsrc)[i * 32 + lane];
-          v[i][0] = x.x, v[i][1] = x.y, v[i][VB / 4 - 2] = x.z, v[i][VB / 4 - 1] = x.w;
-        } else {
-          const uint2 x = reinterpret_cast<const uint2*>(vsrc)[i * 32 + lane];
-          v[i][0] = x.x, v[i][1] = x.y;
+        for (int h = 0; h < kSub; ++h) {
+          pb[h][t][0] = movmatrix(h2bits(__floats2half2_rn(s[h][t][0], s[h][t][1])));
+          pb[h][t][1] = movmatrix(h2bits(__floats2half2_rn(s[h][t][2], s[h][t][3])));
         }
       }
+      // O^T: the lane's tokens (pair 0) and those + 8 (pair 1); of the bytes 4 w + 0..3 of the
+      // lane's channels g VB .., tile 2 w takes 0 and 1, tile 2 w + 1 takes 2 and 3
 #pragma unroll
-      for (int w = 0; w < VB / 4; ++w) {
-        uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-        codes_to_half<KIND>(__byte_perm(v[0][w], v[1][w], 0x5140), a0, a1);
-        codes_to_half<KIND>(__byte_perm(v[2][w], v[3][w], 0x5140), a2, a3);
-        codes_to_half<KIND>(__byte_perm(v[0][w], v[1][w], 0x7362), b0, b1);
-        codes_to_half<KIND>(__byte_perm(v[2][w], v[3][w], 0x7362), b2, b3);
+      for (int h = 0; h < kSub; ++h) {
+        const uint8_t* vsrc = src + (kChunk + h * 16) * D;
+        uint32_t v[4][VB / 4];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
-          mma16816(d0, a0, a1, a2, a3, pb[t][0], pb[t][1]);
-          mma16816(d1, b0, b1, b2, b3, pb[t][0], pb[t][1]);
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* y = vsrc + (i & 1 ? at_v1 : at_v0) + (i >> 1) * 8 * D;
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(y);
+            v[i][0] = x.x, v[i][1] = x.y, v[i][VB / 4 - 2] = x.z, v[i][VB / 4 - 1] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(y);
+            v[i][0] = x.x, v[i][1] = x.y;
+          }
+        }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            acc[t][2 * w][e] = fmaf(vs, d0[e], acc[t][2 * w][e]);
-            acc[t][2 * w + 1][e] = fmaf(vs, d1[e], acc[t][2 * w + 1][e]);
+        for (int w = 0; w < VB / 4; ++w) {
+          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+          codes_to_half<KIND>(__byte_perm(v[0][w], v[1][w], 0x5410), a0, a1);
+          codes_to_half<KIND>(__byte_perm(v[2][w], v[3][w], 0x5410), a2, a3);
+          codes_to_half<KIND>(__byte_perm(v[0][w], v[1][w], 0x7632), b0, b1);
+          codes_to_half<KIND>(__byte_perm(v[2][w], v[3][w], 0x7632), b2, b3);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            mma16816(acc[t][2 * w], a0, a1, a2, a3, pb[h][t][0], pb[h][t][1]);
+            mma16816(acc[t][2 * w + 1], b0, b1, b2, b3, pb[h][t][0], pb[h][t][1]);
           }
         }
       }
     }
-    cp_wait<0>();
-    __syncthreads();  // every warp is done with its ring
 
-    // ---- the warps' results of this part
-    constexpr int kRow = Exchange<D, RT>::kRow;
-    float* xm = xch + kWarps * R * kRow;  // [warp][R] maxima
-    float* xl = xm + kWarps * R;
+    // ---- the warps' results of this part, through the ring place that each warp has just left (the
+    // copies into the others go on).  16-byte unit x of row r lies at x ^ (r / 2 % 4), against bank
+    // conflicts.
+    const bool whole = u.c0 == 0 && u.c1 == u.chunks;
+    float* part = p.part + (size_t)(2 * w0 + (u.c0 == 0 ? 1 : 0)) * R * (D + 2);
+    const int left_at = here == 0 ? kStages - 1 : here - 1;
+    float4* mine = reinterpret_cast<float4*>(my_ring + left_at * Ring<D>::kBytes);
+    if (lane == 0) left_place[warp] = left_at;
 #pragma unroll
-    for (int t = 0; t < RT; ++t) {
+    for (int t = 0; t < RT; ++t)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float s = l[t][e];
@@ -358,33 +446,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
         s += __shfl_xor_sync(0xffffffffu, s, 8);
         s += __shfl_xor_sync(0xffffffffu, s, 16);
         const int r = t * 8 + 2 * tig + e;
-        if (g == 0) xm[warp * R + r] = m[t][e], xl[warp * R + r] = s;
-        float* dst = xch + (size_t)(warp * R + r) * kRow + g * VB;
+        if (g == 0) xm[warp][r] = m[t][e], xl[warp][r] = s;
 #pragma unroll
         for (int j = 0; j < NJ; j += 2)
-          *reinterpret_cast<float4*>(dst + 2 * j) =
+          mine[r * (D / 4) + ((g * (VB / 4) + j / 2) ^ (r >> 1 & 3))] =
               make_float4(acc[t][j][e], acc[t][j][2 + e], acc[t][j + 1][e], acc[t][j + 1][2 + e]);
       }
-    }
     __syncthreads();
-    const bool whole = c0 == 0 && c1 == u.chunks;
-    float* part = p.part + (size_t)(2 * w0 + (c0 == 0 ? 1 : 0)) * R * (D + 2);
     for (int x = tid; x < R * (D / 4); x += kThreads) {
-      const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+      const int r = x / (D / 4), d = x % (D / 4);
       const int rw = u.tile * R + r, i = rw / p.G;
-      if (i >= u.q_len) continue;
+      if (i >= q_len) continue;
       float mt = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, xm[w * R + r]);
+      for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, xm[w][r]);
       const float sub = mt == -INFINITY ? 0.f : mt;
       float ls = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(xm[w * R + r] - sub);
-        ls = fmaf(f, xl[w * R + r], ls);
-        const float4 y = *reinterpret_cast<const float4*>(xch + (size_t)(w * R + r) * kRow + d);
+        const float f = ex2(xm[w][r] - sub);
+        ls = fmaf(f, xl[w][r], ls);
+        const float4 y = reinterpret_cast<const float4*>(ring + w * Ring<D>::kWarpBytes +
+                                                         left_place[w] * Ring<D>::kBytes)[r * (D / 4) + (d ^ (r >> 1 & 3))];
         o[0] = fmaf(f, y.x, o[0]), o[1] = fmaf(f, y.y, o[1]), o[2] = fmaf(f, y.z, o[2]), o[3] = fmaf(f, y.w, o[3]);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] *= kCodeUnit<KIND>;
       if (whole) {
         const float inv = ls > 0.f ? 1.f / ls : 0.f;
         const size_t orow = ((size_t)b * p.H + (size_t)u.hk * p.G + rw % p.G) * p.Nq + i;
@@ -392,14 +479,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) kv_attn_kernel(const Att
         __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&out);
         h[0] = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
         h[1] = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
-        *reinterpret_cast<uint2*>(p.O + orow * D + d) = out;
+        *reinterpret_cast<uint2*>(p.O + orow * D + d * 4) = out;
         if (d == 0) p.LSE[orow] = ls > 0.f ? (mt + log2f(ls)) * 0.69314718055994531f : -INFINITY;
       } else {
-        *reinterpret_cast<float4*>(part + r * D + d) = make_float4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<float4*>(part + r * D + d * 4) = make_float4(o[0], o[1], o[2], o[3]);
         if (d == 0) part[R * D + r] = mt, part[R * D + R + r] = ls;
       }
     }
-    __syncthreads();  // the exchange is read before the next part fills it
+    fence_proxy_async_smem();  // the places are read before they are filled again
+    if (__syncthreads_or(abort)) break;
+  }
+  if (abort) {  // a wait ran out: the copies that are still in flight
+    if (tid == 0) atomicMax(c.status, (int)kDevTimeout);
+    for (; flight > 0; --flight) {
+      int give_up = 0;
+      mbar_wait(&bars[warp][here], phase, &give_up);
+      if (++here == kStages) here = 0, phase ^= 1;
+    }
   }
 }
 
@@ -483,17 +579,34 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R)
   if (d == 0) p.LSE[orow] = ls > 0.f ? (mt + log2f(ls)) * 0.69314718055994531f : -INFINITY;
 }
 
+// The cut: as many CTAs as run at once, kTiers times over if the line can be that long.
+void few_cut(AttnParams& p, int ctas) {
+  const long long most = (long long)p.B * p.c.Hkv * p.tiles * (((long long)p.c.max_pages * p.c.page + kChunk - 1) / kChunk);
+  const long long need = (most + kWarps - 1) / kWarps;
+  p.wide = ctas < kMaxParts / kTiers ? ctas : kMaxParts / kTiers;
+  if (need < p.wide) p.wide = (int)need;
+  p.tiers = most >= (long long)p.wide * kTierChunks ? kTiers : 1;
+}
+
 template <int D, int KIND, int RT>
-int launch_few(const AttnParams& p, int sms, cudaStream_t st) {
+int launch_few(const AttnParams& p, cudaStream_t st) {
   auto kern = kv_attn_kernel<D, KIND, RT>;
-  const size_t smem = (size_t)kWarps * Ring<D>::kWarpBytes + ((size_t)p.B + 1) * 8;
+  // a page's rows [head, token]: boxes of a chunk's tokens
+  const int box = p.c.page < kChunk ? p.c.page : kChunk;
+  const CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  CUtensorMap tk, tv;
+  if (!make_tmap_3d(&tk, p.c.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, (uint64_t)p.c.Hkv * p.c.page, p.c.n_pages, D,
+                    box, swizzle) ||
+      !make_tmap_3d(&tv, p.c.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, (uint64_t)p.c.Hkv * p.c.page, p.c.n_pages, D,
+                    box, swizzle))
+    return 3;
+  const size_t smem = 1024 + (size_t)kWarps * Ring<D>::kWarpBytes + ((size_t)p.B + 1) * 16;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 3;
-  const int grid = sms * kCtasPerSm < kMaxWorkers ? sms * kCtasPerSm : kMaxWorkers;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p) == cudaSuccess ? 0 : 3;
+  return launch_pdl(kern, dim3(p.wide * p.tiers), dim3(kThreads), smem, st, p, tk, tv) == cudaSuccess ? 0 : 3;
 }
 template <int D, int KIND>
-int launch_few(const AttnParams& p, int rows, int sms, cudaStream_t st) {
-  return rows == 8 ? launch_few<D, KIND, 1>(p, sms, st) : launch_few<D, KIND, 2>(p, sms, st);
+int launch_few(const AttnParams& p, int rows, cudaStream_t st) {
+  return rows == 8 ? launch_few<D, KIND, 1>(p, st) : launch_few<D, KIND, 2>(p, st);
 }
 
 // Query rows of a unit: 8 where all rows of a shared head fit in one, 16 up to kFewRows rows, then
@@ -502,12 +615,13 @@ constexpr long long kFewRows = 32;
 
 }  // namespace
 
-int launch_kv_few(const AttnParams& p, int kind, int rows, int sms, cudaStream_t st) {
+int launch_kv_few(AttnParams p, int kind, int rows, int sms, cudaStream_t st) {
+  few_cut(p, sms * kCtasPerSm);
   if (p.c.D == 128)
-    return kind == SAGE_KV_INT8 ? launch_few<128, SAGE_KV_INT8>(p, rows, sms, st)
-                                : launch_few<128, SAGE_KV_E4M3>(p, rows, sms, st);
-  return kind == SAGE_KV_INT8 ? launch_few<64, SAGE_KV_INT8>(p, rows, sms, st)
-                              : launch_few<64, SAGE_KV_E4M3>(p, rows, sms, st);
+    return kind == SAGE_KV_INT8 ? launch_few<128, SAGE_KV_INT8>(p, rows, st)
+                                : launch_few<128, SAGE_KV_E4M3>(p, rows, st);
+  return kind == SAGE_KV_INT8 ? launch_few<64, SAGE_KV_INT8>(p, rows, st)
+                              : launch_few<64, SAGE_KV_E4M3>(p, rows, st);
 }
 
 KvAttnWs kv_attn_ws_layout(int B, int H, int Hkv, int D, int Nq) {
@@ -517,7 +631,7 @@ KvAttnWs kv_attn_ws_layout(int B, int H, int Hkv, int D, int Nq) {
   L.tiles = (int)((rows + L.rows - 1) / L.rows);
   L.info = 0;
   L.part = ((size_t)B * Hkv * L.tiles * 8 + 255) & ~(size_t)255;
-  const size_t workers = L.rows == kChunkRows ? kMaxChunkWorkers : kMaxWorkers;
+  const size_t workers = L.rows == kChunkRows ? kMaxChunkParts : kMaxParts;
   L.total = L.part + workers * 2 * L.rows * (D + 2) * 4;
   return L;
 }

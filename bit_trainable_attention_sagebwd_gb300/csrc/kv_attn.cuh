@@ -19,6 +19,7 @@ struct AttnParams {
   int2* info;      // first and last worker of each unit
   float* part;     // two partial results of each worker: [R][D] sums, then [R] maxima and [R] row sums
   int B, H, G, Nq, tiles, causal;
+  int wide, tiers; // the cut of the line (see Line): CTAs that run at once, tiers at most
   float alpha;     // sm_scale log2 e
 };
 
@@ -27,6 +28,11 @@ namespace {  // internal linkage: each translation unit keeps its own copy
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t h2bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -46,30 +52,45 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Two codes as fp16.  int8, with the sign bit flipped (byte c + 128): 0x6400 + byte is the fp16
-// 1024 + c + 128.  e4m3: sign, exponent and fraction moved to fp16's places give the value times
-// 2^-8 (subnormal codes too), which kCodeUnit takes back in the scales; every byte is finite.
+// Four codes of a word as fp16: bytes (0, 2) and bytes (1, 3), the pairing that takes the fewest
+// instructions; who contracts over the channels or writes them out puts up with the order.
+// int8: byte ^ 0x80 under the exponent 0x64 is the fp16 1024 + c + 128.  e4m3: sign, exponent and
+// fraction moved to fp16's places give the value times 2^-8 (subnormal codes too), which kCodeUnit
+// takes back; every byte is finite.
 template <int KIND>
 constexpr float kCodeUnit = KIND == SAGE_KV_INT8 ? 1.f : 256.f;
 
-// bytes (0, 1) and (2, 3) of a word
 template <int KIND>
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& even, uint32_t& odd) {
   if (KIND == SAGE_KV_INT8) {
-    w ^= 0x80808080u;
-    lo = hsub2(__byte_perm(w, 0x64646464u, 0x4140), 0x64806480u);
-    hi = hsub2(__byte_perm(w, 0x64646464u, 0x4342), 0x64806480u);
+    even = hsub2((w & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
+    odd = hsub2(((w >> 8) & 0x00ff00ffu) ^ 0x64806480u, 0x64806480u);
   } else {
-    const uint32_t a = __byte_perm(w, 0u, 0x1404), b = __byte_perm(w, 0u, 0x3424);
-    lo = (a & 0x80008000u) | ((a >> 1) & 0x3f803f80u);
-    hi = (b & 0x80008000u) | ((b >> 1) & 0x3f803f80u);
+    even = ((w << 7) & 0x3f803f80u) | ((w << 8) & 0x80008000u);
+    odd = ((w >> 1) & 0x3f803f80u) | (w & 0x80008000u);
   }
+}
+
+// P and the V scales.  s_v of a page goes into the exponent: with t_j the logit of key j in powers of
+// two and u_j = t_j + log2 s_v(j), P_j = 2^(u_j - m), m a running reference of the u that keeps the
+// largest P of a row between 2^7 and 2^15, so fp16 holds P whatever the pages' scales are (11 bits
+// down to 2^-21 of the largest, 2^-32 of it absolute below); the row sum takes P_j / s_v(j).  m moves
+// only when a row's maximum passes 2^15, so accumulators are seldom rescaled.  A page of zeros
+// (s_v = 0) takes the largest scale met so far (`ref`) instead; scales below 2^-80 (values below 2^-71)
+// are read as 2^-80, so that the row sums stay in fp32's range.
+constexpr float kRaise = 15.f, kBelow = 7.f;
+__device__ __forceinline__ float value_scale(float vs, float ref) {
+  constexpr float kLeast = 0x1p-80f;
+  return vs > 0.f ? fmaxf(vs, kLeast) : ref > 0.f ? fmaxf(ref, kLeast) : 1.f;
 }
 
 // The power of two that brings a query row's largest element `top` to [2^8, 2^9), where fp16 holds
@@ -138,15 +159,47 @@ __device__ __forceinline__ int row_at(const long long* pre, int B, long long at)
   return lo;
 }
 
-// the most CTAs that share the line
-constexpr int kMaxWorkers = 1024;      // few query rows
-constexpr int kMaxChunkWorkers = 160;  // many (one CTA an SM)
+// The line of work, `total` chunks, cut into parts for the CTAs of a grid in order.  The first `wide` CTAs
+// (those that run at once) take kTier[1] of 64 shares of it in equal parts, the next `wide` CTAs the
+// shares up to kTier[2], and so on: CTAs of one SM do not progress alike (a third of a uniform cut's
+// time passed with the slower ones alone), and the smaller parts, which start as others end, even
+// that out.  Boundaries do not depend on who runs when.  A short line has one tier.
+struct Line {
+  long long total;
+  int wide, tiers;
+  __device__ Line(long long total, int wide, int tiers) : total(total), wide(wide), tiers(tiers) {}
+  __device__ long long tier_at(int t) const {
+    constexpr int kTier[4] = {0, 46, 56, 61};
+    return t >= tiers ? total : t == 0 ? 0 : total * (t == 1 ? kTier[1] : t == 2 ? kTier[2] : kTier[3]) / 64;
+  }
+  __device__ int parts() const { return wide * tiers; }
+  // where part v begins
+  __device__ long long start(int v) const {
+    const int t = v / wide;
+    const long long a = tier_at(t);
+    return a + (tier_at(t + 1) - a) * (v - t * wide) / wide;
+  }
+  // the part that holds place x
+  __device__ int holder(long long x) const {
+    int t = 0;
+    while (t + 1 < tiers && x >= tier_at(t + 1)) ++t;
+    const long long a = tier_at(t), n = tier_at(t + 1) - a;
+    int v = t * wide + (int)((x - a) * wide / n);
+    while (start(v + 1) <= x) ++v;
+    while (start(v) > x) --v;
+    return v;
+  }
+};
+
+// the most parts
+constexpr int kMaxParts = 2048;        // few query rows
+constexpr int kMaxChunkParts = 160;    // many (one CTA an SM)
 constexpr int kChunkRows = 256;        // query rows of a unit, many
 
 }  // namespace
 
 // the kernel of a few (up to 16) query rows a unit, and the one of kChunkRows
-int launch_kv_few(const AttnParams& p, int kind, int rows, int sms, cudaStream_t st);
+int launch_kv_few(AttnParams p, int kind, int rows, int sms, cudaStream_t st);
 int launch_kv_chunk(const AttnParams& p, int kind, int sms, cudaStream_t st);
 
 }  // namespace sage

@@ -13,14 +13,6 @@
 //  - warps 0-3 and 4-7 own a row tile each, a thread a row: S from TMEM, P back into TMEM over S's
 //    columns, from where the second product takes it.
 // Units are cut over the grid like those of the few-row kernel (kv_attn.cu), in 128-key tiles.
-//
-// Scales.  S gets the page's s_k before the exponent.  s_v goes into it: with t_j = S_j and
-// u_j = t_j + log2 s_v(j), P_j = 2^(u_j - m), m a running reference of the u that keeps the largest
-// P of a row between 2^7 and 2^15, so fp16 holds P whatever the pages' scales are (11 bits down to
-// 2^-21 of the largest, 2^-32 of it absolute below); the row sum takes P_j / s_v(j).  m moves only when a
-// row's maximum passes 2^15, so the accumulator is seldom rescaled.  A page of zeros (s_v = 0) takes
-// the largest scale met so far instead; scales below kLeast = 2^-80 (values below 2^-71) are read as
-// kLeast, so that the row sums stay in fp32's range.
 #include "kv_attn.cuh"
 #include "launch.h"
 
@@ -160,9 +152,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
   const long long total = sm.pre[kGroups];
-  const int workers = (int)min((long long)gridDim.x, total), w0 = blockIdx.x;
-  auto start_of = [&](int w) { return total * w / workers; };
-  const long long begin = w0 < workers ? start_of(w0) : 0, stop = w0 < workers ? start_of(w0 + 1) : 0;
+  const Line line(total, (int)min((long long)gridDim.x, max(total, 1ll)), 1);
+  const int w0 = blockIdx.x;
+  const bool idle = total == 0 || w0 >= line.parts();
+  const long long begin = idle ? 0 : line.start(w0), stop = idle ? 0 : line.start(w0 + 1);
   const int per_page = p.c.page >> 4;  // 16-key groups of a page
   const int page_shift = 31 - __clz(per_page);
   // the page of the 16-key group `grp` of a slot; -1: no key there
@@ -337,11 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
     while (ok && walk.more()) {
       const Seg s = walk.next(p);
       const long long unit_id = ((long long)s.b * p.tiles + s.rt) * p.c.Hkv + s.hk;
-      if (s.c0 == 0 && tid == 0) {
-        int last = w0;
-        while (start_of(last + 1) < s.unit_at + s.chunks) ++last;
-        p.info[unit_id] = make_int2(w0, last);
-      }
+      if (s.c0 == 0 && tid == 0)
+        p.info[unit_id] = make_int2(w0, line.holder(s.unit_at + s.chunks - 1));
       if (t == 1 && !s.two) continue;
       const long long row = (long long)s.rt * kChunkRows + t * kTile + r;
       const int i = (int)(row / p.G);
@@ -370,8 +360,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
           const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
           uint32_t h[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            h[e] = h2bits(__floats2half2_rn(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xffff0000u) * up));
+          for (int e = 0; e < 4; e += 2) {  // channels 0, 2 and 1, 3 of each four, as the codes come
+            h[e] = h2bits(__floats2half2_rn(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e + 1] << 16) * up));
+            h[e + 1] = h2bits(
+                __floats2half2_rn(__uint_as_float(x[e] & 0xffff0000u) * up, __uint_as_float(x[e + 1] & 0xffff0000u) * up));
+          }
           *reinterpret_cast<uint4*>(sm.q[t] + (u >> 3) * kAtom + (r >> 3) * 1024 + (r & 7) * 128 +
                                     (((u & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
         }
@@ -402,8 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
 #pragma unroll
         for (int o = 1; o < 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
         ref = fmaxf(ref, __shfl_sync(0xffffffffu, big, 0));
-        constexpr float kLeast = 0x1p-80f;
-        const float ve = vs > 0.f ? fmaxf(vs, kLeast) : ref > 0.f ? fmaxf(ref, kLeast) : 1.f;
+        const float ve = value_scale(vs, ref);
         const float lg = log2f(ve), iv = 1.f / ve;
         ok = ok && mbar_wait(&sm.bar_s[t], n_s & 1, abort);
         ++n_s;
@@ -441,9 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
             mx = fmaxf(mx, fmaf(y, f, __shfl_sync(0xffffffffu, lg, x)));
           }
         }
-        const bool raise = mx > m + 15.f;
+        const bool raise = mx > m + kRaise;
         if (__any_sync(0xffffffffu, raise)) {
-          const float to = raise ? mx - 7.f : m, corr = raise ? ex2(m - to) : 1.f;
+          const float to = raise ? mx - kBelow : m, corr = raise ? ex2(m - to) : 1.f;
           m = to;
           l *= corr;
           if (c > s.c0) {  // (the part's first product overwrites O; PV of the tile before is done: S came after it)
@@ -513,15 +505,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
             uint4 y;
             __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&y);
 #pragma unroll
-            for (int z = 0; z < 4; ++z)
-              h[z] = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * z]), __uint_as_float(o[8 * e + 2 * z + 1]));
+            for (int z = 0; z < 4; ++z)  // (V's channels came as 0, 2, 1, 3 too)
+              h[z] = __floats2bfloat162_rn(__uint_as_float(o[8 * e + (z >> 1) * 4 + (z & 1)]),
+                                           __uint_as_float(o[8 * e + (z >> 1) * 4 + (z & 1) + 2]));
             *reinterpret_cast<uint4*>(p.O + orow * D + d + 8 * e) = y;
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             *reinterpret_cast<uint4*>(part + (size_t)pr * D + d + 4 * e) =
-                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                make_uint4(o[4 * e], o[4 * e + 2], o[4 * e + 1], o[4 * e + 3]);
         }
       }
       if (ok && live) {
@@ -543,7 +536,7 @@ int launch(const AttnParams& p, int sms, cudaStream_t st) {
   auto kern = kv_chunk_kernel<D, KIND>;
   const size_t smem = sizeof(ChunkSmem<D>) + 1024;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 3;
-  const int grid = sms < kMaxChunkWorkers ? sms : kMaxChunkWorkers;
+  const int grid = sms < kMaxChunkParts ? sms : kMaxChunkParts;
   return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p) == cudaSuccess ? 0 : 3;
 }
 

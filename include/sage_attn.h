@@ -350,8 +350,7 @@ int sage_attn_kv_append(const sage_kv_cache *cache, const void *K, const void *V
  * S = sm_scale q . k, O = softmax(S) V, LSE = log sum e^S; a row that sees no key has O = 0 and
  * LSE = -infinity.  Codes and queries enter the products exactly (a query's elements below 2^-25 of its
  * largest are rounded); P is rounded to fp16 relative to the running maximum; everything else is fp32.
- * With more than 32 query rows of a shared head (H / Hkv * Nq) a V scale below 2^-80 is read as 2^-80.
- * sm_scale <= 0 selects 1/sqrt(D).
+ * V scales below 2^-80 are read as 2^-80.  sm_scale <= 0 selects 1/sqrt(D).
  * ws: sage_attn_kv_ws_bytes(B, H, Hkv, D, Nq) bytes, 16-byte aligned, contents free before and after.
  * Deterministic.  B is at most 4096.
  */
