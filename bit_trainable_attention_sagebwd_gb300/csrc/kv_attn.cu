@@ -9,7 +9,8 @@
 //  - The keys of all (batch row, key/value head) units form one line of 32-token chunks, cut into
 //    equal parts for a grid that fills the GPU once; a unit that is cut leaves partial results,
 //    joined by kv_join_kernel in the order of the parts.  Ragged batches and single long
-//    sequences load every SM alike.
+//    sequences load every SM alike.  Every unit begins with kPad places without a chunk, for the time
+//    that its start takes.
 //  - A warp walks its own chunks and keeps kStages - 1 of them in flight with TMA, across the ends of
 //    units, in a ring of its own: a chunk of K or V is one box of a page's [head, token] rows (two with
 //    pages of 16 tokens).  (Copies of 16 bytes a thread, cp.async, read the same bytes at 5.6 TB/s against 6.7.)
@@ -33,10 +34,15 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kSub = 2;           // 16-token MMA row tiles of a chunk
 constexpr int kChunk = 16 * kSub; // tokens of one step of a warp
-constexpr int kStages = 2;        // chunks of a warp in flight or at work
-constexpr int kTiers = 1;         // of the line's cut (see Line)
-constexpr int kTierChunks = 64;   // chunks for each CTA that a line needs to be cut in tiers
-constexpr int kCtasPerSm = 3;     // registers (168 a thread) and the rings (64 KB) allow as many
+// Chunks of a warp in flight or at work, and CTAs an SM: 8 query rows need 168 registers a thread, 16
+// need 255 (at 168 their spills cost a quarter of the time).
+template <int RT>
+constexpr int kStages = RT == 1 ? 2 : 3;
+template <int RT>
+constexpr int kCtasPerSm = RT == 1 ? 3 : 2;
+// What the start of a unit costs a CTA, in chunks of the line.  64 sequences of 500 to 8192 tokens took
+// 109 us without, 101 us with 4, 99 us with 8 to 16; 256 of 100 to 1000 110, 93, 83 and 82 us.
+constexpr int kPad = 12;
 
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -52,39 +58,44 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-template <int D>
+template <int D, int RT>
 struct Ring {
   static constexpr int kBytes = 2 * kChunk * D;  // K and V of a chunk; also 16 rows of D fp32
-  static constexpr int kWarpBytes = kStages * kBytes;
+  static constexpr int kWarpBytes = kStages<RT> * kBytes;
 };
 
-// A part of a unit: chunks [c0, c1) of a row tile of (batch row b, key/value head hk).
+// A part of a unit: chunks [c0, c1) of a row tile of (batch row b, key/value head hk); `next`: where
+// on the line it ends, `unit_at`: where the unit's first chunk is.
 struct FewSeg {
   int b, slot, len, hk, tile, chunks, c0, c1;
-  long long unit_at;
+  long long unit_at, next;
 };
 
 template <int D, int KIND, int RT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<RT>)
     kv_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v) {
   constexpr int R = 8 * RT, NK = D / 16, NJ = D / 16;     // k-steps of S^T, 16-channel tiles of O^T
   constexpr int VB = D / 8;                               // bytes of a V piece (8 lanes cover a row)
+  constexpr int kPlaces = kStages<RT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  long long* pre = reinterpret_cast<long long*>(ring + kWarps * Ring<D>::kWarpBytes);  // [B + 1] chunks before a batch row
+  long long* pre = reinterpret_cast<long long*>(ring + kWarps * Ring<D, RT>::kWarpBytes);  // [B + 1] chunks before a batch row
   int2* rows = reinterpret_cast<int2*>(pre + p.B + 1);                                // [B] slot, length
   __shared__ long long wsum[kWarps];
-  __shared__ uint64_t bars[kWarps][kStages];  // a ring place's copies have landed
-  __shared__ float4 meta[kWarps][kStages][kSub];  // K scale, log2 of V's scale (-inf: no keys there) and its inverse
+  __shared__ uint64_t bars[kWarps][kPlaces];  // a ring place's copies have landed
+  __shared__ float4 meta[kWarps][kPlaces][kSub];  // K scale, log2 of V's scale (-inf: no keys there) and its inverse
   __shared__ int abort;
   __shared__ float xm[kWarps][R], xl[kWarps][R];
   __shared__ int left_place[kWarps];
+  __shared__ __align__(16) __nv_bfloat16 q_buf[2][R * D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tig = lane & 3;
   const sage_kv_cache& c = p.c;
-  if (tid < kWarps * kStages) mbar_init(&bars[0][0] + tid, 1);
+  if (tid < kWarps * kPlaces) mbar_init(&bars[0][0] + tid, 1);
   if (tid == 0) abort = 0;
   fence_mbar_init();
+  tma_prefetch_desc(&tm_k);
+  tma_prefetch_desc(&tm_v);
   pdl_wait();
   pdl_trigger();
 
@@ -94,15 +105,22 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     int slot;
     const int len = row_length(p, b, slot);
     rows[b] = make_int2(slot, len);
-    return (long long)max(1, (len + kChunk - 1) / kChunk) * per_b;
+    return (long long)(kPad + max(1, (len + kChunk - 1) / kChunk)) * per_b;
   });
   __syncthreads();
   const long long total = pre[p.B];
-  // a part has at least one chunk for each warp; a long line is cut in tiers
-  const int wide = (int)min((long long)p.wide, (total + kWarps - 1) / kWarps);
-  const Line line(total, wide, total >= (long long)wide * kTierChunks ? p.tiers : 1);
+  // A part has a chunk for each warp where the units allow it.  A line that does not fill the GPU, or
+  // is one sequence's, is cut so that the parts of units of one length end with them: a part that goes
+  // on into another unit costs its CTA another start.
+  const long long units = (long long)p.B * per_b;
+  int parts = (int)min((long long)p.most_parts, max(units, (total - kPad * units + kWarps - 1) / kWarps));
+  if (parts < p.most_parts || p.B == 1) {
+    const long long up = (parts + units - 1) / units * units;
+    parts = up <= p.most_parts ? (int)up : parts >= units ? parts - (int)(parts % units) : parts;
+  }
+  const Line line{total, parts};
   const int w0 = blockIdx.x;
-  if (w0 >= line.parts()) return;
+  if (w0 >= parts) return;
   const long long begin = line.start(w0), stop = line.start(w0 + 1);
   if (begin >= stop) return;
   // the part of a unit that begins at `at`, in batch row b or behind it
@@ -113,12 +131,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     s.slot = rows[b].x, s.len = rows[b].y;
     s.chunks = max(1, (s.len + kChunk - 1) / kChunk);
     const long long in = at - pre[b];
-    const int in_b = in <= 0xffffffffll ? (int)((uint32_t)in / (uint32_t)s.chunks) : (int)(in / s.chunks);
+    const int size = kPad + s.chunks;
+    const int in_b = in <= 0xffffffffll ? (int)((uint32_t)in / (uint32_t)size) : (int)(in / size);
     s.tile = in_b / c.Hkv;
     s.hk = in_b % c.Hkv;
-    s.unit_at = pre[b] + (long long)in_b * s.chunks;
-    s.c0 = (int)(at - s.unit_at);
-    s.c1 = (int)min((long long)s.chunks, stop - s.unit_at);
+    s.unit_at = pre[b] + (long long)in_b * size + kPad;
+    s.next = min(s.unit_at + s.chunks, stop);
+    s.c0 = (int)max(0ll, at - s.unit_at);
+    s.c1 = (int)max(0ll, s.next - s.unit_at);
     return s;
   };
   // chunk k of this warp in a part is c0 + warp + kWarps k
@@ -126,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 
   // ---- copies.  They run ahead of the products, across parts, in windows of up to 32 chunks: a
   // lane looks after one chunk, its page a window ahead.
-  uint8_t* my_ring = ring + warp * Ring<D>::kWarpBytes;
+  uint8_t* my_ring = ring + warp * Ring<D, RT>::kWarpBytes;
   const int page_shift = 31 - __clz(c.page);
   const bool halves = c.page < kChunk;  // a chunk is two pages of 16 tokens
   int b = row_at(pre, p.B, begin);
@@ -147,12 +167,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     if (++nw * 32 >= nn) {
       nw = 0;
       do {
-        const long long at = ns.unit_at + ns.c1;
-        if (at >= stop) {
+        if (ns.next >= stop) {
           have_next = false;
           return;
         }
-        ns = seg_at(at, ns.b);
+        ns = seg_at(ns.next, ns.b);
         nn = chunks_of(ns);
       } while (nn == 0);
     }
@@ -185,8 +204,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     const int half = halves ? __shfl_sync(0xffffffffu, w_half, at_i) : -1;
     uint64_t* bar = &bars[warp][place];
     if (lane == 0) {
-      uint8_t* dst = my_ring + place * Ring<D>::kBytes;
-      const uint32_t box = Ring<D>::kBytes >> (halves ? 1 : 0);
+      uint8_t* dst = my_ring + place * Ring<D, RT>::kBytes;
+      const uint32_t box = Ring<D, RT>::kBytes >> (halves ? 1 : 0);
       const uint32_t bytes = (page >= 0 ? box : 0) + (half >= 0 ? box : 0);
       if (bytes)
         mbar_arrive_expect_tx(bar, bytes);
@@ -218,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       for (int h = 0; h < kSub; ++h) meta[warp][place][h] = w_meta[h];
     }
     ++at_i, --left, ++flight;
-    place = place + 1 == kStages ? 0 : place + 1;
+    place = place + 1 == kPlaces ? 0 : place + 1;
   };
   // where a lane reads in a 128-byte (D = 64: 64-byte) swizzled box.  MMA row g stands for token
   // tk = g, odd g for g ^ 4: the eight lanes of a load then meet in no bank.  K token tk, unit tig (and
@@ -229,17 +248,36 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const uint32_t at_v1 = D == 128 ? tv * 128 + ((g ^ tv) << 4) : tv * 64 + (((g >> 1) ^ (tv >> 1)) << 4) + (g & 1) * 8;
   if (nn) load_window();
   else next_window();
-#pragma unroll 1
-  for (int k = 0; k < kStages - 1; ++k) issue();
 
   uint32_t phase = 0;
   int here = 0;                    // ring place of the next products
-  for (long long at = begin; at < stop;) {
-    const FewSeg u = seg_at(at, b);
+  // Q of a part's rows, a part ahead
+  auto fetch_q = [&](const FewSeg& u, int to) {
+    const int q_len = row_queries(p, u.b);
+    for (int x = tid; x < R * (D / 8); x += kThreads) {
+      const int r = x / (D / 8), row = u.tile * R + r, i = row / p.G;
+      const bool live = i < q_len;
+      const __nv_bfloat16* q =
+          p.Q + (((size_t)u.b * p.H + (size_t)u.hk * p.G + row % p.G) * p.Nq + (live ? i : 0)) * D + x % (D / 8) * 8;
+      cp_async16_or_zero(smem_u32(&q_buf[to][0]) + x * 16, q, live);
+    }
+    cp_commit();
+  };
+  FewSeg u = seg_at(begin, b);
+  fetch_q(u, 0);
+#pragma unroll 1
+  for (int k = 0; k < kPlaces - 1; ++k) issue();
+  cp_wait<0>();
+  __syncthreads();
+  for (int q_at = 0;; q_at ^= 1) {
     b = u.b;
-    at = u.unit_at + u.c1;
     const int q_len = row_queries(p, b);
-    if (u.c0 == 0 && tid == 0)  // the parts that hold the unit's first and last chunk
+    FewSeg after = u;
+    if (u.next < stop) {
+      after = seg_at(u.next, b);
+      fetch_q(after, q_at ^ 1);
+    }
+    if (u.c0 == 0 && u.c1 > 0 && tid == 0)  // the parts that hold the unit's first and last chunk
       p.info[(long long)b * per_b + u.tile * c.Hkv + u.hk] = make_int2(w0, line.holder(u.unit_at + u.chunks - 1));
 
     // rows of this lane as B columns (row g of each 8-row tile) and as accumulator columns
@@ -250,15 +288,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int t = 0; t < RT; ++t) {
       const int row = u.tile * R + t * 8 + g, i = row / p.G;
       const bool live = i < q_len;
-      const __nv_bfloat16* q =
-          p.Q + (((size_t)b * p.H + (size_t)u.hk * p.G + row % p.G) * p.Nq + (live ? i : 0)) * D;
       float x[NK][4];
       float top = 0.f;
 #pragma unroll
       for (int s = 0; s < NK; ++s) {
         // channels of k-step s: 64 (s / 4) + 16 tig + 4 (s % 4) + 0..3
-        uint2 w = make_uint2(0u, 0u);
-        if (live) w = *reinterpret_cast<const uint2*>(q + (s >> 2) * 64 + tig * 16 + (s & 3) * 4);
+        const uint2 w = *reinterpret_cast<const uint2*>(&q_buf[q_at][(t * 8 + g) * D + (s >> 2) * 64 + tig * 16 + (s & 3) * 4]);
         x[s][0] = __uint_as_float(w.x << 16), x[s][1] = __uint_as_float(w.x & 0xffff0000u);
         x[s][2] = __uint_as_float(w.y << 16), x[s][3] = __uint_as_float(w.y & 0xffff0000u);
 #pragma unroll
@@ -304,11 +339,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (!__all_sync(0xffffffffu, mbar_wait(&bars[warp][here], phase, &abort))) break;
       __syncwarp();  // (meta)
       --flight;
-      const uint8_t* src = my_ring + here * Ring<D>::kBytes;
+      const uint8_t* src = my_ring + here * Ring<D, RT>::kBytes;
       float4 sc[kSub];
 #pragma unroll
       for (int h = 0; h < kSub; ++h) sc[h] = meta[warp][here][h];
-      if (++here == kStages) here = 0, phase ^= 1;
+      if (++here == kPlaces) here = 0, phase ^= 1;
       // S^T
       float s[kSub][RT][4];
 #pragma unroll
@@ -432,10 +467,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     // ---- the warps' results of this part, through the ring place that each warp has just left (the
     // copies into the others go on).  16-byte unit x of row r lies at x ^ (r / 2 % 4), against bank
     // conflicts.
-    const bool whole = u.c0 == 0 && u.c1 == u.chunks;
+    const bool whole = u.c0 == 0 && u.c1 == u.chunks, any = u.c1 > u.c0;
     float* part = p.part + (size_t)(2 * w0 + (u.c0 == 0 ? 1 : 0)) * R * (D + 2);
-    const int left_at = here == 0 ? kStages - 1 : here - 1;
-    float4* mine = reinterpret_cast<float4*>(my_ring + left_at * Ring<D>::kBytes);
+    const int left_at = here == 0 ? kPlaces - 1 : here - 1;
+    float4* mine = reinterpret_cast<float4*>(my_ring + left_at * Ring<D, RT>::kBytes);
     if (lane == 0) left_place[warp] = left_at;
 #pragma unroll
     for (int t = 0; t < RT; ++t)
@@ -456,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     for (int x = tid; x < R * (D / 4); x += kThreads) {
       const int r = x / (D / 4), d = x % (D / 4);
       const int rw = u.tile * R + r, i = rw / p.G;
-      if (i >= q_len) continue;
+      if (!any || i >= q_len) continue;
       float mt = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, xm[w][r]);
@@ -466,8 +501,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       for (int w = 0; w < kWarps; ++w) {
         const float f = ex2(xm[w][r] - sub);
         ls = fmaf(f, xl[w][r], ls);
-        const float4 y = reinterpret_cast<const float4*>(ring + w * Ring<D>::kWarpBytes +
-                                                         left_place[w] * Ring<D>::kBytes)[r * (D / 4) + (d ^ (r >> 1 & 3))];
+        const float4 y = reinterpret_cast<const float4*>(ring + w * Ring<D, RT>::kWarpBytes +
+                                                         left_place[w] * Ring<D, RT>::kBytes)[r * (D / 4) + (d ^ (r >> 1 & 3))];
         o[0] = fmaf(f, y.x, o[0]), o[1] = fmaf(f, y.y, o[1]), o[2] = fmaf(f, y.z, o[2]), o[3] = fmaf(f, y.w, o[3]);
       }
 #pragma unroll
@@ -487,14 +522,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
     }
     fence_proxy_async_smem();  // the places are read before they are filled again
-    if (__syncthreads_or(abort)) break;
+    cp_wait<0>();
+    if (__syncthreads_or(abort) || u.next >= stop || after.c1 == 0) break;
+    u = after;
   }
   if (abort) {  // a wait ran out: the copies that are still in flight
     if (tid == 0) atomicMax(c.status, (int)kDevTimeout);
     for (; flight > 0; --flight) {
       int give_up = 0;
       mbar_wait(&bars[warp][here], phase, &give_up);
-      if (++here == kStages) here = 0, phase ^= 1;
+      if (++here == kPlaces) here = 0, phase ^= 1;
     }
   }
 }
@@ -579,13 +616,13 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R)
   if (d == 0) p.LSE[orow] = ls > 0.f ? (mt + log2f(ls)) * 0.69314718055994531f : -INFINITY;
 }
 
-// The cut: as many CTAs as run at once, kTiers times over if the line can be that long.
-void few_cut(AttnParams& p, int ctas) {
-  const long long most = (long long)p.B * p.c.Hkv * p.tiles * (((long long)p.c.max_pages * p.c.page + kChunk - 1) / kChunk);
-  const long long need = (most + kWarps - 1) / kWarps;
-  p.wide = ctas < kMaxParts / kTiers ? ctas : kMaxParts / kTiers;
-  if (need < p.wide) p.wide = (int)need;
-  p.tiers = most >= (long long)p.wide * kTierChunks ? kTiers : 1;
+// As many CTAs as run at once, fewer where the line cannot be long enough for them.
+void few_grid(AttnParams& p, int ctas) {
+  const long long units = (long long)p.B * p.c.Hkv * p.tiles;
+  const long long chunks = units * (((long long)p.c.max_pages * p.c.page + kChunk - 1) / kChunk);
+  const long long need = (chunks + kWarps - 1) / kWarps > units ? (chunks + kWarps - 1) / kWarps : units;
+  p.most_parts = ctas < kMaxParts ? ctas : kMaxParts;
+  if (need < p.most_parts) p.most_parts = (int)need;
 }
 
 template <int D, int KIND, int RT>
@@ -600,9 +637,9 @@ int launch_few(const AttnParams& p, cudaStream_t st) {
       !make_tmap_3d(&tv, p.c.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, (uint64_t)p.c.Hkv * p.c.page, p.c.n_pages, D,
                     box, swizzle))
     return 3;
-  const size_t smem = 1024 + (size_t)kWarps * Ring<D>::kWarpBytes + ((size_t)p.B + 1) * 16;
+  const size_t smem = 1024 + (size_t)kWarps * Ring<D, RT>::kWarpBytes + ((size_t)p.B + 1) * 16;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 3;
-  return launch_pdl(kern, dim3(p.wide * p.tiers), dim3(kThreads), smem, st, p, tk, tv) == cudaSuccess ? 0 : 3;
+  return launch_pdl(kern, dim3(p.most_parts), dim3(kThreads), smem, st, p, tk, tv) == cudaSuccess ? 0 : 3;
 }
 template <int D, int KIND>
 int launch_few(const AttnParams& p, int rows, cudaStream_t st) {
@@ -616,7 +653,7 @@ constexpr long long kFewRows = 32;
 }  // namespace
 
 int launch_kv_few(AttnParams p, int kind, int rows, int sms, cudaStream_t st) {
-  few_cut(p, sms * kCtasPerSm);
+  few_grid(p, sms * (rows == 8 ? kCtasPerSm<1> : kCtasPerSm<2>));
   if (p.c.D == 128)
     return kind == SAGE_KV_INT8 ? launch_few<128, SAGE_KV_INT8>(p, rows, st)
                                 : launch_few<128, SAGE_KV_E4M3>(p, rows, st);
@@ -663,10 +700,12 @@ int launch_kv_attention(const sage_kv_cache& c, const void* Q, const int* slots,
   ScopedTimer timer("kv_attention", st);
   const bool many = L.rows == kChunkRows;
   if (int rc = many ? launch_kv_chunk(p, c.kind, sms, st) : launch_kv_few(p, c.kind, L.rows, sms, st)) return rc;
+  const long long rows = (long long)p.G * Nq;
+  const unsigned unit_rows = (unsigned)(rows < L.rows ? rows : L.rows);
   const unsigned units = (unsigned)((long long)B * c.Hkv * L.tiles);
   auto join = many ? (c.D == 128 ? kv_join_kernel<128, 1> : kv_join_kernel<64, 1>)
                    : (c.D == 128 ? kv_join_kernel<128, 4> : kv_join_kernel<64, 4>);
-  if (launch_pdl(join, dim3(units, many ? L.rows / 4 : L.rows), dim3(128), 0, st, p, L.rows) != cudaSuccess) return 3;
+  if (launch_pdl(join, dim3(units, many ? L.rows / 4 : unit_rows), dim3(128), 0, st, p, L.rows) != cudaSuccess) return 3;
   return cudaGetLastError() == cudaSuccess ? 0 : 3;
 }
 

@@ -19,7 +19,7 @@ struct AttnParams {
   int2* info;      // first and last worker of each unit
   float* part;     // two partial results of each worker: [R][D] sums, then [R] maxima and [R] row sums
   int B, H, G, Nq, tiles, causal;
-  int wide, tiers; // the cut of the line (see Line): CTAs that run at once, tiers at most
+  int most_parts;  // CTAs of the grid: the parts of the line at most
   float alpha;     // sm_scale log2 e
 };
 
@@ -159,32 +159,20 @@ __device__ __forceinline__ int row_at(const long long* pre, int B, long long at)
   return lo;
 }
 
-// The line of work, `total` chunks, cut into parts for the CTAs of a grid in order.  The first `wide` CTAs
-// (those that run at once) take kTier[1] of 64 shares of it in equal parts, the next `wide` CTAs the
-// shares up to kTier[2], and so on: CTAs of one SM do not progress alike (a third of a uniform cut's
-// time passed with the slower ones alone), and the smaller parts, which start as others end, even
-// that out.  Boundaries do not depend on who runs when.  A short line has one tier.
+// a b / c; the 32-bit division where it serves (a 64-bit one costs a microsecond of a part's start)
+__device__ __forceinline__ long long mul_div(long long a, int b, long long c) {
+  const unsigned long long x = (unsigned long long)a * (unsigned)b;
+  return (x | (unsigned long long)c) >> 32 ? (long long)(x / (unsigned long long)c) : (long long)((uint32_t)x / (uint32_t)c);
+}
+// The line of work, `total` places, cut into equal parts for the CTAs of a grid in order.
 struct Line {
   long long total;
-  int wide, tiers;
-  __device__ Line(long long total, int wide, int tiers) : total(total), wide(wide), tiers(tiers) {}
-  __device__ long long tier_at(int t) const {
-    constexpr int kTier[4] = {0, 46, 56, 61};
-    return t >= tiers ? total : t == 0 ? 0 : total * (t == 1 ? kTier[1] : t == 2 ? kTier[2] : kTier[3]) / 64;
-  }
-  __device__ int parts() const { return wide * tiers; }
+  int parts;
   // where part v begins
-  __device__ long long start(int v) const {
-    const int t = v / wide;
-    const long long a = tier_at(t);
-    return a + (tier_at(t + 1) - a) * (v - t * wide) / wide;
-  }
+  __device__ long long start(int v) const { return mul_div(total, v, parts); }
   // the part that holds place x
   __device__ int holder(long long x) const {
-    int t = 0;
-    while (t + 1 < tiers && x >= tier_at(t + 1)) ++t;
-    const long long a = tier_at(t), n = tier_at(t + 1) - a;
-    int v = t * wide + (int)((x - a) * wide / n);
+    int v = (int)mul_div(x, parts, total);
     while (start(v + 1) <= x) ++v;
     while (start(v) > x) --v;
     return v;
@@ -192,7 +180,7 @@ struct Line {
 };
 
 // the most parts
-constexpr int kMaxParts = 2048;        // few query rows
+constexpr int kMaxParts = 512;         // few query rows
 constexpr int kMaxChunkParts = 160;    // many (one CTA an SM)
 constexpr int kChunkRows = 256;        // query rows of a unit, many
 

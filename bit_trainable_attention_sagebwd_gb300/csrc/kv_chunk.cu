@@ -152,9 +152,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
   const long long total = sm.pre[kGroups];
-  const Line line(total, (int)min((long long)gridDim.x, max(total, 1ll)), 1);
+  const Line line{total, (int)min((long long)gridDim.x, max(total, 1ll))};
   const int w0 = blockIdx.x;
-  const bool idle = total == 0 || w0 >= line.parts();
+  const bool idle = total == 0 || w0 >= line.parts;
   const long long begin = idle ? 0 : line.start(w0), stop = idle ? 0 : line.start(w0 + 1);
   const int per_page = p.c.page >> 4;  // 16-key groups of a page
   const int page_shift = 31 - __clz(per_page);

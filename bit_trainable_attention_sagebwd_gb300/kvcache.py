@@ -15,24 +15,18 @@ from __future__ import annotations
 
 import ctypes
 
-from . import SAGE_ERR_UNSUPPORTED, SageError, _check, lib, sage_kv_cache
+from . import SAGE_ERR_UNSUPPORTED, SageError, lib, sage_kv_cache
 
 _KINDS = {"int8": 0, "e4m3": 1}
 
 
-def _dev(cuda_index):
-    """Context that makes a tensor's device the current one, where it is not."""
-    import torch
-    return torch.cuda.device(cuda_index)
-
-
 def _arg(t, name, dtype, shape, device):
     """The address of a tensor argument after its checks."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the cache is on {device}")
-    if not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError(f"{name}: on {t.device}, the cache is on {device}")
         raise ValueError(f"{name}: not contiguous")
     return t.data_ptr()
 
@@ -66,7 +60,7 @@ class KVCache:
                                self.n_pages, self.hkv, self.page, self.d, self.n_slots, self.max_pages,
                                _KINDS[self.kind])
         self._ref = ctypes.byref(self.c)
-        self._slots_shape = (self.n_slots,)
+        self._slots_shape, self._i32, self._lib = (self.n_slots,), i32, lib()
 
 
 def kv_cache(n_pages, hkv, d, n_slots, max_pages, page=64, kind="int8", device="cuda") -> KVCache:
@@ -89,30 +83,30 @@ def _call(fn, cache, stream, *args):
     """fn(*args, stream) with the cache's device current and, unless a stream is given, on that
     device's current stream."""
     import torch
-    f = getattr(lib(), fn)
     index = cache.device.index
-    if torch.cuda.current_device() == index:
-        s = stream if stream is not None else torch.cuda.current_stream()
-        _check(fn, f(*args, s.cuda_stream))
+    if torch._C._cuda_getDevice() == index:
+        # (the raw handle: torch.cuda.current_stream() alone costs more than a launch)
+        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+        rc = getattr(cache._lib, fn)(*args, s)
     else:
-        with _dev(index):
-            s = stream if stream is not None else torch.cuda.current_stream()
-            _check(fn, f(*args, s.cuda_stream))
+        with torch.cuda.device(index):
+            s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+            rc = getattr(cache._lib, fn)(*args, s)
+    if rc:
+        raise SageError(fn, rc)
 
 
 def _slot_array(t, name, cache):
-    import torch
-    return _arg(t, name, torch.int32, cache._slots_shape, cache.device)
+    return _arg(t, name, cache._i32, cache._slots_shape, cache.device)
 
 
 def _rows(slots, b, cache):
     """The address of a slots argument (None: batch row b is slot b)."""
-    import torch
     if slots is None:
         if b > cache.n_slots:
             raise ValueError(f"{b} batch rows without slots, the cache has {cache.n_slots}")
         return None
-    return _arg(slots, "slots", torch.int32, (b,), cache.device)
+    return _arg(slots, "slots", cache._i32, (b,), cache.device)
 
 
 def kv_append(cache, k, v, pos, n_new, slots=None, k_shift=None, stream=None):
@@ -159,7 +153,7 @@ def kv_attention(q, cache, causal=True, slots=None, q_len=None, sm_scale=None, o
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
     shape = (B, H, Nq, cache.d)
     _call("sage_attn_kv_attention", cache, stream, cache._ref, _arg(q, "q", torch.bfloat16, shape, dev),
-          _rows(slots, B, cache), None if q_len is None else _arg(q_len, "q_len", torch.int32, (B,), dev),
+          _rows(slots, B, cache), None if q_len is None else _arg(q_len, "q_len", cache._i32, (B,), dev),
           _arg(o, "o", torch.bfloat16, shape, dev), _arg(lse, "lse", torch.float32, (B, H, Nq), dev), ws.data_ptr(),
           ws.nbytes, B, H, Nq, int(causal), 0.0 if sm_scale is None else float(sm_scale))
     return o, lse
