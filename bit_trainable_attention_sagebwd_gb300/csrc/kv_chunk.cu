@@ -5,26 +5,29 @@
 // 2 D bytes for every key that 256 rows share.  One CTA an SM takes units of 256 rows (two tiles of
 // 128: the queries of the G heads of a key/value head, token by token) and walks the unit's
 // 128-key tiles:
-//  - warps 8-11 fetch the codes one tile ahead (cp.async, 16 bytes a thread into a place that only
-//    that thread reads), turn them into fp16 (exact) and store them where tcgen05.mma reads them
-//    (128-byte swizzle), two K and two V tiles deep;
+//  - warps 8-11 (K) and 12-15 (V) have the codes brought by TMA a tile ahead, turn them into fp16
+//    (exact) and store them where tcgen05.mma reads them (128-byte swizzle), two tiles deep;
 //  - one thread issues S = Q K^T and O += P V (kind::f16, fp32 accumulators in TMEM) for the two row
 //    tiles in turn, so the tensor core works on one tile while the softmax works on the other;
-//  - warps 0-3 and 4-7 own a row tile each, a thread a row: S from TMEM, P back into TMEM over S's
-//    columns, from where the second product takes it.
+//  - warps 0-3 and 4-7 own a row tile each, a thread a row: S from TMEM twice (maximum, then
+//    exponentials: a row of S does not stay in registers), P back into TMEM over S's columns, from
+//    where the second product takes it.
 // Units are cut over the grid like those of the few-row kernel (kv_attn.cu), in 128-key tiles.
+#include <type_traits>
+
 #include "kv_attn.cuh"
 #include "launch.h"
+#include "tmap.h"
 
 namespace sage {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kTile = 128;                   // keys of a tile, rows of a row tile
 constexpr int kGroups = 128;                 // the batch rows in at most so many groups
-constexpr int kRegsSoftmax = 192, kRegsLoad = 72, kRegsIssue = 56;
-static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsIssue <= 4 * 128, "the launch's registers");
+constexpr int kRegsSoftmax = 152, kRegsLoad = 64, kRegsIssue = 48;
+static_assert(2 * kRegsSoftmax + 2 * kRegsLoad + kRegsIssue <= 5 * 96, "the launch's registers");
 constexpr uint32_t kCols = 512, kColO = 256; // TMEM: S of row tile t at 128 t, O at 256 + 128 t
 
 template <int D>
@@ -32,13 +35,15 @@ struct ChunkSmem {
   uint8_t q[2][kTile * D * 2];
   uint8_t k[2][kTile * D * 2];
   uint8_t v[2][kTile * D * 2];
-  uint8_t raw[2][kTile * D];  // codes of a K and a V tile on their way; a loader reads what it copied
-  uint64_t bar_q[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_s[2], bar_p[2], bar_o[2];
+  uint8_t raw[2][kTile * D];  // codes of a K and a V tile
+  uint64_t bar_q[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_raw[2], bar_s[2], bar_p[2], bar_o[2];
   long long wsum[kThreads / 32];
   long long pre[kGroups + 1];  // tiles before each group of batch rows
   uint32_t tmem_base;
   int abort;
+  int seg[2];                  // for the MMA issuer: 2 x tiles of a part + (it has two row tiles), 0: no more
 };
+static_assert(sizeof(ChunkSmem<128>) + 1024 <= 227 * 1024, "shared memory of a CTA");
 
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -51,6 +56,16 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, 
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// barrier of the 128 threads of a loader group
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // A part of a unit: key tiles [c0, c1) of row tile pair rt of (batch row b, key/value head hk).
 struct Seg {
@@ -71,6 +86,7 @@ __device__ __forceinline__ long long row_chunks(const AttnParams& p, int b) {
   int slot;
   const int len = row_length(p, b, slot), q_len = row_queries(p, b);
   long long n = 0;
+#pragma unroll 1
   for (int rt = 0; rt < p.tiles; ++rt) n += pair_chunks(p, len, q_len, rt);
   return n * p.c.Hkv;
 }
@@ -87,6 +103,7 @@ struct Walk {
   }
   __device__ bool more() const { return at < stop; }
   __device__ Seg next(const AttnParams& p) {
+#pragma unroll 1
     for (long long n; at >= base + (n = row_chunks(p, b)); ++b) base += n;
     Seg s;
     s.b = b;
@@ -94,13 +111,14 @@ struct Walk {
     s.q_len = row_queries(p, b);
     long long unit = base;
     int n = 0, rt = 0;
+#pragma unroll 1
     for (;; ++rt) {
       n = pair_chunks(p, s.len, s.q_len, rt);
       if (at < unit + (long long)n * p.c.Hkv) break;
       unit += (long long)n * p.c.Hkv;
     }
     s.rt = rt;
-    s.hk = (int)((at - unit) / n);
+    s.hk = (int)mul_div(at - unit, 1, n);
     s.chunks = n;
     s.unit_at = unit + (long long)s.hk * n;
     s.c0 = (int)(at - s.unit_at);
@@ -112,7 +130,8 @@ struct Walk {
 };
 
 template <int D, int KIND>
-__global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k,
+                                                                const __grid_constant__ CUtensorMap tm_v) {
   constexpr int kAtoms = D / 64;       // 128-byte columns of a tile row
   constexpr int kAtom = kTile * 128;   // bytes of one
   extern __shared__ uint8_t smem_raw[];
@@ -125,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       mbar_init(&sm.bar_k_empty[s], 1);
       mbar_init(&sm.bar_v_full[s], 128);
       mbar_init(&sm.bar_v_empty[s], 1);
+      mbar_init(&sm.bar_raw[s], 1);
       mbar_init(&sm.bar_s[s], 1);
       mbar_init(&sm.bar_p[s], 128);
       mbar_init(&sm.bar_o[s], 1);
@@ -133,13 +153,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
     fence_mbar_init();
   }
   pdl_wait();
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(&sm.tmem_base, kCols);
     tmem_relinquish();
   }
   const int group = (p.B + kGroups - 1) / kGroups;
   prefix_of<kThreads>(kGroups, sm.pre, sm.wsum, [&](int g) {
     long long n = 0;
+#pragma unroll 1
     for (int b = g * group; b < min(p.B, (g + 1) * group); ++b) n += row_chunks(p, b);
     return n;
   });
@@ -167,9 +188,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
     return -1;
   };
 
-  if (warp >= 12) {
+  if (warp >= 16) {
     regs_decrease<kRegsIssue>();
-    if (warp == 12 && lane == 0 && begin < stop) {
+    if (warp == 16 && lane == 0 && begin < stop) {
       // ---------------- MMA issuer
       constexpr uint32_t id_s = idesc_f16(kTile, kTile, false), id_o = idesc_f16(kTile, D, true);
       uint32_t kc = 0, ns[2] = {0, 0}, np[2] = {0, 0};  // key tiles, segments and P tiles so far
@@ -189,16 +210,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
                       acc | (kk > 0));
       };
       bool ok = true;
-      Walk walk(sm.pre, group, begin, stop);
-      while (ok && walk.more()) {
-        const Seg s = walk.next(p);
-        const int n = s.c1 - s.c0;
-        ok = mbar_wait(&sm.bar_q[0], ns[0] & 1, abort) && (!s.two || mbar_wait(&sm.bar_q[1], ns[1] & 1, abort)) &&
-             mbar_wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1, abort);
+      while (ok) {
+        // a part: its tiles and whether the second row tile has rows, said with the first one's Q
+        if (!mbar_wait(&sm.bar_q[0], ns[0] & 1, abort)) break;
+        const int said = *const_cast<volatile int*>(&sm.seg[ns[0] & 1]), n = said >> 1;
+        const bool two = said & 1;
+        if (n == 0) break;
+        ok = (!two || mbar_wait(&sm.bar_q[1], ns[1] & 1, abort)) && mbar_wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1, abort);
         if (!ok) break;
         tc_fence_after();
         issue_s(0, kc);
-        if (s.two) issue_s(1, kc);
+        if (two) issue_s(1, kc);
         umma_commit(&sm.bar_k_empty[kc & 1]);
         for (int j = 0; j < n; ++j, ++kc) {
           const bool more = j + 1 < n;
@@ -214,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
             tc_fence_after();
             issue_s(0, kc + 1);
           }
-          if (s.two) {
+          if (two) {
             ok = mbar_wait(&sm.bar_p[1], np[1] & 1, abort);
             if (!ok) break;
             ++np[1];
@@ -224,100 +246,104 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
           }
           umma_commit(&sm.bar_v_empty[kc & 1]);
           if (more) {
-            if (s.two) issue_s(1, kc + 1);
+            if (two) issue_s(1, kc + 1);
             umma_commit(&sm.bar_k_empty[(kc + 1) & 1]);
           }
         }
         ++ns[0];
-        if (s.two) ++ns[1];
+        if (two) ++ns[1];
       }
     }
   } else if (warp >= 8) {
     regs_decrease<kRegsLoad>();
-    // ---------------- loaders: thread `lt` takes 16 bytes of kRows rows of a tile
+    // ---------------- loaders: thread `lt` takes 16 bytes of kRows rows of a K or V tile
     constexpr int kPerRow = D / 16, kRowStep = 128 / kPerRow, kRows = kTile / kRowStep;
-    const int lt = tid - 256, r0 = lt / kPerRow, piece = lt % kPerRow;
-    const size_t page_bytes = (size_t)p.c.page * D;
+    const int v = (warp >> 2) - 2, lt = tid & 127, r0 = lt / kPerRow, piece = lt % kPerRow;
+    const bool first = (warp & 3) == 0;  // the warp that has the codes brought: a lane for each page
+    const int boxes = kTile / p.c.page, box_bytes = p.c.page * D;
+    const CUtensorMap* tm = v ? &tm_v : &tm_k;
     Walk walk(sm.pre, group, begin, stop);
     Seg s{};
-    int c = 0;  // the tile that is fetched next; its eight 16-key groups' pages are in lanes 0-7
-    int ids = -1, ids_n = -1;
+    int c = 0, id = -1, id_next = -1;  // the tile that is brought next, the lane's page in it and in the one after
     bool more = walk.more();
-    auto ids_of = [&](int tile) { return lane < 8 ? page_of(s.slot, s.len, tile * 8 + lane) : -1; };
-    // the codes of tile c (zeros where there is no key), 16 bytes at a time
-    auto fetch = [&](int v) {
-      if (more) {
-        const uint8_t* pool = static_cast<const uint8_t*>(v ? p.c.v : p.c.k);
-        const uint32_t dst = smem_u32(sm.raw[v]) + lt * 16;
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int r = r0 + i * kRowStep, grp = r >> 4;
-          const int id = __shfl_sync(0xffffffffu, ids, grp);
-          const int in_page = ((c * 8 + grp) & (per_page - 1)) * 16 + (r & 15);
-          const uint8_t* src = pool + ((size_t)max(id, 0) * p.c.Hkv + s.hk) * page_bytes + (size_t)in_page * D + piece * 16;
-          cp_async16_or_zero(dst + i * 128 * 16, src, id >= 0);
-        }
-      }
-      cp_commit();
+    auto id_of = [&](int tile) {
+      const int token = tile * kTile + lane * p.c.page;
+      return lane < boxes && token < s.len ? p.c.table[(size_t)s.slot * p.c.max_pages + token / p.c.page] : -1;
     };
-    // the tile after tile c
-    auto advance = [&]() {
+    // tile c's codes (what lies behind the keys stays as it was: finite, and masked)
+    auto bring = [&]() {
+      const bool ok = (unsigned)id < (unsigned)p.c.n_pages;
+      if (!ok && id != -1) atomicMax(p.c.status, kDevIndex);
+      const uint32_t all = __ballot_sync(0xffffffffu, ok);
+      if (lane == 0) {
+        if (all)
+          mbar_arrive_expect_tx(&sm.bar_raw[v], __popc(all) * box_bytes);
+        else
+          mbar_arrive(&sm.bar_raw[v]);
+      }
+      __syncwarp();
+      if (ok) tma_load_3d(sm.raw[v] + lane * box_bytes, tm, 0, s.hk * p.c.page, id, &sm.bar_raw[v]);
+    };
+    auto advance = [&]() {  // to the tile after tile c
       if (++c < s.c1) {
-        ids = ids_n;
+        id = id_next;
       } else {
         more = walk.more();
         if (!more) return;
         s = walk.next(p);
         c = s.c0;
-        ids = ids_of(c);
+        id = id_of(c);
       }
-      ids_n = c + 1 < s.c1 ? ids_of(c + 1) : -1;
+      id_next = c + 1 < s.c1 ? id_of(c + 1) : -1;
     };
-    // 16 codes of a row -> two 16-byte chunks of the swizzled tile; lanes whose chunks would meet
-    // in the same banks store them in the other order
-    auto store = [&](uint8_t* tile, const uint8_t* raw) {
+    if (first && more) {
+      s = walk.next(p);
+      c = s.c0;
+      id = id_of(c);
+      id_next = c + 1 < s.c1 ? id_of(c + 1) : -1;
+      bring();
+      advance();
+    }
+    // (after a wait that ran out every thread still meets the others at the barrier of each tile)
+    bool ok = true, flying = begin < stop;
+    const uint32_t n = (uint32_t)(stop - begin);
+    for (uint32_t kc = 0; kc < n; ++kc) {
+      const uint32_t st = kc & 1;
+      ok = ok && mbar_wait(&sm.bar_raw[v], kc & 1, abort);
+      uint4 x[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) x[i] = *reinterpret_cast<const uint4*>(sm.raw[v] + (i * 128 + lt) * 16);
+      group_sync(1 + v);
+      flying = kc + 1 < n && ok;
+      if (first && flying) {
+        bring();
+        advance();
+      }
+      ok = ok && (kc < 2 || mbar_wait(v ? &sm.bar_v_empty[st] : &sm.bar_k_empty[st], ((kc >> 1) - 1) & 1, abort));
+      if (!ok) continue;
+      // 16 codes of a row -> two 16-byte chunks of the swizzled tile; lanes whose chunks would meet
+      // in the same banks store them in the other order
+      uint8_t* tile = v ? sm.v[st] : sm.k[st];
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(raw + (i * 128 + lt) * 16);
         const int r = r0 + i * kRowStep, u = (piece * 2) & 7;
         uint4 lo, hi;
-        codes_to_half<KIND>(x.x, lo.x, lo.y);
-        codes_to_half<KIND>(x.y, lo.z, lo.w);
-        codes_to_half<KIND>(x.z, hi.x, hi.y);
-        codes_to_half<KIND>(x.w, hi.z, hi.w);
+        codes_to_half<KIND>(x[i].x, lo.x, lo.y);
+        codes_to_half<KIND>(x[i].y, lo.z, lo.w);
+        codes_to_half<KIND>(x[i].z, hi.x, hi.y);
+        codes_to_half<KIND>(x[i].w, hi.z, hi.w);
         uint8_t* row = tile + (piece >> 2) * kAtom + (r >> 3) * 1024 + (r & 7) * 128;
         const bool swap = D == 128 && ((piece >> 2) & 1);
         *reinterpret_cast<uint4*>(row + (((u + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
         *reinterpret_cast<uint4*>(row + (((u + !swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
       }
-    };
-    long long n = stop - begin;
-    if (more) {
-      s = walk.next(p);
-      c = s.c0;
-      ids = ids_of(c);
-      ids_n = c + 1 < s.c1 ? ids_of(c + 1) : -1;
-      fetch(0);
-      fetch(1);
-      advance();
+      fence_proxy_async_smem();
+      mbar_arrive(v ? &sm.bar_v_full[st] : &sm.bar_k_full[st]);
     }
-    for (uint32_t kc = 0; kc < n; ++kc) {
-      const uint32_t st = kc & 1, ph = ((kc >> 1) - 1) & 1;
-      bool ok = true;
-#pragma unroll 1
-      for (int v = 0; ok && v < 2; ++v) {  // K, then V
-        cp_wait<1>();
-        ok = kc < 2 || mbar_wait(v ? &sm.bar_v_empty[st] : &sm.bar_k_empty[st], ph, abort);
-        if (!ok) break;
-        store(v ? sm.v[st] : sm.k[st], sm.raw[v]);
-        fence_proxy_async_smem();
-        mbar_arrive(v ? &sm.bar_v_full[st] : &sm.bar_k_full[st]);
-        fetch(v);
-      }
-      if (!ok) break;
-      advance();
+    if (!ok && flying && first) {  // codes that may still be on their way
+      int give_up = 0;
+      mbar_wait(&sm.bar_raw[v], n & 1, &give_up, 100000000ull);
     }
-    cp_wait<0>();
   } else {
     regs_increase<kRegsSoftmax>();
     // ---------------- softmax: thread r of the group owns row r of row tile t
@@ -370,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         }
       }
       fence_proxy_async_smem();
+      if (tid == 0) sm.seg[n_o & 1] = 2 * (s.c1 - s.c0) + s.two;
       mbar_arrive(&sm.bar_q[t]);
       const int lim = live ? row_end(p, s.len, s.q_len, i) : s.len;
       float m = -INFINITY, l = 0.f, ref = 0.f;
@@ -400,39 +427,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         ok = ok && mbar_wait(&sm.bar_s[t], n_s & 1, abort);
         ++n_s;
         tc_fence_after();
-        uint32_t sv[4][32];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) tmem_ld32(s_col + 32 * x, sv[x]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int x = 0; x < 4; ++x) reg_fence32(sv[x]);
         const bool edge = __any_sync(0xffffffffu, lim < (c + 1) * kTile);
         const int left = lim - c * kTile;
+        // first pass: the row's maximum of u
         float mx = -INFINITY;
-        if (edge) {
-          // u of every key, -inf behind the row's last one; the factors below are then 1 and 0
+        uint32_t sv[2][32];
+        tmem_ld32(s_col, sv[0]);
+        auto maximum = [&](auto edge_tile) {
+          constexpr bool kEdge = decltype(edge_tile)::value;
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const float f = __shfl_sync(0xffffffffu, ks, x) * a_row, g = __shfl_sync(0xffffffffu, lg, x);
+          for (int x = 0; x < 4; ++x) {
+            tmem_wait32(sv[x & 1]);
+            if (x < 3) tmem_ld32(s_col + 32 * (x + 1), sv[(x + 1) & 1]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float u = fmaf(__uint_as_float(sv[x >> 1][(x & 1) * 16 + e]), f, g);
-              const float y = x * 16 + e < left ? u : -INFINITY;
-              sv[x >> 1][(x & 1) * 16 + e] = __float_as_uint(y);
-              mx = fmaxf(mx, y);
+            for (int y = 0; y < 2; ++y) {
+              const float f = __shfl_sync(0xffffffffu, ks, 2 * x + y) * a_row, g = __shfl_sync(0xffffffffu, lg, 2 * x + y);
+              float top = -INFINITY;
+              if (kEdge) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  top = fmaxf(top, x * 32 + y * 16 + e < left ? fmaf(__uint_as_float(sv[x & 1][y * 16 + e]), f, g) : -INFINITY);
+                mx = fmaxf(mx, top);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 16; e += 2)
+                  top = max3(top, __uint_as_float(sv[x & 1][y * 16 + e]), __uint_as_float(sv[x & 1][y * 16 + e + 1]));
+                mx = fmaxf(mx, fmaf(top, f, g));
+              }
             }
           }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            float y = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 16; e += 2)
-              y = max3(y, __uint_as_float(sv[x >> 1][(x & 1) * 16 + e]), __uint_as_float(sv[x >> 1][(x & 1) * 16 + e + 1]));
-            const float f = __shfl_sync(0xffffffffu, ks, x) * a_row;
-            mx = fmaxf(mx, fmaf(y, f, __shfl_sync(0xffffffffu, lg, x)));
-          }
-        }
+        };
+        if (edge)
+          maximum(std::true_type());
+        else
+          maximum(std::false_type());
+        tmem_ld32(s_col, sv[0]);  // (for the second pass)
         const bool raise = mx > m + kRaise;
         if (__any_sync(0xffffffffu, raise)) {
           const float to = raise ? mx - kBelow : m, corr = raise ? ex2(m - to) : 1.f;
@@ -444,6 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
               uint32_t o[32];
               tmem_ld32(o_col + d, o);
               tmem_wait32(o);
+              reg_fence32(sv[0]);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
               tmem_st32(o_col + d, o);
@@ -451,33 +481,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
           }
         }
         const float sub = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+        // second pass: P over the columns that have been read
+        auto exponentials = [&](auto edge_tile) {
+          constexpr bool kEdge = decltype(edge_tile)::value;
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int grp = h * 4 + x;
-            const float f = edge ? 1.f : __shfl_sync(0xffffffffu, ks, grp) * a_row;
-            const float g = (edge ? 0.f : __shfl_sync(0xffffffffu, lg, grp)) - sub;
-            const uint64_t f2v = f2(f, f), g2v = f2(g, g);
-            uint64_t sum = f2(0.f, 0.f);
+            tmem_wait32(sv[x & 1]);
+            if (x < 3) tmem_ld32(s_col + 32 * (x + 1), sv[(x + 1) & 1]);
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              float u0, u1;
-              f2split(ffma2(f2(__uint_as_float(sv[grp >> 1][(grp & 1) * 16 + e]),
-                               __uint_as_float(sv[grp >> 1][(grp & 1) * 16 + e + 1])),
-                            f2v, g2v),
-                      u0, u1);
-              u0 = ex2(u0), u1 = ex2(u1);
-              sum = fadd2(sum, f2(u0, u1));
-              w[x * 8 + (e >> 1)] = h2bits(__floats2half2_rn(u0, u1));
+            for (int y = 0; y < 2; ++y) {
+              const float f = __shfl_sync(0xffffffffu, ks, 2 * x + y) * a_row;
+              const float g = __shfl_sync(0xffffffffu, lg, 2 * x + y) - sub;
+              const uint64_t f2v = f2(f, f), g2v = f2(g, g);
+              uint64_t sum = f2(0.f, 0.f);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                float u0, u1;
+                f2split(
+                    ffma2(f2(__uint_as_float(sv[x & 1][y * 16 + e]), __uint_as_float(sv[x & 1][y * 16 + e + 1])), f2v, g2v),
+                    u0, u1);
+                u0 = ex2(u0), u1 = ex2(u1);
+                if (kEdge) {
+                  if (x * 32 + y * 16 + e >= left) u0 = 0.f;
+                  if (x * 32 + y * 16 + e + 1 >= left) u1 = 0.f;
+                }
+                sum = fadd2(sum, f2(u0, u1));
+                w[y * 8 + (e >> 1)] = h2bits(__floats2half2_rn(u0, u1));
+              }
+              float y0, y1;
+              f2split(sum, y0, y1);
+              l = fmaf(y0 + y1, __shfl_sync(0xffffffffu, iv, 2 * x + y), l);
             }
-            float y0, y1;
-            f2split(sum, y0, y1);
-            l = fmaf(y0 + y1, __shfl_sync(0xffffffffu, iv, grp), l);
+            tmem_st16(s_col + x * 16, w);
           }
-          tmem_st32(s_col + h * 32, w);
-        }
+        };
+        if (edge)
+          exponentials(std::true_type());
+        else
+          exponentials(std::false_type());
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sm.bar_p[t]);
@@ -524,20 +566,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
           part[(size_t)kChunkRows * D + pr] = m, part[(size_t)kChunkRows * D + kChunkRows + pr] = l;
       }
     }
+    if (t == 0) {
+      if (tid == 0) sm.seg[n_o & 1] = 0;
+      mbar_arrive(&sm.bar_q[0]);
+    }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) tmem_dealloc(tmem, kCols);
+  if (warp == 16) tmem_dealloc(tmem, kCols);
   if (tid == 0 && sm.abort) atomicMax(p.c.status, (int)kDevTimeout);
 }
 
 template <int D, int KIND>
 int launch(const AttnParams& p, int sms, cudaStream_t st) {
   auto kern = kv_chunk_kernel<D, KIND>;
+  // a page's rows [head, token]: boxes of a page's tokens of a head
+  CUtensorMap tk, tv;
+  if (!make_tmap_3d(&tk, p.c.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, (uint64_t)p.c.Hkv * p.c.page, p.c.n_pages, D,
+                    p.c.page, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_tmap_3d(&tv, p.c.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, (uint64_t)p.c.Hkv * p.c.page, p.c.n_pages, D,
+                    p.c.page, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return 3;
   const size_t smem = sizeof(ChunkSmem<D>) + 1024;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 3;
   const int grid = sms < kMaxChunkParts ? sms : kMaxChunkParts;
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p) == cudaSuccess ? 0 : 3;
+  return launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p, tk, tv) == cudaSuccess ? 0 : 3;
 }
 
 }  // namespace
