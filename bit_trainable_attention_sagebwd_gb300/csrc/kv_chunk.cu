@@ -5,8 +5,9 @@
 // 2 D bytes for every key that 256 rows share.  One CTA an SM takes units of 256 rows (two tiles of
 // 128: the queries of the G heads of a key/value head, token by token) and walks the unit's
 // 128-key tiles:
-//  - warps 8-11 (K) and 12-15 (V) have the codes brought by TMA a tile ahead, turn them into fp16
-//    (exact) and store them where tcgen05.mma reads them (128-byte swizzle), two tiles deep;
+//  - warps 17 and 18 bring the codes of K and V by TMA, a tile ahead; warps 8-11 (K) and 12-15 (V)
+//    turn them into fp16 (exact) and store them where tcgen05.mma reads them (128-byte swizzle), two
+//    tiles deep;
 //  - one thread issues S = Q K^T and O += P V (kind::f16, fp32 accumulators in TMEM) for the two row
 //    tiles in turn, so the tensor core works on one tile while the softmax works on the other;
 //  - warps 0-3 and 4-7 own a row tile each, a thread a row: S from TMEM twice (maximum, then
@@ -36,7 +37,7 @@ struct ChunkSmem {
   uint8_t k[2][kTile * D * 2];
   uint8_t v[2][kTile * D * 2];
   uint8_t raw[2][kTile * D];  // codes of a K and a V tile
-  uint64_t bar_q[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_raw[2], bar_s[2], bar_p[2], bar_o[2];
+  uint64_t bar_q[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_raw[2], bar_raw_empty[2], bar_s[2], bar_p[2], bar_o[2];
   long long wsum[kThreads / 32];
   long long pre[kGroups + 1];  // tiles before each group of batch rows
   uint32_t tmem_base;
@@ -48,15 +49,22 @@ static_assert(sizeof(ChunkSmem<128>) + 1024 <= 227 * 1024, "shared memory of a C
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// D[tmem] (+)= A[tmem] * B[smem]: A's rows are the lanes, two fp16 along K in a column
-__device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// D[tmem] (+)= A[tmem] * B[smem], four along K in one block: A's rows are the lanes, two fp16 along K
+// in a column, 8 columns an MMA; B's descriptor moves by SB (16-byte units)
+template <int SB>
+__device__ __forceinline__ void umma_f16_ts_x4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n .reg .pred p, q;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n"
+      " setp.ne.b32 p, %4, 0;\n setp.eq.b32 q, %4, %4;\n"
+      " add.s32 a1, %1, 8;\n add.s32 a2, %1, 16;\n add.s32 a3, %1, 24;\n"
+      " add.s64 b1, %2, %5;\n add.s64 b2, %2, %6;\n add.s64 b3, %2, %7;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(SB), "n"(2 * SB), "n"(3 * SB)
       : "memory");
 }
-
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -64,9 +72,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// barrier of the 128 threads of a loader group
-__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-
 // A part of a unit: key tiles [c0, c1) of row tile pair rt of (batch row b, key/value head hk).
 struct Seg {
   int b, slot, hk, rt, len, q_len, c0, c1, chunks;
@@ -145,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       mbar_init(&sm.bar_v_full[s], 128);
       mbar_init(&sm.bar_v_empty[s], 1);
       mbar_init(&sm.bar_raw[s], 1);
+      mbar_init(&sm.bar_raw_empty[s], 128);
       mbar_init(&sm.bar_s[s], 1);
       mbar_init(&sm.bar_p[s], 128);
       mbar_init(&sm.bar_o[s], 1);
@@ -194,20 +200,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       // ---------------- MMA issuer
       constexpr uint32_t id_s = idesc_f16(kTile, kTile, false), id_o = idesc_f16(kTile, D, true);
       uint32_t kc = 0, ns[2] = {0, 0}, np[2] = {0, 0};  // key tiles, segments and P tiles so far
+      // descriptors of the first tile of each kind; the second one lies kTile rows behind
+      constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
+      const uint64_t dq = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), dk = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024);
+      const uint64_t dv = sdesc_sw128(smem_u32(sm.v[0]), kAtom, 1024);
       auto issue_s = [&](int t, uint32_t kv) {
-        const uint32_t a = smem_u32(sm.q[t]), b = smem_u32(sm.k[kv & 1]);
+        const uint64_t a = dq + t * kNext, b = dk + (kv & 1) * kNext;
 #pragma unroll
-        for (int h = 0; h < kAtoms; ++h)
-          umma_bf16_x4<2, 2>(tmem + t * 128, sdesc_sw128(a + h * kAtom, 16, 1024), sdesc_sw128(b + h * kAtom, 16, 1024),
-                             id_s, h > 0);
+        for (int h = 0; h < kAtoms; ++h) umma_bf16_x4<2, 2>(tmem + t * 128, a + h * kAtomStep, b + h * kAtomStep, id_s, h > 0);
         umma_commit(&sm.bar_s[t]);
       };
       auto issue_pv = [&](int t, uint32_t kv, uint32_t acc) {
-        const uint32_t b = smem_u32(sm.v[kv & 1]);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_f16_ts(tmem + kColO + t * 128, tmem + t * 128 + kk * 8, sdesc_sw128(b + kk * 2048, kAtom, 1024), id_o,
-                      acc | (kk > 0));
+        const uint64_t b = dv + (kv & 1) * kNext;
+        const uint32_t d = tmem + kColO + t * 128, a = tmem + t * 128;
+        umma_f16_ts_x4<(2048 >> 4)>(d, a, b, id_o, acc);
+        umma_f16_ts_x4<(2048 >> 4)>(d, a + 32, b + (4 * 2048 >> 4), id_o, 1);
       };
       bool ok = true;
       while (ok) {
@@ -254,73 +261,63 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         if (two) ++ns[1];
       }
     }
+    if ((warp == 17 || warp == 18) && begin < stop) {
+      // ---------------- the codes of K (warp 17) or V (18), a tile at a time: a lane for each page
+      const int v = warp - 17, boxes = kTile / p.c.page, box_bytes = p.c.page * D;
+      const CUtensorMap* tm = v ? &tm_v : &tm_k;
+      Walk walk(sm.pre, group, begin, stop);
+      Seg s = walk.next(p);
+      int c = s.c0;
+      auto page_of = [&](int tile) {
+        const int token = tile * kTile + lane * p.c.page;
+        return lane < boxes && token < s.len ? p.c.table[(size_t)s.slot * p.c.max_pages + token / p.c.page] : -1;
+      };
+      int id = page_of(c), id_next = c + 1 < s.c1 ? page_of(c + 1) : -1;
+      uint32_t kc = 0;
+      for (;; ++kc) {
+        // (what lies behind the keys stays as it was: finite, and masked)
+        const bool ok = (unsigned)id < (unsigned)p.c.n_pages;
+        if (!ok && id != -1) atomicMax(p.c.status, kDevIndex);
+        const uint32_t all = __ballot_sync(0xffffffffu, ok);
+        if (!__all_sync(0xffffffffu, kc == 0 || mbar_wait(&sm.bar_raw_empty[v], (kc - 1) & 1, abort))) break;
+        if (lane == 0) {
+          if (all)
+            mbar_arrive_expect_tx(&sm.bar_raw[v], __popc(all) * box_bytes);
+          else
+            mbar_arrive(&sm.bar_raw[v]);
+        }
+        __syncwarp();
+        if (ok) tma_load_3d(sm.raw[v] + lane * box_bytes, tm, 0, s.hk * p.c.page, id, &sm.bar_raw[v]);
+        if (++c < s.c1) {
+          id = id_next;
+        } else {
+          if (!walk.more()) {
+            ++kc;
+            break;
+          }
+          s = walk.next(p);
+          c = s.c0;
+          id = page_of(c);
+        }
+        id_next = c + 1 < s.c1 ? page_of(c + 1) : -1;
+      }
+      int give_up = 0;  // the last copies (after a wait that ran out nobody else waits for them)
+      mbar_wait(&sm.bar_raw[v], (kc - 1) & 1, &give_up);
+    }
   } else if (warp >= 8) {
     regs_decrease<kRegsLoad>();
     // ---------------- loaders: thread `lt` takes 16 bytes of kRows rows of a K or V tile
     constexpr int kPerRow = D / 16, kRowStep = 128 / kPerRow, kRows = kTile / kRowStep;
     const int v = (warp >> 2) - 2, lt = tid & 127, r0 = lt / kPerRow, piece = lt % kPerRow;
-    const bool first = (warp & 3) == 0;  // the warp that has the codes brought: a lane for each page
-    const int boxes = kTile / p.c.page, box_bytes = p.c.page * D;
-    const CUtensorMap* tm = v ? &tm_v : &tm_k;
-    Walk walk(sm.pre, group, begin, stop);
-    Seg s{};
-    int c = 0, id = -1, id_next = -1;  // the tile that is brought next, the lane's page in it and in the one after
-    bool more = walk.more();
-    auto id_of = [&](int tile) {
-      const int token = tile * kTile + lane * p.c.page;
-      return lane < boxes && token < s.len ? p.c.table[(size_t)s.slot * p.c.max_pages + token / p.c.page] : -1;
-    };
-    // tile c's codes (what lies behind the keys stays as it was: finite, and masked)
-    auto bring = [&]() {
-      const bool ok = (unsigned)id < (unsigned)p.c.n_pages;
-      if (!ok && id != -1) atomicMax(p.c.status, kDevIndex);
-      const uint32_t all = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) {
-        if (all)
-          mbar_arrive_expect_tx(&sm.bar_raw[v], __popc(all) * box_bytes);
-        else
-          mbar_arrive(&sm.bar_raw[v]);
-      }
-      __syncwarp();
-      if (ok) tma_load_3d(sm.raw[v] + lane * box_bytes, tm, 0, s.hk * p.c.page, id, &sm.bar_raw[v]);
-    };
-    auto advance = [&]() {  // to the tile after tile c
-      if (++c < s.c1) {
-        id = id_next;
-      } else {
-        more = walk.more();
-        if (!more) return;
-        s = walk.next(p);
-        c = s.c0;
-        id = id_of(c);
-      }
-      id_next = c + 1 < s.c1 ? id_of(c + 1) : -1;
-    };
-    if (first && more) {
-      s = walk.next(p);
-      c = s.c0;
-      id = id_of(c);
-      id_next = c + 1 < s.c1 ? id_of(c + 1) : -1;
-      bring();
-      advance();
-    }
-    // (after a wait that ran out every thread still meets the others at the barrier of each tile)
-    bool ok = true, flying = begin < stop;
     const uint32_t n = (uint32_t)(stop - begin);
     for (uint32_t kc = 0; kc < n; ++kc) {
       const uint32_t st = kc & 1;
-      ok = ok && mbar_wait(&sm.bar_raw[v], kc & 1, abort);
+      if (!mbar_wait(&sm.bar_raw[v], kc & 1, abort)) break;
       uint4 x[kRows];
 #pragma unroll
       for (int i = 0; i < kRows; ++i) x[i] = *reinterpret_cast<const uint4*>(sm.raw[v] + (i * 128 + lt) * 16);
-      group_sync(1 + v);
-      flying = kc + 1 < n && ok;
-      if (first && flying) {
-        bring();
-        advance();
-      }
-      ok = ok && (kc < 2 || mbar_wait(v ? &sm.bar_v_empty[st] : &sm.bar_k_empty[st], ((kc >> 1) - 1) & 1, abort));
-      if (!ok) continue;
+      mbar_arrive(&sm.bar_raw_empty[v]);
+      if (kc >= 2 && !mbar_wait(v ? &sm.bar_v_empty[st] : &sm.bar_k_empty[st], ((kc >> 1) - 1) & 1, abort)) break;
       // 16 codes of a row -> two 16-byte chunks of the swizzled tile; lanes whose chunks would meet
       // in the same banks store them in the other order
       uint8_t* tile = v ? sm.v[st] : sm.k[st];
@@ -339,10 +336,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       }
       fence_proxy_async_smem();
       mbar_arrive(v ? &sm.bar_v_full[st] : &sm.bar_k_full[st]);
-    }
-    if (!ok && flying && first) {  // codes that may still be on their way
-      int give_up = 0;
-      mbar_wait(&sm.bar_raw[v], n & 1, &give_up, 100000000ull);
     }
   } else {
     regs_increase<kRegsSoftmax>();
