@@ -49,20 +49,42 @@ static_assert(sizeof(ChunkSmem<128>) + 1024 <= 227 * 1024, "shared memory of a C
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-// D[tmem] (+)= A[tmem] * B[smem], four along K in one block: A's rows are the lanes, two fp16 along K
-// in a column, 8 columns an MMA; B's descriptor moves by SB (16-byte units)
-template <int SB>
-__device__ __forceinline__ void umma_f16_ts_x4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Issue by a whole warp: one lane (always the same) is elected inside the asm, so the operands stay in
+// uniform registers, where tcgen05 takes them from.  (In a branch of one lane each MMA's descriptors are
+// moved there first, which took longer than the MMA.)  acc == 0: the first of the four overwrites D.
+// S: D[tmem] (+)= A[smem] * B[smem]^T, four along K, the descriptors moving by 32 bytes
+__device__ __forceinline__ void issue_ss_x4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n"
-      " setp.ne.b32 p, %4, 0;\n setp.eq.b32 q, %4, %4;\n"
+      "{\n .reg .pred e, p, q;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 q, %4, %4;\n"
+      " add.s64 a1, %1, 2;\n add.s64 a2, %1, 4;\n add.s64 a3, %1, 6;\n"
+      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// O: D[tmem] (+)= A[tmem] * B[smem], four along K: A's rows are the lanes, two fp16 along K in a column, 8
+// columns an MMA; B's descriptor moves by 16 rows
+__device__ __forceinline__ void issue_ts_x4(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred e, p, q;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 q, %4, %4;\n"
       " add.s32 a1, %1, 8;\n add.s32 a2, %1, 16;\n add.s32 a3, %1, 24;\n"
-      " add.s64 b1, %2, %5;\n add.s64 b2, %2, %6;\n add.s64 b3, %2, %7;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc), "n"(SB), "n"(2 * SB), "n"(3 * SB)
+      " add.s64 b1, %2, 128;\n add.s64 b2, %2, 256;\n add.s64 b3, %2, 384;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -196,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
 
   if (warp >= 16) {
     regs_decrease<kRegsIssue>();
-    if (warp == 16 && lane == 0 && begin < stop) {
+    if (warp == 16 && begin < stop) {
       // ---------------- MMA issuer
       constexpr uint32_t id_s = idesc_f16(kTile, kTile, false), id_o = idesc_f16(kTile, D, true);
       uint32_t kc = 0, ns[2] = {0, 0}, np[2] = {0, 0};  // key tiles, segments and P tiles so far
@@ -207,54 +229,55 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       auto issue_s = [&](int t, uint32_t kv) {
         const uint64_t a = dq + t * kNext, b = dk + (kv & 1) * kNext;
 #pragma unroll
-        for (int h = 0; h < kAtoms; ++h) umma_bf16_x4<2, 2>(tmem + t * 128, a + h * kAtomStep, b + h * kAtomStep, id_s, h > 0);
-        umma_commit(&sm.bar_s[t]);
+        for (int h = 0; h < kAtoms; ++h) issue_ss_x4(tmem + t * 128, a + h * kAtomStep, b + h * kAtomStep, id_s, h > 0);
+        commit(&sm.bar_s[t]);
       };
       auto issue_pv = [&](int t, uint32_t kv, uint32_t acc) {
         const uint64_t b = dv + (kv & 1) * kNext;
         const uint32_t d = tmem + kColO + t * 128, a = tmem + t * 128;
-        umma_f16_ts_x4<(2048 >> 4)>(d, a, b, id_o, acc);
-        umma_f16_ts_x4<(2048 >> 4)>(d, a + 32, b + (4 * 2048 >> 4), id_o, 1);
+        issue_ts_x4(d, a, b, id_o, acc);
+        issue_ts_x4(d, a + 32, b + (4 * 2048 >> 4), id_o, 1);
       };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort)); };
       bool ok = true;
       while (ok) {
         // a part: its tiles and whether the second row tile has rows, said with the first one's Q
-        if (!mbar_wait(&sm.bar_q[0], ns[0] & 1, abort)) break;
+        if (!wait(&sm.bar_q[0], ns[0] & 1)) break;
         const int said = *const_cast<volatile int*>(&sm.seg[ns[0] & 1]), n = said >> 1;
         const bool two = said & 1;
         if (n == 0) break;
-        ok = (!two || mbar_wait(&sm.bar_q[1], ns[1] & 1, abort)) && mbar_wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1, abort);
+        ok = (!two || wait(&sm.bar_q[1], ns[1] & 1)) && wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         issue_s(0, kc);
         if (two) issue_s(1, kc);
-        umma_commit(&sm.bar_k_empty[kc & 1]);
+        commit(&sm.bar_k_empty[kc & 1]);
         for (int j = 0; j < n; ++j, ++kc) {
           const bool more = j + 1 < n;
-          ok = mbar_wait(&sm.bar_v_full[kc & 1], (kc >> 1) & 1, abort) && mbar_wait(&sm.bar_p[0], np[0] & 1, abort);
+          ok = wait(&sm.bar_v_full[kc & 1], (kc >> 1) & 1) && wait(&sm.bar_p[0], np[0] & 1);
           if (!ok) break;
           ++np[0];
           tc_fence_after();
           issue_pv(0, kc, j > 0);
-          if (!more) umma_commit(&sm.bar_o[0]);
+          if (!more) commit(&sm.bar_o[0]);
           if (more) {
-            ok = mbar_wait(&sm.bar_k_full[(kc + 1) & 1], ((kc + 1) >> 1) & 1, abort);
+            ok = wait(&sm.bar_k_full[(kc + 1) & 1], ((kc + 1) >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
             issue_s(0, kc + 1);
           }
           if (two) {
-            ok = mbar_wait(&sm.bar_p[1], np[1] & 1, abort);
+            ok = wait(&sm.bar_p[1], np[1] & 1);
             if (!ok) break;
             ++np[1];
             tc_fence_after();
             issue_pv(1, kc, j > 0);
-            if (!more) umma_commit(&sm.bar_o[1]);
+            if (!more) commit(&sm.bar_o[1]);
           }
-          umma_commit(&sm.bar_v_empty[kc & 1]);
+          commit(&sm.bar_v_empty[kc & 1]);
           if (more) {
             if (two) issue_s(1, kc + 1);
-            umma_commit(&sm.bar_k_empty[(kc + 1) & 1]);
+            commit(&sm.bar_k_empty[(kc + 1) & 1]);
           }
         }
         ++ns[0];
