@@ -27,7 +27,7 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kTile = 128;                   // keys of a tile, rows of a row tile
 constexpr int kGroups = 128;                 // the batch rows in at most so many groups
-constexpr int kRegsSoftmax = 152, kRegsLoad = 64, kRegsIssue = 48;
+constexpr int kRegsSoftmax = 160, kRegsLoad = 56, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + 2 * kRegsLoad + kRegsIssue <= 5 * 96, "the launch's registers");
 constexpr uint32_t kCols = 512, kColO = 256; // TMEM: S of row tile t at 128 t, O at 256 + 128 t
 
@@ -336,27 +336,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
     for (uint32_t kc = 0; kc < n; ++kc) {
       const uint32_t st = kc & 1;
       if (!mbar_wait(&sm.bar_raw[v], kc & 1, abort)) break;
-      uint4 x[kRows];
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) x[i] = *reinterpret_cast<const uint4*>(sm.raw[v] + (i * 128 + lt) * 16);
-      mbar_arrive(&sm.bar_raw_empty[v]);
       if (kc >= 2 && !mbar_wait(v ? &sm.bar_v_empty[st] : &sm.bar_k_empty[st], ((kc >> 1) - 1) & 1, abort)) break;
       // 16 codes of a row -> two 16-byte chunks of the swizzled tile; lanes whose chunks would meet
       // in the same banks store them in the other order
       uint8_t* tile = v ? sm.v[st] : sm.k[st];
-#pragma unroll
+#pragma unroll 2  // (instruction fetch is shared: unrolled in full the kernel took a tenth longer)
       for (int i = 0; i < kRows; ++i) {
+        const uint4 y = *reinterpret_cast<const uint4*>(sm.raw[v] + (i * 128 + lt) * 16);
         const int r = r0 + i * kRowStep, u = (piece * 2) & 7;
         uint4 lo, hi;
-        codes_to_half<KIND>(x[i].x, lo.x, lo.y);
-        codes_to_half<KIND>(x[i].y, lo.z, lo.w);
-        codes_to_half<KIND>(x[i].z, hi.x, hi.y);
-        codes_to_half<KIND>(x[i].w, hi.z, hi.w);
+        codes_to_half<KIND>(y.x, lo.x, lo.y);
+        codes_to_half<KIND>(y.y, lo.z, lo.w);
+        codes_to_half<KIND>(y.z, hi.x, hi.y);
+        codes_to_half<KIND>(y.w, hi.z, hi.w);
         uint8_t* row = tile + (piece >> 2) * kAtom + (r >> 3) * 1024 + (r & 7) * 128;
         const bool swap = D == 128 && ((piece >> 2) & 1);
         *reinterpret_cast<uint4*>(row + (((u + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
         *reinterpret_cast<uint4*>(row + (((u + !swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
       }
+      mbar_arrive(&sm.bar_raw_empty[v]);
       fence_proxy_async_smem();
       mbar_arrive(v ? &sm.bar_v_full[st] : &sm.bar_k_full[st]);
     }
@@ -434,12 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         scales(id, ks_n, vs_n);
         id = id_at(c + 2);
         // the groups' factors of S, log2 of V's scale and its inverse
-        float big = vs;
+        if (lane < 8) ref = fmaxf(ref, vs);
+        if (__any_sync(0xffffffffu, lane < 8 && !(vs > 0.f))) {
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-        ref = fmaxf(ref, __shfl_sync(0xffffffffu, big, 0));
+          for (int o = 1; o < 8; o <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+        }
         const float ve = value_scale(vs, ref);
-        const float lg = log2f(ve), iv = 1.f / ve;
+        const float lg = lg2(ve), iv = __frcp_rn(ve);
         ok = ok && mbar_wait(&sm.bar_s[t], n_s & 1, abort);
         ++n_s;
         tc_fence_after();
