@@ -8,7 +8,6 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
-#include "codes.cuh"
 #include "kv.h"
 #include "launch.h"
 #include "ptx.cuh"
@@ -22,45 +21,67 @@ __device__ __forceinline__ void kv_error(int* status, int code) { atomicMax(stat
 
 // ------------------------------------------------------------------------------ append
 
-constexpr int kAppendThreads = 128;
+// 64 values a thread, at 64 registers: 1024 threads an SM with 128 KB of new tokens on their way
+template <int D, int P>
+constexpr int kAppendThreads = D * P / 64 < 64 ? 64 : D * P / 64;
 
-// e4m3 codes of eight values under the scale s, and what a code stands for under it
-__device__ __forceinline__ uint2 e4m3_codes8(const float (&x)[8], float s) {
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; i += 2)
-    w[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[i], s), __fdiv_rn(x[i + 1], s)),
-                                                    __NV_SATFINITE, __NV_E4M3)
-                 << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
+// What a block's scale s brings to its codes.  RN(x / s) by Markstein's correction (P. Markstein,
+// Computation of elementary functions on the IBM RISC System/6000 processor, 1990): inv = RN(1 / s),
+// q = RN(x inv), r = x - q s (exact), RN(q + r inv) is the rounded quotient unless s's fraction is all
+// ones; r is exact for every x that matters (|x / s| >= 2^-10, below it the code is 0) where
+// s >= 2^-110.  Other scales divide.  With z = -x for x and -r for r a zero keeps its sign: q is RN(z ninv)
+// and the quotient RN(q + (q s + z) ninv), ninv = -inv.
+struct Quant {
+  float s;
+  bool fast;
+  uint64_t ninv2, s2;
+};
+__device__ __forceinline__ Quant quant_of(float s) {
+  Quant q;
+  q.s = s;
+  q.fast = s >= 0x1p-110f && s <= 0x1p110f && (__float_as_uint(s) & 0x7fffffu) != 0x7fffffu;
+  const float inv = q.fast ? __frcp_rn(s) : 0.f;
+  q.ninv2 = f2(-inv, -inv), q.s2 = f2(s, s);
+  return q;
 }
-__device__ __forceinline__ uint2 int8_codes8(const float (&x)[8], float s) {
-  float c[8];
-  const float inv = __frcp_rn(s);
-  if (inv < INFINITY) {
-    int_codes8(x, s, inv, c);
-  } else {  // a subnormal scale whose reciprocal overflows
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = fminf(fmaxf(rintf(__fdiv_rn(x[i], s)), -127.f), 127.f);
+// Codes of four values x = -z: the int8 code is the low byte of RN(x / s) + 1.5 2^23 (|x / s| is at most
+// 127 (1 + 2^-22): nothing to saturate)
+template <int KIND>
+__device__ __forceinline__ uint32_t codes4(float z0, float z1, float z2, float z3, const Quant& q) {
+  float y[4];
+  if (q.fast) {
+    const uint64_t a = f2(z0, z1), b = f2(z2, z3);
+    const uint64_t qa = fmul2(a, q.ninv2), qb = fmul2(b, q.ninv2);
+    f2split(ffma2(ffma2(qa, q.s2, a), q.ninv2, qa), y[0], y[1]);
+    f2split(ffma2(ffma2(qb, q.s2, b), q.ninv2, qb), y[2], y[3]);
+  } else if (q.s > 0.f) {
+    y[0] = __fdiv_rn(-z0, q.s), y[1] = __fdiv_rn(-z1, q.s), y[2] = __fdiv_rn(-z2, q.s), y[3] = __fdiv_rn(-z3, q.s);
+  } else {
+    return 0u;
   }
-  uint32_t w[2] = {0u, 0u};
+  if (KIND == SAGE_KV_INT8) {
+    uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i >> 2] |= ((uint32_t)(int)c[i] & 0xffu) << (8 * (i & 3));
-  return make_uint2(w[0], w[1]);
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(__fadd_rn(y[i], 12582912.f));
+    return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+  }
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
 }
 template <int KIND>
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float s) {
-  if (!(s > 0.f)) return make_uint2(0u, 0u);
-  return KIND == SAGE_KV_INT8 ? int8_codes8(x, s) : e4m3_codes8(x, s);
+__device__ __forceinline__ uint2 codes8(const float (&z)[8], const Quant& q) {
+  return make_uint2(codes4<KIND>(z[0], z[1], z[2], z[3], q), codes4<KIND>(z[4], z[5], z[6], z[7], q));
 }
+// the negated values of eight codes
 template <int KIND>
-__device__ __forceinline__ void values8(uint2 c, float s, float (&x)[8]) {
+__device__ __forceinline__ void negated8(uint2 c, float s, float (&z)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t b = ((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xffu;
     const float v = KIND == SAGE_KV_INT8 ? (float)(int)(int8_t)b
                                          : __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3)));
-    x[i] = __fmul_rn(v, s);
+    z[i] = -__fmul_rn(v, s);
   }
 }
 
@@ -73,11 +94,12 @@ struct AppendParams {
 };
 
 // One CTA per (page that the new tokens of a batch row can touch, key/value head, K or V).  A
-// thread holds its eight channels of P D / 1024 tokens in registers between the maximum and the
+// thread holds its eight channels of up to eight tokens in registers between the maximum and the
 // codes, so the new tokens are read once.
 template <int D, int P, int KIND>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
-  constexpr int TPR = D / 8, RPP = kAppendThreads / TPR, NP = P / RPP;  // threads a token, tokens a pass, passes
+__global__ void __launch_bounds__(kAppendThreads<D, P>, 1024 / kAppendThreads<D, P>) kv_append_kernel(const AppendParams p) {
+  constexpr int kThreads = kAppendThreads<D, P>;
+  constexpr int TPR = D / 8, RPP = kThreads / TPR, NP = P / RPP;  // threads a token, tokens a pass, passes
   static_assert(P % RPP == 0, "a page is a whole number of passes");
   pdl_wait();
   pdl_trigger();
@@ -92,10 +114,23 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
   if (pos < 0 || n <= 0) return;  // nothing new, or refused by sage_attn_kv_extend
   const int j = pos / P + blockIdx.x, t0 = j * P;
   if ((long long)t0 >= (long long)pos + n) return;
+  // the new tokens are on their way while the table is read
+  const int off = max(0, pos - t0);              // tokens of the page that are there already
+  const int end = min((long long)P, (long long)pos + n - t0);
+  // token 0 of the page is token t0 - pos of the new ones
+  const __nv_bfloat16* src =
+      (is_v ? p.V : p.K) + (((size_t)b * p.c.Hkv + hk) * p.Nn) * D + (ptrdiff_t)(t0 - pos) * D;
+  const int g = tid % TPR, r0 = tid / TPR;
+  uint4 u[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int r = r0 + i * RPP;
+    if (r >= off && r < end && n <= p.Nn) u[i] = reinterpret_cast<const uint4*>(src + (size_t)r * D)[g];
+  }
   // a batch row that names a slot again is left out
   if (p.slots) {
     bool again = false;
-    for (int i = tid; i < b; i += kAppendThreads) again |= p.slots[i] == slot;
+    for (int i = tid; i < b; i += kThreads) again |= p.slots[i] == slot;
     if (__syncthreads_or(again)) {
       if (tid == 0) kv_error(p.c.status, kDevIndex);
       return;
@@ -107,68 +142,74 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     if (tid == 0) kv_error(p.c.status, kDevIndex);
     return;
   }
-  const int off = max(0, pos - t0);              // tokens of the page that are there already
-  const int end = min((long long)P, (long long)pos + n - t0);
   const size_t block = (size_t)page * p.c.Hkv + hk;
   float* scale = (is_v ? p.c.v_scale : p.c.k_scale) + block;
   uint8_t* codes = static_cast<uint8_t*>(is_v ? p.c.v : p.c.k) + block * P * D;
-  // token 0 of the page is token t0 - pos of the new ones
-  const __nv_bfloat16* src =
-      (is_v ? p.V : p.K) + (((size_t)b * p.c.Hkv + hk) * p.Nn) * D + (ptrdiff_t)(t0 - pos) * D;
-  const int g = tid % TPR, r0 = tid / TPR;
   const float was = off > 0 ? *scale : 0.f;
+  const bool shifted = !is_v && p.shift;
   float sh[8] = {};
-  if (!is_v && p.shift) {
+  if (shifted) {
     const float4* s4 = reinterpret_cast<const float4*>(p.shift + hk * D + g * 8);
     const float4 a = s4[0], c = s4[1];
     sh[0] = a.x, sh[1] = a.y, sh[2] = a.z, sh[3] = a.w, sh[4] = c.x, sh[5] = c.y, sh[6] = c.z, sh[7] = c.w;
   }
-  uint4 u[NP];
+  auto negated = [&](const uint4& w, float (&z)[8]) {
+    const uint32_t flip = shifted ? 0u : 0x80008000u;
+    const uint32_t v[4] = {w.x ^ flip, w.y ^ flip, w.z ^ flip, w.w ^ flip};
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int r = r0 + i * RPP;
-    if (r >= off && r < end) u[i] = reinterpret_cast<const uint4*>(src + (size_t)r * D)[g];
-  }
-  auto value = [&](const uint4& w, float (&x)[8]) {
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    for (int e = 0; e < 4; ++e) z[2 * e] = __uint_as_float(v[e] << 16), z[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+    if (shifted) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = __fsub_rn(__uint_as_float(v[e] << 16), sh[2 * e]);
-      x[2 * e + 1] = __fsub_rn(__uint_as_float(v[e] & 0xffff0000u), sh[2 * e + 1]);
+      for (int e = 0; e < 8; ++e) z[e] = -__fsub_rn(z[e], sh[e]);
     }
   };
   float top = 0.f;
+  if (shifted) {
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int r = r0 + i * RPP;
-    if (r >= off && r < end) {
-      float x[8];
-      value(u[i], x);
+    for (int i = 0; i < NP; ++i) {
+      const int r = r0 + i * RPP;
+      if (r >= off && r < end) {
+        float z[8];
+        negated(u[i], z);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(z[e]));
+      }
     }
+  } else {  // two values at a time
+    __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int r = r0 + i * RPP;
+      if (r >= off && r < end) {
+        const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&u[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top2 = __hmax2(top2, __habs2(x[e]));
+      }
+    }
+    top = fmaxf(__low2float(top2), __high2float(top2));
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  __shared__ float wtop[kAppendThreads / 32];
+  __shared__ float wtop[kThreads / 32];
   if ((tid & 31) == 0) wtop[tid >> 5] = top;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kAppendThreads / 32; ++i) top = fmaxf(top, wtop[i]);
+  for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, wtop[i]);
   const float fresh = __fmul_rn(top, KIND == SAGE_KV_INT8 ? 1.f / 127.f : 1.f / 448.f);
   const float now = fmaxf(was, fresh);
+  const Quant q = quant_of(now);
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int r = r0 + i * RPP;
     uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)r * D) + g;
     if (r >= off && r < end) {
-      float x[8];
-      value(u[i], x);
-      *dst = codes8<KIND>(x, now);
+      float z[8];
+      negated(u[i], z);
+      *dst = codes8<KIND>(z, q);
     } else if (r < off && now != was) {  // the page's scale grew: what the old codes stand for, under the new one
-      float x[8];
-      values8<KIND>(*dst, was, x);
-      *dst = codes8<KIND>(x, now);
+      float z[8];
+      negated8<KIND>(*dst, was, z);
+      *dst = codes8<KIND>(z, q);
     }
   }
   if (tid == 0) *scale = now;
@@ -190,22 +231,23 @@ auto append_kernel_for(int page, int kind) {
 constexpr int kScanThreads = 1024;
 
 // sum of v over the threads before this one, and over all (whole CTA of kScanThreads)
-__device__ __forceinline__ int block_exclusive(int v, int* warp_sums, int* total) {
+template <class T>
+__device__ __forceinline__ T block_exclusive(T v, T* warp_sums, T* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  int s = v;
+  T s = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, s, o);
+    const T t = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += t;
   }
   __syncthreads();  // the last call's sums have been read
   if (lane == 31) warp_sums[w] = s;
   __syncthreads();
   if (w == 0) {
-    int x = warp_sums[lane];
+    T x = warp_sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, x, o);
+      const T t = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += t;
     }
     warp_sums[lane] = x;
@@ -295,12 +337,14 @@ __device__ __forceinline__ Need slot_need(const sage_kv_cache& c, const int* n_n
 }
 
 // One CTA: the slots' needs are summed in slot order, then refs is scanned for free pages and
-// the r-th free page goes to the slot whose range of needs holds r.  `excl` (shared) keeps the
-// sums, so finding the slot is a binary search.
+// the r-th free page goes to the slot whose range of needs holds r.  Shared memory keeps the sums
+// (so finding the slot is a binary search) and the place in its table where a slot's pages begin.
 __global__ void __launch_bounds__(kScanThreads) kv_extend_kernel(const sage_kv_cache c, const int* __restrict__ n_new,
                                                                  int* __restrict__ pos, int* __restrict__ cow) {
-  extern __shared__ int excl[];  // [n_slots + 1]
+  extern __shared__ int excl[];        // [n_slots + 1]
+  int* first_page = excl + c.n_slots + 1;  // [n_slots]; -1: refused
   __shared__ int warp_sums[32];
+  __shared__ long long need_sums[32];
   constexpr int kPer = 16;  // pages a thread looks at in one step
   pdl_wait();
   pdl_trigger();
@@ -313,14 +357,15 @@ __global__ void __launch_bounds__(kScanThreads) kv_extend_kernel(const sage_kv_c
       const Need q = slot_need(c, n_new, s);
       need = q.count();
       cow[s] = q.last;
+      first_page[s] = q.bad ? -1 : q.have - (q.last >= 0);
       if (q.bad) kv_error(c.status, kDevIndex);
     }
-    int total;
-    const int e = block_exclusive(need, warp_sums, &total);
-    // needs are at most max_pages + 1 each; past 2^30 in all nothing can be served any more
-    const int at = (int)min((long long)carry + e, 1ll << 30);
+    long long total;
+    const long long e = block_exclusive((long long)need, need_sums, &total);
+    // a pool has at most 2^28 pages: past 2^30 in all nothing can be served any more
+    const int at = (int)min(carry + e, 1ll << 30);
     if (s < c.n_slots) excl[s] = at;
-    carry = (int)min((long long)carry + total, 1ll << 30);
+    carry = (int)min(carry + total, 1ll << 30);
   }
   if (tid == 0) excl[c.n_slots] = carry;
   __syncthreads();
@@ -349,9 +394,7 @@ __global__ void __launch_bounds__(kScanThreads) kv_extend_kernel(const sage_kv_c
         if (excl[mid] <= r) lo = mid;
         else hi = mid;
       }
-      const int have = (c.lengths[lo] + c.page - 1) / c.page;
-      const int begin = have - (cow[lo] >= 0);
-      c.table[(size_t)lo * c.max_pages + begin + r - excl[lo]] = page;
+      c.table[(size_t)lo * c.max_pages + first_page[lo] + r - excl[lo]] = page;
       c.refs[page] = 1;
     }
     found += total;
@@ -359,22 +402,20 @@ __global__ void __launch_bounds__(kScanThreads) kv_extend_kernel(const sage_kv_c
   __syncthreads();
   for (int s = tid; s < c.n_slots; s += kScanThreads) {
     const int n = n_new[s], len = c.lengths[s], from = cow[s];
-    const int need = excl[s + 1] - excl[s];
-    const long long cap = (long long)c.max_pages * c.page;
-    const bool bad = len < 0 || n < 0 || (long long)len + n > cap;
-    if (!bad && (need == 0 || excl[s + 1] <= found)) {
+    const int need = excl[s + 1] - excl[s], begin = first_page[s];  // (need: 0 where the sums stand at 2^30)
+    const bool nothing = ((long long)len + n + c.page - 1) / c.page == begin && from < 0;
+    if (begin >= 0 && (nothing || excl[s + 1] <= found)) {
       pos[s] = len;
       if (n > 0) c.lengths[s] = len + n;
       if (from >= 0) atomicSub(c.refs + from, 1);
     } else {
       pos[s] = -1;
       cow[s] = -1;
-      if (!bad) {
+      if (begin >= 0) {
         // too few pages: what this slot has been given goes back
-        int* row = c.table + (size_t)s * c.max_pages;
-        const int begin = (len + c.page - 1) / c.page - (from >= 0);
-        for (int i = 0; i < need && excl[s] + i < found; ++i) c.refs[row[begin + i]] = 0;
-        if (from >= 0) row[begin] = from;
+        int* row = c.table + (size_t)s * c.max_pages + begin;
+        for (int i = 0; i < need && excl[s] + i < found; ++i) c.refs[row[i]] = 0;
+        if (from >= 0) row[0] = from;
         kv_error(c.status, kDevPages);
       }
     }
@@ -490,8 +531,9 @@ int launch_kv_append(const sage_kv_cache& c, const void* K, const void* V, const
                  n_new, B, Nn};
   auto kern = c.D == 128 ? append_kernel_for<128>(c.page, c.kind) : append_kernel_for<64>(c.page, c.kind);
   const unsigned pages = (unsigned)(((long long)Nn + c.page - 2) / c.page + 1);  // that Nn tokens can touch
+  const int threads = c.D * c.page / 64 < 64 ? 64 : c.D * c.page / 64;  // kAppendThreads
   ScopedTimer timer("kv_append", st);
-  if (launch_pdl(kern, dim3(pages, 2 * c.Hkv, B), dim3(kAppendThreads), 0, st, p) != cudaSuccess) return 3;
+  if (launch_pdl(kern, dim3(pages, 2 * c.Hkv, B), dim3(threads), 0, st, p) != cudaSuccess) return 3;
   return cudaGetLastError() == cudaSuccess ? 0 : 3;
 }
 
@@ -509,8 +551,9 @@ int launch_kv_truncate(const sage_kv_cache& c, const int* keep, cudaStream_t st)
 
 int launch_kv_extend(const sage_kv_cache& c, const int* n_new, int* pos, int* cow, cudaStream_t st) {
   ScopedTimer timer("kv_pages", st);
-  const size_t smem = ((size_t)c.n_slots + 1) * 4;  // at most 32 KB (kKvMaxSlots)
-  if (launch_pdl(kv_extend_kernel, dim3(1), dim3(kScanThreads), smem, st, c, n_new, pos, cow) != cudaSuccess ||
+  const size_t smem = (2 * (size_t)c.n_slots + 1) * 4;  // at most 64 KB (kKvMaxSlots)
+  if (cudaFuncSetAttribute(kv_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+      launch_pdl(kv_extend_kernel, dim3(1), dim3(kScanThreads), smem, st, c, n_new, pos, cow) != cudaSuccess ||
       launch_pdl(kv_cow_kernel, dim3(c.n_slots, kCowParts), dim3(256), 0, st, c, (const int*)pos, (const int*)cow) !=
           cudaSuccess)
     return 3;

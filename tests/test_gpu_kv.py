@@ -377,6 +377,20 @@ def test_extend_many_slots_and_pages():
     assert sa.get_status(c.status) == sa.SAGE_ERR_NO_PAGES
 
 
+def test_extend_asks_for_more_than_there_can_be():
+    """Needs whose sum passes 32 bits: nothing is served behind the first one that does not fit."""
+    S = 100  # (100 slots of 2^25 pages: a table of 13 GB)
+    c = sa.kv_cache(50, 1, 64, S, 2 ** 25, page=16)
+    r = kv_ref.Cache(50, 1, 64, S, 4, 16, "int8")
+    n = np.full(S, 2 ** 29 - 4096)
+    n[:3] = [17, 0, 40]
+    pos = sa.kv_extend(c, dev(n)).cpu().numpy()
+    assert pos[:3].tolist() == [0, 0, 0] and (pos[3:] == -1).all()
+    r.extend([17, 0, 40] + [0] * (S - 3))
+    assert np.array_equal(c.lengths.cpu().numpy(), r.lengths) and np.array_equal(c.refs.cpu().numpy(), r.refs)
+    assert sa.get_status(c.status) == sa.SAGE_ERR_NO_PAGES
+
+
 def test_compact_too_small_and_refusals():
     rng = np.random.default_rng(4)
     c, r = pair(12, 1, 64, 3, 6, 16, "e4m3", poison=False)
