@@ -5,14 +5,14 @@
 // 2 D bytes for every key that 256 rows share.  One CTA an SM takes units of 256 rows (two tiles of
 // 128: the queries of the G heads of a key/value head, token by token) and walks the unit's
 // 128-key tiles:
-//  - warps 17 and 18 bring the codes of K and V by TMA, a tile ahead; warps 8-11 (K) and 12-15 (V)
+//  - warps 17 and 18 bring the codes of K and V by TMA, half a tile at a time; warps 8-11 (K) and 12-15 (V)
 //    turn them into fp16 (exact) and store them where tcgen05.mma reads them (128-byte swizzle), two
 //    tiles deep;
 //  - one thread issues S = Q K^T and O += P V (kind::f16, fp32 accumulators in TMEM) for the two row
 //    tiles in turn, so the tensor core works on one tile while the softmax works on the other;
-//  - warps 0-3 and 4-7 own a row tile each, a thread a row: S from TMEM twice (maximum, then
-//    exponentials: a row of S does not stay in registers), P back into TMEM over S's columns, from
-//    where the second product takes it.
+//  - warps 0-3 and 4-7 own a row tile each, a thread a row: S from TMEM, P back into TMEM over S's
+//    columns, from where the second product takes it.  The maximum is found with the exponentials,
+//    not before them: the reference that they need moves seldom (see kRaise).
 // Units are cut over the grid like those of the few-row kernel (kv_attn.cu), in 128-key tiles.
 #include <type_traits>
 
@@ -25,7 +25,7 @@ namespace sage {
 namespace {
 
 constexpr int kThreads = 640;
-constexpr int kTile = 128;                   // keys of a tile, rows of a row tile
+constexpr int kTile = 128, kHalf = 64;       // keys of a tile (and of half of one), rows of a row tile
 constexpr int kGroups = 128;                 // the batch rows in at most so many groups
 constexpr int kRegsSoftmax = 160, kRegsLoad = 56, kRegsIssue = 48;
 static_assert(2 * kRegsSoftmax + 2 * kRegsLoad + kRegsIssue <= 5 * 96, "the launch's registers");
@@ -37,7 +37,7 @@ struct ChunkSmem {
   uint8_t k[2][kTile * D * 2];
   uint8_t v[2][kTile * D * 2];
   uint8_t raw[2][kTile * D];  // codes of a K and a V tile
-  uint64_t bar_q[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_raw[2], bar_raw_empty[2], bar_s[2], bar_p[2], bar_o[2];
+  uint64_t bar_q[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_raw[2][2], bar_raw_empty[2][2], bar_s[2], bar_p[2], bar_o[2];
   long long wsum[kThreads / 32];
   long long pre[kGroups + 1];  // tiles before each group of batch rows
   uint32_t tmem_base;
@@ -171,8 +171,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       mbar_init(&sm.bar_k_empty[s], 1);
       mbar_init(&sm.bar_v_full[s], 128);
       mbar_init(&sm.bar_v_empty[s], 1);
-      mbar_init(&sm.bar_raw[s], 1);
-      mbar_init(&sm.bar_raw_empty[s], 128);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sm.bar_raw[s][h], 1);
+        mbar_init(&sm.bar_raw_empty[s][h], 128);
+      }
       mbar_init(&sm.bar_s[s], 1);
       mbar_init(&sm.bar_p[s], 128);
       mbar_init(&sm.bar_o[s], 1);
@@ -285,47 +287,53 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       }
     }
     if ((warp == 17 || warp == 18) && begin < stop) {
-      // ---------------- the codes of K (warp 17) or V (18), a tile at a time: a lane for each page
-      const int v = warp - 17, boxes = kTile / p.c.page, box_bytes = p.c.page * D;
+      // ---------------- the codes of K (warp 17) or V (18), half a tile at a time: a lane for each page
+      const int v = warp - 17, box = p.c.page < kHalf ? p.c.page : kHalf, boxes = kHalf / box, box_bytes = box * D;
       const CUtensorMap* tm = v ? &tm_v : &tm_k;
       Walk walk(sm.pre, group, begin, stop);
       Seg s = walk.next(p);
-      int c = s.c0;
-      auto page_of = [&](int tile) {
-        const int token = tile * kTile + lane * p.c.page;
+      int c = 2 * s.c0;  // in half tiles
+      auto page_of = [&](int half) {
+        const int token = half * kHalf + lane * box;
         return lane < boxes && token < s.len ? p.c.table[(size_t)s.slot * p.c.max_pages + token / p.c.page] : -1;
       };
-      int id = page_of(c), id_next = c + 1 < s.c1 ? page_of(c + 1) : -1;
-      uint32_t kc = 0;
-      for (;; ++kc) {
+      int id = page_of(c), id_next = page_of(c + 1);
+      uint32_t n = 0;  // half tiles so far
+      for (;; ++n) {
         // (what lies behind the keys stays as it was: finite, and masked)
         const bool ok = (unsigned)id < (unsigned)p.c.n_pages;
         if (!ok && id != -1) atomicMax(p.c.status, kDevIndex);
         const uint32_t all = __ballot_sync(0xffffffffu, ok);
-        if (!__all_sync(0xffffffffu, kc == 0 || mbar_wait(&sm.bar_raw_empty[v], (kc - 1) & 1, abort))) break;
+        uint64_t* full = &sm.bar_raw[v][n & 1];
+        if (!__all_sync(0xffffffffu, n < 2 || mbar_wait(&sm.bar_raw_empty[v][n & 1], ((n >> 1) - 1) & 1, abort))) break;
         if (lane == 0) {
           if (all)
-            mbar_arrive_expect_tx(&sm.bar_raw[v], __popc(all) * box_bytes);
+            mbar_arrive_expect_tx(full, __popc(all) * box_bytes);
           else
-            mbar_arrive(&sm.bar_raw[v]);
+            mbar_arrive(full);
         }
         __syncwarp();
-        if (ok) tma_load_3d(sm.raw[v] + lane * box_bytes, tm, 0, s.hk * p.c.page, id, &sm.bar_raw[v]);
-        if (++c < s.c1) {
+        if (ok)
+          tma_load_3d(sm.raw[v] + (n & 1) * kHalf * D + lane * box_bytes, tm, 0,
+                      s.hk * p.c.page + ((c * kHalf + lane * box) & (p.c.page - 1)), id, full);
+        if (++c < 2 * s.c1) {
           id = id_next;
         } else {
           if (!walk.more()) {
-            ++kc;
+            ++n;
             break;
           }
           s = walk.next(p);
-          c = s.c0;
+          c = 2 * s.c0;
           id = page_of(c);
         }
-        id_next = c + 1 < s.c1 ? page_of(c + 1) : -1;
+        id_next = c + 1 < 2 * s.c1 ? page_of(c + 1) : -1;
       }
-      int give_up = 0;  // the last copies (after a wait that ran out nobody else waits for them)
-      mbar_wait(&sm.bar_raw[v], (kc - 1) & 1, &give_up);
+      // the last copies (after a wait that ran out nobody else waits for them)
+      for (uint32_t k = n < 2 ? 0 : n - 2; k < n; ++k) {
+        int give_up = 0;
+        mbar_wait(&sm.bar_raw[v][k & 1], (k >> 1) & 1, &give_up);
+      }
     }
   } else if (warp >= 8) {
     regs_decrease<kRegsLoad>();
@@ -335,26 +343,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
     const uint32_t n = (uint32_t)(stop - begin);
     for (uint32_t kc = 0; kc < n; ++kc) {
       const uint32_t st = kc & 1;
-      if (!mbar_wait(&sm.bar_raw[v], kc & 1, abort)) break;
       if (kc >= 2 && !mbar_wait(v ? &sm.bar_v_empty[st] : &sm.bar_k_empty[st], ((kc >> 1) - 1) & 1, abort)) break;
       // 16 codes of a row -> two 16-byte chunks of the swizzled tile; lanes whose chunks would meet
       // in the same banks store them in the other order
       uint8_t* tile = v ? sm.v[st] : sm.k[st];
+      bool ok = true;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        ok = ok && mbar_wait(&sm.bar_raw[v][h], kc & 1, abort);
 #pragma unroll 2  // (instruction fetch is shared: unrolled in full the kernel took a tenth longer)
-      for (int i = 0; i < kRows; ++i) {
-        const uint4 y = *reinterpret_cast<const uint4*>(sm.raw[v] + (i * 128 + lt) * 16);
-        const int r = r0 + i * kRowStep, u = (piece * 2) & 7;
-        uint4 lo, hi;
-        codes_to_half<KIND>(y.x, lo.x, lo.y);
-        codes_to_half<KIND>(y.y, lo.z, lo.w);
-        codes_to_half<KIND>(y.z, hi.x, hi.y);
-        codes_to_half<KIND>(y.w, hi.z, hi.w);
-        uint8_t* row = tile + (piece >> 2) * kAtom + (r >> 3) * 1024 + (r & 7) * 128;
-        const bool swap = D == 128 && ((piece >> 2) & 1);
-        *reinterpret_cast<uint4*>(row + (((u + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(row + (((u + !swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+        for (int i = h * (kRows / 2); i < (h + 1) * (kRows / 2); ++i) {
+          const uint4 y = *reinterpret_cast<const uint4*>(sm.raw[v] + (i * 128 + lt) * 16);
+          const int r = r0 + i * kRowStep, u = (piece * 2) & 7;
+          uint4 lo, hi;
+          codes_to_half<KIND>(y.x, lo.x, lo.y);
+          codes_to_half<KIND>(y.y, lo.z, lo.w);
+          codes_to_half<KIND>(y.z, hi.x, hi.y);
+          codes_to_half<KIND>(y.w, hi.z, hi.w);
+          uint8_t* row = tile + (piece >> 2) * kAtom + (r >> 3) * 1024 + (r & 7) * 128;
+          const bool swap = D == 128 && ((piece >> 2) & 1);
+          *reinterpret_cast<uint4*>(row + (((u + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
+          *reinterpret_cast<uint4*>(row + (((u + !swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
+        }
+        mbar_arrive(&sm.bar_raw_empty[v][h]);
       }
-      mbar_arrive(&sm.bar_raw_empty[v]);
+      if (!ok) break;
       fence_proxy_async_smem();
       mbar_arrive(v ? &sm.bar_v_full[st] : &sm.bar_k_full[st]);
     }
@@ -444,66 +457,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         tc_fence_after();
         const bool edge = __any_sync(0xffffffffu, lim < (c + 1) * kTile);
         const int left = lim - c * kTile;
-        // first pass: the row's maximum of u
-        float mx = -INFINITY;
-        uint32_t sv[2][32];
-        tmem_ld32(s_col, sv[0]);
-        auto maximum = [&](auto edge_tile) {
-          constexpr bool kEdge = decltype(edge_tile)::value;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            tmem_wait32(sv[x & 1]);
-            if (x < 3) tmem_ld32(s_col + 32 * (x + 1), sv[(x + 1) & 1]);
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const float f = __shfl_sync(0xffffffffu, ks, 2 * x + y) * a_row, g = __shfl_sync(0xffffffffu, lg, 2 * x + y);
-              float top = -INFINITY;
-              if (kEdge) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  top = fmaxf(top, x * 32 + y * 16 + e < left ? fmaf(__uint_as_float(sv[x & 1][y * 16 + e]), f, g) : -INFINITY);
-                mx = fmaxf(mx, top);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 16; e += 2)
-                  top = max3(top, __uint_as_float(sv[x & 1][y * 16 + e]), __uint_as_float(sv[x & 1][y * 16 + e + 1]));
-                mx = fmaxf(mx, fmaf(top, f, g));
-              }
-            }
-          }
-        };
-        if (edge)
-          maximum(std::true_type());
-        else
-          maximum(std::false_type());
-        tmem_ld32(s_col, sv[0]);  // (for the second pass)
-        const bool raise = mx > m + kRaise;
-        if (__any_sync(0xffffffffu, raise)) {
-          const float to = raise ? mx - kBelow : m, corr = raise ? ex2(m - to) : 1.f;
-          m = to;
-          l *= corr;
-          if (c > s.c0) {  // (the part's first product overwrites O; PV of the tile before is done: S came after it)
-#pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_col + d, o);
-              tmem_wait32(o);
-              reg_fence32(sv[0]);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
-              tmem_st32(o_col + d, o);
-            }
-          }
-        }
-        const float sub = m == -INFINITY ? 0.f : m;
-        // second pass: P over the columns that have been read
+        // P of the row with the reference as it stands, in registers, and the largest u - m; where that
+        // passes kRaise (a part's first tile, and seldom again) the reference is raised and P is
+        // computed once more from S
+        uint32_t w[4][16];
+        float top, sum_l, sub;
         auto exponentials = [&](auto edge_tile) {
           constexpr bool kEdge = decltype(edge_tile)::value;
+          top = -INFINITY, sum_l = 0.f;
+          uint32_t sv[2][32];
+          tmem_ld32(s_col, sv[0]);
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             tmem_wait32(sv[x & 1]);
             if (x < 3) tmem_ld32(s_col + 32 * (x + 1), sv[(x + 1) & 1]);
-            uint32_t w[16];
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const float f = __shfl_sync(0xffffffffu, ks, 2 * x + y) * a_row;
@@ -516,25 +483,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
                 f2split(
                     ffma2(f2(__uint_as_float(sv[x & 1][y * 16 + e]), __uint_as_float(sv[x & 1][y * 16 + e + 1])), f2v, g2v),
                     u0, u1);
-                u0 = ex2(u0), u1 = ex2(u1);
                 if (kEdge) {
-                  if (x * 32 + y * 16 + e >= left) u0 = 0.f;
-                  if (x * 32 + y * 16 + e + 1 >= left) u1 = 0.f;
+                  if (x * 32 + y * 16 + e >= left) u0 = -INFINITY;
+                  if (x * 32 + y * 16 + e + 1 >= left) u1 = -INFINITY;
                 }
+                top = max3(top, u0, u1);
+                u0 = ex2(u0), u1 = ex2(u1);
                 sum = fadd2(sum, f2(u0, u1));
-                w[y * 8 + (e >> 1)] = h2bits(__floats2half2_rn(u0, u1));
+                w[x][y * 8 + (e >> 1)] = h2bits(__floats2half2_rn(u0, u1));
               }
               float y0, y1;
               f2split(sum, y0, y1);
-              l = fmaf(y0 + y1, __shfl_sync(0xffffffffu, iv, 2 * x + y), l);
+              sum_l = fmaf(y0 + y1, __shfl_sync(0xffffffffu, iv, 2 * x + y), sum_l);
             }
-            tmem_st16(s_col + x * 16, w);
           }
         };
-        if (edge)
-          exponentials(std::true_type());
-        else
-          exponentials(std::false_type());
+#pragma unroll 1
+        for (;;) {
+          sub = m == -INFINITY ? 0.f : m;
+          if (edge)
+            exponentials(std::true_type());
+          else
+            exponentials(std::false_type());
+          const bool raise = top > (m == -INFINITY ? -INFINITY : kRaise);
+          if (!__any_sync(0xffffffffu, raise)) break;
+          const float to = raise ? top + sub - kBelow : m, corr = raise ? ex2(m - to) : 1.f;
+          m = to;
+          l *= corr;
+          if (c > s.c0) {  // (the part's first product overwrites O; PV of the tile before is done: S came after it)
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_col + d, o);
+              tmem_wait32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              tmem_st32(o_col + d, o);
+            }
+          }
+        }
+        l += sum_l;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_st16(s_col + x * 16, w[x]);
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sm.bar_p[t]);
@@ -595,12 +585,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
 template <int D, int KIND>
 int launch(const AttnParams& p, int sms, cudaStream_t st) {
   auto kern = kv_chunk_kernel<D, KIND>;
-  // a page's rows [head, token]: boxes of a page's tokens of a head
+  // a page's rows [head, token]: boxes of a page's tokens of a head, at most half a tile
+  const int box = p.c.page < kHalf ? p.c.page : kHalf;
   CUtensorMap tk, tv;
   if (!make_tmap_3d(&tk, p.c.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, (uint64_t)p.c.Hkv * p.c.page, p.c.n_pages, D,
-                    p.c.page, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+                    box, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !make_tmap_3d(&tv, p.c.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, (uint64_t)p.c.Hkv * p.c.page, p.c.n_pages, D,
-                    p.c.page, CU_TENSOR_MAP_SWIZZLE_NONE))
+                    box, CU_TENSOR_MAP_SWIZZLE_NONE))
     return 3;
   const size_t smem = sizeof(ChunkSmem<D>) + 1024;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 3;
