@@ -34,12 +34,16 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kSub = 2;           // 16-token MMA row tiles of a chunk
 constexpr int kChunk = 16 * kSub; // tokens of one step of a warp
-// Chunks of a warp in flight or at work, and CTAs an SM: 8 query rows need 168 registers a thread, 16
-// need 255 (at 168 their spills cost a quarter of the time).
-template <int RT>
-constexpr int kStages = RT == 1 ? 2 : 3;
-template <int RT>
-constexpr int kCtasPerSm = RT == 1 ? 3 : 2;
+// Chunks of a warp in flight or at work, and CTAs an SM.  D = 64 with 8 query rows: three CTAs of 168
+// registers a thread and two chunks (12 sequences of 0.3-16k tokens: 57 us, 63 us the other way).  Else two
+// CTAs of 255 and three chunks: D = 128 gains 3 % by it (4 of 100-131k tokens: 159 us, 164 us the other
+// way), and 16 rows at 168 registers spill (a quarter of the time).
+template <int D, int RT>
+constexpr bool kThreeCtas = D == 64 && RT == 1;
+template <int D, int RT>
+constexpr int kStages = kThreeCtas<D, RT> ? 2 : 3;
+template <int D, int RT>
+constexpr int kCtasPerSm = kThreeCtas<D, RT> ? 3 : 2;
 // What the start of a unit costs a CTA, in chunks of the line.  64 sequences of 500 to 8192 tokens took
 // 109 us without, 101 us with 4, 99 us with 8 to 16; 256 of 100 to 1000 110, 93, 83 and 82 us.
 constexpr int kPad = 12;
@@ -52,6 +56,18 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// Four codes of a word as fp16, in two pairs.  e4m3: the conversion instruction (bytes 0, 1 and 2, 3), true
+// values, NaN for a NaN code; faster here than codes_to_half by a tenth at D = 64 (there it is slower: the
+// packing of P takes the same unit).  int8: bytes 0, 2 and 1, 3.
+template <int KIND>
+__device__ __forceinline__ void pairs(uint32_t w, uint32_t& first, uint32_t& second) {
+  if (KIND == SAGE_KV_INT8)
+    codes_to_half<KIND>(w, first, second);
+  else
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(first), "=r"(second)
+        : "r"(w));
+}
 // transpose of an 8 x 8 block of 16-bit values held one row pair per lane
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
@@ -61,7 +77,7 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
 template <int D, int RT>
 struct Ring {
   static constexpr int kBytes = 2 * kChunk * D;  // K and V of a chunk; also 16 rows of D fp32
-  static constexpr int kWarpBytes = kStages<RT> * kBytes;
+  static constexpr int kWarpBytes = kStages<D, RT> * kBytes;
 };
 
 // A part of a unit: chunks [c0, c1) of a row tile of (batch row b, key/value head hk); `next`: where
@@ -72,12 +88,13 @@ struct FewSeg {
 };
 
 template <int D, int KIND, int RT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm<RT>)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
     kv_attn_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v) {
   constexpr int R = 8 * RT, NK = D / 16, NJ = D / 16;     // k-steps of S^T, 16-channel tiles of O^T
   constexpr int VB = D / 8;                               // bytes of a V piece (8 lanes cover a row)
-  constexpr int kPlaces = kStages<RT>;
+  constexpr int kPlaces = kStages<D, RT>;
+  constexpr bool kNan = KIND == SAGE_KV_E4M3;             // a byte may be NaN (what pairs() makes of int8 is finite)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   long long* pre = reinterpret_cast<long long*>(ring + kWarps * Ring<D, RT>::kWarpBytes);  // [B + 1] chunks before a batch row
@@ -305,10 +322,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<RT>)
       row_power(top, up, down);
 #pragma unroll
       for (int s = 0; s < NK; ++s) {
-        qf[t][s][0] = h2bits(__floats2half2_rn(x[s][0] * up, x[s][2] * up));
-        qf[t][s][1] = h2bits(__floats2half2_rn(x[s][1] * up, x[s][3] * up));
+        constexpr int k1 = KIND == SAGE_KV_INT8 ? 2 : 1, k2 = 3 - k1;  // (as pairs() gives the codes)
+        qf[t][s][0] = h2bits(__floats2half2_rn(x[s][0] * up, x[s][k1] * up));
+        qf[t][s][1] = h2bits(__floats2half2_rn(x[s][k2] * up, x[s][3] * up));
       }
-      const float a = p.alpha * down * kCodeUnit<KIND>;
+      const float a = p.alpha * down;
       // (a row that is not there holds q = 0 and masks nothing; it is not stored)
       const int end = live ? row_end(p, u.len, q_len, i) : u.len;
 #pragma unroll
@@ -360,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<RT>)
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t a0, a1, a2, a3;
-            codes_to_half<KIND>(wa[w], a0, a2);
-            codes_to_half<KIND>(wb[w], a1, a3);
+            pairs<KIND>(wa[w], a0, a2);
+            pairs<KIND>(wb[w], a1, a3);
 #pragma unroll
             for (int t = 0; t < RT; ++t)
               mma16816(s[h][t], a0, a1, a2, a3, qf[t][x * 4 + w][0], qf[t][x * 4 + w][1]);
@@ -369,7 +387,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<RT>)
         }
       }
       // softmax of the lane's tokens tk, tk + 8 of each row tile in rows 2 tig, 2 tig + 1
-      const bool edge = (ch + 1) * kChunk > lim_min;
+      bool edge = (ch + 1) * kChunk > lim_min;
+#pragma unroll
+      for (int h = 0; h < kSub; ++h) edge |= kNan && sc[h].y == -INFINITY;
       bool raise = false;
       float mx[RT][2];
 #pragma unroll
@@ -384,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<RT>)
             s[h][t][2 + e] = fmaf(s[h][t][2 + e], f, sc[h].y);
             if (edge) {
               const int j = ch * kChunk + h * 16 + tk;
-              if (j >= lim[t][e]) s[h][t][e] = -INFINITY;
-              if (j + 8 >= lim[t][e]) s[h][t][2 + e] = -INFINITY;
+              if (j >= lim[t][e] || (kNan && sc[h].y == -INFINITY)) s[h][t][e] = -INFINITY;
+              if (j + 8 >= lim[t][e] || (kNan && sc[h].y == -INFINITY)) s[h][t][2 + e] = -INFINITY;
             }
             mx[t][e] = max3(mx[t][e], s[h][t][e], s[h][t][2 + e]);
           }
@@ -448,13 +468,25 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<RT>)
             v[i][0] = x.x, v[i][1] = x.y;
           }
         }
+        if (kNan && edge) {  // what lies behind the keys may be anything, NaN among it: 0 x NaN must not enter
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = ch * kChunk + h * 16 + (i & 1 ? tv : 2 * tig) + (i >> 1) * 8;
+            if (j >= u.len || sc[h].y == -INFINITY) {
+#pragma unroll
+              for (int w = 0; w < VB / 4; ++w) v[i][w] = 0u;
+            }
+          }
+        }
 #pragma unroll
         for (int w = 0; w < VB / 4; ++w) {
           uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-          codes_to_half<KIND>(__byte_perm(v[0][w], v[1][w], 0x5410), a0, a1);
-          codes_to_half<KIND>(__byte_perm(v[2][w], v[3][w], 0x5410), a2, a3);
-          codes_to_half<KIND>(__byte_perm(v[0][w], v[1][w], 0x7632), b0, b1);
-          codes_to_half<KIND>(__byte_perm(v[2][w], v[3][w], 0x7632), b2, b3);
+          // the lane's two tokens at channels 4 w, 4 w + 1, then 4 w + 2, 4 w + 3
+          constexpr uint32_t k01 = KIND == SAGE_KV_INT8 ? 0x5410 : 0x5140, k23 = KIND == SAGE_KV_INT8 ? 0x7632 : 0x7362;
+          pairs<KIND>(__byte_perm(v[0][w], v[1][w], k01), a0, a1);
+          pairs<KIND>(__byte_perm(v[2][w], v[3][w], k01), a2, a3);
+          pairs<KIND>(__byte_perm(v[0][w], v[1][w], k23), b0, b1);
+          pairs<KIND>(__byte_perm(v[2][w], v[3][w], k23), b2, b3);
 #pragma unroll
           for (int t = 0; t < RT; ++t) {
             mma16816(acc[t][2 * w], a0, a1, a2, a3, pb[h][t][0], pb[h][t][1]);
@@ -505,8 +537,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<RT>)
                                                          left_place[w] * Ring<D, RT>::kBytes)[r * (D / 4) + (d ^ (r >> 1 & 3))];
         o[0] = fmaf(f, y.x, o[0]), o[1] = fmaf(f, y.y, o[1]), o[2] = fmaf(f, y.z, o[2]), o[3] = fmaf(f, y.w, o[3]);
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] *= kCodeUnit<KIND>;
       if (whole) {
         const float inv = ls > 0.f ? 1.f / ls : 0.f;
         const size_t orow = ((size_t)b * p.H + (size_t)u.hk * p.G + rw % p.G) * p.Nq + i;
@@ -626,7 +656,8 @@ void few_grid(AttnParams& p, int ctas) {
 }
 
 template <int D, int KIND, int RT>
-int launch_few(const AttnParams& p, cudaStream_t st) {
+int launch_few(AttnParams p, int sms, cudaStream_t st) {
+  few_grid(p, sms * kCtasPerSm<D, RT>);
   auto kern = kv_attn_kernel<D, KIND, RT>;
   // a page's rows [head, token]: boxes of a chunk's tokens
   const int box = p.c.page < kChunk ? p.c.page : kChunk;
@@ -642,8 +673,8 @@ int launch_few(const AttnParams& p, cudaStream_t st) {
   return launch_pdl(kern, dim3(p.most_parts), dim3(kThreads), smem, st, p, tk, tv) == cudaSuccess ? 0 : 3;
 }
 template <int D, int KIND>
-int launch_few(const AttnParams& p, int rows, cudaStream_t st) {
-  return rows == 8 ? launch_few<D, KIND, 1>(p, st) : launch_few<D, KIND, 2>(p, st);
+int launch_few(const AttnParams& p, int rows, int sms, cudaStream_t st) {
+  return rows == 8 ? launch_few<D, KIND, 1>(p, sms, st) : launch_few<D, KIND, 2>(p, sms, st);
 }
 
 // Query rows of a unit: 8 where all rows of a shared head fit in one, 16 up to kFewRows rows, then
@@ -652,13 +683,12 @@ constexpr long long kFewRows = 32;
 
 }  // namespace
 
-int launch_kv_few(AttnParams p, int kind, int rows, int sms, cudaStream_t st) {
-  few_grid(p, sms * (rows == 8 ? kCtasPerSm<1> : kCtasPerSm<2>));
+int launch_kv_few(const AttnParams& p, int kind, int rows, int sms, cudaStream_t st) {
   if (p.c.D == 128)
-    return kind == SAGE_KV_INT8 ? launch_few<128, SAGE_KV_INT8>(p, rows, st)
-                                : launch_few<128, SAGE_KV_E4M3>(p, rows, st);
-  return kind == SAGE_KV_INT8 ? launch_few<64, SAGE_KV_INT8>(p, rows, st)
-                              : launch_few<64, SAGE_KV_E4M3>(p, rows, st);
+    return kind == SAGE_KV_INT8 ? launch_few<128, SAGE_KV_INT8>(p, rows, sms, st)
+                                : launch_few<128, SAGE_KV_E4M3>(p, rows, sms, st);
+  return kind == SAGE_KV_INT8 ? launch_few<64, SAGE_KV_INT8>(p, rows, sms, st)
+                              : launch_few<64, SAGE_KV_E4M3>(p, rows, sms, st);
 }
 
 KvAttnWs kv_attn_ws_layout(int B, int H, int Hkv, int D, int Nq) {

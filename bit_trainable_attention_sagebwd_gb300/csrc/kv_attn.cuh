@@ -187,7 +187,7 @@ constexpr int kChunkRows = 256;        // query rows of a unit, many
 }  // namespace
 
 // the kernel of a few (up to 16) query rows a unit, and the one of kChunkRows
-int launch_kv_few(AttnParams p, int kind, int rows, int sms, cudaStream_t st);
+int launch_kv_few(const AttnParams& p, int kind, int rows, int sms, cudaStream_t st);
 int launch_kv_chunk(const AttnParams& p, int kind, int sms, cudaStream_t st);
 
 }  // namespace sage
