@@ -427,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       mbar_arrive(&sm.bar_q[t]);
       const int lim = live ? row_end(p, s.len, s.q_len, i) : s.len;
       float m = -INFINITY, l = 0.f, ref = 0.f;
+      bool careful = false;  // (of the warp)
       // lanes 0-7: the tile's eight 16-key groups; scales one tile ahead, pages two
       auto scales = [&](int id, float& ks, float& vs) {
         ks = 0.f, vs = 0.f;
@@ -459,11 +460,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         const int left = lim - c * kTile;
         // P of the row with the reference as it stands, in registers, and the largest u - m; where that
         // passes kRaise (a part's first tile, and seldom again) the reference is raised and P is
-        // computed once more from S
+        // computed once more from S.  The exponent is s f + (g - m), rounded once; past 2^18 that would
+        // no longer agree with the maximum that m was raised to, and it is (s f + g) - m, in the code of
+        // the edge tiles (`careful`).  A second raise is needed where the first one came from a maximum
+        // rounded against the old m; from then on top is exact (Sterbenz), and kTries is never reached.
+        constexpr int kTries = 3;
         uint32_t w[4][16];
         float top, sum_l, sub;
-        auto exponentials = [&](auto edge_tile) {
-          constexpr bool kEdge = decltype(edge_tile)::value;
+        auto exponentials = [&](auto careful_tile) {
+          constexpr bool kCareful = decltype(careful_tile)::value;
           top = -INFINITY, sum_l = 0.f;
           uint32_t sv[2][32];
           tmem_ld32(s_col, sv[0]);
@@ -474,18 +479,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
               const float f = __shfl_sync(0xffffffffu, ks, 2 * x + y) * a_row;
-              const float g = __shfl_sync(0xffffffffu, lg, 2 * x + y) - sub;
+              const float lgx = __shfl_sync(0xffffffffu, lg, 2 * x + y), g = lgx - sub;
               const uint64_t f2v = f2(f, f), g2v = f2(g, g);
               uint64_t sum = f2(0.f, 0.f);
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
+                const float s0 = __uint_as_float(sv[x & 1][y * 16 + e]), s1 = __uint_as_float(sv[x & 1][y * 16 + e + 1]);
                 float u0, u1;
-                f2split(
-                    ffma2(f2(__uint_as_float(sv[x & 1][y * 16 + e]), __uint_as_float(sv[x & 1][y * 16 + e + 1])), f2v, g2v),
-                    u0, u1);
-                if (kEdge) {
-                  if (x * 32 + y * 16 + e >= left) u0 = -INFINITY;
-                  if (x * 32 + y * 16 + e + 1 >= left) u1 = -INFINITY;
+                if (kCareful) {
+                  u0 = x * 32 + y * 16 + e >= left ? -INFINITY : __fsub_rn(__fmaf_rn(s0, f, lgx), sub);
+                  u1 = x * 32 + y * 16 + e + 1 >= left ? -INFINITY : __fsub_rn(__fmaf_rn(s1, f, lgx), sub);
+                } else {
+                  f2split(ffma2(f2(s0, s1), f2v, g2v), u0, u1);
                 }
                 top = max3(top, u0, u1);
                 u0 = ex2(u0), u1 = ex2(u1);
@@ -499,17 +504,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
           }
         };
 #pragma unroll 1
-        for (;;) {
+        for (int tries = 0;; ++tries) {
           sub = m == -INFINITY ? 0.f : m;
-          if (edge)
+          if (edge || careful)
             exponentials(std::true_type());
           else
             exponentials(std::false_type());
           const bool raise = top > (m == -INFINITY ? -INFINITY : kRaise);
-          if (!__any_sync(0xffffffffu, raise)) break;
+          if (!__any_sync(0xffffffffu, raise) || tries == kTries) break;
           const float to = raise ? top + sub - kBelow : m, corr = raise ? ex2(m - to) : 1.f;
           m = to;
           l *= corr;
+          careful = __any_sync(0xffffffffu, fabsf(m) > 0x1p18f && m != -INFINITY);
           if (c > s.c0) {  // (the part's first product overwrites O; PV of the tile before is done: S came after it)
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {

@@ -342,9 +342,9 @@ int sage_attn_kv_append(const sage_kv_cache *cache, const void *K, const void *V
 
 /*
  * Attention of queries over the cache.  Q: bf16 [B, H, Nq, D], query head h reads key/value head
- * h / (H / Hkv); O as Q, LSE fp32 [B, H, Nq].  Batch row b reads slot slots[b] (NULL: slot b; a slot may
- * be named by several rows); its first q_len[b] queries count (q_len int32 [B]; NULL: Nq), rows behind
- * them are neither read nor written.  With len = lengths[slot]: causal (causal != 0) lets query i see
+ * h / (H / Hkv); O as Q, LSE fp32 [B, H, Nq], all apart in memory.  Batch row b reads slot slots[b] (NULL:
+ * slot b; a slot may be named by several rows); its first q_len[b] queries count (q_len int32 [B], values
+ * outside 0 .. Nq count as the nearest; NULL: Nq), rows behind them are neither read nor written.  With len = lengths[slot]: causal (causal != 0) lets query i see
  * keys j <= len - q_len + i, as for the newest q_len tokens of the sequence; otherwise every query sees
  * all len keys (an encoder's states of another length).
  * S = sm_scale q . k, O = softmax(S) V, LSE = log sum e^S; a row that sees no key has O = 0 and
@@ -352,7 +352,8 @@ int sage_attn_kv_append(const sage_kv_cache *cache, const void *K, const void *V
  * largest are rounded); P is rounded to fp16 relative to the running maximum; everything else is fp32.
  * V scales below 2^-80 are read as 2^-80.  sm_scale <= 0 selects 1/sqrt(D).
  * ws: sage_attn_kv_ws_bytes(B, H, Hkv, D, Nq) bytes, 16-byte aligned, contents free before and after.
- * Deterministic.  B is at most 4096.
+ * Deterministic: the same call on the same state gives the same bits (another batch may cut the keys
+ * elsewhere and differ in the last ones).  B is at most 4096.
  */
 size_t sage_attn_kv_ws_bytes(int B, int H, int Hkv, int D, int Nq);
 int sage_attn_kv_attention(const sage_kv_cache *cache, const void *Q, const int *slots, const int *q_len, void *O,
@@ -460,7 +461,8 @@ int sage_attn_step_host(const void *Q, const void *K, const void *V, const void 
 /* Kernel timing for benchmarks.  While enabled (on != 0) the library brackets
  * each launch group with CUDA events recorded on the launching stream: "quantize"
  * (the two quantize kernels), "fwd", "bwd_pre" (D_i, LSE*log2e, dO codes),
- * "bwd_main" and "bwd_dq".  Costs two event records per group; off by default. */
+ * "bwd_main" and "bwd_dq"; of the cache calls "kv_append", "kv_attention", "kv_pages" (fork,
+ * extend, truncate) and "kv_compact".  Costs two event records per group; off by default. */
 int sage_attn_timer_enable(int on);
 
 /* Restrict the timing to the launch group `kernel` (one of the names above; NULL:

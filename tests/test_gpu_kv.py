@@ -234,6 +234,23 @@ def test_attention_sharp_and_wide_values(nq):
         check_attention(c, r, rng, 4, nq, sm_scale=sm_scale, q_scale=q_scale)
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_logits_past_fp32_resolution(nq, kind):
+    """Logits of 10^9 and more: which key wins is beyond fp32, but every output is a mean of values."""
+    rng = np.random.default_rng(13)
+    c, r = pair(20, 2, 128, 2, 10, 64, kind)
+    fill(c, r, rng, [300, 77])
+    q, _ = bf16(rng, (2, 4, nq, 128), 1e4)
+    for sm_scale in (1e3, 1e5, 1e8, 1e12, 1e20):
+        o, lse = sa.kv_attention(q, c, sm_scale=sm_scale)
+        torch.cuda.synchronize()
+        assert sa.get_status(c.status) == sa.SAGE_OK
+        most = max(np.abs(r.values(s, h)[1]).max() for s in range(2) for h in range(2))
+        assert torch.isfinite(o).all() and float(o.abs().max()) <= most * (1 + 2 ** -7)
+        assert torch.isfinite(lse).all()
+
+
 @pytest.mark.parametrize("nq", [1, 40])
 def test_attention_bad_numbers_are_reported(nq):
     """A length past the table, a slot and a page out of range: reported, nothing read out of range,

@@ -2,6 +2,7 @@
 launched, its workspaces have their sizes, the torch helpers check their tensors, and the numpy
 reference of the GPU tests is itself checked (rounding of the codes against torch's casts, a
 closed-form attention)."""
+import functools
 import ctypes
 
 import numpy as np
@@ -108,7 +109,7 @@ def test_workspace_sizes(lib):
 
 
 def test_helpers_check_their_tensors():
-    z = torch.zeros
+    z = functools.partial(torch.zeros, dtype=torch.float32)
     good = dict(k=z((4, 2, 64, 128), dtype=torch.int8), v=z((4, 2, 64, 128), dtype=torch.int8), k_scale=z((4, 2)),
                 v_scale=z((4, 2)), table=z((3, 5), dtype=torch.int32), lengths=z(3, dtype=torch.int32),
                 refs=z(4, dtype=torch.int32), status=z(1, dtype=torch.int32))
