@@ -460,13 +460,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         const int left = lim - c * kTile;
         // P of the row with the reference as it stands, in registers, and the largest u - m; where that
         // passes kRaise (a part's first tile, and seldom again) the reference is raised and P is
-        // computed once more from S.  The exponent is s f + (g - m), rounded once; past 2^18 that would
-        // no longer agree with the maximum that m was raised to, and it is (s f + g) - m, in the code of
-        // the edge tiles (`careful`).  A second raise is needed where the first one came from a maximum
-        // rounded against the old m; from then on top is exact (Sterbenz), and kTries is never reached.
-        constexpr int kTries = 3;
+        // computed once more from S.  The exponent is s f + (g - m), rounded once; where the reference
+        // would pass 2^18 that no longer agrees with the maximum it was raised to, and the rest of the
+        // part uses (s f + g) - m and the largest s f + g, in the code of the edge tiles (`careful`).
         uint32_t w[4][16];
-        float top, sum_l, sub;
+        float top, sum_l, sub;  // top: the largest u - m, careful: the largest u
         auto exponentials = [&](auto careful_tile) {
           constexpr bool kCareful = decltype(careful_tile)::value;
           top = -INFINITY, sum_l = 0.f;
@@ -486,13 +484,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
               for (int e = 0; e < 16; e += 2) {
                 const float s0 = __uint_as_float(sv[x & 1][y * 16 + e]), s1 = __uint_as_float(sv[x & 1][y * 16 + e + 1]);
                 float u0, u1;
+                f2split(ffma2(f2(s0, s1), f2v, kCareful ? f2(lgx, lgx) : g2v), u0, u1);
                 if (kCareful) {
-                  u0 = x * 32 + y * 16 + e >= left ? -INFINITY : __fsub_rn(__fmaf_rn(s0, f, lgx), sub);
-                  u1 = x * 32 + y * 16 + e + 1 >= left ? -INFINITY : __fsub_rn(__fmaf_rn(s1, f, lgx), sub);
-                } else {
-                  f2split(ffma2(f2(s0, s1), f2v, g2v), u0, u1);
+                  if (x * 32 + y * 16 + e >= left) u0 = -INFINITY;
+                  if (x * 32 + y * 16 + e + 1 >= left) u1 = -INFINITY;
                 }
                 top = max3(top, u0, u1);
+                if (kCareful) f2split(fadd2(f2(u0, u1), f2(-sub, -sub)), u0, u1);
                 u0 = ex2(u0), u1 = ex2(u1);
                 sum = fadd2(sum, f2(u0, u1));
                 w[x][y * 8 + (e >> 1)] = h2bits(__floats2half2_rn(u0, u1));
@@ -503,19 +501,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
             }
           }
         };
+        bool exact = edge || careful;
 #pragma unroll 1
-        for (int tries = 0;; ++tries) {
+        for (;;) {
           sub = m == -INFINITY ? 0.f : m;
-          if (edge || careful)
+          if (exact)
             exponentials(std::true_type());
           else
             exponentials(std::false_type());
-          const bool raise = top > (m == -INFINITY ? -INFINITY : kRaise);
-          if (!__any_sync(0xffffffffu, raise) || tries == kTries) break;
-          const float to = raise ? top + sub - kBelow : m, corr = raise ? ex2(m - to) : 1.f;
+          const bool raise = (exact ? top - sub : top) > (m == -INFINITY ? -INFINITY : kRaise);
+          if (!__any_sync(0xffffffffu, raise)) break;
+          const float to = raise ? (exact ? top : top + sub) - kBelow : m, corr = raise ? ex2(m - to) : 1.f;
+          if (!exact && __any_sync(0xffffffffu, raise && fabsf(to) > 0x1p18f)) {
+            careful = exact = true;
+            continue;
+          }
           m = to;
           l *= corr;
-          careful = __any_sync(0xffffffffu, fabsf(m) > 0x1p18f && m != -INFINITY);
+          careful = careful || __any_sync(0xffffffffu, raise && fabsf(to) > 0x1p18f);
           if (c > s.c0) {  // (the part's first product overwrites O; PV of the tile before is done: S came after it)
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {

@@ -11,6 +11,15 @@ import kv_ref
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def fp32_default():
+    """torch's default type as it is for a user: another module of the run may have changed it."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
 def dev(x, dtype=torch.int32):
     return torch.as_tensor(np.asarray(x)).to(dtype).cuda()
 
