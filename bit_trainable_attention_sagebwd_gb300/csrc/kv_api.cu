@@ -65,6 +65,7 @@ int sage_attn_kv_attention(const sage_kv_cache* cache, const void* Q, const int*
   if (!attention_shape_ok(B, H, cache->Hkv, cache->D, Nq)) return SAGE_ERR_UNSUPPORTED;
   if (slots == nullptr && B > cache->n_slots) return SAGE_ERR_INVALID_ARG;
   if (ws_bytes < sage::kv_attn_ws_layout(B, H, cache->Hkv, cache->D, Nq).total) return SAGE_ERR_INVALID_ARG;
+  if (O == Q) return SAGE_ERR_INVALID_ARG;
   return sage::launch_kv_attention(*cache, Q, slots, q_len, O, LSE, ws, B, H, Nq, causal != 0,
                                    sage::resolve_scale(sm_scale, cache->D), static_cast<cudaStream_t>(stream));
 }
@@ -78,6 +79,8 @@ int sage_attn_kv_fork(const sage_kv_cache* cache, const int* src, void* stream) 
 int sage_attn_kv_extend(const sage_kv_cache* cache, const int* n_new, int* pos, int* cow, void* stream) {
   if (int rc = check_cache(cache)) return rc;
   if (!aligned(n_new, 4) || !aligned(pos, 4) || !aligned(cow, 4)) return SAGE_ERR_INVALID_ARG;
+  // n_new is read after cow is written
+  if (n_new == pos || n_new == cow || pos == cow) return SAGE_ERR_INVALID_ARG;
   return sage::launch_kv_extend(*cache, n_new, pos, cow, static_cast<cudaStream_t>(stream));
 }
 

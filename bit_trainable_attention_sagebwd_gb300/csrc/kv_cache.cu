@@ -112,14 +112,15 @@ __global__ void __launch_bounds__(kAppendThreads<D, P>, 1024 / kAppendThreads<D,
   }
   const int pos = p.pos[slot], n = p.n_new[slot];
   if (pos < 0 || n <= 0) return;  // nothing new, or refused by sage_attn_kv_extend
-  const int j = pos / P + blockIdx.x, t0 = j * P;
-  if ((long long)t0 >= (long long)pos + n) return;
+  const int j = pos / P + blockIdx.x;
+  const long long t0 = (long long)j * P;
+  if (t0 >= (long long)pos + n) return;
   // the new tokens are on their way while the table is read
-  const int off = max(0, pos - t0);              // tokens of the page that are there already
-  const int end = min((long long)P, (long long)pos + n - t0);
+  const int off = (int)max(0ll, pos - t0);       // tokens of the page that are there already
+  const int end = (int)min((long long)P, pos - t0 + n);
   // token 0 of the page is token t0 - pos of the new ones
   const __nv_bfloat16* src =
-      (is_v ? p.V : p.K) + (((size_t)b * p.c.Hkv + hk) * p.Nn) * D + (ptrdiff_t)(t0 - pos) * D;
+      (is_v ? p.V : p.K) + (((size_t)b * p.c.Hkv + hk) * p.Nn) * D + (t0 - pos) * D;
   const int g = tid % TPR, r0 = tid / TPR;
   uint4 u[NP];
 #pragma unroll

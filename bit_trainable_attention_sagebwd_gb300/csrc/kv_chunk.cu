@@ -8,7 +8,7 @@
 //  - warps 17 and 18 bring the codes of K and V by TMA, half a tile at a time; warps 8-11 (K) and 12-15 (V)
 //    turn them into fp16 (exact) and store them where tcgen05.mma reads them (128-byte swizzle), two
 //    tiles deep;
-//  - one thread issues S = Q K^T and O += P V (kind::f16, fp32 accumulators in TMEM) for the two row
+//  - warp 16 issues S = Q K^T and O += P V (kind::f16, fp32 accumulators in TMEM) for the two row
 //    tiles in turn, so the tensor core works on one tile while the softmax works on the other;
 //  - warps 0-3 and 4-7 own a row tile each, a thread a row: S from TMEM, P back into TMEM over S's
 //    columns, from where the second product takes it.  The maximum is found with the exponentials,
@@ -118,39 +118,44 @@ __device__ __forceinline__ long long row_chunks(const AttnParams& p, int b) {
   return n * p.c.Hkv;
 }
 
-// A worker's way along the line: the parts from `at` to `stop`, in order.
+// A worker's way along the line: the parts from `at` to `stop`, in order.  It stands at the units of
+// row tile pair rt of batch row b, n tiles each, the first of them at `base`.
 struct Walk {
-  long long at, stop, base;  // base: tiles before batch row b
-  int b;
-  __device__ Walk(const long long* pre, int group, long long begin, long long end) : at(begin), stop(end), base(0), b(0) {
+  long long at, stop, base;
+  int b, rt, n, slot, len, q_len;
+  __device__ Walk(const AttnParams& p, const long long* pre, int group, long long begin, long long end)
+      : at(begin), stop(end), base(0), b(0) {
     if (begin >= end) return;
     const int g = row_at(pre, kGroups, begin);
     b = g * group;
     base = pre[g];
+    enter(p);
+  }
+  __device__ void enter(const AttnParams& p) {
+    len = row_length(p, b, slot);
+    q_len = row_queries(p, b);
+    rt = 0;
+    n = pair_chunks(p, len, q_len, 0);
   }
   __device__ bool more() const { return at < stop; }
   __device__ Seg next(const AttnParams& p) {
 #pragma unroll 1
-    for (long long n; at >= base + (n = row_chunks(p, b)); ++b) base += n;
-    Seg s;
-    s.b = b;
-    s.len = row_length(p, b, s.slot);
-    s.q_len = row_queries(p, b);
-    long long unit = base;
-    int n = 0, rt = 0;
-#pragma unroll 1
-    for (;; ++rt) {
-      n = pair_chunks(p, s.len, s.q_len, rt);
-      if (at < unit + (long long)n * p.c.Hkv) break;
-      unit += (long long)n * p.c.Hkv;
+    while (at >= base + (long long)n * p.c.Hkv) {
+      base += (long long)n * p.c.Hkv;
+      if (++rt < p.tiles) {
+        n = pair_chunks(p, len, q_len, rt);
+      } else {
+        ++b;
+        enter(p);
+      }
     }
-    s.rt = rt;
-    s.hk = (int)mul_div(at - unit, 1, n);
-    s.chunks = n;
-    s.unit_at = unit + (long long)s.hk * n;
+    Seg s;
+    s.b = b, s.slot = slot, s.len = len, s.q_len = q_len, s.rt = rt, s.chunks = n;
+    s.hk = (int)mul_div(at - base, 1, n);
+    s.unit_at = base + (long long)s.hk * n;
     s.c0 = (int)(at - s.unit_at);
     s.c1 = (int)min((long long)n, stop - s.unit_at);
-    s.two = (long long)rt * kChunkRows + kTile < (long long)s.q_len * p.G;
+    s.two = (long long)rt * kChunkRows + kTile < (long long)q_len * p.G;
     at = s.unit_at + s.c1;
     return s;
   }
@@ -290,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       // ---------------- the codes of K (warp 17) or V (18), half a tile at a time: a lane for each page
       const int v = warp - 17, box = p.c.page < kHalf ? p.c.page : kHalf, boxes = kHalf / box, box_bytes = box * D;
       const CUtensorMap* tm = v ? &tm_v : &tm_k;
-      Walk walk(sm.pre, group, begin, stop);
+      Walk walk(p, sm.pre, group, begin, stop);
       Seg s = walk.next(p);
       int c = 2 * s.c0;  // in half tiles
       auto page_of = [&](int half) {
@@ -379,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
     const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + kColO + t * 128;
     uint32_t n_s = 0, n_o = 0;
     bool ok = true;
-    Walk walk(sm.pre, group, begin, stop);
+    Walk walk(p, sm.pre, group, begin, stop);
     while (ok && walk.more()) {
       const Seg s = walk.next(p);
       const long long unit_id = ((long long)s.b * p.tiles + s.rt) * p.c.Hkv + s.hk;

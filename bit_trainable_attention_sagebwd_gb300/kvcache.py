@@ -84,6 +84,8 @@ def _call(fn, cache, stream, *args):
     device's current stream."""
     import torch
     index = cache.device.index
+    if stream is not None and stream.device != cache.device:
+        raise ValueError(f"stream: on {stream.device}, the cache is on {cache.device}")
     if torch._C._cuda_getDevice() == index:
         # (the raw handle: torch.cuda.current_stream() alone costs more than a launch)
         s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
@@ -94,6 +96,14 @@ def _call(fn, cache, stream, *args):
             rc = getattr(cache._lib, fn)(*args, s)
     if rc:
         raise SageError(fn, rc)
+
+
+def _used_on(stream, *tensors):
+    """Tensors that a helper allocated on the current stream and that `stream` works on: their memory is not
+    given to others before it is done."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
 
 
 def _slot_array(t, name, cache):
@@ -145,12 +155,15 @@ def kv_attention(q, cache, causal=True, slots=None, q_len=None, sm_scale=None, o
     dev = cache.device
     if ws is None:
         ws = alloc_kv_ws(cache, B, H, Nq)
+        _used_on(stream, ws)
     elif ws.device != dev:
         raise ValueError(f"ws: on {ws.device}, the cache is on {dev}")
     if o is None:
         o = torch.empty_like(q)
+        _used_on(stream, o)
     if lse is None:
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+        _used_on(stream, lse)
     shape = (B, H, Nq, cache.d)
     _call("sage_attn_kv_attention", cache, stream, cache._ref, _arg(q, "q", torch.bfloat16, shape, dev),
           _rows(slots, B, cache), None if q_len is None else _arg(q_len, "q_len", cache._i32, (B,), dev),
@@ -169,8 +182,12 @@ def kv_extend(cache, n_new, pos=None, cow=None, stream=None):
     where the slot could not be served).  cow, if given, receives the shared page that the slot's last
     page was copied from, or -1."""
     import torch
-    pos = torch.empty_like(n_new) if pos is None else pos
-    cow = torch.empty_like(n_new) if cow is None else cow
+    if pos is None:
+        pos = torch.empty_like(n_new)
+        _used_on(stream, pos)
+    if cow is None:
+        cow = torch.empty_like(n_new)
+        _used_on(stream, cow)
     _call("sage_attn_kv_extend", cache, stream, cache._ref, _slot_array(n_new, "n_new", cache),
           _slot_array(pos, "pos", cache), _slot_array(cow, "cow", cache))
     return pos
@@ -194,6 +211,7 @@ def kv_compact(cache, to, ws=None, stream=None):
         raise ValueError(f"to: on {to.device}, the cache is on {cache.device}")
     if ws is None:
         ws = alloc_kv_compact_ws(cache)
+        _used_on(stream, ws)
     elif ws.device != cache.device:
         raise ValueError(f"ws: on {ws.device}, the cache is on {cache.device}")
     _call("sage_attn_kv_compact", cache, stream, cache._ref, to._ref, ws.data_ptr(), ws.nbytes)

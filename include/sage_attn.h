@@ -371,7 +371,7 @@ int sage_attn_kv_attention(const sage_kv_cache *cache, const void *Q, const int 
  *    filled and listed by another slot too is first copied to a page of the slot's own; cow[s] = the page
  *    it was copied from (else -1).  Slots are served while the needs of the slots up to them fit in the
  *    free pages; one that is not served has pos[s] = -1 and is otherwise left alone
- *    (SAGE_ERR_NO_PAGES; past max_pages pages: SAGE_ERR_INVALID_ARG).
+ *    (SAGE_ERR_NO_PAGES; past max_pages pages: SAGE_ERR_INVALID_ARG).  n_new, pos and cow are apart.
  *  - truncate: slot s with keep[s] >= 0 keeps its first min(keep[s], lengths[s]) tokens and gives the
  *    pages behind them back (refs - 1); keep[s] = 0 frees the slot.
  *  - compact: the live pages of `cache` (refs > 0), in order, become pages 0, 1, ... of the pool `to`;

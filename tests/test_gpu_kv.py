@@ -177,6 +177,7 @@ def test_append_leaves_out_what_it_must_not_write():
     refused([0, 0, 0, 0], [5, 0, 0, 0])                      # more tokens than K and V hold
     refused([2 ** 31 - 8, 0, 0, 0], [4, 0, 0, 0])
     refused([8, 0, 0, 0], [0, 0, 0, 0], [4, -1, 1, 0])       # slots that are not there
+    refused([2 ** 31 - 2, 0, 0, 0], [4, 0, 0, 0])            # tokens on both sides of 2^31
     sa.kv_fork(c, dev([-1, -1, 0, -1]))                      # slots 0 and 2 share a page
     r.fork([-1, -1, 0, -1])
     refused([8, 0, 0, 0], [2, 0, 0, 0])
@@ -258,6 +259,47 @@ def test_attention_logits_past_fp32_resolution(nq, kind):
         most = max(np.abs(r.values(s, h)[1]).max() for s in range(2) for h in range(2))
         assert torch.isfinite(o).all() and float(o.abs().max()) <= most * (1 + 2 ** -7)
         assert torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("e", [8, 22, 34, 60])
+@pytest.mark.parametrize("nq", [1, 40])
+def test_attention_far_keys_before_near_ones(nq, e):
+    """The first pages' logits lie at -2^(e + 3): the near keys behind them get their weights as if the
+    far ones were not there."""
+    rng = np.random.default_rng(e)
+    far, n, d = 3, 570, 128
+    c, r = pair(12, 1, d, 1, 10, 64, "int8")
+    k = rng.standard_normal((1, 1, n, d)).astype(np.float32)
+    k[:, :, :far * 64] = -np.abs(k[:, :, :far * 64])
+    k = torch.from_numpy(k).to(torch.bfloat16)
+    v, vf = bf16(rng, (1, 1, n, d))
+    pos = sa.kv_extend(c, dev([n]))
+    rpos, _ = r.extend([n])
+    sa.kv_append(c, k.cuda(), v, pos, dev([n]))
+    r.append(k.float().numpy(), vf, rpos, [n])
+    same_state(c, r)
+    q = torch.from_numpy(np.abs(rng.standard_normal((1, 2, nq, d))).astype(np.float32)).to(torch.bfloat16)
+    qf = q.double().numpy()
+    c.k_scale[:far] *= 2.0 ** e
+    r.k_scale[:far] = 0.0
+    near = r.attention(qf)[4]                 # max sum |q k| of the keys that count
+    r.k_scale[:far] = c.k_scale[:far].cpu().numpy() * np.float32(2.0 ** (8 - e))   # e^-1000 is 0 as well
+    o, lse, pv, av, mag, rows = r.attention(qf)
+    assert mag.min() > 1000.0
+    got = sa.kv_attention(q.cuda(), c)
+    torch.cuda.synchronize()
+    assert sa.get_status(c.status) == sa.SAGE_OK
+    compare(*got, (o, lse, pv, av, near, rows), n, d)
+
+
+@pytest.mark.parametrize("d,kind", [(64, "int8"), (128, "e4m3")])
+def test_attention_many_tiles_of_queries(d, kind):
+    """Several 256-row units of each batch row, among rows with few or no queries, over short sequences."""
+    rng = np.random.default_rng(d)
+    c, r = pair(40, 2, d, 4, 10, 64, kind)
+    fill(c, r, rng, [333, 0, 129, 64])
+    check_attention(c, r, rng, 6, 600, True, [0, 2, 1, 3, 0], [600, 1, 599, 0, 86])
+    check_attention(c, r, rng, 6, 600, False, [3, 2], [300, 600])
 
 
 @pytest.mark.parametrize("nq", [1, 40])
@@ -514,6 +556,48 @@ def test_serving_run_in_graphs_and_streams():
     r.compact(r2)
     same_state(c2, r2)
     check_attention(c2, r2, rng, H, 5, q_len=[5, 3, 1, 5, 5, 5])
+
+
+def test_helpers_on_a_given_stream(monkeypatch):
+    """What a helper allocates for a call on another stream is not given away while that stream still
+    has to use it."""
+    from bit_trainable_attention_sagebwd_gb300 import kvcache
+    rng = np.random.default_rng(2)
+    c, r = pair(20, 2, 64, 3, 8, 32, "int8")
+    k, kf = bf16(rng, (3, 2, 50, 64))
+    q, qf = bf16(rng, (3, 4, 1, 64))
+    n = dev([50, 7, 0])
+    held = []
+
+    def kept(alloc):
+        def call(*args):
+            t = alloc(*args)
+            held.append((t.data_ptr(), t.nbytes))
+            return t
+        return call
+    monkeypatch.setattr(kvcache, "alloc_kv_ws", kept(kvcache.alloc_kv_ws))
+    monkeypatch.setattr(kvcache, "alloc_kv_compact_ws", kept(kvcache.alloc_kv_compact_ws))
+    to = sa.kv_cache(30, 2, 64, 3, 8, page=32)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(200_000_000)        # about 0.1 s
+    pos = sa.kv_extend(c, n, stream=stream)
+    sa.kv_append(c, k, k, pos, n, stream=stream)
+    o, lse = sa.kv_attention(q, c, stream=stream)
+    sa.kv_compact(c, to, stream=stream)
+    assert not stream.query()
+    assert len(held) == 2
+    for ptr, size in held:
+        later = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        assert all(t.data_ptr() != ptr for t in later)
+    stream.synchronize()
+    rpos, _ = r.extend([50, 7, 0])
+    r.append(kf, kf, rpos, [50, 7, 0])
+    same_state(c, r)
+    assert np.array_equal(pos.cpu().numpy(), rpos)
+    compare(o, lse, r.attention(qf.astype(np.float64)), 50, 64)
+    assert torch.equal(to.lengths, c.lengths)
 
 
 def test_prompt_in_chunks_equals_prompt_at_once():

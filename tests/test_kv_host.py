@@ -88,6 +88,10 @@ def test_bad_arguments_are_refused(lib):
         for name in names:
             for bad in (None, odd):
                 assert c[call](**{name: bad}) == sa.SAGE_ERR_INVALID_ARG
+    a, b = FAKE + 0x1000, FAKE + 0x2000
+    for over in (dict(n_new=a, pos=a, cow=b), dict(n_new=a, pos=b, cow=a), dict(n_new=a, pos=b, cow=b)):
+        assert c["extend"](**over) == sa.SAGE_ERR_INVALID_ARG
+    assert c["attention"](O=FAKE, Q=FAKE) == sa.SAGE_ERR_INVALID_ARG
     assert c["compact"](ws=None) == sa.SAGE_ERR_INVALID_ARG
     assert c["compact"](ws_bytes=sa.sage_attn_kv_compact_ws_bytes(8) - 1) == sa.SAGE_ERR_INVALID_ARG
     assert calls(cache(), to=cache())["compact"]() == sa.SAGE_ERR_INVALID_ARG  # into itself
