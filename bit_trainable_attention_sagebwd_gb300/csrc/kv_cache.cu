@@ -46,10 +46,10 @@ __device__ __forceinline__ Quant quant_of(float s) {
 }
 // Codes of four values x = -z: the int8 code is the low byte of RN(x / s) + 1.5 2^23 (|x / s| is at most
 // 127 (1 + 2^-22): nothing to saturate)
-template <int KIND>
+template <int KIND, bool FAST>
 __device__ __forceinline__ uint32_t codes4(float z0, float z1, float z2, float z3, const Quant& q) {
   float y[4];
-  if (q.fast) {
+  if (FAST) {
     const uint64_t a = f2(z0, z1), b = f2(z2, z3);
     const uint64_t qa = fmul2(a, q.ninv2), qb = fmul2(b, q.ninv2);
     f2split(ffma2(ffma2(qa, q.s2, a), q.ninv2, qa), y[0], y[1]);
@@ -69,9 +69,9 @@ __device__ __forceinline__ uint32_t codes4(float z0, float z1, float z2, float z
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
   return lo | hi << 16;
 }
-template <int KIND>
+template <int KIND, bool FAST>
 __device__ __forceinline__ uint2 codes8(const float (&z)[8], const Quant& q) {
-  return make_uint2(codes4<KIND>(z[0], z[1], z[2], z[3], q), codes4<KIND>(z[4], z[5], z[6], z[7], q));
+  return make_uint2(codes4<KIND, FAST>(z[0], z[1], z[2], z[3], q), codes4<KIND, FAST>(z[4], z[5], z[6], z[7], q));
 }
 // the negated values of eight codes
 template <int KIND>
@@ -199,18 +199,30 @@ __global__ void __launch_bounds__(kAppendThreads<D, P>, 1024 / kAppendThreads<D,
   const float fresh = __fmul_rn(top, KIND == SAGE_KV_INT8 ? 1.f / 127.f : 1.f / 448.f);
   const float now = fmaxf(was, fresh);
   const Quant q = quant_of(now);
+  uint2* dst = reinterpret_cast<uint2*>(codes) + g;  // of token 0; a token is TPR of them
+  float z[8];
+  if (q.fast) {
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int r = r0 + i * RPP;
-    uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)r * D) + g;
-    if (r >= off && r < end) {
-      float z[8];
-      negated(u[i], z);
-      *dst = codes8<KIND>(z, q);
-    } else if (r < off && now != was) {  // the page's scale grew: what the old codes stand for, under the new one
-      float z[8];
-      negated8<KIND>(*dst, was, z);
-      *dst = codes8<KIND>(z, q);
+    for (int i = 0; i < NP; ++i) {
+      const int r = r0 + i * RPP;
+      if (r >= off && r < end) {
+        negated(u[i], z);
+        dst[r * TPR] = codes8<KIND, true>(z, q);
+      }
+    }
+  } else {  // (kept apart and short: the instructions of a page's one pass are fetched, not found)
+#pragma unroll 1
+    for (int r = r0; r < end; r += RPP) {
+      if (r < off) continue;
+      negated(reinterpret_cast<const uint4*>(src + (ptrdiff_t)r * D)[g], z);
+      dst[r * TPR] = codes8<KIND, false>(z, q);
+    }
+  }
+  if (now != was) {  // the page's scale grew: what the old codes stand for, under the new one
+#pragma unroll 1
+    for (int r = r0; r < off; r += RPP) {
+      negated8<KIND>(dst[r * TPR], was, z);
+      dst[r * TPR] = q.fast ? codes8<KIND, true>(z, q) : codes8<KIND, false>(z, q);
     }
   }
   if (tid == 0) *scale = now;
