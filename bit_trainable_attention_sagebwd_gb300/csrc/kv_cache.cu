@@ -21,9 +21,12 @@ __device__ __forceinline__ void kv_error(int* status, int code) { atomicMax(stat
 
 // ------------------------------------------------------------------------------ append
 
-// 64 values a thread, at 64 registers: 1024 threads an SM with 128 KB of new tokens on their way
-template <int D, int P>
-constexpr int kAppendThreads = D * P / 64 < 64 ? 64 : D * P / 64;
+// Threads of a page and head: 64 values each, at 64 registers (1024 threads an SM with 128 KB of new
+// tokens on their way), a warp at least.  A CTA is a page's threads, two pages' where they are a warp: with
+// a CTA of two warps for a 16-token page two prompts of 20k-32k tokens took 70 us, so 54 us; two
+// pages of two warps each (32 tokens of D = 128) take 65 us against 54 us, whatever barrier joins them.
+__host__ __device__ constexpr int append_threads(int D, int P) { return D * P / 64 < 32 ? 32 : D * P / 64; }
+__host__ __device__ constexpr int append_pages(int D, int P) { return append_threads(D, P) < 64 ? 2 : 1; }
 
 // What a block's scale s brings to its codes.  RN(x / s) by Markstein's correction (P. Markstein,
 // Computation of elementary functions on the IBM RISC System/6000 processor, 1990): inv = RN(1 / s),
@@ -93,31 +96,31 @@ struct AppendParams {
   int B, Nn;
 };
 
-// One CTA per (page that the new tokens of a batch row can touch, key/value head, K or V).  A
+// One group of threads per (page that the new tokens of a batch row can touch, key/value head, K or V).  A
 // thread holds its eight channels of up to eight tokens in registers between the maximum and the
-// codes, so the new tokens are read once.
-template <int D, int P, int KIND>
-__global__ void __launch_bounds__(kAppendThreads<D, P>, 1024 / kAppendThreads<D, P>) kv_append_kernel(const AppendParams p) {
-  constexpr int kThreads = kAppendThreads<D, P>;
+// codes, so the new tokens are read once.  SHIFT: k_shift is given.
+template <int D, int P, int KIND, bool SHIFT>
+__global__ void __launch_bounds__(append_threads(D, P) * append_pages(D, P), 1024 / (append_threads(D, P) * append_pages(D, P)))
+    kv_append_kernel(const AppendParams p) {
+  constexpr int kThreads = append_threads(D, P), kPages = append_pages(D, P);
   constexpr int TPR = D / 8, RPP = kThreads / TPR, NP = P / RPP;  // threads a token, tokens a pass, passes
   static_assert(P % RPP == 0, "a page is a whole number of passes");
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.z, hk = blockIdx.y >> 1, tid = threadIdx.x;
+  const int b = blockIdx.z, hk = blockIdx.y >> 1, group = threadIdx.x / kThreads, tid = threadIdx.x % kThreads;
   const bool is_v = blockIdx.y & 1;
   const int slot = p.slots ? p.slots[b] : b;
   if ((unsigned)slot >= (unsigned)p.c.n_slots) {
-    if (tid == 0) kv_error(p.c.status, kDevIndex);
+    if (threadIdx.x == 0) kv_error(p.c.status, kDevIndex);
     return;
   }
   const int pos = p.pos[slot], n = p.n_new[slot];
   if (pos < 0 || n <= 0) return;  // nothing new, or refused by sage_attn_kv_extend
-  const int j = pos / P + blockIdx.x;
+  const int j = pos / P + blockIdx.x * kPages + group;
   const long long t0 = (long long)j * P;
-  if (t0 >= (long long)pos + n) return;
   // the new tokens are on their way while the table is read
   const int off = (int)max(0ll, pos - t0);       // tokens of the page that are there already
-  const int end = (int)min((long long)P, pos - t0 + n);
+  const int end = (int)max(0ll, min((long long)P, pos - t0 + n));  // 0: the page is behind them
   // token 0 of the page is token t0 - pos of the new ones
   const __nv_bfloat16* src =
       (is_v ? p.V : p.K) + (((size_t)b * p.c.Hkv + hk) * p.Nn) * D + (t0 - pos) * D;
@@ -131,12 +134,13 @@ __global__ void __launch_bounds__(kAppendThreads<D, P>, 1024 / kAppendThreads<D,
   // a batch row that names a slot again is left out
   if (p.slots) {
     bool again = false;
-    for (int i = tid; i < b; i += kThreads) again |= p.slots[i] == slot;
+    for (int i = threadIdx.x; i < b; i += kThreads * kPages) again |= p.slots[i] == slot;
     if (__syncthreads_or(again)) {
-      if (tid == 0) kv_error(p.c.status, kDevIndex);
+      if (threadIdx.x == 0) kv_error(p.c.status, kDevIndex);
       return;
     }
   }
+  if (end == 0) return;
   const int page = n <= p.Nn && j < p.c.max_pages ? p.c.table[(size_t)slot * p.c.max_pages + j] : -1;
   // a page that is not reserved, or that another slot lists too, is not written
   if ((unsigned)page >= (unsigned)p.c.n_pages || p.c.refs[page] != 1) {
@@ -147,7 +151,7 @@ __global__ void __launch_bounds__(kAppendThreads<D, P>, 1024 / kAppendThreads<D,
   float* scale = (is_v ? p.c.v_scale : p.c.k_scale) + block;
   uint8_t* codes = static_cast<uint8_t*>(is_v ? p.c.v : p.c.k) + block * P * D;
   const float was = off > 0 ? *scale : 0.f;
-  const bool shifted = !is_v && p.shift;
+  const bool shifted = SHIFT && !is_v;
   float sh[8] = {};
   if (shifted) {
     const float4* s4 = reinterpret_cast<const float4*>(p.shift + hk * D + g * 8);
@@ -191,11 +195,14 @@ __global__ void __launch_bounds__(kAppendThreads<D, P>, 1024 / kAppendThreads<D,
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  __shared__ float wtop[kThreads / 32];
-  if ((tid & 31) == 0) wtop[tid >> 5] = top;
-  __syncthreads();
+  if (kThreads > 32) {
+    static_assert(kThreads == 32 || kPages == 1, "a page's threads are a warp or the CTA");
+    __shared__ float wtop[kThreads / 32];
+    if ((tid & 31) == 0) wtop[tid >> 5] = top;
+    __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, wtop[i]);
+    for (int i = 0; i < kThreads / 32; ++i) top = fmaxf(top, wtop[i]);
+  }
   const float fresh = __fmul_rn(top, KIND == SAGE_KV_INT8 ? 1.f / 127.f : 1.f / 448.f);
   const float now = fmaxf(was, fresh);
   const Quant q = quant_of(now);
@@ -229,14 +236,17 @@ __global__ void __launch_bounds__(kAppendThreads<D, P>, 1024 / kAppendThreads<D,
 }
 
 template <int D, int P>
-auto append_kernel_for(int kind) {
-  return kind == SAGE_KV_INT8 ? kv_append_kernel<D, P, SAGE_KV_INT8> : kv_append_kernel<D, P, SAGE_KV_E4M3>;
+auto append_kernel_for(int kind, bool shift) {
+  return kind == SAGE_KV_INT8
+             ? (shift ? kv_append_kernel<D, P, SAGE_KV_INT8, true> : kv_append_kernel<D, P, SAGE_KV_INT8, false>)
+             : (shift ? kv_append_kernel<D, P, SAGE_KV_E4M3, true> : kv_append_kernel<D, P, SAGE_KV_E4M3, false>);
 }
 template <int D>
-auto append_kernel_for(int page, int kind) {
-  return page == 16 ? append_kernel_for<D, 16>(kind)
-                    : page == 32 ? append_kernel_for<D, 32>(kind)
-                                 : page == 64 ? append_kernel_for<D, 64>(kind) : append_kernel_for<D, 128>(kind);
+auto append_kernel_for(int page, int kind, bool shift) {
+  return page == 16   ? append_kernel_for<D, 16>(kind, shift)
+         : page == 32 ? append_kernel_for<D, 32>(kind, shift)
+         : page == 64 ? append_kernel_for<D, 64>(kind, shift)
+                      : append_kernel_for<D, 128>(kind, shift);
 }
 
 // ------------------------------------------------------------------------------ pages
@@ -542,11 +552,12 @@ int launch_kv_append(const sage_kv_cache& c, const void* K, const void* V, const
                      const int* pos, const int* n_new, int B, int Nn, cudaStream_t st) {
   AppendParams p{c, static_cast<const __nv_bfloat16*>(K), static_cast<const __nv_bfloat16*>(V), k_shift, slots, pos,
                  n_new, B, Nn};
-  auto kern = c.D == 128 ? append_kernel_for<128>(c.page, c.kind) : append_kernel_for<64>(c.page, c.kind);
+  const bool shift = k_shift != nullptr;
+  auto kern = c.D == 128 ? append_kernel_for<128>(c.page, c.kind, shift) : append_kernel_for<64>(c.page, c.kind, shift);
   const unsigned pages = (unsigned)(((long long)Nn + c.page - 2) / c.page + 1);  // that Nn tokens can touch
-  const int threads = c.D * c.page / 64 < 64 ? 64 : c.D * c.page / 64;  // kAppendThreads
+  const int threads = append_threads(c.D, c.page), group = append_pages(c.D, c.page);
   ScopedTimer timer("kv_append", st);
-  if (launch_pdl(kern, dim3(pages, 2 * c.Hkv, B), dim3(threads), 0, st, p) != cudaSuccess) return 3;
+  if (launch_pdl(kern, dim3((pages + group - 1) / group, 2 * c.Hkv, B), dim3(threads * group), 0, st, p) != cudaSuccess) return 3;
   return cudaGetLastError() == cudaSuccess ? 0 : 3;
 }
 
