@@ -266,18 +266,15 @@ __device__ __forceinline__ T block_exclusive(T v, T* warp_sums, T* total) {
   __syncthreads();  // the last call's sums have been read
   if (lane == 31) warp_sums[w] = s;
   __syncthreads();
-  if (w == 0) {
-    T x = warp_sums[lane];
+  T x = warp_sums[lane];  // (every warp for itself: one barrier less)
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const T t = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += t;
-    }
-    warp_sums[lane] = x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const T t = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += t;
   }
-  __syncthreads();
-  *total = warp_sums[31];
-  return s - v + (w ? warp_sums[w - 1] : 0);
+  *total = __shfl_sync(0xffffffffu, x, 31);
+  const T before = __shfl_sync(0xffffffffu, x, w ? w - 1 : 0);
+  return s - v + (w ? before : 0);
 }
 
 // One CTA per slot that takes over another slot's pages.
@@ -372,13 +369,33 @@ __global__ void __launch_bounds__(kScanThreads) kv_extend_kernel(const sage_kv_c
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x;
+  // refs of the thread's pages of a step, on their way a step ahead (a step changes only its own pages)
+  int4 ahead[kPer / 4];
+  auto fetch = [&](int p0) {
+    const long long first = (long long)p0 + tid * kPer;
+#pragma unroll
+    for (int i = 0; i < kPer / 4; ++i) {
+      const long long at = first + 4 * i;
+      ahead[i] = make_int4(1, 1, 1, 1);
+      if (at + 4 <= c.n_pages) {
+        ahead[i] = *reinterpret_cast<const int4*>(c.refs + at);
+      } else {
+        if (at < c.n_pages) ahead[i].x = c.refs[at];
+        if (at + 1 < c.n_pages) ahead[i].y = c.refs[at + 1];
+        if (at + 2 < c.n_pages) ahead[i].z = c.refs[at + 2];
+      }
+    }
+  };
+  fetch(0);
   int carry = 0;
+  int len0 = 0, n0 = 0, from0 = -1;  // of slot tid
   for (int s0 = 0; s0 < c.n_slots; s0 += kScanThreads) {
     const int s = s0 + tid;
     int need = 0;
     if (s < c.n_slots) {
       const Need q = slot_need(c, n_new, s);
       need = q.count();
+      if (s0 == 0) len0 = q.len, n0 = q.n, from0 = q.last;
       cow[s] = q.last;
       first_page[s] = q.bad ? -1 : q.have - (q.last >= 0);
       if (q.bad) kv_error(c.status, kDevIndex);
@@ -396,26 +413,26 @@ __global__ void __launch_bounds__(kScanThreads) kv_extend_kernel(const sage_kv_c
   for (int p0 = 0; p0 < c.n_pages && found < carry; p0 += kScanThreads * kPer) {
     const int first = p0 + tid * kPer;
     unsigned free = 0;
-    if (first + kPer <= c.n_pages) {
 #pragma unroll
-      for (int i = 0; i < kPer / 4; ++i) {
-        const int4 r = reinterpret_cast<const int4*>(c.refs + first)[i];
-        free |= (unsigned)(r.x == 0) << (4 * i) | (unsigned)(r.y == 0) << (4 * i + 1) |
-                (unsigned)(r.z == 0) << (4 * i + 2) | (unsigned)(r.w == 0) << (4 * i + 3);
-      }
-    } else {
-      for (int i = 0; i < kPer; ++i)
-        if (first + i < c.n_pages && c.refs[first + i] == 0) free |= 1u << i;
+    for (int i = 0; i < kPer / 4; ++i) {
+      const int4 r = ahead[i];
+      free |= (unsigned)(r.x == 0) << (4 * i) | (unsigned)(r.y == 0) << (4 * i + 1) |
+              (unsigned)(r.z == 0) << (4 * i + 2) | (unsigned)(r.w == 0) << (4 * i + 3);
     }
+    fetch(p0 + kScanThreads * kPer);
     int total;
     int r = found + block_exclusive(__popc(free), warp_sums, &total);
+    int lo = 0;
     for (; free && r < carry; free &= free - 1, ++r) {
       const int page = first + __ffs(free) - 1;
-      int lo = 0, hi = c.n_slots;  // the slot with excl[lo] <= r < excl[lo + 1]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (excl[mid] <= r) lo = mid;
-        else hi = mid;
+      // the slot with excl[lo] <= r < excl[lo + 1]: often that of the page before or the next one
+      if (excl[lo + 1] <= r && excl[++lo + 1] <= r) {
+        int hi = c.n_slots;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (excl[mid] <= r) lo = mid;
+          else hi = mid;
+        }
       }
       c.table[(size_t)lo * c.max_pages + first_page[lo] + r - excl[lo]] = page;
       c.refs[page] = 1;
@@ -424,7 +441,8 @@ __global__ void __launch_bounds__(kScanThreads) kv_extend_kernel(const sage_kv_c
   }
   __syncthreads();
   for (int s = tid; s < c.n_slots; s += kScanThreads) {
-    const int n = n_new[s], len = c.lengths[s], from = cow[s];
+    const bool kept = s == tid;
+    const int n = kept ? n0 : n_new[s], len = kept ? len0 : c.lengths[s], from = kept ? from0 : cow[s];
     const int need = excl[s + 1] - excl[s], begin = first_page[s];  // (need: 0 where the sums stand at 2^30)
     const bool nothing = ((long long)len + n + c.page - 1) / c.page == begin && from < 0;
     if (begin >= 0 && (nothing || excl[s + 1] <= found)) {
@@ -468,9 +486,17 @@ __global__ void __launch_bounds__(256) kv_cow_kernel(const sage_kv_cache c, cons
   if (from < 0) return;
   const int to = c.table[(size_t)s * c.max_pages + pos[s] / c.page];
   const size_t bytes = (size_t)c.Hkv * c.page * c.D;
-  const size_t t = blockIdx.y * 256 + threadIdx.x, n = kCowParts * 256;
-  copy16(static_cast<uint8_t*>(c.k) + to * bytes, static_cast<const uint8_t*>(c.k) + from * bytes, bytes, t, n);
-  copy16(static_cast<uint8_t*>(c.v) + to * bytes, static_cast<const uint8_t*>(c.v) + from * bytes, bytes, t, n);
+  const size_t t = blockIdx.y * 256 + threadIdx.x, n = kCowParts * 256, m = bytes / 16;
+  const uint4 *kf = static_cast<const uint4*>(c.k) + from * m, *vf = static_cast<const uint4*>(c.v) + from * m;
+  uint4 *kt = static_cast<uint4*>(c.k) + to * m, *vt = static_cast<uint4*>(c.v) + to * m;
+  for (size_t i = t; i < m; i += 2 * n) {
+    const bool two = i + n < m;
+    const uint4 a = kf[i], b = vf[i];
+    uint4 x, y;
+    if (two) x = kf[i + n], y = vf[i + n];
+    kt[i] = a, vt[i] = b;
+    if (two) kt[i + n] = x, vt[i + n] = y;
+  }
   for (size_t h = t; h < (size_t)c.Hkv; h += n) {
     c.k_scale[(size_t)to * c.Hkv + h] = c.k_scale[(size_t)from * c.Hkv + h];
     c.v_scale[(size_t)to * c.Hkv + h] = c.v_scale[(size_t)from * c.Hkv + h];
@@ -576,8 +602,10 @@ int launch_kv_truncate(const sage_kv_cache& c, const int* keep, cudaStream_t st)
 int launch_kv_extend(const sage_kv_cache& c, const int* n_new, int* pos, int* cow, cudaStream_t st) {
   ScopedTimer timer("kv_pages", st);
   const size_t smem = (2 * (size_t)c.n_slots + 1) * 4;  // at most 64 KB (kKvMaxSlots)
-  if (cudaFuncSetAttribute(kv_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-      launch_pdl(kv_extend_kernel, dim3(1), dim3(kScanThreads), smem, st, c, n_new, pos, cow) != cudaSuccess ||
+  if (smem > 40 * 1024 &&  // (48 KB with the static part need no leave)
+      cudaFuncSetAttribute(kv_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return 3;
+  if (launch_pdl(kv_extend_kernel, dim3(1), dim3(kScanThreads), smem, st, c, n_new, pos, cow) != cudaSuccess ||
       launch_pdl(kv_cow_kernel, dim3(c.n_slots, kCowParts), dim3(256), 0, st, c, (const int*)pos, (const int*)cow) !=
           cudaSuccess)
     return 3;
