@@ -33,22 +33,27 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kTile = 128, kHalf = 64;       // keys of a tile (and of half of one), rows of a row tile
 constexpr int kGroups = 128;                 // the batch rows in at most so many groups
-constexpr int kRegsSoftmax = 160, kRegsLoad = 56, kRegsIssue = 48;
+constexpr int kRegsSoftmax = 144, kRegsLoad = 64, kRegsIssue = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsLoad + kRegsIssue <= 5 * 96, "the launch's registers");
 constexpr uint32_t kCols = 512, kColO = 256; // TMEM: S of row tile t at 128 t, O at 256 + 128 t
+
+// half tiles of codes on their way or being converted, for K and for V: what fits
+template <int D>
+constexpr int kRaw = D == 64 ? 4 : 2;
 
 template <int D>
 struct ChunkSmem {
   uint8_t q[2][kTile * D * 2];
   uint8_t k[2][kTile * D * 2];
   uint8_t v[2][kTile * D * 2];
-  uint8_t raw[2][kTile * D];  // codes of a K and a V tile
-  uint64_t bar_q[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_raw[2][2], bar_raw_empty[2][2], bar_s[2], bar_p[2], bar_o[2];
+  uint8_t raw[2][kRaw<D>][kHalf * D];  // codes of K and V
+  uint64_t bar_half, bar_joined;  // turns: the second group's part of the rows is there, has been read
+  uint64_t bar_q[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_raw[2][kRaw<D>], bar_raw_empty[2][kRaw<D>], bar_s[2], bar_p[2], bar_o[2];
   long long wsum[kThreads / 32];
   long long pre[kGroups + 1];  // tiles before each group of batch rows
   uint32_t tmem_base;
   int abort;
-  int seg[2];                  // for the MMA issuer: 2 x tiles of a part + (it has two row tiles), 0: no more
+  int seg[2];                  // for the MMA issuer: 4 x tiles of a part + its Mode, 0: no more
 };
 static_assert(sizeof(ChunkSmem<128>) + 1024 <= 227 * 1024, "shared memory of a CTA");
 
@@ -101,9 +106,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 // A part of a unit: key tiles [c0, c1) of row tile pair rt of (batch row b, key/value head hk).
+// How the two row tiles' places (operands, TMEM, softmax groups) are used in a part: kOne: the first one
+// alone; kTwo: a row tile each, the same key tiles; kTurns: the one row tile in both, the key tiles in
+// turns, joined at the part's end.  (Twelve queries of each of 4 heads on 16 sequences of 900 to 16k tokens: 139 us
+// with the first place alone.)
+enum Mode { kOne, kTwo, kTurns };
 struct Seg {
   int b, slot, hk, rt, len, q_len, c0, c1, chunks;
-  bool two;  // the second row tile has rows
+  Mode mode;
   long long unit_at;
 };
 
@@ -161,7 +171,7 @@ struct Walk {
     s.unit_at = base + (long long)s.hk * n;
     s.c0 = (int)(at - s.unit_at);
     s.c1 = (int)min((long long)n, stop - s.unit_at);
-    s.two = (long long)rt * kChunkRows + kTile < (long long)q_len * p.G;
+    s.mode = (long long)rt * kChunkRows + kTile < (long long)q_len * p.G ? kTwo : s.c1 - s.c0 > 1 ? kTurns : kOne;
     at = s.unit_at + s.c1;
     return s;
   }
@@ -182,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       mbar_init(&sm.bar_k_empty[s], 1);
       mbar_init(&sm.bar_v_full[s], 128);
       mbar_init(&sm.bar_v_empty[s], 1);
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kRaw<D>; ++h) {
         mbar_init(&sm.bar_raw[s][h], 1);
         mbar_init(&sm.bar_raw_empty[s][h], 128);
       }
@@ -190,6 +200,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       mbar_init(&sm.bar_p[s], 128);
       mbar_init(&sm.bar_o[s], 1);
     }
+    mbar_init(&sm.bar_half, 128);
+    mbar_init(&sm.bar_joined, 128);
     sm.abort = 0;
     fence_mbar_init();
   }
@@ -254,11 +266,49 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort)); };
       bool ok = true;
       while (ok) {
-        // a part: its tiles and whether the second row tile has rows, said with the first one's Q
+        // a part: its tiles and mode, said with the first row tile's Q
         if (!wait(&sm.bar_q[0], ns[0] & 1)) break;
-        const int said = *const_cast<volatile int*>(&sm.seg[ns[0] & 1]), n = said >> 1;
-        const bool two = said & 1;
+        const int said = *const_cast<volatile int*>(&sm.seg[ns[0] & 1]), n = said >> 2;
+        const bool two = (said & 3) == kTwo;
         if (n == 0) break;
+        if ((said & 3) == kTurns) {
+          ok = wait(&sm.bar_q[1], ns[1] & 1);
+          auto first = [&](int t) {
+            ok = ok && wait(&sm.bar_k_full[(kc + t) & 1], ((kc + t) >> 1) & 1);
+            if (!ok) return;
+            tc_fence_after();
+            issue_s(t, kc + t);
+            commit(&sm.bar_k_empty[(kc + t) & 1]);
+          };
+          // P V of key tile kc, which is place t's, then S of the place's next one
+          auto turn = [&](int t, int j) {
+            ok = ok && wait(&sm.bar_v_full[kc & 1], (kc >> 1) & 1) && wait(&sm.bar_p[t], np[t] & 1);
+            if (!ok) return;
+            ++np[t];
+            tc_fence_after();
+            issue_pv(t, kc, j > 1);
+            commit(&sm.bar_v_empty[kc & 1]);
+            if (j + 2 >= n) {
+              commit(&sm.bar_o[t]);
+            } else {
+              ok = wait(&sm.bar_k_full[kc & 1], ((kc + 2) >> 1) & 1);
+              if (!ok) return;
+              tc_fence_after();
+              issue_s(t, kc + 2);
+              commit(&sm.bar_k_empty[kc & 1]);
+            }
+            ++kc;
+          };
+          first(0);
+          first(1);
+          for (int j = 0; ok && j < n; j += 2) {
+            turn(0, j);
+            if (ok && j + 1 < n) turn(1, j + 1);
+          }
+          ++ns[0];
+          ++ns[1];
+          continue;
+        }
         ok = (!two || wait(&sm.bar_q[1], ns[1] & 1)) && wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -315,8 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         const bool ok = (unsigned)id < (unsigned)p.c.n_pages;
         if (!ok && id != -1) atomicMax(p.c.status, kDevIndex);
         const uint32_t all = __ballot_sync(0xffffffffu, ok);
-        uint64_t* full = &sm.bar_raw[v][n & 1];
-        if (!__all_sync(0xffffffffu, n < 2 || mbar_wait(&sm.bar_raw_empty[v][n & 1], ((n >> 1) - 1) & 1, abort))) break;
+        const uint32_t at = n % kRaw<D>;
+        uint64_t* full = &sm.bar_raw[v][at];
+        if (!__all_sync(0xffffffffu, n < kRaw<D> || mbar_wait(&sm.bar_raw_empty[v][at], (n / kRaw<D> - 1) & 1, abort))) break;
         if (lane == 0) {
           if (all)
             mbar_arrive_expect_tx(full, __popc(all) * box_bytes);
@@ -325,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         }
         __syncwarp();
         if (ok)
-          tma_load_3d(sm.raw[v] + (n & 1) * kHalf * D + lane * box_bytes, tm, 0,
+          tma_load_3d(sm.raw[v][at] + lane * box_bytes, tm, 0,
                       s.hk * p.c.page + ((c * kHalf + lane * box) & (p.c.page - 1)), id, full);
         if (++c < 2 * s.c1) {
           id = id_next;
@@ -341,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         id_next = c + 1 < 2 * s.c1 ? page_of(c + 1) : -1;
       }
       // the last copies (after a wait that ran out nobody else waits for them)
-      for (uint32_t k = n < 2 ? 0 : n - 2; k < n; ++k) {
+      for (uint32_t k = n < kRaw<D> ? 0 : n - kRaw<D>; k < n; ++k) {
         int give_up = 0;
-        mbar_wait(&sm.bar_raw[v][k & 1], (k >> 1) & 1, &give_up);
+        mbar_wait(&sm.bar_raw[v][k % kRaw<D>], (k / kRaw<D>) & 1, &give_up);
       }
     }
   } else if (warp >= 8) {
@@ -361,11 +412,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       bool ok = true;
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        ok = ok && mbar_wait(&sm.bar_raw[v][h], kc & 1, abort);
+        const uint32_t half = 2 * kc + h, at = half % kRaw<D>;
+        ok = ok && mbar_wait(&sm.bar_raw[v][at], (half / kRaw<D>) & 1, abort);
 #pragma unroll 2  // (instruction fetch is shared: unrolled in full the kernel took a tenth longer)
-        for (int i = h * (kRows / 2); i < (h + 1) * (kRows / 2); ++i) {
-          const uint4 y = *reinterpret_cast<const uint4*>(sm.raw[v] + (i * 128 + lt) * 16);
-          const int r = r0 + i * kRowStep, u = (piece * 2) & 7;
+        for (int i = 0; i < kRows / 2; ++i) {
+          const uint4 y = *reinterpret_cast<const uint4*>(sm.raw[v][at] + (i * 128 + lt) * 16);
+          const int r = h * kHalf + r0 + i * kRowStep, u = (piece * 2) & 7;
           uint4 lo, hi;
           codes_to_half<KIND>(y.x, lo.x, lo.y);
           codes_to_half<KIND>(y.y, lo.z, lo.w);
@@ -376,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
           *reinterpret_cast<uint4*>(row + (((u + swap) ^ (r & 7)) << 4)) = swap ? hi : lo;
           *reinterpret_cast<uint4*>(row + (((u + !swap) ^ (r & 7)) << 4)) = swap ? lo : hi;
         }
-        mbar_arrive(&sm.bar_raw_empty[v][h]);
+        mbar_arrive(&sm.bar_raw_empty[v][at]);
       }
       if (!ok) break;
       fence_proxy_async_smem();
@@ -388,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + kColO + t * 128;
-    uint32_t n_s = 0, n_o = 0;
+    uint32_t n_s = 0, n_o = 0, n_turns = 0;
     bool ok = true;
     Walk walk(p, sm.pre, group, begin, stop);
     while (ok && walk.more()) {
@@ -396,8 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       const long long unit_id = ((long long)s.b * p.tiles + s.rt) * p.c.Hkv + s.hk;
       if (s.c0 == 0 && tid == 0)
         p.info[unit_id] = make_int2(w0, line.holder(s.unit_at + s.chunks - 1));
-      if (t == 1 && !s.two) continue;
-      const long long row = (long long)s.rt * kChunkRows + t * kTile + r;
+      if (t == 1 && s.mode == kOne) continue;
+      const bool turns = s.mode == kTurns;
+      const long long row = (long long)s.rt * kChunkRows + (turns ? 0 : t * kTile) + r;
       const int i = (int)(row / p.G);
       const bool live = i < s.q_len;
       const size_t orow =
@@ -434,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         }
       }
       fence_proxy_async_smem();
-      if (tid == 0) sm.seg[n_o & 1] = 2 * (s.c1 - s.c0) + s.two;
+      if (tid == 0) sm.seg[n_o & 1] = 4 * (s.c1 - s.c0) + s.mode;
       mbar_arrive(&sm.bar_q[t]);
       const int lim = live ? row_end(p, s.len, s.q_len, i) : s.len;
       float m = -INFINITY, l = 0.f, ref = 0.f;
@@ -449,13 +502,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       };
       auto id_at = [&](int c) { return lane < 8 && c < s.c1 ? page_of(s.slot, s.len, c * 8 + lane) : -1; };
       float ks, vs, ks_n, vs_n;
-      int id = id_at(s.c0);
+      const int c0 = s.c0 + (turns ? t : 0), step = turns ? 2 : 1;
+      int id = id_at(c0);
       scales(id, ks, vs);
-      id = id_at(s.c0 + 1);
+      id = id_at(c0 + step);
 #pragma unroll 1
-      for (int c = s.c0; c < s.c1; ++c) {
+      for (int c = c0; c < s.c1; c += step) {
         scales(id, ks_n, vs_n);
-        id = id_at(c + 2);
+        id = id_at(c + 2 * step);
         // the groups' factors of S, log2 of V's scale and its inverse
         if (lane < 8) ref = fmaxf(ref, vs);
         if (__any_sync(0xffffffffu, lane < 8 && !(vs > 0.f))) {
@@ -530,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
           m = to;
           l *= corr;
           careful = careful || __any_sync(0xffffffffu, raise && fabsf(to) > 0x1p18f);
-          if (c > s.c0) {  // (the part's first product overwrites O; PV of the tile before is done: S came after it)
+          if (c > c0) {  // (the part's first product overwrites O; PV of the tile before is done: S came after it)
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
               uint32_t o[32];
@@ -554,6 +608,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       ok = ok && mbar_wait(&sm.bar_o[t], n_o & 1, abort);
       ++n_o;
       tc_fence_after();
+      // turns: both places hold a part of the same rows, thread r of both groups the same row in the same
+      // TMEM lanes: the first group takes both
+      float2* half = reinterpret_cast<float2*>(sm.q[1]);  // (the second place's S are done with Q)
+      float f0 = 1.f, f1 = 0.f;
+      if (turns && t == 1) {
+        half[r] = make_float2(m, l);
+        tc_fence_before();
+        mbar_arrive(&sm.bar_half);
+        ok = ok && mbar_wait(&sm.bar_joined, n_turns & 1, abort);
+        ++n_turns;
+        tc_fence_after();
+        continue;
+      }
+      if (turns) {
+        ok = ok && mbar_wait(&sm.bar_half, n_turns & 1, abort);
+        ++n_turns;
+        tc_fence_after();
+        const float2 x = half[r];
+        const float mt = fmaxf(m, x.x), sub = mt == -INFINITY ? 0.f : mt;
+        f0 = ex2(m - sub), f1 = ex2(x.x - sub);
+        l = l * f0 + x.y * f1;
+        m = mt;
+      }
       const bool whole = s.c0 == 0 && s.c1 == s.chunks;
       float* part = p.part + (size_t)(2 * w0 + (s.c0 == 0 ? 1 : 0)) * kChunkRows * (D + 2);
       const float f = whole ? (l > 0.f ? kCodeUnit<KIND> / l : 0.f) : kCodeUnit<KIND>;
@@ -563,6 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         uint32_t o[32];
         tmem_ld32(o_col + d, o);
         tmem_wait32(o);
+        if (turns) {
+          uint32_t y[32];
+          tmem_ld32(o_col + 128 + d, y);
+          tmem_wait32(y);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            o[e] = __float_as_uint(fmaf(__uint_as_float(y[e]), f1, __uint_as_float(o[e]) * f0));
+        }
         if (!(ok && live)) continue;
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
@@ -583,6 +668,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
             *reinterpret_cast<uint4*>(part + (size_t)pr * D + d + 4 * e) =
                 make_uint4(o[4 * e], o[4 * e + 2], o[4 * e + 1], o[4 * e + 3]);
         }
+      }
+      if (turns) {
+        tc_fence_before();
+        mbar_arrive(&sm.bar_joined);
       }
       if (ok && live) {
         if (whole)
