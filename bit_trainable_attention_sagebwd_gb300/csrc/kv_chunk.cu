@@ -348,22 +348,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       }
     }
     if ((warp == 17 || warp == 18) && begin < stop) {
-      // ---------------- the codes of K (warp 17) or V (18), half a tile at a time: a lane for each page
+      // ---------------- the codes of K (warp 17) or V (18), half a tile at a time: a lane for each page.  The
+      // pages' numbers come in windows of 32 boxes, the next window's a window ahead: a load for each half
+      // tile would hold the copies up.
       const int v = warp - 17, box = p.c.page < kHalf ? p.c.page : kHalf, boxes = kHalf / box, box_bytes = box * D;
       const CUtensorMap* tm = v ? &tm_v : &tm_k;
       Walk walk(p, sm.pre, group, begin, stop);
       Seg s = walk.next(p);
       int c = 2 * s.c0;  // in half tiles
-      auto page_of = [&](int half) {
-        const int token = half * kHalf + lane * box;
-        return lane < boxes && token < s.len ? p.c.table[(size_t)s.slot * p.c.max_pages + token / p.c.page] : -1;
+      const int box_shift = 31 - __clz(boxes), page_shift = 31 - __clz(p.c.page), per = 32 >> box_shift;
+      auto window = [&](int half) {
+        const int at = half + (lane >> box_shift), token = at * kHalf + (lane & (boxes - 1)) * box;
+        return at < 2 * s.c1 && token < s.len ? p.c.table[(size_t)s.slot * p.c.max_pages + (token >> page_shift)] : -1;
       };
-      int id = page_of(c), id_next = page_of(c + 1);
+      int here = 0, ids = window(c), ids_next = window(c + per);  // here: half tiles of the window so far
       uint32_t n = 0;  // half tiles so far
       for (;; ++n) {
         // (what lies behind the keys stays as it was: finite, and masked)
-        const bool ok = (unsigned)id < (unsigned)p.c.n_pages;
-        if (!ok && id != -1) atomicMax(p.c.status, kDevIndex);
+        const int id = __shfl_sync(0xffffffffu, ids, ((here << box_shift) + lane) & 31);
+        const bool ok = lane < boxes && (unsigned)id < (unsigned)p.c.n_pages;
+        if (!ok && lane < boxes && id != -1) atomicMax(p.c.status, kDevIndex);
         const uint32_t all = __ballot_sync(0xffffffffu, ok);
         const uint32_t at = n % kRaw<D>;
         uint64_t* full = &sm.bar_raw[v][at];
@@ -379,7 +383,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
           tma_load_3d(sm.raw[v][at] + lane * box_bytes, tm, 0,
                       s.hk * p.c.page + ((c * kHalf + lane * box) & (p.c.page - 1)), id, full);
         if (++c < 2 * s.c1) {
-          id = id_next;
+          if (++here == per) {
+            here = 0;
+            ids = ids_next;
+            ids_next = window(c + per);
+          }
         } else {
           if (!walk.more()) {
             ++n;
@@ -387,9 +395,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
           }
           s = walk.next(p);
           c = 2 * s.c0;
-          id = page_of(c);
+          here = 0;
+          ids = window(c);
+          ids_next = window(c + per);
         }
-        id_next = c + 1 < 2 * s.c1 ? page_of(c + 1) : -1;
       }
       // the last copies (after a wait that ran out nobody else waits for them)
       for (uint32_t k = n < kRaw<D> ? 0 : n - kRaw<D>; k < n; ++k) {
