@@ -685,8 +685,10 @@ int launch_few(const AttnParams& p, int rows, int sms, cudaStream_t st) {
   return rows == 8 ? launch_few<D, KIND, 1>(p, sms, st) : launch_few<D, KIND, 2>(p, sms, st);
 }
 
-// Query rows of a unit: 8 where all rows of a shared head fit in one, 16 up to kFewRows rows, then
-// the tensor-core kernel's 256.
+// Query rows of a unit: 8 where all rows of a shared head fit in one, 16 up to kFewRows rows, then the
+// tensor-core kernel's 256.  16 sequences of 900 to 16k tokens, 4 query heads to each of 8, D = 128, this
+// kernel against that one: 16 rows 62 us against 130 us, 32 rows 112 against 130, 48 rows 162 against 129;
+// D = 64: 32 rows 77 against 94, 48 rows 110 against 95.
 constexpr long long kFewRows = 32;
 
 }  // namespace

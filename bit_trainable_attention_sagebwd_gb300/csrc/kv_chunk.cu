@@ -4,7 +4,7 @@
 // The products are what counts here: 4 D operations for every (query row, key) pair against
 // 2 D bytes for every key that 256 rows share.  One CTA an SM takes units of 256 rows (two tiles of
 // 128: the queries of the G heads of a key/value head, token by token) and walks the unit's
-// 128-key tiles:
+// 128-key tiles; a unit of one row tile takes its key tiles in turns (Mode):
 //  - warps 17 and 18 bring the codes of K and V by TMA, half a tile at a time; warps 8-11 (K) and 12-15 (V)
 //    turn them into fp16 (exact) and store them where tcgen05.mma reads them (128-byte swizzle), two
 //    tiles deep;
@@ -108,8 +108,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 // A part of a unit: key tiles [c0, c1) of row tile pair rt of (batch row b, key/value head hk).
 // How the two row tiles' places (operands, TMEM, softmax groups) are used in a part: kOne: the first one
 // alone; kTwo: a row tile each, the same key tiles; kTurns: the one row tile in both, the key tiles in
-// turns, joined at the part's end.  (Twelve queries of each of 4 heads on 16 sequences of 900 to 16k tokens: 139 us
-// with the first place alone.)
+// turns, joined at the part's end.  (48 rows on 4 sequences of 100k to 131k tokens, 8 heads of D = 128: 334 us,
+// with the first place alone 376 us.)
 enum Mode { kOne, kTwo, kTurns };
 struct Seg {
   int b, slot, hk, rt, len, q_len, c0, c1, chunks;
