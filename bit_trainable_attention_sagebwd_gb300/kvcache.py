@@ -60,7 +60,10 @@ class KVCache:
                                self.n_pages, self.hkv, self.page, self.d, self.n_slots, self.max_pages,
                                _KINDS[self.kind])
         self._ref = ctypes.byref(self.c)
-        self._slots_shape, self._i32, self._lib = (self.n_slots,), i32, lib()
+        self._slots_shape, self._lib = (self.n_slots,), lib()
+        self._i32, self._f32, self._bf16 = i32, f32, torch.bfloat16
+        # (the raw handle: torch.cuda.current_stream() alone costs more than a launch)
+        self._index, self._device_now, self._stream_of = dev.index, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def kv_cache(n_pages, hkv, d, n_slots, max_pages, page=64, kind="int8", device="cuda") -> KVCache:
@@ -82,20 +85,17 @@ def kv_cache(n_pages, hkv, d, n_slots, max_pages, page=64, kind="int8", device="
 def _call(fn, cache, stream, *args):
     """fn(*args, stream) with the cache's device current and, unless a stream is given, on that
     device's current stream."""
-    import torch
-    index = cache.device.index
-    if stream is not None and stream.device != cache.device:
-        raise ValueError(f"stream: on {stream.device}, the cache is on {cache.device}")
-    if torch._C._cuda_getDevice() == index:
-        # (the raw handle: torch.cuda.current_stream() alone costs more than a launch)
-        s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-        rc = getattr(cache._lib, fn)(*args, s)
+    index = cache._index
+    if stream is None and cache._device_now() == index:
+        rc = fn(*args, cache._stream_of(index))
     else:
+        import torch
+        if stream is not None and stream.device != cache.device:
+            raise ValueError(f"stream: on {stream.device}, the cache is on {cache.device}")
         with torch.cuda.device(index):
-            s = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-            rc = getattr(cache._lib, fn)(*args, s)
+            rc = fn(*args, cache._stream_of(index) if stream is None else stream.cuda_stream)
     if rc:
-        raise SageError(fn, rc)
+        raise SageError(fn.__name__, rc)
 
 
 def _used_on(stream, *tensors):
@@ -123,14 +123,13 @@ def kv_append(cache, k, v, pos, n_new, slots=None, k_shift=None, stream=None):
     """Quantize the first n_new[s] tokens of bf16 k, v [B, Hkv, Nn, D] into the pages of their slots from
     position pos[s] (int32 [n_slots], as kv_extend gives it).  slots: int32 [B], the slot of each batch row
     (None: row b is slot b); k_shift: fp32 [Hkv, D], subtracted from every key (K-smoothing)."""
-    import torch
     if k.dim() != 4:
         raise ValueError("k, v: [B, Hkv, Nn, D] expected")
     b, _, nn, _ = k.shape
     shape, dev = (b, cache.hkv, nn, cache.d), cache.device
-    _call("sage_attn_kv_append", cache, stream, cache._ref, _arg(k, "k", torch.bfloat16, shape, dev),
-          _arg(v, "v", torch.bfloat16, shape, dev),
-          None if k_shift is None else _arg(k_shift, "k_shift", torch.float32, (cache.hkv, cache.d), dev),
+    _call(cache._lib.sage_attn_kv_append, cache, stream, cache._ref, _arg(k, "k", cache._bf16, shape, dev),
+          _arg(v, "v", cache._bf16, shape, dev),
+          None if k_shift is None else _arg(k_shift, "k_shift", cache._f32, (cache.hkv, cache.d), dev),
           _rows(slots, b, cache), _slot_array(pos, "pos", cache), _slot_array(n_new, "n_new", cache), b, nn)
 
 
@@ -165,7 +164,7 @@ def kv_attention(q, cache, causal=True, slots=None, q_len=None, sm_scale=None, o
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
         _used_on(stream, lse)
     shape = (B, H, Nq, cache.d)
-    _call("sage_attn_kv_attention", cache, stream, cache._ref, _arg(q, "q", torch.bfloat16, shape, dev),
+    _call(cache._lib.sage_attn_kv_attention, cache, stream, cache._ref, _arg(q, "q", torch.bfloat16, shape, dev),
           _rows(slots, B, cache), None if q_len is None else _arg(q_len, "q_len", cache._i32, (B,), dev),
           _arg(o, "o", torch.bfloat16, shape, dev), _arg(lse, "lse", torch.float32, (B, H, Nq), dev), ws.data_ptr(),
           ws.nbytes, B, H, Nq, int(causal), 0.0 if sm_scale is None else float(sm_scale))
@@ -174,7 +173,7 @@ def kv_attention(q, cache, causal=True, slots=None, q_len=None, sm_scale=None, o
 
 def kv_fork(cache, src, stream=None):
     """Slot s with src[s] >= 0 (int32 [n_slots]) takes over the tokens of slot src[s]; pages are shared."""
-    _call("sage_attn_kv_fork", cache, stream, cache._ref, _slot_array(src, "src", cache))
+    _call(cache._lib.sage_attn_kv_fork, cache, stream, cache._ref, _slot_array(src, "src", cache))
 
 
 def kv_extend(cache, n_new, pos=None, cow=None, stream=None):
@@ -188,14 +187,14 @@ def kv_extend(cache, n_new, pos=None, cow=None, stream=None):
     if cow is None:
         cow = torch.empty_like(n_new)
         _used_on(stream, cow)
-    _call("sage_attn_kv_extend", cache, stream, cache._ref, _slot_array(n_new, "n_new", cache),
+    _call(cache._lib.sage_attn_kv_extend, cache, stream, cache._ref, _slot_array(n_new, "n_new", cache),
           _slot_array(pos, "pos", cache), _slot_array(cow, "cow", cache))
     return pos
 
 
 def kv_truncate(cache, keep, stream=None):
     """Slot s with keep[s] >= 0 (int32 [n_slots]) keeps its first keep[s] tokens (0: the slot is freed)."""
-    _call("sage_attn_kv_truncate", cache, stream, cache._ref, _slot_array(keep, "keep", cache))
+    _call(cache._lib.sage_attn_kv_truncate, cache, stream, cache._ref, _slot_array(keep, "keep", cache))
 
 
 def alloc_kv_compact_ws(cache):
@@ -214,4 +213,4 @@ def kv_compact(cache, to, ws=None, stream=None):
         _used_on(stream, ws)
     elif ws.device != cache.device:
         raise ValueError(f"ws: on {ws.device}, the cache is on {cache.device}")
-    _call("sage_attn_kv_compact", cache, stream, cache._ref, to._ref, ws.data_ptr(), ws.nbytes)
+    _call(cache._lib.sage_attn_kv_compact, cache, stream, cache._ref, to._ref, ws.data_ptr(), ws.nbytes)
