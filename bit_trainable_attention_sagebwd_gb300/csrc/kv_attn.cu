@@ -690,6 +690,10 @@ int launch_few(const AttnParams& p, int rows, int sms, cudaStream_t st) {
 // kernel against that one: 16 rows 62 us against 130 us, 32 rows 112 against 130, 48 rows 162 against 129;
 // D = 64: 32 rows 77 against 94, 48 rows 110 against 95.
 constexpr long long kFewRows = 32;
+// The join takes a CTA for each row below so many units (each may be cut into many parts: 16 units with 16
+// rows 12.1 us in all against 12.9 us), a warp for each row from there (64 units 11.0 us against 12.0 us, 512
+// units 15.0 us against 15.7 us).
+constexpr unsigned kFewUnits = 64;
 
 }  // namespace
 
@@ -743,9 +747,11 @@ int launch_kv_attention(const sage_kv_cache& c, const void* Q, const int* slots,
   const long long rows = (long long)p.G * Nq;
   const unsigned unit_rows = (unsigned)(rows < L.rows ? rows : L.rows);
   const unsigned units = (unsigned)((long long)B * c.Hkv * L.tiles);
-  auto join = many ? (c.D == 128 ? kv_join_kernel<128, 1> : kv_join_kernel<64, 1>)
-                   : (c.D == 128 ? kv_join_kernel<128, 4> : kv_join_kernel<64, 4>);
-  if (launch_pdl(join, dim3(units, many ? L.rows / 4 : unit_rows), dim3(128), 0, st, p, L.rows) != cudaSuccess) return 3;
+  const bool warp_rows = many || units >= kFewUnits;
+  auto join = warp_rows ? (c.D == 128 ? kv_join_kernel<128, 1> : kv_join_kernel<64, 1>)
+                        : (c.D == 128 ? kv_join_kernel<128, 4> : kv_join_kernel<64, 4>);
+  const unsigned y = warp_rows ? (unit_rows + 3) / 4 : unit_rows;
+  if (launch_pdl(join, dim3(units, y), dim3(128), 0, st, p, L.rows) != cudaSuccess) return 3;
   return cudaGetLastError() == cudaSuccess ? 0 : 3;
 }
 
