@@ -292,6 +292,19 @@ def test_attention_far_keys_before_near_ones(nq, e):
     compare(*got, (o, lse, pv, av, near, rows), n, d)
 
 
+@pytest.mark.parametrize("g,nq", [(1, 33), (4, 9), (8, 12), (1, 128)])
+@pytest.mark.parametrize("page,d,kind", [(16, 64, "e4m3"), (64, 128, "int8"), (128, 128, "e4m3")])
+def test_attention_one_row_tile(page, d, kind, g, nq):
+    """33 to 128 query rows of a shared head: their key tiles are taken in turns.  Lengths of nothing, one, odd
+    and even numbers of 128-key tiles, and one that is cut over many CTAs."""
+    rng = np.random.default_rng(page + g + nq)
+    lengths = [0, 1, 127, 128, 129, 256, 257, 385, 4501]
+    c, r = pair(6000 // page + 40, 2, d, len(lengths), 4608 // page + 1, page, kind)
+    fill(c, r, rng, lengths)
+    check_attention(c, r, rng, 2 * g, nq, True, None, [nq, 1, nq, 0, nq - 1, nq, nq, nq // 2, nq])
+    check_attention(c, r, rng, 2 * g, nq, False, [8, 4])
+
+
 @pytest.mark.parametrize("d,kind", [(64, "int8"), (128, "e4m3")])
 def test_attention_many_tiles_of_queries(d, kind):
     """Several 256-row units of each batch row, among rows with few or no queries, over short sequences."""
