@@ -546,14 +546,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
         o[0] = fmaf(f, y.x, o[0]), o[1] = fmaf(f, y.y, o[1]), o[2] = fmaf(f, y.z, o[2]), o[3] = fmaf(f, y.w, o[3]);
       }
       if (whole) {
-        const float inv = ls > 0.f ? 1.f / ls : 0.f;
+        const float inv = ls != 0.f ? 1.f / ls : 0.f;
         const size_t orow = ((size_t)b * p.H + (size_t)u.hk * p.G + rw % p.G) * p.Nq + i;
         uint2 out;
         __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&out);
         h[0] = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
         h[1] = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
         *reinterpret_cast<uint2*>(p.O + orow * D + d * 4) = out;
-        if (d == 0) p.LSE[orow] = ls > 0.f ? (mt + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+        if (d == 0) p.LSE[orow] = ls != 0.f ? (mt + log2f(ls)) * 0.69314718055994531f : -INFINITY;
       } else {
         *reinterpret_cast<float4*>(part + r * D + d * 4) = make_float4(o[0], o[1], o[2], o[3]);
         if (d == 0) part[R * D + r] = mt, part[R * D + R + r] = ls;
@@ -628,10 +628,10 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R)
   }
   const size_t orow = ((size_t)b * p.H + (size_t)hk * p.G + row % p.G) * p.Nq + i;
   if (WARPS == 1) {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) p.O[orow * D + e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
-    if (lane == 0) p.LSE[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    if (lane == 0) p.LSE[orow] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     return;
   }
   __shared__ float sm[4], sl[4], so[4][D];
@@ -650,8 +650,8 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R)
     ls = fmaf(f, sl[k], ls);
     x = fmaf(f, so[k][d], x);
   }
-  p.O[orow * D + d] = __float2bfloat16_rn(ls > 0.f ? x / ls : 0.f);
-  if (d == 0) p.LSE[orow] = ls > 0.f ? (mt + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+  p.O[orow * D + d] = __float2bfloat16_rn(ls != 0.f ? x / ls : 0.f);
+  if (d == 0) p.LSE[orow] = ls != 0.f ? (mt + log2f(ls)) * 0.69314718055994531f : -INFINITY;
 }
 
 // As many CTAs as run at once, fewer where the line cannot be long enough for them.

@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       }
       const bool whole = s.c0 == 0 && s.c1 == s.chunks;
       float* part = p.part + (size_t)(2 * w0 + (s.c0 == 0 ? 1 : 0)) * kChunkRows * (D + 2);
-      const float f = whole ? (l > 0.f ? kCodeUnit<KIND> / l : 0.f) : kCodeUnit<KIND>;
+      const float f = whole ? (l != 0.f ? kCodeUnit<KIND> / l : 0.f) : kCodeUnit<KIND>;
       const int pr = t * kTile + r;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       }
       if (ok && live) {
         if (whole)
-          p.LSE[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+          p.LSE[orow] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
         else
           part[(size_t)kChunkRows * D + pr] = m, part[(size_t)kChunkRows * D + kChunkRows + pr] = l;
       }

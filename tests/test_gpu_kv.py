@@ -315,6 +315,27 @@ def test_attention_many_tiles_of_queries(d, kind):
     check_attention(c, r, rng, 6, 600, False, [3, 2], [300, 600])
 
 
+@pytest.mark.parametrize("nq", [1, 3, 40, 80])
+def test_attention_queries_that_are_not_finite(nq):
+    """A query of NaN or with an infinite element gives NaN in its own row, and nothing else changes."""
+    rng = np.random.default_rng(21)
+    c, r = pair(200, 2, 128, 3, 110, 64, "int8")
+    fill(c, r, rng, [300, 77, 7000])
+    q, _ = bf16(rng, (3, 4, nq, 128))
+    o, lse = sa.kv_attention(q, c, causal=False)
+    bad = torch.zeros((3, 4, nq), dtype=torch.bool, device="cuda")
+    q2 = q.clone()
+    for b, h in ((0, 1), (2, 3)):
+        q2[b, h, 0] = float("nan")
+        bad[b, h, 0] = True
+    q2[1, 2, nq - 1, 5] = float("inf")
+    bad[1, 2, nq - 1] = True
+    o2, lse2 = sa.kv_attention(q2, c, causal=False)
+    assert torch.isnan(o2[bad]).all() and torch.isnan(lse2[bad]).all()
+    assert torch.equal(o2[~bad], o[~bad]) and torch.equal(lse2[~bad], lse[~bad])
+    assert sa.get_status(c.status) == sa.SAGE_OK
+
+
 @pytest.mark.parametrize("nq", [1, 40])
 def test_attention_bad_numbers_are_reported(nq):
     """A length past the table, a slot and a page out of range: reported, nothing read out of range,
