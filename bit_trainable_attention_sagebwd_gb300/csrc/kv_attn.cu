@@ -574,17 +574,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
   }
 }
 
-// Joins the parts of the units that were cut, in their order.  WARPS = 4: one CTA per (unit, row),
-// a quarter of the parts to each warp (few units, many parts).  WARPS = 1: four rows to a CTA, one
-// to each warp.
-template <int D, int WARPS>
+// Joins the parts of the units that were cut, in their order: one CTA for each (unit, row), a quarter of
+// the parts to each warp (few units, which may have many parts).
+template <int D>
 __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R) {
   constexpr int E = D / 32;  // channels of a lane
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long unit = blockIdx.x;
-  const int r = WARPS == 4 ? blockIdx.y : blockIdx.y * 4 + warp;
+  const int r = blockIdx.y;
   const int per_b = p.c.Hkv * p.tiles, b = (int)(unit / per_b), in_b = (int)(unit % per_b);
   const int hk = in_b % p.c.Hkv, row = in_b / p.c.Hkv * R + r, i = row / p.G;
   if (i >= row_queries(p, b)) return;
@@ -593,12 +592,12 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R)
   const size_t stride = (size_t)R * (D + 2);
   auto part_of = [&](int k) { return p.part + (size_t)(k == w.x ? 2 * k + 1 : 2 * k) * stride; };
   float m = -INFINITY, l = 0.f, o[E] = {};
-  for (int k0 = w.x + (WARPS == 4 ? warp : 0); k0 <= w.y; k0 += 4 * WARPS) {
+  for (int k0 = w.x + warp; k0 <= w.y; k0 += 16) {
     // four parts at a time, their loads in flight together
     float mm[4], ll[4], oo[4][E];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int k = k0 + WARPS * q;
+      const int k = k0 + 4 * q;
       mm[q] = -INFINITY, ll[q] = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) oo[q][e] = 0.f;
@@ -627,13 +626,6 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R)
     m = mn;
   }
   const size_t orow = ((size_t)b * p.H + (size_t)hk * p.G + row % p.G) * p.Nq + i;
-  if (WARPS == 1) {
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) p.O[orow * D + e * 32 + lane] = __float2bfloat16_rn(o[e] * inv);
-    if (lane == 0) p.LSE[orow] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-    return;
-  }
   __shared__ float sm[4], sl[4], so[4][D];
   if (lane == 0) sm[warp] = m, sl[warp] = l;
 #pragma unroll
@@ -652,6 +644,93 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R)
   }
   p.O[orow * D + d] = __float2bfloat16_rn(ls != 0.f ? x / ls : 0.f);
   if (d == 0) p.LSE[orow] = ls != 0.f ? (mt + log2f(ls)) * 0.69314718055994531f : -INFINITY;
+}
+
+// The same for many units: a warp takes JR rows of a unit, PF parts at a time.
+template <int D, int JR>
+__global__ void __launch_bounds__(128) kv_join_rows_kernel(const AttnParams p, int R) {
+  constexpr int E = D / 32;           // channels of a lane, side by side
+  constexpr int PF = JR == 1 ? 4 : 2;
+  pdl_wait();
+  pdl_trigger();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long unit = blockIdx.x;
+  const int r0 = (blockIdx.y * (blockDim.x >> 5) + warp) * JR;  // (R is a multiple of JR)
+  const int per_b = p.c.Hkv * p.tiles, b = (int)(unit / per_b), in_b = (int)(unit % per_b);
+  const int hk = in_b % p.c.Hkv, row0 = in_b / p.c.Hkv * R + r0, q_len = row_queries(p, b);
+  if (row0 / p.G >= q_len) return;
+  const int2 w = p.info[unit];
+  if (w.x == w.y) return;
+  const size_t stride = (size_t)R * (D + 2);
+  float m[JR], l[JR], o[JR][E];
+#pragma unroll
+  for (int x = 0; x < JR; ++x) {
+    m[x] = -INFINITY, l[x] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[x][e] = 0.f;
+  }
+  for (int k0 = w.x; k0 <= w.y; k0 += PF) {
+    float mm[PF][JR], ll[PF][JR], oo[PF][JR][E];
+    // (a row that is not there: whatever the workspace holds, and not stored)
+#pragma unroll
+    for (int q = 0; q < PF; ++q) {
+      const int k = k0 + q;
+      const float* s = p.part + (size_t)(k == w.x ? 2 * k + 1 : 2 * k) * stride;
+#pragma unroll
+      for (int x = 0; x < JR; ++x) {
+        mm[q][x] = -INFINITY, ll[q][x] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) oo[q][x][e] = 0.f;
+        if (k > w.y) continue;
+        const int r = r0 + x;
+        mm[q][x] = s[R * D + r], ll[q][x] = s[R * D + R + r];
+        if (D == 128) {
+          const float4 y = *reinterpret_cast<const float4*>(s + r * D + lane * 4);
+          oo[q][x][0] = y.x, oo[q][x][1] = y.y, oo[q][x][E - 2] = y.z, oo[q][x][E - 1] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(s + r * D + lane * 2);
+          oo[q][x][0] = y.x, oo[q][x][1] = y.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < JR; ++x) {
+      float mn = m[x];
+#pragma unroll
+      for (int q = 0; q < PF; ++q) mn = fmaxf(mn, mm[q][x]);
+      const float sub = mn == -INFINITY ? 0.f : mn;
+      const float f0 = ex2(m[x] - sub);
+      l[x] *= f0;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[x][e] *= f0;
+#pragma unroll
+      for (int q = 0; q < PF; ++q) {
+        const float f = ex2(mm[q][x] - sub);
+        l[x] = fmaf(f, ll[q][x], l[x]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[x][e] = fmaf(f, oo[q][x][e], o[x][e]);
+      }
+      m[x] = mn;
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < JR; ++x) {
+    const int row = row0 + x, i = row / p.G;
+    if (i >= q_len) return;
+    const size_t orow = ((size_t)b * p.H + (size_t)hk * p.G + row % p.G) * p.Nq + i;
+    const float inv = l[x] != 0.f ? 1.f / l[x] : 0.f;
+    uint32_t y[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(o[x][e] * inv, o[x][e + 1] * inv);
+      y[e / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if (D == 128)
+      *reinterpret_cast<uint2*>(p.O + orow * D + lane * 4) = make_uint2(y[0], y[E / 2 - 1]);
+    else
+      *reinterpret_cast<uint32_t*>(p.O + orow * D + lane * 2) = y[0];
+    if (lane == 0) p.LSE[orow] = l[x] != 0.f ? (m[x] + log2f(l[x])) * 0.69314718055994531f : -INFINITY;
+  }
 }
 
 // As many CTAs as run at once, fewer where the line cannot be long enough for them.
@@ -694,6 +773,10 @@ constexpr long long kFewRows = 32;
 // rows 12.1 us in all against 12.9 us), a warp for each row from there (64 units 11.0 us against 12.0 us, 512
 // units 15.0 us against 15.7 us).
 constexpr unsigned kFewUnits = 64;
+// Of many query rows a warp takes four at once from so many units (2048 queries of 32 heads over 8: on 4096 keys
+// 161 us against 167 us, on 32k 900 us against 910 us); with fewer units and more parts that is too few
+// warps (16 units of 210 queries: 44 us against 26 us).
+constexpr unsigned kManyUnits = 128;
 
 }  // namespace
 
@@ -747,11 +830,16 @@ int launch_kv_attention(const sage_kv_cache& c, const void* Q, const int* slots,
   const long long rows = (long long)p.G * Nq;
   const unsigned unit_rows = (unsigned)(rows < L.rows ? rows : L.rows);
   const unsigned units = (unsigned)((long long)B * c.Hkv * L.tiles);
-  const bool warp_rows = many || units >= kFewUnits;
-  auto join = warp_rows ? (c.D == 128 ? kv_join_kernel<128, 1> : kv_join_kernel<64, 1>)
-                        : (c.D == 128 ? kv_join_kernel<128, 4> : kv_join_kernel<64, 4>);
-  const unsigned y = warp_rows ? (unit_rows + 3) / 4 : unit_rows;
-  if (launch_pdl(join, dim3(units, y), dim3(128), 0, st, p, L.rows) != cudaSuccess) return 3;
+  auto join = c.D == 128 ? kv_join_kernel<128> : kv_join_kernel<64>;
+  dim3 join_grid(units, unit_rows), join_block(128);
+  if (many || units >= kFewUnits) {
+    const int rows_each = many && units >= kManyUnits ? 4 : 1;
+    join = rows_each == 4 ? (c.D == 128 ? kv_join_rows_kernel<128, 4> : kv_join_rows_kernel<64, 4>)
+                          : (c.D == 128 ? kv_join_rows_kernel<128, 1> : kv_join_rows_kernel<64, 1>);
+    const unsigned turns = (unit_rows + rows_each - 1) / rows_each, warps = turns < 4 ? turns : 4;
+    join_grid.y = (turns + warps - 1) / warps, join_block.x = 32 * warps;
+  }
+  if (launch_pdl(join, join_grid, join_block, 0, st, p, L.rows) != cudaSuccess) return 3;
   return cudaGetLastError() == cudaSuccess ? 0 : 3;
 }
 
