@@ -121,7 +121,8 @@ def _rows(slots, b, cache):
 
 def kv_append(cache, k, v, pos, n_new, slots=None, k_shift=None, stream=None):
     """Quantize the first n_new[s] tokens of bf16 k, v [B, Hkv, Nn, D] into the pages of their slots from
-    position pos[s] (int32 [n_slots], as kv_extend gives it).  slots: int32 [B], the slot of each batch row
+    position pos[s] (int32 [n_slots], as kv_extend gives it; a slot that was not extended by so many tokens is
+    left alone, SAGE_ERR_INVALID_ARG in the status word).  slots: int32 [B], the slot of each batch row
     (None: row b is slot b); k_shift: fp32 [Hkv, D], subtracted from every key (K-smoothing)."""
     if k.dim() != 4:
         raise ValueError("k, v: [B, Hkv, Nn, D] expected")

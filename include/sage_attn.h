@@ -325,7 +325,7 @@ typedef struct sage_kv_cache {
 /*
  * Quantize new tokens into their pages.  K, V: bf16 [B, Hkv, Nn, D]; batch row b belongs to slot
  * s = slots[b] (slots NULL: s = b); its first n_new[s] tokens become tokens pos[s] .. of the slot
- * (n_new, pos: int32 [n_slots], n_new[s] <= Nn; what K and V hold behind them is not read).  A slot
+ * (n_new, pos: int32 [n_slots]; what K and V hold behind them is not read).  A slot
  * with n_new[s] <= 0 or pos[s] < 0 (as sage_attn_kv_extend leaves a slot that it refused) is left alone.
  * k_shift (NULL: none): fp32 [Hkv, D], 16-byte aligned, subtracted from every key (in fp32): K-smoothing
  * with a fixed mean (SageBwd summary, Results).  A shift that is the same for every token of a head
@@ -334,8 +334,10 @@ typedef struct sage_kv_cache {
  * RN32(1/448) (e4m3): s = RN32(a r) if the page holds no earlier token, else max(its scale, RN32(a r));
  * code = rint(RN32(x / s)) or e4m3(RN32(x / s)), saturating.  Where s has grown, an earlier code c becomes
  * the code of RN32(c s_old) under s.  A block whose s is 0 has codes 0.  Values must be finite.
- * Not written, with SAGE_ERR_INVALID_ARG in the status word: a page that is not reserved or that another
- * slot lists too (refs != 1); a batch row that names the slot of an earlier row again.
+ * A slot's tokens are written in order: what a page holds behind the call's tokens counts as not written yet.
+ * Not written, with SAGE_ERR_INVALID_ARG in the status word: tokens of a slot without room for all of them
+ * (pos[s] + n_new[s] past lengths[s], to which sage_attn_kv_extend has raised it, or n_new[s] past Nn); a page
+ * that another slot lists too (refs != 1); a batch row that names the slot of an earlier row again.
  */
 int sage_attn_kv_append(const sage_kv_cache *cache, const void *K, const void *V, const float *k_shift,
                         const int *slots, const int *pos, const int *n_new, int B, int Nn, void *stream);

@@ -188,6 +188,41 @@ def test_append_leaves_out_what_it_must_not_write():
     assert sa.get_status(c.status) == sa.SAGE_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_append_behind_the_length_of_a_slot(page, kind):
+    """What a table lists behind its slot's length may be another slot's page: tokens that were not given
+    room are not written, wherever the old entries point."""
+    rng = np.random.default_rng(17)
+    c, r = pair(12, 2, 64, 4, 6, page, kind, poison=False)  # (tables of zeros: page 0 everywhere)
+    fill(c, r, rng, [2 * page + 3, 0, 0, 0])
+    k, _ = bf16(rng, (4, 2, 2 * page, 64), 50.0)
+
+    def refused(pos, n, slots=None):
+        sa.kv_append(c, k, k, dev(pos), dev(n), slots=None if slots is None else dev(slots))
+        same_state(c, r)
+        assert sa.get_status(c.status) == sa.SAGE_ERR_INVALID_ARG
+
+    refused([-1, 0, -1, -1], [0, 3, 0, 0])                   # slot 1 was not extended; its table says page 0
+    refused([-1, 0, 0, 0], [0, page, 1, page + 1])           # three such slots
+    refused([-1, 0, 0, 0], [0, 5, 5, 5], [2, 1, 3, 0])       # rows of other slots
+    fill(c, r, rng, [0, page + 2, 0, 0])
+    sa.kv_truncate(c, dev([-1, 4, -1, -1]))                  # slot 1 gives its second page back, slot 2 takes it
+    r.truncate([-1, 4, -1, -1])
+    fill(c, r, rng, [0, 0, page, 0])
+    assert r.table[1, 1] == r.table[2, 0]
+    refused([-1, page, -1, -1], [0, 2, 0, 0])                # slot 1 at its old place
+    refused([-1, 4, -1, -1], [0, page, 0, 0])                # from its last token on, across the end
+    n = [0, 3, 0, 0]
+    pos, (rpos, _) = sa.kv_extend(c, dev(n)), r.extend(n)
+    refused(rpos, [0, page, 0, 0])                           # more than it was extended by
+    k, kf = bf16(rng, (4, 2, 3, 64))
+    sa.kv_append(c, k, k, pos, dev(n))
+    r.append(kf, kf, rpos, n)
+    same_state(c, r)
+    assert sa.get_status(c.status) == sa.SAGE_OK
+
+
 # ------------------------------------------------------------------------------ attention
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
