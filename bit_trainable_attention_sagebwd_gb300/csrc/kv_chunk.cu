@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       int here = 0, ids = window(c), ids_next = window(c + per);  // here: half tiles of the window so far
       uint32_t n = 0;  // half tiles so far
       for (;; ++n) {
-        // (what lies behind the keys stays as it was: finite, and masked)
+        // (what has no page stays as it was: finite, and masked)
         const int id = __shfl_sync(0xffffffffu, ids, ((here << box_shift) + lane) & 31);
         const bool ok = lane < boxes && (unsigned)id < (unsigned)p.c.n_pages;
         if (!ok && lane < boxes && id != -1) atomicMax(p.c.status, kDevIndex);
@@ -501,9 +501,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
       const int lim = live ? row_end(p, s.len, s.q_len, i) : s.len;
       float m = -INFINITY, l = 0.f, ref = 0.f;
       bool careful = false;  // (of the warp)
-      // lanes 0-7: the tile's eight 16-key groups; scales one tile ahead, pages two
+      // lanes 0-7: the tile's eight 16-key groups; scales one tile ahead, pages two.  A group without a page
+      // (past the keys, or a page number out of range) has V's scale at -infinity: its P is 2^-infinity, whatever
+      // codes its places in shared memory still hold.
       auto scales = [&](int id, float& ks, float& vs) {
-        ks = 0.f, vs = 0.f;
+        ks = 0.f, vs = -INFINITY;
         if (id >= 0) {
           ks = p.c.k_scale[(size_t)id * p.c.Hkv + s.hk];
           vs = p.c.v_scale[(size_t)id * p.c.Hkv + s.hk];
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
           for (int o = 1; o < 8; o <<= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
         }
         const float ve = value_scale(vs, ref);
-        const float lg = lg2(ve), iv = __frcp_rn(ve);
+        const float lg = vs == -INFINITY ? -INFINITY : lg2(ve), iv = __frcp_rn(ve);
         ok = ok && mbar_wait(&sm.bar_s[t], n_s & 1, abort);
         ++n_s;
         tc_fence_after();

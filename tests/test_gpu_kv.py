@@ -402,6 +402,31 @@ def test_attention_bad_numbers_are_reported(nq):
     assert not o[1].any() and not o[2].any()
 
 
+@pytest.mark.parametrize("bad", [-1, 60, -2 ** 31, 2 ** 31 - 1])
+@pytest.mark.parametrize("page,d,kind", [(16, 64, "int8"), (64, 128, "e4m3"), (128, 128, "int8"), (32, 64, "e4m3")])
+@pytest.mark.parametrize("nq", [40, 100, 300])
+def test_attention_leaves_out_a_page_out_of_range(nq, page, d, kind, bad):
+    """A page number out of range inside a sequence: reported, its keys left out and nothing put in their place,
+    as if the sequence did not have them.  The last page (partly filled) likewise."""
+    rng = np.random.default_rng(page + nq)
+    c, r = pair(60, 2, d, 3, 12, page, kind)
+    fill(c, r, rng, [8 * page + 5, 40, 9 * page])
+    q, qf = bf16(rng, (3, 4, nq, d))
+    qf = qf.astype(np.float64)
+    n = 9 * page
+    for at, gone, causals in ((8, 5, (False,)), (1, page, (True, False) if nq + 2 * page <= n else (False,))):
+        kept, table = int(c.table[0, at]), r.table[0].copy()
+        c.table[0, at] = bad
+        r.table[0, at:-1] = r.table[0, at + 1:].copy()
+        r.lengths[0] -= gone
+        for causal in causals:
+            o, lse = sa.kv_attention(q, c, causal=causal)
+            assert sa.get_status(c.status) == sa.SAGE_ERR_INVALID_ARG
+            compare(o, lse, r.attention(qf, causal), n, d)
+        c.table[0, at] = kept
+        r.table[0], r.lengths[0] = table, r.lengths[0] + gone
+
+
 def test_attention_offsets_past_32_bits():
     """A pool of more than 2^32 codes, the sequence in its last pages."""
     rng = np.random.default_rng(10)
