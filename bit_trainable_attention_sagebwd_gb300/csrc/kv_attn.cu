@@ -209,8 +209,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
     if (enter) {
       w_page = (unsigned)next_page < (unsigned)c.n_pages ? next_page : -1;
       w_half = (unsigned)next_half < (unsigned)c.n_pages ? next_half : -1;
-      if (w_page != next_page || w_half != next_half) atomicMax(c.status, kDevIndex);
-      w_row = ns.hk * c.page + (((ns.c0 + warp + kWarps * (nw * 32 + lane)) * kChunk) & (c.page - 1));
+      // (by the tokens, not by next_page: a table may say -1 where there are keys)
+      const int k = nw * 32 + lane, token = (ns.c0 + warp + kWarps * k) * kChunk;
+      if (k < nn && ((w_page < 0 && token < ns.len) || (halves && w_half < 0 && token + 16 < ns.len)))
+        atomicMax(c.status, kDevIndex);
+      w_row = ns.hk * c.page + (token & (c.page - 1));
       const int second = halves ? w_half : w_page;
       if (w_page >= 0) {
         ks[0] = c.k_scale[(size_t)w_page * c.Hkv + ns.hk];

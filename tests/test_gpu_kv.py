@@ -404,7 +404,7 @@ def test_attention_bad_numbers_are_reported(nq):
 
 @pytest.mark.parametrize("bad", [-1, 60, -2 ** 31, 2 ** 31 - 1])
 @pytest.mark.parametrize("page,d,kind", [(16, 64, "int8"), (64, 128, "e4m3"), (128, 128, "int8"), (32, 64, "e4m3")])
-@pytest.mark.parametrize("nq", [40, 100, 300])
+@pytest.mark.parametrize("nq", [1, 16, 40, 100, 300])
 def test_attention_leaves_out_a_page_out_of_range(nq, page, d, kind, bad):
     """A page number out of range inside a sequence: reported, its keys left out and nothing put in their place,
     as if the sequence did not have them.  The last page (partly filled) likewise."""
