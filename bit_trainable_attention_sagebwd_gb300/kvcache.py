@@ -98,12 +98,24 @@ def _call(fn, cache, stream, *args):
         raise SageError(fn.__name__, rc)
 
 
-def _used_on(stream, *tensors):
-    """Tensors that a helper allocated on the current stream and that `stream` works on: their memory is not
-    given to others before it is done."""
+def _alloc(stream, make, *args, **kw):
+    """What `make` allocates for a call on `stream` (None: the current one), out of that stream's own memory: a
+    block of the current stream's may have work of that stream before it, which `stream` does not wait for."""
+    if stream is None:
+        return make(*args, **kw)
+    import torch
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _returned(stream, cache, *tensors):
+    """Tensors out of the memory of `stream` that the caller gets: once freed they are not given to others
+    before what the current stream does with them is done."""
     if stream is not None:
+        import torch
+        now = torch.cuda.current_stream(cache.device)
         for t in tensors:
-            t.record_stream(stream)
+            t.record_stream(now)
 
 
 def _slot_array(t, name, cache):
@@ -154,16 +166,15 @@ def kv_attention(q, cache, causal=True, slots=None, q_len=None, sm_scale=None, o
     B, H, Nq, _ = q.shape
     dev = cache.device
     if ws is None:
-        ws = alloc_kv_ws(cache, B, H, Nq)
-        _used_on(stream, ws)
+        ws = _alloc(stream, alloc_kv_ws, cache, B, H, Nq)
     elif ws.device != dev:
         raise ValueError(f"ws: on {ws.device}, the cache is on {dev}")
     if o is None:
-        o = torch.empty_like(q)
-        _used_on(stream, o)
+        o = _alloc(stream, torch.empty_like, q)
+        _returned(stream, cache, o)
     if lse is None:
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
-        _used_on(stream, lse)
+        lse = _alloc(stream, torch.empty, (B, H, Nq), dtype=torch.float32, device=dev)
+        _returned(stream, cache, lse)
     shape = (B, H, Nq, cache.d)
     _call(cache._lib.sage_attn_kv_attention, cache, stream, cache._ref, _arg(q, "q", torch.bfloat16, shape, dev),
           _rows(slots, B, cache), None if q_len is None else _arg(q_len, "q_len", cache._i32, (B,), dev),
@@ -183,11 +194,10 @@ def kv_extend(cache, n_new, pos=None, cow=None, stream=None):
     page was copied from, or -1."""
     import torch
     if pos is None:
-        pos = torch.empty_like(n_new)
-        _used_on(stream, pos)
+        pos = _alloc(stream, torch.empty_like, n_new)
+        _returned(stream, cache, pos)
     if cow is None:
-        cow = torch.empty_like(n_new)
-        _used_on(stream, cow)
+        cow = _alloc(stream, torch.empty_like, n_new)
     _call(cache._lib.sage_attn_kv_extend, cache, stream, cache._ref, _slot_array(n_new, "n_new", cache),
           _slot_array(pos, "pos", cache), _slot_array(cow, "cow", cache))
     return pos
@@ -210,8 +220,7 @@ def kv_compact(cache, to, ws=None, stream=None):
     if to.device != cache.device:
         raise ValueError(f"to: on {to.device}, the cache is on {cache.device}")
     if ws is None:
-        ws = alloc_kv_compact_ws(cache)
-        _used_on(stream, ws)
+        ws = _alloc(stream, alloc_kv_compact_ws, cache)
     elif ws.device != cache.device:
         raise ValueError(f"ws: on {ws.device}, the cache is on {cache.device}")
     _call(cache._lib.sage_attn_kv_compact, cache, stream, cache._ref, to._ref, ws.data_ptr(), ws.nbytes)

@@ -694,6 +694,47 @@ def test_helpers_on_a_given_stream(monkeypatch):
     assert torch.equal(to.lengths, c.lengths)
 
 
+def test_helpers_on_a_given_stream_take_memory_of_that_stream():
+    """What a helper allocates for a call on another stream is not memory that the current stream, which the call
+    does not wait for, still has work on; and what it returned is not given away under the current stream's work."""
+    rng = np.random.default_rng(18)
+    c, r = pair(20, 2, 64, 3, 8, 32, "int8")
+    fill(c, r, rng, [50, 7, 120])
+    q, qf = bf16(rng, (3, 4, 1, 64))
+    q2, _ = bf16(rng, (3, 4, 1, 64))
+    want = r.attention(qf.astype(np.float64))
+    n = dev([3, 0, 40])
+    rpos, _ = r.extend([3, 0, 40])
+    to = sa.kv_cache(30, 2, 64, 3, 8, page=32)
+    sizes = [sa.alloc_kv_ws(c, 3, 4, 1).nbytes, q.nbytes, 3 * 4 * 4, n.nbytes, n.nbytes, sa.alloc_kv_compact_ws(c).nbytes]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()              # what is freed below is what an allocation on the current stream gets
+    freed = [torch.empty(size, dtype=torch.uint8, device="cuda") for size in sizes]
+    torch.cuda._sleep(200_000_000)        # about 0.1 s
+    for t in freed:
+        t.fill_(255)                      # NaN, -1: while or after the calls below work
+    places = {t.data_ptr() for t in freed}
+    t = freed = None
+    o, lse = sa.kv_attention(q, c, stream=stream)
+    pos = sa.kv_extend(c, n, stream=stream)
+    sa.kv_compact(c, to, stream=stream)
+    torch.cuda.synchronize()
+    assert places.isdisjoint({o.data_ptr(), lse.data_ptr(), pos.data_ptr()})
+    compare(o, lse, want, 120, 64)
+    assert np.array_equal(pos.cpu().numpy(), rpos) and torch.equal(to.lengths, c.lengths)
+    assert sa.get_status(c.status) == sa.SAGE_OK
+    kept, place = o.clone(), o.data_ptr()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    later = o.clone()                     # the current stream still has to read o
+    o = None
+    o2, _ = sa.kv_attention(q2, c, stream=stream)
+    assert o2.data_ptr() != place or torch.cuda.current_stream().query()
+    torch.cuda.synchronize()
+    assert torch.equal(later, kept) and not torch.equal(o2, kept)
+
+
 def test_prompt_in_chunks_equals_prompt_at_once():
     """A prompt attended over in chunks against the same prompt in one call (the same cache)."""
     rng = np.random.default_rng(7)
