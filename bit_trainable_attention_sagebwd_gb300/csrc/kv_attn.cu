@@ -758,8 +758,11 @@ int launch_few(AttnParams p, int sms, cudaStream_t st) {
       !make_tmap_3d(&tv, p.c.v, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, D, (uint64_t)p.c.Hkv * p.c.page, p.c.n_pages, D,
                     box, swizzle))
     return 3;
-  const size_t smem = 1024 + (size_t)kWarps * Ring<D, RT>::kWarpBytes + ((size_t)p.B + 1) * 16;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return 3;
+  // The kernel's limit is the process's: always the same one, for the most batch rows, or a call of another
+  // thread could lower it before this launch.
+  const size_t ring = 1024 + (size_t)kWarps * Ring<D, RT>::kWarpBytes, most = ring + ((size_t)kKvMaxBatch + 1) * 16;
+  const size_t smem = ring + ((size_t)p.B + 1) * 16;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) return 3;
   return launch_pdl(kern, dim3(p.most_parts), dim3(kThreads), smem, st, p, tk, tv) == cudaSuccess ? 0 : 3;
 }
 template <int D, int KIND>

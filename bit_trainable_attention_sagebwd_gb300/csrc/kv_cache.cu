@@ -609,9 +609,11 @@ int launch_kv_truncate(const sage_kv_cache& c, const int* keep, cudaStream_t st)
 
 int launch_kv_extend(const sage_kv_cache& c, const int* n_new, int* pos, int* cow, cudaStream_t st) {
   ScopedTimer timer("kv_pages", st);
-  const size_t smem = (2 * (size_t)c.n_slots + 1) * 4;  // at most 64 KB (kKvMaxSlots)
-  if (smem > 40 * 1024 &&  // (48 KB with the static part need no leave)
-      cudaFuncSetAttribute(kv_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  const size_t smem = (2 * (size_t)c.n_slots + 1) * 4;
+  // (48 KB with the static part need no leave; the limit is the process's, so it is the same in every call)
+  constexpr size_t kMost = (2 * (size_t)kKvMaxSlots + 1) * 4;
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(kv_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost) != cudaSuccess)
     return 3;
   if (launch_pdl(kv_extend_kernel, dim3(1), dim3(kScanThreads), smem, st, c, n_new, pos, cow) != cudaSuccess ||
       launch_pdl(kv_cow_kernel, dim3(c.n_slots, kCowParts), dim3(256), 0, st, c, (const int*)pos, (const int*)cow) !=

@@ -1,6 +1,8 @@
 """The 8-bit paged cache on the GPU (sage_attn_kv_*) against its plain numpy form (kv_ref.py):
 codes, scales, tables, lengths and refs bit for bit, attention within the roundings that its
 definition names (kv_ref.attention_tolerances)."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -733,6 +735,52 @@ def test_helpers_on_a_given_stream_take_memory_of_that_stream():
     assert o2.data_ptr() != place or torch.cuda.current_stream().query()
     torch.cuda.synchronize()
     assert torch.equal(later, kept) and not torch.equal(o2, kept)
+
+
+def test_calls_of_two_threads():
+    """Two host threads, each with its own stream, caches and workspaces, whose calls differ in what they take of an
+    SM's shared memory (batch rows of an attention, slots of an extend)."""
+    rng = np.random.default_rng(19)
+    d, many = 128, 700
+    jobs = []
+    for rows, slots in ((2, 5200), (many, 8192)):
+        c, r = pair(many + 8, 1, d, many, 2, 16, "int8")
+        fill(c, r, rng, 1 + np.arange(many) % 5)
+        q, qf = bf16(rng, (rows, 1, 1, d))
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            ws = sa.alloc_kv_ws(c, rows, 1, 1)
+            o, lse = torch.empty_like(q), torch.empty((rows, 1, 1), device="cuda")
+            big = sa.kv_cache(slots, 1, 64, slots, 1, page=16)
+            n = torch.ones(slots, dtype=torch.int32, device="cuda")
+            pos, cow = torch.empty_like(n), torch.empty_like(n)
+        jobs.append((c, r, q, qf, stream, ws, o, lse, big, n, pos, cow))
+    torch.cuda.synchronize()
+    start, failed = threading.Barrier(2), []
+
+    def work(c, r, q, qf, stream, ws, o, lse, big, n, pos, cow):
+        try:
+            start.wait()
+            for i in range(300):
+                sa.kv_attention(q, c, slots=slots_of[len(q)], o=o, lse=lse, ws=ws, stream=stream)
+                if i < 16:
+                    sa.kv_extend(big, n, pos=pos, cow=cow, stream=stream)
+        except Exception as e:
+            failed.append(e)
+
+    slots_of = {len(j[2]): dev(np.arange(len(j[2]))) for j in jobs}
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for c, r, q, qf, stream, ws, o, lse, big, n, pos, cow in jobs:
+        assert sa.get_status(c.status) == sa.SAGE_OK and sa.get_status(big.status) == sa.SAGE_OK
+        compare(o, lse, r.attention(qf.astype(np.float64), slots=list(range(len(q)))), 5, d)
+        assert (big.lengths == 16).all() and (big.refs == 1).all()
 
 
 def test_prompt_in_chunks_equals_prompt_at_once():
