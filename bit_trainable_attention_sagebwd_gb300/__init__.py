@@ -36,7 +36,7 @@ ABI_FUNCTIONS = ("sage_attn_ws_bytes", "sage_attn_bwd_ws_bytes", "sage_attn_quan
                  "sage_attn_fp4_ws_views", "sage_attn_fp4_bwd_ws_bytes", "sage_attn_fp4_bwd",
                  "sage_attn_kv_append", "sage_attn_kv_ws_bytes", "sage_attn_kv_attention", "sage_attn_kv_fork",
                  "sage_attn_kv_extend", "sage_attn_kv_truncate", "sage_attn_kv_compact_ws_bytes",
-                 "sage_attn_kv_compact")
+                 "sage_attn_kv_compact", "sage_attn_selftest_kv_join")
 
 
 class SageError(RuntimeError):
@@ -113,6 +113,7 @@ def lib():
             L.sage_attn_kv_ws_bytes.restype = sz
             L.sage_attn_kv_ws_bytes.argtypes = [i] * 5
             L.sage_attn_kv_attention.argtypes = [cp] + [vp] * 6 + [sz, i, i, i, i, fp, vp]
+            L.sage_attn_selftest_kv_join.argtypes = [cp] + [vp] * 3 + [sz, i, i, i, vp]
             L.sage_attn_kv_fork.argtypes = [cp, vp, vp]
             L.sage_attn_kv_extend.argtypes = [cp, vp, vp, vp, vp]
             L.sage_attn_kv_truncate.argtypes = [cp, vp, vp]
@@ -333,6 +334,10 @@ def sage_attn_get_status(ws, stream):
 
 def sage_attn_selftest_wait(ws, budget_ns, stream):
     return lib().sage_attn_selftest_wait(ws, int(budget_ns), stream)
+
+
+def sage_attn_selftest_kv_join(cache, O, LSE, ws, ws_bytes, B, H, Nq, stream):
+    return lib().sage_attn_selftest_kv_join(cache, O, LSE, ws, ws_bytes, B, H, Nq, stream)
 
 
 def sage_attn_timer_enable(on):

@@ -29,6 +29,8 @@ int launch_kv_append(const sage_kv_cache& c, const void* K, const void* V, const
                      const int* pos, const int* n_new, int B, int Nn, cudaStream_t st);
 int launch_kv_attention(const sage_kv_cache& c, const void* Q, const int* slots, const int* q_len, void* O,
                         float* LSE, void* ws, int B, int H, int Nq, int causal, float sm_scale, cudaStream_t st);
+// the join of an attention call alone (sage_attn_selftest_kv_join)
+int launch_kv_join(const sage_kv_cache& c, void* O, float* LSE, void* ws, int B, int H, int Nq, cudaStream_t st);
 int launch_kv_fork(const sage_kv_cache& c, const int* src, cudaStream_t st);
 int launch_kv_extend(const sage_kv_cache& c, const int* n_new, int* pos, int* cow, cudaStream_t st);
 int launch_kv_truncate(const sage_kv_cache& c, const int* keep, cudaStream_t st);

@@ -70,6 +70,15 @@ int sage_attn_kv_attention(const sage_kv_cache* cache, const void* Q, const int*
                                    sage::resolve_scale(sm_scale, cache->D), static_cast<cudaStream_t>(stream));
 }
 
+int sage_attn_selftest_kv_join(const sage_kv_cache* cache, void* O, float* LSE, void* ws, size_t ws_bytes, int B, int H,
+                               int Nq, void* stream) {
+  if (int rc = check_cache(cache)) return rc;
+  if (!aligned(O, 16) || !aligned(LSE, 4) || !aligned(ws, 16)) return SAGE_ERR_INVALID_ARG;
+  if (!attention_shape_ok(B, H, cache->Hkv, cache->D, Nq)) return SAGE_ERR_UNSUPPORTED;
+  if (ws_bytes < sage::kv_attn_ws_layout(B, H, cache->Hkv, cache->D, Nq).total) return SAGE_ERR_INVALID_ARG;
+  return sage::launch_kv_join(*cache, O, LSE, ws, B, H, Nq, static_cast<cudaStream_t>(stream));
+}
+
 int sage_attn_kv_fork(const sage_kv_cache* cache, const int* src, void* stream) {
   if (int rc = check_cache(cache)) return rc;
   if (!aligned(src, 4)) return SAGE_ERR_INVALID_ARG;

@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttnParams p, int R)
   const int hk = in_b % p.c.Hkv, row = in_b / p.c.Hkv * R + r, i = row / p.G;
   if (i >= row_queries(p, b)) return;
   const int2 w = p.info[unit];
-  if (w.x == w.y) return;
+  if (!was_cut(p, w)) return;
   const size_t stride = (size_t)R * (D + 2);
   auto part_of = [&](int k) { return p.part + (size_t)(k == w.x ? 2 * k + 1 : 2 * k) * stride; };
   float m = -INFINITY, l = 0.f, o[E] = {};
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(128) kv_join_rows_kernel(const AttnParams p, i
   const int hk = in_b % p.c.Hkv, row0 = in_b / p.c.Hkv * R + r0, q_len = row_queries(p, b);
   if (row0 / p.G >= q_len) return;
   const int2 w = p.info[unit];
-  if (w.x == w.y) return;
+  if (!was_cut(p, w)) return;
   const size_t stride = (size_t)R * (D + 2);
   float m[JR], l[JR], o[JR][E];
 #pragma unroll
@@ -806,14 +806,14 @@ KvAttnWs kv_attn_ws_layout(int B, int H, int Hkv, int D, int Nq) {
   return L;
 }
 
-int launch_kv_attention(const sage_kv_cache& c, const void* Q, const int* slots, const int* q_len, void* O,
-                        float* LSE, void* ws, int B, int H, int Nq, int causal, float sm_scale, cudaStream_t st) {
-  const KvAttnWs L = kv_attn_ws_layout(B, H, c.Hkv, c.D, Nq);
+namespace {
+
+// what the kernels of a call share (scales and sizes of the queries left to the caller)
+AttnParams attn_params(const sage_kv_cache& c, const KvAttnWs& L, const int* q_len, void* O, float* LSE, void* ws, int B,
+                       int H, int Nq) {
   uint8_t* w = static_cast<uint8_t*>(ws);
-  AttnParams p;
+  AttnParams p{};
   p.c = c;
-  p.Q = static_cast<const __nv_bfloat16*>(Q);
-  p.slots = slots;
   p.q_len = q_len;
   p.O = static_cast<__nv_bfloat16*>(O);
   p.LSE = LSE;
@@ -824,6 +824,36 @@ int launch_kv_attention(const sage_kv_cache& c, const void* Q, const int* slots,
   p.G = H / c.Hkv;
   p.Nq = Nq;
   p.tiles = L.tiles;
+  p.most_parts = L.rows == kChunkRows ? kMaxChunkParts : kMaxParts;
+  return p;
+}
+
+int launch_join(const AttnParams& p, int R, cudaStream_t st) {
+  const bool many = R == kChunkRows;
+  const long long rows = (long long)p.G * p.Nq;
+  const unsigned unit_rows = (unsigned)(rows < R ? rows : R);
+  const unsigned units = (unsigned)((long long)p.B * p.c.Hkv * p.tiles);
+  auto join = p.c.D == 128 ? kv_join_kernel<128> : kv_join_kernel<64>;
+  dim3 join_grid(units, unit_rows), join_block(128);
+  if (many || units >= kFewUnits) {
+    const int rows_each = many && units >= kManyUnits ? 4 : 1;
+    join = rows_each == 4 ? (p.c.D == 128 ? kv_join_rows_kernel<128, 4> : kv_join_rows_kernel<64, 4>)
+                          : (p.c.D == 128 ? kv_join_rows_kernel<128, 1> : kv_join_rows_kernel<64, 1>);
+    const unsigned turns = (unit_rows + rows_each - 1) / rows_each, warps = turns < 4 ? turns : 4;
+    join_grid.y = (turns + warps - 1) / warps, join_block.x = 32 * warps;
+  }
+  if (launch_pdl(join, join_grid, join_block, 0, st, p, R) != cudaSuccess) return 3;
+  return cudaGetLastError() == cudaSuccess ? 0 : 3;
+}
+
+}  // namespace
+
+int launch_kv_attention(const sage_kv_cache& c, const void* Q, const int* slots, const int* q_len, void* O,
+                        float* LSE, void* ws, int B, int H, int Nq, int causal, float sm_scale, cudaStream_t st) {
+  const KvAttnWs L = kv_attn_ws_layout(B, H, c.Hkv, c.D, Nq);
+  AttnParams p = attn_params(c, L, q_len, O, LSE, ws, B, H, Nq);
+  p.Q = static_cast<const __nv_bfloat16*>(Q);
+  p.slots = slots;
   p.causal = causal;
   p.alpha = (float)((double)sm_scale * 1.4426950408889634074);
   int dev = 0, sms = 0;
@@ -831,22 +861,14 @@ int launch_kv_attention(const sage_kv_cache& c, const void* Q, const int* slots,
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 3;
   ScopedTimer timer("kv_attention", st);
-  const bool many = L.rows == kChunkRows;
-  if (int rc = many ? launch_kv_chunk(p, c.kind, sms, st) : launch_kv_few(p, c.kind, L.rows, sms, st)) return rc;
-  const long long rows = (long long)p.G * Nq;
-  const unsigned unit_rows = (unsigned)(rows < L.rows ? rows : L.rows);
-  const unsigned units = (unsigned)((long long)B * c.Hkv * L.tiles);
-  auto join = c.D == 128 ? kv_join_kernel<128> : kv_join_kernel<64>;
-  dim3 join_grid(units, unit_rows), join_block(128);
-  if (many || units >= kFewUnits) {
-    const int rows_each = many && units >= kManyUnits ? 4 : 1;
-    join = rows_each == 4 ? (c.D == 128 ? kv_join_rows_kernel<128, 4> : kv_join_rows_kernel<64, 4>)
-                          : (c.D == 128 ? kv_join_rows_kernel<128, 1> : kv_join_rows_kernel<64, 1>);
-    const unsigned turns = (unit_rows + rows_each - 1) / rows_each, warps = turns < 4 ? turns : 4;
-    join_grid.y = (turns + warps - 1) / warps, join_block.x = 32 * warps;
-  }
-  if (launch_pdl(join, join_grid, join_block, 0, st, p, L.rows) != cudaSuccess) return 3;
-  return cudaGetLastError() == cudaSuccess ? 0 : 3;
+  if (int rc = L.rows == kChunkRows ? launch_kv_chunk(p, c.kind, sms, st) : launch_kv_few(p, c.kind, L.rows, sms, st))
+    return rc;
+  return launch_join(p, L.rows, st);
+}
+
+int launch_kv_join(const sage_kv_cache& c, void* O, float* LSE, void* ws, int B, int H, int Nq, cudaStream_t st) {
+  const KvAttnWs L = kv_attn_ws_layout(B, H, c.Hkv, c.D, Nq);
+  return launch_join(attn_params(c, L, nullptr, O, LSE, ws, B, H, Nq), L.rows, st);
 }
 
 }  // namespace sage

@@ -16,10 +16,10 @@ struct AttnParams {
   const int *slots, *q_len;
   __nv_bfloat16* O;
   float* LSE;
-  int2* info;      // first and last worker of each unit
+  int2* info;      // first and last worker of each unit; not written where a wait ran out
   float* part;     // two partial results of each worker: [R][D] sums, then [R] maxima and [R] row sums
   int B, H, G, Nq, tiles, causal;
-  int most_parts;  // CTAs of the grid: the parts of the line at most
+  int most_parts;  // CTAs of the grid: the parts of the line at most (the joins: those that the workspace holds)
   float alpha;     // sm_scale log2 e
 };
 
@@ -169,6 +169,12 @@ struct Line {
     return v;
   }
 };
+
+// Whether a unit's first and last part are such as a join may read: two at least, and in the workspace.  After a
+// wait that ran out they are whatever the workspace held, and the unit's rows are left.
+__device__ __forceinline__ bool was_cut(const AttnParams& p, int2 w) {
+  return w.x >= 0 && w.x < w.y && w.y < p.most_parts;
+}
 
 // the most parts
 constexpr int kMaxParts = 512;         // few query rows

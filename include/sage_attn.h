@@ -403,6 +403,15 @@ int sage_attn_get_status(void *ws, void *stream);
  * gives up, records SAGE_ERR_TIMEOUT in the status word of `ws` and returns. */
 int sage_attn_selftest_wait(void *ws, unsigned long long budget_ns, void *stream);
 
+/* Self-test of what follows a wait of sage_attn_kv_attention that ran out: launches the join of its partial
+ * results alone (no q_len: Nq queries each), over a workspace that the caller has filled.  ws: for each of the
+ * B * tiles * Hkv units (tiles = ceil(H / Hkv * Nq / R); R query rows: 8 up to 8 of a shared head, 16 up to 32, else
+ * 256) int32 first and last part, then from the next multiple of 256 bytes the parts, part k of a unit at place
+ * 2 k + 1 if it is the first, else 2 k: fp32 [R, D] sums, [R] maxima (powers of two), [R] row sums.  The rows of
+ * a unit whose parts are not two or more within the workspace are left. */
+int sage_attn_selftest_kv_join(const sage_kv_cache *cache, void *O, float *LSE, void *ws, size_t ws_bytes, int B,
+                               int H, int Nq, void *stream);
+
 /* Size of the library-owned scratch array used by sage_attn_bwd_noalloc. */
 #define SAGE_ATTN_NOALLOC_SCRATCH_BYTES (32u << 20)
 

@@ -429,6 +429,66 @@ def test_attention_leaves_out_a_page_out_of_range(nq, page, d, kind, bad):
         r.table[0], r.lengths[0] = table, r.lengths[0] + gone
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,hkv,g,nq", [(3, 2, 1, 1), (7, 2, 8, 3), (40, 2, 4, 1), (2, 3, 2, 70), (40, 2, 2, 200)])
+def test_join_leaves_units_whose_parts_were_not_written(B, hkv, g, nq, d):
+    """What a wait that ran out leaves: parts of units that nobody wrote, here numbers out of range in every way.  Their
+    rows stay as they were, and the units beside them are joined."""
+    rng = np.random.default_rng(B + nq)
+    c = sa.kv_cache(1, hkv, d, B, 1)
+    rows = g * nq
+    R = 8 if rows <= 8 else 16 if rows <= 32 else 256
+    tiles = -(-rows // R)
+    units, most = B * tiles * hkv, 160 if R == 256 else 512
+    ws = sa.alloc_kv_ws(c, B, hkv * g, nq)
+    at, stride = (units * 8 + 255) // 256 * 256 // 4, R * (d + 2)
+    assert ws.numel() == 4 * (at + 2 * most * stride)
+    ws.view(torch.float32).fill_(float("nan"))
+    bad = [(-1, 1), (0, most), (3, 2 ** 31 - 1), (-2 ** 31, 2 ** 31 - 1), (-2, -1), (5, 3), (2 ** 31 - 1, -2 ** 31), (7, 7),
+           (most, most + 1), (-2 ** 31, 5), (most - 1, most)]
+    info = np.array([bad[i % len(bad)] for i in range(units)], np.int32)
+    # two units are as a call leaves them: one in parts 2 to 4, one in the workspace's last two
+    good = {units // 2: (2, 4), units - 1: (most - 2, most - 1)}
+    parts = torch.zeros((2 * most, R * (d + 2)))
+    sums, m, l = {}, {}, {}
+    for u, (a, b) in good.items():
+        info[u] = a, b
+        for k in range(a, b + 1):
+            x = torch.from_numpy(rng.standard_normal((R, d)).astype(np.float32))
+            top, low = torch.from_numpy(rng.integers(-3, 4, R).astype(np.float32)), torch.from_numpy(rng.uniform(0.5, 2, R).astype(np.float32))
+            parts[2 * k + (k == a)] = torch.cat((x.flatten(), top, low))
+            sums[u, k], m[u, k], l[u, k] = x.double(), top.double(), low.double()
+    flat = ws.view(torch.float32)
+    for u, (a, b) in good.items():
+        for k in range(a, b + 1):
+            i = 2 * k + (k == a)
+            flat[at + i * stride:at + (i + 1) * stride] = parts[i].cuda()
+    ws.view(torch.int32)[:2 * units] = torch.from_numpy(info.reshape(-1)).cuda()
+    o = torch.full((B, hkv * g, nq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, hkv * g, nq), 7.0, device="cuda")
+    rc = sa.sage_attn_selftest_kv_join(c._ref, o.data_ptr(), lse.data_ptr(), ws.data_ptr(), ws.nbytes, B, hkv * g, nq,
+                                       torch.cuda.current_stream().cuda_stream)
+    assert rc == sa.SAGE_OK
+    torch.cuda.synchronize()
+    go, gl = o.double().cpu(), lse.double().cpu()
+    want_o, want_l = torch.full_like(go, 7.0), torch.full_like(gl, 7.0)
+    for u, (a, b) in good.items():
+        bt, hk = divmod(u, hkv)
+        bi, tile = divmod(bt, tiles)
+        w = [2.0 ** m[u, k] for k in range(a, b + 1)]
+        total = sum(f * l[u, k] for f, k in zip(w, range(a, b + 1)))
+        joined = sum(f[:, None] * sums[u, k] for f, k in zip(w, range(a, b + 1))) / total[:, None]
+        for x in range(R):
+            row = tile * R + x
+            if row < rows:
+                want_o[bi, hk * g + row % g, row // g] = joined[x]
+                want_l[bi, hk * g + row % g, row // g] = torch.log(total[x])
+    # Each of up to three terms and the row sum is off by ex2's 2^-22 and a few roundings of 2^-24, O by both: 2^-20
+    # of sum w |x| / total <= max |x| / 0.5; then bf16's half step.
+    tol = 2.0 ** -8 * want_o.abs() + 2.0 ** -19 * (1 + 2.0 ** -8) * max(float(x.abs().max()) for x in sums.values())
+    assert ((go - want_o).abs() <= tol).all() and ((gl - want_l).abs() <= 2.0 ** -19 * (1 + want_l.abs())).all()
+
+
 def test_attention_offsets_past_32_bits():
     """A pool of more than 2^32 codes, the sequence in its last pages."""
     rng = np.random.default_rng(10)

@@ -162,3 +162,15 @@ def test_reference_attention_closed_form():
     _, vals = c.values(0, 0)
     assert np.allclose(o[0, 0, 1], vals.mean(0)) and np.allclose(o[0, 0, 0], vals[:19].mean(0))
     assert np.allclose(lse[0, 0], 2.0 + np.log([19, 20])) and np.all(lse[1] == -np.inf) and not o[1].any()
+
+
+def test_the_selftest_of_the_join_refuses_bad_arguments(lib):
+    n = sa.sage_attn_kv_ws_bytes(4, 4, 2, 128, 1)
+
+    def call(c=None, O=FAKE, LSE=FAKE, ws=FAKE, ws_bytes=n, B=4, H=4, Nq=1):
+        return sa.sage_attn_selftest_kv_join(cache() if c is None else c, O, LSE, ws, ws_bytes, B, H, Nq, None)
+
+    for over in (dict(O=None), dict(O=FAKE + 8), dict(LSE=None), dict(ws=None), dict(ws_bytes=n - 1), dict(c=cache(k=None))):
+        assert call(**over) == sa.SAGE_ERR_INVALID_ARG
+    for over in (dict(B=0), dict(H=3), dict(Nq=0), dict(c=cache(D=96))):
+        assert call(**over) == sa.SAGE_ERR_UNSUPPORTED
