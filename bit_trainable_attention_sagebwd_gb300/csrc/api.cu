@@ -22,8 +22,10 @@ bool aligned16(const void* p) { return p != nullptr && ((uintptr_t)p & 15u) == 0
 // grouped-query attention: Hkv key/value heads, each shared by H / Hkv query heads
 bool groups_ok(int H, int Hkv) { return Hkv >= 1 && Hkv <= H && H % Hkv == 0; }
 
-// One CTA waits on a barrier that nothing arrives at; the bounded wait gives up
-// after budget_ns and the kernel records the timeout in the status word.
+// One warp waits on a barrier that nothing arrives at; the bounded wait gives up after budget_ns and the kernel
+// records the timeout in the status word.  The lanes' budgets differ (a lane's first one that runs out raises the
+// abort flag, which the others meet at other times), and the warp has to give up as one: its lanes then count each
+// other, and a count that misses one is another status.
 __global__ void selftest_wait_kernel(int* status, unsigned long long budget_ns) {
   __shared__ uint64_t bar;
   __shared__ int abort;
@@ -33,9 +35,9 @@ __global__ void selftest_wait_kernel(int* status, unsigned long long budget_ns) 
     sage::fence_mbar_init();
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    if (!sage::mbar_wait(&bar, 0, &abort, budget_ns)) atomicExch(status, sage::kDevTimeout);
-  }
+  const bool came = sage::mbar_wait_warp(&bar, 0, &abort, budget_ns - budget_ns / 64 * threadIdx.x);
+  const unsigned gave_up = __ballot_sync(0xffffffffu, !came);
+  if (threadIdx.x == 0 && gave_up) atomicExch(status, gave_up == 0xffffffffu ? sage::kDevTimeout : sage::kDevSetup);
 }
 
 }  // namespace

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
 #pragma unroll 1
     for (int k = chunks_of(u), ch = u.c0 + warp; k > 0; --k, ch += kWarps) {
       issue();
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars[warp][here], phase, &abort))) break;
+      if (!mbar_wait_warp(&bars[warp][here], phase, &abort)) break;
       __syncwarp();  // (meta)
       --flight;
       const uint8_t* src = my_ring + here * Ring<D, RT>::kBytes;

@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         issue_ts_x4(d, a, b, id_o, acc);
         issue_ts_x4(d, a + 32, b + (4 * 2048 >> 4), id_o, 1);
       };
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort)); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
       bool ok = true;
       while (ok) {
         // a part: its tiles and mode, said with the first row tile's Q
@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         const uint32_t all = __ballot_sync(0xffffffffu, ok);
         const uint32_t at = n % kRaw<D>;
         uint64_t* full = &sm.bar_raw[v][at];
-        if (!__all_sync(0xffffffffu, n < kRaw<D> || mbar_wait(&sm.bar_raw_empty[v][at], (n / kRaw<D> - 1) & 1, abort))) break;
+        if (n >= kRaw<D> && !mbar_wait_warp(&sm.bar_raw_empty[v][at], (n / kRaw<D> - 1) & 1, abort)) break;
         if (lane == 0) {
           if (all)
             mbar_arrive_expect_tx(full, __popc(all) * box_bytes);
@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + kColO + t * 128;
     uint32_t n_s = 0, n_o = 0, n_turns = 0;
-    bool ok = true;
+    bool ok = true;  // (of the warp)
+    auto wait = [&](uint64_t* bar, uint32_t parity) { ok = ok && mbar_wait_warp(bar, parity, abort); };
     Walk walk(p, sm.pre, group, begin, stop);
     while (ok && walk.more()) {
       const Seg s = walk.next(p);
@@ -529,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         }
         const float ve = value_scale(vs, ref);
         const float lg = vs == -INFINITY ? -INFINITY : lg2(ve), iv = __frcp_rn(ve);
-        ok = ok && mbar_wait(&sm.bar_s[t], n_s & 1, abort);
+        wait(&sm.bar_s[t], n_s & 1);
         ++n_s;
         tc_fence_after();
         const bool edge = __any_sync(0xffffffffu, lim < (c + 1) * kTile);
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         ks = ks_n, vs = vs_n;
       }
       // ---- the part's result
-      ok = ok && mbar_wait(&sm.bar_o[t], n_o & 1, abort);
+      wait(&sm.bar_o[t], n_o & 1);
       ++n_o;
       tc_fence_after();
       // turns: both places hold a part of the same rows, thread r of both groups the same row in the same
@@ -627,13 +628,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_chunk_kernel(const AttnParams 
         half[r] = make_float2(m, l);
         tc_fence_before();
         mbar_arrive(&sm.bar_half);
-        ok = ok && mbar_wait(&sm.bar_joined, n_turns & 1, abort);
+        wait(&sm.bar_joined, n_turns & 1);
         ++n_turns;
         tc_fence_after();
         continue;
       }
       if (turns) {
-        ok = ok && mbar_wait(&sm.bar_half, n_turns & 1, abort);
+        wait(&sm.bar_half, n_turns & 1);
         ++n_turns;
         tc_fence_after();
         const float2 x = half[r];

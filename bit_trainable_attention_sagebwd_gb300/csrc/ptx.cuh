@@ -74,6 +74,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
   }
 }
+// The same for a whole warp, which succeeds or gives up as one: a lane that gave up alone, in a loop that it then
+// leaves, would be missing in the warp's later votes and exchanges.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                               uint64_t budget_ns = SAGE_WAIT_NS) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, budget_ns));
+}
 
 // ------------------------------------------------------------ CTA order
 // Linear CTA index -> (tile index t in [0, ntile), head bh).  Heads go in groups of

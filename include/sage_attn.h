@@ -398,7 +398,7 @@ int sage_attn_ws_views(void *ws, int B, int H, int N, int D, sage_ws_views *view
  * a cache also SAGE_ERR_NO_PAGES and SAGE_ERR_INVALID_ARG. */
 int sage_attn_get_status(void *ws, void *stream);
 
-/* Self-test of the bounded wait: launches one CTA that waits on a barrier nothing
+/* Self-test of the bounded wait: launches one warp that waits on a barrier nothing
  * arrives at, with a budget of `budget_ns` nanoseconds (capped at 1 s); the kernel
  * gives up, records SAGE_ERR_TIMEOUT in the status word of `ws` and returns. */
 int sage_attn_selftest_wait(void *ws, unsigned long long budget_ns, void *stream);

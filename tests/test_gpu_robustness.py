@@ -21,6 +21,16 @@ def test_bounded_wait_reports_timeout_and_context_survives():
     assert float(x.sum()) == 1024.0  # the context still works
 
 
+@pytest.mark.parametrize("budget_ns", [0, 1, 1000, 100_003, 3_000_000])
+def test_a_warp_gives_a_wait_up_as_one(budget_ns):
+    """Lanes whose budgets differ: the wait ends for all of them (another status than the timeout's: not for all)."""
+    ws = sa.alloc_ws(1, 1, 128, 64)
+    ws.zero_()
+    for _ in range(20):
+        assert sa.sage_attn_selftest_wait(sa._ptr(ws), budget_ns, sa._stream_ptr()) == sa.SAGE_OK
+        assert sa.get_status(ws) == sa.SAGE_ERR_TIMEOUT
+
+
 def test_unsupported_shapes_raise():
     q = torch.zeros(1, 1, 128, 96, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(sa.SageError):
