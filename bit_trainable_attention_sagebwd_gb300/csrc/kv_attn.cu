@@ -420,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
             }
             mx[t][e] = max3(mx[t][e], s[h][t][e], s[h][t][2 + e]);
           }
-          raise |= mx[t][e] > m[t][e] + kRaise;
+          // (the difference, not m + kRaise, which rounds past it from 2^25 on; -inf less -inf is NaN: false)
+          raise |= mx[t][e] - m[t][e] > kRaise;
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -432,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float to = x > m[t][e] + kRaise ? x - kBelow : m[t][e];
+            const float to = x - m[t][e] > kRaise ? x - kBelow : m[t][e];
             corr[e] = to == m[t][e] ? 1.f : ex2(m[t][e] - to);
             m[t][e] = to;
             l[t][e] *= corr[e];

@@ -298,6 +298,35 @@ def test_attention_logits_past_fp32_resolution(nq, kind):
         assert torch.isfinite(lse).all()
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("e,step", [(25, 8), (26, 8), (27, 16), (12, 16)])
+@pytest.mark.parametrize("nq", [1, 12, 40])
+def test_attention_maxima_sixteen_above_the_reference(nq, e, step, kind):
+    """Logits (in powers of two) that are whole numbers at 2^e and rise by `step` with every fourth chunk of 32
+    keys, so that a warp meets a maximum of 16 above its reference, where fp32's spacing is 4 to 16.  All of it is exact in
+    fp32 but the last steps, so the tolerance takes no error of the logits."""
+    rng = np.random.default_rng(15)
+    page, d, n = 32, 64, 64
+    c, r = pair(n, 1, d, 1, n, page, kind)
+    fill(c, r, rng, [n * page])
+    c.k.view(torch.int8).zero_()
+    c.k.view(torch.int8)[..., 0] = 1 if kind == "int8" else 0x38    # 1
+    r.k[:] = c.k.view(torch.uint8).cpu().numpy()
+    r.k_scale[r.table[0, :n], 0] = np.float32(2.0 ** e + 1024 + step * (np.arange(n) // 4))
+    c.k_scale.copy_(torch.from_numpy(r.k_scale))
+    c.v_scale.fill_(1.0)
+    r.v_scale[:] = 1.0
+    q = torch.zeros((1, 1, nq, d), dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    ln2 = float(np.float32(np.log(2.0)))  # sm_scale log2 e is 1 in fp32
+    o, lse = sa.kv_attention(q.cuda(), c, causal=False, sm_scale=ln2)
+    torch.cuda.synchronize()
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+    want = list(r.attention(q.double().numpy(), False, sm_scale=ln2))
+    want[4] = np.zeros_like(want[4])
+    compare(o, lse, want, n * page, d)
+
+
 @pytest.mark.parametrize("e", [8, 22, 34, 60])
 @pytest.mark.parametrize("nq", [1, 40])
 def test_attention_far_keys_before_near_ones(nq, e):
