@@ -53,8 +53,9 @@ __device__ __forceinline__ Quant quant_of(float s) {
   q.ninv2 = f2(-inv, -inv), q.s2 = f2(s, s);
   return q;
 }
-// Codes of four values x = -z: the int8 code is the low byte of RN(x / s) + 1.5 2^23 (|x / s| is at most
-// 127 (1 + 2^-22): nothing to saturate)
+// Codes of four values x = -z: the int8 code is the low byte of RN(x / s) + 1.5 2^23.  Of a FAST scale |x / s| is at
+// most 127 (1 + 2^-22): nothing to saturate.  A subnormal scale is rounded to so few bits (fp32 keys less a shift
+// reach them) that the quotient may be half as much again.
 template <int KIND, bool FAST>
 __device__ __forceinline__ uint32_t codes4(float z0, float z1, float z2, float z3, const Quant& q) {
   float y[4];
@@ -65,6 +66,10 @@ __device__ __forceinline__ uint32_t codes4(float z0, float z1, float z2, float z
     f2split(ffma2(ffma2(qb, q.s2, b), q.ninv2, qb), y[2], y[3]);
   } else if (q.s > 0.f) {
     y[0] = __fdiv_rn(-z0, q.s), y[1] = __fdiv_rn(-z1, q.s), y[2] = __fdiv_rn(-z2, q.s), y[3] = __fdiv_rn(-z3, q.s);
+    if (KIND == SAGE_KV_INT8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = fminf(fmaxf(y[i], -127.f), 127.f);
+    }
   } else {
     return 0u;
   }

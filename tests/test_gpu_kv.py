@@ -144,6 +144,25 @@ def test_append_extreme_values(kind):
         same_state(c, r)
 
 
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("top", [60, 100, 190, 700, 2000, 40000])
+def test_append_saturates_where_the_scale_is_subnormal(top, kind):
+    """Keys that a shift leaves at `top` units of 2^-149, below what their bf16 form can be: the scale has one or a
+    few bits, quotients pass the largest code and saturate.  Tokens that let the scale grow follow."""
+    rng = np.random.default_rng(14)
+    c, r = pair(4, 2, 64, 1, 4, 16, kind, poison=False)
+    v = torch.zeros((1, 2, 5, 64), dtype=torch.bfloat16)
+    for grow in (1, 3, 2 ** 20):
+        units = rng.integers(-top, top + 1, (2, 64))
+        units[:, 0], units[:, 1] = top, -top
+        shift = np.float32(units * grow * 2.0 ** -149)
+        pos = sa.kv_extend(c, dev([5]))
+        rpos, _ = r.extend([5])
+        sa.kv_append(c, v.cuda(), v.cuda(), pos, dev([5]), k_shift=dev(shift, torch.float32))
+        r.append(v.float().numpy(), v.float().numpy(), rpos, [5], shift=shift)
+        same_state(c, r)
+
+
 def test_append_slots_and_padding():
     """Rows that belong to other slots, rows without tokens, NaN behind the tokens that count."""
     rng = np.random.default_rng(11)
