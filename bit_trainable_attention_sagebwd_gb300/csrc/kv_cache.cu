@@ -568,9 +568,9 @@ __global__ void __launch_bounds__(256) kv_move_kernel(const sage_kv_cache c, con
     const size_t s = i / c.max_pages, j = i % c.max_pages;
     if ((long long)j * c.page < c.lengths[s]) {
       const int page = c.table[i];
-      const bool ok = (unsigned)page < (unsigned)c.n_pages;
-      to.table[i] = ok ? number[page] : -1;
-      if (!ok) kv_error(c.status, kDevIndex);
+      const int now = (unsigned)page < (unsigned)c.n_pages ? number[page] : -1;
+      to.table[i] = now;
+      if (now < 0) kv_error(c.status, kDevIndex);  // out of range, or free and not moved
     }
   }
   for (size_t i = t; i < (size_t)c.n_slots; i += nt) to.lengths[i] = c.lengths[i];

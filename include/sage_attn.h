@@ -381,6 +381,7 @@ int sage_attn_kv_attention(const sage_kv_cache *cache, const void *Q, const int 
  *    D, kind, n_slots and max_pages, may differ in n_pages, and share no memory but, if the caller
  *    likes, the status word; errors go to the one of `cache`.  More live pages than `to` has:
  *    SAGE_ERR_NO_PAGES, and `to` is left alone.
+ *    A listed page that is out of range or free (refs 0) is -1 in the table of `to`, SAGE_ERR_INVALID_ARG.
  *    ws: sage_attn_kv_compact_ws_bytes(cache->n_pages) bytes, 16-byte aligned.
  */
 int sage_attn_kv_fork(const sage_kv_cache *cache, const int *src, void *stream);

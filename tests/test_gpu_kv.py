@@ -689,6 +689,25 @@ def test_compact_too_small_and_refusals():
         sa.kv_attention(q, c, slots=dev([0]))
 
 
+@pytest.mark.parametrize("bad", ["free", -1, 12, -2 ** 31])
+def test_compact_reports_listed_pages_that_are_not_live(bad):
+    rng = np.random.default_rng(16)
+    c, r = pair(12, 1, 64, 2, 6, 16, "int8", poison=False)
+    fill(c, r, rng, [40, 20])
+    to, _ = pair(12, 1, 64, 2, 6, 16, "int8", poison=False)
+    if bad == "free":
+        c.refs[int(r.table[0, 1])] = 0
+    else:
+        c.table[0, 1] = bad
+    sa.kv_compact(c, to)
+    assert sa.get_status(c.status) == sa.SAGE_ERR_INVALID_ARG
+    assert sa.get_status(to.status) == sa.SAGE_OK
+    assert int(to.table[0, 1]) == -1 and (to.table[0, [0, 2]] >= 0).all() and (to.table[1, :2] >= 0).all()
+    q, _ = bf16(rng, (2, 1, 1, 64))
+    sa.kv_attention(q, to)                # and what reads it says so too
+    assert sa.get_status(to.status) == sa.SAGE_ERR_INVALID_ARG
+
+
 # ------------------------------------------------------------------------------ together
 
 def test_serving_run_in_graphs_and_streams():
