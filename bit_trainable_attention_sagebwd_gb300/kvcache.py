@@ -118,6 +118,14 @@ def _returned(stream, cache, *tensors):
             t.record_stream(now)
 
 
+def _workspace(ws, cache):
+    """The checks of a workspace that the caller gives: all of its bytes are written, one behind the other."""
+    if ws.device != cache.device:
+        raise ValueError(f"ws: on {ws.device}, the cache is on {cache.device}")
+    if not ws.is_contiguous():
+        raise ValueError("ws: not contiguous")
+
+
 def _slot_array(t, name, cache):
     return _arg(t, name, cache._i32, cache._slots_shape, cache.device)
 
@@ -167,8 +175,8 @@ def kv_attention(q, cache, causal=True, slots=None, q_len=None, sm_scale=None, o
     dev = cache.device
     if ws is None:
         ws = _alloc(stream, alloc_kv_ws, cache, B, H, Nq)
-    elif ws.device != dev:
-        raise ValueError(f"ws: on {ws.device}, the cache is on {dev}")
+    else:
+        _workspace(ws, cache)
     if o is None:
         o = _alloc(stream, torch.empty_like, q)
         _returned(stream, cache, o)
@@ -221,6 +229,6 @@ def kv_compact(cache, to, ws=None, stream=None):
         raise ValueError(f"to: on {to.device}, the cache is on {cache.device}")
     if ws is None:
         ws = _alloc(stream, alloc_kv_compact_ws, cache)
-    elif ws.device != cache.device:
-        raise ValueError(f"ws: on {ws.device}, the cache is on {cache.device}")
+    else:
+        _workspace(ws, cache)
     _call(cache._lib.sage_attn_kv_compact, cache, stream, cache._ref, to._ref, ws.data_ptr(), ws.nbytes)

@@ -708,6 +708,28 @@ def test_compact_reports_listed_pages_that_are_not_live(bad):
     assert sa.get_status(to.status) == sa.SAGE_ERR_INVALID_ARG
 
 
+def test_workspaces_with_gaps_are_refused():
+    """A strided view has the bytes asked for, but not one behind the other."""
+    rng = np.random.default_rng(20)
+    c, r = pair(8, 1, 64, 2, 4, 16, "int8", poison=False)
+    fill(c, r, rng, [20, 9])
+    to = sa.kv_cache(8, 1, 64, 2, 4, page=16)
+    q, _ = bf16(rng, (2, 1, 1, 64))
+    for ws, call in ((sa.alloc_kv_ws(c, 2, 1, 1), lambda w: sa.kv_attention(q, c, ws=w)),
+                     (sa.alloc_kv_compact_ws(c), lambda w: sa.kv_compact(c, to, ws=w))):
+        big = torch.full((2 * ws.numel(),), 77, dtype=torch.uint8, device="cuda")
+        with pytest.raises(ValueError, match="contiguous"):
+            call(big[::2])
+        torch.cuda.synchronize()
+        assert (big == 77).all()
+        call(big[:ws.numel()])
+        with pytest.raises(sa.SageError):
+            call(ws[:-1])
+        with pytest.raises(ValueError):
+            call(ws.cpu())
+    assert sa.get_status(c.status) == sa.SAGE_OK
+
+
 # ------------------------------------------------------------------------------ together
 
 def test_serving_run_in_graphs_and_streams():
