@@ -537,6 +537,54 @@ def test_join_leaves_units_whose_parts_were_not_written(B, hkv, g, nq, d):
     assert ((go - want_o).abs() <= tol).all() and ((gl - want_l).abs() <= 2.0 ** -19 * (1 + want_l.abs())).all()
 
 
+@pytest.mark.parametrize("nq", [3, 40])
+def test_attention_query_counts_out_of_range(nq):
+    """q_len below 0 counts as 0, above Nq as Nq."""
+    rng = np.random.default_rng(22)
+    c, r = pair(30, 2, 128, 3, 8, 32, "int8")
+    fill(c, r, rng, [50, 7, 120])
+    q, qf = bf16(rng, (3, 4, nq, 128))
+    for given, counts in (([-5, nq + 9, 2], [0, nq, 2]), ([2 ** 31 - 1, -2 ** 31, nq], [nq, 0, nq])):
+        o, lse = torch.full_like(q, 7.0), torch.full((3, 4, nq), 7.0, device="cuda")
+        sa.kv_attention(q, c, q_len=dev(given), o=o, lse=lse)
+        torch.cuda.synchronize()
+        assert sa.get_status(c.status) == sa.SAGE_OK
+        compare(o, lse, r.attention(qf.astype(np.float64), True, None, counts), 120, 128)
+
+
+@pytest.mark.parametrize("d,g,nq", [(64, 1, 1), (128, 4, 4), (128, 1, 40)])
+def test_attention_most_batch_rows(d, g, nq):
+    """4096 rows over 40 slots, each kernel."""
+    rng = np.random.default_rng(23)
+    c, r = pair(64, 1, d, 40, 4, 16, "int8")
+    fill(c, r, rng, 1 + np.arange(40) % 33)
+    slots = np.arange(4096) % 40
+    q, qf = bf16(rng, (4096, g, nq, d))
+    o, lse = sa.kv_attention(q, c, slots=dev(slots))
+    torch.cuda.synchronize()
+    assert sa.get_status(c.status) == sa.SAGE_OK
+    some = list(range(40)) + [2047, 3333, 4095]
+    compare(o[some], lse[some], r.attention(qf[some].astype(np.float64), True, slots[some]), 33, d)
+
+
+def test_attentions_at_once_over_one_cache():
+    """Calls on two streams, each with its own workspace, read one cache at the same time."""
+    rng = np.random.default_rng(24)
+    c, r = pair(300, 2, 128, 3, 150, 32, "e4m3")
+    fill(c, r, rng, [50, 4500, 120])
+    many, manyf = bf16(rng, (3, 4, 20, 128))
+    one, onef = bf16(rng, (3, 4, 1, 128))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        x, y, z = sa.kv_attention(many, c, stream=a), sa.kv_attention(one, c, stream=b), sa.kv_attention(many, c, stream=b)
+    torch.cuda.synchronize()
+    assert sa.get_status(c.status) == sa.SAGE_OK
+    compare(*x, r.attention(manyf.astype(np.float64)), 4500, 128)
+    compare(*y, r.attention(onef.astype(np.float64)), 4500, 128)
+    assert torch.equal(x[0], z[0]) and torch.equal(x[1], z[1])
+
+
 def test_attention_offsets_past_32_bits():
     """A pool of more than 2^32 codes, the sequence in its last pages."""
     rng = np.random.default_rng(10)

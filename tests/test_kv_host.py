@@ -174,3 +174,81 @@ def test_the_selftest_of_the_join_refuses_bad_arguments(lib):
         assert call(**over) == sa.SAGE_ERR_INVALID_ARG
     for over in (dict(B=0), dict(H=3), dict(Nq=0), dict(c=cache(D=96))):
         assert call(**over) == sa.SAGE_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------------------ what the formats cost
+
+def stored(kind, page, n, step, seed, d=64):
+    """Keys and values, each page's tokens of a size of their own that rises and falls, written `step` tokens at a
+    time: the cache, the bf16 values, and for each token and head the scales of its page since it was written."""
+    rng = np.random.default_rng(seed)
+    c = kv_ref.Cache(-(-n // page), 2, d, 1, -(-n // page), page, kind)
+    size = np.exp(rng.uniform(-2, 2, (1, 1, n, 1)))
+    k, v = (torch.from_numpy((rng.standard_normal((1, 2, n, d)) * size).astype(np.float32)).to(torch.bfloat16).float().numpy()
+            for _ in range(2))
+    since = np.zeros((2, 2, n, n), np.float32)  # [K or V, head, token, write]: the page's scale after it, 0: not yet there
+    at = 0
+    while at < n:
+        m = min(step, n - at)
+        pos, _ = c.extend([m])
+        c.append(k[:, :, at:at + m], v[:, :, at:at + m], pos, [m])
+        pages = c.table[0, np.arange(at + m) // page]
+        since[0, :, :at + m, at], since[1, :, :at + m, at] = c.k_scale[pages].T, c.v_scale[pages].T
+        at += m
+    return c, k[0], v[0], since
+
+
+def rounding(kind, x, since):
+    """How far a stored value may be from x: half a step of its code at each scale that its page has had since
+    (the code is rounded anew only where the scale changes), and fp32's roundings of scale, quotient and product.  int8: a
+    step is the scale; e4m3: 2^-3 of the value down to 2^-6 of the unit, below it 2^-9 of the scale."""
+    changed = np.concatenate((since[..., :1] > 0, (since[..., 1:] != since[..., :-1])), -1)
+    s = np.where(changed, since, 0).astype(np.float64)[:, :, None, :]       # [head, token, 1, write]
+    bound = np.zeros(x.shape)
+    for w in range(s.shape[-1]):
+        half = 0.5 * s[..., w] if kind == "int8" else np.where(s[..., w] > 0, np.maximum(2.0 ** -4 * (np.abs(x) + bound), 2.0 ** -10 * s[..., w]), 0)
+        bound += half + 2.0 ** -22 * np.where(s[..., w] > 0, np.abs(x) + bound, 0)
+    return bound
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("step", [1, 7, 100])
+def test_stored_values_are_within_the_formats_rounding(kind, page, step):
+    """One write of a prompt is off by half a step; token by token each growth of the page's scale adds another
+    half step, and the scales end up the same."""
+    n = 100
+    c, k, v, since = stored(kind, page, n, step, page + step)
+    once, *_ = stored(kind, page, n, n, page + step)
+    pages = [np.arange(n) // page]
+    for h in range(2):
+        for x, got, was in zip((k, v), c.values(0, h), since):
+            bound = rounding(kind, x, was)[h]
+            assert np.all(np.abs(got - x[h]) <= bound)
+            if step == n:  # the definition: no value of a page needs a larger step
+                top = np.array([np.abs(x[h][pages[0] == p]).max() for p in pages[0]])
+                worst = top / 254 if kind == "int8" else np.maximum(2.0 ** -4 * np.abs(x[h]).max(1), top / 448 * 2.0 ** -10)
+                # (int8: |x| is up to 127 steps, so 2^-22 |x| is up to 254 x 2^-22 < 2^-14 of half a step)
+                assert np.all(bound.max(1) <= worst * (1 + 2.0 ** -13))
+    assert np.array_equal(c.k_scale, once.k_scale) and np.array_equal(c.v_scale, once.v_scale)
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("step", [1, 100])
+def test_attention_over_stored_values_against_the_keys_themselves(kind, step):
+    """Every logit is off by sm_scale sum |q| dk at most, dk the stored key's rounding; weights by e to twice the
+    largest of these, O by that and by the values' own rounding."""
+    rng = np.random.default_rng(step)
+    n, d = 100, 64
+    c, k, v, since = stored(kind, 64, n, step, 5, d)
+    dk, dv = rounding(kind, k, since[0]), rounding(kind, v, since[1])
+    q = rng.standard_normal((1, 2, 1, d)) * 0.2
+    o, lse, *_ = c.attention(q)
+    for h in range(2):
+        t = k[h] @ q[0, h, 0] / np.sqrt(d)
+        far = (dk[h] @ np.abs(q[0, h, 0])).max() / np.sqrt(d)
+        p = np.exp(t - t.max())
+        p /= p.sum()
+        bound = (np.exp(2 * far) - 1) * (p @ np.abs(v[h])) + np.exp(2 * far) * (p @ dv[h])
+        assert np.all(np.abs(o[0, h, 0] - p @ v[h]) <= bound)
+        assert abs(lse[0, h, 0] - (t.max() + np.log(np.exp(t - t.max()).sum()))) <= far
