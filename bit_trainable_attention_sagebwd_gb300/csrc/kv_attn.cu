@@ -76,6 +76,9 @@ __device__ __forceinline__ void pairs(uint32_t w, uint32_t& first, uint32_t& sec
         : "=r"(first), "=r"(second)
         : "r"(w));
 }
+// A maximum above this one raises the reference m.  Rounded down, no fp32 lies between it and m + kRaise; to nearest
+// it would pass m + kRaise from 2^25 on, and P 2^15.  (Known before the maximum is: its difference from m is not.)
+__device__ __forceinline__ float raise_past(float m) { return __fadd_rd(m, kRaise); }
 // transpose of an 8 x 8 block of 16-bit values held one row pair per lane
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
   const bool halves = c.page < kChunk;  // a chunk is two pages of 16 tokens
   int b = row_at(pre, p.B, begin);
   FewSeg ns = seg_at(begin, b);    // the next window: window nw of part ns, nn chunks of this warp in it
-  int nw = 0, nn = chunks_of(ns), next_page = -1, next_half = -1;
+  int nw = 0, nn = chunks_of(ns), next_page = -1, next_half = -1, next_keys = 0;  // (keys from the lane's chunk on)
   bool have_next = true;
   int left = 0, at_i = 0;          // chunks of the window that are still to be copied, and the next one's lane
   int w_page = -1, w_half = -1, w_row = 0;  // the lane's chunk: page (-1: no keys), that of its second half, row
@@ -185,8 +188,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
   auto load_window = [&]() {
     const int k = nw * 32 + lane, token = (ns.c0 + warp + kWarps * k) * kChunk;
     const int* row = c.table + (size_t)ns.slot * c.max_pages + (token >> page_shift);
-    next_page = k < nn && token < ns.len ? row[0] : -1;
-    next_half = halves && k < nn && token + 16 < ns.len ? row[1] : -1;
+    next_keys = k < nn ? ns.len - token : 0;
+    next_page = next_keys > 0 ? row[0] : -1;
+    next_half = halves && next_keys > 16 ? row[1] : -1;
   };
   auto next_window = [&]() {
     if (++nw * 32 >= nn) {
@@ -209,11 +213,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
     if (enter) {
       w_page = (unsigned)next_page < (unsigned)c.n_pages ? next_page : -1;
       w_half = (unsigned)next_half < (unsigned)c.n_pages ? next_half : -1;
-      // (by the tokens, not by next_page: a table may say -1 where there are keys)
-      const int k = nw * 32 + lane, token = (ns.c0 + warp + kWarps * k) * kChunk;
-      if (k < nn && ((w_page < 0 && token < ns.len) || (halves && w_half < 0 && token + 16 < ns.len)))
-        atomicMax(c.status, kDevIndex);
-      w_row = ns.hk * c.page + (token & (c.page - 1));
+      // (by the keys that are there, not by next_page: a table may say -1 among them)
+      if ((next_keys > 0 && w_page < 0) || (halves && next_keys > 16 && w_half < 0)) atomicMax(c.status, kDevIndex);
+      w_row = ns.hk * c.page + (((ns.c0 + warp + kWarps * (nw * 32 + lane)) * kChunk) & (c.page - 1));
       const int second = halves ? w_half : w_page;
       if (w_page >= 0) {
         ks[0] = c.k_scale[(size_t)w_page * c.Hkv + ns.hk];
@@ -420,8 +422,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
             }
             mx[t][e] = max3(mx[t][e], s[h][t][e], s[h][t][2 + e]);
           }
-          // (the difference, not m + kRaise, which rounds past it from 2^25 on; -inf less -inf is NaN: false)
-          raise |= mx[t][e] - m[t][e] > kRaise;
+          raise |= mx[t][e] > raise_past(m[t][e]);
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float to = x - m[t][e] > kRaise ? x - kBelow : m[t][e];
+            const float to = x > raise_past(m[t][e]) ? x - kBelow : m[t][e];
             corr[e] = to == m[t][e] ? 1.f : ex2(m[t][e] - to);
             m[t][e] = to;
             l[t][e] *= corr[e];
