@@ -127,8 +127,6 @@ __global__ void __launch_bounds__(append_threads(D, P) * append_pages(D, P), 102
   }
   const int pos = p.pos[slot], n = p.n_new[slot], len = p.c.lengths[slot];
   if (pos < 0 || n <= 0) return;  // nothing new, or refused by sage_attn_kv_extend
-  // the table says nothing behind the slot's length: what is listed there may be another slot's page
-  const bool room = n <= p.Nn && (long long)pos + n <= len;
   const int j = pos / P + blockIdx.x * kPages + group;
   const long long t0 = (long long)j * P;
   // the new tokens are on their way while the table is read
@@ -142,7 +140,7 @@ __global__ void __launch_bounds__(append_threads(D, P) * append_pages(D, P), 102
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int r = r0 + i * RPP;
-    if (r >= off && r < end && room) u[i] = reinterpret_cast<const uint4*>(src + (size_t)r * D)[g];
+    if (r >= off && r < end && n <= p.Nn) u[i] = reinterpret_cast<const uint4*>(src + (size_t)r * D)[g];
   }
   // a batch row that names a slot again is left out
   if (p.slots) {
@@ -154,9 +152,11 @@ __global__ void __launch_bounds__(append_threads(D, P) * append_pages(D, P), 102
     }
   }
   if (end == 0) return;
-  const int page = room && j < p.c.max_pages ? p.c.table[(size_t)slot * p.c.max_pages + j] : -1;
-  // tokens without room, a page that is not there, or that another slot lists too: not written
-  if ((unsigned)page >= (unsigned)p.c.n_pages || p.c.refs[page] != 1) {
+  const int page = n <= p.Nn && j < p.c.max_pages ? p.c.table[(size_t)slot * p.c.max_pages + j] : -1;
+  // Tokens past the slot's length, a page that is not there, or that another slot lists too: not written.  Behind the
+  // length the table says nothing: what it lists there may be another slot's page.
+  const bool room = n <= len && pos <= len - n;
+  if (!room || (unsigned)page >= (unsigned)p.c.n_pages || p.c.refs[page] != 1) {
     if (tid == 0) kv_error(p.c.status, kDevIndex);
     return;
   }
