@@ -51,8 +51,8 @@ def test_the_first_call_of_a_host_thread():
 
     def buffers():
         new = {x: torch.zeros_like(q) for x in ("o", "dq", "dk", "dv", "kv_o")}
-        new |= {x: torch.zeros((B, H, N), device="cuda") for x in ("lse", "kv_lse")}
-        return new | dict(one_o=torch.zeros_like(one), one_lse=torch.zeros((B, H, 1), device="cuda"))
+        new |= {x: torch.zeros((B, H, N), dtype=torch.float32, device="cuda") for x in ("lse", "kv_lse")}
+        return new | dict(one_o=torch.zeros_like(one), one_lse=torch.zeros((B, H, 1), dtype=torch.float32, device="cuda"))
 
     here, there = buffers(), buffers()
     kv_ws, one_ws, bws = sa.alloc_kv_ws(c, B, H, N), sa.alloc_kv_ws(c, B, H, 1), sa.alloc_bwd_ws(B, H, N, D)
