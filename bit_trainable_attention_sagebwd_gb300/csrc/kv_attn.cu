@@ -10,7 +10,7 @@
 //    equal parts for a grid that fills the GPU once; a unit that is cut leaves partial results,
 //    joined by kv_join_kernel in the order of the parts.  Ragged batches and single long
 //    sequences load every SM alike.  Every unit begins with kPad places without a chunk, for the time
-//    that its start takes.
+//    that its start takes; on a line too short to fill the GPU some parts are padding alone.
 //  - A warp walks its own chunks and keeps kStages - 1 of them in flight with TMA, across the ends of
 //    units, in a ring of its own: a chunk of K or V is one box of a page's [head, token] rows (two with
 //    pages of 16 tokens).  (Copies of 16 bytes a thread, cp.async, read the same bytes at 5.6 TB/s against 6.7.)
@@ -24,7 +24,7 @@
 //    rounding.  Statistics, scales and sums are fp32.
 //
 // Measured, 32 query heads over 8 of D = 128, the join included: one token for each of 64 sequences of 500 to
-// 8192 tokens (int8, 0.57 GB) in 96 us, of 4 of 100k to 131k (e4m3, 0.95 GB) in 161 us: 5.9 TB/s, 87 % of
+// 8192 tokens (int8, 0.57 GB) in 95 us, of 4 of 100k to 131k (e4m3, 0.95 GB) in 159 us: 5.9 TB/s, 87 % of
 // the rate of a plain copy.  What is left is the start of the units and the join.  With one to four queries each
 // (16 rows, 16 sequences of 900 to 16k tokens, 0.28 GB) 62 us, 4.6 TB/s: eight warps of 255 registers issue
 // in half of the cycles, the ALU (codes into fp16) at 51 %, and neither more warps nor fewer
@@ -53,7 +53,9 @@ constexpr int kStages = kThreeCtas<D, RT> ? 2 : 3;
 template <int D, int RT>
 constexpr int kCtasPerSm = kThreeCtas<D, RT> ? 3 : 2;
 // What the start of a unit costs a CTA, in chunks of the line.  64 sequences of 500 to 8192 tokens took
-// 109 us without, 101 us with 4, 99 us with 8 to 16; 256 of 100 to 1000 110, 93, 83 and 82 us.
+// 109 us without, 101 us with 4, 99 us with 8 to 16; 256 of 100 to 1000 110, 93, 83 and 82 us.  Lines that do
+// not fill the GPU are cut with it too, at a cost: one sequence of 700 tokens on 8 heads is 48 parts, two of each
+// head's six without a chunk.
 constexpr int kPad = 12;
 
 // D (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16)
@@ -137,9 +139,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<D, RT>)
   });
   __syncthreads();
   const long long total = pre[p.B];
-  // A part has a chunk for each warp where the units allow it.  A line that does not fill the GPU, or
-  // is one sequence's, is cut so that the parts of units of one length end with them: a part that goes
-  // on into another unit costs its CTA another start.
+  // As many parts as give each warp a chunk where the units allow it (counted without the padding, which then
+  // takes parts of its own: see kPad).  A line that does not fill the GPU, or is one sequence's, is cut so that the
+  // parts of units of one length end with them: a part that goes on into another unit costs its CTA another start.
   const long long units = (long long)p.B * per_b;
   int parts = (int)min((long long)p.most_parts, max(units, (total - kPad * units + kWarps - 1) / kWarps));
   if (parts < p.most_parts || p.B == 1) {
@@ -762,6 +764,8 @@ int launch_few(AttnParams p, int sms, cudaStream_t st) {
     return 3;
   // The kernel's limit is the process's: always the same one, for the most batch rows, or a call of another
   // thread could lower it before this launch.
+  // (16 bytes for each batch row: at D = 128 two CTAs of the grid share an SM up to 701 rows at 8 query rows, 445 at
+  // 16; beyond, the line goes over the GPU in two turns.)
   const size_t ring = 1024 + (size_t)kWarps * Ring<D, RT>::kWarpBytes, most = ring + ((size_t)kKvMaxBatch + 1) * 16;
   const size_t smem = ring + ((size_t)p.B + 1) * 16;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess) return 3;

@@ -183,7 +183,7 @@ constexpr int kChunkRows = 256;        // query rows of a unit, many
 
 }  // namespace
 
-// the kernel of a few (up to 16) query rows a unit, and the one of kChunkRows
+// the kernel of up to 16 query rows a unit (up to 32 of a shared head, in two units), and the one of kChunkRows
 int launch_kv_few(const AttnParams& p, int kind, int rows, int sms, cudaStream_t st);
 int launch_kv_chunk(const AttnParams& p, int kind, int sms, cudaStream_t st);
 

@@ -7,8 +7,8 @@
 // into `refs` and the maximum of the status word, whose results do not depend on their order.
 //
 // All of it is bound by memory or, in small calls, by the launches.  Measured: kv_append of two prompts of
-// 20k to 32k tokens (8 heads, D = 128, e4m3, 0.32 GB) 53.5 us, 6.1 TB/s, 89 % of the rate of a plain
-// copy; of one token for each of 64 sequences 5.2 us, a launch and its three dependent loads.  fork, extend
+// 20k to 32k tokens (8 heads, D = 128, e4m3, 0.32 GB) 52 us, 6.2 TB/s, 92 % of the rate of a plain
+// copy; of one token for each of 64 sequences 6.3 us from Python, a launch and its three dependent loads.  fork, extend
 // and truncate of 32 prompts into 256 sequences (67 MB of copied pages) 20 us, of which extend's one CTA
 // and the copies are 8 us and 9 us.  kv_compact of 2.7 GB of reads and writes 415 us, 6.5 TB/s, 95 %.
 #include <cuda_bf16.h>
@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(256) kv_cow_kernel(const sage_kv_cache c, cons
 // ------------------------------------------------------------------------------ compact
 
 // ws: int count, then (256-byte aligned) int number[n_pages] (the new number of a live page, -1
-// of a free one) and int live[n_pages] (the live pages in order)
+// of a free one) and int live[n_pages] (the live pages in order).  One CTA: 16 pages a thread and step, an
+// int at a time.  For pools of 10^5 pages and more the steps, one behind the other, would count.
 __global__ void __launch_bounds__(kScanThreads) kv_rank_kernel(const sage_kv_cache c, int to_pages,
                                                                int* __restrict__ count, int* __restrict__ number,
                                                                int* __restrict__ live) {

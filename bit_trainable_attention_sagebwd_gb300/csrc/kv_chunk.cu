@@ -16,7 +16,8 @@
 // Units are cut over the grid like those of the few-row kernel (kv_attn.cu), in 128-key tiles.
 //
 // Measured: the newest 2048 queries of 32 heads on 32k keys of 8 (D = 128, e4m3, 1.07 TFLOP) in 0.90 to
-// 0.92 ms, 1.17 PFLOP/s, 61 % of the rate of a large library product; DRAM is idle (0.26 GB).  The tensor core
+// 0.92 ms, 1.17 PFLOP/s, 61 % of a large library product's rate in a burst, 68 % of its sustained one; DRAM is idle
+// (0.26 GB).  The tensor core
 // works for half of the time and the issue slots are taken for two thirds of it: the conversion of the codes
 // (0.78 ms without it) and the exponentials share the SM's instruction slots.  The conversion
 // instruction for e4m3 in place of shifts took 1.22 ms, a wider softmax (896 threads) was slower.

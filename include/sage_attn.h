@@ -307,7 +307,8 @@ int sage_attn_fp4_bwd(const void *Q, const void *K, const void *V, const void *O
  * The order of a serving step: sage_attn_kv_extend (room for the new tokens), sage_attn_kv_append
  * (their keys and values), sage_attn_kv_attention (their queries).  All sizes that change from step to
  * step are read on the device, so a captured CUDA graph of the step can be replayed.  Calls that
- * change one cache, or use one workspace, must not overlap on the GPU.
+ * change one cache, or use one workspace, must not overlap on the GPU; attention calls on one cache may.  Host
+ * threads may call at the same time.
  */
 typedef enum { SAGE_KV_INT8 = 0, SAGE_KV_E4M3 = 1 } sage_kv_kind;
 
@@ -333,7 +334,9 @@ typedef struct sage_kv_cache {
  * Per (page, head), with a = max|x| over the call's tokens in the page and r = RN32(1/127) (INT8) or
  * RN32(1/448) (e4m3): s = RN32(a r) if the page holds no earlier token, else max(its scale, RN32(a r));
  * code = rint(RN32(x / s)) or e4m3(RN32(x / s)), saturating.  Where s has grown, an earlier code c becomes
- * the code of RN32(c s_old) under s.  A block whose s is 0 has codes 0.  Values must be finite.
+ * the code of RN32(c s_old) under s.  A block whose s is 0 has codes 0.  Values must be finite, which is not
+ * checked: a block's scale passes a NaN over; its code is any in int8, and in e4m3 NaN, which attention answers with
+ * NaN up to 32 query rows of a shared head and reads as +-480 beyond.
  * A slot's tokens are written in order: what a page holds behind the call's tokens counts as not written yet.
  * Not written, with SAGE_ERR_INVALID_ARG in the status word: tokens of a slot without room for all of them
  * (pos[s] + n_new[s] past lengths[s], to which sage_attn_kv_extend has raised it, or n_new[s] past Nn); a page
@@ -346,13 +349,15 @@ int sage_attn_kv_append(const sage_kv_cache *cache, const void *K, const void *V
  * Attention of queries over the cache.  Q: bf16 [B, H, Nq, D], query head h reads key/value head
  * h / (H / Hkv); O as Q, LSE fp32 [B, H, Nq], all apart in memory.  Batch row b reads slot slots[b] (NULL:
  * slot b; a slot may be named by several rows); its first q_len[b] queries count (q_len int32 [B], values
- * outside 0 .. Nq count as the nearest; NULL: Nq), rows behind them are neither read nor written.  With len = lengths[slot]: causal (causal != 0) lets query i see
- * keys j <= len - q_len + i, as for the newest q_len tokens of the sequence; otherwise every query sees
- * all len keys (an encoder's states of another length).
+ * outside 0 .. Nq count as the nearest; NULL: Nq), rows behind them are neither read nor written.  With
+ * len = lengths[slot]: causal (causal != 0) lets query i see keys j <= len - q_len + i, as for the newest q_len
+ * tokens of the sequence; otherwise every query sees all len keys (an encoder's states of another length).
+ * The keys of a page number out of range are left out, a slot or length out of range counts as no keys
+ * (SAGE_ERR_INVALID_ARG in the status word).
  * S = sm_scale q . k, O = softmax(S) V, LSE = log sum e^S; a row that sees no key has O = 0 and
  * LSE = -infinity.  Codes and queries enter the products exactly (a query's elements below 2^-25 of its
  * largest are rounded); P is rounded to fp16 relative to the running maximum; everything else is fp32.
- * V scales below 2^-80 are read as 2^-80.  sm_scale <= 0 selects 1/sqrt(D).
+ * V scales below 2^-80 are read as 2^-80.  sm_scale <= 0 selects 1/sqrt(D).  A query row with a NaN is NaN.
  * ws: sage_attn_kv_ws_bytes(B, H, Hkv, D, Nq) bytes, 16-byte aligned, contents free before and after.
  * Deterministic: the same call on the same state gives the same bits (another batch may cut the keys
  * elsewhere and differ in the last ones).  B is at most 4096.
@@ -371,8 +376,8 @@ int sage_attn_kv_attention(const sage_kv_cache *cache, const void *Q, const int 
  *  - extend: room for n_new[s] >= 0 more tokens: pos[s] = lengths[s], lengths[s] += n_new[s].  The pages
  *    it takes are the free pages with the lowest numbers, in slot order.  A last page that is partly
  *    filled and listed by another slot too is first copied to a page of the slot's own; cow[s] = the page
- *    it was copied from (else -1).  Slots are served while the needs of the slots up to them fit in the
- *    free pages; one that is not served has pos[s] = -1 and is otherwise left alone
+ *    it was copied from (else -1).  A slot is served if it needs no page, or if the needs of all slots up to it
+ *    fit in the free pages; one that is not served has pos[s] = -1 and is otherwise left alone
  *    (SAGE_ERR_NO_PAGES; past max_pages pages: SAGE_ERR_INVALID_ARG).  n_new, pos and cow are apart.
  *  - truncate: slot s with keep[s] >= 0 keeps its first min(keep[s], lengths[s]) tokens and gives the
  *    pages behind them back (refs - 1); keep[s] = 0 frees the slot.
