@@ -42,7 +42,7 @@ inline bool make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType
   };
   CUresult r = encode();
   if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
-    // a host thread that has not used its device yet: the driver's call, unlike the runtime's, does not make
+    // a host thread that has not used its device yet: the encoding, unlike a call of the CUDA runtime, does not make
     // the device's context current by itself (cudaSetDevice does)
     int dev = 0;
     if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
