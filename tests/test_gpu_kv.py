@@ -275,6 +275,17 @@ def test_attention_groups_and_queries(hkv, g, nq, d, kind):
     check_attention(c, r, rng, hkv * g, nq, False, slots[:4], None, sm_scale=0.3)
 
 
+@pytest.mark.parametrize("g,nq", [(33, 1), (100, 2), (128, 1), (300, 1), (257, 3)])
+@pytest.mark.parametrize("page,d,kind", [(16, 128, "e4m3"), (128, 64, "int8")])
+def test_attention_groups_wider_than_a_row_tile(page, d, kind, g, nq):
+    """One key/value head for so many query heads that a token's rows fill a unit, or lie in several."""
+    rng = np.random.default_rng(g + page)
+    c, r = pair(700 // page + 8, 1, d, 3, 500 // page + 1, page, kind)
+    fill(c, r, rng, [333, 1, 64])
+    check_attention(c, r, rng, g, nq, True, [2, 0, 1, 0], [nq, max(1, nq - 1), nq, 0])
+    check_attention(c, r, rng, g, nq, False)
+
+
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
 def test_attention_long(kind):
     """One sequence of 20,011 tokens among short ones: cut over the whole GPU."""
