@@ -36,7 +36,7 @@ ABI_FUNCTIONS = ("sage_attn_ws_bytes", "sage_attn_bwd_ws_bytes", "sage_attn_quan
                  "sage_attn_fp4_ws_views", "sage_attn_fp4_bwd_ws_bytes", "sage_attn_fp4_bwd",
                  "sage_attn_kv_append", "sage_attn_kv_ws_bytes", "sage_attn_kv_attention", "sage_attn_kv_fork",
                  "sage_attn_kv_extend", "sage_attn_kv_truncate", "sage_attn_kv_compact_ws_bytes",
-                 "sage_attn_kv_compact", "sage_attn_selftest_kv_join")
+                 "sage_attn_kv_compact", "sage_attn_selftest_kv_join", "sage_attn_packed_ws_bytes", "sage_attn_packed_fwd")
 
 
 class SageError(RuntimeError):
@@ -57,6 +57,10 @@ class sage_ws_views(ctypes.Structure):
 class sage_kv_cache(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "table", "lengths", "refs", "status")] + \
         [(n, ctypes.c_int) for n in ("n_pages", "Hkv", "page", "D", "n_slots", "max_pages", "kind")]
+
+
+class sage_rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("token", ctypes.c_longlong), ("head", ctypes.c_longlong)]
 
 
 _lib = None
@@ -120,6 +124,10 @@ def lib():
             L.sage_attn_kv_compact_ws_bytes.restype = sz
             L.sage_attn_kv_compact_ws_bytes.argtypes = [i]
             L.sage_attn_kv_compact.argtypes = [cp, cp, vp, sz, vp]
+            rp = ctypes.POINTER(sage_rows)
+            L.sage_attn_packed_ws_bytes.restype = sz
+            L.sage_attn_packed_ws_bytes.argtypes = [i] * 6
+            L.sage_attn_packed_fwd.argtypes = [rp] * 3 + [vp, rp, vp, vp, sz] + [i] * 6 + [fp, vp]
             L.sage_attn_ws_views.argtypes = [vp, i, i, i, i, ctypes.POINTER(sage_ws_views)]
             L.sage_attn_get_status.argtypes = [vp, vp]
             L.sage_attn_selftest_wait.argtypes = [vp, u64, vp]
@@ -246,6 +254,15 @@ def sage_attn_kv_compact_ws_bytes(n_pages):
 
 def sage_attn_kv_compact(cache, to, ws, ws_bytes, stream):
     return lib().sage_attn_kv_compact(cache, to, ws, ws_bytes, stream)
+
+
+def sage_attn_packed_ws_bytes(T, S, H, Hkv, D, backward):
+    return lib().sage_attn_packed_ws_bytes(T, S, H, Hkv, D, int(backward))
+
+
+def sage_attn_packed_fwd(Q, K, V, cu_seqlens, O, LSE, ws, ws_bytes, T, S, H, Hkv, D, causal, sm_scale, stream):
+    return lib().sage_attn_packed_fwd(Q, K, V, cu_seqlens, O, LSE, ws, ws_bytes, T, S, H, Hkv, D, int(causal),
+                                      float(sm_scale), stream)
 
 
 def sage_attn_bwd_noalloc(Q, K, V, O, LSE, dO, dQ, dK, dV, ws, B, H, N, D, causal, qk_norm, k_smooth, sm_scale,
@@ -666,3 +683,4 @@ def ws_tensors(ws, B, H, N, D, hkv=None, q_smooth=False, fp4=False) -> dict:
 
 from .kvcache import (KVCache, alloc_kv_compact_ws, alloc_kv_ws, kv_append, kv_attention, kv_cache,  # noqa: E402,F401
                       kv_compact, kv_extend, kv_fork, kv_truncate)
+from .packed import alloc_packed_ws, packed_forward  # noqa: E402,F401

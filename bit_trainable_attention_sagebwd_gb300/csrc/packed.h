@@ -1,0 +1,25 @@
+// Launchers of attention over packed sequences (the sage_attn_packed_* calls of include/sage_attn.h).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+#include "../../include/sage_attn.h"
+
+namespace sage {
+
+// Most sequences and tokens of one call, and most query heads of a key/value head (their rows share a tile).
+constexpr int kPackedMaxSeqs = 65536;
+constexpr int kPackedMaxTokens = 1 << 30;
+constexpr int kPackedMaxGroup = 128;
+
+struct PackedWs {
+  size_t cuts, part, total;  // (the status word comes first)
+};
+PackedWs packed_ws_layout(int T, int S, int H, int Hkv, int D, bool backward);
+
+int launch_packed_fwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V, const int* cu, const sage_rows& O,
+                      float* LSE, void* ws, int T, int S, int H, int Hkv, int D, int causal, float sm_scale,
+                      cudaStream_t st);
+
+}  // namespace sage

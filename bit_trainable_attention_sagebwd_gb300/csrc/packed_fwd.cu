@@ -1,0 +1,426 @@
+// Attention over packed sequences, forward: O = softmax(sm_scale Q K^T) V and LSE for every sequence of a packed
+// batch, in bf16 with fp32 sums (sage_attn_packed_fwd).
+//
+// One CTA an SM walks its share of the units (packed.cuh): two row tiles of 128 rows and the 128-key tiles that
+// they see.
+//  - warp 9 brings Q and K by TMA, warp 10 V; two key tiles deep;
+//  - warp 8 issues S = Q K^T and O += P V (fp32 accumulators in TMEM) for the two row tiles in turn, so the tensor
+//    core works on one while the softmax works on the other;
+//  - warps 0-3 and 4-7 own a row tile each, a thread a row: S from TMEM, P as bf16 back into TMEM over S's
+//    columns, from where the second product takes it.  With m the row's running reference, P = 2^(S a - m),
+//    a = sm_scale log2 e; m follows the maximum only when that has grown by 2^kRaise, so O is seldom rescaled.
+// TMA copies whole boxes: what lies behind a sequence's end is the next one's.  Rows of S behind it are not
+// stored, columns are masked; of V's rows those that a product reads (up to 15) are zeroed in shared memory, so that
+// nothing of another sequence, a NaN or an infinity among it, enters a sum.
+#include "issue.cuh"
+#include "launch.h"
+#include "packed.cuh"
+#include "timer.h"
+
+namespace sage {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRegsSoftmax = 208, kRegsIssue = 88;
+static_assert(2 * kRegsSoftmax + kRegsIssue <= 3 * 168, "the launch's registers");
+constexpr uint32_t kCols = 512, kColO = 256;  // TMEM: S of place t at 128 t, O at 256 + 128 t
+constexpr float kRaise = 8.f;
+
+struct FwdParams {
+  PackedShape s;
+  __nv_bfloat16* O;
+  long long o_token, o_head;
+  float* LSE;
+  float alpha;  // sm_scale log2 e
+};
+
+template <int D>
+struct FwdSmem {
+  uint8_t q[2][kTile * D * 2];
+  uint8_t k[2][kTile * D * 2];
+  uint8_t v[2][kTile * D * 2];
+  uint64_t bar_q_full[2], bar_q_empty[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_v_raw;
+  uint64_t bar_s[2], bar_p[2], bar_o[2], bar_o_read[2];
+  long long wsum[kThreads / 32];
+  long long pre[kPackedGroups + 1];
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(FwdSmem<128>) + 1024 <= 227 * 1024, "shared memory of a CTA");
+
+// The key tiles of a unit's two row tiles: place `t0` has the first row tile, the other one the second, if there is one.
+// Row tiles alone in their unit take the places in turns (`solo` counts them).
+struct Places {
+  int t0, rows;    // rows: row tiles
+  int end[2];      // by row tile: where its key tiles end
+  __device__ __forceinline__ Places(const PackedShape& p, const Part& s, int& solo) {
+    rows = (2 * s.i + 1) * p.w < s.len ? 2 : 1;
+    t0 = rows == 1 ? (solo++ & 1) : 0;
+    end[0] = p.causal ? min(s.c1, ceil_div(min(s.len, (2 * s.i + 1) * p.w), kTile)) : s.c1;
+    end[1] = rows == 2 ? s.c1 : 0;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_fwd_kernel(const FwdParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v) {
+  constexpr int kAtoms = D / 64;      // 128-byte columns of a tile row
+  constexpr int kAtom = kTile * 128;  // bytes of one
+  extern __shared__ uint8_t smem_raw[];
+  FwdSmem<D>& sm = *reinterpret_cast<FwdSmem<D>*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sm.bar_q_full[t], 1);
+      mbar_init(&sm.bar_q_empty[t], 1);
+      mbar_init(&sm.bar_k_full[t], 1);
+      mbar_init(&sm.bar_k_empty[t], 1);
+      mbar_init(&sm.bar_v_full[t], 1);
+      mbar_init(&sm.bar_v_empty[t], 1);
+      mbar_init(&sm.bar_s[t], 1);
+      mbar_init(&sm.bar_p[t], 128);
+      mbar_init(&sm.bar_o[t], 1);
+      mbar_init(&sm.bar_o_read[t], 128);
+    }
+    mbar_init(&sm.bar_v_raw, 1);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  pdl_wait();
+  if (warp == 8) {
+    tmem_alloc(&sm.tmem_base, kCols);
+    tmem_relinquish();
+  }
+  const int group = ceil_div(p.s.S, kPackedGroups);
+  prefix_of_sequences<kPairs, kThreads>(p.s, group, sm.pre, sm.wsum);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // dependents may come once this CTA holds its TMEM: a later kernel that allocates all columns
+  // must not reach this SM before
+  pdl_trigger();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+  const long long total = sm.pre[kPackedGroups];
+  const Line line{total, (int)min((long long)gridDim.x, max(total, 1ll))};
+  const int w0 = blockIdx.x;
+  const bool idle = total == 0 || w0 >= line.parts;
+  const long long begin = idle ? 0 : line.start(w0), stop = idle ? 0 : line.start(w0 + 1);
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
+  int solo = 0;
+
+  if (warp >= 8) {
+    regs_decrease<kRegsIssue>();
+    if (warp == 8) {
+      // ---------------- MMA issuer
+      constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_o = idesc_bf16(kTile, D, false, true);
+      constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
+      const uint64_t dq = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), dk = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024);
+      const uint64_t dv = sdesc_sw128(smem_u32(sm.v[0]), kAtom, 1024);
+      uint32_t kc = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};  // key tiles, Q tiles, P tiles, O tiles so far
+      // the product P V that follows the next S
+      struct {
+        int t = -1;
+        uint32_t kc;
+        int keys;       // of the tile
+        bool first, last, frees;
+      } due;
+      bool ok = true;
+      auto flush = [&]() {
+        if (due.t < 0) return;
+        const int t = due.t;
+        due.t = -1;
+        const uint32_t st = due.kc & 1;
+        ok = ok && wait(&sm.bar_v_full[st], (due.kc >> 1) & 1) && wait(&sm.bar_p[t], np[t] & 1);
+        ++np[t];
+        if (due.first) {
+          ok = ok && (no[t] == 0 || wait(&sm.bar_o_read[t], (no[t] - 1) & 1));
+          ++no[t];
+        }
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t b = dv + st * kNext;
+        const uint32_t d = tmem + kColO + t * 128, a = tmem + t * 128;
+        if (due.keys >= kTile) {
+          issue_ts_x4(d, a, b, id_o, !due.first);
+          issue_ts_x4(d, a + 32, b + (4 * 2048 >> 4), id_o, 1);
+        } else {
+          for (int x = 0; x * 16 < due.keys; ++x) issue_ts(d, a + 8 * x, b + (x * 2048 >> 4), id_o, x > 0 || !due.first);
+        }
+        if (due.frees) commit(&sm.bar_v_empty[st]);
+        if (due.last) commit(&sm.bar_o[t]);
+      };
+      Walk<kPairs> walk(p.s, sm.pre, group, begin, stop);
+      while (ok && walk.more) {
+        const Part s = walk.next(p.s);
+        const Places pl(p.s, s, solo);
+        for (int j = s.c0; ok && j < s.c1; ++j, ++kc) {
+          const uint32_t st = kc & 1;
+          ok = wait(&sm.bar_k_full[st], (kc >> 1) & 1);
+#pragma unroll 1
+          for (int x = 0; ok && x < pl.rows; ++x) {
+            if (j >= pl.end[x]) continue;
+            const int t = x ^ pl.t0;
+            const bool last_place = x == 1 || pl.rows == 1 || j >= pl.end[1];
+            if (due.t == t) flush();
+            if (j == s.c0) {
+              ok = ok && wait(&sm.bar_q_full[t], nq[t] & 1);
+              ++nq[t];
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t a = dq + t * kNext, b = dk + st * kNext;
+#pragma unroll
+            for (int h = 0; h < kAtoms; ++h) issue_ss_x4(tmem + t * 128, a + h * kAtomStep, b + h * kAtomStep, id_s, h > 0);
+            commit(&sm.bar_s[t]);
+            if (last_place) commit(&sm.bar_k_empty[st]);
+            if (j + 1 == pl.end[x]) commit(&sm.bar_q_empty[t]);
+            flush();
+            due.t = t, due.kc = kc, due.keys = s.len - j * kTile, due.first = j == s.c0, due.last = j + 1 == pl.end[x];
+            due.frees = last_place;
+          }
+        }
+      }
+      flush();
+    } else if (warp == 9) {
+      // ---------------- Q and K
+      uint32_t kc = 0, nq[2] = {0, 0};
+      bool ok = true;
+      const uint32_t q_bytes = p.s.G * p.s.w * D * 2;
+      Walk<kPairs> walk(p.s, sm.pre, group, begin, stop);
+      while (ok && walk.more) {
+        const Part s = walk.next(p.s);
+        const Places pl(p.s, s, solo);
+        auto load_q = [&](int x) {
+          const int t = x ^ pl.t0;
+          ok = ok && (nq[t] == 0 || wait(&sm.bar_q_empty[t], (nq[t] - 1) & 1));
+          ++nq[t];
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(&sm.bar_q_full[t], q_bytes);
+#pragma unroll
+            for (int h = 0; h < kAtoms; ++h)
+              tma_load_3d(sm.q[t] + h * kAtom, &tm_q, h * 64, s.hk * p.s.G, s.at + (2 * s.i + x) * p.s.w, &sm.bar_q_full[t]);
+          }
+        };
+        load_q(0);
+        for (int j = s.c0; ok && j < s.c1; ++j, ++kc) {
+          const uint32_t st = kc & 1;
+          ok = kc < 2 || wait(&sm.bar_k_empty[st], ((kc >> 1) - 1) & 1);
+          if (ok && lane == 0) {
+            mbar_arrive_expect_tx(&sm.bar_k_full[st], kTile * D * 2);
+#pragma unroll
+            for (int h = 0; h < kAtoms; ++h)
+              tma_load_3d(sm.k[st] + h * kAtom, &tm_k, h * 64, s.at + j * kTile, s.hk, &sm.bar_k_full[st]);
+          }
+          __syncwarp();
+          if (j == s.c0 && pl.rows == 2) load_q(1);
+        }
+      }
+      // (the last copies are waited for by those who use them, or, after a wait that ran out, here)
+      int give_up = 0;
+      for (int t = 0; t < 2; ++t) {
+        if (nq[t]) mbar_wait(&sm.bar_q_full[t], (nq[t] - 1) & 1, &give_up);
+        if (kc > (uint32_t)t) mbar_wait(&sm.bar_k_full[(kc - 1 - t) & 1], ((kc - 1 - t) >> 1) & 1, &give_up);
+      }
+    } else if (warp == 10) {
+      // ---------------- V
+      uint32_t kc = 0, nr = 0;
+      bool ok = true;
+      Walk<kPairs> walk(p.s, sm.pre, group, begin, stop);
+      while (ok && walk.more) {
+        const Part s = walk.next(p.s);
+        for (int j = s.c0; ok && j < s.c1; ++j, ++kc) {
+          const uint32_t st = kc & 1;
+          ok = kc < 2 || wait(&sm.bar_v_empty[st], ((kc >> 1) - 1) & 1);
+          if (!ok) break;
+          const int keys = s.len - j * kTile;
+          const bool ragged = keys < kTile && (keys & 15);
+          uint64_t* bar = ragged ? &sm.bar_v_raw : &sm.bar_v_full[st];
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar, kTile * D * 2);
+#pragma unroll
+            for (int h = 0; h < kAtoms; ++h) tma_load_3d(sm.v[st] + h * kAtom, &tm_v, h * 64, s.at + j * kTile, s.hk, bar);
+          }
+          __syncwarp();
+          if (ragged) {
+            // rows up to the next multiple of 16: the product reads them
+            int give_up = 0;
+            ok = __all_sync(0xffffffffu, mbar_wait(bar, nr++ & 1, &give_up));
+            if (!ok) {
+              *abort = 1;
+              break;
+            }
+            const int rows = (16 - keys) & 15;
+            for (int x = lane; x < rows * kAtoms * 8; x += 32) {
+              const int row = keys + x / (kAtoms * 8), c = x % (kAtoms * 8);
+              *reinterpret_cast<uint4*>(sm.v[st] + (c >> 3) * kAtom + row * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.bar_v_full[st]);
+          }
+        }
+      }
+      int give_up = 0;
+      for (uint32_t t = 0; t < 2; ++t)
+        if (kc > t) mbar_wait(&sm.bar_v_full[(kc - 1 - t) & 1], ((kc - 1 - t) >> 1) & 1, &give_up);
+    }
+  } else {
+    regs_increase<kRegsSoftmax>();
+    // ---------------- softmax: thread r of the group owns row r of the row tile at place t
+    const int t = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + kColO + t * 128;
+    const int token = r / p.s.G, head = r - token * p.s.G;  // of the tile
+    uint32_t ns = 0, no = 0;
+    bool ok = true;
+    Walk<kPairs> walk(p.s, sm.pre, group, begin, stop);
+    while (ok && walk.more) {
+      const Part s = walk.next(p.s);
+      const Places pl(p.s, s, solo);
+      const int x = t ^ pl.t0;
+      if (x >= pl.rows) continue;
+      const int i = (2 * s.i + x) * p.s.w + token;
+      const bool live = token < p.s.w && i < s.len;
+      const int lim = live && p.s.causal ? i + 1 : s.len;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int j = s.c0; ok && j < pl.end[x]; ++j) {
+        ok = wait(&sm.bar_s[t], ns++ & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sv[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, sv[c]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) reg_fence32(sv[c]);
+        const int left = lim - j * kTile;
+        if (__any_sync(0xffffffffu, left < kTile)) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e >= left) sv[c][e] = 0xff800000u;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) top = max3(top, __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
+        top *= p.alpha;
+        const bool raise = top > m + kRaise;  // (m = -infinity: whenever there is a key)
+        if (__any_sync(0xffffffffu, raise)) {
+          const float corr = raise ? ex2(m - top) : 1.f;
+          if (raise) m = top;
+          l *= corr;
+          if (j > s.c0) {  // (the part's first product overwrites O; P V of the tile before is done: S came after it)
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_col + d, o);
+              tmem_wait32(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+              tmem_st32(o_col + d, o);
+            }
+          }
+        }
+        const float sub = m == -INFINITY ? 0.f : m;
+        const uint64_t a2 = f2(p.alpha, p.alpha), m2 = f2(-sub, -sub);
+        uint64_t sum = f2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float u0, u1;
+            f2split(ffma2(f2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), a2, m2), u0, u1);
+            u0 = ex2(u0), u1 = ex2(u1);
+            sum = fadd2(sum, f2(u0, u1));
+            const __nv_bfloat162 h = __floats2bfloat162_rn(u0, u1);
+            w[e >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st16(s_col + 16 * c, w);
+        }
+        float y0, y1;
+        f2split(sum, y0, y1);
+        l += y0 + y1;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&sm.bar_p[t]);
+      }
+      // ---- the part's result
+      ok = ok && wait(&sm.bar_o[t], no++ & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const float f = l != 0.f ? 1.f / l : 0.f;
+      const int h = s.hk * p.s.G + head;
+      __nv_bfloat16* orow = p.O + (long long)(s.at + i) * p.o_token + h * p.o_head;
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_col + d, o);
+        tmem_wait32(o);
+        if (!live) continue;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint4 y;
+          __nv_bfloat162* z = reinterpret_cast<__nv_bfloat162*>(&y);
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            z[g] = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * g]) * f, __uint_as_float(o[8 * e + 2 * g + 1]) * f);
+          *reinterpret_cast<uint4*>(orow + d + 8 * e) = y;
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&sm.bar_o_read[t]);
+      if (live) p.LSE[(size_t)h * p.s.T + s.at + i] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, kCols);
+  if (tid == 0 && sm.abort) atomicMax(p.s.status, (int)kDevTimeout);
+}
+
+template <int D>
+int launch(const FwdParams& p, const sage_rows& Q, const sage_rows& K, const sage_rows& V, int H, int sms, cudaStream_t st) {
+  auto kern = packed_fwd_kernel<D>;
+  CUtensorMap tq, tk, tv;
+  if (!make_tmap_queries(&tq, Q, D, H, p.s) || !make_tmap_keys(&tk, K, D, p.s) || !make_tmap_keys(&tv, V, D, p.s))
+    return SAGE_ERR_CUDA;
+  const size_t smem = sizeof(FwdSmem<D>) + 1024;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SAGE_ERR_CUDA;
+  return launch_pdl(kern, dim3(sms), dim3(kThreads), smem, st, p, tq, tk, tv) == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
+}
+
+}  // namespace
+
+PackedWs packed_ws_layout(int, int, int, int, int, bool) {
+  PackedWs l;
+  l.cuts = 256;
+  l.part = l.cuts;
+  l.total = l.part;
+  return l;
+}
+
+int launch_packed_fwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V, const int* cu, const sage_rows& O,
+                      float* LSE, void* ws, int T, int S, int H, int Hkv, int D, int causal, float sm_scale,
+                      cudaStream_t st) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SAGE_ERR_CUDA;
+  FwdParams p;
+  p.s = packed_shape(cu, ws, T, S, H, Hkv, causal);
+  p.O = static_cast<__nv_bfloat16*>(O.p);
+  p.o_token = O.token, p.o_head = O.head;
+  p.LSE = LSE;
+  p.alpha = sm_scale * 1.4426950408889634f;
+  ScopedTimer timer("packed_fwd", st);
+  return D == 128 ? launch<128>(p, Q, K, V, H, sms, st) : launch<64>(p, Q, K, V, H, sms, st);
+}
+
+}  // namespace sage

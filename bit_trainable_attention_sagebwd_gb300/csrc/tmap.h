@@ -22,19 +22,12 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
   return fn;
 }
 
-// 3-D tiled map over a contiguous [outer][rows][inner] tensor of `esize`-byte
-// elements, box = [1][box_rows][box_inner].  With the default 128-byte swizzle
-// box_inner * esize must be 128; without swizzle the box is a dense row-major
-// [box_rows][box_inner] block in shared memory.  Out-of-range rows read as zero.
-// Returns false on error.
-inline bool make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int esize,
-                         uint64_t inner, uint64_t rows, uint64_t outer, uint32_t box_inner,
-                         uint32_t box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+// 3-D tiled map, dims and box innermost first, strides in bytes between rows and between planes.  Returns false on
+// error.
+inline bool encode_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, const cuuint64_t (&dims)[3],
+                           const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
   auto enc = tmap_encoder();
   if (!enc) return false;
-  cuuint64_t dims[3] = {inner, rows, outer};
-  cuuint64_t strides[2] = {inner * (uint64_t)esize, inner * rows * (uint64_t)esize};
-  cuuint32_t box[3] = {box_inner, box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   auto encode = [&]() {
     return enc(map, dtype, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
@@ -48,6 +41,18 @@ inline bool make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType
     if (cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = encode();
   }
   return r == CUDA_SUCCESS;
+}
+
+// 3-D tiled map over a contiguous [outer][rows][inner] tensor of `esize`-byte
+// elements, box = [1][box_rows][box_inner].  With the default 128-byte swizzle
+// box_inner * esize must be 128; without swizzle the box is a dense row-major
+// [box_rows][box_inner] block in shared memory.  Out-of-range rows read as zero.
+// Returns false on error.
+inline bool make_tmap_3d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype, int esize,
+                         uint64_t inner, uint64_t rows, uint64_t outer, uint32_t box_inner,
+                         uint32_t box_rows, CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+  return encode_tmap_3d(map, base, dtype, {inner, rows, outer},
+                        {inner * (uint64_t)esize, inner * rows * (uint64_t)esize}, {box_inner, box_rows, 1}, swizzle);
 }
 
 }  // namespace sage

@@ -1,0 +1,119 @@
+"""Attention over packed sequences: the torch helpers of the sage_attn_packed_* calls (include/sage_attn.h says what
+each computes).
+
+    cu = torch.tensor([0, 700, 700, 1000], dtype=torch.int32, device="cuda")   # three sequences, one of them empty
+    o, lse = packed_forward(q, k, v, cu)                                      # q [T, H, D], k, v [T, Hkv, D]
+    dq, dk, dv = packed_backward(q, k, v, o, lse, do, cu)
+
+Like the other helpers these marshal arguments; everything is computed by the CUDA library on the current stream of
+the tensors' device.  Tensors may be slices of a fused projection or head-major: any strides in multiples of 8
+elements with the channels contiguous.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import SAGE_ERR_UNSUPPORTED, SageError, lib, sage_rows
+
+
+def _rows(x, name, shape, device):
+    """A tensor argument [T, heads, D] after its checks."""
+    import torch
+    if x.dtype is not torch.bfloat16 or tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name}: torch.bfloat16 of shape {tuple(shape)} expected, got {x.dtype} {tuple(x.shape)}")
+    if x.device != device:
+        raise ValueError(f"{name}: on {x.device}, q is on {device}")
+    token, head, channel = x.stride()
+    if channel != 1:
+        raise ValueError(f"{name}: its channels are not contiguous")
+    return ctypes.byref(sage_rows(x.data_ptr(), token, head))
+
+
+def _array(x, name, dtype, shape, device):
+    """The address of a contiguous tensor argument after its checks."""
+    if x.dtype is not dtype or tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} expected, got {x.dtype} {tuple(x.shape)}")
+    if x.device != device:
+        raise ValueError(f"{name}: on {x.device}, q is on {device}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    return x.data_ptr()
+
+
+def _shapes(q, k, cu_seqlens):
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q: [T, H, D], k and v: [T, Hkv, D] expected")
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens: the S + 1 places where the sequences begin and the last one ends expected")
+    if not q.is_cuda:
+        raise ValueError("q: on a GPU expected")
+    T, H, D = q.shape
+    return T, cu_seqlens.shape[0] - 1, H, k.shape[1], D, q.device
+
+
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) with the tensors' device current, on `stream` or that device's current stream."""
+    import torch
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, q is on {device}")
+    if stream is None and torch._C._cuda_getDevice() == device.index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream)
+    if rc:
+        raise SageError(fn.__name__, rc)
+
+
+def _new(stream, device, shape, dtype):
+    """A tensor that the caller gets: out of the memory of the stream that the call runs on, and once freed not given
+    to others before what the current stream does with it is done."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        x = torch.empty(shape, dtype=dtype, device=device)
+    x.record_stream(torch.cuda.current_stream(device))
+    return x
+
+
+def alloc_packed_ws(T, S, H, Hkv, D, backward=False, device="cuda", stream=None):
+    """Workspace of packed_forward and packed_backward (backward=True) for T tokens in S sequences.  Its status word:
+    get_status(ws)."""
+    import torch
+    n = lib().sage_attn_packed_ws_bytes(T, S, H, Hkv, D, int(backward))
+    if n == 0:
+        raise SageError("sage_attn_packed_ws_bytes", SAGE_ERR_UNSUPPORTED)
+    with torch.cuda.stream(stream):
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws[:4].zero_()
+    return ws
+
+
+def _workspace(ws, shape, backward, device, stream):
+    if ws is None:
+        return alloc_packed_ws(*shape, backward, device, stream)
+    if ws.device != device:
+        raise ValueError(f"ws: on {ws.device}, q is on {device}")
+    if not ws.is_contiguous():
+        raise ValueError("ws: not contiguous")
+    return ws
+
+
+def packed_forward(q, k, v, cu_seqlens, causal=True, sm_scale=None, o=None, lse=None, ws=None, stream=None):
+    """Attention of every sequence of a packed batch over itself: bf16 q [T, H, D], k and v [T, Hkv, D], int32
+    cu_seqlens [S + 1].  Returns (O bf16 [T, H, D], LSE fp32 [H, T]); rows behind the last sequence are left as they
+    were.  Entries of cu_seqlens that are out of order or range are reported in the status word of ws."""
+    import torch
+    T, S, H, Hkv, D, dev = _shapes(q, k, cu_seqlens)
+    ws = _workspace(ws, (T, S, H, Hkv, D), False, dev, stream)
+    if o is None:
+        o = _new(stream, dev, (T, H, D), torch.bfloat16)
+    if lse is None:
+        lse = _new(stream, dev, (H, T), torch.float32)
+    kv = (T, Hkv, D)
+    _call(lib().sage_attn_packed_fwd, dev, stream, _rows(q, "q", (T, H, D), dev), _rows(k, "k", kv, dev), _rows(v, "v", kv, dev),
+          _array(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev), _rows(o, "o", (T, H, D), dev),
+          _array(lse, "lse", torch.float32, (H, T), dev), ws.data_ptr(), ws.nbytes, T, S, H, Hkv, D, int(causal),
+          0.0 if sm_scale is None else float(sm_scale))
+    return o, lse

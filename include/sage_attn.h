@@ -396,6 +396,43 @@ size_t sage_attn_kv_compact_ws_bytes(int n_pages);
 int sage_attn_kv_compact(const sage_kv_cache *cache, const sage_kv_cache *to, void *ws, size_t ws_bytes,
                          void *stream);
 
+/*
+ * Attention over packed sequences, in full precision: bf16 operands, fp32 sums.  The tokens of S sequences of
+ * different lengths lie one behind the other; every sequence attends to itself.  For whole prompts and for training
+ * on documents without padding, where the low-bit calls above take sequences of one length ("SageBwd: A Trainable
+ * Low-bit Attention" (euno.news summary), Results, compares with such full-precision attention).
+ *  - Q, O, dO, dQ: bf16 [T, H, D], K, V, dK, dV: bf16 [T, Hkv, D], given as sage_rows: the element (t, h, d) is at
+ *    p[t * token + h * head + d] (strides in elements, positive multiples of 8, below 2^38, p 16-byte aligned), so a
+ *    slice of a fused projection or a head-major tensor serves as it is.  What is written lies apart from what is read,
+ *    and its rows from each other.  LSE: fp32 [H, T].
+ *  - cu_seqlens: int32 [S + 1] on the device, not decreasing, within 0 .. T: sequence s has the tokens
+ *    cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (none: an empty sequence).  Rows before the first and behind the last are
+ *    neither read into a result nor written.  A sequence whose entries are out of order or range counts as empty, with
+ *    SAGE_ERR_INVALID_ARG in the status word.
+ *  - Query head h reads key/value head h / (H / Hkv); Hkv divides H, H / Hkv at most 128, D 64 or 128,
+ *    S at most 65536, T at most 2^30.
+ *  - ws: sage_attn_packed_ws_bytes(.., backward) bytes, 256-byte aligned.  Its first four bytes are the status word, zero
+ *    before the first call (sage_attn_get_status(ws, stream)); the rest is free before and after.
+ *  Lengths are read on the device, so a captured CUDA graph can be replayed with others.  Calls that share a workspace
+ *  must not overlap on the GPU.  Deterministic: the same call gives the same bits.  What a sequence holds, NaN and
+ *  infinities among it, does not reach another one's results.
+ */
+typedef struct sage_rows {
+  void *p;
+  long long token, head; /* strides in elements */
+} sage_rows;
+
+size_t sage_attn_packed_ws_bytes(int T, int S, int H, int Hkv, int D, int backward);
+
+/*
+ * S = sm_scale q . k over the keys of the query's sequence (causal != 0: those up to the query), O = softmax(S) V,
+ * LSE = log sum e^S.  P is rounded to bf16 relative to the row's running reference; everything else is fp32.
+ * sm_scale <= 0 selects 1/sqrt(D).
+ */
+int sage_attn_packed_fwd(const sage_rows *Q, const sage_rows *K, const sage_rows *V, const int *cu_seqlens,
+                         const sage_rows *O, float *LSE, void *ws, size_t ws_bytes, int T, int S, int H, int Hkv, int D,
+                         int causal, float sm_scale, void *stream);
+
 /* Fill `views` with the device pointers inside a quantize workspace (qmean, dsb: NULL). */
 int sage_attn_ws_views(void *ws, int B, int H, int N, int D, sage_ws_views *views);
 
