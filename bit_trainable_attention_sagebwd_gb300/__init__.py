@@ -36,7 +36,8 @@ ABI_FUNCTIONS = ("sage_attn_ws_bytes", "sage_attn_bwd_ws_bytes", "sage_attn_quan
                  "sage_attn_fp4_ws_views", "sage_attn_fp4_bwd_ws_bytes", "sage_attn_fp4_bwd",
                  "sage_attn_kv_append", "sage_attn_kv_ws_bytes", "sage_attn_kv_attention", "sage_attn_kv_fork",
                  "sage_attn_kv_extend", "sage_attn_kv_truncate", "sage_attn_kv_compact_ws_bytes",
-                 "sage_attn_kv_compact", "sage_attn_selftest_kv_join", "sage_attn_packed_ws_bytes", "sage_attn_packed_fwd")
+                 "sage_attn_kv_compact", "sage_attn_selftest_kv_join", "sage_attn_packed_ws_bytes", "sage_attn_packed_fwd",
+                 "sage_attn_packed_bwd")
 
 
 class SageError(RuntimeError):
@@ -128,6 +129,7 @@ def lib():
             L.sage_attn_packed_ws_bytes.restype = sz
             L.sage_attn_packed_ws_bytes.argtypes = [i] * 6
             L.sage_attn_packed_fwd.argtypes = [rp] * 3 + [vp, rp, vp, vp, sz] + [i] * 6 + [fp, vp]
+            L.sage_attn_packed_bwd.argtypes = [rp] * 4 + [vp, rp, vp] + [rp] * 3 + [vp, sz] + [i] * 6 + [fp, vp]
             L.sage_attn_ws_views.argtypes = [vp, i, i, i, i, ctypes.POINTER(sage_ws_views)]
             L.sage_attn_get_status.argtypes = [vp, vp]
             L.sage_attn_selftest_wait.argtypes = [vp, u64, vp]
@@ -263,6 +265,12 @@ def sage_attn_packed_ws_bytes(T, S, H, Hkv, D, backward):
 def sage_attn_packed_fwd(Q, K, V, cu_seqlens, O, LSE, ws, ws_bytes, T, S, H, Hkv, D, causal, sm_scale, stream):
     return lib().sage_attn_packed_fwd(Q, K, V, cu_seqlens, O, LSE, ws, ws_bytes, T, S, H, Hkv, D, int(causal),
                                       float(sm_scale), stream)
+
+
+def sage_attn_packed_bwd(Q, K, V, O, LSE, dO, cu_seqlens, dQ, dK, dV, ws, ws_bytes, T, S, H, Hkv, D, causal, sm_scale,
+                         stream):
+    return lib().sage_attn_packed_bwd(Q, K, V, O, LSE, dO, cu_seqlens, dQ, dK, dV, ws, ws_bytes, T, S, H, Hkv, D,
+                                      int(causal), float(sm_scale), stream)
 
 
 def sage_attn_bwd_noalloc(Q, K, V, O, LSE, dO, dQ, dK, dV, ws, B, H, N, D, causal, qk_norm, k_smooth, sm_scale,
@@ -683,4 +691,4 @@ def ws_tensors(ws, B, H, N, D, hkv=None, q_smooth=False, fp4=False) -> dict:
 
 from .kvcache import (KVCache, alloc_kv_compact_ws, alloc_kv_ws, kv_append, kv_attention, kv_cache,  # noqa: E402,F401
                       kv_compact, kv_extend, kv_fork, kv_truncate)
-from .packed import alloc_packed_ws, packed_forward  # noqa: E402,F401
+from .packed import alloc_packed_ws, packed_backward, packed_forward  # noqa: E402,F401

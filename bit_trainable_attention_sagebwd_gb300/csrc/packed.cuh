@@ -40,7 +40,7 @@ __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((
 
 // first token and length of sequence b; one that does not lie in the tensors counts as empty
 __device__ __forceinline__ void sequence(const PackedShape& p, int b, int& at, int& len) {
-  const int x = p.cu[b], y = p.cu[b + 1];
+  const int x = __ldcg(p.cu + b), y = __ldcg(p.cu + b + 1);
   const bool ok = x >= 0 && y >= x && y <= p.T;
   if (!ok) atomicMax(p.status, kDevSequence);
   at = ok ? x : 0, len = ok ? y - x : 0;

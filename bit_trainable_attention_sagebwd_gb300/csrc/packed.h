@@ -14,12 +14,15 @@ constexpr int kPackedMaxTokens = 1 << 30;
 constexpr int kPackedMaxGroup = 128;
 
 struct PackedWs {
-  size_t cuts, part, total;  // (the status word comes first)
+  size_t stats, total;  // (the status word comes first)
 };
 PackedWs packed_ws_layout(int T, int S, int H, int Hkv, int D, bool backward);
 
 int launch_packed_fwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V, const int* cu, const sage_rows& O,
                       float* LSE, void* ws, int T, int S, int H, int Hkv, int D, int causal, float sm_scale,
                       cudaStream_t st);
+int launch_packed_bwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V, const sage_rows& O, const float* LSE,
+                      const sage_rows& dO, const int* cu, const sage_rows& dQ, const sage_rows& dK, const sage_rows& dV,
+                      void* ws, int T, int S, int H, int Hkv, int D, int causal, float sm_scale, cudaStream_t st);
 
 }  // namespace sage

@@ -53,4 +53,24 @@ int sage_attn_packed_fwd(const sage_rows* Q, const sage_rows* K, const sage_rows
                                  sage::resolve_scale(sm_scale, D), static_cast<cudaStream_t>(stream));
 }
 
+int sage_attn_packed_bwd(const sage_rows* Q, const sage_rows* K, const sage_rows* V, const sage_rows* O, const float* LSE,
+                         const sage_rows* dO, const int* cu_seqlens, const sage_rows* dQ, const sage_rows* dK,
+                         const sage_rows* dV, void* ws, size_t ws_bytes, int T, int S, int H, int Hkv, int D, int causal,
+                         float sm_scale, void* stream) {
+  if (!shape_ok(T, S, H, Hkv, D)) return SAGE_ERR_UNSUPPORTED;
+  if (!rows_ok(Q, T, H) || !rows_ok(K, T, Hkv) || !rows_ok(V, T, Hkv) || !rows_ok(O, T, H) || !rows_ok(dO, T, H) ||
+      !apart(dQ, T, H, D) || !apart(dK, T, Hkv, D) || !apart(dV, T, Hkv, D))
+    return SAGE_ERR_INVALID_ARG;
+  if (!aligned(cu_seqlens, 4) || !aligned(LSE, 4) || !aligned(ws, 256) || !sage::scale_ok(sm_scale)) return SAGE_ERR_INVALID_ARG;
+  if (ws_bytes < sage::packed_ws_layout(T, S, H, Hkv, D, true).total) return SAGE_ERR_INVALID_ARG;
+  const void* read[] = {Q->p, K->p, V->p, O->p, dO->p, LSE};
+  const void* written[] = {dQ->p, dK->p, dV->p};
+  for (const void* w : written)
+    for (const void* r : read)
+      if (w == r) return SAGE_ERR_INVALID_ARG;
+  if (dQ->p == dK->p || dQ->p == dV->p || dK->p == dV->p) return SAGE_ERR_INVALID_ARG;
+  return sage::launch_packed_bwd(*Q, *K, *V, *O, LSE, *dO, cu_seqlens, *dQ, *dK, *dV, ws, T, S, H, Hkv, D, causal != 0,
+                                 sage::resolve_scale(sm_scale, D), static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

@@ -1,0 +1,779 @@
+// Attention over packed sequences, backward (sage_attn_packed_bwd).  With P = e^(S - LSE) recomputed and
+// delta_i = sum_d dO_id O_id:
+//   dV = P^T dO,  dP = dO V^T,  dS = P (dP - delta),  dQ = sm_scale dS K,  dK = sm_scale dS^T Q.
+// Three kernels:
+//   packed_pre   -LSE log2 e and -delta of every query row
+//   packed_dkv   a 128-key tile against the row tiles that see it: dK and dV
+//   packed_dq    a row tile against the key tiles that it sees: dQ
+// dQ in a kernel of its own recomputes S and dP, seven products in place of five.  In exchange nothing is added up in
+// memory: no fp32 sums of dQ go to L2 for every tile (64 KB beside 160 KB of operands from shared memory, which already
+// set the pace), none are cleared and converted, and the gradients are the same bits every time.
+//
+// The two main kernels are alike.  One CTA an SM walks its units (packed.cuh):
+//  - warps 9 and 10 bring the operands by TMA, warp 11 (packed_dkv) the row statistics;
+//  - warp 8 issues the products (bf16 operands, fp32 accumulators in TMEM);
+//  - warps 0-3 and 4-7 turn S into P and dP into dS, the first group the tile's first 64 columns, the second the
+//    others; P and dS go back to TMEM as bf16 over the columns that they come from and are the A operands of the
+//    products that take them.
+// While the warps compute, the products of the tile before and after run: P(i) lets dV(i) and S(i + 1) in, dS(i) lets
+// dK(i) and dP(i + 1) in.
+// Rows that belong to the next sequence: those that a product would sum over are zeroed in shared memory (up to 15 of a
+// tile; the product stops there), the others end in rows that are not stored.
+#include "issue.cuh"
+#include "launch.h"
+#include "packed.cuh"
+#include "timer.h"
+
+namespace sage {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kRegsCompute = 208, kRegsIssue = 88;
+static_assert(2 * kRegsCompute + kRegsIssue <= 3 * 168, "the launch's registers");
+constexpr uint32_t kCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct BwdParams {
+  PackedShape s;
+  const float *nlse, *ndelta;  // [Hkv][T][G]: -LSE log2 e, -delta
+  sage_rows d0, d1;            // packed_dkv: dK, dV; packed_dq: dQ
+  float alpha, sm_scale;       // alpha: sm_scale log2 e
+};
+
+// ------------------------------------------------------------------ row statistics
+struct PreParams {
+  PackedShape s;
+  sage_rows O, dO;
+  const float* LSE;
+  float *nlse, *ndelta;
+};
+
+// D / 8 lanes a row, rows in the order of [T, H]
+template <int D>
+__global__ void __launch_bounds__(256) packed_pre_kernel(const PreParams p) {
+  constexpr int kLanes = D / 8, kRows = 4, kStep = 256 / kLanes;  // rows of a thread, and between them
+  const int tid = threadIdx.x, lane = tid % kLanes, H = p.s.Hkv * p.s.G;
+  const long long rows = (long long)p.s.T * H;
+  const long long r0 = (long long)blockIdx.x * (kStep * kRows) + tid / kLanes;
+  pdl_wait();
+  pdl_trigger();
+  uint4 a[kRows], b[kRows];
+#pragma unroll
+  for (int x = 0; x < kRows; ++x) {
+    const long long r = r0 + x * kStep;
+    if (r < rows) {
+      const int t = (int)(r / H), h = (int)(r - (long long)t * H);
+      a[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.O.p) + t * p.O.token + h * p.O.head) + lane);
+      b[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dO.p) + t * p.dO.token + h * p.dO.head) + lane);
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < kRows; ++x) {
+    const long long r = r0 + x * kStep;
+    float s = 0.f;
+    if (r < rows) {
+      const uint32_t u[4] = {a[x].x, a[x].y, a[x].z, a[x].w}, v[4] = {b[x].x, b[x].y, b[x].z, b[x].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s = fmaf(__uint_as_float(u[e] << 16), __uint_as_float(v[e] << 16), s);
+        s = fmaf(__uint_as_float(u[e] & 0xffff0000u), __uint_as_float(v[e] & 0xffff0000u), s);
+      }
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0 && r < rows) {
+      const int t = (int)(r / H), h = (int)(r - (long long)t * H);
+      const size_t at = ((size_t)(h / p.s.G) * p.s.T + t) * p.s.G + h % p.s.G;
+      const float lse = p.LSE[(size_t)h * p.s.T + t];
+      p.nlse[at] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // (a row that saw nothing: P = 0)
+      p.ndelta[at] = -s;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ shared memory
+template <int D>
+struct BwdSmem {
+  uint8_t a[2][kTile * D * 2];     // the unit's own tiles: packed_dkv K and V, packed_dq Q and dO
+  uint8_t x[2][kTile * D * 2];     // two tiles deep, what the unit walks over: Q, or K
+  uint8_t y[2][kTile * D * 2];     // dO, or V
+  __align__(16) float nlse[2][kTile];
+  __align__(16) float ndelta[2][kTile];
+  uint64_t bar_a_full[2], bar_a_empty[2], bar_x_full[2], bar_x_empty[2], bar_y_full[2], bar_y_empty[2], bar_raw[2];
+  uint64_t bar_st_full[2], bar_st_empty[2];
+  uint64_t bar_s[2], bar_dp, bar_p, bar_ds, bar_acc, bar_acc_read;
+  long long wsum[kThreads / 32];
+  long long pre[kPackedGroups + 1];
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(BwdSmem<128>) + 1024 <= 227 * 1024, "shared memory of a CTA");
+
+template <int D>
+__device__ __forceinline__ void init_barriers(BwdSmem<D>& sm) {
+  for (int t = 0; t < 2; ++t) {
+    mbar_init(&sm.bar_a_full[t], 1);
+    mbar_init(&sm.bar_a_empty[t], 1);
+    mbar_init(&sm.bar_x_full[t], 1);
+    mbar_init(&sm.bar_x_empty[t], 1);
+    mbar_init(&sm.bar_y_full[t], 1);
+    mbar_init(&sm.bar_y_empty[t], 1);
+    mbar_init(&sm.bar_raw[t], 1);
+    mbar_init(&sm.bar_st_full[t], 32);
+    mbar_init(&sm.bar_st_empty[t], 256);
+    mbar_init(&sm.bar_s[t], 1);
+  }
+  mbar_init(&sm.bar_dp, 1);
+  mbar_init(&sm.bar_p, 256);
+  mbar_init(&sm.bar_ds, 256);
+  mbar_init(&sm.bar_acc, 1);
+  mbar_init(&sm.bar_acc_read, 256);
+  sm.abort = 0;
+  fence_mbar_init();
+}
+
+// rows [from, to) of a tile in shared memory become zero (a warp)
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int to) {
+  constexpr int kPieces = D / 8;  // of 16 bytes
+  for (int e = threadIdx.x & 31; e < (to - from) * kPieces; e += 32) {
+    const int row = from + e / kPieces, c = e % kPieces;
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * (kTile * 128) + row * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// One tile by TMA (a warp; lane 0 issues): `load` issues the copies onto the barrier that it gets.  Of a tile with
+// `rows` rows of its own, fewer than the copy brings, those up to the next multiple of 16 are zeroed before `full` is
+// signalled.
+template <int D, class Load>
+__device__ __forceinline__ bool bring(uint8_t* tile, int rows, int copied, uint32_t bytes, uint64_t* full, uint64_t* raw,
+                                      uint32_t& raws, volatile int* abort, Load&& load) {
+  const int lane = threadIdx.x & 31;
+  const bool ragged = rows < copied && (rows & 15);
+  uint64_t* bar = ragged ? raw : full;
+  if (lane == 0) {
+    mbar_arrive_expect_tx(bar, bytes);
+    load(bar);
+  }
+  __syncwarp();
+  if (!ragged) return true;
+  int give_up = 0;
+  if (!__all_sync(0xffffffffu, mbar_wait(raw, raws++ & 1, &give_up))) {
+    *abort = 1;
+    return false;
+  }
+  zero_rows<D>(tile, rows, (rows + 15) & ~15);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(full);
+  return true;
+}
+
+// One tile of a walk after another.  `first`, `last`: of a part.
+template <int KIND>
+struct Tiles {
+  Walk<KIND> walk;
+  Part s;
+  int j;
+  bool valid, first, last;
+  __device__ __forceinline__ Tiles(const PackedShape& p, const long long* pre, int group, long long begin, long long end)
+      : walk(p, pre, group, begin, end), j(0), valid(false), first(false), last(true) {
+    s.c1 = 0;
+    next(p);
+  }
+  __device__ __forceinline__ void next(const PackedShape& p) {
+    first = last;
+    if (last) {
+      valid = walk.more;
+      if (!valid) return;
+      s = walk.next(p);
+      j = s.c0;
+    } else {
+      ++j;
+    }
+    last = j + 1 == s.c1;
+  }
+};
+
+// columns of an A operand in TMEM, 16 bf16 each: P or dS as the two groups write them
+__device__ __forceinline__ uint32_t a_col(int k) { return k < 4 ? 8 * k : 64 + 8 * (k - 4); }
+
+// D (+)= A B over `rows` rows of B, 16 at a time
+__device__ __forceinline__ void issue_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int rows, bool acc) {
+  if (rows > kTile - 16) {
+    issue_ts_x4(d, a, b, idesc, acc);
+    issue_ts_x4(d, a + 64, b + (4 * 2048 >> 4), idesc, 1);
+  } else {
+    for (int k = 0; k * 16 < rows; ++k) issue_ts(d, a + a_col(k), b + (k * 2048 >> 4), idesc, acc || k > 0);
+  }
+}
+
+// 64 values of P or dS of a row, as bf16, to 32 columns
+__device__ __forceinline__ uint32_t bf2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// 32 columns of an accumulator times f to a row's bf16
+__device__ __forceinline__ void store_row(__nv_bfloat16* to, const uint32_t (&o)[32], float f) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    *reinterpret_cast<uint4*>(to + 8 * e) =
+        make_uint4(bf2(__uint_as_float(o[8 * e]) * f, __uint_as_float(o[8 * e + 1]) * f),
+                   bf2(__uint_as_float(o[8 * e + 2]) * f, __uint_as_float(o[8 * e + 3]) * f),
+                   bf2(__uint_as_float(o[8 * e + 4]) * f, __uint_as_float(o[8 * e + 5]) * f),
+                   bf2(__uint_as_float(o[8 * e + 6]) * f, __uint_as_float(o[8 * e + 7]) * f));
+}
+
+// ------------------------------------------------------------------ dK and dV
+// TMEM: S^T (keys x query rows), then P^T, at 0; dP^T, then dS^T, at 128; dV at 256; dK at 384
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_dkv_kernel(const BwdParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do) {
+  constexpr int kAtoms = D / 64, kAtom = kTile * 128;
+  constexpr uint32_t cS = 0, cDP = 128, cDV = 256, cDK = 384;
+  extern __shared__ uint8_t smem_raw[];
+  BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int box = p.s.G * p.s.w;  // rows of a row tile
+  if (tid == 0) init_barriers(sm);
+  if (warp < 4 && box < kTile) {  // the rows that no copy brings
+    zero_rows<D>(warp < 2 ? sm.x[warp] : sm.y[warp - 2], box, kTile);
+    fence_proxy_async_smem();
+  }
+  pdl_wait();
+  if (warp == 8) {
+    tmem_alloc(&sm.tmem_base, kCols);
+    tmem_relinquish();
+  }
+  const int group = ceil_div(p.s.S, kPackedGroups);
+  prefix_of_sequences<kKeys, kThreads>(p.s, group, sm.pre, sm.wsum);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+  const long long total = sm.pre[kPackedGroups];
+  const Line line{total, (int)min((long long)gridDim.x, max(total, 1ll))};
+  const int w0 = blockIdx.x;
+  const bool idle = total == 0 || w0 >= line.parts;
+  const long long begin = idle ? 0 : line.start(w0), stop = idle ? 0 : line.start(w0 + 1);
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
+  // the row tile at hand: the sequence's tile, and its rows
+  auto tile_of = [&](const Tiles<kKeys>& t) { return Units<kKeys>(p.s, t.s.len).first(t.s.i) + t.j; };
+  auto rows_of = [&](const Tiles<kKeys>& t, int rt) { return min(p.s.w, t.s.len - rt * p.s.w) * p.s.G; };
+
+  if (warp >= 8) {
+    regs_decrease<kRegsIssue>();
+    if (warp == 8) {
+      // ---------------- MMA issuer
+      constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_g = idesc_bf16(kTile, D, false, true);
+      constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
+      const uint64_t k_k = sdesc_sw128(smem_u32(sm.a[0]), 16, 1024), v_k = k_k + kNext;
+      const uint64_t q_k = sdesc_sw128(smem_u32(sm.x[0]), 16, 1024), do_k = sdesc_sw128(smem_u32(sm.y[0]), 16, 1024);
+      const uint64_t q_n = sdesc_sw128(smem_u32(sm.x[0]), kAtom, 1024), do_n = sdesc_sw128(smem_u32(sm.y[0]), kAtom, 1024);
+      bool ok = true;
+      uint32_t units = 0;  // that S has been begun of
+      auto issue_s = [&](const Tiles<kKeys>& t, uint32_t n) {
+        if (t.first) ok = ok && wait(&sm.bar_a_full[0], units & 1);
+        ok = ok && wait(&sm.bar_x_full[n & 1], (n >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < kAtoms; ++h)
+          issue_ss_x4(tmem + cS, k_k + h * kAtomStep, q_k + (n & 1) * kNext + h * kAtomStep, id_s, h > 0);
+        commit(&sm.bar_s[0]);
+        if (t.last) commit(&sm.bar_a_empty[0]);
+      };
+      auto issue_dp = [&](const Tiles<kKeys>& t, uint32_t n) {
+        if (t.first) ok = ok && wait(&sm.bar_a_full[1], units++ & 1);
+        ok = ok && wait(&sm.bar_y_full[n & 1], (n >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < kAtoms; ++h)
+          issue_ss_x4(tmem + cDP, v_k + h * kAtomStep, do_k + (n & 1) * kNext + h * kAtomStep, id_s, h > 0);
+        commit(&sm.bar_dp);
+        if (t.last) commit(&sm.bar_a_empty[1]);
+      };
+      Tiles<kKeys> t(p.s, sm.pre, group, begin, stop);
+      if (t.valid) {
+        issue_s(t, 0);
+        issue_dp(t, 0);
+      }
+      uint32_t done = 0;  // units
+      for (uint32_t n = 0; ok && t.valid; ++n) {
+        const int rows = rows_of(t, tile_of(t));
+        const bool first = t.first, last = t.last;
+        t.next(p.s);
+        ok = wait(&sm.bar_p, n & 1);
+        if (first && done) ok = ok && wait(&sm.bar_acc_read, (done - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        issue_rows(tmem + cDV, tmem + cS, do_n + (n & 1) * kNext, id_g, rows, !first);
+        commit(&sm.bar_y_empty[n & 1]);
+        if (t.valid) issue_s(t, n + 1);
+        ok = ok && wait(&sm.bar_ds, n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        issue_rows(tmem + cDK, tmem + cDP, q_n + (n & 1) * kNext, id_g, rows, !first);
+        commit(&sm.bar_x_empty[n & 1]);
+        if (last) {
+          commit(&sm.bar_acc);
+          ++done;
+        }
+        if (t.valid) issue_dp(t, n + 1);
+      }
+    } else if (warp < 11) {
+      // ---------------- K and Q (warp 9), V and dO (warp 10)
+      const int v = warp - 9;
+      const CUtensorMap* tm_a = v ? &tm_v : &tm_k;
+      const CUtensorMap* tm_x = v ? &tm_do : &tm_q;
+      uint64_t *full = v ? sm.bar_y_full : sm.bar_x_full, *empty = v ? sm.bar_y_empty : sm.bar_x_empty;
+      uint32_t units = 0, raws = 0, n = 0;
+      bool ok = true;
+      for (Tiles<kKeys> t(p.s, sm.pre, group, begin, stop); ok && t.valid; t.next(p.s), ++n) {
+        if (t.first) {
+          ok = units == 0 || wait(&sm.bar_a_empty[v], (units - 1) & 1);
+          if (!ok) break;
+          ++units;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.bar_a_full[v], kTile * D * 2);
+#pragma unroll
+            for (int h = 0; h < kAtoms; ++h)
+              tma_load_3d(sm.a[v] + h * kAtom, tm_a, h * 64, t.s.at + t.s.i * kTile, t.s.hk, &sm.bar_a_full[v]);
+          }
+          __syncwarp();
+        }
+        const uint32_t st = n & 1;
+        ok = n < 2 || wait(&empty[st], ((n >> 1) - 1) & 1);
+        if (!ok) break;
+        const int rt = tile_of(t);
+        uint8_t* tile = v ? sm.y[st] : sm.x[st];
+        ok = bring<D>(tile, rows_of(t, rt), box, box * D * 2, &full[st], &sm.bar_raw[v], raws, abort, [&](uint64_t* bar) {
+#pragma unroll
+          for (int h = 0; h < kAtoms; ++h)
+            tma_load_3d(tile + h * kAtom, tm_x, h * 64, t.s.hk * p.s.G, t.s.at + rt * p.s.w, bar);
+        });
+      }
+      // (copies in flight after a wait that ran out)
+      int give_up = 0;
+      if (units) mbar_wait(&sm.bar_a_full[v], (units - 1) & 1, &give_up);
+      for (uint32_t e = 0; e < 2; ++e)
+        if (n > e) mbar_wait(&full[(n - 1 - e) & 1], ((n - 1 - e) >> 1) & 1, &give_up);
+    } else {
+      // ---------------- row statistics; of rows behind the sequence P is 0
+      uint32_t n = 0;
+      for (Tiles<kKeys> t(p.s, sm.pre, group, begin, stop); t.valid; t.next(p.s), ++n) {
+        const uint32_t st = n & 1;
+        const int rt = tile_of(t), rows = rows_of(t, rt);
+        const size_t at = ((size_t)t.s.hk * p.s.T + t.s.at + (size_t)rt * p.s.w) * p.s.G;
+        float a[4], b[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = lane + 32 * e;
+          a[e] = r < rows ? __ldcg(p.nlse + at + r) : -INFINITY;
+          b[e] = r < rows ? __ldcg(p.ndelta + at + r) : 0.f;
+        }
+        if (n >= 2 && !wait(&sm.bar_st_empty[st], ((n >> 1) - 1) & 1)) break;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sm.nlse[st][lane + 32 * e] = a[e];
+          sm.ndelta[st][lane + 32 * e] = b[e];
+        }
+        mbar_arrive(&sm.bar_st_full[st]);
+      }
+    }
+  } else {
+    regs_increase<kRegsCompute>();
+    // ---------------- thread r of group g: key r of the tile, columns [64 g, 64 g + 64)
+    const int g = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_col = tmem + lanes + cS + 64 * g, dp_col = tmem + lanes + cDP + 64 * g;
+    bool ok = true;
+    uint32_t units = 0;
+    Tiles<kKeys> t(p.s, sm.pre, group, begin, stop);
+    const uint64_t a2 = f2(p.alpha, p.alpha);
+    for (uint32_t n = 0; ok && t.valid; t.next(p.s), ++n) {
+      const uint32_t st = n & 1;
+      // causal: columns of tokens before the key are masked
+      const int key = t.s.i * kTile + r, ahead = p.s.causal ? key - tile_of(t) * p.s.w : 0;
+      const int mask = min(ahead, kTile) * p.s.G - 64 * g;  // the group's columns before it
+      ok = wait(&sm.bar_st_full[st], (n >> 1) & 1) && wait(&sm.bar_s[0], n & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sv[2][32];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld32(s_col + 32 * c, sv[c]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) reg_fence32(sv[c]);
+      if (__any_sync(0xffffffffu, mask > 0)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (c * 32 + e < mask) sv[c][e] = 0xff800000u;
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 nl = *reinterpret_cast<const float4*>(&sm.nlse[st][64 * g + 32 * c + e]);
+          float u[4];
+          f2split(ffma2(f2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), a2, f2(nl.x, nl.y)), u[0], u[1]);
+          f2split(ffma2(f2(__uint_as_float(sv[c][e + 2]), __uint_as_float(sv[c][e + 3])), a2, f2(nl.z, nl.w)), u[2], u[3]);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            u[y] = ex2(u[y]);
+            sv[c][e + y] = __float_as_uint(u[y]);
+          }
+          w[e >> 1] = bf2(u[0], u[1]);
+          w[(e >> 1) + 1] = bf2(u[2], u[3]);
+        }
+        tmem_st16(s_col + 16 * c, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&sm.bar_p);
+      ok = wait(&sm.bar_dp, n & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t dv[2][32];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld32(dp_col + 32 * c, dv[c]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) reg_fence32(dv[c]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 nd = *reinterpret_cast<const float4*>(&sm.ndelta[st][64 * g + 32 * c + e]);
+          float x, y;
+          f2split(fmul2(fadd2(f2(__uint_as_float(dv[c][e]), __uint_as_float(dv[c][e + 1])), f2(nd.x, nd.y)),
+                        f2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]))),
+                  x, y);
+          w[e >> 1] = bf2(x, y);
+          f2split(fmul2(fadd2(f2(__uint_as_float(dv[c][e + 2]), __uint_as_float(dv[c][e + 3])), f2(nd.z, nd.w)),
+                        f2(__uint_as_float(sv[c][e + 2]), __uint_as_float(sv[c][e + 3]))),
+                  x, y);
+          w[(e >> 1) + 1] = bf2(x, y);
+        }
+        tmem_st16(dp_col + 16 * c, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&sm.bar_st_empty[st]);
+      mbar_arrive(&sm.bar_ds);
+      if (!t.last) continue;
+      // ---- the unit's sums: channels [D / 2 g, D / 2 (g + 1)) of the key
+      ok = wait(&sm.bar_acc, units++ & 1);
+      if (!ok) break;
+      tc_fence_after();
+      const bool live = key < t.s.len;
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        const sage_rows& to = x ? p.d1 : p.d0;
+        __nv_bfloat16* row = static_cast<__nv_bfloat16*>(to.p) + (long long)(t.s.at + key) * to.token + t.s.hk * to.head + g * (D / 2);
+        const float f = x ? 1.f : p.sm_scale;
+#pragma unroll 1
+        for (int d = 0; d < D / 2; d += 32) {
+          uint32_t o[32];
+          tmem_ld32(tmem + lanes + (x ? cDV : cDK) + g * (D / 2) + d, o);
+          tmem_wait32(o);
+          if (live) store_row(row + d, o, f);
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&sm.bar_acc_read);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, kCols);
+  if (tid == 0 && sm.abort) atomicMax(p.s.status, (int)kDevTimeout);
+}
+
+// ------------------------------------------------------------------ dQ
+// TMEM: S (query rows x keys), then dS, at 0 and 128 in turns; dP at 256; dQ at 384
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_dq_kernel(const BwdParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do) {
+  constexpr int kAtoms = D / 64, kAtom = kTile * 128;
+  constexpr uint32_t cDP = 256, cDQ = 384;
+  extern __shared__ uint8_t smem_raw[];
+  BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int box = p.s.G * p.s.w;
+  if (tid == 0) init_barriers(sm);
+  // (no wait for packed_dkv, of which nothing is read: its CTAs let this kernel in once packed_pre was complete.  The wait
+  // at the end keeps the order for what follows.)
+  if (warp == 8) {
+    tmem_alloc(&sm.tmem_base, kCols);
+    tmem_relinquish();
+  }
+  const int group = ceil_div(p.s.S, kPackedGroups);
+  prefix_of_sequences<kRows, kThreads>(p.s, group, sm.pre, sm.wsum);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort = &sm.abort;
+  const long long total = sm.pre[kPackedGroups];
+  const Line line{total, (int)min((long long)gridDim.x, max(total, 1ll))};
+  const int w0 = blockIdx.x;
+  const bool idle = total == 0 || w0 >= line.parts;
+  const long long begin = idle ? 0 : line.start(w0), stop = idle ? 0 : line.start(w0 + 1);
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
+
+  if (warp >= 8) {
+    regs_decrease<kRegsIssue>();
+    if (warp == 8) {
+      // ---------------- MMA issuer
+      constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_g = idesc_bf16(kTile, D, false, true);
+      constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
+      const uint64_t q_k = sdesc_sw128(smem_u32(sm.a[0]), 16, 1024), do_k = q_k + kNext;
+      const uint64_t k_k = sdesc_sw128(smem_u32(sm.x[0]), 16, 1024), v_k = sdesc_sw128(smem_u32(sm.y[0]), 16, 1024);
+      const uint64_t k_n = sdesc_sw128(smem_u32(sm.x[0]), kAtom, 1024);
+      bool ok = true;
+      uint32_t units_s = 0, units_dp = 0, ns = 0, ndp = 0;
+      auto issue_s = [&](const Tiles<kRows>& t) {
+        const uint32_t n = ns++;
+        if (t.first) ok = ok && wait(&sm.bar_a_full[0], units_s++ & 1);
+        ok = ok && wait(&sm.bar_x_full[n & 1], (n >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < kAtoms; ++h)
+          issue_ss_x4(tmem + (n & 1) * 128, q_k + h * kAtomStep, k_k + (n & 1) * kNext + h * kAtomStep, id_s, h > 0);
+        commit(&sm.bar_s[n & 1]);
+        if (t.last) commit(&sm.bar_a_empty[0]);
+      };
+      auto issue_dp = [&](bool first, bool last) {
+        const uint32_t n = ndp++;
+        if (first) ok = ok && wait(&sm.bar_a_full[1], units_dp++ & 1);
+        ok = ok && wait(&sm.bar_y_full[n & 1], (n >> 1) & 1);
+        if (!ok) return;
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < kAtoms; ++h)
+          issue_ss_x4(tmem + cDP, do_k + h * kAtomStep, v_k + (n & 1) * kNext + h * kAtomStep, id_s, h > 0);
+        commit(&sm.bar_dp);
+        commit(&sm.bar_y_empty[n & 1]);
+        if (last) commit(&sm.bar_a_empty[1]);
+      };
+      // the tile whose dS is waited for, and the one after it, whose S is issued
+      struct At {
+        bool valid = false, first = false, last = false;
+        int keys = 0;
+      } now, then;
+      Tiles<kRows> t(p.s, sm.pre, group, begin, stop);
+      auto take = [&](At& x) {
+        x.valid = t.valid;
+        if (!t.valid) return;
+        x.first = t.first, x.last = t.last, x.keys = min(kTile, t.s.len - t.j * kTile);
+        issue_s(t);
+        t.next(p.s);
+      };
+      take(now);
+      if (now.valid) issue_dp(now.first, now.last);
+      take(then);
+      uint32_t done = 0;
+      for (uint32_t n = 0; ok && now.valid; ++n) {
+        ok = wait(&sm.bar_ds, n & 1);
+        if (!ok) break;
+        if (then.valid) issue_dp(then.first, then.last);
+        if (now.first && done) ok = ok && wait(&sm.bar_acc_read, (done - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        issue_rows(tmem + cDQ, tmem + (n & 1) * 128, k_n + (n & 1) * kNext, id_g, now.keys, !now.first);
+        commit(&sm.bar_x_empty[n & 1]);
+        if (now.last) {
+          commit(&sm.bar_acc);
+          ++done;
+        }
+        now = then;
+        take(then);
+      }
+    } else if (warp < 11) {
+      // ---------------- Q and K (warp 9), dO and V (warp 10)
+      const int v = warp - 9;
+      const CUtensorMap* tm_a = v ? &tm_do : &tm_q;
+      const CUtensorMap* tm_x = v ? &tm_v : &tm_k;
+      uint64_t *full = v ? sm.bar_y_full : sm.bar_x_full, *empty = v ? sm.bar_y_empty : sm.bar_x_empty;
+      uint32_t units = 0, raws = 0, n = 0;
+      bool ok = true;
+      for (Tiles<kRows> t(p.s, sm.pre, group, begin, stop); ok && t.valid; t.next(p.s), ++n) {
+        if (t.first) {
+          ok = units == 0 || wait(&sm.bar_a_empty[v], (units - 1) & 1);
+          if (!ok) break;
+          ++units;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.bar_a_full[v], box * D * 2);
+#pragma unroll
+            for (int h = 0; h < kAtoms; ++h)
+              tma_load_3d(sm.a[v] + h * kAtom, tm_a, h * 64, t.s.hk * p.s.G, t.s.at + t.s.i * p.s.w, &sm.bar_a_full[v]);
+          }
+          __syncwarp();
+        }
+        const uint32_t st = n & 1;
+        ok = n < 2 || wait(&empty[st], ((n >> 1) - 1) & 1);
+        if (!ok) break;
+        uint8_t* tile = v ? sm.y[st] : sm.x[st];
+        ok = bring<D>(tile, min(kTile, t.s.len - t.j * kTile), kTile, kTile * D * 2, &full[st], &sm.bar_raw[v], raws, abort,
+                      [&](uint64_t* bar) {
+#pragma unroll
+                        for (int h = 0; h < kAtoms; ++h)
+                          tma_load_3d(tile + h * kAtom, tm_x, h * 64, t.s.at + t.j * kTile, t.s.hk, bar);
+                      });
+      }
+      int give_up = 0;
+      if (units) mbar_wait(&sm.bar_a_full[v], (units - 1) & 1, &give_up);
+      for (uint32_t e = 0; e < 2; ++e)
+        if (n > e) mbar_wait(&full[(n - 1 - e) & 1], ((n - 1 - e) >> 1) & 1, &give_up);
+    }
+  } else {
+    regs_increase<kRegsCompute>();
+    // ---------------- thread r of group g: row r of the tile, keys [64 g, 64 g + 64)
+    const int g = warp >> 2, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t dp_col = tmem + lanes + cDP + 64 * g;
+    const int token = r / p.s.G, head = r - token * p.s.G;
+    bool ok = true;
+    uint32_t units = 0;
+    Tiles<kRows> t(p.s, sm.pre, group, begin, stop);
+    const uint64_t a2 = f2(p.alpha, p.alpha);
+    float nl = 0.f, nd = 0.f;
+    for (uint32_t n = 0; ok && t.valid; t.next(p.s), ++n) {
+      const int i = t.s.i * p.s.w + token;
+      const bool live = token < p.s.w && i < t.s.len;
+      if (t.first) {
+        const size_t at = ((size_t)t.s.hk * p.s.T + t.s.at + i) * p.s.G + head;
+        nl = live ? __ldcg(p.nlse + at) : -INFINITY;
+        nd = live ? __ldcg(p.ndelta + at) : 0.f;
+      }
+      const int left = (live && p.s.causal ? i + 1 : t.s.len) - t.j * kTile - 64 * g;  // keys that the row sees
+      const uint32_t s_col = tmem + lanes + (n & 1) * 128 + 64 * g;
+      ok = wait(&sm.bar_s[n & 1], (n >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t sv[2][32];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld32(s_col + 32 * c, sv[c]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) reg_fence32(sv[c]);
+      if (__any_sync(0xffffffffu, left < 64)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (c * 32 + e >= left) sv[c][e] = 0xff800000u;
+      }
+      const uint64_t l2 = f2(nl, nl), d2 = f2(nd, nd);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float x, y;
+          f2split(ffma2(f2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), a2, l2), x, y);
+          sv[c][e] = __float_as_uint(ex2(x));
+          sv[c][e + 1] = __float_as_uint(ex2(y));
+        }
+      ok = wait(&sm.bar_dp, n & 1);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t dv[2][32];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) tmem_ld32(dp_col + 32 * c, dv[c]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 2; ++c) reg_fence32(dv[c]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float x, y;
+          f2split(fmul2(fadd2(f2(__uint_as_float(dv[c][e]), __uint_as_float(dv[c][e + 1])), d2),
+                        f2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]))),
+                  x, y);
+          w[e >> 1] = bf2(x, y);
+        }
+        tmem_st16(s_col + 16 * c, w);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&sm.bar_ds);
+      if (!t.last) continue;
+      ok = wait(&sm.bar_acc, units++ & 1);
+      if (!ok) break;
+      tc_fence_after();
+      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(p.d0.p) + (long long)(t.s.at + i) * p.d0.token +
+                           (t.s.hk * p.s.G + head) * p.d0.head + g * (D / 2);
+#pragma unroll 1
+      for (int d = 0; d < D / 2; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(tmem + lanes + cDQ + g * (D / 2) + d, o);
+        tmem_wait32(o);
+        if (live) store_row(row + d, o, p.sm_scale);
+      }
+      tc_fence_before();
+      mbar_arrive(&sm.bar_acc_read);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, kCols);
+  if (tid == 0 && sm.abort) atomicMax(p.s.status, (int)kDevTimeout);
+  pdl_wait();
+}
+
+template <int D>
+int launch(const BwdParams& dkv, const BwdParams& dq, const PreParams& pre, const sage_rows& Q, const sage_rows& K,
+           const sage_rows& V, int H, int sms, cudaStream_t st) {
+  CUtensorMap tq, tk, tv, to;
+  if (!make_tmap_queries(&tq, Q, D, H, dkv.s) || !make_tmap_keys(&tk, K, D, dkv.s) || !make_tmap_keys(&tv, V, D, dkv.s) ||
+      !make_tmap_queries(&to, pre.dO, D, H, dkv.s))
+    return SAGE_ERR_CUDA;
+  const size_t smem = sizeof(BwdSmem<D>) + 1024;
+  if (cudaFuncSetAttribute(packed_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+      cudaFuncSetAttribute(packed_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return SAGE_ERR_CUDA;
+  constexpr int kPerBlock = 256 / (D / 8) * 4;
+  const long long blocks = ((long long)dkv.s.T * H + kPerBlock - 1) / kPerBlock;
+  if (blocks > 0x7fffffffll) return SAGE_ERR_UNSUPPORTED;
+  if (launch_pdl(packed_pre_kernel<D>, dim3((unsigned)blocks), dim3(256), 0, st, pre) != cudaSuccess ||
+      launch_pdl(packed_dkv_kernel<D>, dim3(sms), dim3(kThreads), smem, st, dkv, tq, tk, tv, to) != cudaSuccess ||
+      launch_pdl(packed_dq_kernel<D>, dim3(sms), dim3(kThreads), smem, st, dq, tq, tk, tv, to) != cudaSuccess)
+    return SAGE_ERR_CUDA;
+  return SAGE_OK;
+}
+
+}  // namespace
+
+int launch_packed_bwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V, const sage_rows& O, const float* LSE,
+                      const sage_rows& dO, const int* cu, const sage_rows& dQ, const sage_rows& dK, const sage_rows& dV,
+                      void* ws, int T, int S, int H, int Hkv, int D, int causal, float sm_scale, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SAGE_ERR_CUDA;
+  const PackedWs l = packed_ws_layout(T, S, H, Hkv, D, true);
+  const PackedShape s = packed_shape(cu, ws, T, S, H, Hkv, causal);
+  float* nlse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.stats);
+  float* ndelta = nlse + (size_t)T * H;
+  const PreParams pre{s, O, dO, LSE, nlse, ndelta};
+  const BwdParams dkv{s, nlse, ndelta, dK, dV, sm_scale * kLog2e, sm_scale}, dq{s, nlse, ndelta, dQ, dQ, sm_scale * kLog2e, sm_scale};
+  ScopedTimer timer("packed_bwd", st);
+  return D == 128 ? launch<128>(dkv, dq, pre, Q, K, V, H, sms, st) : launch<64>(dkv, dq, pre, Q, K, V, H, sms, st);
+}
+
+}  // namespace sage

@@ -399,11 +399,11 @@ int launch(const FwdParams& p, const sage_rows& Q, const sage_rows& K, const sag
 
 }  // namespace
 
-PackedWs packed_ws_layout(int, int, int, int, int, bool) {
+PackedWs packed_ws_layout(int T, int, int H, int, int, bool backward) {
+  auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   PackedWs l;
-  l.cuts = 256;
-  l.part = l.cuts;
-  l.total = l.part;
+  l.stats = 256;
+  l.total = l.stats + (backward ? up((size_t)T * H * 2 * sizeof(float)) : 0);
   return l;
 }
 

@@ -117,3 +117,22 @@ def packed_forward(q, k, v, cu_seqlens, causal=True, sm_scale=None, o=None, lse=
           _array(lse, "lse", torch.float32, (H, T), dev), ws.data_ptr(), ws.nbytes, T, S, H, Hkv, D, int(causal),
           0.0 if sm_scale is None else float(sm_scale))
     return o, lse
+
+
+def packed_backward(q, k, v, o, lse, do, cu_seqlens, causal=True, sm_scale=None, dq=None, dk=None, dv=None, ws=None,
+                    stream=None):
+    """The gradients of packed_forward: from its inputs and results and dO [T, H, D], (dQ, dK, dV) bf16 in the shapes of
+    q, k and v.  ws: alloc_packed_ws(.., backward=True)."""
+    import torch
+    T, S, H, Hkv, D, dev = _shapes(q, k, cu_seqlens)
+    ws = _workspace(ws, (T, S, H, Hkv, D), True, dev, stream)
+    qs, kv = (T, H, D), (T, Hkv, D)
+    dq = _new(stream, dev, qs, torch.bfloat16) if dq is None else dq
+    dk = _new(stream, dev, kv, torch.bfloat16) if dk is None else dk
+    dv = _new(stream, dev, kv, torch.bfloat16) if dv is None else dv
+    _call(lib().sage_attn_packed_bwd, dev, stream, _rows(q, "q", qs, dev), _rows(k, "k", kv, dev), _rows(v, "v", kv, dev),
+          _rows(o, "o", qs, dev), _array(lse, "lse", torch.float32, (H, T), dev), _rows(do, "do", qs, dev),
+          _array(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev), _rows(dq, "dq", qs, dev), _rows(dk, "dk", kv, dev),
+          _rows(dv, "dv", kv, dev), ws.data_ptr(), ws.nbytes, T, S, H, Hkv, D, int(causal),
+          0.0 if sm_scale is None else float(sm_scale))
+    return dq, dk, dv

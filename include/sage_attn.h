@@ -433,6 +433,17 @@ int sage_attn_packed_fwd(const sage_rows *Q, const sage_rows *K, const sage_rows
                          const sage_rows *O, float *LSE, void *ws, size_t ws_bytes, int T, int S, int H, int Hkv, int D,
                          int causal, float sm_scale, void *stream);
 
+/*
+ * The gradients: with O and LSE of the forward, P = e^(S - LSE) and delta_i = sum_d dO O:
+ * dV = P^T dO, dS = P (dO V^T - delta), dQ = sm_scale dS K, dK = sm_scale dS^T Q; dK and dV sum over the query heads
+ * of their key/value head.  P and dS are rounded to bf16 for the products that take them; everything else is fp32.
+ * ws: of sage_attn_packed_ws_bytes(.., backward = 1).
+ */
+int sage_attn_packed_bwd(const sage_rows *Q, const sage_rows *K, const sage_rows *V, const sage_rows *O, const float *LSE,
+                         const sage_rows *dO, const int *cu_seqlens, const sage_rows *dQ, const sage_rows *dK,
+                         const sage_rows *dV, void *ws, size_t ws_bytes, int T, int S, int H, int Hkv, int D, int causal,
+                         float sm_scale, void *stream);
+
 /* Fill `views` with the device pointers inside a quantize workspace (qmean, dsb: NULL). */
 int sage_attn_ws_views(void *ws, int B, int H, int N, int D, sage_ws_views *views);
 

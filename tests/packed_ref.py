@@ -58,6 +58,37 @@ def forward(q, k, v, cu, causal, scale):
     return o, lse, o_tol, lse_tol
 
 
+def backward(q, k, v, o, lse, do, cu, causal, scale):
+    """dQ, dK, dV from the given O and LSE, and the bounds of their errors; 0 behind the sequences."""
+    (T, H, D), G = q.shape, q.shape[1] // k.shape[1]
+    out = {n: torch.zeros(x.shape, dtype=torch.float64, device=q.device) for n, x in (("dq", q), ("dk", k), ("dv", v))}
+    tol = {n: torch.zeros_like(x) for n, x in out.items()}
+    for b, e in _sequences(cu):
+        for h in range(H):
+            n = h // G
+            qh, kh, vh = (x[b:e, i].double() for x, i in ((q, h), (k, n), (v, n)))
+            oh, doh, l = o[b:e, h].double(), do[b:e, h].double(), lse[h, b:e, None].double()
+            p = torch.exp(_logits(qh, kh, causal, scale) - l)
+            delta = (doh * oh).sum(-1, keepdim=True)
+            ds = p * (doh @ vh.T - delta)
+            out["dv"][b:e, n] += p.T @ doh
+            out["dq"][b:e, h] = scale * ds @ kh
+            out["dk"][b:e, n] += scale * ds.T @ qh
+            # P off by the logits' errors and LSE's product with log2 e; dP and delta sums of D products in fp32; P and
+            # dS rounded to bf16, the products' sums in fp32
+            slack = _slack(qh, kh, D, scale) * 2 + l.abs() * 8 * FP32
+            sums = (D + 8) * 2 * FP32 * (doh.abs() @ vh.abs().T + (doh * oh).abs().sum(-1, keepdim=True))
+            rest = 2.0 ** -18
+            p_off = p * (BF16 * 1.01 + slack + rest)
+            ds_off = ds.abs() * (BF16 * 1.01 + slack + rest) + p * sums
+            tol["dv"][b:e, n] += p_off.T @ doh.abs()
+            tol["dq"][b:e, h] = scale * ds_off @ kh.abs()
+            tol["dk"][b:e, n] += scale * ds_off.T @ qh.abs()
+    for n in out:
+        tol[n] += BF16 * 1.01 * out[n].abs() + 1e-37
+    return out, tol
+
+
 def check(got, want, tol, what):
     """Every element within its bound (NaN is not)."""
     off = (got.double() - want).abs()

@@ -182,3 +182,146 @@ def test_on_a_stream():
     got = sa.packed_forward(q, k, v, cu, stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------- gradients
+
+def backward_checked(q, k, v, do, cu, causal, scale=None, **kw):
+    D = q.shape[2]
+    o, lse = sa.packed_forward(q, k, v, cu, causal=causal, sm_scale=scale)
+    ws = sa.alloc_packed_ws(q.shape[0], cu.numel() - 1, q.shape[1], k.shape[1], D, backward=True)
+    got = dict(zip(("dq", "dk", "dv"), sa.packed_backward(q, k, v, o, lse, do, cu, causal=causal, sm_scale=scale, ws=ws, **kw)))
+    assert sa.get_status(ws) == sa.SAGE_OK
+    want, tol = ref.backward(q, k, v, o, lse, do, cu, causal, D ** -0.5 if scale is None else scale)
+    b, e = int(cu[0]), int(cu[-1])
+    for n in got:
+        ref.check(got[n][b:e], want[n][b:e], tol[n][b:e], n)
+    return o, lse, got
+
+
+@pytest.mark.parametrize("lens,H,Hkv,D,causal", CASES, ids=IDS)
+def test_backward(lens, H, Hkv, D, causal):
+    q, k, v, do, cu = ref.inputs(lens, H, Hkv, D, seed=1)
+    backward_checked(q, k, v, do, cu, causal)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_gradients_of_rows_around_the_sequences_are_left(D):
+    q, k, v, do, cu = ref.inputs([40, 0, 129, 3], 4, 2, D, before=5, behind=200)
+    kw = {"d" + n: torch.full_like(x, 7.0) for n, x in (("q", q), ("k", k), ("v", v))}
+    _, _, got = backward_checked(q, k, v, do, cu, True, **kw)
+    b, e = int(cu[0]), int(cu[-1])
+    for x in got.values():
+        assert (x[:b] == 7).all() and (x[e:] == 7).all()
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("G", [1, 3, 4])
+def test_gradients_that_are_not_finite_stay_in_their_sequence(bad, causal, G):
+    lens = [100, 37, 5, 150, 33]
+    q, k, v, do, cu = ref.inputs(lens, G, 1, 128)
+    o, lse = sa.packed_forward(q, k, v, cu, causal=causal)
+    clean = sa.packed_backward(q, k, v, o, lse, do, cu, causal=causal)
+    at = cu.tolist()
+    for s in (1, 3):
+        for x in (q, k, v, o, do):
+            x[at[s]:at[s + 1]] = bad
+        lse[:, at[s]:at[s + 1]] = bad
+    got = sa.packed_backward(q, k, v, o, lse, do, cu, causal=causal)
+    for s in (0, 2, 4):
+        rows = slice(at[s], at[s + 1])
+        for x, y in zip(got, clean):
+            assert torch.equal(x[rows], y[rows])
+
+
+@pytest.mark.parametrize("gain,scale", [(30.0, None), (1.0, 1e-6), (1e-3, 5.0)])
+def test_gradients_at_logits_of_any_size(gain, scale):
+    q, k, v, do, cu = ref.inputs([300, 200], 2, 1, 128, gain=gain)
+    backward_checked(q, k, v, do, cu, True, scale)
+
+
+@pytest.mark.parametrize("D,causal", [(64, True), (128, False)])
+def test_gradients_against_differences(D, causal):
+    """Sum dO O of the 64-bit forward along a direction."""
+    lens, H, Hkv = [33, 70], 4, 2
+    q, k, v, do, cu = ref.inputs(lens, H, Hkv, D, seed=3)
+    o, lse = sa.packed_forward(q, k, v, cu, causal=causal)
+    grads = sa.packed_backward(q, k, v, o, lse, do, cu, causal=causal)
+    _, tol = ref.backward(q, k, v, o, lse, do, cu, causal, D ** -0.5)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = [y.double() for y in (q, k, v)]
+    for n, name in enumerate(("dq", "dk", "dv")):
+        way = torch.randn(x[n].shape, dtype=torch.float64, device="cuda", generator=g)
+        h = 1e-5
+
+        def loss(step):
+            y = list(x)
+            y[n] = x[n] + step * way
+            return (do.double() * ref.forward(*y, cu, causal, D ** -0.5)[0]).sum()
+
+        slope = (loss(h) - loss(-h)) / (2 * h)
+        # each gradient's bound along the way; O's rounding enters delta; the difference itself is good to h^2
+        delta_off = ref.BF16 * (do.double() * o.double()).abs().sum() * 10 * D ** -0.5 * way.abs().max() if n < 2 else 0.0
+        most = (tol[name] * way.abs()).sum() + delta_off + 1e-6
+        assert abs(float((grads[n].double() * way).sum() - slope)) <= float(most), name
+
+
+@pytest.mark.parametrize("layout", ["fused", "heads first"])
+def test_strides_of_the_gradients(layout):
+    H, Hkv, D, lens = 6, 2, 64, [70, 200, 1]
+    q, k, v, do, cu = ref.inputs(lens, H, Hkv, D)
+    o, lse = sa.packed_forward(q, k, v, cu)
+    plain = sa.packed_backward(q, k, v, o, lse, do, cu)
+    if layout == "fused":
+        x = torch.cat((q, k, v), 1)
+        q2, k2, v2 = x.split((H, Hkv, Hkv), 1)
+        dx = torch.zeros_like(x)
+        dq, dk, dv = dx.split((H, Hkv, Hkv), 1)
+        o2, do2 = o, do
+    else:
+        q2, k2, v2, o2, do2 = (y.transpose(0, 1).contiguous().transpose(0, 1) for y in (q, k, v, o, do))
+        dq, dk, dv = (torch.zeros_like(y) for y in (q2, k2, v2))
+    got = sa.packed_backward(q2, k2, v2, o2, lse, do2, cu, dq=dq, dk=dk, dv=dv)
+    for x, y in zip(got, plain):
+        assert torch.equal(x, y)
+
+
+def test_the_same_gradients_every_time():
+    q, k, v, do, cu = ref.inputs([3000, 500, 1], 8, 2, 128)
+    o, lse = sa.packed_forward(q, k, v, cu)
+    first = sa.packed_backward(q, k, v, o, lse, do, cu)
+    for _ in range(5):
+        for x, y in zip(first, sa.packed_backward(q, k, v, o, lse, do, cu)):
+            assert torch.equal(x, y)
+
+
+def test_a_captured_step():
+    """Forward and backward in one graph, replayed with other values and lengths."""
+    q, k, v, do, cu = ref.inputs([300, 200, 100], 4, 2, 128)
+    ws = sa.alloc_packed_ws(600, 3, 4, 2, 128, backward=True)
+    o, lse = torch.zeros_like(q), torch.zeros((4, 600), device="cuda")
+    dq, dk, dv = (torch.zeros_like(x) for x in (q, k, v))
+
+    def step():
+        sa.packed_forward(q, k, v, cu, o=o, lse=lse, ws=ws)
+        sa.packed_backward(q, k, v, o, lse, do, cu, dq=dq, dk=dk, dv=dv, ws=ws)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for n, lens in enumerate(([0, 599, 1], [200, 200, 200], [0, 0, 3])):
+        cu.copy_(torch.tensor([0] + lens).cumsum(0).to(torch.int32))
+        q.copy_(ref.inputs([600], 4, 2, 128, seed=n)[0])
+        g.replay()
+        rows = sum(lens)
+        want = sa.packed_forward(q, k, v, cu)
+        grads = sa.packed_backward(q, k, v, *want, do, cu)
+        assert torch.equal(o[:rows], want[0][:rows])
+        for x, y in zip((dq, dk, dv), grads):
+            assert torch.equal(x[:rows], y[:rows])
