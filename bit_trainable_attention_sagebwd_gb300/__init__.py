@@ -37,7 +37,7 @@ ABI_FUNCTIONS = ("sage_attn_ws_bytes", "sage_attn_bwd_ws_bytes", "sage_attn_quan
                  "sage_attn_kv_append", "sage_attn_kv_ws_bytes", "sage_attn_kv_attention", "sage_attn_kv_fork",
                  "sage_attn_kv_extend", "sage_attn_kv_truncate", "sage_attn_kv_compact_ws_bytes",
                  "sage_attn_kv_compact", "sage_attn_selftest_kv_join", "sage_attn_packed_ws_bytes", "sage_attn_packed_fwd",
-                 "sage_attn_packed_bwd")
+                 "sage_attn_packed_bwd", "sage_attn_rotary")
 
 
 class SageError(RuntimeError):
@@ -62,6 +62,14 @@ class sage_kv_cache(ctypes.Structure):
 
 class sage_rows(ctypes.Structure):
     _fields_ = [("p", ctypes.c_void_p), ("token", ctypes.c_longlong), ("head", ctypes.c_longlong)]
+
+
+class sage_rotary(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("gain", ctypes.c_float)]
+
+
+class sage_heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("batch", ctypes.c_longlong), ("token", ctypes.c_longlong), ("head", ctypes.c_longlong)]
 
 
 _lib = None
@@ -130,6 +138,8 @@ def lib():
             L.sage_attn_packed_ws_bytes.argtypes = [i] * 6
             L.sage_attn_packed_fwd.argtypes = [rp] * 3 + [vp, rp, vp, vp, sz] + [i] * 6 + [fp, vp]
             L.sage_attn_packed_bwd.argtypes = [rp] * 4 + [vp, rp, vp] + [rp] * 3 + [vp, sz] + [i] * 6 + [fp, vp]
+            hp = ctypes.POINTER(sage_heads)
+            L.sage_attn_rotary.argtypes = [ctypes.POINTER(sage_rotary)] + [hp] * 4 + [vp] * 3 + [i] * 7 + [vp]
             L.sage_attn_ws_views.argtypes = [vp, i, i, i, i, ctypes.POINTER(sage_ws_views)]
             L.sage_attn_get_status.argtypes = [vp, vp]
             L.sage_attn_selftest_wait.argtypes = [vp, u64, vp]
@@ -271,6 +281,10 @@ def sage_attn_packed_bwd(Q, K, V, O, LSE, dO, cu_seqlens, dQ, dK, dV, ws, ws_byt
                          stream):
     return lib().sage_attn_packed_bwd(Q, K, V, O, LSE, dO, cu_seqlens, dQ, dK, dV, ws, ws_bytes, T, S, H, Hkv, D,
                                       int(causal), float(sm_scale), stream)
+
+
+def sage_attn_rotary(r, Q, Qo, K, Ko, positions, start, cu_seqlens, B, N, S, H, Hkv, D, inverse, stream):
+    return lib().sage_attn_rotary(r, Q, Qo, K, Ko, positions, start, cu_seqlens, B, N, S, H, Hkv, D, int(inverse), stream)
 
 
 def sage_attn_bwd_noalloc(Q, K, V, O, LSE, dO, dQ, dK, dV, ws, B, H, N, D, causal, qk_norm, k_smooth, sm_scale,
@@ -692,3 +706,4 @@ def ws_tensors(ws, B, H, N, D, hkv=None, q_smooth=False, fp4=False) -> dict:
 from .kvcache import (KVCache, alloc_kv_compact_ws, alloc_kv_ws, kv_append, kv_attention, kv_cache,  # noqa: E402,F401
                       kv_compact, kv_extend, kv_fork, kv_truncate)
 from .packed import alloc_packed_ws, packed_backward, packed_forward  # noqa: E402,F401
+from .rotary_positions import Rotary, rotary, rotary_backward, rotary_frequencies, rotary_table  # noqa: E402,F401

@@ -1,0 +1,142 @@
+"""Rotary positions: the table of frequencies and the torch helpers of sage_attn_rotary (include/sage_attn.h says what
+it computes).
+
+    table = rotary_table(128, scaling="ramp", factor=8.0, context=4096)
+    q, k = rotary(table, q, k, cu_seqlens=cu)              # packed [T, H, D]: places in the sequences
+    q, k = rotary(table, q, k, start=pos)                  # [B, H, N, D]: pos[b], pos[b] + 1, ... (kv_extend's pos)
+    dq, dk = rotary_backward(table, dq, dk, cu_seqlens=cu)
+
+Like the other helpers these marshal arguments; everything but the table is computed by the CUDA library on the
+current stream of the tensors' device.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+from . import SAGE_ERR_UNSUPPORTED, SageError, lib, sage_heads, sage_rotary
+from .packed import _array, _call, _new
+
+_SCALINGS = ("none", "linear", "base", "ramp")
+
+
+class Rotary:
+    """Frequencies of rotary positions: int64 `turns` [rot / 2] (2^-64 turns a position), the layout of the pairs and the
+    factor of the turned channels."""
+
+    def __init__(self, turns, interleaved=False, gain=1.0):
+        import torch
+        if turns.dtype != torch.int64 or turns.dim() != 1 or not turns.is_contiguous():
+            raise ValueError("turns: contiguous int64 [rot / 2] expected")
+        if not turns.is_cuda:
+            raise ValueError("turns: on a GPU expected")
+        self.turns, self.rot, self.interleaved, self.gain = turns, 2 * turns.shape[0], bool(interleaved), float(gain)
+        self.device = turns.device
+        self.c = sage_rotary(turns.data_ptr(), self.rot, int(self.interleaved), self.gain)
+
+
+def rotary_frequencies(rot, base=10000.0, scaling="none", factor=1.0, context=4096, fast=32.0, slow=1.0):
+    """(radians a position of each of the rot / 2 pairs as a list, the factor of the turned channels).
+
+    f_c = base^(-2 c / rot), and for contexts `factor` times as long as the one trained at:
+      "linear"  f_c / factor (positions interpolated)
+      "base"    base times factor^(rot / (rot - 2)): the slowest pair as "linear", the fastest as it was
+      "ramp"    pairs that turn more than `fast` times over the trained `context` as they were, fewer than `slow`
+                times f_c / factor, between them in proportion to c; the channels grow by 0.1 ln factor + 1
+    """
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling: one of {_SCALINGS}, got {scaling!r}")
+    if rot < 4 or rot % 2 or not base > 1 or not factor >= 1:
+        raise ValueError("rotary_frequencies: an even rot of 4 at least, base above 1 and factor of 1 at least expected")
+    if scaling == "base":
+        base = base * factor ** (rot / (rot - 2))
+    f = [base ** (-2 * c / rot) for c in range(rot // 2)]
+    if scaling == "linear":
+        return [x / factor for x in f], 1.0
+    if scaling != "ramp":
+        return f, 1.0
+    if not (context > 0 and fast > slow > 0):
+        raise ValueError("rotary_frequencies: context above 0 and fast above slow expected")
+    first, last = (rot * math.log(context / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (fast, slow))
+    first, last = max(0, math.floor(first)), min(rot - 1, math.ceil(last))
+    share = [min(1.0, max(0.0, (c - first) / max(last - first, 1e-3))) for c in range(rot // 2)]
+    return [x * (1 - s) + x / factor * s for x, s in zip(f, share)], 0.1 * math.log(factor) + 1.0
+
+
+def rotary_table(rot, base=10000.0, scaling="none", factor=1.0, context=4096, fast=32.0, slow=1.0, interleaved=False,
+                 frequencies=None, gain=None, device="cuda") -> Rotary:
+    """The table of rotary_frequencies(rot, ..), or of given `frequencies` (rot / 2 radians a position); `gain` in place
+    of the scaling's factor of the turned channels."""
+    import torch
+    if rot % 16 or not 16 <= rot <= 128:
+        raise SageError("rotary_table", SAGE_ERR_UNSUPPORTED)
+    if frequencies is None:
+        frequencies, of_scaling = rotary_frequencies(rot, base, scaling, factor, context, fast, slow)
+    else:
+        frequencies, of_scaling = [float(f) for f in frequencies], 1.0
+    if len(frequencies) != rot // 2 or not all(math.isfinite(f) for f in frequencies):
+        raise ValueError(f"frequencies: {rot // 2} finite numbers expected")
+    # (the quotient has 53 bits, which 2^64 leaves as they are)
+    turns = [int(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in frequencies]
+    turns = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
+    return Rotary(torch.tensor(turns, dtype=torch.int64).to(device), interleaved, of_scaling if gain is None else gain)
+
+
+def _heads(x, name, shape, device):
+    """A tensor argument, [T, H, D] or [B, H, N, D], after its checks."""
+    import torch
+    if x.dtype is not torch.bfloat16 or tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name}: torch.bfloat16 of shape {tuple(shape)} expected, got {x.dtype} {tuple(x.shape)}")
+    if x.device != device:
+        raise ValueError(f"{name}: on {x.device}, the table is on {device}")
+    if x.stride(-1) != 1:
+        raise ValueError(f"{name}: its channels are not contiguous")
+    if x.dim() == 3:
+        return ctypes.byref(sage_heads(x.data_ptr(), 0, x.stride(0), x.stride(1)))
+    return ctypes.byref(sage_heads(x.data_ptr(), x.stride(0), x.stride(2), x.stride(1)))
+
+
+def _turn(table, q, k, cu_seqlens, start, positions, q_out, k_out, stream, inverse):
+    import torch
+    dev = table.device
+    if q.dim() not in (3, 4) or (k is not None and k.dim() != q.dim()):
+        raise ValueError("q, k: both [T, H, D] or both [B, H, N, D] expected")
+    packed = q.dim() == 3
+    if packed:
+        (N, H, D), B = q.shape, 1
+    else:
+        B, H, N, D = q.shape
+    if cu_seqlens is not None and (not packed or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2):
+        raise ValueError("cu_seqlens: [S + 1], with packed [T, H, D] tensors, expected")
+    S = 0 if cu_seqlens is None else cu_seqlens.shape[0] - 1
+    if table.rot > D:
+        raise SageError("rotary", SAGE_ERR_UNSUPPORTED)
+    hkv = 0 if k is None else k.shape[1]
+    ks = (N, hkv, D) if packed else (B, hkv, N, D)
+    if q_out is None:
+        q_out = _new(stream, dev, q.shape, torch.bfloat16)
+    if k is not None and k_out is None:
+        k_out = _new(stream, dev, ks, torch.bfloat16)
+    i32 = torch.int32
+    _call(lib().sage_attn_rotary, dev, stream, ctypes.byref(table.c), _heads(q, "q", q.shape, dev),
+          _heads(q_out, "q_out", q.shape, dev), None if k is None else _heads(k, "k", ks, dev),
+          None if k is None else _heads(k_out, "k_out", ks, dev),
+          None if positions is None else _array(positions, "positions", i32, (N,) if packed else (B, N), dev),
+          None if start is None else _array(start, "start", i32, (S,) if S else (B,), dev),
+          None if cu_seqlens is None else _array(cu_seqlens, "cu_seqlens", i32, (S + 1,), dev), B, N, S, H, hkv, D,
+          int(inverse))
+    return q_out if k is None else (q_out, k_out)
+
+
+def rotary(table, q, k=None, cu_seqlens=None, start=None, positions=None, q_out=None, k_out=None, stream=None):
+    """q and k (bf16, both [T, H, D] or both [B, H, N, D]) turned by their positions, in one pass; q_out may be q, k_out k.
+
+    Positions: `positions`, int32 [T] or [B, N]; or start[b] + t (int32 [B]; None: t); or with cu_seqlens (int32 [S + 1],
+    packed tensors) a token's place in its sequence + start[s] (int32 [S]); tokens of no sequence are left as they were.
+    Returns q_out, with k (q_out, k_out)."""
+    return _turn(table, q, k, cu_seqlens, start, positions, q_out, k_out, stream, False)
+
+
+def rotary_backward(table, dq, dk=None, cu_seqlens=None, start=None, positions=None, q_out=None, k_out=None, stream=None):
+    """The gradients of rotary's inputs from those of its outputs: the same call with the angles negated."""
+    return _turn(table, dq, dk, cu_seqlens, start, positions, q_out, k_out, stream, True)

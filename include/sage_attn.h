@@ -444,6 +444,39 @@ int sage_attn_packed_bwd(const sage_rows *Q, const sage_rows *K, const sage_rows
                          const sage_rows *dV, void *ws, size_t ws_bytes, int T, int S, int H, int Hkv, int D, int causal,
                          float sm_scale, void *stream);
 
+/*
+ * Rotary positions: what queries and keys get between their projection and any of the attentions above.  The first rot
+ * channels of every head form rot / 2 pairs (a, b): channels c and c + rot / 2, or (interleaved != 0) 2 c and 2 c + 1.
+ * At position n pair c becomes
+ *   gain (a cos n f_c - b sin n f_c,  a sin n f_c + b cos n f_c);
+ * the other channels stay as they are.  inverse != 0 turns by -n f_c: the gradients' way back.  Values are bf16,
+ * computed in fp32 and rounded once.
+ *  - turns: uint64 [rot / 2] on the device, 8-byte aligned: f_c in 2^-64 turns (2 pi radians), so positions of any size
+ *    keep their angle (the product wraps at whole turns; sine and cosine are good to 2^-22 or so).
+ *  - Q, Qo: [B, N, H, D], K, Ko (both NULL: none): [B, N, Hkv, D], the element (b, t, h, d) at
+ *    p[b * batch + t * token + h * head + d] (multiples of 8, p 16-byte aligned).  Qo may be Q, and Ko K, with the same
+ *    strides; otherwise what is written lies apart from what is read, and its rows from each other.
+ *  - The position of token t of batch row b: positions[b * N + t] (int32 [B, N]); or t + start[b] (int32 [B], NULL:
+ *    zeros: sage_attn_kv_extend's pos serves); or, with cu_seqlens (int32 [S + 1], not decreasing, B = 1), t's place in
+ *    its sequence + start[s] (int32 [S], NULL: zeros).  Tokens of no sequence are left as they were.
+ *    positions goes with neither of the others.  All are read on the device.
+ *  - D 64 or 128; rot a multiple of 16 up to D; B N below 2^31.
+ */
+typedef struct sage_rotary {
+  const uint64_t *turns;
+  int rot, interleaved;
+  float gain;
+} sage_rotary;
+
+typedef struct sage_heads {
+  void *p;
+  long long batch, token, head; /* strides in elements */
+} sage_heads;
+
+int sage_attn_rotary(const sage_rotary *r, const sage_heads *Q, const sage_heads *Qo, const sage_heads *K,
+                     const sage_heads *Ko, const int *positions, const int *start, const int *cu_seqlens, int B, int N,
+                     int S, int H, int Hkv, int D, int inverse, void *stream);
+
 /* Fill `views` with the device pointers inside a quantize workspace (qmean, dsb: NULL). */
 int sage_attn_ws_views(void *ws, int B, int H, int N, int D, sage_ws_views *views);
 
@@ -527,7 +560,8 @@ int sage_attn_step_host(const void *Q, const void *K, const void *V, const void 
  * each launch group with CUDA events recorded on the launching stream: "quantize"
  * (the two quantize kernels), "fwd", "bwd_pre" (D_i, LSE*log2e, dO codes),
  * "bwd_main" and "bwd_dq"; of the cache calls "kv_append", "kv_attention", "kv_pages" (fork,
- * extend, truncate) and "kv_compact".  Costs two event records per group; off by default. */
+ * extend, truncate) and "kv_compact"; "packed_fwd",
+ * "packed_bwd" and "rotary".  Costs two event records per group; off by default. */
 int sage_attn_timer_enable(int on);
 
 /* Restrict the timing to the launch group `kernel` (one of the names above; NULL:
