@@ -106,8 +106,13 @@ __device__ __forceinline__ long long places(const PackedShape& p, int b) {
   return len > 0 ? Units<KIND>(p, len).total() * p.Hkv : 0;
 }
 
-// Where a cut at offset `off` of a unit of n tiles is made.
-__device__ __forceinline__ int snap(long long off, int n) { return 2 * off <= n ? 0 : n; }
+// Where a cut at offset `off` of a unit of n tiles is made: not within kSnap tiles of its ends, since each part costs
+// its way through memory and the join.
+constexpr int kSnap = 2;
+__device__ __forceinline__ int snap(long long off, int n) {
+  if (off >= n) return n;
+  return off <= kSnap ? 0 : off >= n - kSnap ? n : (int)off;
+}
 
 // A part of a unit: tiles [c0, c1) of its n, of key/value head hk of the sequence at token `at`.
 struct Part {
@@ -202,6 +207,34 @@ struct Walk {
     return s;
   }
 };
+
+// A unit that was cut, written by the worker behind its first cut: its parts are those of the workers before, where it
+// begins, to `last`.  Worker x leaves its part of a unit at place 2 x + 1 if the unit begins with it, else 2 x.
+struct Cut {
+  int b, hk, i, last;  // b < 0: no such unit
+};
+constexpr int kMaxParts = 160;  // CTAs of a grid (one an SM)
+
+// The record of worker w0, whose walk stands at its beginning
+template <int KIND>
+__device__ __forceinline__ Cut first_cut(const PackedShape& p, const Line& line, const Walk<KIND>& walk, int w0) {
+  Cut c{-1, 0, 0, 0};
+  if (!walk.more || walk.c0 == 0) return c;
+  const int n = Units<KIND>(p, walk.len).tiles(walk.i);
+  const long long before = line.start(w0 - 1) - walk.unit_at;
+  if (before > 0 && snap(before, n) > 0) return c;  // (it lies in the unit too)
+  int last = w0;
+  while (last + 1 < line.parts) {
+    const long long off = line.start(last + 1) - walk.unit_at;
+    if (off >= n || snap(off, n) == n) break;
+    ++last;
+  }
+  return Cut{walk.b, walk.hk, walk.i, last};
+}
+// what a join may read (after a wait that ran out records are whatever the workspace held)
+__device__ __forceinline__ bool was_cut(const PackedShape& p, const Cut& c, int w0) {
+  return c.b >= 0 && c.b < p.S && (unsigned)c.hk < (unsigned)p.Hkv && c.i >= 0 && c.last >= w0 && w0 > 0 && c.last < kMaxParts;
+}
 
 // pre[g]: the places before each group of sequences, and their number behind the last (all threads of the CTA, which
 // must synchronise before they read it)

@@ -38,6 +38,8 @@ struct BwdParams {
   PackedShape s;
   const float *nlse, *ndelta;  // [Hkv][T][G]: -LSE log2 e, -delta
   sage_rows d0, d1;            // packed_dkv: dK, dV; packed_dq: dQ
+  Cut* cuts;
+  float* part;                 // two of each worker: [128][D] sums of d0, and of d1
   float alpha, sm_scale;       // alpha: sm_scale log2 e
 };
 
@@ -177,11 +179,17 @@ struct Tiles {
   Part s;
   int j;
   bool valid, first, last;
-  __device__ __forceinline__ Tiles(const PackedShape& p, const long long* pre, int group, long long begin, long long end)
+  Cut cut;  // (with the line)
+  __device__ __forceinline__ Tiles(const PackedShape& p, const long long* pre, int group, long long begin, long long end,
+                                   const Line* line = nullptr)
       : walk(p, pre, group, begin, end), j(0), valid(false), first(false), last(true) {
     s.c1 = 0;
+    if (line) cut = first_cut(p, *line, walk, blockIdx.x);
     next(p);
   }
+  __device__ __forceinline__ bool whole() const { return s.c0 == 0 && s.c1 == s.n; }
+  // where a part's sums go
+  __device__ __forceinline__ int place() const { return 2 * blockIdx.x + (s.c0 == 0 ? 1 : 0); }
   __device__ __forceinline__ void next(const PackedShape& p) {
     first = last;
     if (last) {
@@ -224,6 +232,11 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* to, const uint32_t (&o)
                    bf2(__uint_as_float(o[8 * e + 2]) * f, __uint_as_float(o[8 * e + 3]) * f),
                    bf2(__uint_as_float(o[8 * e + 4]) * f, __uint_as_float(o[8 * e + 5]) * f),
                    bf2(__uint_as_float(o[8 * e + 6]) * f, __uint_as_float(o[8 * e + 7]) * f));
+}
+
+__device__ __forceinline__ void store_part(float* to, const uint32_t (&o)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(to + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
 }
 
 // ------------------------------------------------------------------ dK and dV
@@ -395,7 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_col = tmem + lanes + cS + 64 * g, dp_col = tmem + lanes + cDP + 64 * g;
     bool ok = true;
     uint32_t units = 0;
-    Tiles<kKeys> t(p.s, sm.pre, group, begin, stop);
+    Tiles<kKeys> t(p.s, sm.pre, group, begin, stop, &line);
+    if (tid == 0) p.cuts[w0] = t.cut;
     const uint64_t a2 = f2(p.alpha, p.alpha);
     for (uint32_t n = 0; ok && t.valid; t.next(p.s), ++n) {
       const uint32_t st = n & 1;
@@ -487,7 +501,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t o[32];
           tmem_ld32(tmem + lanes + (x ? cDV : cDK) + g * (D / 2) + d, o);
           tmem_wait32(o);
-          if (live) store_row(row + d, o, f);
+          if (!live) continue;
+          if (t.whole())
+            store_row(row + d, o, f);
+          else
+            store_part(p.part + ((size_t)t.place() * 2 + x) * kTile * D + (size_t)r * D + g * (D / 2) + d, o);
         }
       }
       tc_fence_before();
@@ -649,7 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int token = r / p.s.G, head = r - token * p.s.G;
     bool ok = true;
     uint32_t units = 0;
-    Tiles<kRows> t(p.s, sm.pre, group, begin, stop);
+    Tiles<kRows> t(p.s, sm.pre, group, begin, stop, &line);
+    if (tid == 0) p.cuts[w0] = t.cut;
     const uint64_t a2 = f2(p.alpha, p.alpha);
     float nl = 0.f, nd = 0.f;
     for (uint32_t n = 0; ok && t.valid; t.next(p.s), ++n) {
@@ -724,7 +743,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[32];
         tmem_ld32(tmem + lanes + cDQ + g * (D / 2) + d, o);
         tmem_wait32(o);
-        if (live) store_row(row + d, o, p.sm_scale);
+        if (!live) continue;
+        if (t.whole())
+          store_row(row + d, o, p.sm_scale);
+        else
+          store_part(p.part + (size_t)t.place() * kTile * D + (size_t)r * D + g * (D / 2) + d, o);
       }
       tc_fence_before();
       mbar_arrive(&sm.bar_acc_read);
@@ -735,6 +758,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) tmem_dealloc(tmem, kCols);
   if (tid == 0 && sm.abort) atomicMax(p.s.status, (int)kDevTimeout);
   pdl_wait();
+}
+
+// ------------------------------------------------------------------ units that were cut
+// blockIdx.z: dK, dV, dQ; a thread adds up four channels of a row's parts
+constexpr int kJoinSlices = 4;
+template <int D>
+__global__ void __launch_bounds__(256) packed_bwd_join_kernel(const BwdParams dkv, const BwdParams dq) {
+  const int w0 = blockIdx.x, what = blockIdx.z;
+  pdl_wait();
+  pdl_trigger();
+  const BwdParams& p = what < 2 ? dkv : dq;
+  const Cut c = p.cuts[w0];
+  if (!was_cut(p.s, c, w0)) return;
+  int at, len;
+  sequence(p.s, c.b, at, len);
+  const sage_rows& to = what == 1 ? p.d1 : p.d0;
+  const size_t stride = (size_t)(what < 2 ? 2 : 1) * kTile * D;
+  const float* part = p.part + (what == 1 ? kTile * D : 0);
+  const float f = what == 1 ? 1.f : p.sm_scale;
+  constexpr int kPer = D / 4;  // threads of a row
+#pragma unroll 1
+  for (int r = blockIdx.y * (256 / kPer) + threadIdx.x / kPer; r < kTile; r += kJoinSlices * (256 / kPer)) {
+    const int d = threadIdx.x % kPer * 4;
+    const int token = what < 2 ? r : r / p.s.G, i = c.i * (what < 2 ? kTile : p.s.w) + token;
+    if (i >= len || (what == 2 && token >= p.s.w)) continue;
+    const int h = what < 2 ? c.hk : c.hk * p.s.G + r - token * p.s.G;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = w0 - 1; w <= c.last; ++w) {
+      const float4 x = *reinterpret_cast<const float4*>(part + (size_t)(2 * w + (w < w0)) * stride + (size_t)r * D + d);
+      sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
+    }
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(to.p) + (long long)(at + i) * to.token + h * to.head + d) =
+        make_uint2(bf2(sum.x * f, sum.y * f), bf2(sum.z * f, sum.w * f));
+  }
 }
 
 template <int D>
@@ -751,9 +808,11 @@ int launch(const BwdParams& dkv, const BwdParams& dq, const PreParams& pre, cons
   constexpr int kPerBlock = 256 / (D / 8) * 4;
   const long long blocks = ((long long)dkv.s.T * H + kPerBlock - 1) / kPerBlock;
   if (blocks > 0x7fffffffll) return SAGE_ERR_UNSUPPORTED;
+  const int grid = sms < kMaxParts ? sms : kMaxParts;
   if (launch_pdl(packed_pre_kernel<D>, dim3((unsigned)blocks), dim3(256), 0, st, pre) != cudaSuccess ||
-      launch_pdl(packed_dkv_kernel<D>, dim3(sms), dim3(kThreads), smem, st, dkv, tq, tk, tv, to) != cudaSuccess ||
-      launch_pdl(packed_dq_kernel<D>, dim3(sms), dim3(kThreads), smem, st, dq, tq, tk, tv, to) != cudaSuccess)
+      launch_pdl(packed_dkv_kernel<D>, dim3(grid), dim3(kThreads), smem, st, dkv, tq, tk, tv, to) != cudaSuccess ||
+      launch_pdl(packed_dq_kernel<D>, dim3(grid), dim3(kThreads), smem, st, dq, tq, tk, tv, to) != cudaSuccess ||
+      launch_pdl(packed_bwd_join_kernel<D>, dim3(grid, kJoinSlices, 3), dim3(256), 0, st, dkv, dq) != cudaSuccess)
     return SAGE_ERR_CUDA;
   return SAGE_OK;
 }
@@ -771,7 +830,10 @@ int launch_packed_bwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V
   float* nlse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.stats);
   float* ndelta = nlse + (size_t)T * H;
   const PreParams pre{s, O, dO, LSE, nlse, ndelta};
-  const BwdParams dkv{s, nlse, ndelta, dK, dV, sm_scale * kLog2e, sm_scale}, dq{s, nlse, ndelta, dQ, dQ, sm_scale * kLog2e, sm_scale};
+  Cut* cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(ws) + l.cuts);
+  float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.part);
+  const BwdParams dkv{s, nlse, ndelta, dK, dV, cuts, part, sm_scale * kLog2e, sm_scale};
+  const BwdParams dq{s, nlse, ndelta, dQ, dQ, cuts + kMaxParts, part + (size_t)2 * kMaxParts * 2 * kTile * D, sm_scale * kLog2e, sm_scale};
   ScopedTimer timer("packed_bwd", st);
   return D == 128 ? launch<128>(dkv, dq, pre, Q, K, V, H, sms, st) : launch<64>(dkv, dq, pre, Q, K, V, H, sms, st);
 }

@@ -12,6 +12,8 @@
 // TMA copies whole boxes: what lies behind a sequence's end is the next one's.  Rows of S behind it are not
 // stored, columns are masked; of V's rows those that a product reads (up to 15) are zeroed in shared memory, so that
 // nothing of another sequence, a NaN or an infinity among it, enters a sum.
+#include <type_traits>
+
 #include "issue.cuh"
 #include "launch.h"
 #include "packed.cuh"
@@ -32,8 +34,11 @@ struct FwdParams {
   __nv_bfloat16* O;
   long long o_token, o_head;
   float* LSE;
+  Cut* cuts;
+  float* part;  // two of each worker: [256][D] sums, [256] references, [256] row sums
   float alpha;  // sm_scale log2 e
 };
+constexpr int kUnitRows = 2 * kTile;  // of a unit
 
 template <int D>
 struct FwdSmem {
@@ -53,12 +58,12 @@ static_assert(sizeof(FwdSmem<128>) + 1024 <= 227 * 1024, "shared memory of a CTA
 // Row tiles alone in their unit take the places in turns (`solo` counts them).
 struct Places {
   int t0, rows;    // rows: row tiles
-  int end[2];      // by row tile: where its key tiles end
+  int end0, end1;  // by row tile: where its key tiles end
   __device__ __forceinline__ Places(const PackedShape& p, const Part& s, int& solo) {
     rows = (2 * s.i + 1) * p.w < s.len ? 2 : 1;
     t0 = rows == 1 ? (solo++ & 1) : 0;
-    end[0] = p.causal ? min(s.c1, ceil_div(min(s.len, (2 * s.i + 1) * p.w), kTile)) : s.c1;
-    end[1] = rows == 2 ? s.c1 : 0;
+    end0 = p.causal ? min(s.c1, ceil_div(min(s.len, (2 * s.i + 1) * p.w), kTile)) : s.c1;
+    end1 = s.c1;
   }
 };
 
@@ -101,12 +106,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // dependents may come once this CTA holds its TMEM: a later kernel that allocates all columns
   // must not reach this SM before
   pdl_trigger();
-  const uint32_t tmem = sm.tmem_base;
+  constexpr uint32_t tmem = 0;  // (where an allocation of all columns begins)
   volatile int* abort = &sm.abort;
   const long long total = sm.pre[kPackedGroups];
   const Line line{total, (int)min((long long)gridDim.x, max(total, 1ll))};
   const int w0 = blockIdx.x;
-  const bool idle = total == 0 || w0 >= line.parts;
+  if (sm.tmem_base != tmem && tid == 0) atomicMax(p.s.status, (int)kDevSetup);
+  const bool idle = total == 0 || w0 >= line.parts || sm.tmem_base != tmem;
   const long long begin = idle ? 0 : line.start(w0), stop = idle ? 0 : line.start(w0 + 1);
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
   int solo = 0;
@@ -114,76 +120,79 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     regs_decrease<kRegsIssue>();
     if (warp == 8) {
-      // ---------------- MMA issuer
+      // ---------------- MMA issuer.  An S goes in, then the P V of the S before it, whose softmax has had time.
       constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_o = idesc_bf16(kTile, D, false, true);
       constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
       const uint64_t dq = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), dk = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024);
       const uint64_t dv = sdesc_sw128(smem_u32(sm.v[0]), kAtom, 1024);
-      uint32_t kc = 0, nq[2] = {0, 0}, np[2] = {0, 0}, no[2] = {0, 0};  // key tiles, Q tiles, P tiles, O tiles so far
-      // the product P V that follows the next S
-      struct {
-        int t = -1;
-        uint32_t kc;
-        int keys;       // of the tile
-        bool first, last, frees;
-      } due;
+      uint32_t kc = 0, v_seen = 0;                       // key tiles so far, V tiles that were waited for
+      uint32_t q_ph = 0, p_ph = 0, o_ph = 3, o_any = 0;  // by place: phases of Q, P and O, and whether there was an O
+      int due = -1;                                      // the place whose P V follows
+      uint32_t due_kc = 0;
+      int due_keys = 0;
+      bool due_first = false, due_last = false, due_frees = false;
       bool ok = true;
       auto flush = [&]() {
-        if (due.t < 0) return;
-        const int t = due.t;
-        due.t = -1;
-        const uint32_t st = due.kc & 1;
-        ok = ok && wait(&sm.bar_v_full[st], (due.kc >> 1) & 1) && wait(&sm.bar_p[t], np[t] & 1);
-        ++np[t];
-        if (due.first) {
-          ok = ok && (no[t] == 0 || wait(&sm.bar_o_read[t], (no[t] - 1) & 1));
-          ++no[t];
+        if (due < 0) return;
+        const int t = due;
+        due = -1;
+        const uint32_t st = due_kc & 1;
+        if (due_kc == v_seen) {
+          ok = ok && wait(&sm.bar_v_full[st], (due_kc >> 1) & 1);
+          ++v_seen;
+        }
+        ok = ok && wait(&sm.bar_p[t], (p_ph >> t) & 1);
+        p_ph ^= 1 << t;
+        if (due_first) {
+          if ((o_any >> t) & 1) ok = ok && wait(&sm.bar_o_read[t], (o_ph >> t) & 1);
+          o_any |= 1 << t, o_ph ^= 1 << t;
         }
         if (!ok) return;
         tc_fence_after();
         const uint64_t b = dv + st * kNext;
-        const uint32_t d = tmem + kColO + t * 128, a = tmem + t * 128;
-        if (due.keys >= kTile) {
-          issue_ts_x4(d, a, b, id_o, !due.first);
+        const uint32_t d = kColO + t * 128, a = t * 128;
+        if (due_keys >= kTile) {
+          issue_ts_x4(d, a, b, id_o, !due_first);
           issue_ts_x4(d, a + 32, b + (4 * 2048 >> 4), id_o, 1);
         } else {
-          for (int x = 0; x * 16 < due.keys; ++x) issue_ts(d, a + 8 * x, b + (x * 2048 >> 4), id_o, x > 0 || !due.first);
+#pragma unroll 1
+          for (int e = 0; e * 16 < due_keys; ++e) issue_ts(d, a + 8 * e, b + (e * 2048 >> 4), id_o, e > 0 || !due_first);
         }
-        if (due.frees) commit(&sm.bar_v_empty[st]);
-        if (due.last) commit(&sm.bar_o[t]);
+        if (due_frees) commit(&sm.bar_v_empty[st]);
+        if (due_last) commit(&sm.bar_o[t]);
       };
       Walk<kPairs> walk(p.s, sm.pre, group, begin, stop);
+#pragma unroll 1
       while (ok && walk.more) {
         const Part s = walk.next(p.s);
         const Places pl(p.s, s, solo);
+#pragma unroll 1
         for (int j = s.c0; ok && j < s.c1; ++j, ++kc) {
           const uint32_t st = kc & 1;
           ok = wait(&sm.bar_k_full[st], (kc >> 1) & 1);
 #pragma unroll 1
-          for (int x = 0; ok && x < pl.rows; ++x) {
-            if (j >= pl.end[x]) continue;
+          for (int x = j < pl.end0 ? 0 : 1; ok && x < pl.rows; ++x) {
             const int t = x ^ pl.t0;
-            const bool last_place = x == 1 || pl.rows == 1 || j >= pl.end[1];
-            if (due.t == t) flush();
+            const bool last = j + 1 == (x ? pl.end1 : pl.end0), frees = x + 1 == pl.rows;
+            if (due == t) flush();
             if (j == s.c0) {
-              ok = ok && wait(&sm.bar_q_full[t], nq[t] & 1);
-              ++nq[t];
+              ok = ok && wait(&sm.bar_q_full[t], (q_ph >> t) & 1);
+              q_ph ^= 1 << t;
             }
             if (!ok) break;
             tc_fence_after();
             const uint64_t a = dq + t * kNext, b = dk + st * kNext;
 #pragma unroll
-            for (int h = 0; h < kAtoms; ++h) issue_ss_x4(tmem + t * 128, a + h * kAtomStep, b + h * kAtomStep, id_s, h > 0);
+            for (int h = 0; h < kAtoms; ++h) issue_ss_x4(t * 128, a + h * kAtomStep, b + h * kAtomStep, id_s, h > 0);
             commit(&sm.bar_s[t]);
-            if (last_place) commit(&sm.bar_k_empty[st]);
-            if (j + 1 == pl.end[x]) commit(&sm.bar_q_empty[t]);
+            if (frees) commit(&sm.bar_k_empty[st]);
+            if (last) commit(&sm.bar_q_empty[t]);
             flush();
-            due.t = t, due.kc = kc, due.keys = s.len - j * kTile, due.first = j == s.c0, due.last = j + 1 == pl.end[x];
-            due.frees = last_place;
+            due = t, due_kc = kc, due_keys = s.len - j * kTile, due_first = j == s.c0, due_last = last, due_frees = frees;
           }
         }
       }
-      flush();
+      if (ok) flush();
     } else if (warp == 9) {
       // ---------------- Q and K
       uint32_t kc = 0, nq[2] = {0, 0};
@@ -277,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t ns = 0, no = 0;
     bool ok = true;
     Walk<kPairs> walk(p.s, sm.pre, group, begin, stop);
+    if (tid == 0) p.cuts[w0] = first_cut(p.s, line, walk, w0);
     while (ok && walk.more) {
       const Part s = walk.next(p.s);
       const Places pl(p.s, s, solo);
@@ -286,30 +296,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = token < p.s.w && i < s.len;
       const int lim = live && p.s.causal ? i + 1 : s.len;
       float m = -INFINITY, l = 0.f;
+      const int end = x ? pl.end1 : pl.end0;
 #pragma unroll 1
-      for (int j = s.c0; ok && j < pl.end[x]; ++j) {
+      for (int j = s.c0; ok && j < end; ++j) {
         ok = wait(&sm.bar_s[t], ns++ & 1);
         if (!ok) break;
         tc_fence_after();
-        uint32_t sv[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, sv[c]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 4; ++c) reg_fence32(sv[c]);
+        // (twice over S in loops: unrolled whole, the code of the warps' roles together takes longer to fetch than to run)
         const int left = lim - j * kTile;
-        if (__any_sync(0xffffffffu, left < kTile)) {
+        const bool edge = __any_sync(0xffffffffu, left < kTile);
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (apart: one chain of maxima would wait for itself)
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 64) {
+          uint32_t v[2][32];
+          tmem_ld32(s_col + c, v[0]);
+          tmem_ld32(s_col + c + 32, v[1]);
+          tmem_ld_wait();
+          reg_fence32(v[0]);
+          reg_fence32(v[1]);
+          if (edge) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+            for (int e = 0; e < 64; ++e)
+              if (c + e >= left) v[e >> 5][e & 31] = 0xff800000u;
+          }
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c * 32 + e >= left) sv[c][e] = 0xff800000u;
+          for (int e = 0; e < 64; e += 2)
+            tops[(e >> 1) & 3] = max3(tops[(e >> 1) & 3], __uint_as_float(v[e >> 5][e & 31]), __uint_as_float(v[e >> 5][(e & 31) + 1]));
         }
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) top = max3(top, __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
+        float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
         top *= p.alpha;
         const bool raise = top > m + kRaise;  // (m = -infinity: whenever there is a key)
         if (__any_sync(0xffffffffu, raise)) {
@@ -330,23 +344,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float sub = m == -INFINITY ? 0.f : m;
         const uint64_t a2 = f2(p.alpha, p.alpha), m2 = f2(-sub, -sub);
-        uint64_t sum = f2(0.f, 0.f);
+        uint64_t sums[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 32) {
+          uint32_t v[32], w[16];
+          tmem_ld32(s_col + c, v);
+          tmem_wait32(v);
+          if (edge) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
+            for (int e = 0; e < 32; ++e)
+              if (c + e >= left) v[e] = 0xff800000u;
+          }
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float u0, u1;
-            f2split(ffma2(f2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), a2, m2), u0, u1);
+            f2split(ffma2(f2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), a2, m2), u0, u1);
             u0 = ex2(u0), u1 = ex2(u1);
-            sum = fadd2(sum, f2(u0, u1));
+            sums[(e >> 1) & 1] = fadd2(sums[(e >> 1) & 1], f2(u0, u1));
             const __nv_bfloat162 h = __floats2bfloat162_rn(u0, u1);
             w[e >> 1] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          tmem_st16(s_col + 16 * c, w);
+          tmem_st16(s_col + (c >> 1), w);
         }
         float y0, y1;
-        f2split(sum, y0, y1);
+        f2split(fadd2(sums[0], sums[1]), y0, y1);
         l += y0 + y1;
         tmem_st_wait();
         tc_fence_before();
@@ -356,6 +377,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = ok && wait(&sm.bar_o[t], no++ & 1);
       if (!ok) break;
       tc_fence_after();
+      const bool whole = s.c0 == 0 && s.c1 == s.n;
+      float* part = p.part + (size_t)(2 * w0 + (s.c0 == 0 ? 1 : 0)) * kUnitRows * (D + 2);
       const float f = l != 0.f ? 1.f / l : 0.f;
       const int h = s.hk * p.s.G + head;
       __nv_bfloat16* orow = p.O + (long long)(s.at + i) * p.o_token + h * p.o_head;
@@ -365,6 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(o_col + d, o);
         tmem_wait32(o);
         if (!live) continue;
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(part + (size_t)(x * kTile + r) * D + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          continue;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint4 y;
@@ -377,13 +406,56 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       mbar_arrive(&sm.bar_o_read[t]);
-      if (live) p.LSE[(size_t)h * p.s.T + s.at + i] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (live && !whole)
+        part[(size_t)kUnitRows * D + x * kTile + r] = m, part[(size_t)kUnitRows * (D + 1) + x * kTile + r] = l;
+      else if (live)
+        p.LSE[(size_t)h * p.s.T + s.at + i] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, kCols);
+  if (warp == 8) tmem_dealloc(sm.tmem_base, kCols);
   if (tid == 0 && sm.abort) atomicMax(p.s.status, (int)kDevTimeout);
+}
+
+// The rows of units that were cut: a warp a row, D / 32 channels a lane.  O = sum O_k 2^(m_k - M) / sum l_k 2^(m_k - M).
+constexpr int kJoinWarps = 8, kJoinSlices = 8;
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) packed_fwd_join_kernel(const FwdParams p) {
+  const int w0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  const Cut c = p.cuts[w0];
+  if (!was_cut(p.s, c, w0)) return;
+  int at, len;
+  sequence(p.s, c.b, at, len);
+  constexpr int kPer = D / 32;
+  constexpr size_t kPart = (size_t)kUnitRows * (D + 2);
+#pragma unroll 1
+  for (int row = blockIdx.y * kJoinWarps + warp; row < kUnitRows; row += kJoinWarps * kJoinSlices) {
+    const int x = row / kTile, r = row % kTile, token = r / p.s.G;
+    const int i = (2 * c.i + x) * p.s.w + token;
+    if (token >= p.s.w || i >= len) continue;
+    // (the first part lies at place 2 (w0 - 1) + 1, the others at 2 w)
+    float top = -INFINITY;
+    for (int w = w0 - 1; w <= c.last; ++w)
+      top = fmaxf(top, p.part[(size_t)(2 * w + (w < w0)) * kPart + (size_t)kUnitRows * D + row]);
+    const float sub = top == -INFINITY ? 0.f : top;
+    float o[kPer] = {}, l = 0.f;
+    for (int w = w0 - 1; w <= c.last; ++w) {
+      const float* part = p.part + (size_t)(2 * w + (w < w0)) * kPart;
+      const float f = ex2(part[(size_t)kUnitRows * D + row] - sub);
+      l = fmaf(part[(size_t)kUnitRows * (D + 1) + row], f, l);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) o[e] = fmaf(part[(size_t)row * D + lane * kPer + e], f, o[e]);
+    }
+    const float f = l != 0.f ? 1.f / l : 0.f;
+    const int h = c.hk * p.s.G + r - token * p.s.G;
+    __nv_bfloat162* to = reinterpret_cast<__nv_bfloat162*>(p.O + (long long)(at + i) * p.o_token + h * p.o_head + lane * kPer);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) to[e / 2] = __floats2bfloat162_rn(o[e] * f, o[e + 1] * f);
+    if (lane == 0) p.LSE[(size_t)h * p.s.T + at + i] = l != 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
 }
 
 template <int D>
@@ -394,15 +466,22 @@ int launch(const FwdParams& p, const sage_rows& Q, const sage_rows& K, const sag
     return SAGE_ERR_CUDA;
   const size_t smem = sizeof(FwdSmem<D>) + 1024;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SAGE_ERR_CUDA;
-  return launch_pdl(kern, dim3(sms), dim3(kThreads), smem, st, p, tq, tk, tv) == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
+  const int grid = sms < kMaxParts ? sms : kMaxParts;
+  if (launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p, tq, tk, tv) != cudaSuccess ||
+      launch_pdl(packed_fwd_join_kernel<D>, dim3(grid, kJoinSlices), dim3(32 * kJoinWarps), 0, st, p) != cudaSuccess)
+    return SAGE_ERR_CUDA;
+  return SAGE_OK;
 }
 
 }  // namespace
 
-PackedWs packed_ws_layout(int T, int, int H, int, int, bool backward) {
+PackedWs packed_ws_layout(int T, int, int H, int, int D, bool backward) {
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   PackedWs l;
-  l.stats = 256;
+  l.cuts = 256;
+  l.part = l.cuts + up(2 * kMaxParts * sizeof(Cut));
+  // (the backward's are dK, dV and dQ of 128 rows each)
+  l.stats = l.part + up((size_t)2 * kMaxParts * (backward ? 3 * kTile * D : kUnitRows * (D + 2)) * sizeof(float));
   l.total = l.stats + (backward ? up((size_t)T * H * 2 * sizeof(float)) : 0);
   return l;
 }
@@ -418,6 +497,9 @@ int launch_packed_fwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V
   p.O = static_cast<__nv_bfloat16*>(O.p);
   p.o_token = O.token, p.o_head = O.head;
   p.LSE = LSE;
+  const PackedWs l = packed_ws_layout(T, S, H, Hkv, D, false);
+  p.cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(ws) + l.cuts);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.part);
   p.alpha = sm_scale * 1.4426950408889634f;
   ScopedTimer timer("packed_fwd", st);
   return D == 128 ? launch<128>(p, Q, K, V, H, sms, st) : launch<64>(p, Q, K, V, H, sms, st);
