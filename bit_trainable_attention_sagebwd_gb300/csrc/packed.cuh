@@ -7,8 +7,9 @@
 //   kPairs  two row tiles against the key tiles that they see     (the forward)
 //   kRows   one row tile against the same                         (dQ)
 //   kKeys   one key tile (128 keys) against the row tiles that see it  (dK, dV)
-// The units of a sequence follow each other, key/value head by head; every unit counts its tiles and kUnitCost
-// more, so that the line of all units can be cut into equal shares of time.
+// The units of a sequence follow each other, key/value head by head.  Every unit counts the tokens that it sees and
+// kUnitCost more, so that the line of all units can be cut into equal shares of time.  One warp of a CTA walks its
+// share and hands the parts to the others (Feed).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -26,13 +27,15 @@ struct PackedShape {
   const int* cu;
   int* status;
   int T, S, Hkv, G, w, causal;
+  unsigned inv_w;  // 2^32 / w, rounded up (w > 1)
+  __device__ __forceinline__ int over_w(int n) const { return w > 1 ? (int)__umulhi((unsigned)n, inv_w) : n; }  // n / w
 };
 
 namespace {  // internal linkage: each translation unit keeps its own copy
 
 constexpr int kDevSequence = 7;  // (kDevIndex of the cache calls: a number on the device is out of range)
 constexpr int kTile = 128;
-constexpr int kUnitCost = 1;
+constexpr int kUnitCost = 256;  // a unit's beginning and end, in tokens
 
 enum UnitKind { kPairs, kRows, kKeys };
 
@@ -46,56 +49,60 @@ __device__ __forceinline__ void sequence(const PackedShape& p, int b, int& at, i
   at = ok ? x : 0, len = ok ? y - x : 0;
 }
 
-// sum of floor((a i + b) / m) over i < n, by exchanging the roles of the two axes as in Euclid's algorithm
-// (a n + b stays below 2^31 here)
-__device__ __forceinline__ long long floor_sum(unsigned n, unsigned a, unsigned b, unsigned m) {
-  long long sum = 0;
-#pragma unroll 1
-  while (n) {
-    if (a >= m) {
-      sum += (long long)n * (n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      sum += (long long)n * (b / m);
-      b %= m;
-    }
-    const unsigned y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const unsigned x = m;
-    m = a;
-    a = x;
-  }
-  return sum;
-}
-
 // A sequence's units, for one key/value head
 template <int KIND>
 struct Units {
   int len, u;  // u: tokens of a unit
-  int causal, w;
-  __device__ __forceinline__ Units(const PackedShape& p, int len_)
-      : len(len_), u(KIND == kPairs ? 2 * p.w : KIND == kRows ? p.w : kTile), causal(p.causal), w(p.w) {}
-  __device__ __forceinline__ int count() const { return ceil_div(len, u); }
+  const PackedShape& p;
+  __device__ __forceinline__ Units(const PackedShape& p_, int len_)
+      : len(len_), u(KIND == kPairs ? 2 * p_.w : KIND == kRows ? p_.w : kTile), p(p_) {}
+  __device__ __forceinline__ int row_tiles() const { return p.over_w(len + p.w - 1); }
+  __device__ __forceinline__ int count() const {
+    return KIND == kKeys ? (len + kTile - 1) / kTile : KIND == kRows ? row_tiles() : (row_tiles() + 1) / 2;
+  }
   // the first tile that unit i sees, of those of the sequence (kKeys; elsewhere 0)
-  __device__ __forceinline__ int first(int i) const { return KIND == kKeys && causal ? i * kTile / w : 0; }
+  __device__ __forceinline__ int first(int i) const { return KIND == kKeys && p.causal ? p.over_w(i * kTile) : 0; }
   // tiles of unit i
   __device__ __forceinline__ int tiles(int i) const {
-    if (KIND == kKeys) return ceil_div(len, w) - first(i);
-    return ceil_div(causal ? min(len, (i + 1) * u) : len, kTile);
+    if (KIND == kKeys) return row_tiles() - first(i);
+    return ((p.causal ? min(len, (i + 1) * u) : len) + kTile - 1) / kTile;
   }
-  // places of the line before unit i
+  // places of the line before unit i, and its own (tokens as if every unit were whole; below 2^50)
   __device__ __forceinline__ long long before(int i) const {
-    long long n = (long long)i * kUnitCost;
-    if (i == 0) return n;
-    if (!causal) return n + (long long)i * tiles(0);
-    if (KIND == kKeys) return n + (long long)i * ceil_div(len, w) - floor_sum(i, kTile, 0, w);
-    const bool all = i == count();  // (the last unit ends with the sequence)
-    return n + floor_sum(all ? i - 1 : i, u, u + kTile - 1, kTile) + (all ? ceil_div(len, kTile) : 0);
+    if (!p.causal) return (long long)i * (len + kUnitCost);
+    if (KIND == kKeys) return (long long)i * (len + kUnitCost) - (long long)i * (i - 1) / 2 * kTile;
+    return (long long)i * (i + 1) / 2 * u + (long long)i * kUnitCost;
+  }
+  __device__ __forceinline__ int own(int i) const {
+    return kUnitCost + (!p.causal ? len : KIND == kKeys ? len - i * kTile : (i + 1) * u);
   }
   __device__ __forceinline__ long long total() const { return before(count()); }
+  // the unit that holds place x of a head: the root of before(i) = x, put right
+  __device__ __forceinline__ int at(long long x) const {
+    const float c = kUnitCost, f = (float)x;
+    float i;
+    if (!p.causal) {
+      i = f / ((float)len + c);
+    } else if (KIND == kKeys) {
+      const float a = (float)len + c + kTile / 2;
+      i = (a - sqrtf(fmaxf(0.f, a * a - 2 * kTile * f))) / kTile;
+    } else {
+      const float a = (float)u / 2 + c;
+      i = (sqrtf(fmaf(a, a, 2 * (float)u * f)) - a) / (float)u;
+    }
+    int k = min(max((int)i, 0), count() - 1);
+    while (k > 0 && before(k) > x) --k;
+    while (k + 1 < count() && before(k + 1) <= x) ++k;
+    return k;
+  }
+  // the tile of a unit where a cut at offset `off` is made: not within kSnap tiles of its ends, since each part costs
+  // its way through memory and the join
+  __device__ __forceinline__ int cut(long long off, int n) const {
+    if (off <= 0) return 0;
+    const int c = off >= (1 << 25) ? n : KIND == kKeys ? p.over_w((int)off) : (int)off / kTile;
+    return c >= n - kSnap ? n : c <= kSnap ? 0 : c;
+  }
+  static constexpr int kSnap = 2;
 };
 
 // places of all of sequence b's units
@@ -106,15 +113,23 @@ __device__ __forceinline__ long long places(const PackedShape& p, int b) {
   return len > 0 ? Units<KIND>(p, len).total() * p.Hkv : 0;
 }
 
-// Where a cut at offset `off` of a unit of n tiles is made: not within kSnap tiles of its ends, since each part costs
-// its way through memory and the join.
-constexpr int kSnap = 2;
-__device__ __forceinline__ int snap(long long off, int n) {
-  if (off >= n) return n;
-  return off <= kSnap ? 0 : off >= n - kSnap ? n : (int)off;
-}
+// The line of all units, cut into equal parts for the CTAs of a grid, of kLeast places at least (two cuts must not
+// fall into one tile).
+constexpr int kLeast = 512;
+static_assert(kLeast >= 2 * kTile, "a tile between two cuts");
+struct Shares {
+  long long total, each;
+  int parts, rest;
+  __device__ __forceinline__ Shares(long long total_, int most) : total(total_) {
+    parts = (int)min((long long)most, max(total / kLeast, 1ll));
+    each = total / parts;
+    rest = (int)(total - each * parts);
+  }
+  // where part v begins
+  __device__ __forceinline__ long long start(int v) const { return each * v + (unsigned)(rest * v) / (unsigned)parts; }
+};
 
-// A part of a unit: tiles [c0, c1) of its n, of key/value head hk of the sequence at token `at`.
+// A part of a unit: tiles [c0, c1) of its n, of key/value head hk of the sequence at token `at`.  c1 = 0: no more parts.
 struct Part {
   int b, at, len, hk, i, n, c0, c1;
 };
@@ -130,52 +145,50 @@ struct Walk {
     if (!more) return;
     const int lane = threadIdx.x & 31;
     const int g = row_at(pre, kPackedGroups, begin);
-    // the sequence, 32 of the group at a time
     long long base = pre[g];
-    const int end_b = min(p.S, (g + 1) * group);
-    b = end_b;
-    for (int b0 = g * group; b0 < end_b; b0 += 32) {
-      long long s = b0 + lane < end_b ? places<KIND>(p, b0 + lane) : 0;
+    b = g;
+    if (group > 1) {
+      // the sequence, 32 of the group at a time
+      const int end_b = min(p.S, (g + 1) * group);
+      b = end_b;
+      for (int b0 = g * group; b0 < end_b; b0 += 32) {
+        long long s = b0 + lane < end_b ? places<KIND>(p, b0 + lane) : 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += x;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, s, o);
+          if (lane >= o) s += x;
+        }
+        const int k = __popc(__ballot_sync(0xffffffffu, base + s <= begin));
+        const long long before = __shfl_sync(0xffffffffu, s, max(k - 1, 0));
+        if (k > 0) base += before;
+        b = min(end_b, b0 + k);
+        if (k < 32) break;
       }
-      const int k = __popc(__ballot_sync(0xffffffffu, base + s <= begin));
-      const long long before = __shfl_sync(0xffffffffu, s, max(k - 1, 0));
-      if (k > 0) base += before;
-      b = min(end_b, b0 + k);
-      if (k < 32) break;
     }
-    if (b >= end_b) {  // (not reached while the sequences stand still)
+    if (b < p.S) sequence(p, b, at, len);
+    if (len <= 0) {  // (not while the sequences stand still)
       more = false;
       return;
     }
-    sequence(p, b, at, len);
     const Units<KIND> us(p, len);
     const long long head = us.total();
-    hk = (int)mul_div(begin - base, 1, head);
+    hk = min((int)((float)(begin - base) / (float)head), p.Hkv - 1);
+    while (hk > 0 && hk * head > begin - base) --hk;
+    while (hk + 1 < p.Hkv && (hk + 1) * head <= begin - base) ++hk;
     base += hk * head;
-    // the unit, by a search with a place for each lane
-    int lo = 0, hi = us.count();
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) >> 5, c = lo + (lane + 1) * step;
-      const int k = __popc(__ballot_sync(0xffffffffu, c < hi && base + us.before(c) <= begin));
-      hi = min(hi, lo + (k + 1) * step);
-      lo += k * step;
-    }
-    i = lo;
-    unit_at = base + us.before(lo);
-    const int n = us.tiles(lo);
-    c0 = snap(begin - unit_at, n);
-    if (c0 >= n) advance(p, n);
+    i = us.at(begin - base);
+    unit_at = base + us.before(i);
+    const int n = us.tiles(i);
+    c0 = us.cut(begin - unit_at, n);
+    if (c0 >= n) advance(p);
     settle(p);
   }
   // to the next unit
-  __device__ __forceinline__ void advance(const PackedShape& p, int n) {
-    unit_at += n + kUnitCost;
+  __device__ __forceinline__ void advance(const PackedShape& p) {
+    const Units<KIND> us(p, len);
+    unit_at += us.own(i);
     c0 = 0;
-    if (++i < Units<KIND>(p, len).count()) return;
+    if (++i < us.count()) return;
     i = 0;
     if (++hk < p.Hkv) return;
     hk = 0;
@@ -190,18 +203,17 @@ struct Walk {
   // whether anything of the unit at hand lies before the end
   __device__ __forceinline__ void settle(const PackedShape& p) {
     if (!more) return;
-    const long long off = stop - unit_at;
-    if (off <= 0 || snap(off, Units<KIND>(p, len).tiles(i)) <= c0) more = false;
+    const Units<KIND> us(p, len);
+    if (us.cut(stop - unit_at, us.tiles(i)) <= c0) more = false;
   }
   __device__ __forceinline__ Part next(const PackedShape& p) {
-    const int n = Units<KIND>(p, len).tiles(i);
-    Part s{b, at, len, hk, i, n, c0, n};
-    const long long off = stop - unit_at;
-    if (off < n + kUnitCost) s.c1 = snap(off, n);
+    const Units<KIND> us(p, len);
+    const int n = us.tiles(i);
+    const Part s{b, at, len, hk, i, n, c0, us.cut(stop - unit_at, n)};
     if (s.c1 < n) {
       more = false;
     } else {
-      advance(p, n);
+      advance(p);
       settle(p);
     }
     return s;
@@ -217,24 +229,75 @@ constexpr int kMaxParts = 160;  // CTAs of a grid (one an SM)
 
 // The record of worker w0, whose walk stands at its beginning
 template <int KIND>
-__device__ __forceinline__ Cut first_cut(const PackedShape& p, const Line& line, const Walk<KIND>& walk, int w0) {
-  Cut c{-1, 0, 0, 0};
-  if (!walk.more || walk.c0 == 0) return c;
-  const int n = Units<KIND>(p, walk.len).tiles(walk.i);
-  const long long before = line.start(w0 - 1) - walk.unit_at;
-  if (before > 0 && snap(before, n) > 0) return c;  // (it lies in the unit too)
+__device__ __forceinline__ Cut first_cut(const PackedShape& p, const Shares& line, const Walk<KIND>& walk, int w0) {
+  const Cut none{-1, 0, 0, 0};
+  if (!walk.more || walk.c0 == 0) return none;
+  const Units<KIND> us(p, walk.len);
+  const int n = us.tiles(walk.i);
+  if (us.cut(line.start(w0 - 1) - walk.unit_at, n) > 0) return none;  // (the worker before begins in the unit too)
   int last = w0;
-  while (last + 1 < line.parts) {
-    const long long off = line.start(last + 1) - walk.unit_at;
-    if (off >= n || snap(off, n) == n) break;
-    ++last;
-  }
+  while (last + 1 < line.parts && us.cut(line.start(last + 1) - walk.unit_at, n) < n) ++last;
   return Cut{walk.b, walk.hk, walk.i, last};
 }
 // what a join may read (after a wait that ran out records are whatever the workspace held)
 __device__ __forceinline__ bool was_cut(const PackedShape& p, const Cut& c, int w0) {
   return c.b >= 0 && c.b < p.S && (unsigned)c.hk < (unsigned)p.Hkv && c.i >= 0 && c.last >= w0 && w0 > 0 && c.last < kMaxParts;
 }
+
+// The parts, from the warp that walks to those that work: a ring in shared memory.
+constexpr int kRing = 8;
+struct FeedRing {
+  alignas(16) Part part[kRing];
+  uint64_t full[kRing], empty[kRing];
+  __device__ __forceinline__ void init(int readers) {  // (warps)
+    for (int x = 0; x < kRing; ++x) {
+      mbar_init(&full[x], 1);
+      mbar_init(&empty[x], readers);
+    }
+  }
+};
+
+// The walking warp's part: everything of its CTA's share, and the record of the unit that was cut before it.
+template <int KIND>
+__device__ __forceinline__ void feed(const PackedShape& p, FeedRing& ring, const long long* pre, int group, const Shares& line,
+                                     bool idle, Cut* cuts, volatile int* abort) {
+  const int w0 = blockIdx.x, lane = threadIdx.x & 31;
+  Walk<KIND> walk(p, pre, group, idle ? 0 : line.start(w0), idle ? 0 : line.start(w0 + 1));
+  const Cut cut = first_cut(p, line, walk, w0);
+  if (lane == 0) cuts[w0] = cut;
+  for (uint32_t n = 0;; ++n) {
+    const bool more = walk.more;
+    Part s{};
+    if (more) s = walk.next(p);
+    const uint32_t x = n % kRing;
+    if (n >= kRing && !mbar_wait_warp(&ring.empty[x], (n / kRing - 1) & 1, abort)) return;
+    if (lane == 0) {
+      ring.part[x] = s;
+      mbar_arrive(&ring.full[x]);
+    }
+    __syncwarp();
+    if (!more) return;
+  }
+}
+
+// A working warp's view: next() is false behind the last part, or after a wait that ran out.
+struct Feed {
+  FeedRing& ring;
+  volatile int* abort;
+  uint32_t n = 0;
+  __device__ __forceinline__ Feed(FeedRing& ring_, volatile int* abort_) : ring(ring_), abort(abort_) {}
+  __device__ __forceinline__ bool next(Part& s) {
+    const uint32_t x = n % kRing;
+    if (!mbar_wait_warp(&ring.full[x], (n / kRing) & 1, abort)) return false;
+    const int4* from = reinterpret_cast<const int4*>(&ring.part[x]);
+    const int4 a = from[0], b = from[1];
+    s = Part{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&ring.empty[x]);
+    ++n;
+    return s.c1 > 0;
+  }
+};
 
 // pre[g]: the places before each group of sequences, and their number behind the last (all threads of the CTA, which
 // must synchronise before they read it)
@@ -250,7 +313,8 @@ __device__ __forceinline__ void prefix_of_sequences(const PackedShape& p, int gr
 
 inline PackedShape packed_shape(const int* cu, void* ws, int T, int S, int H, int Hkv, int causal) {
   const int G = H / Hkv;
-  return PackedShape{cu, static_cast<int*>(ws), T, S, Hkv, G, kTile / G, causal};
+  const int w = kTile / G;
+  return PackedShape{cu, static_cast<int*>(ws), T, S, Hkv, G, w, causal, w > 1 ? (unsigned)(((1ull << 32) + w - 1) / w) : 0u};
 }
 
 // Row tiles of queries: w tokens of the G heads of a key/value head, 64 channels

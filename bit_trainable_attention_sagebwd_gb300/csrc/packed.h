@@ -10,7 +10,7 @@ namespace sage {
 
 // Most sequences and tokens of one call, and most query heads of a key/value head (their rows share a tile).
 constexpr int kPackedMaxSeqs = 65536;
-constexpr int kPackedMaxTokens = 1 << 30;
+constexpr int kPackedMaxTokens = 1 << 24;
 constexpr int kPackedMaxGroup = 128;
 
 struct PackedWs {

@@ -28,9 +28,9 @@ namespace sage {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kRegsCompute = 208, kRegsIssue = 88;
-static_assert(2 * kRegsCompute + kRegsIssue <= 3 * 168, "the launch's registers");
+constexpr int kThreads = 512;  // (whole warpgroups, for the register split)
+constexpr int kRegsCompute = 176, kRegsIssue = 80;
+static_assert(2 * kRegsCompute + 2 * kRegsIssue <= 4 * 128, "the launch's registers");
 constexpr uint32_t kCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -105,6 +105,7 @@ struct BwdSmem {
   uint64_t bar_a_full[2], bar_a_empty[2], bar_x_full[2], bar_x_empty[2], bar_y_full[2], bar_y_empty[2], bar_raw[2];
   uint64_t bar_st_full[2], bar_st_empty[2];
   uint64_t bar_s[2], bar_dp, bar_p, bar_ds, bar_acc, bar_acc_read;
+  FeedRing ring;
   long long wsum[kThreads / 32];
   long long pre[kPackedGroups + 1];
   uint32_t tmem_base;
@@ -113,7 +114,7 @@ struct BwdSmem {
 static_assert(sizeof(BwdSmem<128>) + 1024 <= 227 * 1024, "shared memory of a CTA");
 
 template <int D>
-__device__ __forceinline__ void init_barriers(BwdSmem<D>& sm) {
+__device__ __forceinline__ void init_barriers(BwdSmem<D>& sm, int readers) {
   for (int t = 0; t < 2; ++t) {
     mbar_init(&sm.bar_a_full[t], 1);
     mbar_init(&sm.bar_a_empty[t], 1);
@@ -126,6 +127,7 @@ __device__ __forceinline__ void init_barriers(BwdSmem<D>& sm) {
     mbar_init(&sm.bar_st_empty[t], 256);
     mbar_init(&sm.bar_s[t], 1);
   }
+  sm.ring.init(readers);
   mbar_init(&sm.bar_dp, 1);
   mbar_init(&sm.bar_p, 256);
   mbar_init(&sm.bar_ds, 256);
@@ -172,36 +174,26 @@ __device__ __forceinline__ bool bring(uint8_t* tile, int rows, int copied, uint3
   return true;
 }
 
-// One tile of a walk after another.  `first`, `last`: of a part.
-template <int KIND>
+// One tile of the parts after another.  `first`, `last`: of a part.
 struct Tiles {
-  Walk<KIND> walk;
+  Feed feed;
   Part s;
   int j;
   bool valid, first, last;
-  Cut cut;  // (with the line)
-  __device__ __forceinline__ Tiles(const PackedShape& p, const long long* pre, int group, long long begin, long long end,
-                                   const Line* line = nullptr)
-      : walk(p, pre, group, begin, end), j(0), valid(false), first(false), last(true) {
-    s.c1 = 0;
-    if (line) cut = first_cut(p, *line, walk, blockIdx.x);
-    next(p);
-  }
-  __device__ __forceinline__ bool whole() const { return s.c0 == 0 && s.c1 == s.n; }
-  // where a part's sums go
-  __device__ __forceinline__ int place() const { return 2 * blockIdx.x + (s.c0 == 0 ? 1 : 0); }
-  __device__ __forceinline__ void next(const PackedShape& p) {
+  __device__ __forceinline__ Tiles(FeedRing& ring, volatile int* abort) : feed(ring, abort), s{}, j(0), valid(false), first(false), last(true) { next(); }
+  __device__ __forceinline__ void next() {
     first = last;
     if (last) {
-      valid = walk.more;
-      if (!valid) return;
-      s = walk.next(p);
+      valid = feed.next(s);
       j = s.c0;
     } else {
       ++j;
     }
     last = j + 1 == s.c1;
   }
+  __device__ __forceinline__ bool whole() const { return s.c0 == 0 && s.c1 == s.n; }
+  // where a part's sums go
+  __device__ __forceinline__ int place() const { return 2 * blockIdx.x + (s.c0 == 0 ? 1 : 0); }
 };
 
 // columns of an A operand in TMEM, 16 bf16 each: P or dS as the two groups write them
@@ -251,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int box = p.s.G * p.s.w;  // rows of a row tile
-  if (tid == 0) init_barriers(sm);
+  if (tid == 0) init_barriers(sm, 12);
   if (warp < 4 && box < kTile) {  // the rows that no copy brings
     zero_rows<D>(warp < 2 ? sm.x[warp] : sm.y[warp - 2], box, kTile);
     fence_proxy_async_smem();
@@ -269,15 +261,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
-  const long long total = sm.pre[kPackedGroups];
-  const Line line{total, (int)min((long long)gridDim.x, max(total, 1ll))};
-  const int w0 = blockIdx.x;
-  const bool idle = total == 0 || w0 >= line.parts;
-  const long long begin = idle ? 0 : line.start(w0), stop = idle ? 0 : line.start(w0 + 1);
+  const Shares line(sm.pre[kPackedGroups], gridDim.x);
+  const bool idle = line.total == 0 || (int)blockIdx.x >= line.parts;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
   // the row tile at hand: the sequence's tile, and its rows
-  auto tile_of = [&](const Tiles<kKeys>& t) { return Units<kKeys>(p.s, t.s.len).first(t.s.i) + t.j; };
-  auto rows_of = [&](const Tiles<kKeys>& t, int rt) { return min(p.s.w, t.s.len - rt * p.s.w) * p.s.G; };
+  auto tile_of = [&](const Tiles& t) { return Units<kKeys>(p.s, t.s.len).first(t.s.i) + t.j; };
+  auto rows_of = [&](const Tiles& t, int rt) { return min(p.s.w, t.s.len - rt * p.s.w) * p.s.G; };
 
   if (warp >= 8) {
     regs_decrease<kRegsIssue>();
@@ -290,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t q_n = sdesc_sw128(smem_u32(sm.x[0]), kAtom, 1024), do_n = sdesc_sw128(smem_u32(sm.y[0]), kAtom, 1024);
       bool ok = true;
       uint32_t units = 0;  // that S has been begun of
-      auto issue_s = [&](const Tiles<kKeys>& t, uint32_t n) {
+      auto issue_s = [&](const Tiles& t, uint32_t n) {
         if (t.first) ok = ok && wait(&sm.bar_a_full[0], units & 1);
         ok = ok && wait(&sm.bar_x_full[n & 1], (n >> 1) & 1);
         if (!ok) return;
@@ -301,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(&sm.bar_s[0]);
         if (t.last) commit(&sm.bar_a_empty[0]);
       };
-      auto issue_dp = [&](const Tiles<kKeys>& t, uint32_t n) {
+      auto issue_dp = [&](const Tiles& t, uint32_t n) {
         if (t.first) ok = ok && wait(&sm.bar_a_full[1], units++ & 1);
         ok = ok && wait(&sm.bar_y_full[n & 1], (n >> 1) & 1);
         if (!ok) return;
@@ -312,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(&sm.bar_dp);
         if (t.last) commit(&sm.bar_a_empty[1]);
       };
-      Tiles<kKeys> t(p.s, sm.pre, group, begin, stop);
+      Tiles t(sm.ring, abort);
       if (t.valid) {
         issue_s(t, 0);
         issue_dp(t, 0);
@@ -321,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t n = 0; ok && t.valid; ++n) {
         const int rows = rows_of(t, tile_of(t));
         const bool first = t.first, last = t.last;
-        t.next(p.s);
+        t.next();
         ok = wait(&sm.bar_p, n & 1);
         if (first && done) ok = ok && wait(&sm.bar_acc_read, (done - 1) & 1);
         if (!ok) break;
@@ -348,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t *full = v ? sm.bar_y_full : sm.bar_x_full, *empty = v ? sm.bar_y_empty : sm.bar_x_empty;
       uint32_t units = 0, raws = 0, n = 0;
       bool ok = true;
-      for (Tiles<kKeys> t(p.s, sm.pre, group, begin, stop); ok && t.valid; t.next(p.s), ++n) {
+      for (Tiles t(sm.ring, abort); ok && t.valid; t.next(), ++n) {
         if (t.first) {
           ok = units == 0 || wait(&sm.bar_a_empty[v], (units - 1) & 1);
           if (!ok) break;
@@ -377,10 +366,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (units) mbar_wait(&sm.bar_a_full[v], (units - 1) & 1, &give_up);
       for (uint32_t e = 0; e < 2; ++e)
         if (n > e) mbar_wait(&full[(n - 1 - e) & 1], ((n - 1 - e) >> 1) & 1, &give_up);
-    } else {
+    } else if (warp == 12) {
+      feed<kKeys>(p.s, sm.ring, sm.pre, group, line, idle, p.cuts, abort);
+    } else if (warp == 11) {
       // ---------------- row statistics; of rows behind the sequence P is 0
       uint32_t n = 0;
-      for (Tiles<kKeys> t(p.s, sm.pre, group, begin, stop); t.valid; t.next(p.s), ++n) {
+      for (Tiles t(sm.ring, abort); t.valid; t.next(), ++n) {
         const uint32_t st = n & 1;
         const int rt = tile_of(t), rows = rows_of(t, rt);
         const size_t at = ((size_t)t.s.hk * p.s.T + t.s.at + (size_t)rt * p.s.w) * p.s.G;
@@ -408,10 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_col = tmem + lanes + cS + 64 * g, dp_col = tmem + lanes + cDP + 64 * g;
     bool ok = true;
     uint32_t units = 0;
-    Tiles<kKeys> t(p.s, sm.pre, group, begin, stop, &line);
-    if (tid == 0) p.cuts[w0] = t.cut;
+    Tiles t(sm.ring, abort);
     const uint64_t a2 = f2(p.alpha, p.alpha);
-    for (uint32_t n = 0; ok && t.valid; t.next(p.s), ++n) {
+    for (uint32_t n = 0; ok && t.valid; t.next(), ++n) {
       const uint32_t st = n & 1;
       // causal: columns of tokens before the key are masked
       const int key = t.s.i * kTile + r, ahead = p.s.causal ? key - tile_of(t) * p.s.w : 0;
@@ -530,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int box = p.s.G * p.s.w;
-  if (tid == 0) init_barriers(sm);
+  if (tid == 0) init_barriers(sm, 11);
   // (no wait for packed_dkv, of which nothing is read: its CTAs let this kernel in once packed_pre was complete.  The wait
   // at the end keeps the order for what follows.)
   if (warp == 8) {
@@ -545,11 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
-  const long long total = sm.pre[kPackedGroups];
-  const Line line{total, (int)min((long long)gridDim.x, max(total, 1ll))};
-  const int w0 = blockIdx.x;
-  const bool idle = total == 0 || w0 >= line.parts;
-  const long long begin = idle ? 0 : line.start(w0), stop = idle ? 0 : line.start(w0 + 1);
+  const Shares line(sm.pre[kPackedGroups], gridDim.x);
+  const bool idle = line.total == 0 || (int)blockIdx.x >= line.parts;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
 
   if (warp >= 8) {
@@ -563,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t k_n = sdesc_sw128(smem_u32(sm.x[0]), kAtom, 1024);
       bool ok = true;
       uint32_t units_s = 0, units_dp = 0, ns = 0, ndp = 0;
-      auto issue_s = [&](const Tiles<kRows>& t) {
+      auto issue_s = [&](const Tiles& t) {
         const uint32_t n = ns++;
         if (t.first) ok = ok && wait(&sm.bar_a_full[0], units_s++ & 1);
         ok = ok && wait(&sm.bar_x_full[n & 1], (n >> 1) & 1);
@@ -593,13 +580,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool valid = false, first = false, last = false;
         int keys = 0;
       } now, then;
-      Tiles<kRows> t(p.s, sm.pre, group, begin, stop);
+      Tiles t(sm.ring, abort);
       auto take = [&](At& x) {
         x.valid = t.valid;
         if (!t.valid) return;
         x.first = t.first, x.last = t.last, x.keys = min(kTile, t.s.len - t.j * kTile);
         issue_s(t);
-        t.next(p.s);
+        t.next();
       };
       take(now);
       if (now.valid) issue_dp(now.first, now.last);
@@ -629,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t *full = v ? sm.bar_y_full : sm.bar_x_full, *empty = v ? sm.bar_y_empty : sm.bar_x_empty;
       uint32_t units = 0, raws = 0, n = 0;
       bool ok = true;
-      for (Tiles<kRows> t(p.s, sm.pre, group, begin, stop); ok && t.valid; t.next(p.s), ++n) {
+      for (Tiles t(sm.ring, abort); ok && t.valid; t.next(), ++n) {
         if (t.first) {
           ok = units == 0 || wait(&sm.bar_a_empty[v], (units - 1) & 1);
           if (!ok) break;
@@ -657,6 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (units) mbar_wait(&sm.bar_a_full[v], (units - 1) & 1, &give_up);
       for (uint32_t e = 0; e < 2; ++e)
         if (n > e) mbar_wait(&full[(n - 1 - e) & 1], ((n - 1 - e) >> 1) & 1, &give_up);
+    } else if (warp == 12) {
+      feed<kRows>(p.s, sm.ring, sm.pre, group, line, idle, p.cuts, abort);
     }
   } else {
     regs_increase<kRegsCompute>();
@@ -667,11 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int token = r / p.s.G, head = r - token * p.s.G;
     bool ok = true;
     uint32_t units = 0;
-    Tiles<kRows> t(p.s, sm.pre, group, begin, stop, &line);
-    if (tid == 0) p.cuts[w0] = t.cut;
+    Tiles t(sm.ring, abort);
     const uint64_t a2 = f2(p.alpha, p.alpha);
     float nl = 0.f, nd = 0.f;
-    for (uint32_t n = 0; ok && t.valid; t.next(p.s), ++n) {
+    for (uint32_t n = 0; ok && t.valid; t.next(), ++n) {
       const int i = t.s.i * p.s.w + token;
       const bool live = token < p.s.w && i < t.s.len;
       if (t.first) {

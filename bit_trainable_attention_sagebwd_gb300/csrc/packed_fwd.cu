@@ -3,7 +3,7 @@
 //
 // One CTA an SM walks its share of the units (packed.cuh): two row tiles of 128 rows and the 128-key tiles that
 // they see.
-//  - warp 9 brings Q and K by TMA, warp 10 V; two key tiles deep;
+//  - warp 12 walks, warp 9 brings Q and K by TMA, warp 10 V; two key tiles deep;
 //  - warp 8 issues S = Q K^T and O += P V (fp32 accumulators in TMEM) for the two row tiles in turn, so the tensor
 //    core works on one while the softmax works on the other;
 //  - warps 0-3 and 4-7 own a row tile each, a thread a row: S from TMEM, P as bf16 back into TMEM over S's
@@ -23,9 +23,7 @@ namespace sage {
 
 namespace {
 
-constexpr int kThreads = 384;
-constexpr int kRegsSoftmax = 208, kRegsIssue = 88;
-static_assert(2 * kRegsSoftmax + kRegsIssue <= 3 * 168, "the launch's registers");
+constexpr int kThreads = 416;
 constexpr uint32_t kCols = 512, kColO = 256;  // TMEM: S of place t at 128 t, O at 256 + 128 t
 constexpr float kRaise = 8.f;
 
@@ -46,7 +44,8 @@ struct FwdSmem {
   uint8_t k[2][kTile * D * 2];
   uint8_t v[2][kTile * D * 2];
   uint64_t bar_q_full[2], bar_q_empty[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_v_raw;
-  uint64_t bar_s[2], bar_p[2], bar_o[2], bar_o_read[2];
+  uint64_t bar_s[2], bar_p[2], bar_o[2], bar_o_read[2], bar_turn[2];
+  FeedRing ring;
   long long wsum[kThreads / 32];
   long long pre[kPackedGroups + 1];
   uint32_t tmem_base;
@@ -59,10 +58,11 @@ static_assert(sizeof(FwdSmem<128>) + 1024 <= 227 * 1024, "shared memory of a CTA
 struct Places {
   int t0, rows;    // rows: row tiles
   int end0, end1;  // by row tile: where its key tiles end
+  __device__ __forceinline__ Places() : t0(0), rows(0), end0(0), end1(0) {}
   __device__ __forceinline__ Places(const PackedShape& p, const Part& s, int& solo) {
     rows = (2 * s.i + 1) * p.w < s.len ? 2 : 1;
     t0 = rows == 1 ? (solo++ & 1) : 0;
-    end0 = p.causal ? min(s.c1, ceil_div(min(s.len, (2 * s.i + 1) * p.w), kTile)) : s.c1;
+    end0 = p.causal ? min(s.c1, (min(s.len, (2 * s.i + 1) * p.w) + kTile - 1) / kTile) : s.c1;
     end1 = s.c1;
   }
 };
@@ -81,15 +81,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.bar_q_full[t], 1);
       mbar_init(&sm.bar_q_empty[t], 1);
       mbar_init(&sm.bar_k_full[t], 1);
-      mbar_init(&sm.bar_k_empty[t], 1);
+      mbar_init(&sm.bar_k_empty[t], 2);
       mbar_init(&sm.bar_v_full[t], 1);
-      mbar_init(&sm.bar_v_empty[t], 1);
+      mbar_init(&sm.bar_v_empty[t], 2);
       mbar_init(&sm.bar_s[t], 1);
+      mbar_init(&sm.bar_turn[t], 1);
       mbar_init(&sm.bar_p[t], 128);
       mbar_init(&sm.bar_o[t], 1);
       mbar_init(&sm.bar_o_read[t], 128);
     }
     mbar_init(&sm.bar_v_raw, 1);
+    sm.ring.init(12);
     sm.abort = 0;
     fence_mbar_init();
   }
@@ -108,99 +110,103 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_trigger();
   constexpr uint32_t tmem = 0;  // (where an allocation of all columns begins)
   volatile int* abort = &sm.abort;
-  const long long total = sm.pre[kPackedGroups];
-  const Line line{total, (int)min((long long)gridDim.x, max(total, 1ll))};
+  const Shares line(sm.pre[kPackedGroups], gridDim.x);
   const int w0 = blockIdx.x;
   if (sm.tmem_base != tmem && tid == 0) atomicMax(p.s.status, (int)kDevSetup);
-  const bool idle = total == 0 || w0 >= line.parts || sm.tmem_base != tmem;
-  const long long begin = idle ? 0 : line.start(w0), stop = idle ? 0 : line.start(w0 + 1);
+  const bool idle = line.total == 0 || w0 >= line.parts || sm.tmem_base != tmem;
+  Feed parts(sm.ring, abort);
+  Part s;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
   int solo = 0;
 
   if (warp >= 8) {
-    regs_decrease<kRegsIssue>();
-    if (warp == 8) {
-      // ---------------- MMA issuer.  An S goes in, then the P V of the S before it, whose softmax has had time.
-      constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_o = idesc_bf16(kTile, D, false, true);
-      constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
-      const uint64_t dq = sdesc_sw128(smem_u32(sm.q[0]), 16, 1024), dk = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024);
-      const uint64_t dv = sdesc_sw128(smem_u32(sm.v[0]), kAtom, 1024);
-      uint32_t kc = 0, v_seen = 0;                       // key tiles so far, V tiles that were waited for
-      uint32_t q_ph = 0, p_ph = 0, o_ph = 3, o_any = 0;  // by place: phases of Q, P and O, and whether there was an O
-      int due = -1;                                      // the place whose P V follows
-      uint32_t due_kc = 0;
-      int due_keys = 0;
-      bool due_first = false, due_last = false, due_frees = false;
-      bool ok = true;
-      auto flush = [&]() {
-        if (due < 0) return;
-        const int t = due;
-        due = -1;
-        const uint32_t st = due_kc & 1;
-        if (due_kc == v_seen) {
-          ok = ok && wait(&sm.bar_v_full[st], (due_kc >> 1) & 1);
-          ++v_seen;
-        }
-        ok = ok && wait(&sm.bar_p[t], (p_ph >> t) & 1);
-        p_ph ^= 1 << t;
-        if (due_first) {
-          if ((o_any >> t) & 1) ok = ok && wait(&sm.bar_o_read[t], (o_ph >> t) & 1);
-          o_any |= 1 << t, o_ph ^= 1 << t;
-        }
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t b = dv + st * kNext;
-        const uint32_t d = kColO + t * 128, a = t * 128;
-        if (due_keys >= kTile) {
-          issue_ts_x4(d, a, b, id_o, !due_first);
-          issue_ts_x4(d, a + 32, b + (4 * 2048 >> 4), id_o, 1);
-        } else {
+    if (warp == 8 || warp == 11) {
+      // ---------------- MMA issuers, warp 8 for the first place, warp 11 for the second.  P V of a key tile and S of the
+      // next one go in together; what comes early (K, V, Q, the turn) is waited for before P.  Place and stage are
+      // constants of the code that issues, so its descriptors need no arithmetic.
+      auto issuer = [&](auto place) {
+        constexpr int t = decltype(place)::value;
+        constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_o = idesc_bf16(kTile, D, false, true);
+        constexpr uint32_t s_col = t * 128, o_col = kColO + t * 128;
+        uint32_t kc = 0, np = 0, nu = 0, turns = 0;  // key tiles that came by, P tiles and units here, turns taken
+        bool ok = true;
+        auto issue_s = [&](auto stage, bool last) {
+          constexpr int st = decltype(stage)::value;
+          const uint64_t a = sdesc_sw128(smem_u32(sm.q[t]), 16, 1024), b = sdesc_sw128(smem_u32(sm.k[st]), 16, 1024);
+#pragma unroll
+          for (int h = 0; h < kAtoms; ++h) issue_ss_x4(s_col, a + h * (kAtom >> 4), b + h * (kAtom >> 4), id_s, h > 0);
+          commit(&sm.bar_s[t]);
+          commit(&sm.bar_k_empty[st]);
+          if (last) commit(&sm.bar_q_empty[t]);
+        };
+        auto products = [&](auto stage, int keys, bool first, bool again, bool last) {
+          constexpr int st = decltype(stage)::value;
+          const uint64_t b = sdesc_sw128(smem_u32(sm.v[st]), kAtom, 1024);
+          if (keys >= kTile) {
+            issue_ts_x4(o_col, s_col, b, id_o, !first);
+            issue_ts_x4(o_col, s_col + 32, b + (4 * 2048 >> 4), id_o, 1);
+          } else {
 #pragma unroll 1
-          for (int e = 0; e * 16 < due_keys; ++e) issue_ts(d, a + 8 * e, b + (e * 2048 >> 4), id_o, e > 0 || !due_first);
-        }
-        if (due_frees) commit(&sm.bar_v_empty[st]);
-        if (due_last) commit(&sm.bar_o[t]);
-      };
-      Walk<kPairs> walk(p.s, sm.pre, group, begin, stop);
+            for (int e = 0; e * 16 < keys; ++e) issue_ts(o_col, s_col + 8 * e, b + (e * 2048 >> 4), id_o, e > 0 || !first);
+          }
+          commit(&sm.bar_v_empty[st]);
+          if (again)
+            issue_s(std::integral_constant<int, st ^ 1>(), last);
+          else
+            commit(&sm.bar_o[t]);
+        };
 #pragma unroll 1
-      while (ok && walk.more) {
-        const Part s = walk.next(p.s);
-        const Places pl(p.s, s, solo);
-#pragma unroll 1
-        for (int j = s.c0; ok && j < s.c1; ++j, ++kc) {
-          const uint32_t st = kc & 1;
-          ok = wait(&sm.bar_k_full[st], (kc >> 1) & 1);
-#pragma unroll 1
-          for (int x = j < pl.end0 ? 0 : 1; ok && x < pl.rows; ++x) {
-            const int t = x ^ pl.t0;
-            const bool last = j + 1 == (x ? pl.end1 : pl.end0), frees = x + 1 == pl.rows;
-            if (due == t) flush();
-            if (j == s.c0) {
-              ok = ok && wait(&sm.bar_q_full[t], (q_ph >> t) & 1);
-              q_ph ^= 1 << t;
-            }
+        while (ok && parts.next(s)) {
+          const Places pl(p.s, s, solo);
+          const int x = t ^ pl.t0, end = x < pl.rows ? (x ? pl.end1 : pl.end0) : s.c0;
+          if (s.c0 < end) {
+            ok = wait(&sm.bar_q_full[t], nu & 1) && wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t a = dq + t * kNext, b = dk + st * kNext;
-#pragma unroll
-            for (int h = 0; h < kAtoms; ++h) issue_ss_x4(t * 128, a + h * kAtomStep, b + h * kAtomStep, id_s, h > 0);
-            commit(&sm.bar_s[t]);
-            if (frees) commit(&sm.bar_k_empty[st]);
-            if (last) commit(&sm.bar_q_empty[t]);
-            flush();
-            due = t, due_kc = kc, due_keys = s.len - j * kTile, due_first = j == s.c0, due_last = last, due_frees = frees;
+            if (kc & 1) issue_s(std::integral_constant<int, 1>(), s.c0 + 1 == end);
+            else issue_s(std::integral_constant<int, 0>(), s.c0 + 1 == end);
+          }
+#pragma unroll 1
+          for (int j = s.c0; ok && j < end; ++j, ++kc) {
+            ok = wait(&sm.bar_v_full[kc & 1], (kc >> 1) & 1);
+            if (j + 1 < end) ok = ok && wait(&sm.bar_k_full[(kc + 1) & 1], ((kc + 1) >> 1) & 1);
+            if (j == s.c0) ok = ok && (nu == 0 || wait(&sm.bar_o_read[t], (nu - 1) & 1));
+            // Where both places have the key tile their products go in in turns: mixed they would end together, and the
+            // tensor core wait for both softmaxes.
+            const bool paired = pl.rows == 2 && j < pl.end0;
+            if (paired) {
+              if (turns + t > 0) ok = ok && wait(&sm.bar_turn[t], (turns + t - 1) & 1);
+              ++turns;
+            }
+            ok = ok && wait(&sm.bar_p[t], np++ & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (kc & 1) products(std::integral_constant<int, 1>(), s.len - j * kTile, j == s.c0, j + 1 < end, j + 2 == end);
+            else products(std::integral_constant<int, 0>(), s.len - j * kTile, j == s.c0, j + 1 < end, j + 2 == end);
+            if (paired && lane == 0) mbar_arrive(&sm.bar_turn[t ^ 1]);
+            __syncwarp();
+          }
+          if (s.c0 < end) ++nu;
+          // tiles that only the other place takes
+#pragma unroll 1
+          for (int j = max(end, s.c0); ok && j < s.c1; ++j, ++kc) {
+            ok = wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1);
+            if (ok && lane == 0) mbar_arrive(&sm.bar_k_empty[kc & 1]);
+            ok = ok && wait(&sm.bar_v_full[kc & 1], (kc >> 1) & 1);
+            if (ok && lane == 0) mbar_arrive(&sm.bar_v_empty[kc & 1]);
           }
         }
-      }
-      if (ok) flush();
+      };
+      if (warp == 8)
+        issuer(std::integral_constant<int, 0>());
+      else
+        issuer(std::integral_constant<int, 1>());
     } else if (warp == 9) {
       // ---------------- Q and K
       uint32_t kc = 0, nq[2] = {0, 0};
       bool ok = true;
       const uint32_t q_bytes = p.s.G * p.s.w * D * 2;
-      Walk<kPairs> walk(p.s, sm.pre, group, begin, stop);
-      while (ok && walk.more) {
-        const Part s = walk.next(p.s);
+      while (ok && parts.next(s)) {
         const Places pl(p.s, s, solo);
         auto load_q = [&](int x) {
           const int t = x ^ pl.t0;
@@ -233,13 +239,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (nq[t]) mbar_wait(&sm.bar_q_full[t], (nq[t] - 1) & 1, &give_up);
         if (kc > (uint32_t)t) mbar_wait(&sm.bar_k_full[(kc - 1 - t) & 1], ((kc - 1 - t) >> 1) & 1, &give_up);
       }
+    } else if (warp == 12) {
+      feed<kPairs>(p.s, sm.ring, sm.pre, group, line, idle, p.cuts, abort);
     } else if (warp == 10) {
       // ---------------- V
       uint32_t kc = 0, nr = 0;
       bool ok = true;
-      Walk<kPairs> walk(p.s, sm.pre, group, begin, stop);
-      while (ok && walk.more) {
-        const Part s = walk.next(p.s);
+      while (ok && parts.next(s)) {
         for (int j = s.c0; ok && j < s.c1; ++j, ++kc) {
           const uint32_t st = kc & 1;
           ok = kc < 2 || wait(&sm.bar_v_empty[st], ((kc >> 1) - 1) & 1);
@@ -277,7 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kc > t) mbar_wait(&sm.bar_v_full[(kc - 1 - t) & 1], ((kc - 1 - t) >> 1) & 1, &give_up);
     }
   } else {
-    regs_increase<kRegsSoftmax>();
     // ---------------- softmax: thread r of the group owns row r of the row tile at place t
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -285,10 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int token = r / p.s.G, head = r - token * p.s.G;  // of the tile
     uint32_t ns = 0, no = 0;
     bool ok = true;
-    Walk<kPairs> walk(p.s, sm.pre, group, begin, stop);
-    if (tid == 0) p.cuts[w0] = first_cut(p.s, line, walk, w0);
-    while (ok && walk.more) {
-      const Part s = walk.next(p.s);
+    while (ok && parts.next(s)) {
       const Places pl(p.s, s, solo);
       const int x = t ^ pl.t0;
       if (x >= pl.rows) continue;
@@ -345,16 +347,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sub = m == -INFINITY ? 0.f : m;
         const uint64_t a2 = f2(p.alpha, p.alpha), m2 = f2(-sub, -sub);
         uint64_t sums[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll 1
-        for (int c = 0; c < kTile; c += 32) {
-          uint32_t v[32], w[16];
-          tmem_ld32(s_col + c, v);
-          tmem_wait32(v);
+        // P of 32 keys from S of theirs
+        auto some = [&](int c, uint32_t (&v)[32]) {
           if (edge) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (c + e >= left) v[e] = 0xff800000u;
           }
+          uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float u0, u1;
@@ -365,13 +365,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[e >> 1] = *reinterpret_cast<const uint32_t*>(&h);
           }
           tmem_st16(s_col + (c >> 1), w);
+        };
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(s_col + c, v);
+          tmem_wait32(v);
+          some(c, v);
         }
-        float y0, y1;
-        f2split(fadd2(sums[0], sums[1]), y0, y1);
-        l += y0 + y1;
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&sm.bar_p[t]);
+        float y0, y1;
+        f2split(fadd2(sums[0], sums[1]), y0, y1);
+        l += y0 + y1;
       }
       // ---- the part's result
       ok = ok && wait(&sm.bar_o[t], no++ & 1);
