@@ -133,12 +133,11 @@ def lib():
             L.sage_attn_kv_compact_ws_bytes.restype = sz
             L.sage_attn_kv_compact_ws_bytes.argtypes = [i]
             L.sage_attn_kv_compact.argtypes = [cp, cp, vp, sz, vp]
-            rp = ctypes.POINTER(sage_rows)
+            rp = hp = vp  # (sage_rows and sage_heads, of which the helpers lay several side by side)
             L.sage_attn_packed_ws_bytes.restype = sz
             L.sage_attn_packed_ws_bytes.argtypes = [i] * 6
             L.sage_attn_packed_fwd.argtypes = [rp] * 3 + [vp, rp, vp, vp, sz] + [i] * 6 + [fp, vp]
             L.sage_attn_packed_bwd.argtypes = [rp] * 4 + [vp, rp, vp] + [rp] * 3 + [vp, sz] + [i] * 6 + [fp, vp]
-            hp = ctypes.POINTER(sage_heads)
             L.sage_attn_rotary.argtypes = [ctypes.POINTER(sage_rotary)] + [hp] * 4 + [vp] * 3 + [i] * 7 + [vp]
             L.sage_attn_ws_views.argtypes = [vp, i, i, i, i, ctypes.POINTER(sage_ws_views)]
             L.sage_attn_get_status.argtypes = [vp, vp]

@@ -130,8 +130,15 @@ struct Shares {
 };
 
 // A part of a unit: tiles [c0, c1) of its n, of key/value head hk of the sequence at token `at`.  c1 = 0: no more parts.
+// A unit that was cut has parts with the workers `first`, .. `first` + parts - 1, who leave their sums at places: that
+// of the unit's beginning at 2 first + 1, the others at 2 w.  (A worker has two such parts at most: its first and its last.)
 struct Part {
-  int b, at, len, hk, i, n, c0, c1;
+  int at, len, hk, i, n, c0, c1, cut;  // cut: first << 16 | parts
+  __device__ __forceinline__ bool whole() const { return c0 == 0 && c1 == n; }
+  __device__ __forceinline__ int first() const { return cut >> 16; }
+  __device__ __forceinline__ int parts() const { return cut & 0xffff; }
+  __device__ __forceinline__ int place(int k) const { return 2 * (first() + k) + (k == 0 ? 1 : 0); }  // of part k
+  __device__ __forceinline__ int place() const { return 2 * blockIdx.x + (c0 == 0 ? 1 : 0); }         // of this one
 };
 
 // A worker's way along the line: the parts from place `begin` to `end`, in order.  All lanes of a warp walk together.
@@ -206,10 +213,18 @@ struct Walk {
     const Units<KIND> us(p, len);
     if (us.cut(stop - unit_at, us.tiles(i)) <= c0) more = false;
   }
-  __device__ __forceinline__ Part next(const PackedShape& p) {
+  __device__ __forceinline__ Part next(const PackedShape& p, const Shares& line) {
     const Units<KIND> us(p, len);
     const int n = us.tiles(i);
-    const Part s{b, at, len, hk, i, n, c0, us.cut(stop - unit_at, n)};
+    Part s{at, len, hk, i, n, c0, us.cut(stop - unit_at, n), 0};
+    if (!s.whole()) {
+      int v = blockIdx.x;
+      if (c0 > 0)
+        while (v > 0 && us.cut(line.start(v) - unit_at, n) > 0) --v;
+      int last = v;
+      while (last + 1 < line.parts && us.cut(line.start(last + 1) - unit_at, n) < n) ++last;
+      s.cut = v << 16 | (last - v + 1);
+    }
     if (s.c1 < n) {
       more = false;
     } else {
@@ -220,29 +235,7 @@ struct Walk {
   }
 };
 
-// A unit that was cut, written by the worker behind its first cut: its parts are those of the workers before, where it
-// begins, to `last`.  Worker x leaves its part of a unit at place 2 x + 1 if the unit begins with it, else 2 x.
-struct Cut {
-  int b, hk, i, last;  // b < 0: no such unit
-};
 constexpr int kMaxParts = 160;  // CTAs of a grid (one an SM)
-
-// The record of worker w0, whose walk stands at its beginning
-template <int KIND>
-__device__ __forceinline__ Cut first_cut(const PackedShape& p, const Shares& line, const Walk<KIND>& walk, int w0) {
-  const Cut none{-1, 0, 0, 0};
-  if (!walk.more || walk.c0 == 0) return none;
-  const Units<KIND> us(p, walk.len);
-  const int n = us.tiles(walk.i);
-  if (us.cut(line.start(w0 - 1) - walk.unit_at, n) > 0) return none;  // (the worker before begins in the unit too)
-  int last = w0;
-  while (last + 1 < line.parts && us.cut(line.start(last + 1) - walk.unit_at, n) < n) ++last;
-  return Cut{walk.b, walk.hk, walk.i, last};
-}
-// what a join may read (after a wait that ran out records are whatever the workspace held)
-__device__ __forceinline__ bool was_cut(const PackedShape& p, const Cut& c, int w0) {
-  return c.b >= 0 && c.b < p.S && (unsigned)c.hk < (unsigned)p.Hkv && c.i >= 0 && c.last >= w0 && w0 > 0 && c.last < kMaxParts;
-}
 
 // The parts, from the warp that walks to those that work: a ring in shared memory.
 constexpr int kRing = 8;
@@ -257,18 +250,16 @@ struct FeedRing {
   }
 };
 
-// The walking warp's part: everything of its CTA's share, and the record of the unit that was cut before it.
+// The walking warp's part: everything of its CTA's share.
 template <int KIND>
 __device__ __forceinline__ void feed(const PackedShape& p, FeedRing& ring, const long long* pre, int group, const Shares& line,
-                                     bool idle, Cut* cuts, volatile int* abort) {
+                                     bool idle, volatile int* abort) {
   const int w0 = blockIdx.x, lane = threadIdx.x & 31;
   Walk<KIND> walk(p, pre, group, idle ? 0 : line.start(w0), idle ? 0 : line.start(w0 + 1));
-  const Cut cut = first_cut(p, line, walk, w0);
-  if (lane == 0) cuts[w0] = cut;
   for (uint32_t n = 0;; ++n) {
     const bool more = walk.more;
     Part s{};
-    if (more) s = walk.next(p);
+    if (more) s = walk.next(p, line);
     const uint32_t x = n % kRing;
     if (n >= kRing && !mbar_wait_warp(&ring.empty[x], (n / kRing - 1) & 1, abort)) return;
     if (lane == 0) {
@@ -298,6 +289,66 @@ struct Feed {
     return s.c1 > 0;
   }
 };
+
+// The joining of a unit that was cut, by those who finish its last part (in time, whichever it is): a group of 128
+// threads has written its part's sums; true in all of them if it was the last to do so.  Sums are then added in the order
+// of the parts, so the bits do not depend on who came last.  The counter is zero before and after.
+struct Meeting {
+  uint64_t written, told;
+  int last;
+  __device__ __forceinline__ void init() {
+    mbar_init(&written, 128);
+    mbar_init(&told, 1);
+  }
+  // n: how often the group has met here before
+  __device__ __forceinline__ bool was_last(int* counter, int parts, uint32_t n, volatile int* abort, bool& ok) {
+    __threadfence();
+    mbar_arrive(&written);
+    if ((threadIdx.x & 127) < 32) {
+      ok = ok && mbar_wait_warp(&written, n & 1, abort);
+      if (ok && (threadIdx.x & 31) == 0) {
+        last = atomicAdd(counter, 1) == parts - 1;
+        if (last) atomicExch(counter, 0);
+        mbar_arrive(&told);
+      }
+      __syncwarp();
+    }
+    ok = ok && mbar_wait_warp(&told, n & 1, abort);
+    __threadfence();
+    return ok && *const_cast<volatile int*>(&last);
+  }
+};
+// counters of the workspace, behind the status word
+constexpr int kCounters = 2 * kMaxParts;  // of each kernel: two of each worker
+enum { kFwdCounters = 64, kKeyCounters = kFwdCounters + kCounters, kRowCounters = kKeyCounters + kCounters,
+       kHeader = kRowCounters + kCounters };  // in words
+static_assert(kHeader == 1024, "the workspace's first 4096 bytes");
+
+// Sums of a part: float4 of four channels, [D / 4][128 rows], so that a warp's threads, a row each, meet in memory
+__device__ __forceinline__ void store_sums(float* part, int d, int r, const uint32_t (&o)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4)
+    *reinterpret_cast<uint4*>(part + (size_t)((d + e) * kTile + r * 4)) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+}
+// o += f * those
+__device__ __forceinline__ void add_sums(const float* part, int d, int r, float f, float (&o)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4) {
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(part + (size_t)((d + e) * kTile + r * 4)));
+    o[e] = fmaf(x.x, f, o[e]), o[e + 1] = fmaf(x.y, f, o[e + 1]), o[e + 2] = fmaf(x.z, f, o[e + 2]), o[e + 3] = fmaf(x.w, f, o[e + 3]);
+  }
+}
+__device__ __forceinline__ uint32_t bf2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// 32 channels of a row times f, as bf16
+__device__ __forceinline__ void store_row(__nv_bfloat16* to, const float (&o)[32], float f) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8)
+    *reinterpret_cast<uint4*>(to + e) = make_uint4(bf2(o[e] * f, o[e + 1] * f), bf2(o[e + 2] * f, o[e + 3] * f),
+                                                   bf2(o[e + 4] * f, o[e + 5] * f), bf2(o[e + 6] * f, o[e + 7] * f));
+}
 
 // pre[g]: the places before each group of sequences, and their number behind the last (all threads of the CTA, which
 // must synchronise before they read it)

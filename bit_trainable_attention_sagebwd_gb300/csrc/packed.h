@@ -14,7 +14,7 @@ constexpr int kPackedMaxTokens = 1 << 24;
 constexpr int kPackedMaxGroup = 128;
 
 struct PackedWs {
-  size_t cuts, part, stats, total;  // (the status word comes first)
+  size_t part, stats, total;  // (the status word and the counters come first)
 };
 PackedWs packed_ws_layout(int T, int S, int H, int Hkv, int D, bool backward);
 

@@ -38,8 +38,7 @@ struct BwdParams {
   PackedShape s;
   const float *nlse, *ndelta;  // [Hkv][T][G]: -LSE log2 e, -delta
   sage_rows d0, d1;            // packed_dkv: dK, dV; packed_dq: dQ
-  Cut* cuts;
-  float* part;                 // two of each worker: [128][D] sums of d0, and of d1
+  float* part;                 // of each worker two places: [D / 4][128] sums of four channels of d0, and of d1
   float alpha, sm_scale;       // alpha: sm_scale log2 e
 };
 
@@ -106,6 +105,7 @@ struct BwdSmem {
   uint64_t bar_st_full[2], bar_st_empty[2];
   uint64_t bar_s[2], bar_dp, bar_p, bar_ds, bar_acc, bar_acc_read;
   FeedRing ring;
+  Meeting meeting[2];
   long long wsum[kThreads / 32];
   long long pre[kPackedGroups + 1];
   uint32_t tmem_base;
@@ -116,6 +116,7 @@ static_assert(sizeof(BwdSmem<128>) + 1024 <= 227 * 1024, "shared memory of a CTA
 template <int D>
 __device__ __forceinline__ void init_barriers(BwdSmem<D>& sm, int readers) {
   for (int t = 0; t < 2; ++t) {
+    sm.meeting[t].init();
     mbar_init(&sm.bar_a_full[t], 1);
     mbar_init(&sm.bar_a_empty[t], 1);
     mbar_init(&sm.bar_x_full[t], 1);
@@ -191,9 +192,6 @@ struct Tiles {
     }
     last = j + 1 == s.c1;
   }
-  __device__ __forceinline__ bool whole() const { return s.c0 == 0 && s.c1 == s.n; }
-  // where a part's sums go
-  __device__ __forceinline__ int place() const { return 2 * blockIdx.x + (s.c0 == 0 ? 1 : 0); }
 };
 
 // columns of an A operand in TMEM, 16 bf16 each: P or dS as the two groups write them
@@ -207,28 +205,6 @@ __device__ __forceinline__ void issue_rows(uint32_t d, uint32_t a, uint64_t b, u
   } else {
     for (int k = 0; k * 16 < rows; ++k) issue_ts(d, a + a_col(k), b + (k * 2048 >> 4), idesc, acc || k > 0);
   }
-}
-
-// 64 values of P or dS of a row, as bf16, to 32 columns
-__device__ __forceinline__ uint32_t bf2(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// 32 columns of an accumulator times f to a row's bf16
-__device__ __forceinline__ void store_row(__nv_bfloat16* to, const uint32_t (&o)[32], float f) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    *reinterpret_cast<uint4*>(to + 8 * e) =
-        make_uint4(bf2(__uint_as_float(o[8 * e]) * f, __uint_as_float(o[8 * e + 1]) * f),
-                   bf2(__uint_as_float(o[8 * e + 2]) * f, __uint_as_float(o[8 * e + 3]) * f),
-                   bf2(__uint_as_float(o[8 * e + 4]) * f, __uint_as_float(o[8 * e + 5]) * f),
-                   bf2(__uint_as_float(o[8 * e + 6]) * f, __uint_as_float(o[8 * e + 7]) * f));
-}
-
-__device__ __forceinline__ void store_part(float* to, const uint32_t (&o)[32]) {
-#pragma unroll
-  for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(to + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
 }
 
 // ------------------------------------------------------------------ dK and dV
@@ -367,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t e = 0; e < 2; ++e)
         if (n > e) mbar_wait(&full[(n - 1 - e) & 1], ((n - 1 - e) >> 1) & 1, &give_up);
     } else if (warp == 12) {
-      feed<kKeys>(p.s, sm.ring, sm.pre, group, line, idle, p.cuts, abort);
+      feed<kKeys>(p.s, sm.ring, sm.pre, group, line, idle, abort);
     } else if (warp == 11) {
       // ---------------- row statistics; of rows behind the sequence P is 0
       uint32_t n = 0;
@@ -398,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + cS + 64 * g, dp_col = tmem + lanes + cDP + 64 * g;
     bool ok = true;
-    uint32_t units = 0;
+    uint32_t units = 0, joins = 0;
     Tiles t(sm.ring, abort);
     const uint64_t a2 = f2(p.alpha, p.alpha);
     for (uint32_t n = 0; ok && t.valid; t.next(), ++n) {
@@ -480,26 +456,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait(&sm.bar_acc, units++ & 1);
       if (!ok) break;
       tc_fence_after();
-      const bool live = key < t.s.len;
+      const bool live = key < t.s.len, whole = t.s.whole();
+      auto row_of = [&](int x) {
+        const sage_rows& to = x ? p.d1 : p.d0;
+        return static_cast<__nv_bfloat16*>(to.p) + (long long)(t.s.at + key) * to.token + t.s.hk * to.head;
+      };
+      auto part_of = [&](int place, int x) { return p.part + (size_t)(2 * place + x) * kTile * D; };
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
-        const sage_rows& to = x ? p.d1 : p.d0;
-        __nv_bfloat16* row = static_cast<__nv_bfloat16*>(to.p) + (long long)(t.s.at + key) * to.token + t.s.hk * to.head + g * (D / 2);
-        const float f = x ? 1.f : p.sm_scale;
 #pragma unroll 1
-        for (int d = 0; d < D / 2; d += 32) {
+        for (int d = g * (D / 2); d < (g + 1) * (D / 2); d += 32) {
           uint32_t o[32];
-          tmem_ld32(tmem + lanes + (x ? cDV : cDK) + g * (D / 2) + d, o);
+          tmem_ld32(tmem + lanes + (x ? cDV : cDK) + d, o);
           tmem_wait32(o);
-          if (!live) continue;
-          if (t.whole())
-            store_row(row + d, o, f);
-          else
-            store_part(p.part + ((size_t)t.place() * 2 + x) * kTile * D + (size_t)r * D + g * (D / 2) + d, o);
+          if (whole && live) store_row(row_of(x) + d, reinterpret_cast<const float(&)[32]>(o), x ? 1.f : p.sm_scale);
+          if (!whole) store_sums(part_of(t.s.place(), x), d, r, o);
         }
       }
       tc_fence_before();
       mbar_arrive(&sm.bar_acc_read);
+      if (whole || !sm.meeting[g].was_last(p.s.status + kKeyCounters + 2 * t.s.first() + g, t.s.parts(), joins++, abort, ok)) continue;
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+#pragma unroll 1
+        for (int d = g * (D / 2); d < (g + 1) * (D / 2); d += 32) {
+          float o[32] = {};
+#pragma unroll 1
+          for (int k = 0; k < t.s.parts(); ++k) add_sums(part_of(t.s.place(k), x), d, r, 1.f, o);
+          if (live) store_row(row_of(x) + d, o, x ? 1.f : p.sm_scale);
+        }
+      }
     }
   }
   tc_fence_before();
@@ -645,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t e = 0; e < 2; ++e)
         if (n > e) mbar_wait(&full[(n - 1 - e) & 1], ((n - 1 - e) >> 1) & 1, &give_up);
     } else if (warp == 12) {
-      feed<kRows>(p.s, sm.ring, sm.pre, group, line, idle, p.cuts, abort);
+      feed<kRows>(p.s, sm.ring, sm.pre, group, line, idle, abort);
     }
   } else {
     regs_increase<kRegsCompute>();
@@ -655,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t dp_col = tmem + lanes + cDP + 64 * g;
     const int token = r / p.s.G, head = r - token * p.s.G;
     bool ok = true;
-    uint32_t units = 0;
+    uint32_t units = 0, joins = 0;
     Tiles t(sm.ring, abort);
     const uint64_t a2 = f2(p.alpha, p.alpha);
     float nl = 0.f, nd = 0.f;
@@ -725,20 +711,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       __nv_bfloat16* row = static_cast<__nv_bfloat16*>(p.d0.p) + (long long)(t.s.at + i) * p.d0.token +
-                           (t.s.hk * p.s.G + head) * p.d0.head + g * (D / 2);
+                           (t.s.hk * p.s.G + head) * p.d0.head;
+      const bool whole = t.s.whole();
 #pragma unroll 1
-      for (int d = 0; d < D / 2; d += 32) {
+      for (int d = g * (D / 2); d < (g + 1) * (D / 2); d += 32) {
         uint32_t o[32];
-        tmem_ld32(tmem + lanes + cDQ + g * (D / 2) + d, o);
+        tmem_ld32(tmem + lanes + cDQ + d, o);
         tmem_wait32(o);
-        if (!live) continue;
-        if (t.whole())
-          store_row(row + d, o, p.sm_scale);
-        else
-          store_part(p.part + (size_t)t.place() * kTile * D + (size_t)r * D + g * (D / 2) + d, o);
+        if (whole && live) store_row(row + d, reinterpret_cast<const float(&)[32]>(o), p.sm_scale);
+        if (!whole) store_sums(p.part + (size_t)t.s.place() * kTile * D, d, r, o);
       }
       tc_fence_before();
       mbar_arrive(&sm.bar_acc_read);
+      if (whole || !sm.meeting[g].was_last(p.s.status + kRowCounters + 2 * t.s.first() + g, t.s.parts(), joins++, abort, ok)) continue;
+#pragma unroll 1
+      for (int d = g * (D / 2); d < (g + 1) * (D / 2); d += 32) {
+        float o[32] = {};
+#pragma unroll 1
+        for (int k = 0; k < t.s.parts(); ++k) add_sums(p.part + (size_t)t.s.place(k) * kTile * D, d, r, 1.f, o);
+        if (live) store_row(row + d, o, p.sm_scale);
+      }
     }
   }
   tc_fence_before();
@@ -746,40 +738,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) tmem_dealloc(tmem, kCols);
   if (tid == 0 && sm.abort) atomicMax(p.s.status, (int)kDevTimeout);
   pdl_wait();
-}
-
-// ------------------------------------------------------------------ units that were cut
-// blockIdx.z: dK, dV, dQ; a thread adds up four channels of a row's parts
-constexpr int kJoinSlices = 4;
-template <int D>
-__global__ void __launch_bounds__(256) packed_bwd_join_kernel(const BwdParams dkv, const BwdParams dq) {
-  const int w0 = blockIdx.x, what = blockIdx.z;
-  pdl_wait();
-  pdl_trigger();
-  const BwdParams& p = what < 2 ? dkv : dq;
-  const Cut c = p.cuts[w0];
-  if (!was_cut(p.s, c, w0)) return;
-  int at, len;
-  sequence(p.s, c.b, at, len);
-  const sage_rows& to = what == 1 ? p.d1 : p.d0;
-  const size_t stride = (size_t)(what < 2 ? 2 : 1) * kTile * D;
-  const float* part = p.part + (what == 1 ? kTile * D : 0);
-  const float f = what == 1 ? 1.f : p.sm_scale;
-  constexpr int kPer = D / 4;  // threads of a row
-#pragma unroll 1
-  for (int r = blockIdx.y * (256 / kPer) + threadIdx.x / kPer; r < kTile; r += kJoinSlices * (256 / kPer)) {
-    const int d = threadIdx.x % kPer * 4;
-    const int token = what < 2 ? r : r / p.s.G, i = c.i * (what < 2 ? kTile : p.s.w) + token;
-    if (i >= len || (what == 2 && token >= p.s.w)) continue;
-    const int h = what < 2 ? c.hk : c.hk * p.s.G + r - token * p.s.G;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int w = w0 - 1; w <= c.last; ++w) {
-      const float4 x = *reinterpret_cast<const float4*>(part + (size_t)(2 * w + (w < w0)) * stride + (size_t)r * D + d);
-      sum.x += x.x, sum.y += x.y, sum.z += x.z, sum.w += x.w;
-    }
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(to.p) + (long long)(at + i) * to.token + h * to.head + d) =
-        make_uint2(bf2(sum.x * f, sum.y * f), bf2(sum.z * f, sum.w * f));
-  }
 }
 
 template <int D>
@@ -799,8 +757,7 @@ int launch(const BwdParams& dkv, const BwdParams& dq, const PreParams& pre, cons
   const int grid = sms < kMaxParts ? sms : kMaxParts;
   if (launch_pdl(packed_pre_kernel<D>, dim3((unsigned)blocks), dim3(256), 0, st, pre) != cudaSuccess ||
       launch_pdl(packed_dkv_kernel<D>, dim3(grid), dim3(kThreads), smem, st, dkv, tq, tk, tv, to) != cudaSuccess ||
-      launch_pdl(packed_dq_kernel<D>, dim3(grid), dim3(kThreads), smem, st, dq, tq, tk, tv, to) != cudaSuccess ||
-      launch_pdl(packed_bwd_join_kernel<D>, dim3(grid, kJoinSlices, 3), dim3(256), 0, st, dkv, dq) != cudaSuccess)
+      launch_pdl(packed_dq_kernel<D>, dim3(grid), dim3(kThreads), smem, st, dq, tq, tk, tv, to) != cudaSuccess)
     return SAGE_ERR_CUDA;
   return SAGE_OK;
 }
@@ -818,10 +775,9 @@ int launch_packed_bwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V
   float* nlse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.stats);
   float* ndelta = nlse + (size_t)T * H;
   const PreParams pre{s, O, dO, LSE, nlse, ndelta};
-  Cut* cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(ws) + l.cuts);
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.part);
-  const BwdParams dkv{s, nlse, ndelta, dK, dV, cuts, part, sm_scale * kLog2e, sm_scale};
-  const BwdParams dq{s, nlse, ndelta, dQ, dQ, cuts + kMaxParts, part + (size_t)2 * kMaxParts * 2 * kTile * D, sm_scale * kLog2e, sm_scale};
+  const BwdParams dkv{s, nlse, ndelta, dK, dV, part, sm_scale * kLog2e, sm_scale};
+  const BwdParams dq{s, nlse, ndelta, dQ, dQ, part + (size_t)2 * kMaxParts * 2 * kTile * D, sm_scale * kLog2e, sm_scale};
   ScopedTimer timer("packed_bwd", st);
   return D == 128 ? launch<128>(dkv, dq, pre, Q, K, V, H, sms, st) : launch<64>(dkv, dq, pre, Q, K, V, H, sms, st);
 }

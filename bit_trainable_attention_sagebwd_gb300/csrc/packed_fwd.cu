@@ -32,11 +32,9 @@ struct FwdParams {
   __nv_bfloat16* O;
   long long o_token, o_head;
   float* LSE;
-  Cut* cuts;
-  float* part;  // two of each worker: [256][D] sums, [256] references, [256] row sums
+  float* part;  // of each worker two places, of each two row tiles: [D / 4][128] sums of four, [128] references, [128] row sums
   float alpha;  // sm_scale log2 e
 };
-constexpr int kUnitRows = 2 * kTile;  // of a unit
 
 template <int D>
 struct FwdSmem {
@@ -46,6 +44,7 @@ struct FwdSmem {
   uint64_t bar_q_full[2], bar_q_empty[2], bar_k_full[2], bar_k_empty[2], bar_v_full[2], bar_v_empty[2], bar_v_raw;
   uint64_t bar_s[2], bar_p[2], bar_o[2], bar_o_read[2], bar_turn[2];
   FeedRing ring;
+  Meeting meeting[2];
   long long wsum[kThreads / 32];
   long long pre[kPackedGroups + 1];
   uint32_t tmem_base;
@@ -78,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
+      sm.meeting[t].init();
       mbar_init(&sm.bar_q_full[t], 1);
       mbar_init(&sm.bar_q_empty[t], 1);
       mbar_init(&sm.bar_k_full[t], 1);
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (kc > (uint32_t)t) mbar_wait(&sm.bar_k_full[(kc - 1 - t) & 1], ((kc - 1 - t) >> 1) & 1, &give_up);
       }
     } else if (warp == 12) {
-      feed<kPairs>(p.s, sm.ring, sm.pre, group, line, idle, p.cuts, abort);
+      feed<kPairs>(p.s, sm.ring, sm.pre, group, line, idle, abort);
     } else if (warp == 10) {
       // ---------------- V
       uint32_t kc = 0, nr = 0;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + t * 128, o_col = tmem + lanes + kColO + t * 128;
     const int token = r / p.s.G, head = r - token * p.s.G;  // of the tile
-    uint32_t ns = 0, no = 0;
+    uint32_t ns = 0, no = 0, joins = 0;
     bool ok = true;
     while (ok && parts.next(s)) {
       const Places pl(p.s, s, solo);
@@ -384,85 +384,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = ok && wait(&sm.bar_o[t], no++ & 1);
       if (!ok) break;
       tc_fence_after();
-      const bool whole = s.c0 == 0 && s.c1 == s.n;
-      float* part = p.part + (size_t)(2 * w0 + (s.c0 == 0 ? 1 : 0)) * kUnitRows * (D + 2);
-      const float f = l != 0.f ? 1.f / l : 0.f;
       const int h = s.hk * p.s.G + head;
       __nv_bfloat16* orow = p.O + (long long)(s.at + i) * p.o_token + h * p.o_head;
+      constexpr size_t kPart = (size_t)kTile * (D + 2);
+      auto finish = [&]() {  // the row's LSE, and O's factor
+        if (live) p.LSE[(size_t)h * p.s.T + s.at + i] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        return l != 0.f ? 1.f / l : 0.f;
+      };
+      const bool whole = s.whole();
+      const float f = whole ? finish() : 1.f;
+      float* part = p.part + (size_t)(2 * s.place() + x) * kPart;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         uint32_t o[32];
         tmem_ld32(o_col + d, o);
         tmem_wait32(o);
-        if (!live) continue;
-        if (!whole) {
-#pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<uint4*>(part + (size_t)(x * kTile + r) * D + d + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          continue;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4 y;
-          __nv_bfloat162* z = reinterpret_cast<__nv_bfloat162*>(&y);
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            z[g] = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * g]) * f, __uint_as_float(o[8 * e + 2 * g + 1]) * f);
-          *reinterpret_cast<uint4*>(orow + d + 8 * e) = y;
-        }
+        if (whole && live) store_row(orow + d, reinterpret_cast<const float(&)[32]>(o), f);
+        if (!whole) store_sums(part, d, r, o);
       }
       tc_fence_before();
       mbar_arrive(&sm.bar_o_read[t]);
-      if (live && !whole)
-        part[(size_t)kUnitRows * D + x * kTile + r] = m, part[(size_t)kUnitRows * (D + 1) + x * kTile + r] = l;
-      else if (live)
-        p.LSE[(size_t)h * p.s.T + s.at + i] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      if (whole) continue;
+      part[(size_t)kTile * D + r] = m;
+      part[(size_t)kTile * (D + 1) + r] = l;
+      if (!sm.meeting[t].was_last(p.s.status + kFwdCounters + 2 * s.first() + x, s.parts(), joins++, abort, ok)) continue;
+      // O = sum O_k 2^(m_k - M) / sum l_k 2^(m_k - M)
+      const float* parts_of = p.part + x * kPart;
+      auto at = [&](int k) { return parts_of + (size_t)(2 * s.place(k)) * kPart; };
+      m = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int k = 0; k < s.parts(); ++k) m = fmaxf(m, __ldcg(at(k) + (size_t)kTile * D + r));
+      const float sub = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+      for (int k = 0; k < s.parts(); ++k)
+        l = fmaf(__ldcg(at(k) + (size_t)kTile * (D + 1) + r), ex2(__ldcg(at(k) + (size_t)kTile * D + r) - sub), l);
+      const float g = finish();
+#pragma unroll 1
+      for (int d = 0; d < D; d += 32) {
+        float o[32] = {};
+#pragma unroll 1
+        for (int k = 0; k < s.parts(); ++k) add_sums(at(k), d, r, ex2(__ldcg(at(k) + (size_t)kTile * D + r) - sub), o);
+        if (live) store_row(orow + d, o, g);
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 8) tmem_dealloc(sm.tmem_base, kCols);
   if (tid == 0 && sm.abort) atomicMax(p.s.status, (int)kDevTimeout);
-}
-
-// The rows of units that were cut: a warp a row, D / 32 channels a lane.  O = sum O_k 2^(m_k - M) / sum l_k 2^(m_k - M).
-constexpr int kJoinWarps = 8, kJoinSlices = 8;
-template <int D>
-__global__ void __launch_bounds__(32 * kJoinWarps) packed_fwd_join_kernel(const FwdParams p) {
-  const int w0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  pdl_trigger();
-  const Cut c = p.cuts[w0];
-  if (!was_cut(p.s, c, w0)) return;
-  int at, len;
-  sequence(p.s, c.b, at, len);
-  constexpr int kPer = D / 32;
-  constexpr size_t kPart = (size_t)kUnitRows * (D + 2);
-#pragma unroll 1
-  for (int row = blockIdx.y * kJoinWarps + warp; row < kUnitRows; row += kJoinWarps * kJoinSlices) {
-    const int x = row / kTile, r = row % kTile, token = r / p.s.G;
-    const int i = (2 * c.i + x) * p.s.w + token;
-    if (token >= p.s.w || i >= len) continue;
-    // (the first part lies at place 2 (w0 - 1) + 1, the others at 2 w)
-    float top = -INFINITY;
-    for (int w = w0 - 1; w <= c.last; ++w)
-      top = fmaxf(top, p.part[(size_t)(2 * w + (w < w0)) * kPart + (size_t)kUnitRows * D + row]);
-    const float sub = top == -INFINITY ? 0.f : top;
-    float o[kPer] = {}, l = 0.f;
-    for (int w = w0 - 1; w <= c.last; ++w) {
-      const float* part = p.part + (size_t)(2 * w + (w < w0)) * kPart;
-      const float f = ex2(part[(size_t)kUnitRows * D + row] - sub);
-      l = fmaf(part[(size_t)kUnitRows * (D + 1) + row], f, l);
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] = fmaf(part[(size_t)row * D + lane * kPer + e], f, o[e]);
-    }
-    const float f = l != 0.f ? 1.f / l : 0.f;
-    const int h = c.hk * p.s.G + r - token * p.s.G;
-    __nv_bfloat162* to = reinterpret_cast<__nv_bfloat162*>(p.O + (long long)(at + i) * p.o_token + h * p.o_head + lane * kPer);
-#pragma unroll
-    for (int e = 0; e < kPer; e += 2) to[e / 2] = __floats2bfloat162_rn(o[e] * f, o[e + 1] * f);
-    if (lane == 0) p.LSE[(size_t)h * p.s.T + at + i] = l != 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
-  }
 }
 
 template <int D>
@@ -474,8 +443,7 @@ int launch(const FwdParams& p, const sage_rows& Q, const sage_rows& K, const sag
   const size_t smem = sizeof(FwdSmem<D>) + 1024;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return SAGE_ERR_CUDA;
   const int grid = sms < kMaxParts ? sms : kMaxParts;
-  if (launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p, tq, tk, tv) != cudaSuccess ||
-      launch_pdl(packed_fwd_join_kernel<D>, dim3(grid, kJoinSlices), dim3(32 * kJoinWarps), 0, st, p) != cudaSuccess)
+  if (launch_pdl(kern, dim3(grid), dim3(kThreads), smem, st, p, tq, tk, tv) != cudaSuccess)
     return SAGE_ERR_CUDA;
   return SAGE_OK;
 }
@@ -485,10 +453,9 @@ int launch(const FwdParams& p, const sage_rows& Q, const sage_rows& K, const sag
 PackedWs packed_ws_layout(int T, int, int H, int, int D, bool backward) {
   auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   PackedWs l;
-  l.cuts = 256;
-  l.part = l.cuts + up(2 * kMaxParts * sizeof(Cut));
+  l.part = kHeader * sizeof(int);
   // (the backward's are dK, dV and dQ of 128 rows each)
-  l.stats = l.part + up((size_t)2 * kMaxParts * (backward ? 3 * kTile * D : kUnitRows * (D + 2)) * sizeof(float));
+  l.stats = l.part + up((size_t)2 * kMaxParts * kTile * (backward ? 3 * D : 2 * (D + 2)) * sizeof(float));
   l.total = l.stats + (backward ? up((size_t)T * H * 2 * sizeof(float)) : 0);
   return l;
 }
@@ -505,7 +472,6 @@ int launch_packed_fwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V
   p.o_token = O.token, p.o_head = O.head;
   p.LSE = LSE;
   const PackedWs l = packed_ws_layout(T, S, H, Hkv, D, false);
-  p.cuts = reinterpret_cast<Cut*>(static_cast<uint8_t*>(ws) + l.cuts);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.part);
   p.alpha = sm_scale * 1.4426950408889634f;
   ScopedTimer timer("packed_fwd", st);

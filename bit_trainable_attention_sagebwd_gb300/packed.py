@@ -13,30 +13,34 @@ from __future__ import annotations
 
 import ctypes
 
-from . import SAGE_ERR_UNSUPPORTED, SageError, lib, sage_rows
+from . import SAGE_ERR_UNSUPPORTED, SageError, lib
+
+_I64x12, _I64x24 = ctypes.c_longlong * 12, ctypes.c_longlong * 24
 
 
-def _rows(x, name, shape, device):
-    """A tensor argument [T, heads, D] after its checks."""
-    import torch
-    if x.dtype is not torch.bfloat16 or tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{name}: torch.bfloat16 of shape {tuple(shape)} expected, got {x.dtype} {tuple(x.shape)}")
-    if x.device != device:
-        raise ValueError(f"{name}: on {x.device}, q is on {device}")
-    token, head, channel = x.stride()
-    if channel != 1:
-        raise ValueError(f"{name}: its channels are not contiguous")
-    return ctypes.byref(sage_rows(x.data_ptr(), token, head))
-
-
-def _array(x, name, dtype, shape, device):
-    """The address of a contiguous tensor argument after its checks."""
-    if x.dtype is not dtype or tuple(x.shape) != tuple(shape):
+def _refuse(x, name, dtype, shape, device, whose="q is"):
+    """Why a tensor argument is refused."""
+    if x.dtype is not dtype or x.shape != shape:
         raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} expected, got {x.dtype} {tuple(x.shape)}")
     if x.device != device:
-        raise ValueError(f"{name}: on {x.device}, q is on {device}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
+        raise ValueError(f"{name}: on {x.device}, {whose} on {device}")
+    raise ValueError(f"{name}: not contiguous")
+
+
+def _rows(x, name, bf16, shape, device):
+    """The members of a sage_rows of a tensor argument [T, heads, D], after its checks."""
+    token, head, channel = x.stride()
+    if x.dtype is not bf16 or x.shape != shape or x.device != device:
+        _refuse(x, name, bf16, shape, device)
+    if channel != 1:
+        raise ValueError(f"{name}: its channels are not contiguous")
+    return x.data_ptr(), token, head
+
+
+def _array(x, name, dtype, shape, device, whose="q is"):
+    """The address of a contiguous tensor argument after its checks."""
+    if x.dtype is not dtype or x.shape != shape or x.device != device or not x.is_contiguous():
+        _refuse(x, name, dtype, shape, device, whose)
     return x.data_ptr()
 
 
@@ -86,7 +90,7 @@ def alloc_packed_ws(T, S, H, Hkv, D, backward=False, device="cuda", stream=None)
         raise SageError("sage_attn_packed_ws_bytes", SAGE_ERR_UNSUPPORTED)
     with torch.cuda.stream(stream):
         ws = torch.empty(n, dtype=torch.uint8, device=device)
-        ws[:4].zero_()
+        ws[:4096].zero_()
     return ws
 
 
@@ -106,16 +110,18 @@ def packed_forward(q, k, v, cu_seqlens, causal=True, sm_scale=None, o=None, lse=
     were.  Entries of cu_seqlens that are out of order or range are reported in the status word of ws."""
     import torch
     T, S, H, Hkv, D, dev = _shapes(q, k, cu_seqlens)
+    bf16, qs, kv = torch.bfloat16, (T, H, D), (T, Hkv, D)
     ws = _workspace(ws, (T, S, H, Hkv, D), False, dev, stream)
     if o is None:
-        o = _new(stream, dev, (T, H, D), torch.bfloat16)
+        o = _new(stream, dev, qs, bf16)
     if lse is None:
         lse = _new(stream, dev, (H, T), torch.float32)
-    kv = (T, Hkv, D)
-    _call(lib().sage_attn_packed_fwd, dev, stream, _rows(q, "q", (T, H, D), dev), _rows(k, "k", kv, dev), _rows(v, "v", kv, dev),
-          _array(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev), _rows(o, "o", (T, H, D), dev),
-          _array(lse, "lse", torch.float32, (H, T), dev), ws.data_ptr(), ws.nbytes, T, S, H, Hkv, D, int(causal),
-          0.0 if sm_scale is None else float(sm_scale))
+    rows = _I64x12(*_rows(q, "q", bf16, qs, dev), *_rows(k, "k", bf16, kv, dev), *_rows(v, "v", bf16, kv, dev),
+                   *_rows(o, "o", bf16, qs, dev))  # four sage_rows
+    at = ctypes.addressof(rows)
+    _call(lib().sage_attn_packed_fwd, dev, stream, at, at + 24, at + 48,
+          _array(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev), at + 72, _array(lse, "lse", torch.float32, (H, T), dev),
+          ws.data_ptr(), ws.nbytes, T, S, H, Hkv, D, int(causal), 0.0 if sm_scale is None else float(sm_scale))
     return o, lse
 
 
@@ -125,14 +131,17 @@ def packed_backward(q, k, v, o, lse, do, cu_seqlens, causal=True, sm_scale=None,
     q, k and v.  ws: alloc_packed_ws(.., backward=True)."""
     import torch
     T, S, H, Hkv, D, dev = _shapes(q, k, cu_seqlens)
+    bf16, qs, kv = torch.bfloat16, (T, H, D), (T, Hkv, D)
     ws = _workspace(ws, (T, S, H, Hkv, D), True, dev, stream)
-    qs, kv = (T, H, D), (T, Hkv, D)
-    dq = _new(stream, dev, qs, torch.bfloat16) if dq is None else dq
-    dk = _new(stream, dev, kv, torch.bfloat16) if dk is None else dk
-    dv = _new(stream, dev, kv, torch.bfloat16) if dv is None else dv
-    _call(lib().sage_attn_packed_bwd, dev, stream, _rows(q, "q", qs, dev), _rows(k, "k", kv, dev), _rows(v, "v", kv, dev),
-          _rows(o, "o", qs, dev), _array(lse, "lse", torch.float32, (H, T), dev), _rows(do, "do", qs, dev),
-          _array(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev), _rows(dq, "dq", qs, dev), _rows(dk, "dk", kv, dev),
-          _rows(dv, "dv", kv, dev), ws.data_ptr(), ws.nbytes, T, S, H, Hkv, D, int(causal),
+    dq = _new(stream, dev, qs, bf16) if dq is None else dq
+    dk = _new(stream, dev, kv, bf16) if dk is None else dk
+    dv = _new(stream, dev, kv, bf16) if dv is None else dv
+    rows = _I64x24(*_rows(q, "q", bf16, qs, dev), *_rows(k, "k", bf16, kv, dev), *_rows(v, "v", bf16, kv, dev),
+                   *_rows(o, "o", bf16, qs, dev), *_rows(do, "do", bf16, qs, dev), *_rows(dq, "dq", bf16, qs, dev),
+                   *_rows(dk, "dk", bf16, kv, dev), *_rows(dv, "dv", bf16, kv, dev))  # eight sage_rows
+    at = ctypes.addressof(rows)
+    _call(lib().sage_attn_packed_bwd, dev, stream, at, at + 24, at + 48, at + 72,
+          _array(lse, "lse", torch.float32, (H, T), dev), at + 96, _array(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev),
+          at + 120, at + 144, at + 168, ws.data_ptr(), ws.nbytes, T, S, H, Hkv, D, int(causal),
           0.0 if sm_scale is None else float(sm_scale))
     return dq, dk, dv

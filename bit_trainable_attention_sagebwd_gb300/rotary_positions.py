@@ -14,9 +14,10 @@ from __future__ import annotations
 import ctypes
 import math
 
-from . import SAGE_ERR_UNSUPPORTED, SageError, lib, sage_heads, sage_rotary
-from .packed import _array, _call, _new
+from . import SAGE_ERR_UNSUPPORTED, SageError, lib, sage_rotary
+from .packed import _array, _call, _new, _refuse
 
+_I64x8, _I64x16 = ctypes.c_longlong * 8, ctypes.c_longlong * 16
 _SCALINGS = ("none", "linear", "base", "ramp")
 
 
@@ -33,6 +34,7 @@ class Rotary:
         self.turns, self.rot, self.interleaved, self.gain = turns, 2 * turns.shape[0], bool(interleaved), float(gain)
         self.device = turns.device
         self.c = sage_rotary(turns.data_ptr(), self.rot, int(self.interleaved), self.gain)
+        self._ref = ctypes.byref(self.c)
 
 
 def rotary_frequencies(rot, base=10000.0, scaling="none", factor=1.0, context=4096, fast=32.0, slow=1.0):
@@ -82,18 +84,16 @@ def rotary_table(rot, base=10000.0, scaling="none", factor=1.0, context=4096, fa
     return Rotary(torch.tensor(turns, dtype=torch.int64).to(device), interleaved, of_scaling if gain is None else gain)
 
 
-def _heads(x, name, shape, device):
-    """A tensor argument, [T, H, D] or [B, H, N, D], after its checks."""
-    import torch
-    if x.dtype is not torch.bfloat16 or tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{name}: torch.bfloat16 of shape {tuple(shape)} expected, got {x.dtype} {tuple(x.shape)}")
-    if x.device != device:
-        raise ValueError(f"{name}: on {x.device}, the table is on {device}")
-    if x.stride(-1) != 1:
+def _heads(x, name, bf16, shape, device):
+    """The members of a sage_heads of a tensor argument, [T, H, D] or [B, H, N, D], after its checks."""
+    stride = x.stride()
+    if x.dtype is not bf16 or x.shape != shape or x.device != device:
+        _refuse(x, name, bf16, shape, device, "the table is")
+    if stride[-1] != 1:
         raise ValueError(f"{name}: its channels are not contiguous")
-    if x.dim() == 3:
-        return ctypes.byref(sage_heads(x.data_ptr(), 0, x.stride(0), x.stride(1)))
-    return ctypes.byref(sage_heads(x.data_ptr(), x.stride(0), x.stride(2), x.stride(1)))
+    if len(stride) == 3:
+        return x.data_ptr(), 0, stride[0], stride[1]
+    return x.data_ptr(), stride[0], stride[2], stride[1]
 
 
 def _turn(table, q, k, cu_seqlens, start, positions, q_out, k_out, stream, inverse):
@@ -111,20 +111,27 @@ def _turn(table, q, k, cu_seqlens, start, positions, q_out, k_out, stream, inver
     S = 0 if cu_seqlens is None else cu_seqlens.shape[0] - 1
     if table.rot > D:
         raise SageError("rotary", SAGE_ERR_UNSUPPORTED)
-    hkv = 0 if k is None else k.shape[1]
-    ks = (N, hkv, D) if packed else (B, hkv, N, D)
+    bf16, i32, whose = torch.bfloat16, torch.int32, "the table is"
     if q_out is None:
-        q_out = _new(stream, dev, q.shape, torch.bfloat16)
-    if k is not None and k_out is None:
-        k_out = _new(stream, dev, ks, torch.bfloat16)
-    i32 = torch.int32
-    _call(lib().sage_attn_rotary, dev, stream, ctypes.byref(table.c), _heads(q, "q", q.shape, dev),
-          _heads(q_out, "q_out", q.shape, dev), None if k is None else _heads(k, "k", ks, dev),
-          None if k is None else _heads(k_out, "k_out", ks, dev),
-          None if positions is None else _array(positions, "positions", i32, (N,) if packed else (B, N), dev),
-          None if start is None else _array(start, "start", i32, (S,) if S else (B,), dev),
-          None if cu_seqlens is None else _array(cu_seqlens, "cu_seqlens", i32, (S + 1,), dev), B, N, S, H, hkv, D,
-          int(inverse))
+        q_out = _new(stream, dev, q.shape, bf16)
+    heads = _heads(q, "q", bf16, q.shape, dev) + _heads(q_out, "q_out", bf16, q.shape, dev)
+    if k is None:
+        hkv, heads = 0, _I64x8(*heads)  # two sage_heads
+        at = ctypes.addressof(heads)
+        keys = keys_out = None
+    else:
+        hkv = k.shape[1]
+        ks = (N, hkv, D) if packed else (B, hkv, N, D)
+        if k_out is None:
+            k_out = _new(stream, dev, ks, bf16)
+        heads = _I64x16(*heads, *_heads(k, "k", bf16, ks, dev), *_heads(k_out, "k_out", bf16, ks, dev))  # four
+        at = ctypes.addressof(heads)
+        keys, keys_out = at + 64, at + 96
+    _call(lib().sage_attn_rotary, dev, stream, table._ref, at, at + 32, keys, keys_out,
+          None if positions is None else _array(positions, "positions", i32, (N,) if packed else (B, N), dev, whose),
+          None if start is None else _array(start, "start", i32, (S,) if S else (B,), dev, whose),
+          None if cu_seqlens is None else _array(cu_seqlens, "cu_seqlens", i32, (S + 1,), dev, whose), B, N, S, H, hkv, D,
+          inverse)
     return q_out if k is None else (q_out, k_out)
 
 

@@ -17,8 +17,7 @@ def lib():
 
 
 FAKE = 0x10000  # aligned, never dereferenced: the checks fail first
-NULL_ROWS = ctypes.POINTER(sa.sage_rows)()
-NULL_HEADS = ctypes.POINTER(sa.sage_heads)()
+NULL_ROWS = NULL_HEADS = None
 
 
 def rows(p=FAKE, token=512, head=128):
@@ -32,6 +31,7 @@ def forward(**o):
     s = SHAPE | {n: o[n] for n in SHAPE if n in o}
     t = {n: o.get(n, rows(FAKE + 0x1000 * i)) for i, n in enumerate(("Q", "K", "V", "O"))}
     ws_bytes = o.get("ws_bytes", sa.sage_attn_packed_ws_bytes(*SHAPE.values(), False))
+    t = {n: x and ctypes.byref(x) for n, x in t.items()}
     return sa.sage_attn_packed_fwd(t["Q"], t["K"], t["V"], o.get("cu", FAKE), t["O"], o.get("LSE", FAKE), o.get("ws", FAKE),
                                    ws_bytes, *s.values(), 1, o.get("sm_scale", 0.0), None)
 
@@ -41,6 +41,7 @@ def backward(**o):
     names = ("Q", "K", "V", "O", "dO", "dQ", "dK", "dV")
     t = {n: o.get(n, rows(FAKE + 0x1000 * (i + 1))) for i, n in enumerate(names)}
     ws_bytes = o.get("ws_bytes", sa.sage_attn_packed_ws_bytes(*SHAPE.values(), True))
+    t = {n: x and ctypes.byref(x) for n, x in t.items()}
     return sa.sage_attn_packed_bwd(t["Q"], t["K"], t["V"], t["O"], o.get("LSE", FAKE), t["dO"], o.get("cu", FAKE), t["dQ"], t["dK"],
                                    t["dV"], o.get("ws", FAKE), ws_bytes, *s.values(), 1, o.get("sm_scale", 0.0), None)
 
@@ -106,6 +107,7 @@ def heads(p=FAKE, batch=64 * 128, token=512, head=128):
 def turn(**o):
     r = sa.sage_rotary(o.get("turns", FAKE), o.get("rot", 64), 0, o.get("gain", 1.0))
     t = {n: o.get(n, heads(FAKE + 0x1000 * i)) for i, n in enumerate(("Q", "Qo", "K", "Ko"))}
+    t = {n: x and ctypes.byref(x) for n, x in t.items()}
     a = dict(positions=None, start=FAKE, cu=None, B=2, N=16, S=0, H=4, Hkv=2, D=128)
     a |= {n: o[n] for n in a if n in o}
     return sa.sage_attn_rotary(NULL if o.get("null") else r, *t.values(), *a.values(), 0, None)
