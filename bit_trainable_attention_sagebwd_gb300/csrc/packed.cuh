@@ -41,6 +41,13 @@ enum UnitKind { kPairs, kRows, kKeys };
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1) / (unsigned)b); }
 
+// One arrival of a warp, for all of its lanes (one of each lane queues up at the barrier)
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+  __syncwarp();
+}
+
 // first token and length of sequence b; one that does not lie in the tensors counts as empty
 __device__ __forceinline__ void sequence(const PackedShape& p, int b, int& at, int& len) {
   const int x = __ldcg(p.cu + b), y = __ldcg(p.cu + b + 1);
@@ -297,13 +304,13 @@ struct Meeting {
   uint64_t written, told;
   int last;
   __device__ __forceinline__ void init() {
-    mbar_init(&written, 128);
+    mbar_init(&written, 4);
     mbar_init(&told, 1);
   }
   // n: how often the group has met here before
   __device__ __forceinline__ bool was_last(int* counter, int parts, uint32_t n, volatile int* abort, bool& ok) {
     __threadfence();
-    mbar_arrive(&written);
+    warp_arrive(&written);
     if ((threadIdx.x & 127) < 32) {
       ok = ok && mbar_wait_warp(&written, n & 1, abort);
       if (ok && (threadIdx.x & 31) == 0) {

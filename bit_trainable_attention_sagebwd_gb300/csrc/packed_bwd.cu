@@ -124,16 +124,16 @@ __device__ __forceinline__ void init_barriers(BwdSmem<D>& sm, int readers) {
     mbar_init(&sm.bar_y_full[t], 1);
     mbar_init(&sm.bar_y_empty[t], 1);
     mbar_init(&sm.bar_raw[t], 1);
-    mbar_init(&sm.bar_st_full[t], 32);
-    mbar_init(&sm.bar_st_empty[t], 256);
+    mbar_init(&sm.bar_st_full[t], 1);
+    mbar_init(&sm.bar_st_empty[t], 8);
     mbar_init(&sm.bar_s[t], 1);
   }
   sm.ring.init(readers);
   mbar_init(&sm.bar_dp, 1);
-  mbar_init(&sm.bar_p, 256);
-  mbar_init(&sm.bar_ds, 256);
+  mbar_init(&sm.bar_p, 8);
+  mbar_init(&sm.bar_ds, 8);
   mbar_init(&sm.bar_acc, 1);
-  mbar_init(&sm.bar_acc_read, 256);
+  mbar_init(&sm.bar_acc_read, 8);
   sm.abort = 0;
   fence_mbar_init();
 }
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sm.nlse[st][lane + 32 * e] = a[e];
           sm.ndelta[st][lane + 32 * e] = b[e];
         }
-        mbar_arrive(&sm.bar_st_full[st]);
+        warp_arrive(&sm.bar_st_full[st]);
       }
     }
   } else {
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sm.bar_p);
+      warp_arrive(&sm.bar_p);
       ok = wait(&sm.bar_dp, n & 1);
       if (!ok) break;
       tc_fence_after();
@@ -449,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sm.bar_st_empty[st]);
-      mbar_arrive(&sm.bar_ds);
+      warp_arrive(&sm.bar_st_empty[st]);
+      warp_arrive(&sm.bar_ds);
       if (!t.last) continue;
       // ---- the unit's sums: channels [D / 2 g, D / 2 (g + 1)) of the key
       ok = wait(&sm.bar_acc, units++ & 1);
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(&sm.bar_acc_read);
+      warp_arrive(&sm.bar_acc_read);
       if (whole || !sm.meeting[g].was_last(p.s.status + kKeyCounters + 2 * t.s.first() + g, t.s.parts(), joins++, abort, ok)) continue;
 #pragma unroll 1
       for (int x = 0; x < 2; ++x) {
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sm.bar_ds);
+      warp_arrive(&sm.bar_ds);
       if (!t.last) continue;
       ok = wait(&sm.bar_acc, units++ & 1);
       if (!ok) break;
@@ -722,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!whole) store_sums(p.part + (size_t)t.s.place() * kTile * D, d, r, o);
       }
       tc_fence_before();
-      mbar_arrive(&sm.bar_acc_read);
+      warp_arrive(&sm.bar_acc_read);
       if (whole || !sm.meeting[g].was_last(p.s.status + kRowCounters + 2 * t.s.first() + g, t.s.parts(), joins++, abort, ok)) continue;
 #pragma unroll 1
       for (int d = g * (D / 2); d < (g + 1) * (D / 2); d += 32) {

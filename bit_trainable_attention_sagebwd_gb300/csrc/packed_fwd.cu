@@ -86,9 +86,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.bar_v_empty[t], 2);
       mbar_init(&sm.bar_s[t], 1);
       mbar_init(&sm.bar_turn[t], 1);
-      mbar_init(&sm.bar_p[t], 128);
+      mbar_init(&sm.bar_p[t], 4);
       mbar_init(&sm.bar_o[t], 1);
-      mbar_init(&sm.bar_o_read[t], 128);
+      mbar_init(&sm.bar_o_read[t], 4);
     }
     mbar_init(&sm.bar_v_raw, 1);
     sm.ring.init(12);
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&sm.bar_p[t]);
+        warp_arrive(&sm.bar_p[t]);
         float y0, y1;
         f2split(fadd2(sums[0], sums[1]), y0, y1);
         l += y0 + y1;
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!whole) store_sums(part, d, r, o);
       }
       tc_fence_before();
-      mbar_arrive(&sm.bar_o_read[t]);
+      warp_arrive(&sm.bar_o_read[t]);
       if (whole) continue;
       part[(size_t)kTile * D + r] = m;
       part[(size_t)kTile * (D + 1) + r] = l;
