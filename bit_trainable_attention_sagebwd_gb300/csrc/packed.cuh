@@ -297,21 +297,21 @@ struct Feed {
   }
 };
 
-// The joining of a unit that was cut, by those who finish its last part (in time, whichever it is): a group of 128
-// threads has written its part's sums; true in all of them if it was the last to do so.  Sums are then added in the order
+// The joining of a unit that was cut, by those who finish its last part (in time, whichever it is): a group of
+// warps has written its part's sums; true in all of them if it was the last to do so.  Sums are then added in the order
 // of the parts, so the bits do not depend on who came last.  The counter is zero before and after.
 struct Meeting {
   uint64_t written, told;
   int last;
-  __device__ __forceinline__ void init() {
-    mbar_init(&written, 4);
+  __device__ __forceinline__ void init(int warps) {
+    mbar_init(&written, warps);
     mbar_init(&told, 1);
   }
-  // n: how often the group has met here before
-  __device__ __forceinline__ bool was_last(int* counter, int parts, uint32_t n, volatile int* abort, bool& ok) {
+  // n: how often the group has met here before; leads: whether the warp is the group's first
+  __device__ __forceinline__ bool was_last(int* counter, int parts, uint32_t n, bool leads, volatile int* abort, bool& ok) {
     __threadfence();
     warp_arrive(&written);
-    if ((threadIdx.x & 127) < 32) {
+    if (leads) {
       ok = ok && mbar_wait_warp(&written, n & 1, abort);
       if (ok && (threadIdx.x & 31) == 0) {
         last = atomicAdd(counter, 1) == parts - 1;

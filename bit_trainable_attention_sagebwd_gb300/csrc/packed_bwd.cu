@@ -10,11 +10,11 @@
 // set the pace), none are cleared and converted, and the gradients are the same bits every time.
 //
 // The two main kernels are alike.  One CTA an SM walks its units (packed.cuh):
-//  - warps 9 and 10 bring the operands by TMA, warp 11 (packed_dkv) the row statistics;
-//  - warp 8 issues the products (bf16 operands, fp32 accumulators in TMEM);
-//  - warps 0-3 and 4-7 turn S into P and dP into dS, the first group the tile's first 64 columns, the second the
-//    others; P and dS go back to TMEM as bf16 over the columns that they come from and are the A operands of the
-//    products that take them.
+//  - warp 19 walks, warp 17 brings the operands by TMA, warp 18 the row statistics (packed_dkv) or some of the operands
+//    (packed_dq);
+//  - warp 16 issues the products (bf16 operands, fp32 accumulators in TMEM);
+//  - warps 0-15 turn S into P and dP into dS, each group of four 32 of the tile's columns; P and dS go back to TMEM as
+//    bf16 over the columns that they come from and are the A operands of the products that take them.
 // While the warps compute, the products of the tile before and after run: P(i) lets dV(i) and S(i + 1) in, dS(i) lets
 // dK(i) and dP(i + 1) in.
 // Rows that belong to the next sequence: those that a product would sum over are zeroed in shared memory (up to 15 of a
@@ -28,9 +28,8 @@ namespace sage {
 
 namespace {
 
-constexpr int kThreads = 512;  // (whole warpgroups, for the register split)
-constexpr int kRegsCompute = 176, kRegsIssue = 80;
-static_assert(2 * kRegsCompute + 2 * kRegsIssue <= 4 * 128, "the launch's registers");
+constexpr int kWorkWarps = 16, kWarps = kWorkWarps + 4, kThreads = 32 * kWarps;  // (five a scheduler: 96 registers a thread)
+constexpr int kIssuer = 16, kLoader = 17, kSecond = 18, kWalker = 19;  // kSecond: the row statistics, or V and dO
 constexpr uint32_t kCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -94,49 +93,63 @@ __global__ void __launch_bounds__(256) packed_pre_kernel(const PreParams p) {
 }
 
 // ------------------------------------------------------------------ shared memory
-template <int D>
+template <int D, int XS, int YS>
 struct BwdSmem {
-  uint8_t a[2][kTile * D * 2];     // the unit's own tiles: packed_dkv K and V, packed_dq Q and dO
-  uint8_t x[2][kTile * D * 2];     // two tiles deep, what the unit walks over: Q, or K
-  uint8_t y[2][kTile * D * 2];     // dO, or V
+  uint8_t a[2][kTile * D * 2];   // the unit's own tiles: packed_dkv K and V, packed_dq Q and dO
+  uint8_t x[XS][kTile * D * 2];  // what the unit walks over: Q, or K
+  uint8_t y[YS][kTile * D * 2];  // dO, or V
   __align__(16) float nlse[2][kTile];
   __align__(16) float ndelta[2][kTile];
-  uint64_t bar_a_full[2], bar_a_empty[2], bar_x_full[2], bar_x_empty[2], bar_y_full[2], bar_y_empty[2], bar_raw[2];
+  uint64_t bar_a_full[2], bar_a_empty[2], bar_x_full[XS], bar_x_empty[XS], bar_y_full[YS], bar_y_empty[YS], bar_raw[2];
   uint64_t bar_st_full[2], bar_st_empty[2];
   uint64_t bar_s[2], bar_dp, bar_p, bar_ds, bar_acc, bar_acc_read;
   FeedRing ring;
-  Meeting meeting[2];
-  long long wsum[kThreads / 32];
+  Meeting meeting;
+  long long wsum[kWarps];
   long long pre[kPackedGroups + 1];
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(BwdSmem<128>) + 1024 <= 227 * 1024, "shared memory of a CTA");
+static_assert(sizeof(BwdSmem<128, 2, 2>) + 1024 <= 227 * 1024 && sizeof(BwdSmem<128, 3, 1>) + 1024 <= 227 * 1024,
+              "shared memory of a CTA");
 
-template <int D>
-__device__ __forceinline__ void init_barriers(BwdSmem<D>& sm, int readers) {
+template <int D, int XS, int YS>
+__device__ __forceinline__ void init_barriers(BwdSmem<D, XS, YS>& sm, int readers) {
   for (int t = 0; t < 2; ++t) {
-    sm.meeting[t].init();
     mbar_init(&sm.bar_a_full[t], 1);
     mbar_init(&sm.bar_a_empty[t], 1);
-    mbar_init(&sm.bar_x_full[t], 1);
-    mbar_init(&sm.bar_x_empty[t], 1);
-    mbar_init(&sm.bar_y_full[t], 1);
-    mbar_init(&sm.bar_y_empty[t], 1);
     mbar_init(&sm.bar_raw[t], 1);
     mbar_init(&sm.bar_st_full[t], 1);
-    mbar_init(&sm.bar_st_empty[t], 8);
+    mbar_init(&sm.bar_st_empty[t], kWorkWarps);
     mbar_init(&sm.bar_s[t], 1);
   }
+  for (int t = 0; t < XS; ++t) {
+    mbar_init(&sm.bar_x_full[t], 1);
+    mbar_init(&sm.bar_x_empty[t], 1);
+  }
+  for (int t = 0; t < YS; ++t) {
+    mbar_init(&sm.bar_y_full[t], 1);
+    mbar_init(&sm.bar_y_empty[t], 1);
+  }
   sm.ring.init(readers);
+  sm.meeting.init(kWorkWarps);
   mbar_init(&sm.bar_dp, 1);
-  mbar_init(&sm.bar_p, 8);
-  mbar_init(&sm.bar_ds, 8);
+  mbar_init(&sm.bar_p, kWorkWarps);
+  mbar_init(&sm.bar_ds, kWorkWarps);
   mbar_init(&sm.bar_acc, 1);
-  mbar_init(&sm.bar_acc_read, 8);
+  mbar_init(&sm.bar_acc_read, kWorkWarps);
   sm.abort = 0;
   fence_mbar_init();
 }
+
+// A place in a ring of N: how often it has come round, and where it stands
+template <int N>
+struct Turn {
+  uint32_t at = 0, round = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) at = 0, ++round;
+  }
+};
 
 // rows [from, to) of a tile in shared memory become zero (a warp)
 template <int D>
@@ -194,15 +207,16 @@ struct Tiles {
   }
 };
 
-// columns of an A operand in TMEM, 16 bf16 each: P or dS as the two groups write them
-__device__ __forceinline__ uint32_t a_col(int k) { return k < 4 ? 8 * k : 64 + 8 * (k - 4); }
+// columns of an A operand in TMEM, 16 bf16 each: P or dS as the four groups write them
+__device__ __forceinline__ uint32_t a_col(int k) { return 32 * (k >> 1) + 8 * (k & 1); }
 
 // D (+)= A B over `rows` rows of B, 16 at a time
 __device__ __forceinline__ void issue_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, int rows, bool acc) {
   if (rows > kTile - 16) {
-    issue_ts_x4(d, a, b, idesc, acc);
-    issue_ts_x4(d, a + 64, b + (4 * 2048 >> 4), idesc, 1);
+    issue_ts_x4_pairs(d, a, b, idesc, acc);
+    issue_ts_x4_pairs(d, a + 64, b + (4 * 2048 >> 4), idesc, 1);
   } else {
+#pragma unroll 1
     for (int k = 0; k * 16 < rows; ++k) issue_ts(d, a + a_col(k), b + (k * 2048 >> 4), idesc, acc || k > 0);
   }
 }
@@ -216,16 +230,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kAtoms = D / 64, kAtom = kTile * 128;
   constexpr uint32_t cS = 0, cDP = 128, cDV = 256, cDK = 384;
   extern __shared__ uint8_t smem_raw[];
-  BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  using Smem = BwdSmem<D, 2, 2>;
+  Smem& sm = *reinterpret_cast<Smem*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int box = p.s.G * p.s.w;  // rows of a row tile
-  if (tid == 0) init_barriers(sm, 12);
+  if (tid == 0) init_barriers(sm, kWorkWarps + 3);
   if (warp < 4 && box < kTile) {  // the rows that no copy brings
     zero_rows<D>(warp < 2 ? sm.x[warp] : sm.y[warp - 2], box, kTile);
     fence_proxy_async_smem();
   }
   pdl_wait();
-  if (warp == 8) {
+  if (warp == kIssuer) {
     tmem_alloc(&sm.tmem_base, kCols);
     tmem_relinquish();
   }
@@ -244,9 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tile_of = [&](const Tiles& t) { return Units<kKeys>(p.s, t.s.len).first(t.s.i) + t.j; };
   auto rows_of = [&](const Tiles& t, int rt) { return min(p.s.w, t.s.len - rt * p.s.w) * p.s.G; };
 
-  if (warp >= 8) {
-    regs_decrease<kRegsIssue>();
-    if (warp == 8) {
+  if (warp >= kWorkWarps) {
+    if (warp == kIssuer) {
       // ---------------- MMA issuer
       constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_g = idesc_bf16(kTile, D, false, true);
       constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
@@ -305,46 +319,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (t.valid) issue_dp(t, n + 1);
       }
-    } else if (warp < 11) {
-      // ---------------- K and Q (warp 9), V and dO (warp 10)
-      const int v = warp - 9;
-      const CUtensorMap* tm_a = v ? &tm_v : &tm_k;
-      const CUtensorMap* tm_x = v ? &tm_do : &tm_q;
-      uint64_t *full = v ? sm.bar_y_full : sm.bar_x_full, *empty = v ? sm.bar_y_empty : sm.bar_x_empty;
-      uint32_t units = 0, raws = 0, n = 0;
+    } else if (warp == kLoader) {
+      // ---------------- K and V; dO and Q, in the order in which they are given back
+      uint32_t units = 0, raws[2] = {0, 0}, n = 0;
       bool ok = true;
       for (Tiles t(sm.ring, abort); ok && t.valid; t.next(), ++n) {
-        if (t.first) {
-          ok = units == 0 || wait(&sm.bar_a_empty[v], (units - 1) & 1);
-          if (!ok) break;
-          ++units;
-          if (lane == 0) {
+        const uint32_t st = n & 1;
+        const int rt = tile_of(t), rows = rows_of(t, rt);
+        auto own = [&](int v, const CUtensorMap* tm) {
+          if (!t.first) return;
+          ok = ok && (units == 0 || wait(&sm.bar_a_empty[v], (units - 1) & 1));
+          if (ok && lane == 0) {
             mbar_arrive_expect_tx(&sm.bar_a_full[v], kTile * D * 2);
 #pragma unroll
             for (int h = 0; h < kAtoms; ++h)
-              tma_load_3d(sm.a[v] + h * kAtom, tm_a, h * 64, t.s.at + t.s.i * kTile, t.s.hk, &sm.bar_a_full[v]);
+              tma_load_3d(sm.a[v] + h * kAtom, tm, h * 64, t.s.at + t.s.i * kTile, t.s.hk, &sm.bar_a_full[v]);
           }
           __syncwarp();
-        }
-        const uint32_t st = n & 1;
-        ok = n < 2 || wait(&empty[st], ((n >> 1) - 1) & 1);
-        if (!ok) break;
-        const int rt = tile_of(t);
-        uint8_t* tile = v ? sm.y[st] : sm.x[st];
-        ok = bring<D>(tile, rows_of(t, rt), box, box * D * 2, &full[st], &sm.bar_raw[v], raws, abort, [&](uint64_t* bar) {
+        };
+        auto walked = [&](uint8_t* tile, const CUtensorMap* tm, uint64_t* full, uint64_t* empty, int v) {
+          ok = ok && (n < 2 || wait(empty, ((n >> 1) - 1) & 1));
+          ok = ok && bring<D>(tile, rows, box, box * D * 2, full, &sm.bar_raw[v], raws[v], abort, [&](uint64_t* bar) {
 #pragma unroll
-          for (int h = 0; h < kAtoms; ++h)
-            tma_load_3d(tile + h * kAtom, tm_x, h * 64, t.s.hk * p.s.G, t.s.at + rt * p.s.w, bar);
-        });
+                 for (int h = 0; h < kAtoms; ++h)
+                   tma_load_3d(tile + h * kAtom, tm, h * 64, t.s.hk * p.s.G, t.s.at + rt * p.s.w, bar);
+               });
+        };
+        own(0, &tm_k);
+        if (t.first) walked(sm.x[st], &tm_q, &sm.bar_x_full[st], &sm.bar_x_empty[st], 0);
+        own(1, &tm_v);
+        walked(sm.y[st], &tm_do, &sm.bar_y_full[st], &sm.bar_y_empty[st], 1);
+        if (!t.first) walked(sm.x[st], &tm_q, &sm.bar_x_full[st], &sm.bar_x_empty[st], 0);
+        if (t.first) ++units;
       }
       // (copies in flight after a wait that ran out)
       int give_up = 0;
-      if (units) mbar_wait(&sm.bar_a_full[v], (units - 1) & 1, &give_up);
+      for (int v = 0; v < 2; ++v)
+        if (units) mbar_wait(&sm.bar_a_full[v], (units - 1) & 1, &give_up);
       for (uint32_t e = 0; e < 2; ++e)
-        if (n > e) mbar_wait(&full[(n - 1 - e) & 1], ((n - 1 - e) >> 1) & 1, &give_up);
-    } else if (warp == 12) {
+        if (n > e) {
+          mbar_wait(&sm.bar_x_full[(n - 1 - e) & 1], ((n - 1 - e) >> 1) & 1, &give_up);
+          mbar_wait(&sm.bar_y_full[(n - 1 - e) & 1], ((n - 1 - e) >> 1) & 1, &give_up);
+        }
+    } else if (warp == kWalker) {
       feed<kKeys>(p.s, sm.ring, sm.pre, group, line, idle, abort);
-    } else if (warp == 11) {
+    } else if (warp == kSecond) {
       // ---------------- row statistics; of rows behind the sequence P is 0
       uint32_t n = 0;
       for (Tiles t(sm.ring, abort); t.valid; t.next(), ++n) {
@@ -368,11 +387,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    regs_increase<kRegsCompute>();
-    // ---------------- thread r of group g: key r of the tile, columns [64 g, 64 g + 64)
+    // ---------------- thread r of group g: key r of the tile, columns [32 g, 32 g + 32)
     const int g = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_col = tmem + lanes + cS + 64 * g, dp_col = tmem + lanes + cDP + 64 * g;
+    const uint32_t s_col = tmem + lanes + cS + 32 * g, dp_col = tmem + lanes + cDP + 32 * g;
     bool ok = true;
     uint32_t units = 0, joins = 0;
     Tiles t(sm.ring, abort);
@@ -381,116 +399,95 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t st = n & 1;
       // causal: columns of tokens before the key are masked
       const int key = t.s.i * kTile + r, ahead = p.s.causal ? key - tile_of(t) * p.s.w : 0;
-      const int mask = min(ahead, kTile) * p.s.G - 64 * g;  // the group's columns before it
+      const int mask = min(ahead, kTile) * p.s.G - 32 * g;  // the group's columns before it
       ok = wait(&sm.bar_st_full[st], (n >> 1) & 1) && wait(&sm.bar_s[0], n & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t sv[2][32];
-#pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld32(s_col + 32 * c, sv[c]);
-      tmem_ld_wait();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) reg_fence32(sv[c]);
+      uint32_t sv[32];
+      tmem_ld32(s_col, sv);
+      tmem_wait32(sv);
       if (__any_sync(0xffffffffu, mask > 0)) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e < mask) sv[c][e] = 0xff800000u;
+        for (int e = 0; e < 32; ++e)
+          if (e < mask) sv[e] = 0xff800000u;
       }
+      uint32_t w[16];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[16];
+      for (int e = 0; e < 32; e += 4) {
+        const float4 nl = *reinterpret_cast<const float4*>(&sm.nlse[st][32 * g + e]);
+        float u[4];
+        f2split(ffma2(f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), a2, f2(nl.x, nl.y)), u[0], u[1]);
+        f2split(ffma2(f2(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), a2, f2(nl.z, nl.w)), u[2], u[3]);
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 nl = *reinterpret_cast<const float4*>(&sm.nlse[st][64 * g + 32 * c + e]);
-          float u[4];
-          f2split(ffma2(f2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), a2, f2(nl.x, nl.y)), u[0], u[1]);
-          f2split(ffma2(f2(__uint_as_float(sv[c][e + 2]), __uint_as_float(sv[c][e + 3])), a2, f2(nl.z, nl.w)), u[2], u[3]);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            u[y] = ex2(u[y]);
-            sv[c][e + y] = __float_as_uint(u[y]);
-          }
-          w[e >> 1] = bf2(u[0], u[1]);
-          w[(e >> 1) + 1] = bf2(u[2], u[3]);
+        for (int y = 0; y < 4; ++y) {
+          u[y] = ex2(u[y]);
+          sv[e + y] = __float_as_uint(u[y]);
         }
-        tmem_st16(s_col + 16 * c, w);
+        w[e >> 1] = bf2(u[0], u[1]);
+        w[(e >> 1) + 1] = bf2(u[2], u[3]);
       }
+      tmem_st16(s_col, w);
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&sm.bar_p);
       ok = wait(&sm.bar_dp, n & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t dv[2][32];
+      uint32_t dv[32];
+      tmem_ld32(dp_col, dv);
+      tmem_wait32(dv);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld32(dp_col + 32 * c, dv[c]);
-      tmem_ld_wait();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) reg_fence32(dv[c]);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float4 nd = *reinterpret_cast<const float4*>(&sm.ndelta[st][64 * g + 32 * c + e]);
-          float x, y;
-          f2split(fmul2(fadd2(f2(__uint_as_float(dv[c][e]), __uint_as_float(dv[c][e + 1])), f2(nd.x, nd.y)),
-                        f2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]))),
-                  x, y);
-          w[e >> 1] = bf2(x, y);
-          f2split(fmul2(fadd2(f2(__uint_as_float(dv[c][e + 2]), __uint_as_float(dv[c][e + 3])), f2(nd.z, nd.w)),
-                        f2(__uint_as_float(sv[c][e + 2]), __uint_as_float(sv[c][e + 3]))),
-                  x, y);
-          w[(e >> 1) + 1] = bf2(x, y);
-        }
-        tmem_st16(dp_col + 16 * c, w);
+      for (int e = 0; e < 32; e += 4) {
+        const float4 nd = *reinterpret_cast<const float4*>(&sm.ndelta[st][32 * g + e]);
+        float x, y;
+        f2split(fmul2(fadd2(f2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), f2(nd.x, nd.y)),
+                      f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]))),
+                x, y);
+        w[e >> 1] = bf2(x, y);
+        f2split(fmul2(fadd2(f2(__uint_as_float(dv[e + 2]), __uint_as_float(dv[e + 3])), f2(nd.z, nd.w)),
+                      f2(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]))),
+                x, y);
+        w[(e >> 1) + 1] = bf2(x, y);
       }
+      tmem_st16(dp_col, w);
       tmem_st_wait();
       tc_fence_before();
-      warp_arrive(&sm.bar_st_empty[st]);
       warp_arrive(&sm.bar_ds);
+      warp_arrive(&sm.bar_st_empty[st]);
       if (!t.last) continue;
-      // ---- the unit's sums: channels [D / 2 g, D / 2 (g + 1)) of the key
+      // ---- the unit's sums: groups 0 and 1 half of dK's channels each, groups 2 and 3 of dV's
       ok = wait(&sm.bar_acc, units++ & 1);
       if (!ok) break;
       tc_fence_after();
       const bool live = key < t.s.len, whole = t.s.whole();
-      auto row_of = [&](int x) {
-        const sage_rows& to = x ? p.d1 : p.d0;
-        return static_cast<__nv_bfloat16*>(to.p) + (long long)(t.s.at + key) * to.token + t.s.hk * to.head;
-      };
-      auto part_of = [&](int place, int x) { return p.part + (size_t)(2 * place + x) * kTile * D; };
+      const int x = g >> 1, d0 = (g & 1) * (D / 2);
+      const sage_rows& to = x ? p.d1 : p.d0;
+      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(to.p) + (long long)(t.s.at + key) * to.token + t.s.hk * to.head;
+      auto part_of = [&](int place) { return p.part + (size_t)(2 * place + x) * kTile * D; };
+      const float f = x ? 1.f : p.sm_scale;
 #pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-#pragma unroll 1
-        for (int d = g * (D / 2); d < (g + 1) * (D / 2); d += 32) {
-          uint32_t o[32];
-          tmem_ld32(tmem + lanes + (x ? cDV : cDK) + d, o);
-          tmem_wait32(o);
-          if (whole && live) store_row(row_of(x) + d, reinterpret_cast<const float(&)[32]>(o), x ? 1.f : p.sm_scale);
-          if (!whole) store_sums(part_of(t.s.place(), x), d, r, o);
-        }
+      for (int d = d0; d < d0 + D / 2; d += 32) {
+        uint32_t o[32];
+        tmem_ld32(tmem + lanes + (x ? cDV : cDK) + d, o);
+        tmem_wait32(o);
+        if (whole && live) store_row(row + d, reinterpret_cast<const float(&)[32]>(o), f);
+        if (!whole) store_sums(part_of(t.s.place()), d, r, o);
       }
       tc_fence_before();
       warp_arrive(&sm.bar_acc_read);
-      if (whole || !sm.meeting[g].was_last(p.s.status + kKeyCounters + 2 * t.s.first() + g, t.s.parts(), joins++, abort, ok)) continue;
+      if (whole || !sm.meeting.was_last(p.s.status + kKeyCounters + 2 * t.s.first(), t.s.parts(), joins++, warp == 0, abort, ok)) continue;
 #pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
+      for (int d = d0; d < d0 + D / 2; d += 32) {
+        float o[32] = {};
 #pragma unroll 1
-        for (int d = g * (D / 2); d < (g + 1) * (D / 2); d += 32) {
-          float o[32] = {};
-#pragma unroll 1
-          for (int k = 0; k < t.s.parts(); ++k) add_sums(part_of(t.s.place(k), x), d, r, 1.f, o);
-          if (live) store_row(row_of(x) + d, o, x ? 1.f : p.sm_scale);
-        }
+        for (int k = 0; k < t.s.parts(); ++k) add_sums(part_of(t.s.place(k)), d, r, 1.f, o);
+        if (live) store_row(row + d, o, f);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, kCols);
+  if (warp == kIssuer) tmem_dealloc(tmem, kCols);
   if (tid == 0 && sm.abort) atomicMax(p.s.status, (int)kDevTimeout);
 }
 
@@ -501,15 +498,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     packed_dq_kernel(const BwdParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do) {
   constexpr int kAtoms = D / 64, kAtom = kTile * 128;
+  // (K's tile is held by dQ's product until dS is there, V's only by dP)
+  constexpr int kStagesK = 3, kStagesV = 1;
   constexpr uint32_t cDP = 256, cDQ = 384;
   extern __shared__ uint8_t smem_raw[];
-  BwdSmem<D>& sm = *reinterpret_cast<BwdSmem<D>*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  using Smem = BwdSmem<D, kStagesK, kStagesV>;
+  Smem& sm = *reinterpret_cast<Smem*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int box = p.s.G * p.s.w;
-  if (tid == 0) init_barriers(sm, 11);
+  if (tid == 0) init_barriers(sm, kWorkWarps + 3);
   // (no wait for packed_dkv, of which nothing is read: its CTAs let this kernel in once packed_pre was complete.  The wait
   // at the end keeps the order for what follows.)
-  if (warp == 8) {
+  if (warp == kIssuer) {
     tmem_alloc(&sm.tmem_base, kCols);
     tmem_relinquish();
   }
@@ -525,9 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool idle = line.total == 0 || (int)blockIdx.x >= line.parts;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
 
-  if (warp >= 8) {
-    regs_decrease<kRegsIssue>();
-    if (warp == 8) {
+  if (warp >= kWorkWarps) {
+    if (warp == kIssuer) {
       // ---------------- MMA issuer
       constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_g = idesc_bf16(kTile, D, false, true);
       constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
@@ -535,30 +534,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t k_k = sdesc_sw128(smem_u32(sm.x[0]), 16, 1024), v_k = sdesc_sw128(smem_u32(sm.y[0]), 16, 1024);
       const uint64_t k_n = sdesc_sw128(smem_u32(sm.x[0]), kAtom, 1024);
       bool ok = true;
-      uint32_t units_s = 0, units_dp = 0, ns = 0, ndp = 0;
+      uint32_t units_s = 0, units_dp = 0, ns = 0;
+      Turn<kStagesK> kt;                 // K's stage of S and of dQ
+      uint32_t kq = 0;
+      Turn<kStagesV> vt;
       auto issue_s = [&](const Tiles& t) {
         const uint32_t n = ns++;
         if (t.first) ok = ok && wait(&sm.bar_a_full[0], units_s++ & 1);
-        ok = ok && wait(&sm.bar_x_full[n & 1], (n >> 1) & 1);
+        ok = ok && wait(&sm.bar_x_full[kt.at], kt.round & 1);
         if (!ok) return;
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < kAtoms; ++h)
-          issue_ss_x4(tmem + (n & 1) * 128, q_k + h * kAtomStep, k_k + (n & 1) * kNext + h * kAtomStep, id_s, h > 0);
+          issue_ss_x4(tmem + (n & 1) * 128, q_k + h * kAtomStep, k_k + kt.at * kNext + h * kAtomStep, id_s, h > 0);
+        kt.next();
         commit(&sm.bar_s[n & 1]);
         if (t.last) commit(&sm.bar_a_empty[0]);
       };
       auto issue_dp = [&](bool first, bool last) {
-        const uint32_t n = ndp++;
         if (first) ok = ok && wait(&sm.bar_a_full[1], units_dp++ & 1);
-        ok = ok && wait(&sm.bar_y_full[n & 1], (n >> 1) & 1);
+        ok = ok && wait(&sm.bar_y_full[vt.at], vt.round & 1);
         if (!ok) return;
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < kAtoms; ++h)
-          issue_ss_x4(tmem + cDP, do_k + h * kAtomStep, v_k + (n & 1) * kNext + h * kAtomStep, id_s, h > 0);
+          issue_ss_x4(tmem + cDP, do_k + h * kAtomStep, v_k + vt.at * kNext + h * kAtomStep, id_s, h > 0);
         commit(&sm.bar_dp);
-        commit(&sm.bar_y_empty[n & 1]);
+        commit(&sm.bar_y_empty[vt.at]);
+        vt.next();
         if (last) commit(&sm.bar_a_empty[1]);
       };
       // the tile whose dS is waited for, and the one after it, whose S is issued
@@ -585,8 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (now.first && done) ok = ok && wait(&sm.bar_acc_read, (done - 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        issue_rows(tmem + cDQ, tmem + (n & 1) * 128, k_n + (n & 1) * kNext, id_g, now.keys, !now.first);
-        commit(&sm.bar_x_empty[n & 1]);
+        issue_rows(tmem + cDQ, tmem + (n & 1) * 128, k_n + kq * kNext, id_g, now.keys, !now.first);
+        commit(&sm.bar_x_empty[kq]);
+        if (++kq == kStagesK) kq = 0;
         if (now.last) {
           commit(&sm.bar_acc);
           ++done;
@@ -594,15 +598,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         now = then;
         take(then);
       }
-    } else if (warp < 11) {
-      // ---------------- Q and K (warp 9), dO and V (warp 10)
-      const int v = warp - 9;
+    } else if (warp < kWalker) {
+      // ---------------- Q and K (the first loader), dO and V (the second)
+      const int v = warp - kLoader;
       const CUtensorMap* tm_a = v ? &tm_do : &tm_q;
       const CUtensorMap* tm_x = v ? &tm_v : &tm_k;
       uint64_t *full = v ? sm.bar_y_full : sm.bar_x_full, *empty = v ? sm.bar_y_empty : sm.bar_x_empty;
-      uint32_t units = 0, raws = 0, n = 0;
+      const uint32_t stages = v ? kStagesV : kStagesK;
+      uint32_t units = 0, raws = 0, st = 0, round = 0;
       bool ok = true;
-      for (Tiles t(sm.ring, abort); ok && t.valid; t.next(), ++n) {
+      for (Tiles t(sm.ring, abort); ok && t.valid; t.next()) {
         if (t.first) {
           ok = units == 0 || wait(&sm.bar_a_empty[v], (units - 1) & 1);
           if (!ok) break;
@@ -615,8 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        const uint32_t st = n & 1;
-        ok = n < 2 || wait(&empty[st], ((n >> 1) - 1) & 1);
+        ok = round == 0 || wait(&empty[st], (round - 1) & 1);
         if (!ok) break;
         uint8_t* tile = v ? sm.y[st] : sm.x[st];
         ok = bring<D>(tile, min(kTile, t.s.len - t.j * kTile), kTile, kTile * D * 2, &full[st], &sm.bar_raw[v], raws, abort,
@@ -625,20 +629,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int h = 0; h < kAtoms; ++h)
                           tma_load_3d(tile + h * kAtom, tm_x, h * 64, t.s.at + t.j * kTile, t.s.hk, bar);
                       });
+        if (++st == stages) st = 0, ++round;
       }
+      // (copies in flight after a wait that ran out)
       int give_up = 0;
       if (units) mbar_wait(&sm.bar_a_full[v], (units - 1) & 1, &give_up);
-      for (uint32_t e = 0; e < 2; ++e)
-        if (n > e) mbar_wait(&full[(n - 1 - e) & 1], ((n - 1 - e) >> 1) & 1, &give_up);
-    } else if (warp == 12) {
+      for (uint32_t e = 0; e < stages; ++e) {
+        if (st == 0 && round == 0) break;
+        if (st == 0) st = stages, --round;
+        --st;
+        mbar_wait(&full[st], round & 1, &give_up);
+      }
+    } else if (warp == kWalker) {
       feed<kRows>(p.s, sm.ring, sm.pre, group, line, idle, abort);
     }
   } else {
-    regs_increase<kRegsCompute>();
-    // ---------------- thread r of group g: row r of the tile, keys [64 g, 64 g + 64)
+    // ---------------- thread r of group g: row r of the tile, keys [32 g, 32 g + 32)
     const int g = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t dp_col = tmem + lanes + cDP + 64 * g;
+    const uint32_t dp_col = tmem + lanes + cDP + 32 * g;
     const int token = r / p.s.G, head = r - token * p.s.G;
     bool ok = true;
     uint32_t units = 0, joins = 0;
@@ -653,89 +662,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         nl = live ? __ldcg(p.nlse + at) : -INFINITY;
         nd = live ? __ldcg(p.ndelta + at) : 0.f;
       }
-      const int left = (live && p.s.causal ? i + 1 : t.s.len) - t.j * kTile - 64 * g;  // keys that the row sees
-      const uint32_t s_col = tmem + lanes + (n & 1) * 128 + 64 * g;
+      const int left = (live && p.s.causal ? i + 1 : t.s.len) - t.j * kTile - 32 * g;  // keys that the row sees
+      const uint32_t s_col = tmem + lanes + (n & 1) * 128 + 32 * g;
       ok = wait(&sm.bar_s[n & 1], (n >> 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t sv[2][32];
+      uint32_t sv[32];
+      tmem_ld32(s_col, sv);
+      tmem_wait32(sv);
+      if (__any_sync(0xffffffffu, left < 32)) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld32(s_col + 32 * c, sv[c]);
-      tmem_ld_wait();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) reg_fence32(sv[c]);
-      if (__any_sync(0xffffffffu, left < 64)) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (c * 32 + e >= left) sv[c][e] = 0xff800000u;
+        for (int e = 0; e < 32; ++e)
+          if (e >= left) sv[e] = 0xff800000u;
       }
       const uint64_t l2 = f2(nl, nl), d2 = f2(nd, nd);
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float x, y;
-          f2split(ffma2(f2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), a2, l2), x, y);
-          sv[c][e] = __float_as_uint(ex2(x));
-          sv[c][e + 1] = __float_as_uint(ex2(y));
-        }
+      for (int e = 0; e < 32; e += 2) {
+        float x, y;
+        f2split(ffma2(f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), a2, l2), x, y);
+        sv[e] = __float_as_uint(ex2(x));
+        sv[e + 1] = __float_as_uint(ex2(y));
+      }
       ok = wait(&sm.bar_dp, n & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t dv[2][32];
+      uint32_t dv[32], w[16];
+      tmem_ld32(dp_col, dv);
+      tmem_wait32(dv);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) tmem_ld32(dp_col + 32 * c, dv[c]);
-      tmem_ld_wait();
-#pragma unroll
-      for (int c = 0; c < 2; ++c) reg_fence32(dv[c]);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          float x, y;
-          f2split(fmul2(fadd2(f2(__uint_as_float(dv[c][e]), __uint_as_float(dv[c][e + 1])), d2),
-                        f2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]))),
-                  x, y);
-          w[e >> 1] = bf2(x, y);
-        }
-        tmem_st16(s_col + 16 * c, w);
+      for (int e = 0; e < 32; e += 2) {
+        float x, y;
+        f2split(fmul2(fadd2(f2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), d2),
+                      f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]))),
+                x, y);
+        w[e >> 1] = bf2(x, y);
       }
+      tmem_st16(s_col, w);
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&sm.bar_ds);
       if (!t.last) continue;
+      // ---- the unit's sums, 32 channels a group (D = 64: the first two)
       ok = wait(&sm.bar_acc, units++ & 1);
       if (!ok) break;
       tc_fence_after();
+      const int d = 32 * g;
       __nv_bfloat16* row = static_cast<__nv_bfloat16*>(p.d0.p) + (long long)(t.s.at + i) * p.d0.token +
-                           (t.s.hk * p.s.G + head) * p.d0.head;
+                           (t.s.hk * p.s.G + head) * p.d0.head + d;
       const bool whole = t.s.whole();
-#pragma unroll 1
-      for (int d = g * (D / 2); d < (g + 1) * (D / 2); d += 32) {
+      if (d < D) {
         uint32_t o[32];
         tmem_ld32(tmem + lanes + cDQ + d, o);
         tmem_wait32(o);
-        if (whole && live) store_row(row + d, reinterpret_cast<const float(&)[32]>(o), p.sm_scale);
+        if (whole && live) store_row(row, reinterpret_cast<const float(&)[32]>(o), p.sm_scale);
         if (!whole) store_sums(p.part + (size_t)t.s.place() * kTile * D, d, r, o);
       }
       tc_fence_before();
       warp_arrive(&sm.bar_acc_read);
-      if (whole || !sm.meeting[g].was_last(p.s.status + kRowCounters + 2 * t.s.first() + g, t.s.parts(), joins++, abort, ok)) continue;
-#pragma unroll 1
-      for (int d = g * (D / 2); d < (g + 1) * (D / 2); d += 32) {
+      if (whole || !sm.meeting.was_last(p.s.status + kRowCounters + 2 * t.s.first(), t.s.parts(), joins++, warp == 0, abort, ok)) continue;
+      if (d < D) {
         float o[32] = {};
 #pragma unroll 1
         for (int k = 0; k < t.s.parts(); ++k) add_sums(p.part + (size_t)t.s.place(k) * kTile * D, d, r, 1.f, o);
-        if (live) store_row(row + d, o, p.sm_scale);
+        if (live) store_row(row, o, p.sm_scale);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, kCols);
+  if (warp == kIssuer) tmem_dealloc(tmem, kCols);
   if (tid == 0 && sm.abort) atomicMax(p.s.status, (int)kDevTimeout);
   pdl_wait();
 }
@@ -747,9 +742,9 @@ int launch(const BwdParams& dkv, const BwdParams& dq, const PreParams& pre, cons
   if (!make_tmap_queries(&tq, Q, D, H, dkv.s) || !make_tmap_keys(&tk, K, D, dkv.s) || !make_tmap_keys(&tv, V, D, dkv.s) ||
       !make_tmap_queries(&to, pre.dO, D, H, dkv.s))
     return SAGE_ERR_CUDA;
-  const size_t smem = sizeof(BwdSmem<D>) + 1024;
+  const size_t smem = sizeof(BwdSmem<D, 2, 2>) + 1024, smem_q = sizeof(BwdSmem<D, 3, 1>) + 1024;
   if (cudaFuncSetAttribute(packed_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
-      cudaFuncSetAttribute(packed_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      cudaFuncSetAttribute(packed_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_q) != cudaSuccess)
     return SAGE_ERR_CUDA;
   constexpr int kPerBlock = 256 / (D / 8) * 4;
   const long long blocks = ((long long)dkv.s.T * H + kPerBlock - 1) / kPerBlock;
@@ -757,7 +752,7 @@ int launch(const BwdParams& dkv, const BwdParams& dq, const PreParams& pre, cons
   const int grid = sms < kMaxParts ? sms : kMaxParts;
   if (launch_pdl(packed_pre_kernel<D>, dim3((unsigned)blocks), dim3(256), 0, st, pre) != cudaSuccess ||
       launch_pdl(packed_dkv_kernel<D>, dim3(grid), dim3(kThreads), smem, st, dkv, tq, tk, tv, to) != cudaSuccess ||
-      launch_pdl(packed_dq_kernel<D>, dim3(grid), dim3(kThreads), smem, st, dq, tq, tk, tv, to) != cudaSuccess)
+      launch_pdl(packed_dq_kernel<D>, dim3(grid), dim3(kThreads), smem_q, st, dq, tq, tk, tv, to) != cudaSuccess)
     return SAGE_ERR_CUDA;
   return SAGE_OK;
 }

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
-      sm.meeting[t].init();
+      sm.meeting[t].init(4);
       mbar_init(&sm.bar_q_full[t], 1);
       mbar_init(&sm.bar_q_empty[t], 1);
       mbar_init(&sm.bar_k_full[t], 1);
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (whole) continue;
       part[(size_t)kTile * D + r] = m;
       part[(size_t)kTile * (D + 1) + r] = l;
-      if (!sm.meeting[t].was_last(p.s.status + kFwdCounters + 2 * s.first() + x, s.parts(), joins++, abort, ok)) continue;
+      if (!sm.meeting[t].was_last(p.s.status + kFwdCounters + 2 * s.first() + x, s.parts(), joins++, (warp & 3) == 0, abort, ok)) continue;
       // O = sum O_k 2^(m_k - M) / sum l_k 2^(m_k - M)
       const float* parts_of = p.part + x * kPart;
       auto at = [&](int k) { return parts_of + (size_t)(2 * s.place(k)) * kPart; };
