@@ -10,8 +10,7 @@
 // set the pace), none are cleared and converted, and the gradients are the same bits every time.
 //
 // The two main kernels are alike.  One CTA an SM walks its units (packed.cuh):
-//  - warp 19 walks, warp 17 brings the operands by TMA, warp 18 the row statistics (packed_dkv) or some of the operands
-//    (packed_dq);
+//  - warp 19 walks, warp 17 (in packed_dq 18 too) brings the operands by TMA;
 //  - warp 16 issues the products (bf16 operands, fp32 accumulators in TMEM);
 //  - warps 0-15 turn S into P and dP into dS, each group of four 32 of the tile's columns; P and dS go back to TMEM as
 //    bf16 over the columns that they come from and are the A operands of the products that take them.
@@ -29,13 +28,14 @@ namespace sage {
 namespace {
 
 constexpr int kWorkWarps = 16, kWarps = kWorkWarps + 4, kThreads = 32 * kWarps;  // (five a scheduler: 96 registers a thread)
-constexpr int kIssuer = 16, kLoader = 17, kSecond = 18, kWalker = 19;  // kSecond: the row statistics, or V and dO
+constexpr int kIssuer = 16, kLoader = 17, kWalker = 19;  // (18: a second loader, in packed_dq)
 constexpr uint32_t kCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BwdParams {
   PackedShape s;
-  const float *nlse, *ndelta;  // [Hkv][T][G]: -LSE log2 e, -delta
+  const float *nlse, *ndelta;  // [Hkv][T][G]: -LSE log2 e, -delta (packed_dq)
+  const uint4* more;           // [Hkv][T][G]: the same as further channels of Q and dO (packed_dkv)
   sage_rows d0, d1;            // packed_dkv: dK, dV; packed_dq: dQ
   float* part;                 // of each worker two places: [D / 4][128] sums of four channels of d0, and of d1
   float alpha, sm_scale;       // alpha: sm_scale log2 e
@@ -47,7 +47,31 @@ struct PreParams {
   sage_rows O, dO;
   const float* LSE;
   float *nlse, *ndelta;
+  uint4* more;
+  float sm_scale;
 };
+
+// The row terms in the products.  packed_dkv has the query rows along the columns, so a row's LSE and delta are another
+// number in every register of a thread; read from shared memory by 16 warps they took half of the time (the tensor core
+// takes all of its bandwidth).  Instead they are channels: Q gets -LSE / sm_scale and dO -delta, each as three bf16 whose
+// sum has 24 bits, K and V ones; one more step along K, and S sm_scale - LSE and dP - delta are there.
+constexpr float kNever = -1e30f;  // in the place of -LSE / sm_scale: P = 0
+__device__ __forceinline__ uint32_t bf16_of(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ void split3(float x, uint32_t (&b)[3]) {
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    b[k] = bf16_of(x);
+    x -= __uint_as_float(b[k] << 16);
+    if (!(fabsf(x) < INFINITY)) x = 0.f;  // (an infinity or a NaN is all in the first)
+  }
+}
+// channels 0-2 of LSE, 3-5 of delta
+__device__ __forceinline__ uint4 more_channels(float l, float d) {
+  uint32_t a[3], b[3];
+  split3(l, a);
+  split3(d, b);
+  return make_uint4(a[0] | a[1] << 16, a[2] | b[0] << 16, b[1] | b[2] << 16, 0u);
+}
 
 // D / 8 lanes a row, rows in the order of [T, H]
 template <int D>
@@ -88,6 +112,7 @@ __global__ void __launch_bounds__(256) packed_pre_kernel(const PreParams p) {
       const float lse = p.LSE[(size_t)h * p.s.T + t];
       p.nlse[at] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // (a row that saw nothing: P = 0)
       p.ndelta[at] = -s;
+      p.more[at] = more_channels(lse == -INFINITY ? kNever : -lse / p.sm_scale, -s);
     }
   }
 }
@@ -98,10 +123,11 @@ struct BwdSmem {
   uint8_t a[2][kTile * D * 2];   // the unit's own tiles: packed_dkv K and V, packed_dq Q and dO
   uint8_t x[XS][kTile * D * 2];  // what the unit walks over: Q, or K
   uint8_t y[YS][kTile * D * 2];  // dO, or V
-  __align__(16) float nlse[2][kTile];
-  __align__(16) float ndelta[2][kTile];
+  // packed_dkv: the further channels of the tiles walked over, and ones in the places of LSE's and of delta's; 16 channels
+  // unswizzled, the first eight of 128 rows, then the others (zeros)
+  __align__(128) uint8_t more[XS == 2 ? 2 : 1][XS == 2 ? kTile * 32 : 16];
+  __align__(128) uint8_t ones[2][XS == 2 ? kTile * 32 : 16];
   uint64_t bar_a_full[2], bar_a_empty[2], bar_x_full[XS], bar_x_empty[XS], bar_y_full[YS], bar_y_empty[YS], bar_raw[2];
-  uint64_t bar_st_full[2], bar_st_empty[2];
   uint64_t bar_s[2], bar_dp, bar_p, bar_ds, bar_acc, bar_acc_read;
   FeedRing ring;
   Meeting meeting;
@@ -119,8 +145,6 @@ __device__ __forceinline__ void init_barriers(BwdSmem<D, XS, YS>& sm, int reader
     mbar_init(&sm.bar_a_full[t], 1);
     mbar_init(&sm.bar_a_empty[t], 1);
     mbar_init(&sm.bar_raw[t], 1);
-    mbar_init(&sm.bar_st_full[t], 1);
-    mbar_init(&sm.bar_st_empty[t], kWorkWarps);
     mbar_init(&sm.bar_s[t], 1);
   }
   for (int t = 0; t < XS; ++t) {
@@ -162,11 +186,11 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int to) {
 }
 
 // One tile by TMA (a warp; lane 0 issues): `load` issues the copies onto the barrier that it gets.  Of a tile with
-// `rows` rows of its own, fewer than the copy brings, those up to the next multiple of 16 are zeroed before `full` is
-// signalled.
-template <int D, class Load>
+// `rows` rows of its own, fewer than the copy brings, those up to the next multiple of 16 are zeroed (and `fill`ed) before
+// `full` is signalled.
+template <int D, class Load, class Fill>
 __device__ __forceinline__ bool bring(uint8_t* tile, int rows, int copied, uint32_t bytes, uint64_t* full, uint64_t* raw,
-                                      uint32_t& raws, volatile int* abort, Load&& load) {
+                                      uint32_t& raws, volatile int* abort, Load&& load, Fill&& fill) {
   const int lane = threadIdx.x & 31;
   const bool ragged = rows < copied && (rows & 15);
   uint64_t* bar = ragged ? raw : full;
@@ -182,6 +206,7 @@ __device__ __forceinline__ bool bring(uint8_t* tile, int rows, int copied, uint3
     return false;
   }
   zero_rows<D>(tile, rows, (rows + 15) & ~15);
+  fill(rows, (rows + 15) & ~15);
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(full);
@@ -234,11 +259,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem& sm = *reinterpret_cast<Smem*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int box = p.s.G * p.s.w;  // rows of a row tile
-  if (tid == 0) init_barriers(sm, kWorkWarps + 3);
-  if (warp < 4 && box < kTile) {  // the rows that no copy brings
-    zero_rows<D>(warp < 2 ? sm.x[warp] : sm.y[warp - 2], box, kTile);
-    fence_proxy_async_smem();
+  if (tid == 0) init_barriers(sm, kWorkWarps + 2);
+  if (warp < 4 && box < kTile) zero_rows<D>(warp < 2 ? sm.x[warp] : sm.y[warp - 2], box, kTile);  // the rows that no copy brings
+  for (int e = tid; e < 4 * kTile; e += kThreads) {
+    // the further channels: P = 0 in rows that no copy brings; ones
+    const int what = e / kTile, r = e % kTile;
+    uint4* to = reinterpret_cast<uint4*>(what < 2 ? sm.more[what] : sm.ones[what - 2]);
+    to[r] = what < 2 ? more_channels(kNever, 0.f) : what == 2 ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0x3f800000u, 0x3f803f80u, 0u);
+    to[kTile + r] = make_uint4(0u, 0u, 0u, 0u);
   }
+  fence_proxy_async_smem();
   pdl_wait();
   if (warp == kIssuer) {
     tmem_alloc(&sm.tmem_base, kCols);
@@ -266,6 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
       const uint64_t k_k = sdesc_sw128(smem_u32(sm.a[0]), 16, 1024), v_k = k_k + kNext;
       const uint64_t q_k = sdesc_sw128(smem_u32(sm.x[0]), 16, 1024), do_k = sdesc_sw128(smem_u32(sm.y[0]), 16, 1024);
+      constexpr uint64_t kMore = kTile * 32 >> 4;
+      const uint64_t one_k = sdesc_none(smem_u32(sm.ones[0]), kTile * 16, 128), more_k = sdesc_none(smem_u32(sm.more[0]), kTile * 16, 128);
       const uint64_t q_n = sdesc_sw128(smem_u32(sm.x[0]), kAtom, 1024), do_n = sdesc_sw128(smem_u32(sm.y[0]), kAtom, 1024);
       bool ok = true;
       uint32_t units = 0;  // that S has been begun of
@@ -277,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < kAtoms; ++h)
           issue_ss_x4(tmem + cS, k_k + h * kAtomStep, q_k + (n & 1) * kNext + h * kAtomStep, id_s, h > 0);
+        issue_ss(tmem + cS, one_k, more_k + (n & 1) * kMore, id_s, 1);
         commit(&sm.bar_s[0]);
         if (t.last) commit(&sm.bar_a_empty[0]);
       };
@@ -288,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int h = 0; h < kAtoms; ++h)
           issue_ss_x4(tmem + cDP, v_k + h * kAtomStep, do_k + (n & 1) * kNext + h * kAtomStep, id_s, h > 0);
+        issue_ss(tmem + cDP, one_k + kMore, more_k + (n & 1) * kMore, id_s, 1);
         commit(&sm.bar_dp);
         if (t.last) commit(&sm.bar_a_empty[1]);
       };
@@ -339,11 +373,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         auto walked = [&](uint8_t* tile, const CUtensorMap* tm, uint64_t* full, uint64_t* empty, int v) {
           ok = ok && (n < 2 || wait(empty, ((n >> 1) - 1) & 1));
-          ok = ok && bring<D>(tile, rows, box, box * D * 2, full, &sm.bar_raw[v], raws[v], abort, [&](uint64_t* bar) {
+          ok = ok && bring<D>(tile, rows, box, box * D * 2 + (v ? 0 : rows * 16), full, &sm.bar_raw[v], raws[v], abort,
+                              [&](uint64_t* bar) {
 #pragma unroll
-                 for (int h = 0; h < kAtoms; ++h)
-                   tma_load_3d(tile + h * kAtom, tm, h * 64, t.s.hk * p.s.G, t.s.at + rt * p.s.w, bar);
-               });
+                                for (int h = 0; h < kAtoms; ++h)
+                                  tma_load_3d(tile + h * kAtom, tm, h * 64, t.s.hk * p.s.G, t.s.at + rt * p.s.w, bar);
+                                if (v == 0)  // (with Q: dP of the tile before is done once Q's tile is free)
+                                  bulk_load(sm.more[st], p.more + ((size_t)t.s.hk * p.s.T + t.s.at + (size_t)rt * p.s.w) * p.s.G,
+                                            rows * 16, bar);
+                              },
+                              [&](int from, int to) {
+                                if (v == 0 && from + lane < to) reinterpret_cast<uint4*>(sm.more[st])[from + lane] = more_channels(kNever, 0.f);
+                              });
         };
         own(0, &tm_k);
         if (t.first) walked(sm.x[st], &tm_q, &sm.bar_x_full[st], &sm.bar_x_empty[st], 0);
@@ -363,28 +404,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kWalker) {
       feed<kKeys>(p.s, sm.ring, sm.pre, group, line, idle, abort);
-    } else if (warp == kSecond) {
-      // ---------------- row statistics; of rows behind the sequence P is 0
-      uint32_t n = 0;
-      for (Tiles t(sm.ring, abort); t.valid; t.next(), ++n) {
-        const uint32_t st = n & 1;
-        const int rt = tile_of(t), rows = rows_of(t, rt);
-        const size_t at = ((size_t)t.s.hk * p.s.T + t.s.at + (size_t)rt * p.s.w) * p.s.G;
-        float a[4], b[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = lane + 32 * e;
-          a[e] = r < rows ? __ldcg(p.nlse + at + r) : -INFINITY;
-          b[e] = r < rows ? __ldcg(p.ndelta + at + r) : 0.f;
-        }
-        if (n >= 2 && !wait(&sm.bar_st_empty[st], ((n >> 1) - 1) & 1)) break;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sm.nlse[st][lane + 32 * e] = a[e];
-          sm.ndelta[st][lane + 32 * e] = b[e];
-        }
-        warp_arrive(&sm.bar_st_full[st]);
-      }
     }
   } else {
     // ---------------- thread r of group g: key r of the tile, columns [32 g, 32 g + 32)
@@ -396,11 +415,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Tiles t(sm.ring, abort);
     const uint64_t a2 = f2(p.alpha, p.alpha);
     for (uint32_t n = 0; ok && t.valid; t.next(), ++n) {
-      const uint32_t st = n & 1;
       // causal: columns of tokens before the key are masked
       const int key = t.s.i * kTile + r, ahead = p.s.causal ? key - tile_of(t) * p.s.w : 0;
       const int mask = min(ahead, kTile) * p.s.G - 32 * g;  // the group's columns before it
-      ok = wait(&sm.bar_st_full[st], (n >> 1) & 1) && wait(&sm.bar_s[0], n & 1);
+      ok = wait(&sm.bar_s[0], n & 1);
       if (!ok) break;
       tc_fence_after();
       uint32_t sv[32];
@@ -413,18 +431,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint32_t w[16];
 #pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 nl = *reinterpret_cast<const float4*>(&sm.nlse[st][32 * g + e]);
-        float u[4];
-        f2split(ffma2(f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), a2, f2(nl.x, nl.y)), u[0], u[1]);
-        f2split(ffma2(f2(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])), a2, f2(nl.z, nl.w)), u[2], u[3]);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          u[y] = ex2(u[y]);
-          sv[e + y] = __float_as_uint(u[y]);
-        }
-        w[e >> 1] = bf2(u[0], u[1]);
-        w[(e >> 1) + 1] = bf2(u[2], u[3]);
+      for (int e = 0; e < 32; e += 2) {
+        float x, y;
+        f2split(fmul2(f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), a2), x, y);
+        x = ex2(x), y = ex2(y);
+        sv[e] = __float_as_uint(x), sv[e + 1] = __float_as_uint(y);
+        w[e >> 1] = bf2(x, y);
       }
       tmem_st16(s_col, w);
       tmem_st_wait();
@@ -437,23 +449,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(dp_col, dv);
       tmem_wait32(dv);
 #pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 nd = *reinterpret_cast<const float4*>(&sm.ndelta[st][32 * g + e]);
+      for (int e = 0; e < 32; e += 2) {
         float x, y;
-        f2split(fmul2(fadd2(f2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), f2(nd.x, nd.y)),
-                      f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]))),
-                x, y);
+        f2split(fmul2(f2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]))), x, y);
         w[e >> 1] = bf2(x, y);
-        f2split(fmul2(fadd2(f2(__uint_as_float(dv[e + 2]), __uint_as_float(dv[e + 3])), f2(nd.z, nd.w)),
-                      f2(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]))),
-                x, y);
-        w[(e >> 1) + 1] = bf2(x, y);
       }
       tmem_st16(dp_col, w);
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&sm.bar_ds);
-      warp_arrive(&sm.bar_st_empty[st]);
       if (!t.last) continue;
       // ---- the unit's sums: groups 0 and 1 half of dK's channels each, groups 2 and 3 of dV's
       ok = wait(&sm.bar_acc, units++ & 1);
@@ -628,7 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int h = 0; h < kAtoms; ++h)
                           tma_load_3d(tile + h * kAtom, tm_x, h * 64, t.s.at + t.j * kTile, t.s.hk, bar);
-                      });
+                      },
+                      [](int, int) {});
         if (++st == stages) st = 0, ++round;
       }
       // (copies in flight after a wait that ran out)
@@ -769,10 +774,11 @@ int launch_packed_bwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V
   const PackedShape s = packed_shape(cu, ws, T, S, H, Hkv, causal);
   float* nlse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.stats);
   float* ndelta = nlse + (size_t)T * H;
-  const PreParams pre{s, O, dO, LSE, nlse, ndelta};
+  uint4* more = reinterpret_cast<uint4*>(ndelta + (size_t)T * H + ((4 - 2 * (size_t)T * H % 4) & 3));
+  const PreParams pre{s, O, dO, LSE, nlse, ndelta, more, sm_scale};
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.part);
-  const BwdParams dkv{s, nlse, ndelta, dK, dV, part, sm_scale * kLog2e, sm_scale};
-  const BwdParams dq{s, nlse, ndelta, dQ, dQ, part + (size_t)2 * kMaxParts * 2 * kTile * D, sm_scale * kLog2e, sm_scale};
+  const BwdParams dkv{s, nlse, ndelta, more, dK, dV, part, sm_scale * kLog2e, sm_scale};
+  const BwdParams dq{s, nlse, ndelta, more, dQ, dQ, part + (size_t)2 * kMaxParts * 2 * kTile * D, sm_scale * kLog2e, sm_scale};
   ScopedTimer timer("packed_bwd", st);
   return D == 128 ? launch<128>(dkv, dq, pre, Q, K, V, H, sms, st) : launch<64>(dkv, dq, pre, Q, K, V, H, sms, st);
 }

@@ -456,7 +456,7 @@ PackedWs packed_ws_layout(int T, int, int H, int, int D, bool backward) {
   l.part = kHeader * sizeof(int);
   // (the backward's are dK, dV and dQ of 128 rows each)
   l.stats = l.part + up((size_t)2 * kMaxParts * kTile * (backward ? 3 * D : 2 * (D + 2)) * sizeof(float));
-  l.total = l.stats + (backward ? up((size_t)T * H * 2 * sizeof(float)) : 0);
+  l.total = l.stats + (backward ? up((size_t)T * H * (2 * sizeof(float) + 16) + 16) : 0);
   return l;
 }
 
