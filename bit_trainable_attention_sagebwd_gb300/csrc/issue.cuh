@@ -47,7 +47,21 @@ __device__ __forceinline__ void issue_ts_x4(uint32_t d, uint32_t a, uint64_t b, 
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// the same with A's columns in two pairs, 32 apart
+// S: D[tmem] (+)= A[tmem] * B[smem]^T, four along K: B's descriptor moves by 32 bytes
+__device__ __forceinline__ void issue_ts_x4_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred e, p, q;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n"
+      " elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n setp.eq.b32 q, %4, %4;\n"
+      " add.s32 a1, %1, 8;\n add.s32 a2, %1, 16;\n add.s32 a3, %1, 24;\n"
+      " add.s64 b1, %2, 2;\n add.s64 b2, %2, 4;\n add.s64 b3, %2, 6;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+// (of O) the same with A's columns in two pairs, 32 apart
 __device__ __forceinline__ void issue_ts_x4_pairs(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred e, p, q;\n .reg .b64 b1, b2, b3;\n .reg .b32 a1, a2, a3;\n"

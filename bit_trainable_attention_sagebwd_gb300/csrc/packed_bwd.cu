@@ -10,8 +10,9 @@
 // set the pace), none are cleared and converted, and the gradients are the same bits every time.
 //
 // The two main kernels are alike.  One CTA an SM walks its units (packed.cuh):
-//  - warp 19 walks, warp 17 (in packed_dq 18 too) brings the operands by TMA;
-//  - warp 16 issues the products (bf16 operands, fp32 accumulators in TMEM);
+//  - warp 19 walks, warp 17 brings the operands by TMA;
+//  - warps 16 and 18 issue the products (bf16 operands, fp32 accumulators in TMEM): one alone spends more time on its
+//    waits than the products leave it;
 //  - warps 0-15 turn S into P and dP into dS, each group of four 32 of the tile's columns; P and dS go back to TMEM as
 //    bf16 over the columns that they come from and are the A operands of the products that take them.
 // While the warps compute, the products of the tile before and after run: P(i) lets dV(i) and S(i + 1) in, dS(i) lets
@@ -28,7 +29,7 @@ namespace sage {
 namespace {
 
 constexpr int kWorkWarps = 16, kWarps = kWorkWarps + 4, kThreads = 32 * kWarps;  // (five a scheduler: 96 registers a thread)
-constexpr int kIssuer = 16, kLoader = 17, kWalker = 19;  // (18: a second loader, in packed_dq)
+constexpr int kIssuer = 16, kLoader = 17, kSecond = 18, kWalker = 19;  // kSecond: the second issuer
 constexpr uint32_t kCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -36,6 +37,7 @@ struct BwdParams {
   PackedShape s;
   const float *nlse, *ndelta;  // [Hkv][T][G]: -LSE log2 e, -delta (packed_dq)
   const uint4* more;           // [Hkv][T][G]: the same as further channels of Q and dO (packed_dkv)
+  sage_rows dout;              // packed_dq
   sage_rows d0, d1;            // packed_dkv: dK, dV; packed_dq: dQ
   float* part;                 // of each worker two places: [D / 4][128] sums of four channels of d0, and of d1
   float alpha, sm_scale;       // alpha: sm_scale log2 e
@@ -120,15 +122,15 @@ __global__ void __launch_bounds__(256) packed_pre_kernel(const PreParams p) {
 // ------------------------------------------------------------------ shared memory
 template <int D, int XS, int YS>
 struct BwdSmem {
-  uint8_t a[2][kTile * D * 2];   // the unit's own tiles: packed_dkv K and V, packed_dq Q and dO
   uint8_t x[XS][kTile * D * 2];  // what the unit walks over: Q, or K
   uint8_t y[YS][kTile * D * 2];  // dO, or V
+  uint8_t a[XS == 2 ? 2 : 1][kTile * D * 2];  // the unit's own tiles: packed_dkv K and V, packed_dq Q
   // packed_dkv: the further channels of the tiles walked over, and ones in the places of LSE's and of delta's; 16 channels
   // unswizzled, the first eight of 128 rows, then the others (zeros)
   __align__(128) uint8_t more[XS == 2 ? 2 : 1][XS == 2 ? kTile * 32 : 16];
   __align__(128) uint8_t ones[2][XS == 2 ? kTile * 32 : 16];
   uint64_t bar_a_full[2], bar_a_empty[2], bar_x_full[XS], bar_x_empty[XS], bar_y_full[YS], bar_y_empty[YS], bar_raw[2];
-  uint64_t bar_s[2], bar_dp, bar_p, bar_ds, bar_acc, bar_acc_read;
+  uint64_t bar_s[2], bar_dp, bar_p, bar_ds, bar_acc, bar_acc_read, bar_s_read, bar_dp_read, bar_ds_free;
   FeedRing ring;
   Meeting meeting;
   long long wsum[kWarps];
@@ -136,13 +138,13 @@ struct BwdSmem {
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(BwdSmem<128, 2, 2>) + 1024 <= 227 * 1024 && sizeof(BwdSmem<128, 3, 1>) + 1024 <= 227 * 1024,
+static_assert(sizeof(BwdSmem<128, 2, 2>) + 1024 <= 227 * 1024 && sizeof(BwdSmem<128, 3, 2>) + 1024 <= 227 * 1024,
               "shared memory of a CTA");
 
 template <int D, int XS, int YS>
 __device__ __forceinline__ void init_barriers(BwdSmem<D, XS, YS>& sm, int readers) {
   for (int t = 0; t < 2; ++t) {
-    mbar_init(&sm.bar_a_full[t], 1);
+    mbar_init(&sm.bar_a_full[t], XS == 3 && t == 1 ? kWorkWarps : 1);  // (packed_dq's dO comes through the work warps)
     mbar_init(&sm.bar_a_empty[t], 1);
     mbar_init(&sm.bar_raw[t], 1);
     mbar_init(&sm.bar_s[t], 1);
@@ -153,15 +155,18 @@ __device__ __forceinline__ void init_barriers(BwdSmem<D, XS, YS>& sm, int reader
   }
   for (int t = 0; t < YS; ++t) {
     mbar_init(&sm.bar_y_full[t], 1);
-    mbar_init(&sm.bar_y_empty[t], 1);
+    mbar_init(&sm.bar_y_empty[t], XS == 2 ? 2 : 1);  // (packed_dkv: dV and dP have dO)
   }
   sm.ring.init(readers);
   sm.meeting.init(kWorkWarps);
   mbar_init(&sm.bar_dp, 1);
   mbar_init(&sm.bar_p, kWorkWarps);
   mbar_init(&sm.bar_ds, kWorkWarps);
-  mbar_init(&sm.bar_acc, 1);
+  mbar_init(&sm.bar_acc, XS == 2 ? 2 : 1);  // (packed_dkv: dV and dK)
   mbar_init(&sm.bar_acc_read, kWorkWarps);
+  mbar_init(&sm.bar_s_read, kWorkWarps);
+  mbar_init(&sm.bar_dp_read, kWorkWarps);
+  mbar_init(&sm.bar_ds_free, 1);
   sm.abort = 0;
   fence_mbar_init();
 }
@@ -232,6 +237,12 @@ struct Tiles {
   }
 };
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // columns of an A operand in TMEM, 16 bf16 each: P or dS as the four groups write them
 __device__ __forceinline__ uint32_t a_col(int k) { return 32 * (k >> 1) + 8 * (k & 1); }
 
@@ -259,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem& sm = *reinterpret_cast<Smem*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int box = p.s.G * p.s.w;  // rows of a row tile
-  if (tid == 0) init_barriers(sm, kWorkWarps + 2);
+  if (tid == 0) init_barriers(sm, kWorkWarps + 3);
   if (warp < 4 && box < kTile) zero_rows<D>(warp < 2 ? sm.x[warp] : sm.y[warp - 2], box, kTile);  // the rows that no copy brings
   for (int e = tid; e < 4 * kTile; e += kThreads) {
     // the further channels: P = 0 in rows that no copy brings; ones
@@ -290,68 +301,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto rows_of = [&](const Tiles& t, int rt) { return min(p.s.w, t.s.len - rt * p.s.w) * p.s.G; };
 
   if (warp >= kWorkWarps) {
-    if (warp == kIssuer) {
-      // ---------------- MMA issuer
-      constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_g = idesc_bf16(kTile, D, false, true);
-      constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
-      const uint64_t k_k = sdesc_sw128(smem_u32(sm.a[0]), 16, 1024), v_k = k_k + kNext;
-      const uint64_t q_k = sdesc_sw128(smem_u32(sm.x[0]), 16, 1024), do_k = sdesc_sw128(smem_u32(sm.y[0]), 16, 1024);
-      constexpr uint64_t kMore = kTile * 32 >> 4;
-      const uint64_t one_k = sdesc_none(smem_u32(sm.ones[0]), kTile * 16, 128), more_k = sdesc_none(smem_u32(sm.more[0]), kTile * 16, 128);
-      const uint64_t q_n = sdesc_sw128(smem_u32(sm.x[0]), kAtom, 1024), do_n = sdesc_sw128(smem_u32(sm.y[0]), kAtom, 1024);
+    constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_g = idesc_bf16(kTile, D, false, true);
+    constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4, kMore = kTile * 32 >> 4;
+    if (warp == kIssuer || warp == kSecond) {
+      // ---------------- MMA issuers: the first dV of a tile and S of the next one, the second dK and dP of the next one
+      const int v = warp == kSecond;
+      const uint64_t own_k = sdesc_sw128(smem_u32(sm.a[v]), 16, 1024);                              // K, or V
+      const uint64_t walked_k = sdesc_sw128(smem_u32(v ? sm.y[0] : sm.x[0]), 16, 1024);             // Q, or dO
+      const uint64_t summed = sdesc_sw128(smem_u32(v ? sm.x[0] : sm.y[0]), kAtom, 1024);            // dO, or Q
+      const uint64_t one_k = sdesc_none(smem_u32(sm.ones[v]), kTile * 16, 128), more_k = sdesc_none(smem_u32(sm.more[0]), kTile * 16, 128);
+      uint64_t *full = v ? sm.bar_y_full : sm.bar_x_full, *given = v ? sm.bar_x_empty : sm.bar_y_empty;
+      uint64_t *ready = v ? &sm.bar_dp : &sm.bar_s[0], *due = v ? &sm.bar_ds : &sm.bar_p;
+      const uint32_t d_s = tmem + (v ? cDP : cS), d_g = tmem + (v ? cDK : cDV);
       bool ok = true;
-      uint32_t units = 0;  // that S has been begun of
+      uint32_t units = 0, done = 0;
+      // S or dP
       auto issue_s = [&](const Tiles& t, uint32_t n) {
-        if (t.first) ok = ok && wait(&sm.bar_a_full[0], units & 1);
-        ok = ok && wait(&sm.bar_x_full[n & 1], (n >> 1) & 1);
+        if (t.first) ok = ok && wait(&sm.bar_a_full[v], units++ & 1);
+        ok = ok && wait(&full[n & 1], (n >> 1) & 1);
+        if (v) ok = ok && wait(&sm.bar_x_full[n & 1], (n >> 1) & 1);  // (the further channels come with Q)
         if (!ok) return;
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < kAtoms; ++h)
-          issue_ss_x4(tmem + cS, k_k + h * kAtomStep, q_k + (n & 1) * kNext + h * kAtomStep, id_s, h > 0);
-        issue_ss(tmem + cS, one_k, more_k + (n & 1) * kMore, id_s, 1);
-        commit(&sm.bar_s[0]);
-        if (t.last) commit(&sm.bar_a_empty[0]);
-      };
-      auto issue_dp = [&](const Tiles& t, uint32_t n) {
-        if (t.first) ok = ok && wait(&sm.bar_a_full[1], units++ & 1);
-        ok = ok && wait(&sm.bar_y_full[n & 1], (n >> 1) & 1);
-        if (!ok) return;
-        tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < kAtoms; ++h)
-          issue_ss_x4(tmem + cDP, v_k + h * kAtomStep, do_k + (n & 1) * kNext + h * kAtomStep, id_s, h > 0);
-        issue_ss(tmem + cDP, one_k + kMore, more_k + (n & 1) * kMore, id_s, 1);
-        commit(&sm.bar_dp);
-        if (t.last) commit(&sm.bar_a_empty[1]);
+          issue_ss_x4(d_s, own_k + h * kAtomStep, walked_k + (n & 1) * kNext + h * kAtomStep, id_s, h > 0);
+        issue_ss(d_s, one_k, more_k + (n & 1) * kMore, id_s, 1);
+        commit(ready);
+        if (v) commit(&sm.bar_y_empty[n & 1]);
+        if (t.last) commit(&sm.bar_a_empty[v]);
       };
       Tiles t(sm.ring, abort);
-      if (t.valid) {
-        issue_s(t, 0);
-        issue_dp(t, 0);
-      }
-      uint32_t done = 0;  // units
+      if (t.valid) issue_s(t, 0);
       for (uint32_t n = 0; ok && t.valid; ++n) {
         const int rows = rows_of(t, tile_of(t));
         const bool first = t.first, last = t.last;
         t.next();
-        ok = wait(&sm.bar_p, n & 1);
-        if (first && done) ok = ok && wait(&sm.bar_acc_read, (done - 1) & 1);
+        if (first && done) ok = wait(&sm.bar_acc_read, (done - 1) & 1);
+        ok = ok && wait(due, n & 1);
         if (!ok) break;
         tc_fence_after();
-        issue_rows(tmem + cDV, tmem + cS, do_n + (n & 1) * kNext, id_g, rows, !first);
-        commit(&sm.bar_y_empty[n & 1]);
-        if (t.valid) issue_s(t, n + 1);
-        ok = ok && wait(&sm.bar_ds, n & 1);
-        if (!ok) break;
-        tc_fence_after();
-        issue_rows(tmem + cDK, tmem + cDP, q_n + (n & 1) * kNext, id_g, rows, !first);
-        commit(&sm.bar_x_empty[n & 1]);
+        issue_rows(d_g, d_s, summed + (n & 1) * kNext, id_g, rows, !first);
+        commit(&given[n & 1]);
         if (last) {
           commit(&sm.bar_acc);
           ++done;
         }
-        if (t.valid) issue_dp(t, n + 1);
+        if (t.valid) issue_s(t, n + 1);
       }
     } else if (warp == kLoader) {
       // ---------------- K and V; dO and Q, in the order in which they are given back
@@ -496,20 +491,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------------ dQ
-// TMEM: S (query rows x keys), then dS, at 0 and 128 in turns; dP at 256; dQ at 384
+// TMEM: S (query rows x keys) at 0, dP at 128, dQ at 256; behind it dO, from where it is dP's A operand (in shared memory
+// it would take 32 KB of its bandwidth for each key tile), and dS.  S and dP of the next tile go in as soon as this
+// one's have been read, so the warps do not wait for them.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dq_kernel(const BwdParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do) {
+                     const __grid_constant__ CUtensorMap tm_v) {
   constexpr int kAtoms = D / 64, kAtom = kTile * 128;
   // (K's tile is held by dQ's product until dS is there, V's only by dP)
-  constexpr int kStagesK = 3, kStagesV = 1;
-  constexpr uint32_t cDP = 256, cDQ = 384;
+  constexpr int kStagesK = 3, kStagesV = 2;
+  constexpr uint32_t cS = 0, cDP = 128, cDQ = 256, cDO = cDQ + D, cDS = cDO + D / 2;
+  static_assert(cDS + 64 <= kCols, "TMEM");
   extern __shared__ uint8_t smem_raw[];
   using Smem = BwdSmem<D, kStagesK, kStagesV>;
   Smem& sm = *reinterpret_cast<Smem*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int box = p.s.G * p.s.w;
+  const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) init_barriers(sm, kWorkWarps + 3);
   // (no wait for packed_dkv, of which nothing is read: its CTAs let this kernel in once packed_pre was complete.  The wait
   // at the end keeps the order for what follows.)
@@ -530,121 +527,111 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
 
   if (warp >= kWorkWarps) {
+    constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_g = idesc_bf16(kTile, D, false, true);
+    constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
     if (warp == kIssuer) {
-      // ---------------- MMA issuer
-      constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_g = idesc_bf16(kTile, D, false, true);
-      constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
-      const uint64_t q_k = sdesc_sw128(smem_u32(sm.a[0]), 16, 1024), do_k = q_k + kNext;
+      // ---------------- MMA issuer of S and dP
       const uint64_t k_k = sdesc_sw128(smem_u32(sm.x[0]), 16, 1024), v_k = sdesc_sw128(smem_u32(sm.y[0]), 16, 1024);
-      const uint64_t k_n = sdesc_sw128(smem_u32(sm.x[0]), kAtom, 1024);
+      const uint64_t q_k = sdesc_sw128(smem_u32(sm.a[0]), 16, 1024);
       bool ok = true;
-      uint32_t units_s = 0, units_dp = 0, ns = 0;
-      Turn<kStagesK> kt;                 // K's stage of S and of dQ
-      uint32_t kq = 0;
+      Turn<kStagesK> kt;
       Turn<kStagesV> vt;
-      auto issue_s = [&](const Tiles& t) {
-        const uint32_t n = ns++;
-        if (t.first) ok = ok && wait(&sm.bar_a_full[0], units_s++ & 1);
+      uint32_t units = 0, n = 0;
+      for (Tiles t(sm.ring, abort); t.valid; t.next(), ++n) {
+        if (t.first) ok = ok && wait(&sm.bar_a_full[0], units & 1);
         ok = ok && wait(&sm.bar_x_full[kt.at], kt.round & 1);
-        if (!ok) return;
+        if (n > 0) ok = ok && wait(&sm.bar_s_read, (n - 1) & 1);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < kAtoms; ++h)
-          issue_ss_x4(tmem + (n & 1) * 128, q_k + h * kAtomStep, k_k + kt.at * kNext + h * kAtomStep, id_s, h > 0);
-        kt.next();
-        commit(&sm.bar_s[n & 1]);
+          issue_ss_x4(tmem + cS, q_k + h * kAtomStep, k_k + kt.at * kNext + h * kAtomStep, id_s, h > 0);
+        commit(&sm.bar_s[0]);
         if (t.last) commit(&sm.bar_a_empty[0]);
-      };
-      auto issue_dp = [&](bool first, bool last) {
-        if (first) ok = ok && wait(&sm.bar_a_full[1], units_dp++ & 1);
+        kt.next();
+        if (t.first) ok = wait(&sm.bar_a_full[1], units++ & 1);
         ok = ok && wait(&sm.bar_y_full[vt.at], vt.round & 1);
-        if (!ok) return;
+        if (n > 0) ok = ok && wait(&sm.bar_dp_read, (n - 1) & 1);
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < kAtoms; ++h)
-          issue_ss_x4(tmem + cDP, do_k + h * kAtomStep, v_k + vt.at * kNext + h * kAtomStep, id_s, h > 0);
+          issue_ts_x4_rows(tmem + cDP, tmem + cDO + 32 * h, v_k + vt.at * kNext + h * kAtomStep, id_s, h > 0);
         commit(&sm.bar_dp);
         commit(&sm.bar_y_empty[vt.at]);
         vt.next();
-        if (last) commit(&sm.bar_a_empty[1]);
-      };
-      // the tile whose dS is waited for, and the one after it, whose S is issued
-      struct At {
-        bool valid = false, first = false, last = false;
-        int keys = 0;
-      } now, then;
-      Tiles t(sm.ring, abort);
-      auto take = [&](At& x) {
-        x.valid = t.valid;
-        if (!t.valid) return;
-        x.first = t.first, x.last = t.last, x.keys = min(kTile, t.s.len - t.j * kTile);
-        issue_s(t);
-        t.next();
-      };
-      take(now);
-      if (now.valid) issue_dp(now.first, now.last);
-      take(then);
-      uint32_t done = 0;
-      for (uint32_t n = 0; ok && now.valid; ++n) {
-        ok = wait(&sm.bar_ds, n & 1);
-        if (!ok) break;
-        if (then.valid) issue_dp(then.first, then.last);
-        if (now.first && done) ok = ok && wait(&sm.bar_acc_read, (done - 1) & 1);
+      }
+    } else if (warp == kSecond) {
+      // ---------------- MMA issuer of dQ
+      const uint64_t k_n = sdesc_sw128(smem_u32(sm.x[0]), kAtom, 1024);
+      bool ok = true;
+      Turn<kStagesK> kt;
+      uint32_t done = 0, n = 0;
+      for (Tiles t(sm.ring, abort); t.valid; t.next(), ++n) {
+        if (t.first && done) ok = wait(&sm.bar_acc_read, (done - 1) & 1);
+        const int keys = t.s.len - t.j * kTile;
+        const uint64_t b = k_n + kt.at * kNext;
+        ok = ok && wait(&sm.bar_x_full[kt.at], kt.round & 1) && wait(&sm.bar_ds, n & 1);
         if (!ok) break;
         tc_fence_after();
-        issue_rows(tmem + cDQ, tmem + (n & 1) * 128, k_n + kq * kNext, id_g, now.keys, !now.first);
-        commit(&sm.bar_x_empty[kq]);
-        if (++kq == kStagesK) kq = 0;
-        if (now.last) {
+        if (keys > kTile - 16) {
+          issue_ts_x4(tmem + cDQ, tmem + cDS, b, id_g, !t.first);
+          issue_ts_x4(tmem + cDQ, tmem + cDS + 32, b + (4 * 2048 >> 4), id_g, 1);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k * 16 < keys; ++k) issue_ts(tmem + cDQ, tmem + cDS + 8 * k, b + (k * 2048 >> 4), id_g, k > 0 || !t.first);
+        }
+        commit(&sm.bar_ds_free);
+        commit(&sm.bar_x_empty[kt.at]);
+        kt.next();
+        if (t.last) {
           commit(&sm.bar_acc);
           ++done;
         }
-        now = then;
-        take(then);
       }
-    } else if (warp < kWalker) {
-      // ---------------- Q and K (the first loader), dO and V (the second)
-      const int v = warp - kLoader;
-      const CUtensorMap* tm_a = v ? &tm_do : &tm_q;
-      const CUtensorMap* tm_x = v ? &tm_v : &tm_k;
-      uint64_t *full = v ? sm.bar_y_full : sm.bar_x_full, *empty = v ? sm.bar_y_empty : sm.bar_x_empty;
-      const uint32_t stages = v ? kStagesV : kStagesK;
-      uint32_t units = 0, raws = 0, st = 0, round = 0;
+    } else if (warp == kLoader) {
+      // ---------------- Q; K and V
+      Turn<kStagesK> kt;
+      Turn<kStagesV> vt;
+      uint32_t units = 0, raws[2] = {0, 0};
+      const int lane = tid & 31, box = p.s.G * p.s.w;
       bool ok = true;
       for (Tiles t(sm.ring, abort); ok && t.valid; t.next()) {
         if (t.first) {
-          ok = units == 0 || wait(&sm.bar_a_empty[v], (units - 1) & 1);
+          ok = units == 0 || wait(&sm.bar_a_empty[0], (units - 1) & 1);
           if (!ok) break;
           ++units;
           if (lane == 0) {
-            mbar_arrive_expect_tx(&sm.bar_a_full[v], box * D * 2);
+            mbar_arrive_expect_tx(&sm.bar_a_full[0], box * D * 2);
 #pragma unroll
             for (int h = 0; h < kAtoms; ++h)
-              tma_load_3d(sm.a[v] + h * kAtom, tm_a, h * 64, t.s.hk * p.s.G, t.s.at + t.s.i * p.s.w, &sm.bar_a_full[v]);
+              tma_load_3d(sm.a[0] + h * kAtom, &tm_q, h * 64, t.s.hk * p.s.G, t.s.at + t.s.i * p.s.w, &sm.bar_a_full[0]);
           }
           __syncwarp();
         }
-        ok = round == 0 || wait(&empty[st], (round - 1) & 1);
-        if (!ok) break;
-        uint8_t* tile = v ? sm.y[st] : sm.x[st];
-        ok = bring<D>(tile, min(kTile, t.s.len - t.j * kTile), kTile, kTile * D * 2, &full[st], &sm.bar_raw[v], raws, abort,
-                      [&](uint64_t* bar) {
+        auto key_tile = [&](uint8_t* tile, const CUtensorMap* tm, uint64_t* full, uint64_t* empty, uint32_t round, int v) {
+          ok = ok && (round == 0 || wait(empty, (round - 1) & 1));
+          ok = ok && bring<D>(tile, min(kTile, t.s.len - t.j * kTile), kTile, kTile * D * 2, full, &sm.bar_raw[v], raws[v], abort,
+                              [&](uint64_t* bar) {
 #pragma unroll
-                        for (int h = 0; h < kAtoms; ++h)
-                          tma_load_3d(tile + h * kAtom, tm_x, h * 64, t.s.at + t.j * kTile, t.s.hk, bar);
-                      },
-                      [](int, int) {});
-        if (++st == stages) st = 0, ++round;
+                                for (int h = 0; h < kAtoms; ++h)
+                                  tma_load_3d(tile + h * kAtom, tm, h * 64, t.s.at + t.j * kTile, t.s.hk, bar);
+                              },
+                              [](int, int) {});
+        };
+        key_tile(sm.x[kt.at], &tm_k, &sm.bar_x_full[kt.at], &sm.bar_x_empty[kt.at], kt.round, 0);
+        key_tile(sm.y[vt.at], &tm_v, &sm.bar_y_full[vt.at], &sm.bar_y_empty[vt.at], vt.round, 1);
+        if (!ok) break;
+        kt.next();
+        vt.next();
       }
       // (copies in flight after a wait that ran out)
       int give_up = 0;
-      if (units) mbar_wait(&sm.bar_a_full[v], (units - 1) & 1, &give_up);
-      for (uint32_t e = 0; e < stages; ++e) {
-        if (st == 0 && round == 0) break;
-        if (st == 0) st = stages, --round;
-        --st;
-        mbar_wait(&full[st], round & 1, &give_up);
-      }
+      if (units) mbar_wait(&sm.bar_a_full[0], (units - 1) & 1, &give_up);
+      for (uint32_t e = 0; e < kStagesK; ++e)
+        if (e < kt.at || kt.round > 0) mbar_wait(&sm.bar_x_full[e], (e < kt.at ? kt.round : kt.round - 1) & 1, &give_up);
+      for (uint32_t e = 0; e < kStagesV; ++e)
+        if (e < vt.at || vt.round > 0) mbar_wait(&sm.bar_y_full[e], (e < vt.at ? vt.round : vt.round - 1) & 1, &give_up);
     } else if (warp == kWalker) {
       feed<kRows>(p.s, sm.ring, sm.pre, group, line, idle, abort);
     }
@@ -652,29 +639,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- thread r of group g: row r of the tile, keys [32 g, 32 g + 32)
     const int g = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t dp_col = tmem + lanes + cDP + 32 * g;
+    const uint32_t s_col = tmem + lanes + cS + 32 * g, dp_col = tmem + lanes + cDP + 32 * g;
     const int token = r / p.s.G, head = r - token * p.s.G;
     bool ok = true;
-    uint32_t units = 0, joins = 0;
+    uint32_t joins = 0, units = 0;
     Tiles t(sm.ring, abort);
     const uint64_t a2 = f2(p.alpha, p.alpha);
     float nl = 0.f, nd = 0.f;
-    for (uint32_t n = 0; ok && t.valid; t.next(), ++n) {
-      const int i = t.s.i * p.s.w + token;
-      const bool live = token < p.s.w && i < t.s.len;
-      if (t.first) {
-        const size_t at = ((size_t)t.s.hk * p.s.T + t.s.at + i) * p.s.G + head;
-        nl = live ? __ldcg(p.nlse + at) : -INFINITY;
-        nd = live ? __ldcg(p.ndelta + at) : 0.f;
+    int i = 0;
+    bool live = false;
+    // The row of a unit: its terms, and the group's D / 4 channels of dO to TMEM (dP of the unit before is done: its result
+    // has been read)
+    auto begin_unit = [&]() {
+      i = t.s.i * p.s.w + token;
+      live = token < p.s.w && i < t.s.len;
+      const size_t at = ((size_t)t.s.hk * p.s.T + t.s.at + i) * p.s.G + head;
+      nl = live ? __ldcg(p.nlse + at) : -INFINITY;
+      nd = live ? __ldcg(p.ndelta + at) : 0.f;
+      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dout.p) + (long long)(t.s.at + i) * p.dout.token +
+                                                        (t.s.hk * p.s.G + head) * p.dout.head + g * (D / 4));
+      uint4 v[D / 32];
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) v[e] = live ? row[e] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int e = 0; e < D / 32; e += 2) {
+        const uint32_t w[8] = {v[e].x, v[e].y, v[e].z, v[e].w, v[e + 1].x, v[e + 1].y, v[e + 1].z, v[e + 1].w};
+        tmem_st8(tmem + lanes + cDO + g * (D / 8) + 4 * e, w);
       }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&sm.bar_a_full[1]);
+    };
+    if (t.valid) begin_unit();
+    for (uint32_t n = 0; ok && t.valid; ++n) {
       const int left = (live && p.s.causal ? i + 1 : t.s.len) - t.j * kTile - 32 * g;  // keys that the row sees
-      const uint32_t s_col = tmem + lanes + (n & 1) * 128 + 32 * g;
-      ok = wait(&sm.bar_s[n & 1], (n >> 1) & 1);
+      ok = wait(&sm.bar_s[0], n & 1);
       if (!ok) break;
       tc_fence_after();
       uint32_t sv[32];
       tmem_ld32(s_col, sv);
       tmem_wait32(sv);
+      tc_fence_before();
+      warp_arrive(&sm.bar_s_read);
       if (__any_sync(0xffffffffu, left < 32)) {
 #pragma unroll
         for (int e = 0; e < 32; ++e)
@@ -694,6 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t dv[32], w[16];
       tmem_ld32(dp_col, dv);
       tmem_wait32(dv);
+      tc_fence_before();
+      warp_arrive(&sm.bar_dp_read);
 #pragma unroll
       for (int e = 0; e < 32; e += 2) {
         float x, y;
@@ -702,34 +710,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x, y);
         w[e >> 1] = bf2(x, y);
       }
-      tmem_st16(s_col, w);
+      if (n > 0) ok = wait(&sm.bar_ds_free, (n - 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_st16(tmem + lanes + cDS + 16 * g, w);
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&sm.bar_ds);
-      if (!t.last) continue;
+      const bool last = t.last;
+      const Part s = t.s;
+      const int row_i = i;
+      const bool was_live = live;
+      t.next();
+      if (!last) continue;
+      if (t.valid) begin_unit();
       // ---- the unit's sums, 32 channels a group (D = 64: the first two)
       ok = wait(&sm.bar_acc, units++ & 1);
       if (!ok) break;
       tc_fence_after();
       const int d = 32 * g;
-      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(p.d0.p) + (long long)(t.s.at + i) * p.d0.token +
-                           (t.s.hk * p.s.G + head) * p.d0.head + d;
-      const bool whole = t.s.whole();
+      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(p.d0.p) + (long long)(s.at + row_i) * p.d0.token +
+                           (s.hk * p.s.G + head) * p.d0.head + d;
+      const bool whole = s.whole();
       if (d < D) {
         uint32_t o[32];
         tmem_ld32(tmem + lanes + cDQ + d, o);
         tmem_wait32(o);
-        if (whole && live) store_row(row, reinterpret_cast<const float(&)[32]>(o), p.sm_scale);
-        if (!whole) store_sums(p.part + (size_t)t.s.place() * kTile * D, d, r, o);
+        if (whole && was_live) store_row(row, reinterpret_cast<const float(&)[32]>(o), p.sm_scale);
+        if (!whole) store_sums(p.part + (size_t)s.place() * kTile * D, d, r, o);
       }
       tc_fence_before();
       warp_arrive(&sm.bar_acc_read);
-      if (whole || !sm.meeting.was_last(p.s.status + kRowCounters + 2 * t.s.first(), t.s.parts(), joins++, warp == 0, abort, ok)) continue;
+      if (whole || !sm.meeting.was_last(p.s.status + kRowCounters + 2 * s.first(), s.parts(), joins++, warp == 0, abort, ok)) continue;
       if (d < D) {
         float o[32] = {};
 #pragma unroll 1
-        for (int k = 0; k < t.s.parts(); ++k) add_sums(p.part + (size_t)t.s.place(k) * kTile * D, d, r, 1.f, o);
-        if (live) store_row(row, o, p.sm_scale);
+        for (int k = 0; k < s.parts(); ++k) add_sums(p.part + (size_t)s.place(k) * kTile * D, d, r, 1.f, o);
+        if (was_live) store_row(row, o, p.sm_scale);
       }
     }
   }
@@ -747,7 +764,7 @@ int launch(const BwdParams& dkv, const BwdParams& dq, const PreParams& pre, cons
   if (!make_tmap_queries(&tq, Q, D, H, dkv.s) || !make_tmap_keys(&tk, K, D, dkv.s) || !make_tmap_keys(&tv, V, D, dkv.s) ||
       !make_tmap_queries(&to, pre.dO, D, H, dkv.s))
     return SAGE_ERR_CUDA;
-  const size_t smem = sizeof(BwdSmem<D, 2, 2>) + 1024, smem_q = sizeof(BwdSmem<D, 3, 1>) + 1024;
+  const size_t smem = sizeof(BwdSmem<D, 2, 2>) + 1024, smem_q = sizeof(BwdSmem<D, 3, 2>) + 1024;
   if (cudaFuncSetAttribute(packed_dkv_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
       cudaFuncSetAttribute(packed_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_q) != cudaSuccess)
     return SAGE_ERR_CUDA;
@@ -757,7 +774,7 @@ int launch(const BwdParams& dkv, const BwdParams& dq, const PreParams& pre, cons
   const int grid = sms < kMaxParts ? sms : kMaxParts;
   if (launch_pdl(packed_pre_kernel<D>, dim3((unsigned)blocks), dim3(256), 0, st, pre) != cudaSuccess ||
       launch_pdl(packed_dkv_kernel<D>, dim3(grid), dim3(kThreads), smem, st, dkv, tq, tk, tv, to) != cudaSuccess ||
-      launch_pdl(packed_dq_kernel<D>, dim3(grid), dim3(kThreads), smem_q, st, dq, tq, tk, tv, to) != cudaSuccess)
+      launch_pdl(packed_dq_kernel<D>, dim3(grid), dim3(kThreads), smem_q, st, dq, tq, tk, tv) != cudaSuccess)
     return SAGE_ERR_CUDA;
   return SAGE_OK;
 }
@@ -777,8 +794,8 @@ int launch_packed_bwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V
   uint4* more = reinterpret_cast<uint4*>(ndelta + (size_t)T * H + ((4 - 2 * (size_t)T * H % 4) & 3));
   const PreParams pre{s, O, dO, LSE, nlse, ndelta, more, sm_scale};
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.part);
-  const BwdParams dkv{s, nlse, ndelta, more, dK, dV, part, sm_scale * kLog2e, sm_scale};
-  const BwdParams dq{s, nlse, ndelta, more, dQ, dQ, part + (size_t)2 * kMaxParts * 2 * kTile * D, sm_scale * kLog2e, sm_scale};
+  const BwdParams dkv{s, nlse, ndelta, more, dO, dK, dV, part, sm_scale * kLog2e, sm_scale};
+  const BwdParams dq{s, nlse, ndelta, more, dO, dQ, dQ, part + (size_t)2 * kMaxParts * 2 * kTile * D, sm_scale * kLog2e, sm_scale};
   ScopedTimer timer("packed_bwd", st);
   return D == 128 ? launch<128>(dkv, dq, pre, Q, K, V, H, sms, st) : launch<64>(dkv, dq, pre, Q, K, V, H, sms, st);
 }
