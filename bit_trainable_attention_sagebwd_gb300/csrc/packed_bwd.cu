@@ -406,12 +406,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + cS + 32 * g, dp_col = tmem + lanes + cDP + 32 * g;
     bool ok = true;
-    uint32_t units = 0, joins = 0;
-    Tiles t(sm.ring, abort);
+    uint32_t units = 0, joins = 0, n = 0;
+    Feed parts(sm.ring, abort);
+    Part s;
     const uint64_t a2 = f2(p.alpha, p.alpha);
-    for (uint32_t n = 0; ok && t.valid; t.next(), ++n) {
-      // causal: columns of tokens before the key are masked
-      const int key = t.s.i * kTile + r, ahead = p.s.causal ? key - tile_of(t) * p.s.w : 0;
+    while (ok && parts.next(s)) {
+    const int key = s.i * kTile + r;
+    // causal: columns of tokens before the key are masked
+    int ahead = p.s.causal ? key - (Units<kKeys>(p.s, s.len).first(s.i) + s.c0) * p.s.w : 0;
+#pragma unroll 1
+    for (int j = s.c0; j < s.c1; ++j, ++n, ahead -= p.s.w) {
       const int mask = min(ahead, kTile) * p.s.G - 32 * g;  // the group's columns before it
       ok = wait(&sm.bar_s[0], n & 1);
       if (!ok) break;
@@ -453,15 +457,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&sm.bar_ds);
-      if (!t.last) continue;
+    }
       // ---- the unit's sums: groups 0 and 1 half of dK's channels each, groups 2 and 3 of dV's
-      ok = wait(&sm.bar_acc, units++ & 1);
+      ok = ok && wait(&sm.bar_acc, units++ & 1);
       if (!ok) break;
       tc_fence_after();
-      const bool live = key < t.s.len, whole = t.s.whole();
+      const bool live = key < s.len, whole = s.whole();
       const int x = g >> 1, d0 = (g & 1) * (D / 2);
       const sage_rows& to = x ? p.d1 : p.d0;
-      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(to.p) + (long long)(t.s.at + key) * to.token + t.s.hk * to.head;
+      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(to.p) + (long long)(s.at + key) * to.token + s.hk * to.head;
       auto part_of = [&](int place) { return p.part + (size_t)(2 * place + x) * kTile * D; };
       const float f = x ? 1.f : p.sm_scale;
 #pragma unroll 1
@@ -470,16 +474,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tmem + lanes + (x ? cDV : cDK) + d, o);
         tmem_wait32(o);
         if (whole && live) store_row(row + d, reinterpret_cast<const float(&)[32]>(o), f);
-        if (!whole) store_sums(part_of(t.s.place()), d, r, o);
+        if (!whole) store_sums(part_of(s.place()), d, r, o);
       }
       tc_fence_before();
       warp_arrive(&sm.bar_acc_read);
-      if (whole || !sm.meeting.was_last(p.s.status + kKeyCounters + 2 * t.s.first(), t.s.parts(), joins++, warp == 0, abort, ok)) continue;
+      if (whole || !sm.meeting.was_last(p.s.status + kKeyCounters + 2 * s.first(), s.parts(), joins++, warp == 0, abort, ok)) continue;
 #pragma unroll 1
       for (int d = d0; d < d0 + D / 2; d += 32) {
         float o[32] = {};
 #pragma unroll 1
-        for (int k = 0; k < t.s.parts(); ++k) add_sums(part_of(t.s.place(k)), d, r, 1.f, o);
+        for (int k = 0; k < s.parts(); ++k) add_sums(part_of(s.place(k)), d, r, 1.f, o);
         if (live) store_row(row + d, o, f);
       }
     }
@@ -642,8 +646,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_col = tmem + lanes + cS + 32 * g, dp_col = tmem + lanes + cDP + 32 * g;
     const int token = r / p.s.G, head = r - token * p.s.G;
     bool ok = true;
-    uint32_t joins = 0, units = 0;
-    Tiles t(sm.ring, abort);
+    uint32_t joins = 0, units = 0, n = 0;
+    Feed parts(sm.ring, abort);
+    Part s;
     const uint64_t a2 = f2(p.alpha, p.alpha);
     float nl = 0.f, nd = 0.f;
     int i = 0;
@@ -651,13 +656,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The row of a unit: its terms, and the group's D / 4 channels of dO to TMEM (dP of the unit before is done: its result
     // has been read)
     auto begin_unit = [&]() {
-      i = t.s.i * p.s.w + token;
-      live = token < p.s.w && i < t.s.len;
-      const size_t at = ((size_t)t.s.hk * p.s.T + t.s.at + i) * p.s.G + head;
+      i = s.i * p.s.w + token;
+      live = token < p.s.w && i < s.len;
+      const size_t at = ((size_t)s.hk * p.s.T + s.at + i) * p.s.G + head;
       nl = live ? __ldcg(p.nlse + at) : -INFINITY;
       nd = live ? __ldcg(p.ndelta + at) : 0.f;
-      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dout.p) + (long long)(t.s.at + i) * p.dout.token +
-                                                        (t.s.hk * p.s.G + head) * p.dout.head + g * (D / 4));
+      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dout.p) + (long long)(s.at + i) * p.dout.token +
+                                                        (s.hk * p.s.G + head) * p.dout.head + g * (D / 4));
       uint4 v[D / 32];
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) v[e] = live ? row[e] : make_uint4(0u, 0u, 0u, 0u);
@@ -670,9 +675,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       warp_arrive(&sm.bar_a_full[1]);
     };
-    if (t.valid) begin_unit();
-    for (uint32_t n = 0; ok && t.valid; ++n) {
-      const int left = (live && p.s.causal ? i + 1 : t.s.len) - t.j * kTile - 32 * g;  // keys that the row sees
+    bool more = parts.next(s);
+    if (more) begin_unit();
+    while (ok && more) {
+    int left = (live && p.s.causal ? i + 1 : s.len) - s.c0 * kTile - 32 * g;  // keys that the row sees
+#pragma unroll 1
+    for (int j = s.c0; j < s.c1; ++j, ++n, left -= kTile) {
       ok = wait(&sm.bar_s[0], n & 1);
       if (!ok) break;
       tc_fence_after();
@@ -717,35 +725,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&sm.bar_ds);
-      const bool last = t.last;
-      const Part s = t.s;
+    }
+      if (!ok) break;
+      const Part done = s;
       const int row_i = i;
       const bool was_live = live;
-      t.next();
-      if (!last) continue;
-      if (t.valid) begin_unit();
+      more = parts.next(s);
+      if (more) begin_unit();
       // ---- the unit's sums, 32 channels a group (D = 64: the first two)
       ok = wait(&sm.bar_acc, units++ & 1);
       if (!ok) break;
       tc_fence_after();
       const int d = 32 * g;
-      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(p.d0.p) + (long long)(s.at + row_i) * p.d0.token +
-                           (s.hk * p.s.G + head) * p.d0.head + d;
-      const bool whole = s.whole();
+      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(p.d0.p) + (long long)(done.at + row_i) * p.d0.token +
+                           (done.hk * p.s.G + head) * p.d0.head + d;
+      const bool whole = done.whole();
       if (d < D) {
         uint32_t o[32];
         tmem_ld32(tmem + lanes + cDQ + d, o);
         tmem_wait32(o);
         if (whole && was_live) store_row(row, reinterpret_cast<const float(&)[32]>(o), p.sm_scale);
-        if (!whole) store_sums(p.part + (size_t)s.place() * kTile * D, d, r, o);
+        if (!whole) store_sums(p.part + (size_t)done.place() * kTile * D, d, r, o);
       }
       tc_fence_before();
       warp_arrive(&sm.bar_acc_read);
-      if (whole || !sm.meeting.was_last(p.s.status + kRowCounters + 2 * s.first(), s.parts(), joins++, warp == 0, abort, ok)) continue;
+      if (whole || !sm.meeting.was_last(p.s.status + kRowCounters + 2 * done.first(), done.parts(), joins++, warp == 0, abort, ok)) continue;
       if (d < D) {
         float o[32] = {};
 #pragma unroll 1
-        for (int k = 0; k < s.parts(); ++k) add_sums(p.part + (size_t)s.place(k) * kTile * D, d, r, 1.f, o);
+        for (int k = 0; k < done.parts(); ++k) add_sums(p.part + (size_t)done.place(k) * kTile * D, d, r, 1.f, o);
         if (was_live) store_row(row, o, p.sm_scale);
       }
     }
