@@ -7,8 +7,8 @@
 //   kPairs  two row tiles against the key tiles that they see     (the forward)
 //   kRows   one row tile against the same                         (dQ)
 //   kKeys   one key tile (128 keys) against the row tiles that see it  (dK, dV)
-// The units of a sequence follow each other, key/value head by head.  Every unit counts the tokens that it sees and
-// kUnitCost more, so that the line of all units can be cut into equal shares of time.  One warp of a CTA walks its
+// The units of a sequence follow each other, key/value head by head.  Every unit counts the tokens that it sees
+// (kKeys: `per` times) and kUnitCost more, so that the line of all units can be cut into equal shares of time.  One warp of a CTA walks its
 // share and hands the parts to the others (Feed).
 #pragma once
 
@@ -27,8 +27,9 @@ struct PackedShape {
   const int* cu;
   int* status;
   int T, S, Hkv, G, w, causal;
-  unsigned inv_w;  // 2^32 / w, rounded up (w > 1)
-  __device__ __forceinline__ int over_w(int n) const { return w > 1 ? (int)__umulhi((unsigned)n, inv_w) : n; }  // n / w
+  int per;                  // kKeys: places a token, so that a row tile counts about what a key tile does
+  unsigned inv_w, inv_pw;  // 2^32 / w, rounded up (w > 1); the same of per w
+  __device__ __forceinline__ int over_w(int n) const { return w > 1 ? (int)__umulhi((unsigned)n, inv_w) : n; }  // n / w, n < 2^25
 };
 
 namespace {  // internal linkage: each translation unit keeps its own copy
@@ -75,13 +76,15 @@ struct Units {
     return ((p.causal ? min(len, (i + 1) * u) : len) + kTile - 1) / kTile;
   }
   // places of the line before unit i, and its own (tokens as if every unit were whole; below 2^50)
+  __device__ __forceinline__ int per() const { return KIND == kKeys ? p.per : 1; }
   __device__ __forceinline__ long long before(int i) const {
-    if (!p.causal) return (long long)i * (len + kUnitCost);
-    if (KIND == kKeys) return (long long)i * (len + kUnitCost) - (long long)i * (i - 1) / 2 * kTile;
+    const long long all = (long long)i * ((long long)len * per() + kUnitCost);
+    if (!p.causal) return all;
+    if (KIND == kKeys) return all - (long long)i * (i - 1) / 2 * (kTile * per());
     return (long long)i * (i + 1) / 2 * u + (long long)i * kUnitCost;
   }
-  __device__ __forceinline__ int own(int i) const {
-    return kUnitCost + (!p.causal ? len : KIND == kKeys ? len - i * kTile : (i + 1) * u);
+  __device__ __forceinline__ long long own(int i) const {
+    return kUnitCost + (long long)(!p.causal ? len : KIND == kKeys ? len - i * kTile : (i + 1) * u) * per();
   }
   __device__ __forceinline__ long long total() const { return before(count()); }
   // the unit that holds place x of a head: the root of before(i) = x, put right
@@ -89,10 +92,10 @@ struct Units {
     const float c = kUnitCost, f = (float)x;
     float i;
     if (!p.causal) {
-      i = f / ((float)len + c);
+      i = f / ((float)len * per() + c);
     } else if (KIND == kKeys) {
-      const float a = (float)len + c + kTile / 2;
-      i = (a - sqrtf(fmaxf(0.f, a * a - 2 * kTile * f))) / kTile;
+      const float t = kTile * per(), a = (float)len * per() + c + t / 2;
+      i = (a - sqrtf(fmaxf(0.f, a * a - 2 * t * f))) / t;
     } else {
       const float a = (float)u / 2 + c;
       i = (sqrtf(fmaf(a, a, 2 * (float)u * f)) - a) / (float)u;
@@ -106,7 +109,8 @@ struct Units {
   // its way through memory and the join
   __device__ __forceinline__ int cut(long long off, int n) const {
     if (off <= 0) return 0;
-    const int c = off >= (1 << 25) ? n : KIND == kKeys ? p.over_w((int)off) : (int)off / kTile;
+    const int c = KIND != kKeys ? (int)min(off / kTile, (long long)n)
+                  : off < (1 << 25) ? (int)__umulhi((unsigned)off, p.inv_pw) : (int)min(off / (p.per * p.w), (long long)n);
     return c >= n - kSnap ? n : c <= kSnap ? 0 : c;
   }
   static constexpr int kSnap = 2;
@@ -371,8 +375,9 @@ __device__ __forceinline__ void prefix_of_sequences(const PackedShape& p, int gr
 
 inline PackedShape packed_shape(const int* cu, void* ws, int T, int S, int H, int Hkv, int causal) {
   const int G = H / Hkv;
-  const int w = kTile / G;
-  return PackedShape{cu, static_cast<int*>(ws), T, S, Hkv, G, w, causal, w > 1 ? (unsigned)(((1ull << 32) + w - 1) / w) : 0u};
+  const int w = kTile / G, per = kTile / w;
+  auto inverse = [](int n) { return n > 1 ? (unsigned)(((1ull << 32) + n - 1) / n) : 0u; };
+  return PackedShape{cu, static_cast<int*>(ws), T, S, Hkv, G, w, causal, per, inverse(w), inverse(per * w)};
 }
 
 // Row tiles of queries: w tokens of the G heads of a key/value head, 64 channels

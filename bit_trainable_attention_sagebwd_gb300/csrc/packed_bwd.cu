@@ -80,25 +80,28 @@ template <int D>
 __global__ void __launch_bounds__(256) packed_pre_kernel(const PreParams p) {
   constexpr int kLanes = D / 8, kRows = 4, kStep = 256 / kLanes;  // rows of a thread, and between them
   const int tid = threadIdx.x, lane = tid % kLanes, H = p.s.Hkv * p.s.G;
-  const long long rows = (long long)p.s.T * H;
-  const long long r0 = (long long)blockIdx.x * (kStep * kRows) + tid / kLanes;
+  const long long r0 = (long long)blockIdx.x * (kStep * kRows);
+  const int t0 = (int)(r0 / H), h0 = (int)(r0 - (long long)t0 * H);  // the block's first row
   pdl_wait();
   pdl_trigger();
   uint4 a[kRows], b[kRows];
+  int ts[kRows], hs[kRows];
 #pragma unroll
   for (int x = 0; x < kRows; ++x) {
-    const long long r = r0 + x * kStep;
-    if (r < rows) {
-      const int t = (int)(r / H), h = (int)(r - (long long)t * H);
+    const int n = h0 + x * kStep + tid / kLanes;
+    const int t = t0 + n / H, h = n % H;
+    ts[x] = t, hs[x] = h;
+    a[x] = b[x] = make_uint4(0u, 0u, 0u, 0u);
+    if (t < p.s.T) {
       a[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.O.p) + t * p.O.token + h * p.O.head) + lane);
       b[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dO.p) + t * p.dO.token + h * p.dO.head) + lane);
     }
   }
 #pragma unroll
   for (int x = 0; x < kRows; ++x) {
-    const long long r = r0 + x * kStep;
+    const int t = ts[x], h = hs[x];
     float s = 0.f;
-    if (r < rows) {
+    {
       const uint32_t u[4] = {a[x].x, a[x].y, a[x].z, a[x].w}, v[4] = {b[x].x, b[x].y, b[x].z, b[x].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -108,8 +111,7 @@ __global__ void __launch_bounds__(256) packed_pre_kernel(const PreParams p) {
     }
 #pragma unroll
     for (int o = kLanes / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0 && r < rows) {
-      const int t = (int)(r / H), h = (int)(r - (long long)t * H);
+    if (lane == 0 && t < p.s.T) {
       const size_t at = ((size_t)(h / p.s.G) * p.s.T + t) * p.s.G + h % p.s.G;
       const float lse = p.LSE[(size_t)h * p.s.T + t];
       p.nlse[at] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // (a row that saw nothing: P = 0)
