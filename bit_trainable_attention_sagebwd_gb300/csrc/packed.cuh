@@ -36,9 +36,10 @@ namespace {  // internal linkage: each translation unit keeps its own copy
 
 constexpr int kDevSequence = 7;  // (kDevIndex of the cache calls: a number on the device is out of range)
 constexpr int kTile = 128;
-constexpr int kUnitCost = 256;  // a unit's beginning and end, in tokens
-
 enum UnitKind { kPairs, kRows, kKeys };
+template <int KIND>
+constexpr int kUnitCost = KIND == kPairs ? 320 : 384;  // a unit's beginning and end, in places
+
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1) / (unsigned)b); }
 
@@ -78,18 +79,18 @@ struct Units {
   // places of the line before unit i, and its own (tokens as if every unit were whole; below 2^50)
   __device__ __forceinline__ int per() const { return KIND == kKeys ? p.per : 1; }
   __device__ __forceinline__ long long before(int i) const {
-    const long long all = (long long)i * ((long long)len * per() + kUnitCost);
+    const long long all = (long long)i * ((long long)len * per() + kUnitCost<KIND>);
     if (!p.causal) return all;
     if (KIND == kKeys) return all - (long long)i * (i - 1) / 2 * (kTile * per());
-    return (long long)i * (i + 1) / 2 * u + (long long)i * kUnitCost;
+    return (long long)i * (i + 1) / 2 * u + (long long)i * kUnitCost<KIND>;
   }
   __device__ __forceinline__ long long own(int i) const {
-    return kUnitCost + (long long)(!p.causal ? len : KIND == kKeys ? len - i * kTile : (i + 1) * u) * per();
+    return kUnitCost<KIND> + (long long)(!p.causal ? len : KIND == kKeys ? len - i * kTile : (i + 1) * u) * per();
   }
   __device__ __forceinline__ long long total() const { return before(count()); }
   // the unit that holds place x of a head: the root of before(i) = x, put right
   __device__ __forceinline__ int at(long long x) const {
-    const float c = kUnitCost, f = (float)x;
+    const float c = kUnitCost<KIND>, f = (float)x;
     float i;
     if (!p.causal) {
       i = f / ((float)len * per() + c);
@@ -113,7 +114,7 @@ struct Units {
                   : off < (1 << 25) ? (int)__umulhi((unsigned)off, p.inv_pw) : (int)min(off / (p.per * p.w), (long long)n);
     return c >= n - kSnap ? n : c <= kSnap ? 0 : c;
   }
-  static constexpr int kSnap = 2;
+  static constexpr int kSnap = 3;
 };
 
 // places of all of sequence b's units
@@ -353,13 +354,38 @@ __device__ __forceinline__ uint32_t bf2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 32 channels of a row times f, as bf16
-__device__ __forceinline__ void store_row(__nv_bfloat16* to, const float (&o)[32], float f) {
+// Rows of bf16 to memory, a thread a row.  Four neighbours exchange 16-byte pieces so that each store of a warp writes 64
+// bytes of eight rows, not 16 of 32 (half sectors, a line each).
+struct RowStore {
+  __nv_bfloat16* to[4];  // of the four's rows; null: not stored
+  __device__ __forceinline__ explicit RowStore(__nv_bfloat16* row) {
 #pragma unroll
-  for (int e = 0; e < 32; e += 8)
-    *reinterpret_cast<uint4*>(to + e) = make_uint4(bf2(o[e] * f, o[e + 1] * f), bf2(o[e + 2] * f, o[e + 3] * f),
-                                                   bf2(o[e + 4] * f, o[e + 5] * f), bf2(o[e + 6] * f, o[e + 7] * f));
-}
+    for (int s = 0; s < 4; ++s)
+      to[s] = reinterpret_cast<__nv_bfloat16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), (threadIdx.x & 28) + s));
+  }
+  // channels [d, d + 32) times f (all lanes of the warp)
+  __device__ __forceinline__ void put(const float (&o)[32], int d, float f) const {
+    uint32_t u[4][4];
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) u[e >> 3][(e >> 1) & 3] = bf2(o[e] * f, o[e + 1] * f);
+    auto swap = [&](uint32_t (&x)[4], uint32_t (&y)[4], int bit) {
+      const bool up = threadIdx.x & bit;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x[e] : y[e], bit);
+        x[e] = up ? got : x[e];
+        y[e] = up ? y[e] : got;
+      }
+    };
+    swap(u[0], u[1], 1);
+    swap(u[2], u[3], 1);
+    swap(u[0], u[2], 2);
+    swap(u[1], u[3], 2);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      if (to[s]) *reinterpret_cast<uint4*>(to[s] + d + 8 * (threadIdx.x & 3)) = make_uint4(u[s][0], u[s][1], u[s][2], u[s][3]);
+  }
+};
 
 // pre[g]: the places before each group of sequences, and their number behind the last (all threads of the CTA, which
 // must synchronise before they read it)

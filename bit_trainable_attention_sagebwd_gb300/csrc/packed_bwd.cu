@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool live = key < s.len, whole = s.whole();
       const int x = g >> 1, d0 = (g & 1) * (D / 2);
       const sage_rows& to = x ? p.d1 : p.d0;
-      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(to.p) + (long long)(s.at + key) * to.token + s.hk * to.head;
+      const RowStore out(live ? static_cast<__nv_bfloat16*>(to.p) + (long long)(s.at + key) * to.token + s.hk * to.head : nullptr);
       auto part_of = [&](int place) { return p.part + (size_t)(2 * place + x) * kTile * D; };
       const float f = x ? 1.f : p.sm_scale;
 #pragma unroll 1
@@ -475,8 +475,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[32];
         tmem_ld32(tmem + lanes + (x ? cDV : cDK) + d, o);
         tmem_wait32(o);
-        if (whole && live) store_row(row + d, reinterpret_cast<const float(&)[32]>(o), f);
-        if (!whole) store_sums(part_of(s.place()), d, r, o);
+        if (whole)
+          out.put(reinterpret_cast<const float(&)[32]>(o), d, f);
+        else
+          store_sums(part_of(s.place()), d, r, o);
       }
       tc_fence_before();
       warp_arrive(&sm.bar_acc_read);
@@ -486,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float o[32] = {};
 #pragma unroll 1
         for (int k = 0; k < s.parts(); ++k) add_sums(part_of(s.place(k)), d, r, 1.f, o);
-        if (live) store_row(row + d, o, f);
+        out.put(o, d, f);
       }
     }
   }
@@ -739,15 +741,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const int d = 32 * g;
-      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(p.d0.p) + (long long)(done.at + row_i) * p.d0.token +
-                           (done.hk * p.s.G + head) * p.d0.head + d;
+      const RowStore out(was_live ? static_cast<__nv_bfloat16*>(p.d0.p) + (long long)(done.at + row_i) * p.d0.token +
+                                        (done.hk * p.s.G + head) * p.d0.head
+                                  : nullptr);
       const bool whole = done.whole();
       if (d < D) {
         uint32_t o[32];
         tmem_ld32(tmem + lanes + cDQ + d, o);
         tmem_wait32(o);
-        if (whole && was_live) store_row(row, reinterpret_cast<const float(&)[32]>(o), p.sm_scale);
-        if (!whole) store_sums(p.part + (size_t)done.place() * kTile * D, d, r, o);
+        if (whole)
+          out.put(reinterpret_cast<const float(&)[32]>(o), d, p.sm_scale);
+        else
+          store_sums(p.part + (size_t)done.place() * kTile * D, d, r, o);
       }
       tc_fence_before();
       warp_arrive(&sm.bar_acc_read);
@@ -756,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float o[32] = {};
 #pragma unroll 1
         for (int k = 0; k < done.parts(); ++k) add_sums(p.part + (size_t)done.place(k) * kTile * D, d, r, 1.f, o);
-        if (was_live) store_row(row, o, p.sm_scale);
+        out.put(o, d, p.sm_scale);
       }
     }
   }

@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const int h = s.hk * p.s.G + head;
-      __nv_bfloat16* orow = p.O + (long long)(s.at + i) * p.o_token + h * p.o_head;
+      const RowStore out(live ? p.O + (long long)(s.at + i) * p.o_token + h * p.o_head : nullptr);
       constexpr size_t kPart = (size_t)kTile * (D + 2);
       auto finish = [&]() {  // the row's LSE, and O's factor
         if (live) p.LSE[(size_t)h * p.s.T + s.at + i] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
@@ -399,8 +399,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[32];
         tmem_ld32(o_col + d, o);
         tmem_wait32(o);
-        if (whole && live) store_row(orow + d, reinterpret_cast<const float(&)[32]>(o), f);
-        if (!whole) store_sums(part, d, r, o);
+        if (whole)
+          out.put(reinterpret_cast<const float(&)[32]>(o), d, f);
+        else
+          store_sums(part, d, r, o);
       }
       tc_fence_before();
       warp_arrive(&sm.bar_o_read[t]);
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float o[32] = {};
 #pragma unroll 1
         for (int k = 0; k < s.parts(); ++k) add_sums(at(k), d, r, ex2(__ldcg(at(k) + (size_t)kTile * D + r) - sub), o);
-        if (live) store_row(orow + d, o, g);
+        out.put(o, d, g);
       }
     }
   }
