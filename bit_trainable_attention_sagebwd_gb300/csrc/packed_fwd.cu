@@ -12,8 +12,6 @@
 // TMA copies whole boxes: what lies behind a sequence's end is the next one's.  Rows of S behind it are not
 // stored, columns are masked; of V's rows those that a product reads (up to 15) are zeroed in shared memory, so that
 // nothing of another sequence, a NaN or an infinity among it, enters a sum.
-#include <type_traits>
-
 #include "issue.cuh"
 #include "launch.h"
 #include "packed.cuh"
@@ -122,85 +120,78 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) {
     if (warp == 8 || warp == 11) {
       // ---------------- MMA issuers, warp 8 for the first place, warp 11 for the second.  P V of a key tile and S of the
-      // next one go in together; what comes early (K, V, Q, the turn) is waited for before P.  Place and stage are
-      // constants of the code that issues, so its descriptors need no arithmetic.
-      auto issuer = [&](auto place) {
-        constexpr int t = decltype(place)::value;
-        constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_o = idesc_bf16(kTile, D, false, true);
-        constexpr uint32_t s_col = t * 128, o_col = kColO + t * 128;
-        uint32_t kc = 0, np = 0, nu = 0, turns = 0;  // key tiles that came by, P tiles and units here, turns taken
-        bool ok = true;
-        auto issue_s = [&](auto stage, bool last) {
-          constexpr int st = decltype(stage)::value;
-          const uint64_t a = sdesc_sw128(smem_u32(sm.q[t]), 16, 1024), b = sdesc_sw128(smem_u32(sm.k[st]), 16, 1024);
-#pragma unroll
-          for (int h = 0; h < kAtoms; ++h) issue_ss_x4(s_col, a + h * (kAtom >> 4), b + h * (kAtom >> 4), id_s, h > 0);
-          commit(&sm.bar_s[t]);
-          commit(&sm.bar_k_empty[st]);
-          if (last) commit(&sm.bar_q_empty[t]);
-        };
-        auto products = [&](auto stage, int keys, bool first, bool again, bool last) {
-          constexpr int st = decltype(stage)::value;
-          const uint64_t b = sdesc_sw128(smem_u32(sm.v[st]), kAtom, 1024);
-          if (keys >= kTile) {
-            issue_ts_x4(o_col, s_col, b, id_o, !first);
-            issue_ts_x4(o_col, s_col + 32, b + (4 * 2048 >> 4), id_o, 1);
+      // next one go in together; what comes early (K, V, Q, the turn) is waited for before P.  Every MMA stands here
+      // once: copies for each place and stage, whose descriptors would be constants, take longer to fetch than they save.
+      const int t = warp == 8 ? 0 : 1;
+      constexpr uint32_t id_s = idesc_bf16(kTile, kTile, false, false), id_o = idesc_bf16(kTile, D, false, true);
+      constexpr uint64_t kNext = (uint64_t)kTile * D * 2 >> 4, kAtomStep = kAtom >> 4;
+      const uint64_t dq = sdesc_sw128(smem_u32(sm.q[t]), 16, 1024), dk = sdesc_sw128(smem_u32(sm.k[0]), 16, 1024);
+      const uint64_t dv = sdesc_sw128(smem_u32(sm.v[0]), kAtom, 1024);
+      const uint32_t s_col = t * 128, o_col = kColO + t * 128;
+      uint32_t kc = 0, np = 0, nu = 0, turns = 0;  // key tiles that came by, P tiles and units here, turns taken
+      bool ok = true;
+#pragma unroll 1
+      while (ok && parts.next(s)) {
+        const Places pl(p.s, s, solo);
+        const int x = t ^ pl.t0, end = x < pl.rows ? (x ? pl.end1 : pl.end0) : s.c0;
+        // P V of tile j (kc) and S of tile j + 1; before the first tile S alone
+#pragma unroll 1
+        for (int j = s.c0 - 1; ok && j < end && s.c0 < end; ++j) {
+          const bool pv = j >= s.c0, more = j + 1 < end;
+          const uint32_t st = kc & 1, next = pv ? kc + 1 : kc;
+          bool paired = false;
+          if (more) ok = wait(&sm.bar_k_full[next & 1], (next >> 1) & 1);
+          if (!pv) {
+            ok = ok && wait(&sm.bar_q_full[t], nu & 1);
           } else {
-#pragma unroll 1
-            for (int e = 0; e * 16 < keys; ++e) issue_ts(o_col, s_col + 8 * e, b + (e * 2048 >> 4), id_o, e > 0 || !first);
-          }
-          commit(&sm.bar_v_empty[st]);
-          if (again)
-            issue_s(std::integral_constant<int, st ^ 1>(), last);
-          else
-            commit(&sm.bar_o[t]);
-        };
-#pragma unroll 1
-        while (ok && parts.next(s)) {
-          const Places pl(p.s, s, solo);
-          const int x = t ^ pl.t0, end = x < pl.rows ? (x ? pl.end1 : pl.end0) : s.c0;
-          if (s.c0 < end) {
-            ok = wait(&sm.bar_q_full[t], nu & 1) && wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (kc & 1) issue_s(std::integral_constant<int, 1>(), s.c0 + 1 == end);
-            else issue_s(std::integral_constant<int, 0>(), s.c0 + 1 == end);
-          }
-#pragma unroll 1
-          for (int j = s.c0; ok && j < end; ++j, ++kc) {
-            ok = wait(&sm.bar_v_full[kc & 1], (kc >> 1) & 1);
-            if (j + 1 < end) ok = ok && wait(&sm.bar_k_full[(kc + 1) & 1], ((kc + 1) >> 1) & 1);
+            ok = ok && wait(&sm.bar_v_full[st], (kc >> 1) & 1);
             if (j == s.c0) ok = ok && (nu == 0 || wait(&sm.bar_o_read[t], (nu - 1) & 1));
             // Where both places have the key tile their products go in in turns: mixed they would end together, and the
             // tensor core wait for both softmaxes.
-            const bool paired = pl.rows == 2 && j < pl.end0;
+            paired = pl.rows == 2 && j < pl.end0;
             if (paired) {
               if (turns + t > 0) ok = ok && wait(&sm.bar_turn[t], (turns + t - 1) & 1);
               ++turns;
             }
             ok = ok && wait(&sm.bar_p[t], np++ & 1);
-            if (!ok) break;
-            tc_fence_after();
-            if (kc & 1) products(std::integral_constant<int, 1>(), s.len - j * kTile, j == s.c0, j + 1 < end, j + 2 == end);
-            else products(std::integral_constant<int, 0>(), s.len - j * kTile, j == s.c0, j + 1 < end, j + 2 == end);
-            if (paired && lane == 0) mbar_arrive(&sm.bar_turn[t ^ 1]);
-            __syncwarp();
           }
-          if (s.c0 < end) ++nu;
-          // tiles that only the other place takes
+          if (!ok) break;
+          tc_fence_after();
+          if (pv) {
+            const uint64_t b = dv + st * kNext;
+            const int keys = s.len - j * kTile;
+            if (keys >= kTile) {
+              issue_ts_x4(o_col, s_col, b, id_o, j > s.c0);
+              issue_ts_x4(o_col, s_col + 32, b + (4 * 2048 >> 4), id_o, 1);
+            } else {
 #pragma unroll 1
-          for (int j = max(end, s.c0); ok && j < s.c1; ++j, ++kc) {
-            ok = wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1);
-            if (ok && lane == 0) mbar_arrive(&sm.bar_k_empty[kc & 1]);
-            ok = ok && wait(&sm.bar_v_full[kc & 1], (kc >> 1) & 1);
-            if (ok && lane == 0) mbar_arrive(&sm.bar_v_empty[kc & 1]);
+              for (int e = 0; e * 16 < keys; ++e) issue_ts(o_col, s_col + 8 * e, b + (e * 2048 >> 4), id_o, e > 0 || j > s.c0);
+            }
+            commit(&sm.bar_v_empty[st]);
+            if (!more) commit(&sm.bar_o[t]);
+            ++kc;
           }
+          if (more) {
+            const uint64_t b = dk + (next & 1) * kNext;
+#pragma unroll
+            for (int h = 0; h < kAtoms; ++h) issue_ss_x4(s_col, dq + h * kAtomStep, b + h * kAtomStep, id_s, h > 0);
+            commit(&sm.bar_s[t]);
+            commit(&sm.bar_k_empty[next & 1]);
+            if (j + 2 == end) commit(&sm.bar_q_empty[t]);
+          }
+          if (paired && lane == 0) mbar_arrive(&sm.bar_turn[t ^ 1]);
+          __syncwarp();
         }
-      };
-      if (warp == 8)
-        issuer(std::integral_constant<int, 0>());
-      else
-        issuer(std::integral_constant<int, 1>());
+        if (s.c0 < end) ++nu;
+        // tiles that only the other place takes
+#pragma unroll 1
+        for (int j = max(end, s.c0); ok && j < s.c1; ++j, ++kc) {
+          ok = wait(&sm.bar_k_full[kc & 1], (kc >> 1) & 1);
+          if (ok && lane == 0) mbar_arrive(&sm.bar_k_empty[kc & 1]);
+          ok = ok && wait(&sm.bar_v_full[kc & 1], (kc >> 1) & 1);
+          if (ok && lane == 0) mbar_arrive(&sm.bar_v_empty[kc & 1]);
+        }
+      }
     } else if (warp == 9) {
       // ---------------- Q and K
       uint32_t kc = 0, nq[2] = {0, 0};
@@ -306,7 +297,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         // (twice over S in loops: unrolled whole, the code of the warps' roles together takes longer to fetch than to run)
         const int left = lim - j * kTile;
-        const bool edge = __any_sync(0xffffffffu, left < kTile);
+        if (__any_sync(0xffffffffu, left < kTile)) {  // masked in TMEM, so that the loops behind need not ask
+#pragma unroll 1
+          for (int c = 0; c < kTile; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(s_col + c, v);
+            tmem_wait32(v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c + e >= left) v[e] = 0xff800000u;
+            tmem_st32(s_col + c, v);
+          }
+          tmem_st_wait();
+        }
         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (apart: one chain of maxima would wait for itself)
 #pragma unroll 1
         for (int c = 0; c < kTile; c += 64) {
@@ -316,11 +319,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           reg_fence32(v[0]);
           reg_fence32(v[1]);
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e)
-              if (c + e >= left) v[e >> 5][e & 31] = 0xff800000u;
-          }
 #pragma unroll
           for (int e = 0; e < 64; e += 2)
             tops[(e >> 1) & 3] = max3(tops[(e >> 1) & 3], __uint_as_float(v[e >> 5][e & 31]), __uint_as_float(v[e >> 5][(e & 31) + 1]));
@@ -347,31 +345,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sub = m == -INFINITY ? 0.f : m;
         const uint64_t a2 = f2(p.alpha, p.alpha), m2 = f2(-sub, -sub);
         uint64_t sums[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-        // P of 32 keys from S of theirs
-        auto some = [&](int c, uint32_t (&v)[32]) {
-          if (edge) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c + e >= left) v[e] = 0xff800000u;
-          }
-          uint32_t w[16];
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 32) {
+          uint32_t v[32], w[16];
+          tmem_ld32(s_col + c, v);
+          tmem_wait32(v);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float u0, u1;
             f2split(ffma2(f2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), a2, m2), u0, u1);
             u0 = ex2(u0), u1 = ex2(u1);
             sums[(e >> 1) & 1] = fadd2(sums[(e >> 1) & 1], f2(u0, u1));
-            const __nv_bfloat162 h = __floats2bfloat162_rn(u0, u1);
-            w[e >> 1] = *reinterpret_cast<const uint32_t*>(&h);
+            w[e >> 1] = bf2(u0, u1);
           }
           tmem_st16(s_col + (c >> 1), w);
-        };
-#pragma unroll 1
-        for (int c = 0; c < kTile; c += 32) {
-          uint32_t v[32];
-          tmem_ld32(s_col + c, v);
-          tmem_wait32(v);
-          some(c, v);
         }
         tmem_st_wait();
         tc_fence_before();
