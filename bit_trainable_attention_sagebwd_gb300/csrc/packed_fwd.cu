@@ -210,8 +210,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(sm.q[t] + h * kAtom, &tm_q, h * 64, s.hk * p.s.G, s.at + (2 * s.i + x) * p.s.w, &sm.bar_q_full[t]);
           }
         };
-        load_q(0);
-        for (int j = s.c0; ok && j < s.c1; ++j, ++kc) {
+        // the first row tile, a key tile, the second row tile, the other key tiles
+#pragma unroll 1
+        for (int j = s.c0; ok && j < max(s.c1, s.c0 + pl.rows); ++j) {
+          if (j - s.c0 < pl.rows) load_q(j - s.c0);
+          if (!ok || j >= s.c1) continue;
           const uint32_t st = kc & 1;
           ok = kc < 2 || wait(&sm.bar_k_empty[st], ((kc >> 1) - 1) & 1);
           if (ok && lane == 0) {
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(sm.k[st] + h * kAtom, &tm_k, h * 64, s.at + j * kTile, s.hk, &sm.bar_k_full[st]);
           }
           __syncwarp();
-          if (j == s.c0 && pl.rows == 2) load_q(1);
+          ++kc;
         }
       }
       // (the last copies are waited for by those who use them, or, after a wait that ran out, here)
@@ -345,11 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sub = m == -INFINITY ? 0.f : m;
         const uint64_t a2 = f2(p.alpha, p.alpha), m2 = f2(-sub, -sub);
         uint64_t sums[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll 1
-        for (int c = 0; c < kTile; c += 32) {
-          uint32_t v[32], w[16];
-          tmem_ld32(s_col + c, v);
-          tmem_wait32(v);
+        // P of 32 keys while the next ones' S come
+        auto exps = [&](const uint32_t (&v)[32], int c) {
+          uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float u0, u1;
@@ -359,6 +360,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[e >> 1] = bf2(u0, u1);
           }
           tmem_st16(s_col + (c >> 1), w);
+        };
+        uint32_t v0[32], v1[32];
+        tmem_ld32(s_col, v0);
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 64) {
+          tmem_wait32(v0);
+          tmem_ld32(s_col + c + 32, v1);
+          exps(v0, c);
+          tmem_wait32(v1);
+          if (c + 64 < kTile) tmem_ld32(s_col + c + 64, v0);
+          exps(v1, c + 32);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -374,46 +386,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int h = s.hk * p.s.G + head;
       const RowStore out(live ? p.O + (long long)(s.at + i) * p.o_token + h * p.o_head : nullptr);
       constexpr size_t kPart = (size_t)kTile * (D + 2);
-      auto finish = [&]() {  // the row's LSE, and O's factor
-        if (live) p.LSE[(size_t)h * p.s.T + s.at + i] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-        return l != 0.f ? 1.f / l : 0.f;
-      };
+      auto part_of = [&](int k) { return p.part + (size_t)(2 * s.place(k) + x) * kPart; };
       const bool whole = s.whole();
-      const float f = whole ? finish() : 1.f;
-      float* part = p.part + (size_t)(2 * s.place() + x) * kPart;
+      if (!whole) {
+        float* part = p.part + (size_t)(2 * s.place() + x) * kPart;
+#pragma unroll 1
+        for (int d = 0; d < D; d += 32) {
+          uint32_t o[32];
+          tmem_ld32(o_col + d, o);
+          tmem_wait32(o);
+          store_sums(part, d, r, o);
+        }
+        tc_fence_before();
+        warp_arrive(&sm.bar_o_read[t]);
+        part[(size_t)kTile * D + r] = m;
+        part[(size_t)kTile * (D + 1) + r] = l;
+        if (!sm.meeting[t].was_last(p.s.status + kFwdCounters + 2 * s.first() + x, s.parts(), joins++, (warp & 3) == 0, abort, ok)) continue;
+        // O = sum O_k 2^(m_k - M) / sum l_k 2^(m_k - M)
+        m = -INFINITY, l = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < s.parts(); ++k) m = fmaxf(m, __ldcg(part_of(k) + (size_t)kTile * D + r));
+        const float sub = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+        for (int k = 0; k < s.parts(); ++k)
+          l = fmaf(__ldcg(part_of(k) + (size_t)kTile * (D + 1) + r), ex2(__ldcg(part_of(k) + (size_t)kTile * D + r) - sub), l);
+      }
+      const float g = l != 0.f ? 1.f / l : 0.f, sub = m == -INFINITY ? 0.f : m;
+      if (live) p.LSE[(size_t)h * p.s.T + s.at + i] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
 #pragma unroll 1
       for (int d = 0; d < D; d += 32) {
         uint32_t o[32];
-        tmem_ld32(o_col + d, o);
-        tmem_wait32(o);
-        if (whole)
-          out.put(reinterpret_cast<const float(&)[32]>(o), d, f);
-        else
-          store_sums(part, d, r, o);
+        if (whole) {
+          tmem_ld32(o_col + d, o);
+          tmem_wait32(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+#pragma unroll 1
+          for (int k = 0; k < s.parts(); ++k)
+            add_sums(part_of(k), d, r, ex2(__ldcg(part_of(k) + (size_t)kTile * D + r) - sub), reinterpret_cast<float(&)[32]>(o));
+        }
+        out.put(reinterpret_cast<const float(&)[32]>(o), d, g);
       }
-      tc_fence_before();
-      warp_arrive(&sm.bar_o_read[t]);
-      if (whole) continue;
-      part[(size_t)kTile * D + r] = m;
-      part[(size_t)kTile * (D + 1) + r] = l;
-      if (!sm.meeting[t].was_last(p.s.status + kFwdCounters + 2 * s.first() + x, s.parts(), joins++, (warp & 3) == 0, abort, ok)) continue;
-      // O = sum O_k 2^(m_k - M) / sum l_k 2^(m_k - M)
-      const float* parts_of = p.part + x * kPart;
-      auto at = [&](int k) { return parts_of + (size_t)(2 * s.place(k)) * kPart; };
-      m = -INFINITY, l = 0.f;
-#pragma unroll 1
-      for (int k = 0; k < s.parts(); ++k) m = fmaxf(m, __ldcg(at(k) + (size_t)kTile * D + r));
-      const float sub = m == -INFINITY ? 0.f : m;
-#pragma unroll 1
-      for (int k = 0; k < s.parts(); ++k)
-        l = fmaf(__ldcg(at(k) + (size_t)kTile * (D + 1) + r), ex2(__ldcg(at(k) + (size_t)kTile * D + r) - sub), l);
-      const float g = finish();
-#pragma unroll 1
-      for (int d = 0; d < D; d += 32) {
-        float o[32] = {};
-#pragma unroll 1
-        for (int k = 0; k < s.parts(); ++k) add_sums(at(k), d, r, ex2(__ldcg(at(k) + (size_t)kTile * D + r) - sub), o);
-        out.put(o, d, g);
+      if (whole) {
+        tc_fence_before();
+        warp_arrive(&sm.bar_o_read[t]);
       }
     }
   }
