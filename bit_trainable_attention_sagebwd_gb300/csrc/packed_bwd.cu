@@ -131,7 +131,7 @@ struct BwdSmem {
   // unswizzled, the first eight of 128 rows, then the others (zeros)
   __align__(128) uint8_t more[XS == 2 ? 2 : 1][XS == 2 ? kTile * 32 : 16];
   __align__(128) uint8_t ones[2][XS == 2 ? kTile * 32 : 16];
-  uint64_t bar_a_full[2], bar_a_empty[2], bar_x_full[XS], bar_x_empty[XS], bar_y_full[YS], bar_y_empty[YS], bar_raw[2];
+  uint64_t bar_a_full[2], bar_a_empty[2], bar_x_full[XS], bar_x_empty[XS], bar_y_full[YS], bar_y_empty[YS], bar_raw;
   uint64_t bar_s[2], bar_dp, bar_p, bar_ds, bar_acc, bar_acc_read, bar_s_read, bar_dp_read, bar_ds_free;
   FeedRing ring;
   Meeting meeting;
@@ -148,9 +148,9 @@ __device__ __forceinline__ void init_barriers(BwdSmem<D, XS, YS>& sm, int reader
   for (int t = 0; t < 2; ++t) {
     mbar_init(&sm.bar_a_full[t], XS == 3 && t == 1 ? kWorkWarps : 1);  // (packed_dq's dO comes through the work warps)
     mbar_init(&sm.bar_a_empty[t], 1);
-    mbar_init(&sm.bar_raw[t], 1);
     mbar_init(&sm.bar_s[t], 1);
   }
+  mbar_init(&sm.bar_raw, 1);
   for (int t = 0; t < XS; ++t) {
     mbar_init(&sm.bar_x_full[t], 1);
     mbar_init(&sm.bar_x_empty[t], 1);
@@ -223,19 +223,21 @@ __device__ __forceinline__ bool bring(uint8_t* tile, int rows, int copied, uint3
 // One tile of the parts after another.  `first`, `last`: of a part.
 struct Tiles {
   Feed feed;
-  Part s;
-  int j;
-  bool valid, first, last;
-  __device__ __forceinline__ Tiles(FeedRing& ring, volatile int* abort) : feed(ring, abort), s{}, j(0), valid(false), first(false), last(true) { next(); }
-  __device__ __forceinline__ void next() {
+  Part s{};
+  int j = 0;
+  bool first = false, last = true;
+  __device__ __forceinline__ Tiles(FeedRing& ring, volatile int* abort) : feed(ring, abort) {}
+  // false: there are no more
+  __device__ __forceinline__ bool next() {
     first = last;
-    if (last) {
-      valid = feed.next(s);
-      j = s.c0;
-    } else {
+    if (!last) {
       ++j;
+    } else {
+      if (!feed.next(s)) return false;
+      j = s.c0;
     }
     last = j + 1 == s.c1;
+    return true;
   }
 };
 
@@ -317,12 +319,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t d_s = tmem + (v ? cDP : cS), d_g = tmem + (v ? cDK : cDV);
       bool ok = true;
       uint32_t units = 0, done = 0;
-      // S or dP
-      auto issue_s = [&](const Tiles& t, uint32_t n) {
-        if (t.first) ok = ok && wait(&sm.bar_a_full[v], units++ & 1);
+      int rows = 0;
+      Tiles t(sm.ring, abort);
+      // dV or dK of tile n - 1, then S or dP of tile n
+#pragma unroll 1
+      for (uint32_t n = 0;; ++n) {
+        const bool first = t.first, last = t.last, more = t.next();
+        if (n > 0) {
+          if (first && done) ok = wait(&sm.bar_acc_read, (done - 1) & 1);
+          ok = ok && wait(due, (n - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_rows(d_g, d_s, summed + ((n - 1) & 1) * kNext, id_g, rows, !first);
+          commit(&given[(n - 1) & 1]);
+          if (last) {
+            commit(&sm.bar_acc);
+            ++done;
+          }
+        }
+        if (!more) break;
+        rows = rows_of(t, tile_of(t));
+        if (t.first) ok = wait(&sm.bar_a_full[v], units++ & 1);
         ok = ok && wait(&full[n & 1], (n >> 1) & 1);
         if (v) ok = ok && wait(&sm.bar_x_full[n & 1], (n >> 1) & 1);  // (the further channels come with Q)
-        if (!ok) return;
+        if (!ok) break;
         tc_fence_after();
 #pragma unroll
         for (int h = 0; h < kAtoms; ++h)
@@ -331,50 +351,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(ready);
         if (v) commit(&sm.bar_y_empty[n & 1]);
         if (t.last) commit(&sm.bar_a_empty[v]);
-      };
-      Tiles t(sm.ring, abort);
-      if (t.valid) issue_s(t, 0);
-      for (uint32_t n = 0; ok && t.valid; ++n) {
-        const int rows = rows_of(t, tile_of(t));
-        const bool first = t.first, last = t.last;
-        t.next();
-        if (first && done) ok = wait(&sm.bar_acc_read, (done - 1) & 1);
-        ok = ok && wait(due, n & 1);
-        if (!ok) break;
-        tc_fence_after();
-        issue_rows(d_g, d_s, summed + (n & 1) * kNext, id_g, rows, !first);
-        commit(&given[n & 1]);
-        if (last) {
-          commit(&sm.bar_acc);
-          ++done;
-        }
-        if (t.valid) issue_s(t, n + 1);
       }
     } else if (warp == kLoader) {
       // ---------------- K and V; dO and Q, in the order in which they are given back
-      uint32_t units = 0, raws[2] = {0, 0}, n = 0;
+      uint32_t units = 0, raws = 0, n = 0;  // (both kinds of tile: each is waited for before the next)
       bool ok = true;
-      for (Tiles t(sm.ring, abort); ok && t.valid; t.next(), ++n) {
+      Tiles t(sm.ring, abort);
+#pragma unroll 1
+      for (; ok && t.next(); ++n) {
         const uint32_t st = n & 1;
         const int rt = tile_of(t), rows = rows_of(t, rt);
-        auto own = [&](int v, const CUtensorMap* tm) {
-          if (!t.first) return;
-          ok = ok && (units == 0 || wait(&sm.bar_a_empty[v], (units - 1) & 1));
-          if (ok && lane == 0) {
-            mbar_arrive_expect_tx(&sm.bar_a_full[v], kTile * D * 2);
+        // a unit's first: K, Q, V, dO; then dO, Q
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          const int v = t.first ? x : x ^ 1;
+          if (t.first) {
+            ok = ok && (units == 0 || wait(&sm.bar_a_empty[v], (units - 1) & 1));
+            if (ok && lane == 0) {
+              mbar_arrive_expect_tx(&sm.bar_a_full[v], kTile * D * 2);
 #pragma unroll
-            for (int h = 0; h < kAtoms; ++h)
-              tma_load_3d(sm.a[v] + h * kAtom, tm, h * 64, t.s.at + t.s.i * kTile, t.s.hk, &sm.bar_a_full[v]);
+              for (int h = 0; h < kAtoms; ++h)
+                tma_load_3d(sm.a[v] + h * kAtom, v ? &tm_v : &tm_k, h * 64, t.s.at + t.s.i * kTile, t.s.hk, &sm.bar_a_full[v]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-        };
-        auto walked = [&](uint8_t* tile, const CUtensorMap* tm, uint64_t* full, uint64_t* empty, int v) {
-          ok = ok && (n < 2 || wait(empty, ((n >> 1) - 1) & 1));
-          ok = ok && bring<D>(tile, rows, box, box * D * 2 + (v ? 0 : rows * 16), full, &sm.bar_raw[v], raws[v], abort,
+          uint8_t* tile = v ? sm.y[st] : sm.x[st];
+          ok = ok && (n < 2 || wait(v ? &sm.bar_y_empty[st] : &sm.bar_x_empty[st], ((n >> 1) - 1) & 1));
+          ok = ok && bring<D>(tile, rows, box, box * D * 2 + (v ? 0 : rows * 16), v ? &sm.bar_y_full[st] : &sm.bar_x_full[st],
+                              &sm.bar_raw, raws, abort,
                               [&](uint64_t* bar) {
 #pragma unroll
                                 for (int h = 0; h < kAtoms; ++h)
-                                  tma_load_3d(tile + h * kAtom, tm, h * 64, t.s.hk * p.s.G, t.s.at + rt * p.s.w, bar);
+                                  tma_load_3d(tile + h * kAtom, v ? &tm_do : &tm_q, h * 64, t.s.hk * p.s.G, t.s.at + rt * p.s.w, bar);
                                 if (v == 0)  // (with Q: dP of the tile before is done once Q's tile is free)
                                   bulk_load(sm.more[st], p.more + ((size_t)t.s.hk * p.s.T + t.s.at + (size_t)rt * p.s.w) * p.s.G,
                                             rows * 16, bar);
@@ -382,12 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               [&](int from, int to) {
                                 if (v == 0 && from + lane < to) reinterpret_cast<uint4*>(sm.more[st])[from + lane] = more_channels(kNever, 0.f);
                               });
-        };
-        own(0, &tm_k);
-        if (t.first) walked(sm.x[st], &tm_q, &sm.bar_x_full[st], &sm.bar_x_empty[st], 0);
-        own(1, &tm_v);
-        walked(sm.y[st], &tm_do, &sm.bar_y_full[st], &sm.bar_y_empty[st], 1);
-        if (!t.first) walked(sm.x[st], &tm_q, &sm.bar_x_full[st], &sm.bar_x_empty[st], 0);
+        }
         if (t.first) ++units;
       }
       // (copies in flight after a wait that ran out)
@@ -410,56 +413,56 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t units = 0, joins = 0, n = 0;
     Feed parts(sm.ring, abort);
-    Part s;
+    Part s{};
     const uint64_t a2 = f2(p.alpha, p.alpha);
     while (ok && parts.next(s)) {
-    const int key = s.i * kTile + r;
-    // causal: columns of tokens before the key are masked
-    int ahead = p.s.causal ? key - (Units<kKeys>(p.s, s.len).first(s.i) + s.c0) * p.s.w : 0;
+      const int key = s.i * kTile + r;
+      // causal: columns of tokens before the key are masked
+      int ahead = p.s.causal ? key - (Units<kKeys>(p.s, s.len).first(s.i) + s.c0) * p.s.w : 0;
 #pragma unroll 1
-    for (int j = s.c0; j < s.c1; ++j, ++n, ahead -= p.s.w) {
-      const int mask = min(ahead, kTile) * p.s.G - 32 * g;  // the group's columns before it
-      ok = wait(&sm.bar_s[0], n & 1);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sv[32];
-      tmem_ld32(s_col, sv);
-      tmem_wait32(sv);
-      if (__any_sync(0xffffffffu, mask > 0)) {
+      for (int j = s.c0; j < s.c1; ++j, ++n, ahead -= p.s.w) {
+        const int mask = min(ahead, kTile) * p.s.G - 32 * g;  // the group's columns before it
+        ok = wait(&sm.bar_s[0], n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sv[32];
+        tmem_ld32(s_col, sv);
+        tmem_wait32(sv);
+        if (__any_sync(0xffffffffu, mask > 0)) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (e < mask) sv[e] = 0xff800000u;
-      }
-      uint32_t w[16];
+          for (int e = 0; e < 32; ++e)
+            if (e < mask) sv[e] = 0xff800000u;
+        }
+        uint32_t w[16];
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float x, y;
-        f2split(fmul2(f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), a2), x, y);
-        x = ex2(x), y = ex2(y);
-        sv[e] = __float_as_uint(x), sv[e + 1] = __float_as_uint(y);
-        w[e >> 1] = bf2(x, y);
-      }
-      tmem_st16(s_col, w);
-      tmem_st_wait();
-      tc_fence_before();
-      warp_arrive(&sm.bar_p);
-      ok = wait(&sm.bar_dp, n & 1);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t dv[32];
-      tmem_ld32(dp_col, dv);
-      tmem_wait32(dv);
+        for (int e = 0; e < 32; e += 2) {
+          float x, y;
+          f2split(fmul2(f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), a2), x, y);
+          x = ex2(x), y = ex2(y);
+          sv[e] = __float_as_uint(x), sv[e + 1] = __float_as_uint(y);
+          w[e >> 1] = bf2(x, y);
+        }
+        tmem_st16(s_col, w);
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&sm.bar_p);
+        ok = wait(&sm.bar_dp, n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t dv[32];
+        tmem_ld32(dp_col, dv);
+        tmem_wait32(dv);
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float x, y;
-        f2split(fmul2(f2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]))), x, y);
-        w[e >> 1] = bf2(x, y);
+        for (int e = 0; e < 32; e += 2) {
+          float x, y;
+          f2split(fmul2(f2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]))), x, y);
+          w[e >> 1] = bf2(x, y);
+        }
+        tmem_st16(dp_col, w);
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&sm.bar_ds);
       }
-      tmem_st16(dp_col, w);
-      tmem_st_wait();
-      tc_fence_before();
-      warp_arrive(&sm.bar_ds);
-    }
       // ---- the unit's sums: groups 0 and 1 half of dK's channels each, groups 2 and 3 of dV's
       ok = ok && wait(&sm.bar_acc, units++ & 1);
       if (!ok) break;
@@ -471,24 +474,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto part_of = [&](int place) { return p.part + (size_t)(2 * place + x) * kTile * D; };
       const float f = x ? 1.f : p.sm_scale;
 #pragma unroll 1
-      for (int d = d0; d < d0 + D / 2; d += 32) {
-        uint32_t o[32];
-        tmem_ld32(tmem + lanes + (x ? cDV : cDK) + d, o);
-        tmem_wait32(o);
-        if (whole)
-          out.put(reinterpret_cast<const float(&)[32]>(o), d, f);
-        else
-          store_sums(part_of(s.place()), d, r, o);
-      }
-      tc_fence_before();
-      warp_arrive(&sm.bar_acc_read);
-      if (whole || !sm.meeting.was_last(p.s.status + kKeyCounters + 2 * s.first(), s.parts(), joins++, warp == 0, abort, ok)) continue;
+      for (int round = whole ? 1 : 0; round < 2; ++round) {  // a unit's part goes to memory before its sums, if it has others
 #pragma unroll 1
-      for (int d = d0; d < d0 + D / 2; d += 32) {
-        float o[32] = {};
+        for (int d = d0; d < d0 + D / 2; d += 32) {
+          uint32_t o[32];
+          if (whole || round == 0) {
+            tmem_ld32(tmem + lanes + (x ? cDV : cDK) + d, o);
+            tmem_wait32(o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0;
 #pragma unroll 1
-        for (int k = 0; k < s.parts(); ++k) add_sums(part_of(s.place(k)), d, r, 1.f, o);
-        out.put(o, d, f);
+            for (int k = 0; k < s.parts(); ++k) add_sums(part_of(s.place(k)), d, r, 1.f, reinterpret_cast<float(&)[32]>(o));
+          }
+          if (round)
+            out.put(reinterpret_cast<const float(&)[32]>(o), d, f);
+          else
+            store_sums(part_of(s.place()), d, r, o);
+        }
+        if (whole || round == 0) {
+          tc_fence_before();
+          warp_arrive(&sm.bar_acc_read);
+        }
+        if (round == 0 &&
+            !sm.meeting.was_last(p.s.status + kKeyCounters + 2 * s.first(), s.parts(), joins++, warp == 0, abort, ok))
+          break;
       }
     }
   }
@@ -545,7 +555,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       Turn<kStagesK> kt;
       Turn<kStagesV> vt;
       uint32_t units = 0, n = 0;
-      for (Tiles t(sm.ring, abort); t.valid; t.next(), ++n) {
+      Tiles t(sm.ring, abort);
+#pragma unroll 1
+      for (; t.next(); ++n) {
         if (t.first) ok = ok && wait(&sm.bar_a_full[0], units & 1);
         ok = ok && wait(&sm.bar_x_full[kt.at], kt.round & 1);
         if (n > 0) ok = ok && wait(&sm.bar_s_read, (n - 1) & 1);
@@ -575,7 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       Turn<kStagesK> kt;
       uint32_t done = 0, n = 0;
-      for (Tiles t(sm.ring, abort); t.valid; t.next(), ++n) {
+      Tiles t(sm.ring, abort);
+#pragma unroll 1
+      for (; t.next(); ++n) {
         if (t.first && done) ok = wait(&sm.bar_acc_read, (done - 1) & 1);
         const int keys = t.s.len - t.j * kTile;
         const uint64_t b = k_n + kt.at * kNext;
@@ -601,10 +615,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- Q; K and V
       Turn<kStagesK> kt;
       Turn<kStagesV> vt;
-      uint32_t units = 0, raws[2] = {0, 0};
+      uint32_t units = 0, raws = 0;
       const int lane = tid & 31, box = p.s.G * p.s.w;
       bool ok = true;
-      for (Tiles t(sm.ring, abort); ok && t.valid; t.next()) {
+      Tiles t(sm.ring, abort);
+#pragma unroll 1
+      while (ok && t.next()) {
         if (t.first) {
           ok = units == 0 || wait(&sm.bar_a_empty[0], (units - 1) & 1);
           if (!ok) break;
@@ -617,18 +633,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        auto key_tile = [&](uint8_t* tile, const CUtensorMap* tm, uint64_t* full, uint64_t* empty, uint32_t round, int v) {
-          ok = ok && (round == 0 || wait(empty, (round - 1) & 1));
-          ok = ok && bring<D>(tile, min(kTile, t.s.len - t.j * kTile), kTile, kTile * D * 2, full, &sm.bar_raw[v], raws[v], abort,
+#pragma unroll 1
+        for (int v = 0; v < 2; ++v) {
+          const uint32_t st = v ? vt.at : kt.at, round = v ? vt.round : kt.round;
+          uint8_t* tile = v ? sm.y[st] : sm.x[st];
+          ok = ok && (round == 0 || wait(v ? &sm.bar_y_empty[st] : &sm.bar_x_empty[st], (round - 1) & 1));
+          ok = ok && bring<D>(tile, min(kTile, t.s.len - t.j * kTile), kTile, kTile * D * 2,
+                              v ? &sm.bar_y_full[st] : &sm.bar_x_full[st], &sm.bar_raw, raws, abort,
                               [&](uint64_t* bar) {
 #pragma unroll
                                 for (int h = 0; h < kAtoms; ++h)
-                                  tma_load_3d(tile + h * kAtom, tm, h * 64, t.s.at + t.j * kTile, t.s.hk, bar);
+                                  tma_load_3d(tile + h * kAtom, v ? &tm_v : &tm_k, h * 64, t.s.at + t.j * kTile, t.s.hk, bar);
                               },
                               [](int, int) {});
-        };
-        key_tile(sm.x[kt.at], &tm_k, &sm.bar_x_full[kt.at], &sm.bar_x_empty[kt.at], kt.round, 0);
-        key_tile(sm.y[vt.at], &tm_v, &sm.bar_y_full[vt.at], &sm.bar_y_empty[vt.at], vt.round, 1);
+        }
         if (!ok) break;
         kt.next();
         vt.next();
@@ -652,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t joins = 0, units = 0, n = 0;
     Feed parts(sm.ring, abort);
-    Part s;
+    Part s{};
     const uint64_t a2 = f2(p.alpha, p.alpha);
     float nl = 0.f, nd = 0.f;
     int i = 0;
@@ -682,87 +700,84 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = parts.next(s);
     if (more) begin_unit();
     while (ok && more) {
-    int left = (live && p.s.causal ? i + 1 : s.len) - s.c0 * kTile - 32 * g;  // keys that the row sees
+      int left = (live && p.s.causal ? i + 1 : s.len) - s.c0 * kTile - 32 * g;  // keys that the row sees
 #pragma unroll 1
-    for (int j = s.c0; j < s.c1; ++j, ++n, left -= kTile) {
-      ok = wait(&sm.bar_s[0], n & 1);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t sv[32];
-      tmem_ld32(s_col, sv);
-      tmem_wait32(sv);
-      tc_fence_before();
-      warp_arrive(&sm.bar_s_read);
-      if (__any_sync(0xffffffffu, left < 32)) {
+      for (int j = s.c0; j < s.c1; ++j, ++n, left -= kTile) {
+        ok = wait(&sm.bar_s[0], n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sv[32];
+        tmem_ld32(s_col, sv);
+        tmem_wait32(sv);
+        tc_fence_before();
+        warp_arrive(&sm.bar_s_read);
+        if (__any_sync(0xffffffffu, left < 32)) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (e >= left) sv[e] = 0xff800000u;
-      }
-      const uint64_t l2 = f2(nl, nl), d2 = f2(nd, nd);
+          for (int e = 0; e < 32; ++e)
+            if (e >= left) sv[e] = 0xff800000u;
+        }
+        const uint64_t l2 = f2(nl, nl), d2 = f2(nd, nd);
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float x, y;
-        f2split(ffma2(f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), a2, l2), x, y);
-        sv[e] = __float_as_uint(ex2(x));
-        sv[e + 1] = __float_as_uint(ex2(y));
-      }
-      ok = wait(&sm.bar_dp, n & 1);
-      if (!ok) break;
-      tc_fence_after();
-      uint32_t dv[32], w[16];
-      tmem_ld32(dp_col, dv);
-      tmem_wait32(dv);
-      tc_fence_before();
-      warp_arrive(&sm.bar_dp_read);
+        for (int e = 0; e < 32; e += 2) {
+          float x, y;
+          f2split(ffma2(f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), a2, l2), x, y);
+          sv[e] = __float_as_uint(ex2(x));
+          sv[e + 1] = __float_as_uint(ex2(y));
+        }
+        ok = wait(&sm.bar_dp, n & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t dv[32], w[16];
+        tmem_ld32(dp_col, dv);
+        tmem_wait32(dv);
+        tc_fence_before();
+        warp_arrive(&sm.bar_dp_read);
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        float x, y;
-        f2split(fmul2(fadd2(f2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), d2),
-                      f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]))),
-                x, y);
-        w[e >> 1] = bf2(x, y);
+        for (int e = 0; e < 32; e += 2) {
+          float x, y;
+          f2split(fmul2(fadd2(f2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), d2),
+                        f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]))),
+                  x, y);
+          w[e >> 1] = bf2(x, y);
+        }
+        if (n > 0) ok = wait(&sm.bar_ds_free, (n - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        tmem_st16(tmem + lanes + cDS + 16 * g, w);
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&sm.bar_ds);
       }
-      if (n > 0) ok = wait(&sm.bar_ds_free, (n - 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      tmem_st16(tmem + lanes + cDS + 16 * g, w);
-      tmem_st_wait();
-      tc_fence_before();
-      warp_arrive(&sm.bar_ds);
-    }
       if (!ok) break;
       const Part done = s;
       const int row_i = i;
       const bool was_live = live;
       more = parts.next(s);
       if (more) begin_unit();
-      // ---- the unit's sums, 32 channels a group (D = 64: the first two)
+      // ---- the unit's sums, 32 channels a group (D = 64: the first two store)
       ok = wait(&sm.bar_acc, units++ & 1);
       if (!ok) break;
       tc_fence_after();
-      const int d = 32 * g;
-      const RowStore out(was_live ? static_cast<__nv_bfloat16*>(p.d0.p) + (long long)(done.at + row_i) * p.d0.token +
-                                        (done.hk * p.s.G + head) * p.d0.head
-                                  : nullptr);
-      const bool whole = done.whole();
-      if (d < D) {
-        uint32_t o[32];
-        tmem_ld32(tmem + lanes + cDQ + d, o);
-        tmem_wait32(o);
-        if (whole)
-          out.put(reinterpret_cast<const float(&)[32]>(o), d, p.sm_scale);
-        else
-          store_sums(p.part + (size_t)done.place() * kTile * D, d, r, o);
-      }
+      const int d = 32 * g % D;
+      const bool mine = 32 * g < D, whole = done.whole();
+      uint32_t o[32];
+      tmem_ld32(tmem + lanes + cDQ + d, o);
+      tmem_wait32(o);
+      if (mine && !whole) store_sums(p.part + (size_t)done.place() * kTile * D, d, r, o);
       tc_fence_before();
       warp_arrive(&sm.bar_acc_read);
-      if (whole || !sm.meeting.was_last(p.s.status + kRowCounters + 2 * done.first(), done.parts(), joins++, warp == 0, abort, ok)) continue;
-      if (d < D) {
-        float o[32] = {};
+      if (!whole) {
+        if (!sm.meeting.was_last(p.s.status + kRowCounters + 2 * done.first(), done.parts(), joins++, warp == 0, abort, ok)) continue;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0;
 #pragma unroll 1
-        for (int k = 0; k < done.parts(); ++k) add_sums(p.part + (size_t)done.place(k) * kTile * D, d, r, 1.f, o);
-        out.put(o, d, p.sm_scale);
+        for (int k = 0; k < done.parts(); ++k)
+          add_sums(p.part + (size_t)done.place(k) * kTile * D, d, r, 1.f, reinterpret_cast<float(&)[32]>(o));
       }
+      RowStore(was_live && mine ? static_cast<__nv_bfloat16*>(p.d0.p) + (long long)(done.at + row_i) * p.d0.token +
+                                      (done.hk * p.s.G + head) * p.d0.head
+                                : nullptr)
+          .put(reinterpret_cast<const float(&)[32]>(o), d, p.sm_scale);
     }
   }
   tc_fence_before();
