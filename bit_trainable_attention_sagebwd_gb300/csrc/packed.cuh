@@ -40,7 +40,6 @@ enum UnitKind { kPairs, kRows, kKeys };
 template <int KIND>
 constexpr int kUnitCost = KIND == kPairs ? 320 : 384;  // a unit's beginning and end, in places
 
-
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1) / (unsigned)b); }
 
 // One arrival of a warp, for all of its lanes (one of each lane queues up at the barrier)
@@ -117,10 +116,10 @@ struct Units {
   static constexpr int kSnap = 3;
 };
 
-// places of all of sequence b's units
+// places of all of sequence b's units, and its tokens
 template <int KIND>
-__device__ __forceinline__ long long places(const PackedShape& p, int b) {
-  int at, len;
+__device__ __forceinline__ long long places(const PackedShape& p, int b, int& len) {
+  int at;
   sequence(p, b, at, len);
   return len > 0 ? Units<KIND>(p, len).total() * p.Hkv : 0;
 }
@@ -171,7 +170,8 @@ struct Walk {
       const int end_b = min(p.S, (g + 1) * group);
       b = end_b;
       for (int b0 = g * group; b0 < end_b; b0 += 32) {
-        long long s = b0 + lane < end_b ? places<KIND>(p, b0 + lane) : 0;
+        int n;
+        long long s = b0 + lane < end_b ? places<KIND>(p, b0 + lane, n) : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const long long x = __shfl_up_sync(0xffffffffu, s, o);
@@ -387,16 +387,28 @@ struct RowStore {
   }
 };
 
-// pre[g]: the places before each group of sequences, and their number behind the last (all threads of the CTA, which
-// must synchronise before they read it)
+// pre[g]: the places before each group of sequences, and their number behind the last; `tokens`, zero before: of all
+// sequences (all threads of the CTA, which must synchronise before they read either)
 template <int KIND, int NT>
-__device__ __forceinline__ void prefix_of_sequences(const PackedShape& p, int group, long long* pre, long long* wsum) {
+__device__ __forceinline__ void prefix_of_sequences(const PackedShape& p, int group, long long* pre, long long* wsum,
+                                                    unsigned long long* tokens) {
+  unsigned long long sum = 0;
   prefix_of<NT>(kPackedGroups, pre, wsum, [&](int g) {
     long long n = 0;
 #pragma unroll 1
-    for (int b = g * group; b < min(p.S, (g + 1) * group); ++b) n += places<KIND>(p, b);
+    for (int b = g * group; b < min(p.S, (g + 1) * group); ++b) {
+      int len;
+      n += places<KIND>(p, b, len);
+      sum += len;
+    }
     return n;
   });
+  if (sum) atomicAdd(tokens, sum);
+}
+// Sequences that lie over one another (cu_seqlens out of order) could be any amount of work: beyond twice the tensors'
+// tokens none of it is done.
+__device__ __forceinline__ bool too_many(const PackedShape& p, unsigned long long tokens) {
+  return tokens > 2 * (unsigned long long)p.T;
 }
 
 inline PackedShape packed_shape(const int* cu, void* ws, int T, int S, int H, int Hkv, int causal) {

@@ -137,6 +137,7 @@ struct BwdSmem {
   Meeting meeting;
   long long wsum[kWarps];
   long long pre[kPackedGroups + 1];
+  unsigned long long tokens;
   uint32_t tmem_base;
   int abort;
 };
@@ -170,6 +171,7 @@ __device__ __forceinline__ void init_barriers(BwdSmem<D, XS, YS>& sm, int reader
   mbar_init(&sm.bar_dp_read, kWorkWarps);
   mbar_init(&sm.bar_ds_free, 1);
   sm.abort = 0;
+  sm.tokens = 0;
   fence_mbar_init();
 }
 
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   const int group = ceil_div(p.s.S, kPackedGroups);
-  prefix_of_sequences<kKeys, kThreads>(p.s, group, sm.pre, sm.wsum);
+  prefix_of_sequences<kKeys, kThreads>(p.s, group, sm.pre, sm.wsum, &sm.tokens);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
   const Shares line(sm.pre[kPackedGroups], gridDim.x);
-  const bool idle = line.total == 0 || (int)blockIdx.x >= line.parts;
+  const bool idle = line.total == 0 || too_many(p.s, sm.tokens) || (int)blockIdx.x >= line.parts;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
   // the row tile at hand: the sequence's tile, and its rows
   auto tile_of = [&](const Tiles& t) { return Units<kKeys>(p.s, t.s.len).first(t.s.i) + t.j; };
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   const int group = ceil_div(p.s.S, kPackedGroups);
-  prefix_of_sequences<kRows, kThreads>(p.s, group, sm.pre, sm.wsum);
+  prefix_of_sequences<kRows, kThreads>(p.s, group, sm.pre, sm.wsum, &sm.tokens);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort = &sm.abort;
   const Shares line(sm.pre[kPackedGroups], gridDim.x);
-  const bool idle = line.total == 0 || (int)blockIdx.x >= line.parts;
+  const bool idle = line.total == 0 || too_many(p.s, sm.tokens) || (int)blockIdx.x >= line.parts;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };
 
   if (warp >= kWorkWarps) {

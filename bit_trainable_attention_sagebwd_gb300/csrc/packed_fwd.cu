@@ -45,6 +45,7 @@ struct FwdSmem {
   Meeting meeting[2];
   long long wsum[kThreads / 32];
   long long pre[kPackedGroups + 1];
+  unsigned long long tokens;
   uint32_t tmem_base;
   int abort;
 };
@@ -91,6 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sm.bar_v_raw, 1);
     sm.ring.init(12);
     sm.abort = 0;
+    sm.tokens = 0;
     fence_mbar_init();
   }
   pdl_wait();
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   const int group = ceil_div(p.s.S, kPackedGroups);
-  prefix_of_sequences<kPairs, kThreads>(p.s, group, sm.pre, sm.wsum);
+  prefix_of_sequences<kPairs, kThreads>(p.s, group, sm.pre, sm.wsum, &sm.tokens);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -111,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Shares line(sm.pre[kPackedGroups], gridDim.x);
   const int w0 = blockIdx.x;
   if (sm.tmem_base != tmem && tid == 0) atomicMax(p.s.status, (int)kDevSetup);
-  const bool idle = line.total == 0 || w0 >= line.parts || sm.tmem_base != tmem;
+  const bool idle = line.total == 0 || too_many(p.s, sm.tokens) || w0 >= line.parts || sm.tmem_base != tmem;
   Feed parts(sm.ring, abort);
   Part s;
   auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_warp(bar, parity, abort); };

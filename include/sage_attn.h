@@ -408,7 +408,8 @@ int sage_attn_kv_compact(const sage_kv_cache *cache, const sage_kv_cache *to, vo
  *  - cu_seqlens: int32 [S + 1] on the device, not decreasing, within 0 .. T: sequence s has the tokens
  *    cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (none: an empty sequence).  Rows before the first and behind the last are
  *    neither read into a result nor written.  A sequence whose entries are out of order or range counts as empty, with
- *    SAGE_ERR_INVALID_ARG in the status word.
+ *    SAGE_ERR_INVALID_ARG in the status word (and all of them where the others, which may then lie over one another, have
+ *    more than 2 T tokens together).
  *  - Query head h reads key/value head h / (H / Hkv); Hkv divides H, H / Hkv at most 128, D 64 or 128,
  *    S at most 65536, T at most 2^24.
  *  - ws: sage_attn_packed_ws_bytes(.., backward) bytes, 256-byte aligned.  Its first 4096 bytes are zero before the
