@@ -329,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool first = t.first, last = t.last, more = t.next();
         if (n > 0) {
           if (first && done) ok = wait(&sm.bar_acc_read, (done - 1) & 1);
+          if (!v) ok = ok && wait(&sm.bar_y_full[(n - 1) & 1], ((n - 1) >> 1) & 1);  // (dO, which S did not need)
           ok = ok && wait(due, (n - 1) & 1);
           if (!ok) break;
           tc_fence_after();

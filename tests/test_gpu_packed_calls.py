@@ -115,6 +115,17 @@ def test_one_long_sequence_over_many_ctas(lens, H, Hkv, D, causal):
     backward_checked(q, k, v, do, cu, causal)
 
 
+@pytest.mark.parametrize("D,H,Hkv", [(128, 16, 16), (64, 16, 4)])
+def test_gradients_of_many_documents(D, H, Hkv):
+    """Many short units one behind the other on each SM, which nothing but the waits keeps apart."""
+    lens = [101, 543, 119, 1298, 121, 194, 102, 1027, 727, 203, 336, 2048, 215, 107, 370, 329, 340, 251, 271, 190]
+    q, k, v, do, cu = ref.inputs(lens, H, Hkv, D)
+    o, lse, got = backward_checked(q, k, v, do, cu, True)
+    for _ in range(10):
+        for x, y in zip(got.values(), sa.packed_backward(q, k, v, o, lse, do, cu)):
+            assert torch.equal(x, y)
+
+
 # ------------------------------------------------------------------- workspaces
 
 def test_a_workspace_full_of_anything():
