@@ -131,6 +131,7 @@ struct BwdSmem {
   // unswizzled, the first eight of 128 rows, then the others (zeros)
   __align__(128) uint8_t more[XS == 2 ? 2 : 1][XS == 2 ? kTile * 32 : 16];
   __align__(128) uint8_t ones[2][XS == 2 ? kTile * 32 : 16];
+  __align__(128) uint4 low[XS == 2 ? 1 : 4 * kTile];  // packed_dq: the second halves of dS (see there), [group][row]
   uint64_t bar_a_full[2], bar_a_empty[2], bar_x_full[XS], bar_x_empty[XS], bar_y_full[YS], bar_y_empty[YS], bar_raw;
   uint64_t bar_s[2], bar_dp, bar_p, bar_ds, bar_acc, bar_acc_read, bar_s_read, bar_dp_read, bar_ds_free;
   FeedRing ring;
@@ -515,6 +516,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // TMEM: S (query rows x keys) at 0, dP at 128, dQ at 256; behind it dO, from where it is dP's A operand (in shared memory
 // it would take 32 KB of its bandwidth for each key tile), and dS.  S and dP of the next tile go in as soon as this
 // one's have been read, so the warps do not wait for them.
+// dS's rounding to bf16 is most of what dQ is off by: a row of dS sums to zero, its roundings do not, so what the keys
+// have in common stays in their error.  Of the first eight of every 32 keys the rounding's rest goes into dQ as well
+// (`low`, a further bf16, 16 keys an MMA): a quarter of that error's square for 4% of the time, 1.29 to 1.35 ms for
+// 8192 tokens.  For all keys TMEM has no columns left.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dq_kernel(const BwdParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -587,6 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kSecond) {
       // ---------------- MMA issuer of dQ
       const uint64_t k_n = sdesc_sw128(smem_u32(sm.x[0]), kAtom, 1024);
+      // the low halves: eight keys each of two groups, 32 keys apart
+      const uint64_t k_far = sdesc_sw128(smem_u32(sm.x[0]), kAtom, 4096), low = sdesc_none(smem_u32(sm.low), kTile * 16, 128);
       bool ok = true;
       Turn<kStagesK> kt;
       uint32_t done = 0, n = 0;
@@ -606,6 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int k = 0; k * 16 < keys; ++k) issue_ts(tmem + cDQ, tmem + cDS + 8 * k, b + (k * 2048 >> 4), id_g, k > 0 || !t.first);
         }
+        // (not where a group's keys lie behind the sequence)
+#pragma unroll 1
+        for (int k = 0; k < 2 && keys > 64 * k + 32; ++k)
+          issue_ss(tmem + cDQ, low + k * (2 * kTile * 16 >> 4), k_far + kt.at * kNext + k * (8 * 1024 >> 4), id_g, 1);
         commit(&sm.bar_ds_free);
         commit(&sm.bar_x_empty[kt.at]);
         kt.next();
@@ -730,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(&sm.bar_dp, n & 1);
         if (!ok) break;
         tc_fence_after();
-        uint32_t dv[32], w[16];
+        uint32_t dv[32], w[16], low[4];
         tmem_ld32(dp_col, dv);
         tmem_wait32(dv);
         tc_fence_before();
@@ -742,12 +753,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]))),
                   x, y);
           w[e >> 1] = bf2(x, y);
+          if (e < 8) low[e >> 1] = bf2(x - __uint_as_float(w[e >> 1] << 16), y - __uint_as_float(w[e >> 1] & 0xffff0000u));
         }
         if (n > 0) ok = wait(&sm.bar_ds_free, (n - 1) & 1);
         if (!ok) break;
         tc_fence_after();
         tmem_st16(tmem + lanes + cDS + 16 * g, w);
+        sm.low[g * kTile + r] = make_uint4(low[0], low[1], low[2], low[3]);
         tmem_st_wait();
+        fence_proxy_async_smem();
         tc_fence_before();
         warp_arrive(&sm.bar_ds);
       }
