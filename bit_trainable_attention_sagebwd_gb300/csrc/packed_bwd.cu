@@ -519,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dS's rounding to bf16 is most of what dQ is off by: a row of dS sums to zero, its roundings do not, so what the keys
 // have in common stays in their error.  Of the first eight of every 32 keys the rounding's rest goes into dQ as well
 // (`low`, a further bf16, 16 keys an MMA): a quarter of that error's square for 4% of the time, 1.29 to 1.35 ms for
-// 8192 tokens.  For all keys TMEM has no columns left.
+// 8192 tokens.  For all keys TMEM has no columns left.  (Sequences of 32 keys or fewer: of the first sixteen.)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dq_kernel(const BwdParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -613,10 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int k = 0; k * 16 < keys; ++k) issue_ts(tmem + cDQ, tmem + cDS + 8 * k, b + (k * 2048 >> 4), id_g, k > 0 || !t.first);
         }
-        // (not where a group's keys lie behind the sequence)
+        // (not where a group's keys lie behind the sequence; 32 keys or fewer: the first sixteen)
 #pragma unroll 1
-        for (int k = 0; k < 2 && keys > 64 * k + 32; ++k)
-          issue_ss(tmem + cDQ, low + k * (2 * kTile * 16 >> 4), k_far + kt.at * kNext + k * (8 * 1024 >> 4), id_g, 1);
+        for (int k = 0; k == 0 || (k < 2 && keys > 64 * k + 32); ++k)
+          issue_ss(tmem + cDQ, low + k * (2 * kTile * 16 >> 4), (keys > 32 ? k_far : k_n) + kt.at * kNext + k * (8 * 1024 >> 4), id_g, 1);
         commit(&sm.bar_ds_free);
         commit(&sm.bar_x_empty[kt.at]);
         kt.next();
@@ -717,18 +717,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       int left = (live && p.s.causal ? i + 1 : s.len) - s.c0 * kTile - 32 * g;  // keys that the row sees
 #pragma unroll 1
       for (int j = s.c0; j < s.c1; ++j, ++n, left -= kTile) {
+        // (of 32 keys or fewer the second group gives keys 8 to 15 their low halves)
+        const int back = g == 1 && s.len - j * kTile <= 32 ? 24 : 0;
         ok = wait(&sm.bar_s[0], n & 1);
         if (!ok) break;
         tc_fence_after();
         uint32_t sv[32];
-        tmem_ld32(s_col, sv);
+        tmem_ld32(s_col - back, sv);
         tmem_wait32(sv);
         tc_fence_before();
         warp_arrive(&sm.bar_s_read);
-        if (__any_sync(0xffffffffu, left < 32)) {
+        if (__any_sync(0xffffffffu, left + back < 32)) {
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (e >= left) sv[e] = 0xff800000u;
+            if (e >= left + back) sv[e] = 0xff800000u;
         }
         const uint64_t l2 = f2(nl, nl), d2 = f2(nd, nd);
 #pragma unroll
@@ -742,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         uint32_t dv[32], w[16], low[4];
-        tmem_ld32(dp_col, dv);
+        tmem_ld32(dp_col - back, dv);
         tmem_wait32(dv);
         tc_fence_before();
         warp_arrive(&sm.bar_dp_read);
