@@ -9,6 +9,16 @@ import packed_ref as ref
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(autouse=True)
+def fp32_default():
+    """torch's default type as it is for a user: another module of the run may have changed it."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
 # lengths, H, Hkv, D, causal
 CASES = [
     ([1], 1, 1, 64, True),

@@ -13,6 +13,15 @@ from test_gpu_rotary import check, ints, table, turned, values
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def fp32_default():
+    """torch's default type as it is for a user: another module of the run may have changed it."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
 def places(lens):
     return torch.cat([torch.arange(n) for n in lens]).cuda()
 

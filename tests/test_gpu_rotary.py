@@ -8,6 +8,16 @@ import bit_trainable_attention_sagebwd_gb300 as sa
 
 pytestmark = pytest.mark.gpu
 
+
+@pytest.fixture(autouse=True)
+def fp32_default():
+    """torch's default type as it is for a user: another module of the run may have changed it."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
 BF16 = torch.finfo(torch.bfloat16).eps / 2
 
 
