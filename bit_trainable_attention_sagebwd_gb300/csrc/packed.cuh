@@ -8,8 +8,8 @@
 //   kRows   one row tile against the same                         (dQ)
 //   kKeys   one key tile (128 keys) against the row tiles that see it  (dK, dV)
 // The units of a sequence follow each other, key/value head by head.  Every unit counts the tokens that it sees
-// (kKeys: `per` times) and kUnitCost more, so that the line of all units can be cut into equal shares of time.  One warp of a CTA walks its
-// share and hands the parts to the others (Feed).
+// (kKeys: `per` times) and kUnitCost more, so that the line of all units can be cut into equal shares of time.  One warp
+// of a CTA walks its share and hands the parts to the others (Feed).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -38,7 +38,10 @@ constexpr int kDevSequence = 7;  // (kDevIndex of the cache calls: a number on t
 constexpr int kTile = 128;
 enum UnitKind { kPairs, kRows, kKeys };
 template <int KIND>
-constexpr int kUnitCost = KIND == kPairs ? 320 : 384;  // a unit's beginning and end, in places
+// A unit's beginning and end, in places.  By measurement (64 to 768 tried): kPairs at 320 in place of 192 takes prompts of
+// 17 to 2048 tokens from 123 to 129 us, 512 to 138 us; kRows and kKeys at 384 each take documents of 100 to 2048 tokens from
+// 189 to 194 us, at 256 each D = 64 from 442 to 461 us.
+constexpr int kUnitCost = KIND == kPairs ? 192 : KIND == kRows ? 384 : 192;
 
 __host__ __device__ __forceinline__ int ceil_div(int a, int b) { return (int)(((unsigned)a + (unsigned)b - 1) / (unsigned)b); }
 
@@ -106,7 +109,8 @@ struct Units {
     return k;
   }
   // the tile of a unit where a cut at offset `off` is made: not within kSnap tiles of its ends, since each part costs
-  // its way through memory and the join
+  // its way through memory and the join (6 in place of 3: gradients of 4 documents 35.3 us, not 32.2 us, the others within
+  // 2%; the forward counts on 2 at least, so that both row tiles of a unit have tiles in each part)
   __device__ __forceinline__ int cut(long long off, int n) const {
     if (off <= 0) return 0;
     const int c = KIND != kKeys ? (int)min(off / kTile, (long long)n)
@@ -114,6 +118,7 @@ struct Units {
     return c >= n - kSnap ? n : c <= kSnap ? 0 : c;
   }
   static constexpr int kSnap = 3;
+  static_assert(kSnap >= 2, "a part's tiles of both row tiles");
 };
 
 // places of all of sequence b's units, and its tokens
@@ -125,7 +130,7 @@ __device__ __forceinline__ long long places(const PackedShape& p, int b, int& le
 }
 
 // The line of all units, cut into equal parts for the CTAs of a grid, of kLeast places at least (two cuts must not
-// fall into one tile).
+// fall into one tile; four key tiles, since a part of fewer is mostly beginning and end).
 constexpr int kLeast = 512;
 static_assert(kLeast >= 2 * kTile, "a tile between two cuts");
 struct Shares {
