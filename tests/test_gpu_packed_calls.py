@@ -124,6 +124,31 @@ def test_one_long_sequence_over_many_ctas(lens, H, Hkv, D, causal):
     backward_checked(q, k, v, do, cu, causal)
 
 
+def test_the_most_tokens_and_sequences():
+    """2^24 tokens in 65536 sequences: those at the beginning, in the middle and at the end as if alone."""
+    S, n, H, Hkv, D = 65536, 256, 2, 1, 64
+    T = S * n
+    g = torch.Generator("cuda").manual_seed(0)
+    q, do = (torch.randn((T, H, D), device="cuda", generator=g, dtype=torch.bfloat16) for _ in range(2))
+    k, v = (torch.randn((T, Hkv, D), device="cuda", generator=g, dtype=torch.bfloat16) for _ in range(2))
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda") * n
+    cu[1:-1] += torch.randint(-100, 101, (S - 1,), device="cuda", generator=g, dtype=torch.int32)
+    o, lse = sa.packed_forward(q, k, v, cu)
+    ws = sa.alloc_packed_ws(T, S, H, Hkv, D, backward=True)
+    grads = sa.packed_backward(q, k, v, o, lse, do, cu, ws=ws)
+    assert sa.get_status(ws) == sa.SAGE_OK
+    for s in (0, 127, 128, S // 2, S - 3):
+        b, e = int(cu[s]), int(cu[s + 3])
+        x = [y[b:e] for y in (q, k, v, do)]
+        part = cu[s:s + 4] - b
+        want = ref.forward(*x[:3], part, True, D ** -0.5)
+        ref.check(o[b:e], want[0], want[2], f"O of {s}")
+        ref.check(lse[:, b:e], want[1], want[3], f"LSE of {s}")
+        want, tol = ref.backward(*x[:3], o[b:e], lse[:, b:e], x[3], part, True, D ** -0.5)
+        for got, name in zip(grads, ("dq", "dk", "dv")):
+            ref.check(got[b:e], want[name], tol[name], f"{name} of {s}")
+
+
 @pytest.mark.parametrize("D,H,Hkv", [(128, 16, 16), (64, 16, 4)])
 def test_gradients_of_many_documents(D, H, Hkv):
     """Many short units one behind the other on each SM, which nothing but the waits keeps apart."""
