@@ -352,7 +352,8 @@ __device__ __forceinline__ void add_sums(const float* part, int d, int r, float 
 #pragma unroll
   for (int e = 0; e < 32; e += 4) {
     const float4 x = __ldcg(reinterpret_cast<const float4*>(part + (size_t)((d + e) * kTile + r * 4)));
-    o[e] = fmaf(x.x, f, o[e]), o[e + 1] = fmaf(x.y, f, o[e + 1]), o[e + 2] = fmaf(x.z, f, o[e + 2]), o[e + 3] = fmaf(x.w, f, o[e + 3]);
+    o[e] = fmaf(x.x, f, o[e]), o[e + 1] = fmaf(x.y, f, o[e + 1]);
+    o[e + 2] = fmaf(x.z, f, o[e + 2]), o[e + 3] = fmaf(x.w, f, o[e + 3]);
   }
 }
 __device__ __forceinline__ uint32_t bf2(float a, float b) {
@@ -366,7 +367,8 @@ struct RowStore {
   __device__ __forceinline__ explicit RowStore(__nv_bfloat16* row) {
 #pragma unroll
     for (int s = 0; s < 4; ++s)
-      to[s] = reinterpret_cast<__nv_bfloat16*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), (threadIdx.x & 28) + s));
+      to[s] = reinterpret_cast<__nv_bfloat16*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(row), (threadIdx.x & 28) + s));
   }
   // channels [d, d + 32) times f (all lanes of the warp)
   __device__ __forceinline__ void put(const float (&o)[32], int d, float f) const {

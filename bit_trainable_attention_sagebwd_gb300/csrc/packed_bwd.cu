@@ -108,8 +108,10 @@ __global__ void __launch_bounds__(256) packed_pre_kernel(const PreParams p) {
     unsigned t, h;
     a[x] = b[x] = make_uint4(0u, 0u, 0u, 0u);
     if (row(x, t, h)) {
-      a[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.O.p) + t * p.O.token + h * p.O.head) + lane);
-      b[x] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dO.p) + t * p.dO.token + h * p.dO.head) + lane);
+      auto piece = [&](const sage_rows& y) {
+        return __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(y.p) + t * y.token + h * y.head) + lane);
+      };
+      a[x] = piece(p.O), b[x] = piece(p.dO);
     }
   }
   float delta = 0.f;  // of the lane's row
@@ -299,7 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the further channels: P = 0 in rows that no copy brings; ones
     const int what = e / kTile, r = e % kTile;
     uint4* to = reinterpret_cast<uint4*>(what < 2 ? sm.more[what] : sm.ones[what - 2]);
-    to[r] = what < 2 ? more_channels(kNever, 0.f) : what == 2 ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u) : make_uint4(0u, 0x3f800000u, 0x3f803f80u, 0u);
+    to[r] = what < 2    ? more_channels(kNever, 0.f)
+            : what == 2 ? make_uint4(0x3f803f80u, 0x3f80u, 0u, 0u)
+                        : make_uint4(0u, 0x3f800000u, 0x3f803f80u, 0u);
     to[kTile + r] = make_uint4(0u, 0u, 0u, 0u);
   }
   fence_proxy_async_smem();
@@ -332,7 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t own_k = sdesc_sw128(smem_u32(sm.a[v]), 16, 1024);                              // K, or V
       const uint64_t walked_k = sdesc_sw128(smem_u32(v ? sm.y[0] : sm.x[0]), 16, 1024);             // Q, or dO
       const uint64_t summed = sdesc_sw128(smem_u32(v ? sm.x[0] : sm.y[0]), kAtom, 1024);            // dO, or Q
-      const uint64_t one_k = sdesc_none(smem_u32(sm.ones[v]), kTile * 16, 128), more_k = sdesc_none(smem_u32(sm.more[0]), kTile * 16, 128);
+      const uint64_t one_k = sdesc_none(smem_u32(sm.ones[v]), kTile * 16, 128);
+      const uint64_t more_k = sdesc_none(smem_u32(sm.more[0]), kTile * 16, 128);
       uint64_t *full = v ? sm.bar_y_full : sm.bar_x_full, *given = v ? sm.bar_x_empty : sm.bar_y_empty;
       uint64_t *ready = v ? &sm.bar_dp : &sm.bar_s[0], *due = v ? &sm.bar_ds : &sm.bar_p;
       const uint32_t d_s = tmem + (v ? cDP : cS), d_g = tmem + (v ? cDK : cDV);
@@ -402,13 +407,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                               [&](uint64_t* bar) {
 #pragma unroll
                                 for (int h = 0; h < kAtoms; ++h)
-                                  tma_load_3d(tile + h * kAtom, v ? &tm_do : &tm_q, h * 64, t.s.hk * p.s.G, t.s.at + rt * p.s.w, bar);
+                                  tma_load_3d(tile + h * kAtom, v ? &tm_do : &tm_q, h * 64, t.s.hk * p.s.G, t.s.at + rt * p.s.w,
+                                              bar);
                                 if (v == 0)  // (with Q: dP of the tile before is done once Q's tile is free)
                                   bulk_load(sm.more[st], p.more + ((size_t)t.s.hk * p.s.T + t.s.at + (size_t)rt * p.s.w) * p.s.G,
                                             rows * 16, bar);
                               },
                               [&](int from, int to) {
-                                if (v == 0 && from + lane < to) reinterpret_cast<uint4*>(sm.more[st])[from + lane] = more_channels(kNever, 0.f);
+                                if (v == 0 && from + lane < to)
+                                  reinterpret_cast<uint4*>(sm.more[st])[from + lane] = more_channels(kNever, 0.f);
                               });
         }
         if (t.first) ++units;
@@ -475,7 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
           float x, y;
-          f2split(fmul2(f2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]))), x, y);
+          f2split(fmul2(f2(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])),
+                        f2(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1]))),
+                  x, y);
           w[e >> 1] = bf2(x, y);
         }
         tmem_st16(dp_col, w);
@@ -627,12 +636,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           issue_ts_x4(tmem + cDQ, tmem + cDS + 32, b + (4 * 2048 >> 4), id_g, 1);
         } else {
 #pragma unroll 1
-          for (int k = 0; k * 16 < keys; ++k) issue_ts(tmem + cDQ, tmem + cDS + 8 * k, b + (k * 2048 >> 4), id_g, k > 0 || !t.first);
+          for (int k = 0; k * 16 < keys; ++k)
+            issue_ts(tmem + cDQ, tmem + cDS + 8 * k, b + (k * 2048 >> 4), id_g, k > 0 || !t.first);
         }
         // (not where a group's keys lie behind the sequence; 32 keys or fewer: the first sixteen)
 #pragma unroll 1
         for (int k = 0; k == 0 || (k < 2 && keys > 64 * k + 32); ++k)
-          issue_ss(tmem + cDQ, low + k * (2 * kTile * 16 >> 4), (keys > 32 ? k_far : k_n) + kt.at * kNext + k * (8 * 1024 >> 4), id_g, 1);
+          issue_ss(tmem + cDQ, low + k * (2 * kTile * 16 >> 4), (keys > 32 ? k_far : k_n) + kt.at * kNext + k * (8 * 1024 >> 4),
+                   id_g, 1);
         commit(&sm.bar_ds_free);
         commit(&sm.bar_x_empty[kt.at]);
         kt.next();
@@ -713,7 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t at = ((size_t)s.hk * p.s.T + s.at + i) * p.s.G + head;
       nl = live ? __ldcg(p.nlse + at) : -INFINITY;
       nd = live ? __ldcg(p.ndelta + at) : 0.f;
-      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dout.p) + (long long)(s.at + i) * p.dout.token +
+      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dout.p) +
+                                                        (long long)(s.at + i) * p.dout.token +
                                                         (s.hk * p.s.G + head) * p.dout.head + g * (D / 4));
       uint4 v[D / 32];
 #pragma unroll
@@ -802,7 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       warp_arrive(&sm.bar_acc_read);
       if (!whole) {
-        if (!sm.meeting.was_last(p.s.status + kRowCounters + 2 * done.first(), done.parts(), joins++, warp == 0, abort, ok)) continue;
+        if (!sm.meeting.was_last(p.s.status + kRowCounters + 2 * done.first(), done.parts(), joins++, warp == 0, abort, ok))
+          continue;
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0;
 #pragma unroll 1
@@ -861,7 +874,8 @@ int launch_packed_bwd(const sage_rows& Q, const sage_rows& K, const sage_rows& V
   const PreParams pre{s, O, dO, LSE, nlse, ndelta, more, sm_scale, inverse(H), inverse(s.G)};
   float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + l.part);
   const BwdParams dkv{s, nlse, ndelta, more, dO, dK, dV, part, sm_scale * kLog2e, sm_scale};
-  const BwdParams dq{s, nlse, ndelta, more, dO, dQ, dQ, part + (size_t)2 * kMaxParts * 2 * kTile * D, sm_scale * kLog2e, sm_scale};
+  const BwdParams dq{s,  nlse, ndelta, more, dO, dQ, dQ, part + (size_t)2 * kMaxParts * 2 * kTile * D, sm_scale * kLog2e,
+                     sm_scale};
   ScopedTimer timer("packed_bwd", st);
   return D == 128 ? launch<128>(dkv, dq, pre, Q, K, V, H, sms, st) : launch<64>(dkv, dq, pre, Q, K, V, H, sms, st);
 }

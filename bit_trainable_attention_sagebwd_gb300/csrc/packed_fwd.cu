@@ -334,7 +334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           reg_fence32(v[1]);
 #pragma unroll
           for (int e = 0; e < 64; e += 2)
-            tops[(e >> 1) & 3] = max3(tops[(e >> 1) & 3], __uint_as_float(v[e >> 5][e & 31]), __uint_as_float(v[e >> 5][(e & 31) + 1]));
+            tops[(e >> 1) & 3] =
+                max3(tops[(e >> 1) & 3], __uint_as_float(v[e >> 5][e & 31]), __uint_as_float(v[e >> 5][(e & 31) + 1]));
         }
         float top = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
         top *= p.alpha;
@@ -411,7 +412,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         warp_arrive(&sm.bar_o_read[t]);
         part[(size_t)kTile * D + r] = m;
         part[(size_t)kTile * (D + 1) + r] = l;
-        if (!sm.meeting[t].was_last(p.s.status + kFwdCounters + 2 * s.first() + x, s.parts(), joins++, (warp & 3) == 0, abort, ok)) continue;
+        if (!sm.meeting[t].was_last(p.s.status + kFwdCounters + 2 * s.first() + x, s.parts(), joins++, (warp & 3) == 0, abort,
+                                    ok))
+          continue;
         // O = sum O_k 2^(m_k - M) / sum l_k 2^(m_k - M)
         m = -INFINITY, l = 0.f;
 #pragma unroll 1

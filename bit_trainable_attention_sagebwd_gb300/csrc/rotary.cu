@@ -3,7 +3,8 @@
 //
 // HBM-bound: each value is read and written once.  A thread takes 16 channels of a token (two pieces of 16 bytes, whose
 // pairs it holds whole in either layout) in up to kHeads heads, so that eight sines and cosines serve kHeads times 16
-// values; all its loads are in flight before the first product.
+// values; all its loads are in flight before the first product.  32768 tokens of 32 and 8 heads: 98 us, 6.8 TB/s, what a
+// copy reaches; 64 tokens: 2.4 us, a launch.
 //
 // The angle of pair c at position n is n times a frequency, of which only the part of a turn counts.  Frequencies come
 // as 64-bit fractions of a turn, so n f modulo a turn is an integer product that wraps by itself: exact up to 2^-65 n
@@ -127,15 +128,16 @@ int launch(const RotaryParams& p, cudaStream_t st) {
   const int heads = p.heads[0] + p.heads[1], groups = (heads + kHeads - 1) / kHeads;
   const long long blocks = ((long long)p.B * p.N * groups * (D / 16) + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffll) return SAGE_ERR_UNSUPPORTED;
-  return launch_pdl(rotary_kernel<D, kHeads>, dim3((unsigned)blocks), dim3(kThreads), 0, st, p, groups) == cudaSuccess ? SAGE_OK
-                                                                                                                   : SAGE_ERR_CUDA;
+  const cudaError_t e = launch_pdl(rotary_kernel<D, kHeads>, dim3((unsigned)blocks), dim3(kThreads), 0, st, p, groups);
+  return e == cudaSuccess ? SAGE_OK : SAGE_ERR_CUDA;
 }
 
 }  // namespace
 
 int launch_rotary(const RotaryParams& p, int D, cudaStream_t st) {
   ScopedTimer timer("rotary", st);
-  // four heads a thread where that still fills the GPU (152 SMs of 2048 threads), else one
+  // four heads a thread where that still fills the GPU (152 SMs of 2048 threads), else one (64 tokens of 40 heads: 2.4 us
+  // with one, 3.1 us with four; 32768 tokens: 192 us with one, 98 us with four)
   const long long threads = (long long)p.B * p.N * ((p.heads[0] + p.heads[1] + 3) / 4) * (D / 16);
   if (threads >= 152 * 2048) return D == 128 ? launch<128, 4>(p, st) : launch<64, 4>(p, st);
   return D == 128 ? launch<128, 1>(p, st) : launch<64, 1>(p, st);

@@ -53,7 +53,8 @@ int sage_attn_rotary(const sage_rotary* r, const sage_heads* Q, const sage_heads
   if ((K == nullptr) != (Ko == nullptr)) return SAGE_ERR_INVALID_ARG;
   if (K != nullptr && (!heads_ok(K) || !apart(Ko, B, N, Hkv, D) || !same_or_apart(K, Ko))) return SAGE_ERR_INVALID_ARG;
   if (K != nullptr && (Qo->p == Ko->p || Qo->p == K->p || Ko->p == Q->p)) return SAGE_ERR_INVALID_ARG;
-  if (!aligned_or_null(positions, 4) || !aligned_or_null(start, 4) || !aligned_or_null(cu_seqlens, 4)) return SAGE_ERR_INVALID_ARG;
+  if (!aligned_or_null(positions, 4) || !aligned_or_null(start, 4) || !aligned_or_null(cu_seqlens, 4))
+    return SAGE_ERR_INVALID_ARG;
   if (positions != nullptr && (start != nullptr || cu_seqlens != nullptr)) return SAGE_ERR_INVALID_ARG;
   if (cu_seqlens != nullptr && B != 1) return SAGE_ERR_INVALID_ARG;
   if (cu_seqlens != nullptr && (S < 1 || S > (1 << 30))) return SAGE_ERR_UNSUPPORTED;
