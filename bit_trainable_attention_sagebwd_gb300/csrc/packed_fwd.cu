@@ -12,11 +12,12 @@
 //    rounding to bf16 (what the product takes) is the only one on the way; row sums are of P before it.
 // A unit that was cut leaves its parts' sums in the workspace; whoever finishes last adds them up.
 //
-// 16384 tokens, 16 heads of 2, D = 128, causal: 0.68 ms, 1.54 PFLOP/s, 80% of what a bf16 product reaches here.  What
+// 16384 tokens, 16 heads of 2, D = 128, causal: 0.66 ms, 1.58 PFLOP/s, 83% of what a bf16 product reaches here.  What
 // bounds it: the chain S, softmax, P V of a row tile, of which two run at once (tensor core 63%, issue slots 41%, the
 // exponentials' unit 32%; the softmax warps wait for TMEM most).  What the code of the five roles takes to fetch counts as
 // much: the softmax unrolled whole costs 12%, copies of the issue for place and stage 10%.  A row's columns shared by two
-// threads (16 softmax warps, maxima exchanged): 0.70 ms.  At D = 64 the same chain is 0.71 us a tile beside 0.89 us.
+// threads (16 softmax warps, maxima exchanged): 0.70 ms.  At D = 64 the same chain is 0.71 us a tile beside 0.89 us; S three
+// tiles ahead of P V there (a third place for S in TMEM) took 0.18 ms where this takes 0.15: both softmaxes then run at once.
 // TMA copies whole boxes: what lies behind a sequence's end is the next one's.  Rows of S behind it are not
 // stored, columns are masked; of V's rows those that a product reads (up to 15) are zeroed in shared memory, so that
 // nothing of another sequence, a NaN or an infinity among it, enters a sum.
@@ -359,29 +360,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sub = m == -INFINITY ? 0.f : m;
         const uint64_t a2 = f2(p.alpha, p.alpha), m2 = f2(-sub, -sub);
         uint64_t sums[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-        // P of 32 keys while the next ones' S come
-        auto exps = [&](const uint32_t (&v)[32], int c) {
-          uint32_t w[16];
+        // P of 64 keys at once: a store of 32 columns takes no longer than one of 16
+        uint32_t w[32];
+        auto exps = [&](const uint32_t (&v)[32], int at) {
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float u0, u1;
             f2split(ffma2(f2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), a2, m2), u0, u1);
             u0 = ex2(u0), u1 = ex2(u1);
             sums[(e >> 1) & 1] = fadd2(sums[(e >> 1) & 1], f2(u0, u1));
-            w[e >> 1] = bf2(u0, u1);
+            w[at + (e >> 1)] = bf2(u0, u1);
           }
-          tmem_st16(s_col + (c >> 1), w);
         };
-        uint32_t v0[32], v1[32];
-        tmem_ld32(s_col, v0);
 #pragma unroll 1
         for (int c = 0; c < kTile; c += 64) {
+          uint32_t v0[32], v1[32];
+          tmem_ld32(s_col + c, v0);
           tmem_wait32(v0);
           tmem_ld32(s_col + c + 32, v1);
-          exps(v0, c);
+          exps(v0, 0);
           tmem_wait32(v1);
-          if (c + 64 < kTile) tmem_ld32(s_col + c + 64, v0);
-          exps(v1, c + 32);
+          exps(v1, 16);
+          tmem_st32(s_col + (c >> 1), w);
         }
         tmem_st_wait();
         tc_fence_before();
