@@ -1,6 +1,7 @@
 // Host-side kernel launch with programmatic stream serialization: the kernel may begin
 // while its predecessor on the stream drains, and waits for it with griddepcontrol.wait
-// (pdl_wait) before it reads or writes anything the predecessor touches.
+// (pdl_wait) before it reads or writes anything the predecessor touches.  One exception: packed_dq, which reads nothing of
+// packed_dkv and takes from it the word that packed_pre is complete (pdl_wait_unless).
 #pragma once
 
 #include <cuda_runtime.h>

@@ -335,7 +335,9 @@ struct Meeting {
     return ok && *const_cast<volatile int*>(&last);
   }
 };
-// counters of the workspace, behind the status word
+// words of the workspace's header behind the status word: whether packed_dkv has seen packed_pre's results (pdl_tell), and
+// counters
+constexpr int kTermsTold = 32;
 constexpr int kCounters = 2 * kMaxParts;  // of each kernel: two of each worker
 enum { kFwdCounters = 64, kKeyCounters = kFwdCounters + kCounters, kRowCounters = kKeyCounters + kCounters,
        kHeader = kRowCounters + kCounters };  // in words

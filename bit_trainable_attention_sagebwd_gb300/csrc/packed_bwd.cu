@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_proxy_async_smem();
   pdl_wait();
+  if (blockIdx.x == 0 && tid == kThreads - 1) pdl_tell(p.s.status + kTermsTold);
   if (warp == kIssuer) {
     tmem_alloc(&sm.tmem_base, kCols);
     tmem_relinquish();
@@ -559,8 +560,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem& sm = *reinterpret_cast<Smem*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   const int tid = threadIdx.x, warp = tid >> 5;
   if (tid == 0) init_barriers(sm, kWorkWarps + 3);
-  // (no wait for packed_dkv, of which nothing is read: its CTAs let this kernel in once packed_pre was complete.  The wait
-  // at the end keeps the order for what follows.)
+  // (packed_dkv, of which nothing is read, may still run: its CTAs let this kernel in behind their wait for packed_pre.
+  // With the ordinary wait for all of packed_dkv: gradients of 4 short sequences 42.3 us, not 32.0, documents 203, not 188.)
+  pdl_wait_unless(p.s.status + kTermsTold);
   if (warp == kIssuer) {
     tmem_alloc(&sm.tmem_base, kCols);
     tmem_relinquish();
@@ -833,6 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kIssuer) tmem_dealloc(tmem, kCols);
   if (tid == 0 && sm.abort) atomicMax(p.s.status, (int)kDevTimeout);
   pdl_wait();
+  if (blockIdx.x == 0 && tid == 0) atomicExch(p.s.status + kTermsTold, 0);
 }
 
 template <int D>

@@ -111,6 +111,17 @@ inline int l2_head_group(size_t bytes_per_head, int BH) {
 // reads, then lets its own successor launch.  Without the launch attribute both are no-ops.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// A kernel that reads nothing of its direct predecessor, only of what that one waited for, may run beside it: the
+// predecessor says so behind its own wait (pdl_tell, by one thread, before the CTA's trigger), and what it could see then
+// is seen here as well (release and acquire; the fence is for TMA's reads).  Not told yet: the ordinary wait.  Before the
+// end of such a kernel a pdl_wait keeps the order for what follows, and `told` is zeroed behind it for the next call.
+__device__ __forceinline__ void pdl_tell(int* told) { asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(told) : "memory"); }
+__device__ __forceinline__ void pdl_wait_unless(const int* told) {
+  int yes;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(yes) : "l"(told) : "memory");
+  if (yes == 0) pdl_wait();
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
 
 // ----------------------------------------------------------------------- TMA
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2,

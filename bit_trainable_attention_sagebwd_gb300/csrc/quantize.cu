@@ -747,7 +747,8 @@ int launch_quantize(const void* Q, const void* K, const void* V, int B, int H, i
   int* status = reinterpret_cast<int*>(w + L.status);
   const size_t stage = (size_t)128 * D * 2;  // one staged token block
   ScopedTimer timer("quantize", st);
-  // the per-head counters (and normally the status word) are cleared before the kernels
+  // the per-head counters (and normally the status word) are cleared before the kernels; this is also what lets them read
+  // Q, K and V before their waits: no programmatic launch, it comes behind all of a kernel that writes those (rotary's, say)
   const size_t clear_from = clear_status ? L.status : L.sync;
   if (cudaMemsetAsync(w + clear_from, 0, L.qc - clear_from, st) != cudaSuccess) return 3;
   auto stats = D == 128 ? (qk_norm ? kstats_kernel<128, true> : kstats_kernel<128, false>)
