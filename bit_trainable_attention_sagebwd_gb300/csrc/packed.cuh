@@ -309,7 +309,9 @@ struct Feed {
 
 // The joining of a unit that was cut, by those who finish its last part (in time, whichever it is): a group of
 // warps has written its part's sums; true in all of them if it was the last to do so.  Sums are then added in the order
-// of the parts, so the bits do not depend on who came last.  The counter is zero before and after.
+// of the parts, so the bits do not depend on who came last.  The counter is zero before and after.  The lane that counts
+// has fences of its own on both sides: the sums of the other warps, which it knows of by `written`, go out with its count,
+// and what the other parts' counts brought is there for those that it tells.
 struct Meeting {
   uint64_t written, told;
   int last;
@@ -324,7 +326,9 @@ struct Meeting {
     if (leads) {
       ok = ok && mbar_wait_warp(&written, n & 1, abort);
       if (ok && (threadIdx.x & 31) == 0) {
+        __threadfence();
         last = atomicAdd(counter, 1) == parts - 1;
+        __threadfence();
         if (last) atomicExch(counter, 0);
         mbar_arrive(&told);
       }

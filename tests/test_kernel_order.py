@@ -75,3 +75,12 @@ def test_a_kernel_that_does_not_wait_is_told_and_keeps_the_order():
     assert "st.release.gpu" in body(ptx, "pdl_tell")
     told = body(ptx, "pdl_wait_unless")
     assert told.index("ld.acquire.gpu") < told.index("pdl_wait()") < told.index("fence.proxy.async.global")
+
+
+def test_the_sums_of_all_warps_go_out_with_the_count():
+    """Of a join only the lane that counts releases what it has learned of: a fence between its wait for the other warps
+    and the count, one between the count and its word to them, and theirs before they read."""
+    calls = re.findall(r"__threadfence|warp_arrive\(&written|mbar_wait_warp\(&written|atomicAdd|mbar_arrive\(&told|mbar_wait_warp\(&told"
+                       r"|return ok", body(source("packed.cuh"), "was_last"))
+    assert calls == ["__threadfence", "warp_arrive(&written", "mbar_wait_warp(&written", "__threadfence", "atomicAdd",
+                     "__threadfence", "mbar_arrive(&told", "mbar_wait_warp(&told", "__threadfence", "return ok"]
