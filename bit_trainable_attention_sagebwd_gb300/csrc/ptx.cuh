@@ -10,8 +10,9 @@
 
 namespace sage {
 
-// device-side status codes (kept in the workspace header word)
-enum : int { kDevOk = 0, kDevTimeout = 4, kDevSetup = 5 };
+// device-side status codes (kept in the workspace header word).  Where several are reported the largest is kept: these two,
+// after which a workspace's counters may have to be cleared, hide behind no number out of range (6 and 7).
+enum : int { kDevOk = 0, kDevSetup = 8, kDevTimeout = 9 };
 
 // Wall-clock budget of one wait; generous next to any single tile of work.
 #ifndef SAGE_WAIT_NS

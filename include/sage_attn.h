@@ -413,8 +413,9 @@ int sage_attn_kv_compact(const sage_kv_cache *cache, const sage_kv_cache *to, vo
  *  - Query head h reads key/value head h / (H / Hkv); Hkv divides H, H / Hkv at most 128, D 64 or 128,
  *    S at most 65536, T at most 2^24.
  *  - ws: sage_attn_packed_ws_bytes(.., backward) bytes, 256-byte aligned.  Its first 4096 bytes are zero before the
- *    first call, and again after SAGE_ERR_TIMEOUT: they begin with the status word (sage_attn_get_status(ws, stream)) and
- *    hold counters that every call leaves at zero.  The rest is free before and after.
+ *    first call, and again after SAGE_ERR_TIMEOUT or SAGE_ERR_CUDA, which no other report hides: they begin with the status
+ *    word (sage_attn_get_status(ws, stream)) and hold counters that every call leaves at zero.  The rest is free before and
+ *    after.
  *  Lengths are read on the device, so a captured CUDA graph can be replayed with others.  Calls that share a workspace
  *  must not overlap on the GPU.  Deterministic: the same call gives the same bits.  What a sequence holds, NaN and
  *  infinities among it, does not reach another one's results.
