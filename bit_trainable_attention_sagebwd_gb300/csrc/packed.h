@@ -12,6 +12,8 @@ namespace sage {
 constexpr int kPackedMaxSeqs = 65536;
 constexpr int kPackedMaxTokens = 1 << 24;
 constexpr int kPackedMaxGroup = 128;
+// Least sm_scale of the backward, which divides LSE by it: the log of 2^24 keys over 2^-120 is still below 2^125.
+constexpr float kPackedLeastScale = 0x1p-120f;
 
 struct PackedWs {
   size_t part, stats, total;  // (the status word and the counters come first)

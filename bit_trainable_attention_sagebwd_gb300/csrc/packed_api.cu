@@ -57,7 +57,7 @@ int sage_attn_packed_bwd(const sage_rows* Q, const sage_rows* K, const sage_rows
                          const sage_rows* dO, const int* cu_seqlens, const sage_rows* dQ, const sage_rows* dK,
                          const sage_rows* dV, void* ws, size_t ws_bytes, int T, int S, int H, int Hkv, int D, int causal,
                          float sm_scale, void* stream) {
-  if (!shape_ok(T, S, H, Hkv, D)) return SAGE_ERR_UNSUPPORTED;
+  if (!shape_ok(T, S, H, Hkv, D) || (sm_scale > 0.f && sm_scale < sage::kPackedLeastScale)) return SAGE_ERR_UNSUPPORTED;
   if (!rows_ok(Q, T, H) || !rows_ok(K, T, Hkv) || !rows_ok(V, T, Hkv) || !rows_ok(O, T, H) || !rows_ok(dO, T, H) ||
       !apart(dQ, T, H, D) || !apart(dK, T, Hkv, D) || !apart(dV, T, Hkv, D))
     return SAGE_ERR_INVALID_ARG;

@@ -440,7 +440,8 @@ int sage_attn_packed_fwd(const sage_rows *Q, const sage_rows *K, const sage_rows
  * The gradients: with O and LSE of the forward, P = e^(S - LSE) and delta_i = sum_d dO O:
  * dV = P^T dO, dS = P (dO V^T - delta), dQ = sm_scale dS K, dK = sm_scale dS^T Q; dK and dV sum over the query heads
  * of their key/value head.  P and dS are rounded to bf16 for the products that take them (dQ gets the rest of one in
- * four of dS's roundings, too); everything else is fp32.
+ * four of dS's roundings, too); everything else is fp32.  sm_scale between 0 and 2^-120 is refused (LSE / sm_scale has to
+ * be a number).
  * ws: of sage_attn_packed_ws_bytes(.., backward = 1).
  */
 int sage_attn_packed_bwd(const sage_rows *Q, const sage_rows *K, const sage_rows *V, const sage_rows *O, const float *LSE,

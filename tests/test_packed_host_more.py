@@ -3,7 +3,10 @@ the table's fractions, and the 64-bit reference of the gradients against differe
 import os
 import re
 
+import pytest
+
 import bit_trainable_attention_sagebwd_gb300 as sa
+from test_packed_host import backward, lib  # noqa: F401
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(sa.__file__)), "csrc")
 
@@ -19,3 +22,9 @@ def test_a_wait_that_ran_out_hides_behind_no_other_report():
     assert code["kDevOk"] == 0 and code["kDevSequence"] == code["kDevIndex"]
     for x in ("kDevSetup", "kDevTimeout"):
         assert all(code[x] > code[y] for y in ("kDevPages", "kDevIndex", "kDevSequence"))
+
+
+@pytest.mark.parametrize("scale", [1e-45, 1e-38, 5e-38, 7e-37])
+def test_gradients_at_scales_that_LSE_cannot_be_divided_by(lib, scale):
+    """(Below 5e-38 LSE / sm_scale was infinite for some 700 keys, and every P 0.)"""
+    assert backward(sm_scale=scale) == sa.SAGE_ERR_UNSUPPORTED
