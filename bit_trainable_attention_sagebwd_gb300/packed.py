@@ -7,7 +7,7 @@ each computes).
 
 Like the other helpers these marshal arguments; everything is computed by the CUDA library on the current stream of
 the tensors' device.  Tensors may be slices of a fused projection or head-major: any strides in multiples of 8
-elements with the channels contiguous.
+elements with the channels contiguous.  A batch without a token (T = 0) gives empty results, and nothing is launched.
 """
 from __future__ import annotations
 
@@ -81,13 +81,19 @@ def _new(stream, device, shape, dtype):
     return x
 
 
+def _ws_bytes(T, S, H, Hkv, D, backward):
+    """(of no tokens as of one)"""
+    n = lib().sage_attn_packed_ws_bytes(T or 1, S, H, Hkv, D, int(backward))
+    if n == 0:
+        raise SageError("sage_attn_packed_ws_bytes", SAGE_ERR_UNSUPPORTED)
+    return n
+
+
 def alloc_packed_ws(T, S, H, Hkv, D, backward=False, device="cuda", stream=None):
     """Workspace of packed_forward and packed_backward (backward=True) for T tokens in S sequences.  Its status word:
     get_status(ws)."""
     import torch
-    n = lib().sage_attn_packed_ws_bytes(T, S, H, Hkv, D, int(backward))
-    if n == 0:
-        raise SageError("sage_attn_packed_ws_bytes", SAGE_ERR_UNSUPPORTED)
+    n = _ws_bytes(T, S, H, Hkv, D, backward)
     with torch.cuda.stream(stream):
         ws = torch.empty(n, dtype=torch.uint8, device=device)
         ws[:4096].zero_()
@@ -119,8 +125,12 @@ def packed_forward(q, k, v, cu_seqlens, causal=True, sm_scale=None, o=None, lse=
     rows = _I64x12(*_rows(q, "q", bf16, qs, dev), *_rows(k, "k", bf16, kv, dev), *_rows(v, "v", bf16, kv, dev),
                    *_rows(o, "o", bf16, qs, dev))  # four sage_rows
     at = ctypes.addressof(rows)
-    _call(lib().sage_attn_packed_fwd, dev, stream, at, at + 24, at + 48,
-          _array(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev), at + 72, _array(lse, "lse", torch.float32, (H, T), dev),
+    cu_at = _array(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev)
+    lse_at = _array(lse, "lse", torch.float32, (H, T), dev)
+    if T == 0:
+        _ws_bytes(T, S, H, Hkv, D, False)
+        return o, lse
+    _call(lib().sage_attn_packed_fwd, dev, stream, at, at + 24, at + 48, cu_at, at + 72, lse_at,
           ws.data_ptr(), ws.nbytes, T, S, H, Hkv, D, int(causal), 0.0 if sm_scale is None else float(sm_scale))
     return o, lse
 
@@ -140,8 +150,12 @@ def packed_backward(q, k, v, o, lse, do, cu_seqlens, causal=True, sm_scale=None,
                    *_rows(o, "o", bf16, qs, dev), *_rows(do, "do", bf16, qs, dev), *_rows(dq, "dq", bf16, qs, dev),
                    *_rows(dk, "dk", bf16, kv, dev), *_rows(dv, "dv", bf16, kv, dev))  # eight sage_rows
     at = ctypes.addressof(rows)
-    _call(lib().sage_attn_packed_bwd, dev, stream, at, at + 24, at + 48, at + 72,
-          _array(lse, "lse", torch.float32, (H, T), dev), at + 96, _array(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev),
+    lse_at = _array(lse, "lse", torch.float32, (H, T), dev)
+    cu_at = _array(cu_seqlens, "cu_seqlens", torch.int32, (S + 1,), dev)
+    if T == 0:
+        _ws_bytes(T, S, H, Hkv, D, True)
+        return dq, dk, dv
+    _call(lib().sage_attn_packed_bwd, dev, stream, at, at + 24, at + 48, at + 72, lse_at, at + 96, cu_at,
           at + 120, at + 144, at + 168, ws.data_ptr(), ws.nbytes, T, S, H, Hkv, D, int(causal),
           0.0 if sm_scale is None else float(sm_scale))
     return dq, dk, dv

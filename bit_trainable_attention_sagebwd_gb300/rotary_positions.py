@@ -127,11 +127,13 @@ def _turn(table, q, k, cu_seqlens, start, positions, q_out, k_out, stream, inver
         heads = _I64x16(*heads, *_heads(k, "k", bf16, ks, dev), *_heads(k_out, "k_out", bf16, ks, dev))  # four
         at = ctypes.addressof(heads)
         keys, keys_out = at + 64, at + 96
-    _call(lib().sage_attn_rotary, dev, stream, table._ref, at, at + 32, keys, keys_out,
-          None if positions is None else _array(positions, "positions", i32, (N,) if packed else (B, N), dev, whose),
-          None if start is None else _array(start, "start", i32, (S,) if S else (B,), dev, whose),
-          None if cu_seqlens is None else _array(cu_seqlens, "cu_seqlens", i32, (S + 1,), dev, whose), B, N, S, H, hkv, D,
-          inverse)
+    where = (None if positions is None else _array(positions, "positions", i32, (N,) if packed else (B, N), dev, whose),
+             None if start is None else _array(start, "start", i32, (S,) if S else (B,), dev, whose),
+             None if cu_seqlens is None else _array(cu_seqlens, "cu_seqlens", i32, (S + 1,), dev, whose))
+    if B * N:
+        _call(lib().sage_attn_rotary, dev, stream, table._ref, at, at + 32, keys, keys_out, *where, B, N, S, H, hkv, D, inverse)
+    elif D not in (64, 128):
+        raise SageError("rotary", SAGE_ERR_UNSUPPORTED)
     return q_out if k is None else (q_out, k_out)
 
 
@@ -140,7 +142,7 @@ def rotary(table, q, k=None, cu_seqlens=None, start=None, positions=None, q_out=
 
     Positions: `positions`, int32 [T] or [B, N]; or start[b] + t (int32 [B]; None: t); or with cu_seqlens (int32 [S + 1],
     packed tensors) a token's place in its sequence + start[s] (int32 [S]); tokens of no sequence are left as they were.
-    Returns q_out, with k (q_out, k_out)."""
+    Returns q_out, with k (q_out, k_out); without a token nothing is launched."""
     return _turn(table, q, k, cu_seqlens, start, positions, q_out, k_out, stream, False)
 
 

@@ -411,7 +411,7 @@ int sage_attn_kv_compact(const sage_kv_cache *cache, const sage_kv_cache *to, vo
  *    SAGE_ERR_INVALID_ARG in the status word (and all of them where the others, which may then lie over one another, have
  *    more than 2 T tokens together).
  *  - Query head h reads key/value head h / (H / Hkv); Hkv divides H, H / Hkv at most 128, D 64 or 128,
- *    S at most 65536, T at most 2^24.
+ *    S at most 65536, T 1 to 2^24 (the torch helpers take 0 as well, without a launch).
  *  - ws: sage_attn_packed_ws_bytes(.., backward) bytes, 256-byte aligned.  Its first 4096 bytes are zero before the
  *    first call, and again after SAGE_ERR_TIMEOUT or SAGE_ERR_CUDA, which no other report hides: they begin with the status
  *    word (sage_attn_get_status(ws, stream)) and hold counters that every call leaves at zero.  The rest is free before and
@@ -465,7 +465,7 @@ int sage_attn_packed_bwd(const sage_rows *Q, const sage_rows *K, const sage_rows
  *    zeros: sage_attn_kv_extend's pos serves); or, with cu_seqlens (int32 [S + 1], not decreasing, B = 1), t's place in
  *    its sequence + start[s] (int32 [S], NULL: zeros).  Tokens of no sequence are left as they were.
  *    positions goes with neither of the others.  All are read on the device.
- *  - D 64 or 128; rot a multiple of 16 up to D; B N below 2^31.
+ *  - D 64 or 128; rot a multiple of 16 up to D; B N from 1 to below 2^31 (the torch helpers take 0 as well).
  */
 typedef struct sage_rotary {
   const uint64_t *turns;

@@ -1,8 +1,11 @@
 """More of packed attention and rotary positions on the GPU."""
 import pytest
+import torch
 
+import bit_trainable_attention_sagebwd_gb300 as sa
 import packed_ref as ref
 from test_gpu_packed import backward_checked, forward_checked, fp32_default  # noqa: F401
+from test_gpu_rotary import table
 
 pytestmark = pytest.mark.gpu
 
@@ -13,3 +16,32 @@ def test_the_least_scale(D):
     q, k, v, do, cu = ref.inputs([300, 1, 77], 4, 2, D, seed=2)
     forward_checked(q, k, v, cu, True, 2.0 ** -120)
     backward_checked(q, k, v, do, cu, True, 2.0 ** -120)
+
+
+@pytest.mark.parametrize("S", [1, 3])
+def test_batches_without_a_token(S):
+    """A step whose share of the documents is empty: every call gives empty results."""
+    q, k = (torch.empty((0, h, 64), dtype=torch.bfloat16, device="cuda") for h in (4, 2))
+    cu = torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+    t, _, _ = table(64, False)
+    ws = sa.alloc_packed_ws(0, S, 4, 2, 64, backward=True)
+    for given in (None, ws):
+        tq, tk = sa.rotary(t, q, k, cu_seqlens=cu)
+        o, lse = sa.packed_forward(tq, tk, k, cu, ws=given)
+        assert o.shape == q.shape and o.dtype == q.dtype and lse.shape == (4, 0) and lse.dtype == torch.float32
+        grads = sa.packed_backward(tq, tk, k, o, lse, o, cu, ws=given)
+        assert [x.shape for x in grads] == [q.shape, k.shape, k.shape]
+        assert [x.shape for x in sa.rotary_backward(t, *grads[:2], cu_seqlens=cu)] == [q.shape, k.shape]
+    assert sa.get_status(ws) == sa.SAGE_OK
+    for shape in ((0, 4, 1, 64), (2, 4, 0, 64)):
+        x = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+        assert sa.rotary(t, x, start=torch.zeros(shape[0], dtype=torch.int32, device="cuda")).shape == shape
+    # refused as with tokens
+    with pytest.raises(sa.SageError):
+        sa.packed_forward(q[:, :3], k, k, cu, ws=ws)
+    with pytest.raises(ValueError):
+        sa.packed_forward(q.half(), k, k, cu)
+    with pytest.raises(ValueError):
+        sa.packed_backward(q, k, k, q, torch.empty((3, 0), device="cuda"), q, cu)
+    with pytest.raises(sa.SageError):
+        sa.rotary(t, torch.empty((0, 4, 96), dtype=torch.bfloat16, device="cuda"))
