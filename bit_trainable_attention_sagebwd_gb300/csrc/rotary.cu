@@ -7,8 +7,9 @@
 // copy reaches; 64 tokens: 2.4 us, a launch.
 //
 // The angle of pair c at position n is n times a frequency, of which only the part of a turn counts.  Frequencies come
-// as 64-bit fractions of a turn, so n f modulo a turn is an integer product that wraps by itself: exact up to 2^-65 n
-// turns at any position, where an fp32 product would lose the angle at 2^20.
+// as 64-bit fractions of a turn, so n f modulo a turn is an integer product that wraps by itself: off by 2^-65 n turns at
+// most (and by what the caller's frequency is off n times: n f 2^-53 for a double's rounding), where an fp32 product would
+// lose the angle at 2^20.
 #include <cuda_bf16.h>
 
 #include "launch.h"

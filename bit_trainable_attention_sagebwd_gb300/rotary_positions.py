@@ -12,6 +12,7 @@ current stream of the tensors' device.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 from . import SAGE_ERR_UNSUPPORTED, SageError, lib, sage_rotary
@@ -65,6 +66,30 @@ def rotary_frequencies(rot, base=10000.0, scaling="none", factor=1.0, context=40
     return [x * (1 - s) + x / factor * s for x, s in zip(f, share)], 0.1 * math.log(factor) + 1.0
 
 
+@functools.lru_cache(maxsize=8)
+def _pi(bits):
+    """pi 2^bits, rounded down, by Machin's formula: 16 arctan 1/5 - 4 arctan 1/239."""
+    one = 1 << (bits + 32)
+
+    def arctan_of_inverse(n):
+        total, power, k = 0, one // n, 0
+        while power:
+            total += (-1) ** k * (power // (2 * k + 1))
+            power //= n * n
+            k += 1
+        return total
+
+    return (16 * arctan_of_inverse(5) - 4 * arctan_of_inverse(239)) >> 32
+
+
+def _turns(f):
+    """The nearest whole number of 2^-64 turns to f radians, less whole turns: in [-2^63, 2^63)."""
+    n, d = abs(f).as_integer_ratio()
+    bits = 256 + (n.bit_length() >> 7 << 7)                 # more by 128 than whole turns take
+    t = ((n << (64 + bits)) // (d * _pi(bits)) + 1) >> 1    # f / (2 pi) 2^64 and a half, rounded down
+    return ((t if f > 0 else -t) + 2 ** 63) % 2 ** 64 - 2 ** 63
+
+
 def rotary_table(rot, base=10000.0, scaling="none", factor=1.0, context=4096, fast=32.0, slow=1.0, interleaved=False,
                  frequencies=None, gain=None, device="cuda") -> Rotary:
     """The table of rotary_frequencies(rot, ..), or of given `frequencies` (rot / 2 radians a position); `gain` in place
@@ -78,10 +103,7 @@ def rotary_table(rot, base=10000.0, scaling="none", factor=1.0, context=4096, fa
         frequencies, of_scaling = [float(f) for f in frequencies], 1.0
     if len(frequencies) != rot // 2 or not all(math.isfinite(f) for f in frequencies):
         raise ValueError(f"frequencies: {rot // 2} finite numbers expected")
-    # (the quotient has 53 bits, which 2^64 leaves as they are)
-    turns = [int(math.fmod(f / (2 * math.pi), 1.0) * 2.0 ** 64) % 2 ** 64 for f in frequencies]
-    turns = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
-    return Rotary(torch.tensor(turns, dtype=torch.int64).to(device), interleaved, of_scaling if gain is None else gain)
+    return Rotary(torch.tensor([_turns(f) for f in frequencies], dtype=torch.int64).to(device), interleaved, of_scaling if gain is None else gain)
 
 
 def _heads(x, name, bf16, shape, device):

@@ -1,11 +1,14 @@
 """More of packed attention and rotary positions without a GPU: the device status words, calls without tokens, small scales,
 the table's fractions, and the 64-bit reference of the gradients against differences."""
+import decimal
+import math
 import os
 import re
 
 import pytest
 
 import bit_trainable_attention_sagebwd_gb300 as sa
+from bit_trainable_attention_sagebwd_gb300 import rotary_positions
 from test_packed_host import backward, lib  # noqa: F401
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(sa.__file__)), "csrc")
@@ -28,3 +31,25 @@ def test_a_wait_that_ran_out_hides_behind_no_other_report():
 def test_gradients_at_scales_that_LSE_cannot_be_divided_by(lib, scale):
     """(Below 5e-38 LSE / sm_scale was infinite for some 700 keys, and every P 0.)"""
     assert backward(sm_scale=scale) == sa.SAGE_ERR_UNSUPPORTED
+
+
+PI = decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+FREQUENCIES = [1.0, -1.0, 0.5, 1e-4, 10000.0 ** (-126 / 128), 500000.0 ** (-2 / 128), 1e-12, 1e-300, 0.0, math.pi, 2 * math.pi, -7.25, 6.283,
+               1e5, -1e9, 2.0 ** 60]
+
+
+@pytest.mark.parametrize("f", FREQUENCIES, ids=str)
+def test_fractions_of_a_turn_are_the_nearest(f):
+    """Against 100 digits: what a table holds is off by half of 2^-64 turns at most, whole turns apart."""
+    with decimal.localcontext(prec=160):
+        exact = decimal.Decimal(f) / (2 * PI) * 2 ** 64
+        got = rotary_positions._turns(f)
+        off = (exact - got) % 2 ** 64
+        assert -2 ** 63 <= got < 2 ** 63 and min(off, 2 ** 64 - off) <= decimal.Decimal("0.5000001")
+
+
+def test_the_digits_of_pi():
+    with decimal.localcontext(prec=160):
+        for bits in (64, 300, 330):
+            off = PI * 2 ** bits - rotary_positions._pi(bits)
+            assert -1 <= off <= 2
