@@ -45,3 +45,26 @@ def test_batches_without_a_token(S):
         sa.packed_backward(q, k, k, q, torch.empty((3, 0), device="cuda"), q, cu)
     with pytest.raises(sa.SageError):
         sa.rotary(t, torch.empty((0, 4, 96), dtype=torch.bfloat16, device="cuda"))
+
+
+@pytest.mark.parametrize("D,causal,G", [(64, True, 2), (128, False, 3)])
+def test_gradients_along_themselves_against_differences(D, causal, G):
+    """Sum dO O of the 64-bit forward along each gradient, whose slope is the gradient's square.  The library's is off by its own
+    rounding (2^-8 / sqrt 3 in relative L2), P's and dS's (the same, half as much again where rows cancel) and O's in delta:
+    1e-2 of the slope at most."""
+    Hkv, scale = 2, D ** -0.5
+    q, k, v, do, cu = ref.inputs([33, 1, 70], G * Hkv, Hkv, D, seed=3)
+    o, lse = sa.packed_forward(q, k, v, cu, causal=causal)
+    got = dict(zip(("dq", "dk", "dv"), sa.packed_backward(q, k, v, o, lse, do, cu, causal=causal)))
+    x = [y.double() for y in (q, k, v)]
+    want, _ = ref.backward(*x, *ref.forward(*x, cu, causal, scale)[:2], do, cu, causal, scale)
+    for n, (name, way) in enumerate(want.items()):
+        h = 1e-4 / float(way.norm())
+
+        def loss(step):
+            y = list(x)
+            y[n] = x[n] + step * way
+            return (do.double() * ref.forward(*y, cu, causal, scale)[0]).sum()
+
+        slope = float((loss(h) - loss(-h)) / (2 * h))
+        assert abs(float((got[name].double() * way).sum()) - slope) <= 1e-2 * slope, name

@@ -6,7 +6,9 @@ import os
 import re
 
 import pytest
+import torch
 
+import packed_ref as ref
 import bit_trainable_attention_sagebwd_gb300 as sa
 from bit_trainable_attention_sagebwd_gb300 import rotary_positions
 from test_packed_host import backward, lib  # noqa: F401
@@ -53,3 +55,27 @@ def test_the_digits_of_pi():
         for bits in (64, 300, 330):
             off = PI * 2 ** bits - rotary_positions._pi(bits)
             assert -1 <= off <= 2
+
+
+# ------------------------------------------------------------------- what the GPU's results are compared with
+
+@pytest.mark.parametrize("D,causal,G", [(64, True, 2), (128, False, 3)])
+def test_the_reference_gradients_against_differences(D, causal, G):
+    """Sum dO O of the 64-bit forward along a direction at random: the reference's gradients, from its own O and LSE."""
+    Hkv, scale = 2, D ** -0.5
+    *x, do, cu = ref.inputs([33, 1, 70], G * Hkv, Hkv, D, seed=3, device="cpu")
+    x, do = [y.double() for y in x], do.double()
+    o, lse, _, _ = ref.forward(*x, cu, causal, scale)
+    grads, _ = ref.backward(*x, o, lse, do, cu, causal, scale)
+    g = torch.Generator().manual_seed(5)
+    for n, name in enumerate(("dq", "dk", "dv")):
+        way, h = torch.randn(x[n].shape, dtype=torch.float64, generator=g), 1e-4
+
+        def loss(step):
+            y = list(x)
+            y[n] = x[n] + step * way
+            return (do * ref.forward(*y, cu, causal, scale)[0]).sum()
+
+        # (off by h^2 of the third derivative, and by 64-bit rounding over h)
+        slope = float((loss(h) - loss(-h)) / (2 * h))
+        assert abs(float((grads[name] * way).sum()) - slope) <= 1e-6 * float(grads[name].norm() * way.norm()), name
