@@ -4,6 +4,7 @@ import torch
 
 import bit_trainable_attention_sagebwd_gb300 as sa
 import packed_ref as ref
+import packed_rests as rests
 from test_gpu_packed import backward_checked, forward_checked, fp32_default  # noqa: F401
 from test_gpu_rotary import table
 
@@ -68,3 +69,12 @@ def test_gradients_along_themselves_against_differences(D, causal, G):
 
         slope = float((loss(h) - loss(-h)) / (2 * h))
         assert abs(float((got[name].double() * way).sum()) - slope) <= 1e-2 * slope, name
+
+
+@pytest.mark.parametrize("G", [1, 2, 5])
+@pytest.mark.parametrize("D,causal", [(64, False), (64, True), (128, False), (128, True)])
+def test_the_rests_of_dS_go_into_dQ(D, causal, G):
+    q, k, v, do, cu = rests.inputs(G, D, 7 + G, "cuda")
+    o, lse = sa.packed_forward(q, k, v, cu, causal=causal)
+    dq, _, _ = sa.packed_backward(q, k, v, o, lse, do, cu, causal=causal)
+    rests.check(dq, ref.backward(q, k, v, o, lse, do, cu, causal, D ** -0.5)[0]["dq"], cu)

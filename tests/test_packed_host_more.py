@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import packed_ref as ref
+import packed_rests as rests
 import bit_trainable_attention_sagebwd_gb300 as sa
 from bit_trainable_attention_sagebwd_gb300 import rotary_positions
 from test_packed_host import backward, lib  # noqa: F401
@@ -79,3 +80,35 @@ def test_the_reference_gradients_against_differences(D, causal, G):
         # (off by h^2 of the third derivative, and by 64-bit rounding over h)
         slope = float((loss(h) - loss(-h)) / (2 * h))
         assert abs(float((grads[name] * way).sum()) - slope) <= 1e-6 * float(grads[name].norm() * way.norm()), name
+
+
+def emulated(q, k, v, o, lse, do, cu, causal, low):
+    """dQ with dS rounded to bf16 and what `low` makes of the roundings' rests."""
+    D, out = q.shape[2], torch.zeros_like(q)
+    for b, e in zip(cu.tolist(), cu.tolist()[1:]):
+        for h in range(q.shape[1]):
+            kh, doh = k[b:e, 0].double(), do[b:e, h].double()
+            p = torch.exp(ref._logits(q[b:e, h].double(), kh, causal, D ** -0.5) - lse[h, b:e, None].double())
+            ds = p * (doh @ v[b:e, 0].double().T - (doh * o[b:e, h].double()).sum(-1, keepdim=True))
+            high = ds.to(torch.bfloat16).double()
+            out[b:e, h] = (D ** -0.5 * (high + low((ds - high) * rests.carried(e - b))) @ kh).to(torch.bfloat16)
+    return out
+
+
+@pytest.mark.parametrize("D,causal", [(64, False), (64, True), (128, False), (128, True)])
+def test_the_check_of_the_rests_sees_what_is_wrong(D, causal):
+    q, k, v, do, cu = rests.inputs(2, D, 7, "cpu")
+    o, lse, _, _ = ref.forward(q, k, v, cu, causal, D ** -0.5)
+    o, lse = o.to(torch.bfloat16), lse.float()
+    want = ref.backward(q, k, v, o, lse, do, cu, causal, D ** -0.5)[0]["dq"]
+
+    def dq(low):
+        return emulated(q, k, v, o, lse, do, cu, causal, low)
+
+    rests.check(dq(lambda x: x.to(torch.bfloat16).double()), want, cu)
+    at = cu.tolist()
+    for wrong in (lambda x: 0 * x, lambda x: -x, lambda x: x.roll(8, 1)):
+        got = dq(wrong)
+        for n, b, e in zip(rests.LENS, at, at[1:]):
+            off = float((got[b:e].double() - want[b:e]).norm() / want[b:e].norm())
+            assert off > rests.MOST, (n, off)
