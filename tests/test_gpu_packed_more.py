@@ -78,3 +78,25 @@ def test_the_rests_of_dS_go_into_dQ(D, causal, G):
     o, lse = sa.packed_forward(q, k, v, cu, causal=causal)
     dq, _, _ = sa.packed_backward(q, k, v, o, lse, do, cu, causal=causal)
     rests.check(dq, ref.backward(q, k, v, o, lse, do, cu, causal, D ** -0.5)[0]["dq"], cu)
+
+
+@pytest.mark.parametrize("entries", [[0, 50, 110, 181], [-1, 50, 110, 180], [0, 2 ** 31 - 1, 110, 180], [0, 50, 40, 180],
+                                     [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1, 0]], ids=str)
+def test_gradients_beside_sequences_out_of_order_or_range(entries):
+    """Rows of one sequence, and only of one, get what a call on that sequence alone gives."""
+    q, k, v, do, cu = ref.inputs([180], 2, 1, 64)
+    o, lse = sa.packed_forward(q, k, v, cu)
+    out = [torch.full_like(x, 7.0) for x in (q, k, v)]
+    sa.packed_backward(q, k, v, o, lse, do, torch.tensor(entries, dtype=torch.int32, device="cuda"), dq=out[0], dk=out[1], dv=out[2])
+    good = [(b, e) for b, e in zip(entries, entries[1:]) if 0 <= b <= e <= 180]
+    times = torch.zeros(180, dtype=torch.int32)
+    for b, e in good:
+        times[b:e] += 1
+    for b, e in good:
+        alone = torch.tensor([0, e - b], dtype=torch.int32, device="cuda")
+        want = sa.packed_backward(*(x[b:e] for x in (q, k, v, o)), lse[:, b:e].contiguous(), do[b:e], alone)
+        once = (times[b:e] == 1).cuda()
+        for x, y in zip(out, want):
+            assert torch.equal(x[b:e][once], y[once])
+    for x in out:
+        assert (x[(times == 0).cuda()] == 7).all()
