@@ -100,3 +100,21 @@ def test_gradients_beside_sequences_out_of_order_or_range(entries):
             assert torch.equal(x[b:e][once], y[once])
     for x in out:
         assert (x[(times == 0).cuda()] == 7).all()
+
+
+@pytest.mark.parametrize("N", [300, 20000])
+def test_turned_and_quantized_at_once(N):
+    """rotary, and quantize right behind it on the same stream, which stages keys and values before it waits: the codes of
+    the turned ones."""
+    t, _, _ = table(128, False)
+    g = torch.Generator("cuda").manual_seed(0)
+    q, k, v = (torch.randn((1, 4, N, 128), device="cuda", generator=g).to(torch.bfloat16) for _ in range(3))
+    tq, tk = sa.rotary(t, q, k)
+    torch.cuda.synchronize()
+    o, lse = sa.forward(sa.quantize(tq, tk, v), 1, 4, N, 128, causal=True)[:2]
+    q2, k2 = torch.zeros_like(q), torch.zeros_like(k)
+    for _ in range(10):
+        q2.zero_(), k2.zero_()
+        sa.rotary(t, q, k, q_out=q2, k_out=k2)
+        got = sa.forward(sa.quantize(q2, k2, v), 1, 4, N, 128, causal=True)[:2]
+        assert torch.equal(got[0], o) and torch.equal(got[1], lse)
