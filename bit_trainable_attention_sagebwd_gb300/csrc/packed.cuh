@@ -129,8 +129,9 @@ __device__ __forceinline__ long long places(const PackedShape& p, int b, int& le
   return len > 0 ? Units<KIND>(p, len).total() * p.Hkv : 0;
 }
 
-// The line of all units, cut into equal parts for the CTAs of a grid, of kLeast places at least (two cuts must not
-// fall into one tile; four key tiles, since a part of fewer is mostly beginning and end).
+// The line of all units, cut into equal parts for the CTAs of a grid, of kLeast places at least: two cuts must not fall into
+// one tile, and a part of fewer than four key tiles would be mostly beginning and end (not measured against 256, which would
+// do for the first; short calls leave CTAs without work by it: 700 tokens of 32 heads of 8 take 99 of 152).
 constexpr int kLeast = 512;
 static_assert(kLeast >= 2 * kTile, "a tile between two cuts");
 struct Shares {
@@ -401,7 +402,8 @@ struct RowStore {
 };
 
 // pre[g]: the places before each group of sequences, and their number behind the last; `tokens`, zero before: of all
-// sequences (all threads of the CTA, which must synchronise before they read either)
+// sequences (all threads of the CTA, which must synchronise before they read either).  Every CTA sums all of them: the forward
+// of 512 empty sequences takes 3.4 us, of 4096 9.4 us, of 65536 121 us (of one token each, 8 heads of 2: 1.8 ms).
 template <int KIND, int NT>
 __device__ __forceinline__ void prefix_of_sequences(const PackedShape& p, int group, long long* pre, long long* wsum,
                                                     unsigned long long* tokens) {

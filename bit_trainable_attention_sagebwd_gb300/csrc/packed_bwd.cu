@@ -21,7 +21,9 @@
 // tile; the product stops there), the others end in rows that are not stored.
 //
 // 8192 tokens, 32 heads of 8, D = 128, causal: 1.34 ms, 1.02 PFLOP/s of the five products' operations (1.43 of the seven's
-// that run, 75% of what a bf16 product reaches here): 0.73 ms dK and dV, 0.60 ms dQ, 0.04 ms the row terms, each alone.
+// that run, 75% of what a bf16 product reaches here in a burst): 0.72 ms dK and dV, 0.59 ms dQ, 0.03 ms the row terms, each
+// alone.  Repeated for seconds, under the power limit: 1.45 ms, 0.95 PFLOP/s (1.33 of the seven's, 76% of what one reaches
+// then).
 // What bounds it: shared memory's bandwidth and the tensor core (70% and 66% active) with the chain between the products.
 #include "issue.cuh"
 #include "launch.h"
@@ -545,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dS's rounding to bf16 is most of what dQ is off by: a row of dS sums to zero, its roundings do not, so what the keys
 // have in common stays in their error.  Of the first eight of every 32 keys the rounding's rest goes into dQ as well
 // (`low`, a further bf16, 16 keys an MMA): a quarter of that error's square for 4% of the time, 1.29 to 1.35 ms for
-// 8192 tokens.  For all keys TMEM has no columns left.  (Sequences of 32 keys or fewer: of the first sixteen.)
+// 8192 tokens.  For all keys TMEM has no columns left at D = 128; at D = 64, where 96 are free, it was not tried.  (A last tile
+// of 32 keys or fewer: of the first sixteen; of 33 to 96: of the first two groups of 32.)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dq_kernel(const BwdParams p, const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

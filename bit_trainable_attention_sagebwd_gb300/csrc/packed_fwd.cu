@@ -12,15 +12,17 @@
 //    rounding to bf16 (what the product takes) is the only one on the way; row sums are of P before it.
 // A unit that was cut leaves its parts' sums in the workspace; whoever finishes last adds them up.
 //
-// 16384 tokens, 16 heads of 2, D = 128, causal: 0.66 ms, 1.58 PFLOP/s, 83% of what a bf16 product reaches here.  What
-// bounds it: the chain S, softmax, P V of a row tile, of which two run at once (tensor core 63%, issue slots 41%, the
-// exponentials' unit 32%; the softmax warps wait for TMEM most).  What the code of the five roles takes to fetch counts as
-// much: the softmax unrolled whole costs 12%, copies of the issue for place and stage 10%.  A row's columns shared by two
-// threads (16 softmax warps, maxima exchanged): 0.70 ms.  At D = 64 the same chain is 0.71 us a tile beside 0.89 us; S three
-// tiles ahead of P V there (a third place for S in TMEM) took 0.18 ms where this takes 0.15: both softmaxes then run at once.
+// 16001 tokens, 16 heads of 2, D = 128, causal: 0.66 ms, 1.58 PFLOP/s, 82% of what a bf16 product reaches here in a burst;
+// repeated for seconds, under the power limit, 0.715 ms, 1.47 PFLOP/s, 84% of what one reaches then.  What bounds it: the
+// chain S, softmax, P V of a row tile, of which two run at once (tensor core 65%, issue slots 41%, the exponentials' unit
+// 33%; the softmax warps wait for TMEM most).  What the code of the five roles takes to fetch counts as much: the softmax
+// unrolled whole costs 12%, copies of the issue for place and stage 10%.  A row's columns shared by two threads (16 softmax
+// warps, maxima exchanged): 0.70 ms.  At D = 64 the same chain is 0.71 us a tile beside 0.89 us; S three tiles ahead of P V
+// there (a third place for S in TMEM) took 0.18 ms where this takes 0.15: both softmaxes then run at once.
 // TMA copies whole boxes: what lies behind a sequence's end is the next one's.  Rows of S behind it are not
 // stored, columns are masked; of V's rows those that a product reads (up to 15) are zeroed in shared memory, so that
-// nothing of another sequence, a NaN or an infinity among it, enters a sum.
+// nothing of another sequence, a NaN or an infinity among it, enters a sum.  (Of its own sequence's later keys a causal row
+// takes V with weight 0, as far as its tile goes: 0 times an infinity is NaN, as in the formula.)
 #include "issue.cuh"
 #include "launch.h"
 #include "packed.cuh"

@@ -137,8 +137,9 @@ int launch(const RotaryParams& p, cudaStream_t st) {
 
 int launch_rotary(const RotaryParams& p, int D, cudaStream_t st) {
   ScopedTimer timer("rotary", st);
-  // four heads a thread where that still fills the GPU (152 SMs of 2048 threads), else one (64 tokens of 40 heads: 2.4 us
-  // with one, 3.1 us with four; 32768 tokens: 192 us with one, 98 us with four)
+  // four heads a thread where there are 152 x 2048 threads of them, else one.  With one and with four, 40 heads: 64 tokens
+  // 2.3 and 2.8 us, 250 3.7 and 3.5, 1000 7.8 and 6.5, 2000 12.9 and 10.2, 4000 24.2 and 16.3, 32000 174 and 96.  They cross
+  // near 200 tokens, well below the switch, which lies at 3900: up to there the one that is taken is the slower.
   const long long threads = (long long)p.B * p.N * ((p.heads[0] + p.heads[1] + 3) / 4) * (D / 16);
   if (threads >= 152 * 2048) return D == 128 ? launch<128, 4>(p, st) : launch<64, 4>(p, st);
   return D == 128 ? launch<128, 1>(p, st) : launch<64, 1>(p, st);

@@ -45,7 +45,8 @@ def rotary_frequencies(rot, base=10000.0, scaling="none", factor=1.0, context=40
       "linear"  f_c / factor (positions interpolated)
       "base"    base times factor^(rot / (rot - 2)): the slowest pair as "linear", the fastest as it was
       "ramp"    pairs that turn more than `fast` times over the trained `context` as they were, fewer than `slow`
-                times f_c / factor, between them in proportion to c; the channels grow by 0.1 ln factor + 1
+                times f_c / factor, between them in proportion to c (the borders on whole pairs, rounded away from
+                each other, from pair 0 on); the channels grow by 0.1 ln factor + 1
     """
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling: one of {_SCALINGS}, got {scaling!r}")

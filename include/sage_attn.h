@@ -397,10 +397,10 @@ int sage_attn_kv_compact(const sage_kv_cache *cache, const sage_kv_cache *to, vo
                          void *stream);
 
 /*
- * Attention over packed sequences, in full precision: bf16 operands, fp32 sums.  The tokens of S sequences of
- * different lengths lie one behind the other; every sequence attends to itself.  For whole prompts and for training
- * on documents without padding, where the low-bit calls above take sequences of one length ("SageBwd: A Trainable
- * Low-bit Attention" (euno.news summary), Results, compares with such full-precision attention).
+ * Attention over packed sequences, 16-bit where the calls above have 8 or 4: bf16 operands, fp32 sums.  The tokens of S
+ * sequences of different lengths lie one behind the other; every sequence attends to itself.  For whole prompts and for
+ * training on documents without padding, where the low-bit calls above take sequences of one length ("SageBwd: A
+ * Trainable Low-bit Attention" (euno.news summary), Results, compares with such an attention as the full-precision one).
  *  - Q, O, dO, dQ: bf16 [T, H, D], K, V, dK, dV: bf16 [T, Hkv, D], given as sage_rows: the element (t, h, d) is at
  *    p[t * token + h * head + d] (strides in elements, positive multiples of 8, below 2^38, p 16-byte aligned), so a
  *    slice of a fused projection or a head-major tensor serves as it is.  What is written lies apart from what is read,
@@ -418,7 +418,8 @@ int sage_attn_kv_compact(const sage_kv_cache *cache, const sage_kv_cache *to, vo
  *    after.
  *  Lengths are read on the device, so a captured CUDA graph can be replayed with others.  Calls that share a workspace
  *  must not overlap on the GPU.  Deterministic: the same call gives the same bits.  What a sequence holds, NaN and
- *  infinities among it, does not reach another one's results.
+ *  infinities among it, does not reach another one's results; within its own sequence a value that is not finite may
+ *  reach rows that weigh it 0 (causal ones before it), since 0 times it is NaN.
  */
 typedef struct sage_rows {
   void *p;
@@ -429,8 +430,8 @@ size_t sage_attn_packed_ws_bytes(int T, int S, int H, int Hkv, int D, int backwa
 
 /*
  * S = sm_scale q . k over the keys of the query's sequence (causal != 0: those up to the query), O = softmax(S) V,
- * LSE = log sum e^S.  P is rounded to bf16 relative to the row's running reference; everything else is fp32.
- * sm_scale <= 0 selects 1/sqrt(D).
+ * LSE = log sum e^S.  P is rounded to bf16 relative to the row's running reference (2^-8 at most; fp16, which the
+ * high-precision calls above take, is not V's type); everything else is fp32.  sm_scale <= 0 selects 1/sqrt(D).
  */
 int sage_attn_packed_fwd(const sage_rows *Q, const sage_rows *K, const sage_rows *V, const int *cu_seqlens,
                          const sage_rows *O, float *LSE, void *ws, size_t ws_bytes, int T, int S, int H, int Hkv, int D,
